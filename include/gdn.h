@@ -317,6 +317,90 @@ int gdn_recurrent_step(const void *q, const void *k, const void *v, const float 
                        const float *beta, void *S, void *out, int N, int dk, int dv, int dtype,
                        void *stream);
 
+/* ------------------------------------------------------------------------
+ * Softmax attention: the layers of a hybrid model that stand between its
+ * delta-rule layers (Sykra 0.3.3 README, "Architectural Highlights": one layer
+ * in four).  Whole prompts and their gradients, and a paged 8-bit cache for
+ * the tokens that follow.
+ *
+ * Shared by the entry points below
+ *   - Hq query heads read Hkv key heads, Hq a multiple of Hkv: query head h
+ *     reads key head h / (Hq / Hkv).  D, the head size, is 64 or 128.
+ *   - q, k, v, out and gradients are bf16 (dtype GDN_BF16; others
+ *     GDN_ERR_UNSUPPORTED).  A row (one token) holds its heads one after the
+ *     other; the distance between rows is an argument, in elements, at least
+ *     the row's length and a multiple of 8, so that the parts of one fused
+ *     projection can be passed as they are.
+ *   - Softmax statistics and every sum are float32; probabilities are rounded
+ *     to 16 bits where they enter a matrix product.
+ *   - lse is the natural logarithm of a row's sum of exp(scale q.k), float32.
+ *   - Lengths, offsets, tables and slots are int32 on the device.  Their
+ *     values are not known to the call: entries that would lead outside the
+ *     buffers are clamped or skipped as described, never followed.
+ *   - A cache holds `num_blocks` blocks of `block_tokens` tokens (16, 32, 64
+ *     or 128), stored [num_blocks, Hkv, block_tokens, D] in 8 bits with one
+ *     float32 scale per (block, key head), stored [num_blocks, Hkv]; a value
+ *     is its code times its scale.  num_blocks * block_tokens is below 2^31.
+ *   - Errors as for gdn_chunk_fwd.
+ * ------------------------------------------------------------------------ */
+
+/* Codes of a cache (the `cache_format` argument). */
+enum { GDN_CACHE_I8 = 0,   /* signed integers in [-127, 127]                  */
+       GDN_CACHE_E4M3 = 1  /* 8-bit floats, OCP e4m3, largest 448             */ };
+
+/*
+ * Block tables and slots of a step, from the requests' lengths.
+ *
+ *   seq_lens, new_lens  [R] tokens held, tokens that this step adds
+ *   block_table [R, width]  row r: the blocks of request r in order; entries
+ *               past those that seq_lens[r] tokens occupy are ignored.  The
+ *               blocks that the new tokens need are appended in place.
+ *   free_blocks [n_free]  blocks to hand out, taken from the front in the
+ *               order of the requests
+ *   slot_map [T]  written: for each new token (packed, request after request)
+ *               block * block_tokens + offset; -1 behind the last token and
+ *               for tokens of refused requests
+ *   cu_seqlens [R + 1]  written: offsets of the requests' new tokens, at most T
+ *   lens_after [R]  written: tokens held afterwards; may not alias seq_lens
+ *   used [2]    written: how many free blocks were taken; how many requests
+ *               were refused
+ *
+ * A request is refused if a length is negative, its blocks exceed the table's
+ * width, its tokens exceed the slot map, or the free list does not reach its
+ * blocks (the needs of every request before it count, refused or not, unless
+ * their own lengths are at fault).  A refused request keeps its table row and
+ * its length; a negative new length counts as no tokens.  A block outside
+ * [0, num_blocks) gets slot -1.  R below 2^20.  One launch.
+ */
+int gdn_block_tables(const int *seq_lens, const int *new_lens, int *block_table, const int *free_blocks,
+                     int *slot_map, int *cu_seqlens, int *lens_after, int *used, int R, int width, int n_free,
+                     int block_tokens, int num_blocks, int T, void *stream);
+
+/*
+ * Writes rows of keys and values into the cache.
+ *
+ *   k, v       [T] rows of Hkv * D bf16 values, k_stride and v_stride apart
+ *   slot_map   [T] slots as from gdn_block_tables; tokens whose slot lies
+ *              outside the cache are skipped
+ *   k_cache, v_cache, k_scale, v_scale  updated in place
+ *
+ * For each (block, head) that new rows fall into, with a = max |x| over them
+ * and M = 127 (int8) or 448 (e4m3):
+ *     s = max(a / M, old scale if older rows stand before the new ones, 2^-100)
+ *     code = rne(x / s);   older codes = rne(code * old / s) if s grew.
+ * Rows behind the new ones are left as they were.  A block whose first row is
+ * new starts a scale of its own, whatever its scale was.  NaN is stored as
+ * zero, infinities as the largest code of the largest bf16 value's scale.
+ *
+ * No two tokens may have the same slot, and the tokens of one block must
+ * follow one another in the call with ascending slots, as gdn_block_tables
+ * gives them; otherwise the block's contents are undefined.
+ * T * Hkv below 2^28.
+ */
+int gdn_cache_append(const void *k, const void *v, const int *slot_map, void *k_cache, void *v_cache,
+                     float *k_scale, float *v_scale, long long k_stride, long long v_stride, int T, int Hkv,
+                     int D, int block_tokens, int num_blocks, int dtype, int cache_format, void *stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *gdn_status_str(int status);
 

@@ -1,0 +1,112 @@
+"""Torch helpers of the attention layer's entry points (include/gdn.h): block tables, the 8-bit paged cache, its
+single-token read, attention over whole prompts and its gradients.
+
+They check dtypes, shapes, strides and devices, allocate what is not passed in, pass ``data_ptr()`` and the current
+HIP stream of the tensors' device, and raise on a non-OK status.  Rows are [tokens, heads, D] with the heads of a row
+side by side; the distance between rows is free, so that q, k and v can be parts of one fused projection.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import gdn as raw
+
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+_FORMATS = {torch.int8: raw.GDN_CACHE_I8, torch.float8_e4m3fn: raw.GDN_CACHE_E4M3}
+
+
+def _device(t, who):
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{who}: tensors must live on a HIP device")
+    return dev
+
+
+def _dense(t, name, shape, dtype, dev):
+    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raw._check(t, name, shape, dtype, dev)
+
+
+def _rows(t, name, shape, dev):
+    """Distance between the rows of t [tokens, heads, D], whose rows are dense."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != _BF16:
+        raise TypeError(f"{name}: expected {_BF16}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name}: expected device {dev}, got {t.device}")
+    tokens, heads, d = shape
+    row, head, one = t.stride()
+    if one != 1 or (head != d and heads != 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    if tokens <= 1:
+        return max(row, heads * d) // 8 * 8 if row % 8 else max(row, heads * d)
+    if row < heads * d or row % 8:
+        raise ValueError(f"{name}: rows must be a multiple of 8 elements apart and not overlap")
+    return row
+
+
+def _call(dev, stream, fn, *args):
+    """fn(*args, stream) with `dev` as the current device."""
+    if torch.cuda.current_device() == dev.index:
+        s = fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else stream)
+    else:
+        with torch.cuda.device(dev):
+            s = fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else stream)
+    if s != raw.GDN_OK:
+        raise raw.GdnError(s)
+
+
+def block_tables(seq_lens, new_lens, block_table, free_blocks, block_tokens: int, num_blocks: int, tokens: int,
+                 stream=None):
+    """Extends block_table [R, width] in place by the blocks that new_lens [R] more tokens need beyond seq_lens [R],
+    taken from the front of free_blocks.  All int32.  tokens: the length of the slot map, at least the sum of new_lens
+    (what is over is filled with -1).
+
+    Returns (slot_map [tokens], cu_seqlens [R + 1], lens_after [R], used [2]: free blocks taken, requests refused).
+    """
+    dev = _device(seq_lens, "block_tables")
+    r, width = block_table.shape
+    _dense(seq_lens, "seq_lens", (r,), _I32, dev)
+    _dense(new_lens, "new_lens", (r,), _I32, dev)
+    _dense(block_table, "block_table", (r, width), _I32, dev)
+    _dense(free_blocks, "free_blocks", (free_blocks.numel(),), _I32, dev)
+    if tokens < 0:
+        raise ValueError("block_tables: tokens is negative")
+    # one allocation, each part 16-byte aligned
+    a, b, c = -(-tokens // 4) * 4, (r + 4) // 4 * 4, -(-r // 4) * 4
+    buf = torch.empty(a + b + c + 2, dtype=_I32, device=dev)
+    slot_map, cu, after, used = buf[:tokens], buf[a:a + r + 1], buf[a + b:a + b + r], buf[a + b + c:]
+    p = buf.data_ptr()
+    _call(dev, stream, raw.load().gdn_block_tables, seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
+          free_blocks.data_ptr(), p, p + 4 * a, p + 4 * (a + b), p + 4 * (a + b + c), r, width, free_blocks.numel(),
+          block_tokens, num_blocks, tokens)
+    return slot_map, cu, after, used
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, dev):
+    nb, hkv, bt, d = k_cache.shape
+    fmt = _FORMATS.get(k_cache.dtype)
+    if fmt is None:
+        raise TypeError(f"unsupported cache dtype {k_cache.dtype}; use int8 or float8_e4m3fn")
+    _dense(k_cache, "k_cache", (nb, hkv, bt, d), k_cache.dtype, dev)
+    _dense(v_cache, "v_cache", (nb, hkv, bt, d), k_cache.dtype, dev)
+    _dense(k_scale, "k_scale", (nb, hkv), _F32, dev)
+    _dense(v_scale, "v_scale", (nb, hkv), _F32, dev)
+    return nb, hkv, bt, d, fmt
+
+
+def cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=None):
+    """Writes the rows k, v [T, Hkv, D] bf16 into the cache at slot_map [T] int32 (see block_tables), in place.
+
+    k_cache, v_cache [num_blocks, Hkv, block_tokens, D] int8 or float8_e4m3fn; k_scale, v_scale [num_blocks, Hkv]
+    float32: a value is its code times the scale of its block and head.
+    """
+    dev = _device(k, "cache_append")
+    nb, hkv, bt, d, fmt = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    t = k.shape[0]
+    ks, vs = _rows(k, "k", (t, hkv, d), dev), _rows(v, "v", (t, hkv, d), dev)
+    _dense(slot_map, "slot_map", (t,), _I32, dev)
+    _call(dev, stream, raw.load().gdn_cache_append, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), ks, vs, t, hkv, d, bt, nb,
+          raw.GDN_BF16, fmt)

@@ -1,0 +1,74 @@
+// attn_api.cpp -- the C ABI of the attention layer (declared in include/gdn.h):
+// validates every argument before anything is enqueued, then launches.
+#include <stdint.h>
+
+#include "../../include/gdn.h"
+#include "gdn_attn.hpp"
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <int N> bool all_aligned(const void* const (&ptrs)[N]) {
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return false;
+  return true;
+}
+
+int status(hipError_t e) { return e == hipSuccess ? GDN_OK : GDN_ERR_HIP; }
+
+bool known_dtype(int d) { return d == GDN_F32 || d == GDN_BF16 || d == GDN_C64; }
+
+bool block_ok(int bt) { return bt == 16 || bt == 32 || bt == 64 || bt == 128; }
+
+// A row stride: room for the row, 16-byte aligned rows, no offset past 2^62.
+bool stride_ok(long long s, long long row) { return s >= row && s % 8 == 0 && s < (1LL << 40); }
+
+constexpr int kMaxRequests = 1 << 20;
+
+// Sizes of a cache and of the heads that read it.
+int cache_shape(int Hkv, int D, int bt, int num_blocks) {
+  if (Hkv <= 0 || D <= 0 || bt <= 0 || num_blocks < 0) return GDN_ERR_SHAPE;
+  if ((long long)num_blocks * bt >= (1LL << 31) || Hkv >= (1 << 20)) return GDN_ERR_SHAPE;
+  if ((D != 64 && D != 128) || !block_ok(bt)) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdn_block_tables(const int* seq_lens, const int* new_lens, int* block_table, const int* free_blocks,
+                     int* slot_map, int* cu_seqlens, int* lens_after, int* used, int R, int width, int n_free,
+                     int block_tokens, int num_blocks, int T, void* stream) {
+  if (R < 0 || width < 0 || n_free < 0 || num_blocks < 0 || T < 0 || block_tokens <= 0) return GDN_ERR_SHAPE;
+  if (R >= kMaxRequests || (long long)num_blocks * block_tokens >= (1LL << 31) || (long long)width * block_tokens >= (1LL << 31))
+    return GDN_ERR_SHAPE;
+  if (!block_ok(block_tokens)) return GDN_ERR_UNSUPPORTED;
+  if (!cu_seqlens || !used || (T && !slot_map) || (n_free && !free_blocks)) return GDN_ERR_NULL;
+  if (R && (!seq_lens || !new_lens || !lens_after || (width && !block_table))) return GDN_ERR_NULL;
+  const void* ptrs[] = {seq_lens, new_lens, block_table, free_blocks, slot_map, cu_seqlens, lens_after, used};
+  if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
+  return status(gdn::launch_block_tables({seq_lens, new_lens, block_table, free_blocks, slot_map, cu_seqlens,
+                                          lens_after, used, R, width, n_free, block_tokens, num_blocks, T, stream}));
+}
+
+int gdn_cache_append(const void* k, const void* v, const int* slot_map, void* k_cache, void* v_cache, float* k_scale,
+                     float* v_scale, long long k_stride, long long v_stride, int T, int Hkv, int D, int block_tokens,
+                     int num_blocks, int dtype, int cache_format, void* stream) {
+  if (!known_dtype(dtype)) return GDN_ERR_DTYPE;
+  if (cache_format != GDN_CACHE_I8 && cache_format != GDN_CACHE_E4M3) return GDN_ERR_DTYPE;
+  if (T < 0) return GDN_ERR_SHAPE;
+  if (const int s = cache_shape(Hkv, D, block_tokens, num_blocks)) return s;
+  if (dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+  const long long row = (long long)Hkv * D;
+  if ((long long)T * Hkv >= (1LL << 28) || !stride_ok(k_stride, row) || !stride_ok(v_stride, row)) return GDN_ERR_SHAPE;
+  if (T == 0 || num_blocks == 0) return GDN_OK;
+  if (!k || !v || !slot_map || !k_cache || !v_cache || !k_scale || !v_scale) return GDN_ERR_NULL;
+  const void* ptrs[] = {k, v, slot_map, k_cache, v_cache, k_scale, v_scale};
+  if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
+  return status(gdn::launch_cache_append({k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_stride, v_stride, T,
+                                          Hkv, D, block_tokens, num_blocks, cache_format, stream}));
+}
+
+}  // extern "C"

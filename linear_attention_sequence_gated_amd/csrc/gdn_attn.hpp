@@ -1,0 +1,40 @@
+// gdn_attn.hpp -- internal interface of the attention layer's kernels: block
+// tables, the 8-bit paged cache, its single-token read, prompt attention and
+// its gradients.  Arguments arrive validated (attn_api.cpp).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gdn {
+
+struct TablesArgs {
+  const int* seq_lens;
+  const int* new_lens;
+  int* block_table;
+  const int* free_blocks;
+  int* slot_map;
+  int* cu_seqlens;
+  int* lens_after;
+  int* used;
+  int R, width, n_free, bt, num_blocks, T;
+  void* stream;
+};
+hipError_t launch_block_tables(const TablesArgs& a);
+
+// Strides are distances between tokens, in elements.
+struct AppendArgs {
+  const void* k;
+  const void* v;
+  const int* slot_map;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  long long ks, vs;
+  int T, H, D, bt, num_blocks, fmt;
+  void* stream;
+};
+hipError_t launch_cache_append(const AppendArgs& a);
+
+}  // namespace gdn

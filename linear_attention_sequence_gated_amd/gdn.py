@@ -21,11 +21,13 @@ LIB_PATH = os.path.join(_HERE, "libgdn.so")
 GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE = 0, 1, 2, 3
 GDN_ERR_UNSUPPORTED, GDN_ERR_ALIGN, GDN_ERR_WORKSPACE, GDN_ERR_HIP = 4, 5, 6, 7
 GDN_F32, GDN_BF16, GDN_C64 = 0, 1, 2
+GDN_CACHE_I8, GDN_CACHE_E4M3 = 0, 1
 GDN_NOALLOC_MAX_WORKSPACE = 128 << 20  # include/gdn.h
 
 EXPORTS = ("gdn_chunk_fwd_workspace_bytes", "gdn_chunk_fwd", "gdn_chunk_fwd_prologue_workspace_bytes",
            "gdn_chunk_fwd_prologue", "gdn_chunk_bwd_workspace_bytes",
-           "gdn_chunk_bwd", "gdn_fwd_channel_decay", "gdn_recurrent_step", "gdn_status_str", "gdn_chunk_fwd_noalloc")
+           "gdn_chunk_bwd", "gdn_fwd_channel_decay", "gdn_recurrent_step", "gdn_status_str", "gdn_chunk_fwd_noalloc",
+           "gdn_block_tables", "gdn_cache_append")
 
 _lib = None
 
@@ -45,7 +47,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
     if not os.path.exists(p):
         raise ImportError(f"{p} is missing: build it with `python -m linear_attention_sequence_gated_amd.build`")
     lib = ctypes.CDLL(p)
-    vp, ci, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    vp, ci, sz, ll, fl = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong, ctypes.c_float
     lib.gdn_chunk_fwd_workspace_bytes.argtypes = [ci] * 7
     lib.gdn_chunk_fwd_workspace_bytes.restype = sz
     lib.gdn_chunk_fwd.argtypes = [vp, vp, vp, vp, vp, vp, ci, vp, vp, ci, ci, ci, ci, ci, ci, vp, sz, vp]
@@ -65,6 +67,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.gdn_recurrent_step.restype = ci
     lib.gdn_chunk_fwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, ci, vp, vp, ci, ci, ci, ci, ci, ci, vp]
     lib.gdn_chunk_fwd_noalloc.restype = ci
+    lib.gdn_block_tables.argtypes = [vp] * 8 + [ci] * 6 + [vp]
+    lib.gdn_block_tables.restype = ci
+    lib.gdn_cache_append.argtypes = [vp] * 7 + [ll] * 2 + [ci] * 7 + [vp]
+    lib.gdn_cache_append.restype = ci
     lib.gdn_status_str.argtypes = [ci]
     lib.gdn_status_str.restype = ctypes.c_char_p
     if path is None:
@@ -119,6 +125,18 @@ def gdn_fwd_channel_decay(q, k, v, r, beta, S0, out, S_final, B, T, H, dk, dv, d
 
 def gdn_recurrent_step(q, k, v, alpha, beta, S, out, N, dk, dv, dtype, stream) -> int:
     return int(load().gdn_recurrent_step(q, k, v, alpha, beta, S, out, N, dk, dv, dtype, stream))
+
+
+def gdn_block_tables(seq_lens, new_lens, block_table, free_blocks, slot_map, cu_seqlens, lens_after, used, R, width,
+                     n_free, block_tokens, num_blocks, T, stream) -> int:
+    return int(load().gdn_block_tables(seq_lens, new_lens, block_table, free_blocks, slot_map, cu_seqlens, lens_after,
+                                       used, R, width, n_free, block_tokens, num_blocks, T, stream))
+
+
+def gdn_cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_stride, v_stride, T, Hkv, D, block_tokens,
+                     num_blocks, dtype, cache_format, stream) -> int:
+    return int(load().gdn_cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_stride, v_stride, T, Hkv,
+                                       D, block_tokens, num_blocks, dtype, cache_format, stream))
 
 
 # ------------------------------------------------------------- torch helpers

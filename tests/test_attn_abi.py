@@ -1,0 +1,73 @@
+"""Refusals of the attention layer's entry points, on the CPU: no call here reaches a kernel (each fails validation or
+has nothing to do)."""
+import pytest
+
+import linear_attention_sequence_gated_amd as gdn
+from linear_attention_sequence_gated_amd import gdn as raw
+
+A = 0x10000  # a 16-byte aligned fake address; validation rejects before any use
+
+
+def tables(**kw):
+    args = dict(seq_lens=A, new_lens=A, block_table=A, free_blocks=A, slot_map=A, cu_seqlens=A, lens_after=A, used=A,
+                R=4, width=8, n_free=10, block_tokens=16, num_blocks=64, T=100, stream=None)
+    args.update(kw)
+    return gdn.gdn_block_tables(**args)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(R=-1), raw.GDN_ERR_SHAPE), (dict(width=-1), raw.GDN_ERR_SHAPE), (dict(n_free=-1), raw.GDN_ERR_SHAPE),
+    (dict(T=-1), raw.GDN_ERR_SHAPE), (dict(num_blocks=-1), raw.GDN_ERR_SHAPE), (dict(block_tokens=0), raw.GDN_ERR_SHAPE),
+    (dict(R=1 << 20), raw.GDN_ERR_SHAPE), (dict(num_blocks=1 << 27), raw.GDN_ERR_SHAPE),
+    (dict(width=1 << 27), raw.GDN_ERR_SHAPE), (dict(block_tokens=48), raw.GDN_ERR_UNSUPPORTED),
+    (dict(block_tokens=8), raw.GDN_ERR_UNSUPPORTED), (dict(block_tokens=256), raw.GDN_ERR_UNSUPPORTED),
+    *((dict([(n, None)]), raw.GDN_ERR_NULL) for n in ("seq_lens", "new_lens", "block_table", "free_blocks", "slot_map",
+                                                      "cu_seqlens", "lens_after", "used")),
+    *((dict([(n, A + 4)]), raw.GDN_ERR_ALIGN) for n in ("seq_lens", "new_lens", "block_table", "free_blocks", "slot_map",
+                                                        "cu_seqlens", "lens_after", "used")),
+])
+def test_tables_argument_errors(kw, status):
+    assert tables(**kw) == status
+
+
+def append(**kw):
+    args = dict(k=A, v=A, slot_map=A, k_cache=A, v_cache=A, k_scale=A, v_scale=A, k_stride=256, v_stride=256, T=10,
+                Hkv=4, D=64, block_tokens=16, num_blocks=64, dtype=gdn.GDN_BF16, cache_format=gdn.GDN_CACHE_I8, stream=None)
+    args.update(kw)
+    return gdn.gdn_cache_append(**args)
+
+
+CACHE_ERRORS = [
+    (dict(dtype=7), raw.GDN_ERR_DTYPE), (dict(dtype=gdn.GDN_F32), raw.GDN_ERR_UNSUPPORTED),
+    (dict(dtype=gdn.GDN_C64), raw.GDN_ERR_UNSUPPORTED), (dict(cache_format=2), raw.GDN_ERR_DTYPE),
+    (dict(cache_format=-1), raw.GDN_ERR_DTYPE), (dict(Hkv=0), raw.GDN_ERR_SHAPE), (dict(D=0), raw.GDN_ERR_SHAPE),
+    (dict(num_blocks=-1), raw.GDN_ERR_SHAPE), (dict(num_blocks=1 << 27), raw.GDN_ERR_SHAPE),
+    (dict(block_tokens=0), raw.GDN_ERR_SHAPE), (dict(block_tokens=24), raw.GDN_ERR_UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("kw,status", CACHE_ERRORS + [
+    (dict(T=-1), raw.GDN_ERR_SHAPE), (dict(T=1 << 26), raw.GDN_ERR_SHAPE), (dict(D=96, k_stride=384, v_stride=384), raw.GDN_ERR_UNSUPPORTED),
+    (dict(k_stride=255), raw.GDN_ERR_SHAPE), (dict(v_stride=248), raw.GDN_ERR_SHAPE), (dict(k_stride=260), raw.GDN_ERR_SHAPE),
+    (dict(k_stride=-256), raw.GDN_ERR_SHAPE),
+    *((dict([(n, None)]), raw.GDN_ERR_NULL) for n in ("k", "v", "slot_map", "k_cache", "v_cache", "k_scale", "v_scale")),
+    *((dict([(n, A + 8)]), raw.GDN_ERR_ALIGN) for n in ("k", "v", "slot_map", "k_cache", "v_cache", "k_scale", "v_scale")),
+])
+def test_append_argument_errors(kw, status):
+    assert append(**kw) == status
+
+
+def test_append_of_nothing_is_noop():
+    none = dict(k=None, v=None, slot_map=None, k_cache=None, v_cache=None, k_scale=None, v_scale=None)
+    assert append(T=0, **none) == raw.GDN_OK
+    assert append(num_blocks=0, **none) == raw.GDN_OK
+
+
+def test_cache_helpers_refuse_on_cpu():
+    torch = pytest.importorskip("torch")
+    i = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="HIP device"):
+        gdn.block_tables(i, i, i.view(2, 2), i, 16, 4, 4)
+    x, c, s = torch.zeros(4, 1, 64, dtype=torch.bfloat16), torch.zeros(2, 1, 16, 64, dtype=torch.int8), torch.zeros(2, 1)
+    with pytest.raises(ValueError, match="HIP device"):
+        gdn.cache_append(x, x, i, c, c, s, s)
