@@ -401,6 +401,27 @@ int gdn_cache_append(const void *k, const void *v, const int *slot_map, void *k_
                      float *k_scale, float *v_scale, long long k_stride, long long v_stride, int T, int Hkv,
                      int D, int block_tokens, int num_blocks, int dtype, int cache_format, void *stream);
 
+/*
+ * Attention of one new token per request over the cache.
+ *
+ *   q          [R] rows of Hq * D, q_stride apart
+ *   block_table [R, width], seq_lens [R]: request r attends to the first
+ *              seq_lens[r] tokens of its blocks (at most width *
+ *              block_tokens).  Blocks outside [0, num_blocks) are left out.
+ *   out        [R, Hq, D] written;  lse [R, Hq] written, may be NULL
+ *
+ * A request without tokens gets zeros and an lse of -infinity.  What the cache
+ * holds behind a request's last token is never used, whatever its bits.
+ * Scales are positive and finite.  Workspace: gdn_attn_decode_workspace_bytes;
+ * scratch on entry and exit, no clearing needed.  R below 2^20.
+ */
+size_t gdn_attn_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int block_tokens, int width);
+int gdn_attn_decode(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                    const float *v_scale, const int *block_table, const int *seq_lens, void *out, float *lse,
+                    float scale, long long q_stride, int R, int Hq, int Hkv, int D, int block_tokens,
+                    int num_blocks, int width, int dtype, int cache_format, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *gdn_status_str(int status);
 

@@ -110,3 +110,39 @@ def cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=None
     _call(dev, stream, raw.load().gdn_cache_append, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), ks, vs, t, hkv, d, bt, nb,
           raw.GDN_BF16, fmt)
+
+
+def attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale: float | None = None, out=None,
+                lse=None, workspace=None, stream=None):
+    """Attention of one new token per request, q [R, Hq, D] bf16, over the first seq_lens [R] tokens of its blocks
+    block_table [R, width] (int32) in the cache (see cache_append).  scale: 1 / sqrt(D) unless given.
+
+    Returns (out [R, Hq, D] bf16, lse [R, Hq] float32).  The workspace is allocated here unless one of at least
+    gdn_attn_decode_workspace_bytes(...) bytes is passed.
+    """
+    dev = _device(q, "attn_decode")
+    nb, hkv, bt, d, fmt = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    r, hq, _ = q.shape
+    width = block_table.shape[1]
+    qs = _rows(q, "q", (r, hq, d), dev)
+    _dense(block_table, "block_table", (r, width), _I32, dev)
+    _dense(seq_lens, "seq_lens", (r,), _I32, dev)
+    if out is None:
+        out = torch.empty((r, hq, d), dtype=_BF16, device=dev)
+    else:
+        _dense(out, "out", (r, hq, d), _BF16, dev)
+    if lse is None:
+        lse = torch.empty((r, hq), dtype=_F32, device=dev)
+    else:
+        _dense(lse, "lse", (r, hq), _F32, dev)
+    lib = raw.load()
+    need = lib.gdn_attn_decode_workspace_bytes(r, hq, hkv, d, bt, width)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous on the device of q")
+    _call(dev, stream, lib.gdn_attn_decode, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+          v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+          d ** -0.5 if scale is None else scale, qs, r, hq, hkv, d, bt, nb, width, raw.GDN_BF16, fmt,
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out, lse

@@ -34,6 +34,21 @@ int cache_shape(int Hkv, int D, int bt, int num_blocks) {
   return GDN_OK;
 }
 
+// Heads: whole groups, and few enough for the launches.
+int heads_shape(int Hq, int Hkv, int D) {
+  if (Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv || Hq >= (1 << 20)) return GDN_ERR_SHAPE;
+  return D == 64 || D == 128 ? GDN_OK : GDN_ERR_UNSUPPORTED;
+}
+
+int decode_shape(int R, int Hq, int Hkv, int D, int bt, int width) {
+  if (R < 0 || width < 0 || bt <= 0 || R >= kMaxRequests || (long long)width * bt >= (1LL << 31)) return GDN_ERR_SHAPE;
+  if (const int s = heads_shape(Hq, Hkv, D)) return s;
+  if ((long long)R * Hq >= (1LL << 24)) return GDN_ERR_SHAPE;  // one workgroup of 256 joins one (request, head)
+  // the units of 128 tokens over all requests stay 32-bit numbers
+  if (((long long)width * bt + 127) / 128 * R >= (1LL << 31)) return GDN_ERR_SHAPE;
+  return block_ok(bt) ? GDN_OK : GDN_ERR_UNSUPPORTED;
+}
+
 }  // namespace
 
 extern "C" {
@@ -69,6 +84,33 @@ int gdn_cache_append(const void* k, const void* v, const int* slot_map, void* k_
   if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
   return status(gdn::launch_cache_append({k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_stride, v_stride, T,
                                           Hkv, D, block_tokens, num_blocks, cache_format, stream}));
+}
+
+size_t gdn_attn_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int block_tokens, int width) {
+  if (decode_shape(R, Hq, Hkv, D, block_tokens, width)) return 0;
+  return gdn::attn_decode_workspace_bytes(R, Hq, Hkv, D, block_tokens, width);
+}
+
+int gdn_attn_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                    const float* v_scale, const int* block_table, const int* seq_lens, void* out, float* lse,
+                    float scale, long long q_stride, int R, int Hq, int Hkv, int D, int block_tokens, int num_blocks,
+                    int width, int dtype, int cache_format, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!known_dtype(dtype)) return GDN_ERR_DTYPE;
+  if (cache_format != GDN_CACHE_I8 && cache_format != GDN_CACHE_E4M3) return GDN_ERR_DTYPE;
+  if (const int s = cache_shape(Hkv, D, block_tokens, num_blocks)) return s;
+  if (const int s = decode_shape(R, Hq, Hkv, D, block_tokens, width)) return s;
+  if (dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+  if (!stride_ok(q_stride, (long long)Hq * D)) return GDN_ERR_SHAPE;
+  if (R == 0) return GDN_OK;
+  if (!q || !seq_lens || !out || (width && !block_table)) return GDN_ERR_NULL;
+  if (num_blocks && (!k_cache || !v_cache || !k_scale || !v_scale)) return GDN_ERR_NULL;
+  const void* ptrs[] = {q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse, workspace};
+  if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
+  const size_t need = gdn::attn_decode_workspace_bytes(R, Hq, Hkv, D, block_tokens, width);
+  if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+  return status(gdn::launch_attn_decode({q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse,
+                                         static_cast<float*>(workspace), scale, q_stride, R, Hq, Hkv, D, block_tokens,
+                                         num_blocks, width, cache_format, stream}));
 }
 
 }  // extern "C"

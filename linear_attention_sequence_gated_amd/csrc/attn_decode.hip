@@ -1,0 +1,528 @@
+// attn_decode.hip -- attention of one new token per request over the 8-bit
+// paged cache.
+//
+// For a request's n tokens and one key head, with codes kc, vc and the scales
+// ks, vs of the token's block,
+//   s_j = scale ks_j (q . kc_j),   o = sum_j e^(s_j) vs_j vc_j / sum_j e^(s_j).
+// The cache is read once (2 D bytes per token and head); everything else is
+// small, so the kernel is bound by HBM and is built to keep loads in flight.
+//
+// Work is counted in units of 128 tokens of one (request, head) and dealt out
+// in equal contiguous shares to a fixed number of workgroups, whatever the
+// lengths: a long request is split over many workgroups and short ones are
+// taken several to a workgroup.  The shares follow from the lengths, which
+// only the device knows, so every workgroup finds its own with a prefix sum.
+// A workgroup that covers all of a (request, head) writes the result;
+// otherwise it writes its sums, its share's maximum included, and a second
+// launch joins them in the order of the tokens.
+//
+// The query heads that share a key head (up to 16 at a time) are the columns of
+// the products: S^T = K Q^T and O^T = V^T P^T, both 16x16x32 in fp16.  The
+// accumulator layout of S^T is the operand layout of P^T, so probabilities
+// never leave their lane.  Codes are exact in fp16 (int8 through u 2^-10 -
+// 128 2^-10, one packed multiply-add for two); q is moved into fp16's range by
+// a power of two per head, which is exact down to 2^-28 of its largest entry.
+// The running maximum m is that of s_j + log2 vs_j, so that the weights
+// p_j = 2^(s_j - m) vs_j that are rounded to fp16 (half an ulp: 2^-12) are at
+// most one whatever the blocks' scales; the denominator sums 2^(s_j - m) in
+// float32.
+#include <hip/hip_bf16.h>
+
+#include "../../include/gdn.h"
+#include "gdn_attn.hpp"
+#include "gdn_launch.hpp"
+#include "gdn_pipe.hpp"
+
+namespace gdn {
+namespace {
+
+using pipe::make_rsrc;
+using pipe::u32x2;
+using pipe::u32x4;
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+
+constexpr int kUnit = 128, kWaves = 4, kTile = kUnit / kWaves;  // tokens of a unit, of a wave's tile
+constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
+constexpr float kLowest = -3e38f;  // running maximum before the first token
+constexpr float kCodeUp = 1024.f;  // int8 codes enter the products times 2^-10
+
+struct DecodeSizes {
+  int R, Hq, Hkv, G, NG, Gc, bt, width, num_blocks, W;
+};
+
+// Tokens of a request that its table row can hold.
+__device__ __forceinline__ int tokens_of(const int* lens, int r, const DecodeSizes& z) {
+  const int n = lens[r];
+  const long long most = (long long)z.width * z.bt;
+  return n <= 0 ? 0 : (n < most ? n : (int)most);
+}
+__device__ __forceinline__ int units_of(int n) { return (n + kUnit - 1) / kUnit; }
+
+__device__ __forceinline__ int wave_scan(int x) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d);
+    if ((int)(threadIdx.x & 63) >= d) x += y;
+  }
+  return x;
+}
+
+// Two int8 codes (offset by 128), zero-extended to 16 bits, as fp16 times 2^-10.
+__device__ __forceinline__ unsigned i8_f16(unsigned w) {
+  const f16x2 up{(_Float16)16384.f, (_Float16)16384.f}, off{(_Float16)-0.125f, (_Float16)-0.125f};
+  return __builtin_bit_cast(unsigned, __builtin_elementwise_fma(__builtin_bit_cast(f16x2, w), up, off));
+}
+template <bool HI> __device__ __forceinline__ unsigned e4m3_f16(unsigned w) {
+  return __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.f, HI));
+}
+
+// Eight consecutive codes as an fp16 operand.
+template <int FMT> __device__ __forceinline__ f16x8 codes8(unsigned a, unsigned b) {
+  u32x4 r;
+  if constexpr (FMT == GDN_CACHE_I8) {
+    a ^= 0x80808080u;
+    b ^= 0x80808080u;
+    r[0] = i8_f16(__builtin_amdgcn_perm(0u, a, 0x0c010c00u));
+    r[1] = i8_f16(__builtin_amdgcn_perm(0u, a, 0x0c030c02u));
+    r[2] = i8_f16(__builtin_amdgcn_perm(0u, b, 0x0c010c00u));
+    r[3] = i8_f16(__builtin_amdgcn_perm(0u, b, 0x0c030c02u));
+  } else {
+    r[0] = e4m3_f16<false>(a);
+    r[1] = e4m3_f16<true>(a);
+    r[2] = e4m3_f16<false>(b);
+    r[3] = e4m3_f16<true>(b);
+  }
+  return __builtin_bit_cast(f16x8, r);
+}
+
+// Four rows of four codes (row j in w[j]) as four columns: out[i] holds code i
+// of the four rows as fp16 (two words).
+template <int FMT> __device__ __forceinline__ void columns4(const unsigned (&w)[4], u32x2 (&out)[4]) {
+  if constexpr (FMT == GDN_CACHE_I8) {
+    unsigned x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = w[j] ^ 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned sel = 0x0c000c00u | (unsigned)i | ((unsigned)(4 + i) << 16);
+      out[i] = u32x2{i8_f16(__builtin_amdgcn_perm(x[1], x[0], sel)), i8_f16(__builtin_amdgcn_perm(x[3], x[2], sel))};
+    }
+  } else {
+    // bytes (0, 1) and (2, 3) of the row pairs, then the pairs side by side
+    const unsigned a01 = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), a23 = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+    const unsigned b01 = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u), b23 = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+    out[0] = u32x2{e4m3_f16<false>(a01), e4m3_f16<false>(b01)};
+    out[1] = u32x2{e4m3_f16<true>(a01), e4m3_f16<true>(b01)};
+    out[2] = u32x2{e4m3_f16<false>(a23), e4m3_f16<false>(b23)};
+    out[3] = u32x2{e4m3_f16<true>(a23), e4m3_f16<true>(b23)};
+  }
+}
+
+// A wave's tile of 32 tokens: two halves of 16, which may lie in two blocks.
+// Lane (g, c) holds of half j the codes 16 g .. (D = 64) or 32 g .. (D = 128)
+// of token c for K, and NB codes from NB c on of tokens 4 g + i for V.
+template <int D> struct Tile {
+  static constexpr int KW = D / 16, VW = D / 64, NB = D / 16;  // words
+  unsigned k[2][KW];
+  unsigned v[2][4][VW];
+  float ks[2], vs[2];
+  int n[2];  // tokens of the half that count
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(Tile<D>& t, int tok, int n, const int* row, int h, const DecodeArgs& a,
+                                          const DecodeSizes& z) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int sh = __builtin_ctz(z.bt);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int p = tok + 16 * j;
+    int left = n - p;
+    left = left < 0 ? 0 : (left > 16 ? 16 : left);
+    int id = left ? row[p >> sh] : 0;
+    if (id < 0 || id >= z.num_blocks) left = 0;
+    if (!left) id = 0;
+    const size_t tile = (size_t)id * z.Hkv + h;
+    const size_t at = (tile * z.bt + (p & (z.bt - 1))) * D;
+    const __amdgpu_buffer_rsrc_t rk = make_rsrc(static_cast<const char*>(a.k_cache) + at, left * D);
+    const __amdgpu_buffer_rsrc_t rv = make_rsrc(static_cast<const char*>(a.v_cache) + at, left * D);
+    t.n[j] = left;
+    t.ks[j] = left ? a.k_scale[tile] : 0.f;
+    t.vs[j] = left ? a.v_scale[tile] : 1.f;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const u32x4 w = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(rk, c * D + (D / 4) * g + 16 * i, 0, 0));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t.k[j][4 * i + e] = w[e];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int off = (4 * g + i) * D + (D / 16) * c;
+      if constexpr (D == 64) {
+        t.v[j][i][0] = __builtin_amdgcn_raw_buffer_load_b32(rv, off, 0, 0);
+      } else {
+        const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rv, off, 0, 0));
+        t.v[j][i][0] = w[0];
+        t.v[j][i][1] = w[1];
+      }
+    }
+  }
+}
+
+// What a wave carries over the tokens of a (request, head): lane (g, c) has
+// column c (a query head), rows NB (4 g + r) + i of O^T in acc[i][r].
+template <int D> struct Sums {
+  f32x4 acc[D / 16];
+  float m, l;  // m is shared by the lanes of a column, l is the lane's own part
+};
+
+template <int D, int FMT>
+__device__ __forceinline__ void take_tile(Sums<D>& s, const Tile<D>& t, const f16x8 (&q)[D / 32], float qfac) {
+  constexpr int NB = D / 16;
+  const int g = (threadIdx.x & 63) >> 4;
+  float x[2][4], top = kLowest;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    f32x4 y = pipe::zero4();
+#pragma unroll
+    for (int ks = 0; ks < D / 32; ++ks)
+      y = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes8<FMT>(t.k[j][2 * ks], t.k[j][2 * ks + 1]), q[ks], y, 0, 0, 0);
+    const float f = qfac * t.ks[j];
+    const float lv = __builtin_amdgcn_logf(t.vs[j]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[j][i] = 4 * g + i < t.n[j] ? y[i] * f : -INFINITY;
+      top = fmaxf(top, x[j][i] + lv);
+    }
+  }
+  top = fmaxf(top, __shfl_xor(top, 16));
+  top = fmaxf(top, __shfl_xor(top, 32));
+  const float m = fmaxf(s.m, top);
+  if (__any(m != s.m)) {
+    const float c = __builtin_amdgcn_exp2f(s.m - m);
+    s.l *= c;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) s.acc[i] *= c;
+    s.m = m;
+  }
+  f16x8 p;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float e = __builtin_amdgcn_exp2f(x[j][i] - m);
+      s.l += e;
+      p[4 * j + i] = (_Float16)(e * t.vs[j]);
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < D / 64; ++w) {
+    u32x2 col[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const unsigned rows[4] = {t.v[j][0][w], t.v[j][1][w], t.v[j][2][w], t.v[j][3][w]};
+      columns4<FMT>(rows, col[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32x4 v{col[0][i][0], col[0][i][1], col[1][i][0], col[1][i][1]};
+      s.acc[4 * w + i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, v), p, s.acc[4 * w + i], 0, 0, 0);
+    }
+  }
+}
+
+template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a, DecodeSizes z) {
+  constexpr int NB = D / 16, LD = D + 4;
+  __shared__ float part[kWaves][16][LD];
+  __shared__ float ml[kWaves][2][16];
+  __shared__ int scan[kWaves], found[2];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, c = lane & 15;
+  const int heads = z.Hkv * z.NG;
+
+  // this workgroup's share [u0, u1) of the units, and the request it starts in
+  const int per = (z.R + 255) / 256, ra = tid * per;
+  int mine = 0;
+  for (int i = 0; i < per; ++i)
+    if (ra + i < z.R) mine += units_of(tokens_of(a.seq_lens, ra + i, z));
+  const int incl = wave_scan(mine);
+  if (lane == 63) scan[wave] = incl;
+  __syncthreads();
+  int before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) before += scan[w];
+    total += scan[w];
+  }
+  const long long U = (long long)total * heads;
+  const long long u0 = U * blockIdx.x / z.W, u1 = U * (blockIdx.x + 1) / z.W;
+  if (u0 >= u1) return;
+  if (u0 >= (long long)before * heads && u0 < (long long)(before + mine) * heads) {
+    int r = ra, at = before;
+    for (;; ++r) {
+      const int nu = units_of(tokens_of(a.seq_lens, r, z));
+      if (u0 < (long long)(at + nu) * heads) break;
+      at += nu;
+    }
+    found[0] = r;
+    found[1] = at;
+  }
+  __syncthreads();
+  int r = __builtin_amdgcn_readfirstlane(found[0]);
+  long long base = (long long)__builtin_amdgcn_readfirstlane(found[1]) * heads;  // first unit of request r
+
+  bool first = true;
+  for (long long u = u0; u < u1;) {
+    const int n = tokens_of(a.seq_lens, r, z), nu = units_of(n);
+    const int hh = (int)((u - base) / nu), h = hh / z.NG, q0 = h * z.G + (hh - h * z.NG) * 16;
+    const int cols = min(16, (h + 1) * z.G - q0);
+    const int ua = (int)(u - base - (long long)hh * nu);                       // units of (r, hh): [ua, ub)
+    const int ub = (int)min((long long)nu, ua + (u1 - u));
+    const int* row = a.block_table + (size_t)r * z.width;
+
+    // query operands, moved into fp16's range
+    f16x8 q[D / 32];
+    float qfac;
+    {
+      const __hip_bfloat16* src =
+          static_cast<const __hip_bfloat16*>(a.q) + (long long)r * a.qs + (long long)(q0 + min(c, cols - 1)) * D;
+      u32x4 w[D / 32];
+      float top = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < D / 32; ++ks) {
+        w[ks] = *reinterpret_cast<const u32x4*>(src + (D / 4) * g + 8 * ks);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(pipe::lo_f(w[ks][e])), fabsf(pipe::hi_f(w[ks][e]))));
+      }
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const int e2 = __builtin_amdgcn_frexp_expf(top);
+      const float down = __builtin_amdgcn_ldexpf(1.f, 14 - e2 > 126 ? 126 : 14 - e2);
+      qfac = a.scale * kLog2e / down * (FMT == GDN_CACHE_I8 ? kCodeUp : 1.f);
+#pragma unroll
+      for (int ks = 0; ks < D / 32; ++ks)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          q[ks][2 * e] = (_Float16)(pipe::lo_f(w[ks][e]) * down);
+          q[ks][2 * e + 1] = (_Float16)(pipe::hi_f(w[ks][e]) * down);
+        }
+    }
+
+    Sums<D> s;
+    s.m = kLowest;
+    s.l = 0.f;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) s.acc[i] = pipe::zero4();
+    const int end = min(n, ub * kUnit);
+    Tile<D> t0, t1;
+    int tok = ua * kUnit + wave * kTile;
+    if (tok < end) {
+      load_tile<D>(t0, tok, end, row, h, a, z);
+      for (;;) {
+        if (tok + kUnit < end) load_tile<D>(t1, tok + kUnit, end, row, h, a, z);
+        take_tile<D, FMT>(s, t0, q, qfac);
+        tok += kUnit;
+        if (tok >= end) break;
+        if (tok + kUnit < end) load_tile<D>(t0, tok + kUnit, end, row, h, a, z);
+        take_tile<D, FMT>(s, t1, q, qfac);
+        tok += kUnit;
+        if (tok >= end) break;
+      }
+    }
+
+    // join the waves
+    s.l += __shfl_xor(s.l, 16);
+    s.l += __shfl_xor(s.l, 32);
+    if (lane < 16) {
+      ml[wave][0][c] = s.m;
+      ml[wave][1][c] = s.l;
+    }
+    __syncthreads();
+    float M = ml[0][0][c];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) M = fmaxf(M, ml[w][0][c]);
+    float L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) L += ml[w][1][c] * __builtin_amdgcn_exp2f(ml[w][0][c] - M);
+    const float mine_w = __builtin_amdgcn_exp2f(s.m - M) * (FMT == GDN_CACHE_I8 ? kCodeUp : 1.f);
+    if (c < cols) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int w = 0; w < NB / 4; ++w)
+          *reinterpret_cast<f32x4*>(&part[wave][c][NB * (4 * g + i) + 4 * w]) =
+              f32x4{s.acc[4 * w][i] * mine_w, s.acc[4 * w + 1][i] * mine_w, s.acc[4 * w + 2][i] * mine_w,
+                    s.acc[4 * w + 3][i] * mine_w};
+    }
+    const bool whole = ua == 0 && ub == nu;
+    const size_t slot = 2 * (size_t)blockIdx.x + (first ? 0 : 1);
+    float* o_ws = a.ws + slot * z.Gc * (D + 2);
+    if (wave == 0 && lane < cols) {
+      if (whole) {
+        if (a.lse) a.lse[(size_t)r * z.Hq + q0 + lane] = L > 0.f ? (M + __builtin_amdgcn_logf(L)) * kLn2 : -INFINITY;
+      } else {
+        o_ws[z.Gc * D + 2 * lane] = M;
+        o_ws[z.Gc * D + 2 * lane + 1] = L;
+      }
+    }
+    __syncthreads();
+    for (int x = tid; x < cols * D / 4; x += 256) {
+      const int col = x / (D / 4), d = 4 * (x % (D / 4));
+      f32x4 o = pipe::zero4();
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) o += *reinterpret_cast<const f32x4*>(&part[w][col][d]);
+      if (whole) {
+        float Mc = ml[0][0][col], Lc = 0.f;
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) Mc = fmaxf(Mc, ml[w][0][col]);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) Lc += ml[w][1][col] * __builtin_amdgcn_exp2f(ml[w][0][col] - Mc);
+        const float inv = Lc > 0.f ? 1.f / Lc : 0.f;
+        o *= inv;
+        *reinterpret_cast<u32x2*>(static_cast<__bf16*>(a.out) + ((size_t)r * z.Hq + q0 + col) * D + d) = pipe::cvt4(o);
+      } else {
+        *reinterpret_cast<f32x4*>(o_ws + col * D + d) = o;
+      }
+    }
+    __syncthreads();
+    first = false;
+    u += ub - ua;
+    if (u < u1 && u >= base + (long long)nu * heads) {  // the next request that has tokens
+      base += (long long)nu * heads;
+      for (++r;; r += 64) {
+        const unsigned long long some = __ballot(r + lane < z.R && tokens_of(a.seq_lens, min(r + lane, z.R - 1), z) > 0);
+        if (some) {
+          r += __builtin_ctzll(some);
+          break;
+        }
+      }
+      r = __builtin_amdgcn_readfirstlane(r);
+    }
+  }
+}
+
+// Joins the shares of one (request, query head), in the order of the tokens;
+// heads that one workgroup covered are done already.  Requests without tokens
+// get their zeros here.
+template <int D> __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs a, DecodeSizes z) {
+  constexpr int NP = 256 / (D / 4);  // shares taken side by side
+  __shared__ float sum[NP][D];
+  __shared__ float red[4];
+  __shared__ int scan[2][kWaves];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int r = blockIdx.x / z.Hq, hq = blockIdx.x % z.Hq, h = hq / z.G, in = hq - h * z.G, hh = h * z.NG + in / 16, col = in % 16;
+  const int n = tokens_of(a.seq_lens, r, z), nu = units_of(n), heads = z.Hkv * z.NG;
+  __bf16* out = static_cast<__bf16*>(a.out) + ((size_t)r * z.Hq + hq) * D;
+  if (nu == 0) {
+    if (tid < D / 4) *reinterpret_cast<u32x2*>(out + 4 * tid) = u32x2{0u, 0u};
+    if (tid == 0 && a.lse) a.lse[(size_t)r * z.Hq + hq] = -INFINITY;
+    return;
+  }
+  int all = 0, pre = 0;
+  for (int i = tid; i < z.R; i += 256) {
+    const int x = units_of(tokens_of(a.seq_lens, i, z));
+    all += x;
+    pre += i < r ? x : 0;
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    all += __shfl_xor(all, d);
+    pre += __shfl_xor(pre, d);
+  }
+  if (lane == 0) {
+    scan[0][wave] = all;
+    scan[1][wave] = pre;
+  }
+  __syncthreads();
+  all = scan[0][0] + scan[0][1] + scan[0][2] + scan[0][3];
+  pre = scan[1][0] + scan[1][1] + scan[1][2] + scan[1][3];
+  const long long U = (long long)all * heads, P = (long long)pre * heads + (long long)hh * nu;
+  // the workgroup that takes unit x: the first whose share ends past it
+  auto taker = [&](long long x) { return (int)(((x + 1) * z.W + U - 1) / U - 1); };
+  const int i0 = taker(P), i1 = taker(P + nu - 1);
+  if (i0 == i1) return;
+  auto at = [&](int i) {
+    const bool head_of_share = U * i / z.W >= P;
+    return a.ws + (2 * (size_t)i + (head_of_share ? 0 : 1)) * z.Gc * (D + 2);
+  };
+  float M = kLowest;
+  for (int i = i0 + tid; i <= i1; i += 256)
+    if (U * i / z.W < U * (i + 1) / z.W) M = fmaxf(M, at(i)[z.Gc * D + 2 * col]);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) M = fmaxf(M, __shfl_xor(M, d));
+  if (lane == 0) red[wave] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const int part = tid / (D / 4), d = 4 * (tid % (D / 4));
+  f32x4 o = pipe::zero4();
+  float L = 0.f;
+#pragma unroll 4
+  for (int i = i0 + part; i <= i1; i += NP) {
+    if (U * i / z.W >= U * (i + 1) / z.W) continue;  // a share without units
+    const float* w = at(i);
+    const float e = __builtin_amdgcn_exp2f(w[z.Gc * D + 2 * col] - M);
+    L += e * w[z.Gc * D + 2 * col + 1];
+    o += *reinterpret_cast<const f32x4*>(w + col * D + d) * e;
+  }
+  *reinterpret_cast<f32x4*>(&sum[part][d]) = o;
+  __shared__ float ls[NP];
+  if (d == 0) ls[part] = L;
+  __syncthreads();
+  if (tid < D / 4) {
+    L = 0.f;
+    o = pipe::zero4();
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      L += ls[p];
+      o += *reinterpret_cast<const f32x4*>(&sum[p][4 * tid]);
+    }
+    o *= L > 0.f ? 1.f / L : 0.f;
+    *reinterpret_cast<u32x2*>(out + 4 * tid) = pipe::cvt4(o);
+    if (tid == 0 && a.lse) a.lse[(size_t)r * z.Hq + hq] = L > 0.f ? (M + __builtin_amdgcn_logf(L)) * kLn2 : -INFINITY;
+  }
+}
+
+DecodeSizes sizes(int R, int Hq, int Hkv, int D, int bt, int width, int num_blocks) {
+  DecodeSizes z{};
+  z.R = R;
+  z.Hq = Hq;
+  z.Hkv = Hkv;
+  z.G = Hq / Hkv;
+  z.NG = (z.G + 15) / 16;
+  z.Gc = z.G < 16 ? z.G : 16;
+  z.bt = bt;
+  z.width = width;
+  z.num_blocks = num_blocks;
+  // what the CUs hold at once (three workgroups of the 139 registers that
+  // d = 64 takes, two at d = 128), and no more than there can be units
+  const long long units = ((long long)width * bt + kUnit - 1) / kUnit * R * Hkv * z.NG;
+  const int most = 256 * (D == 64 ? 3 : 2);
+  z.W = units < most ? (int)units : most;
+  return z;
+}
+
+template <int D, int FMT> hipError_t launch(const DecodeArgs& a, const DecodeSizes& z) {
+  hipStream_t st = static_cast<hipStream_t>(a.stream);
+  if (z.W) {
+    const hipError_t e = launch_kernel(attn_decode_kernel<D, FMT>, dim3(z.W), dim3(256), st, a, z);
+    if (e != hipSuccess) return e;
+  }
+  return launch_kernel(attn_decode_join_kernel<D>, dim3(z.R * z.Hq), dim3(256), st, a, z);
+}
+
+}  // namespace
+
+size_t attn_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int bt, int width) {
+  const DecodeSizes z = sizes(R, Hq, Hkv, D, bt, width, 0);
+  return ((size_t)2 * z.W * z.Gc * (D + 2) * sizeof(float) + 15) / 16 * 16;
+}
+
+hipError_t launch_attn_decode(const DecodeArgs& a) {
+  const DecodeSizes z = sizes(a.R, a.Hq, a.Hkv, a.D, a.bt, a.width, a.num_blocks);
+  if (a.fmt == GDN_CACHE_I8)
+    return a.D == 64 ? launch<64, GDN_CACHE_I8>(a, z) : launch<128, GDN_CACHE_I8>(a, z);
+  return a.D == 64 ? launch<64, GDN_CACHE_E4M3>(a, z) : launch<128, GDN_CACHE_E4M3>(a, z);
+}
+
+}  // namespace gdn

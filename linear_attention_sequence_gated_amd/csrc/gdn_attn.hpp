@@ -37,4 +37,23 @@ struct AppendArgs {
 };
 hipError_t launch_cache_append(const AppendArgs& a);
 
+struct DecodeArgs {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int* block_table;
+  const int* seq_lens;
+  void* out;
+  float* lse;
+  float* ws;
+  float scale;
+  long long qs;
+  int R, Hq, Hkv, D, bt, num_blocks, width, fmt;
+  void* stream;
+};
+size_t attn_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int bt, int width);
+hipError_t launch_attn_decode(const DecodeArgs& a);
+
 }  // namespace gdn

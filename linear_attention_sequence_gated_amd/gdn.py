@@ -27,7 +27,7 @@ GDN_NOALLOC_MAX_WORKSPACE = 128 << 20  # include/gdn.h
 EXPORTS = ("gdn_chunk_fwd_workspace_bytes", "gdn_chunk_fwd", "gdn_chunk_fwd_prologue_workspace_bytes",
            "gdn_chunk_fwd_prologue", "gdn_chunk_bwd_workspace_bytes",
            "gdn_chunk_bwd", "gdn_fwd_channel_decay", "gdn_recurrent_step", "gdn_status_str", "gdn_chunk_fwd_noalloc",
-           "gdn_block_tables", "gdn_cache_append")
+           "gdn_block_tables", "gdn_cache_append", "gdn_attn_decode_workspace_bytes", "gdn_attn_decode")
 
 _lib = None
 
@@ -71,6 +71,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.gdn_block_tables.restype = ci
     lib.gdn_cache_append.argtypes = [vp] * 7 + [ll] * 2 + [ci] * 7 + [vp]
     lib.gdn_cache_append.restype = ci
+    lib.gdn_attn_decode_workspace_bytes.argtypes = [ci] * 6
+    lib.gdn_attn_decode_workspace_bytes.restype = sz
+    lib.gdn_attn_decode.argtypes = [vp] * 9 + [fl, ll] + [ci] * 9 + [vp, sz, vp]
+    lib.gdn_attn_decode.restype = ci
     lib.gdn_status_str.argtypes = [ci]
     lib.gdn_status_str.restype = ctypes.c_char_p
     if path is None:
@@ -137,6 +141,18 @@ def gdn_cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_strid
                      num_blocks, dtype, cache_format, stream) -> int:
     return int(load().gdn_cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_stride, v_stride, T, Hkv,
                                        D, block_tokens, num_blocks, dtype, cache_format, stream))
+
+
+def gdn_attn_decode_workspace_bytes(R, Hq, Hkv, D, block_tokens, width) -> int:
+    return int(load().gdn_attn_decode_workspace_bytes(R, Hq, Hkv, D, block_tokens, width))
+
+
+def gdn_attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse, scale, q_stride, R, Hq,
+                    Hkv, D, block_tokens, num_blocks, width, dtype, cache_format, workspace, workspace_bytes,
+                    stream) -> int:
+    return int(load().gdn_attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse, scale,
+                                      q_stride, R, Hq, Hkv, D, block_tokens, num_blocks, width, dtype, cache_format,
+                                      workspace, workspace_bytes, stream))
 
 
 # ------------------------------------------------------------- torch helpers

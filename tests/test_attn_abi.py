@@ -63,6 +63,37 @@ def test_append_of_nothing_is_noop():
     assert append(num_blocks=0, **none) == raw.GDN_OK
 
 
+def decode(**kw):
+    args = dict(q=A, k_cache=A, v_cache=A, k_scale=A, v_scale=A, block_table=A, seq_lens=A, out=A, lse=A, scale=0.125,
+                q_stride=512, R=3, Hq=8, Hkv=4, D=64, block_tokens=16, num_blocks=64, width=9, dtype=gdn.GDN_BF16,
+                cache_format=gdn.GDN_CACHE_I8, workspace=A, workspace_bytes=1 << 40, stream=None)
+    args.update(kw)
+    return gdn.gdn_attn_decode(**args)
+
+
+@pytest.mark.parametrize("kw,status", CACHE_ERRORS + [
+    (dict(R=-1), raw.GDN_ERR_SHAPE), (dict(R=1 << 20), raw.GDN_ERR_SHAPE), (dict(width=-1), raw.GDN_ERR_SHAPE),
+    (dict(width=1 << 27), raw.GDN_ERR_SHAPE), (dict(Hq=6), raw.GDN_ERR_SHAPE), (dict(Hq=0), raw.GDN_ERR_SHAPE),
+    (dict(R=1 << 19, Hq=64, q_stride=4096), raw.GDN_ERR_SHAPE), (dict(R=1 << 18, width=1 << 26), raw.GDN_ERR_SHAPE),
+    (dict(D=32), raw.GDN_ERR_UNSUPPORTED), (dict(q_stride=504), raw.GDN_ERR_SHAPE), (dict(q_stride=516), raw.GDN_ERR_SHAPE),
+    *((dict([(n, None)]), raw.GDN_ERR_NULL) for n in ("q", "k_cache", "v_cache", "k_scale", "v_scale", "block_table",
+                                                      "seq_lens", "out")),
+    *((dict([(n, A + 8)]), raw.GDN_ERR_ALIGN) for n in ("q", "k_cache", "v_cache", "k_scale", "v_scale", "block_table",
+                                                        "seq_lens", "out", "lse", "workspace")),
+    (dict(workspace=None), raw.GDN_ERR_WORKSPACE), (dict(workspace_bytes=0), raw.GDN_ERR_WORKSPACE),
+])
+def test_decode_argument_errors(kw, status):
+    assert decode(**kw) == status
+
+
+def test_decode_workspace():
+    need = gdn.gdn_attn_decode_workspace_bytes(3, 8, 4, 64, 16, 9)  # 2 units of 128 tokens x 3 x 4, two shares each
+    assert need == 2 * 24 * 2 * 66 * 4
+    assert decode(workspace_bytes=need - 1) == raw.GDN_ERR_WORKSPACE
+    assert gdn.gdn_attn_decode_workspace_bytes(3, 8, 3, 64, 16, 9) == 0  # unsupported arguments
+    assert decode(R=0, q=None, seq_lens=None, out=None) == raw.GDN_OK
+
+
 def test_cache_helpers_refuse_on_cpu():
     torch = pytest.importorskip("torch")
     i = torch.zeros(4, dtype=torch.int32)
@@ -71,3 +102,5 @@ def test_cache_helpers_refuse_on_cpu():
     x, c, s = torch.zeros(4, 1, 64, dtype=torch.bfloat16), torch.zeros(2, 1, 16, 64, dtype=torch.int8), torch.zeros(2, 1)
     with pytest.raises(ValueError, match="HIP device"):
         gdn.cache_append(x, x, i, c, c, s, s)
+    with pytest.raises(ValueError, match="HIP device"):
+        gdn.attn_decode(x, c, c, s, s, i.view(4, 1), i)
