@@ -422,6 +422,24 @@ int gdn_attn_decode(const void *q, const void *k_cache, const void *v_cache, con
                     int num_blocks, int width, int dtype, int cache_format, void *workspace,
                     size_t workspace_bytes, void *stream);
 
+/*
+ * Causal attention over whole prompts, packed one after the other.
+ *
+ *   q, k, v    [T] rows of Hq * D, Hkv * D, Hkv * D
+ *   cu_seqlens [R + 1] ascending: sequence r is the rows cu_seqlens[r] to
+ *              cu_seqlens[r + 1] - 1; row i attends to the rows of its
+ *              sequence up to itself.  Lengths of zero are fine.
+ *   out        [T, Hq, D] written;  lse [Hq, T] written
+ *
+ * Rows in no sequence (before cu_seqlens[0], from cu_seqlens[R] on) are left
+ * as they were, in out and lse.  Values of masked
+ * keys and rows never reach a result, whatever they are.  T * Hq and the row
+ * strides are below 2^28 and 2^24.
+ */
+int gdn_attn_prompt(const void *q, const void *k, const void *v, const int *cu_seqlens, void *out, float *lse,
+                    float scale, long long q_stride, long long k_stride, long long v_stride, int T, int R, int Hq,
+                    int Hkv, int D, int dtype, void *stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *gdn_status_str(int status);
 

@@ -146,3 +146,36 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, sc
           d ** -0.5 if scale is None else scale, qs, r, hq, hkv, d, bt, nb, width, raw.GDN_BF16, fmt,
           workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out, lse
+
+
+def _prompt(q, k, v, cu_seqlens, who):
+    dev = _device(q, who)
+    t, hq, d = q.shape
+    hkv = k.shape[1]
+    _dense(cu_seqlens, "cu_seqlens", (cu_seqlens.numel(),), _I32, dev)
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens: needs at least one entry")
+    strides = _rows(q, "q", (t, hq, d), dev), _rows(k, "k", (t, hkv, d), dev), _rows(v, "v", (t, hkv, d), dev)
+    return dev, t, cu_seqlens.numel() - 1, hq, hkv, d, strides
+
+
+def attn_prompt(q, k, v, cu_seqlens, scale: float | None = None, out=None, lse=None, stream=None):
+    """Causal attention over packed prompts: q [T, Hq, D], k, v [T, Hkv, D] bf16, cu_seqlens [R + 1] int32 the offsets
+    of the sequences.  scale: 1 / sqrt(D) unless given.
+
+    Returns (out [T, Hq, D] bf16, lse [Hq, T] float32).  Rows in no sequence are not written; outputs that are
+    allocated here hold zeros there.
+    """
+    dev, t, r, hq, hkv, d, strides = _prompt(q, k, v, cu_seqlens, "attn_prompt")
+    if out is None:
+        out = torch.zeros((t, hq, d), dtype=_BF16, device=dev)
+    else:
+        _dense(out, "out", (t, hq, d), _BF16, dev)
+    if lse is None:
+        lse = torch.zeros((hq, t), dtype=_F32, device=dev)
+    else:
+        _dense(lse, "lse", (hq, t), _F32, dev)
+    _call(dev, stream, raw.load().gdn_attn_prompt, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
+          out.data_ptr(), lse.data_ptr(), d ** -0.5 if scale is None else scale, *strides, t, r, hq, hkv, d,
+          raw.GDN_BF16)
+    return out, lse

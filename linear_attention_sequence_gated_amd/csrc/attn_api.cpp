@@ -40,6 +40,15 @@ int heads_shape(int Hq, int Hkv, int D) {
   return D == 64 || D == 128 ? GDN_OK : GDN_ERR_UNSUPPORTED;
 }
 
+// A row stride of which 64 rows stay inside 32-bit byte offsets.
+bool near_ok(long long s, long long row) { return stride_ok(s, row) && s < (1LL << 24); }
+
+int prompt_shape(int T, int R, int Hq, int Hkv, int D) {
+  if (T < 0 || R < 0 || R >= kMaxRequests) return GDN_ERR_SHAPE;
+  if (const int s = heads_shape(Hq, Hkv, D)) return s;
+  return (long long)T * Hq < (1LL << 28) ? GDN_OK : GDN_ERR_SHAPE;
+}
+
 int decode_shape(int R, int Hq, int Hkv, int D, int bt, int width) {
   if (R < 0 || width < 0 || bt <= 0 || R >= kMaxRequests || (long long)width * bt >= (1LL << 31)) return GDN_ERR_SHAPE;
   if (const int s = heads_shape(Hq, Hkv, D)) return s;
@@ -111,6 +120,22 @@ int gdn_attn_decode(const void* q, const void* k_cache, const void* v_cache, con
   return status(gdn::launch_attn_decode({q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse,
                                          static_cast<float*>(workspace), scale, q_stride, R, Hq, Hkv, D, block_tokens,
                                          num_blocks, width, cache_format, stream}));
+}
+
+int gdn_attn_prompt(const void* q, const void* k, const void* v, const int* cu_seqlens, void* out, float* lse,
+                    float scale, long long q_stride, long long k_stride, long long v_stride, int T, int R, int Hq,
+                    int Hkv, int D, int dtype, void* stream) {
+  if (!known_dtype(dtype)) return GDN_ERR_DTYPE;
+  if (const int s = prompt_shape(T, R, Hq, Hkv, D)) return s;
+  if (dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+  const long long qrow = (long long)Hq * D, krow = (long long)Hkv * D;
+  if (!near_ok(q_stride, qrow) || !near_ok(k_stride, krow) || !near_ok(v_stride, krow)) return GDN_ERR_SHAPE;
+  if (T == 0 || R == 0) return GDN_OK;
+  if (!q || !k || !v || !cu_seqlens || !out || !lse) return GDN_ERR_NULL;
+  const void* ptrs[] = {q, k, v, cu_seqlens, out, lse};
+  if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
+  return status(gdn::launch_attn_prompt(
+      {q, k, v, cu_seqlens, out, lse, scale, q_stride, k_stride, v_stride, T, R, Hq, Hkv, D, stream}));
 }
 
 }  // extern "C"

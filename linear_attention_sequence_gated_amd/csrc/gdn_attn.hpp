@@ -56,4 +56,18 @@ struct DecodeArgs {
 size_t attn_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int bt, int width);
 hipError_t launch_attn_decode(const DecodeArgs& a);
 
+struct PromptArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const int* cu;
+  void* out;
+  float* lse;
+  float scale;
+  long long qs, ks, vs;
+  int T, R, Hq, Hkv, D;
+  void* stream;
+};
+hipError_t launch_attn_prompt(const PromptArgs& a);
+
 }  // namespace gdn

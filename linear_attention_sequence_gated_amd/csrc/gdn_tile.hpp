@@ -1,0 +1,169 @@
+// gdn_tile.hpp -- bf16 32x32x16 matrix-core tiles for the prompt attention
+// kernels: rows staged in LDS by direct loads, operands read from there, and
+// the rows' sequences.
+//
+// 32x32 accumulators: lane l holds column l % 32, element e (0..15) is row
+// 8 (e / 4) + 4 (l / 32) + e % 4.  An operand of the product holds row (or
+// column) l % 32 and eight values of k; the kernels take for k, of a 16-wide
+// block, 4 h + j and 8 + 4 h + j (h = l / 32, j = 0..3), where an accumulator
+// tile is fed back: its elements 8 b .. 8 b + 7 are then the operand of block b
+// as they stand.
+#pragma once
+
+#include <hip/hip_bf16.h>
+
+#include "gdn_pipe.hpp"
+
+namespace gdn {
+namespace tile {
+
+using pipe::u32x2;
+using pipe::u32x4;
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+typedef __attribute__((address_space(3))) void lds_void;
+
+__device__ __forceinline__ f32x16 mma(const u32x4& a, const u32x4& b, const f32x16& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+// A lane's value (r[0] or r[1]) and that of lane ^ 32 (the other).  The second
+// operand is hidden from the optimiser, which takes the swap of a value with
+// itself for that value.
+struct Halves {
+  float a, b;
+};
+__device__ __forceinline__ Halves halves(float x) {
+  int u = __builtin_bit_cast(int, x), w = u;
+  asm("" : "+v"(w));
+  const auto r = __builtin_amdgcn_permlane32_swap(u, w, false, false);
+  return {__builtin_bit_cast(float, (int)r[0]), __builtin_bit_cast(float, (int)r[1])};
+}
+__device__ __forceinline__ float max_halves(float x) {
+  const Halves h = halves(x);
+  return fmaxf(h.a, h.b);
+}
+__device__ __forceinline__ float sum_halves(float x) {
+  const Halves h = halves(x);
+  return h.a + h.b;
+}
+
+// Elements 8 b .. 8 b + 7 of an accumulator tile as a bf16 operand.
+__device__ __forceinline__ u32x4 operand(const f32x16& x, int b) {
+  return u32x4{pipe::cvt2(x[8 * b], x[8 * b + 1]), pipe::cvt2(x[8 * b + 2], x[8 * b + 3]),
+               pipe::cvt2(x[8 * b + 4], x[8 * b + 5]), pipe::cvt2(x[8 * b + 6], x[8 * b + 7])};
+}
+
+// Rows [r0, r0 + n) of a [rows, heads, D] array whose rows are `stride`
+// elements apart, seen through a buffer resource that ends with them: what lies
+// behind reads as zero.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, long long stride, long long r0, int n, int D) {
+  const uint32_t bytes = n > 0 ? (uint32_t)((n - 1) * stride + D) * 2u : 0u;
+  return pipe::make_rsrc(static_cast<const __hip_bfloat16*>(base) + r0 * stride, bytes);
+}
+
+// N rows of D values staged in LDS in the swizzled layout of pipe::row_off, by
+// loads that go straight to LDS: a wave's load fills 64 consecutive 16-byte
+// pieces, so the swizzle is in which piece of the row each lane asks for.
+template <int D, int N, int NW> struct Stage {
+  static constexpr int NU = D / 8, LOADS = N * NU / 64 / NW;
+  static_assert(N * NU % (64 * NW) == 0, "whole loads");
+  uint32_t off[LOADS];  // byte offset of the lane's pieces from the first row
+  __device__ __forceinline__ void init(long long stride, int wave) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int p = (wave * LOADS + i) * 64 + lane, r = p / NU, u = p % NU;
+      const int piece = (pipe::row_off<D>(r, 8 * u) - r * D) / 8;
+      off[i] = (uint32_t)(r * stride * 2) + piece * 16;
+    }
+  }
+  __device__ __forceinline__ void load(__bf16* lds, __amdgpu_buffer_rsrc_t rsrc, int wave) const {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (wave * LOADS + i) * 512), 16, off[i], 0, 0, 0);
+  }
+};
+
+// Operand rows: row r0 + l % 32 of a staged tile, its values 16 ks + 8 h .. + 7.
+template <int D> __device__ __forceinline__ int row_base(int lane) { return pipe::row_off<D>(lane & 31, 8 * (lane >> 5)) * 2; }
+template <int D> __device__ __forceinline__ u32x4 row_frag(const __bf16* lds, int base, int r0, int ks) {
+  return *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(lds) + ((base ^ (32 * ks)) + r0 * D * 2));
+}
+
+// Transposed operands: column 32 t + l % 32 of a staged tile, rows r0 + 4 h + j
+// and r0 + 8 + 4 h + j (r0 a multiple of 16).
+template <int D> __device__ __forceinline__ int col_base(int lane) {
+  const int c = lane & 15;
+  return pipe::row_off<D>(4 * (lane >> 5) + (c >> 2), 16 * ((lane >> 4) & 1) + 4 * (c & 3)) * 2;
+}
+template <int D> __device__ __forceinline__ u32x4 col_frag(const __bf16* lds, int base, int r0, int t) {
+  const char* p = reinterpret_cast<const char*>(lds);
+  const u32x2 a = pipe::ld4_tr(reinterpret_cast<const __bf16*>(p + ((base ^ (64 * t)) + r0 * D * 2)));
+  const u32x2 b = pipe::ld4_tr(reinterpret_cast<const __bf16*>(p + ((base ^ (64 * t) ^ 32) + (r0 + 8) * D * 2)));
+  return pipe::pair(a, b);
+}
+
+// Waits until this wave's loads into LDS have arrived, then for the others.
+__device__ __forceinline__ void staged_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// ------------------------------------------------------------------ sequences
+// The largest s in [lo, hi] with at(s) <= row, given at(lo) <= row.
+template <class At> __device__ __forceinline__ int last_at_most(At at, int lo, int hi, int row) {
+  while (lo < hi) {
+    const int mid = lo + (hi - lo + 1) / 2;
+    if (at(mid) <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Of rows [r0, r0 + N), by NT threads: their sequence's first row in beg[] and
+// the row behind its last in end[] (which may be NULL); rows of no sequence get
+// beg = end = -1.  0 <= beg <= row < end <= T whatever cu holds.  Ends with a
+// barrier.  The sequence of r0 is found NT probes at a time; the offsets behind
+// it are staged in `window` (N + 1 entries), where the other rows look theirs up.
+template <int N, int NT>
+__device__ __forceinline__ void find_rows(const int* cu, int R, int T, int r0, int* window, int* beg, int* end) {
+  const int t = threadIdx.x;
+  int lo = 0;
+  for (int n = R + 1;;) {
+    const int step = (n + NT - 1) / NT, i = t * step;
+    const int cnt = __syncthreads_count(i < n && cu[lo + i] <= r0);
+    if (cnt > 1) lo += (cnt - 1) * step;
+    if (cnt == 0 || step == 1) break;
+    n = min(step, R + 1 - lo);
+  }
+  // cu[lo] is the last offset at or before r0 (or lo = 0 and there is none)
+  const int last = min(R - lo, N);
+  for (int i = t; i <= last; i += NT) window[i] = cu[lo + i];
+  __syncthreads();
+  for (int i = t; i < N; i += NT) {
+    const int row = r0 + i;
+    int s = last_at_most([&](int x) { return window[x]; }, 0, last, row) + lo;
+    if (s == lo + last) s = last_at_most([&](int x) { return cu[x]; }, s, R, row);
+    int b = -1, e = -1;
+    if (s < R && row < T) {
+      b = cu[s];
+      e = min(cu[s + 1], T);
+      if (b > row || e <= row) b = e = -1;
+      else b = max(b, 0);
+    }
+    beg[i] = b;
+    if (end) end[i] = e;
+  }
+  __syncthreads();
+}
+
+}  // namespace tile
+}  // namespace gdn

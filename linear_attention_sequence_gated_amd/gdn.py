@@ -27,7 +27,8 @@ GDN_NOALLOC_MAX_WORKSPACE = 128 << 20  # include/gdn.h
 EXPORTS = ("gdn_chunk_fwd_workspace_bytes", "gdn_chunk_fwd", "gdn_chunk_fwd_prologue_workspace_bytes",
            "gdn_chunk_fwd_prologue", "gdn_chunk_bwd_workspace_bytes",
            "gdn_chunk_bwd", "gdn_fwd_channel_decay", "gdn_recurrent_step", "gdn_status_str", "gdn_chunk_fwd_noalloc",
-           "gdn_block_tables", "gdn_cache_append", "gdn_attn_decode_workspace_bytes", "gdn_attn_decode")
+           "gdn_block_tables", "gdn_cache_append", "gdn_attn_decode_workspace_bytes", "gdn_attn_decode",
+           "gdn_attn_prompt")
 
 _lib = None
 
@@ -75,6 +76,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.gdn_attn_decode_workspace_bytes.restype = sz
     lib.gdn_attn_decode.argtypes = [vp] * 9 + [fl, ll] + [ci] * 9 + [vp, sz, vp]
     lib.gdn_attn_decode.restype = ci
+    lib.gdn_attn_prompt.argtypes = [vp] * 6 + [fl] + [ll] * 3 + [ci] * 6 + [vp]
+    lib.gdn_attn_prompt.restype = ci
     lib.gdn_status_str.argtypes = [ci]
     lib.gdn_status_str.restype = ctypes.c_char_p
     if path is None:
@@ -153,6 +156,12 @@ def gdn_attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
     return int(load().gdn_attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse, scale,
                                       q_stride, R, Hq, Hkv, D, block_tokens, num_blocks, width, dtype, cache_format,
                                       workspace, workspace_bytes, stream))
+
+
+def gdn_attn_prompt(q, k, v, cu_seqlens, out, lse, scale, q_stride, k_stride, v_stride, T, R, Hq, Hkv, D, dtype,
+                    stream) -> int:
+    return int(load().gdn_attn_prompt(q, k, v, cu_seqlens, out, lse, scale, q_stride, k_stride, v_stride, T, R, Hq,
+                                      Hkv, D, dtype, stream))
 
 
 # ------------------------------------------------------------- torch helpers

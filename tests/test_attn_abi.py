@@ -94,6 +94,37 @@ def test_decode_workspace():
     assert decode(R=0, q=None, seq_lens=None, out=None) == raw.GDN_OK
 
 
+def prompt(**kw):
+    args = dict(q=A, k=A, v=A, cu_seqlens=A, out=A, lse=A, scale=0.125, q_stride=512, k_stride=256, v_stride=256, T=100,
+                R=3, Hq=8, Hkv=4, D=64, dtype=gdn.GDN_BF16, stream=None)
+    args.update(kw)
+    return gdn.gdn_attn_prompt(**args)
+
+
+PROMPT_ERRORS = [
+    (dict(dtype=3), raw.GDN_ERR_DTYPE), (dict(dtype=gdn.GDN_F32), raw.GDN_ERR_UNSUPPORTED),
+    (dict(T=-1), raw.GDN_ERR_SHAPE), (dict(R=-1), raw.GDN_ERR_SHAPE), (dict(R=1 << 20), raw.GDN_ERR_SHAPE),
+    (dict(T=1 << 25), raw.GDN_ERR_SHAPE), (dict(Hq=6), raw.GDN_ERR_SHAPE), (dict(Hkv=0), raw.GDN_ERR_SHAPE),
+    (dict(Hq=-8, Hkv=-4), raw.GDN_ERR_SHAPE), (dict(D=0), raw.GDN_ERR_SHAPE), (dict(D=256), raw.GDN_ERR_UNSUPPORTED),
+    (dict(q_stride=256), raw.GDN_ERR_SHAPE), (dict(k_stride=252), raw.GDN_ERR_SHAPE), (dict(v_stride=260), raw.GDN_ERR_SHAPE),
+    (dict(k_stride=1 << 24), raw.GDN_ERR_SHAPE),
+]
+
+
+@pytest.mark.parametrize("kw,status", PROMPT_ERRORS + [
+    *((dict([(n, None)]), raw.GDN_ERR_NULL) for n in ("q", "k", "v", "cu_seqlens", "out", "lse")),
+    *((dict([(n, A + 8)]), raw.GDN_ERR_ALIGN) for n in ("q", "k", "v", "cu_seqlens", "out", "lse")),
+])
+def test_prompt_argument_errors(kw, status):
+    assert prompt(**kw) == status
+
+
+def test_prompt_of_nothing_is_noop():
+    none = dict(q=None, k=None, v=None, cu_seqlens=None, out=None, lse=None)
+    assert prompt(T=0, **none) == raw.GDN_OK
+    assert prompt(R=0, **none) == raw.GDN_OK
+
+
 def test_cache_helpers_refuse_on_cpu():
     torch = pytest.importorskip("torch")
     i = torch.zeros(4, dtype=torch.int32)
@@ -104,3 +135,5 @@ def test_cache_helpers_refuse_on_cpu():
         gdn.cache_append(x, x, i, c, c, s, s)
     with pytest.raises(ValueError, match="HIP device"):
         gdn.attn_decode(x, c, c, s, s, i.view(4, 1), i)
+    with pytest.raises(ValueError, match="HIP device"):
+        gdn.attn_prompt(x, x, x, i)
