@@ -440,6 +440,28 @@ int gdn_attn_prompt(const void *q, const void *k, const void *v, const int *cu_s
                     float scale, long long q_stride, long long k_stride, long long v_stride, int T, int R, int Hq,
                     int Hkv, int D, int dtype, void *stream);
 
+/*
+ * Gradients of sum(out * grad_out) for gdn_attn_prompt's forward, from the out
+ * and lse that it returned.
+ *
+ *   grad_out, grad_q  [T] rows of Hq * D;  grad_k, grad_v  [T] rows of Hkv * D,
+ *              summed over the query heads that share them; bf16
+ *
+ * Each gradient is summed in float32 in a fixed order and rounded once, to
+ * bf16; probabilities and score gradients are rounded to bf16 where they enter
+ * a product.  Rows in no sequence are left as they were.  A non-finite value
+ * of a row gives non-finite gradients where its row's probabilities reach, and
+ * none outside its sequence.  Workspace: gdn_attn_prompt_bwd_workspace_bytes,
+ * scratch on entry and exit, no clearing needed.
+ */
+size_t gdn_attn_prompt_bwd_workspace_bytes(int T, int Hq, int Hkv, int D);
+int gdn_attn_prompt_bwd(const void *q, const void *k, const void *v, const void *out, const float *lse,
+                        const void *grad_out, const int *cu_seqlens, void *grad_q, void *grad_k, void *grad_v,
+                        float scale, long long q_stride, long long k_stride, long long v_stride,
+                        long long grad_out_stride, long long grad_q_stride, long long grad_k_stride,
+                        long long grad_v_stride, int T, int R, int Hq, int Hkv, int D, int dtype, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *gdn_status_str(int status);
 

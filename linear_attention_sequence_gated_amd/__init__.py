@@ -6,12 +6,12 @@ ABI of include/gdn.h); this package is its thin ctypes binding.
 """
 from .gdn import (GDN_BF16, GDN_C64, GDN_CACHE_E4M3, GDN_CACHE_I8, GDN_F32, GDN_NOALLOC_MAX_WORKSPACE, GdnError, chunk_bwd, chunk_fwd, chunk_fwd_prologue,  # noqa: F401
                   fwd_channel_decay, gdn_attn_decode, gdn_attn_decode_workspace_bytes,
-                  gdn_attn_prompt, gdn_block_tables, gdn_cache_append, gdn_chunk_bwd, gdn_chunk_bwd_workspace_bytes, gdn_chunk_fwd,
+                  gdn_attn_prompt, gdn_attn_prompt_bwd, gdn_attn_prompt_bwd_workspace_bytes, gdn_block_tables, gdn_cache_append, gdn_chunk_bwd, gdn_chunk_bwd_workspace_bytes, gdn_chunk_fwd,
                   gdn_chunk_fwd_noalloc, gdn_chunk_fwd_prologue, gdn_chunk_fwd_prologue_workspace_bytes,
                   gdn_chunk_fwd_workspace_bytes, gdn_fwd_channel_decay, gdn_recurrent_step,
                   gdn_status_str, load, recurrent_step)
 
-_ATTN = ("attn_decode", "attn_prompt", "block_tables", "cache_append")
+_ATTN = ("attn_decode", "attn_prompt", "attn_prompt_bwd", "block_tables", "cache_append")
 
 
 def __getattr__(name):

@@ -179,3 +179,27 @@ def attn_prompt(q, k, v, cu_seqlens, scale: float | None = None, out=None, lse=N
           out.data_ptr(), lse.data_ptr(), d ** -0.5 if scale is None else scale, *strides, t, r, hq, hkv, d,
           raw.GDN_BF16)
     return out, lse
+
+
+def attn_prompt_bwd(q, k, v, out, lse, grad_out, cu_seqlens, scale: float | None = None, grad_q=None, grad_k=None,
+                    grad_v=None, stream=None):
+    """Gradients of sum(out * grad_out) for attn_prompt's forward, from the out and lse that it returned.
+
+    Returns (grad_q, grad_k, grad_v) bf16, the latter two summed over the query heads that share them.  Passed in, they
+    may be parts of one tensor.  Rows in no sequence are not written; gradients that are allocated here hold zeros
+    there.  The workspace is allocated here with torch.
+    """
+    dev, t, r, hq, hkv, d, strides = _prompt(q, k, v, cu_seqlens, "attn_prompt_bwd")
+    _dense(out, "out", (t, hq, d), _BF16, dev)
+    _dense(lse, "lse", (hq, t), _F32, dev)
+    shapes = {"grad_q": (t, hq, d), "grad_k": (t, hkv, d), "grad_v": (t, hkv, d)}
+    grads = [torch.zeros(s, dtype=_BF16, device=dev) if g is None else g for g, s in zip((grad_q, grad_k, grad_v), shapes.values())]
+    gstrides = [_rows(g, n, s, dev) for g, (n, s) in zip(grads, shapes.items())]
+    gos = _rows(grad_out, "grad_out", (t, hq, d), dev)
+    lib = raw.load()
+    ws = torch.empty(lib.gdn_attn_prompt_bwd_workspace_bytes(t, hq, hkv, d), dtype=torch.uint8, device=dev)
+    _call(dev, stream, lib.gdn_attn_prompt_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+          lse.data_ptr(), grad_out.data_ptr(), cu_seqlens.data_ptr(), *(g.data_ptr() for g in grads),
+          d ** -0.5 if scale is None else scale, *strides, gos, *gstrides, t, r, hq, hkv, d, raw.GDN_BF16,
+          ws.data_ptr(), ws.numel())
+    return tuple(grads)

@@ -14,32 +14,6 @@ constexpr float kLowest = -1e30f;  // running maximum before the first token
 constexpr float kSlack = 8.f;      // the maximum in use may lie this far (powers of two) below the true one
 constexpr int kN = 64;             // keys of a tile
 
-// Non-finite bf16 values have all exponent bits set; the larger of a word's
-// halves without their signs, over words.
-__device__ __forceinline__ unsigned worst(unsigned m, unsigned w) {
-  typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
-  const u16x2 a = __builtin_bit_cast(u16x2, m), b = __builtin_bit_cast(u16x2, w & 0x7fff7fffu);
-  return __builtin_bit_cast(unsigned, __builtin_elementwise_max(a, b));
-}
-__device__ __forceinline__ bool finite(unsigned m) { return (m & 0xffffu) < 0x7f80u && (m >> 16) < 0x7f80u; }
-
-// A word with its non-finite halves replaced: by zero, or (kind 1, 2, 3) one
-// where the half is +infinity, -infinity, NaN and zero elsewhere.
-__device__ __forceinline__ unsigned pick(unsigned w, int kind) {
-  unsigned r = 0;
-#pragma unroll
-  for (int s = 0; s < 32; s += 16) {
-    const unsigned x = (w >> s) & 0xffffu, a = x & 0x7fffu;
-    const bool bad = a >= 0x7f80u;
-    const bool hit = kind == 1 ? x == 0x7f80u : kind == 2 ? x == 0xff80u : a > 0x7f80u;
-    r |= (kind == 0 ? (bad ? 0u : x) : (hit ? 0x3f80u : 0u)) << s;
-  }
-  return r;
-}
-__device__ __forceinline__ u32x4 pick(const u32x4& w, int kind) {
-  return u32x4{pick(w[0], kind), pick(w[1], kind), pick(w[2], kind), pick(w[3], kind)};
-}
-
 template <int D, int QT, int NW> struct Fwd {
   static constexpr int BM = 32 * QT * NW, NT = 64 * NW, KS = D / 16, DT = D / 32;
   struct Lds {

@@ -70,4 +70,24 @@ struct PromptArgs {
 };
 hipError_t launch_attn_prompt(const PromptArgs& a);
 
+struct PromptBwdArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* out;
+  const float* lse;
+  const void* grad_out;
+  const int* cu;
+  void* grad_q;
+  void* grad_k;
+  void* grad_v;
+  float* ws;
+  float scale;
+  long long qs, ks, vs, gos, gqs, gks, gvs;
+  int T, R, Hq, Hkv, D;
+  void* stream;
+};
+size_t attn_prompt_bwd_workspace_bytes(int T, int Hq);
+hipError_t launch_attn_prompt_bwd(const PromptBwdArgs& a);
+
 }  // namespace gdn

@@ -68,6 +68,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, lo
   return pipe::make_rsrc(static_cast<const __hip_bfloat16*>(base) + r0 * stride, bytes);
 }
 
+// 64 pieces of 16 bytes (of 4), straight to consecutive LDS, by one wave.  Not
+// templates: the host's pass does not know the 16-byte form.
+__device__ __forceinline__ void stage_pieces(__bf16* lds, __amdgpu_buffer_rsrc_t rsrc, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)lds, 16, off, 0, 0, 0);
+}
+__device__ __forceinline__ void stage_words(float* lds, __amdgpu_buffer_rsrc_t rsrc) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)lds, 4, (threadIdx.x & 63) * 4, 0, 0, 0);
+}
+
 // N rows of D values staged in LDS in the swizzled layout of pipe::row_off, by
 // loads that go straight to LDS: a wave's load fills 64 consecutive 16-byte
 // pieces, so the swizzle is in which piece of the row each lane asks for.
@@ -87,7 +96,7 @@ template <int D, int N, int NW> struct Stage {
   __device__ __forceinline__ void load(__bf16* lds, __amdgpu_buffer_rsrc_t rsrc, int wave) const {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (wave * LOADS + i) * 512), 16, off[i], 0, 0, 0);
+      stage_pieces(lds + (wave * LOADS + i) * 512, rsrc, off[i]);
   }
 };
 
@@ -115,6 +124,33 @@ __device__ __forceinline__ void staged_barrier() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
+}
+
+// ----------------------------------------------------------- non-finite values
+// Non-finite bf16 values have all exponent bits set; the larger of a word's
+// halves without their signs, over words.
+__device__ __forceinline__ unsigned worst(unsigned m, unsigned w) {
+  typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
+  const u16x2 a = __builtin_bit_cast(u16x2, m), b = __builtin_bit_cast(u16x2, w & 0x7fff7fffu);
+  return __builtin_bit_cast(unsigned, __builtin_elementwise_max(a, b));
+}
+__device__ __forceinline__ bool finite(unsigned m) { return (m & 0xffffu) < 0x7f80u && (m >> 16) < 0x7f80u; }
+
+// A word with its non-finite halves replaced: by zero, or (kind 1, 2, 3) one
+// where the half is +infinity, -infinity, NaN and zero elsewhere.
+__device__ __forceinline__ unsigned pick(unsigned w, int kind) {
+  unsigned r = 0;
+#pragma unroll
+  for (int s = 0; s < 32; s += 16) {
+    const unsigned x = (w >> s) & 0xffffu, a = x & 0x7fffu;
+    const bool bad = a >= 0x7f80u;
+    const bool hit = kind == 1 ? x == 0x7f80u : kind == 2 ? x == 0xff80u : a > 0x7f80u;
+    r |= (kind == 0 ? (bad ? 0u : x) : (hit ? 0x3f80u : 0u)) << s;
+  }
+  return r;
+}
+__device__ __forceinline__ u32x4 pick(const u32x4& w, int kind) {
+  return u32x4{pick(w[0], kind), pick(w[1], kind), pick(w[2], kind), pick(w[3], kind)};
 }
 
 // ------------------------------------------------------------------ sequences

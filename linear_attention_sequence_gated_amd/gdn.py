@@ -28,7 +28,7 @@ EXPORTS = ("gdn_chunk_fwd_workspace_bytes", "gdn_chunk_fwd", "gdn_chunk_fwd_prol
            "gdn_chunk_fwd_prologue", "gdn_chunk_bwd_workspace_bytes",
            "gdn_chunk_bwd", "gdn_fwd_channel_decay", "gdn_recurrent_step", "gdn_status_str", "gdn_chunk_fwd_noalloc",
            "gdn_block_tables", "gdn_cache_append", "gdn_attn_decode_workspace_bytes", "gdn_attn_decode",
-           "gdn_attn_prompt")
+           "gdn_attn_prompt", "gdn_attn_prompt_bwd_workspace_bytes", "gdn_attn_prompt_bwd")
 
 _lib = None
 
@@ -78,6 +78,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.gdn_attn_decode.restype = ci
     lib.gdn_attn_prompt.argtypes = [vp] * 6 + [fl] + [ll] * 3 + [ci] * 6 + [vp]
     lib.gdn_attn_prompt.restype = ci
+    lib.gdn_attn_prompt_bwd_workspace_bytes.argtypes = [ci] * 4
+    lib.gdn_attn_prompt_bwd_workspace_bytes.restype = sz
+    lib.gdn_attn_prompt_bwd.argtypes = [vp] * 10 + [fl] + [ll] * 7 + [ci] * 6 + [vp, sz, vp]
+    lib.gdn_attn_prompt_bwd.restype = ci
     lib.gdn_status_str.argtypes = [ci]
     lib.gdn_status_str.restype = ctypes.c_char_p
     if path is None:
@@ -162,6 +166,18 @@ def gdn_attn_prompt(q, k, v, cu_seqlens, out, lse, scale, q_stride, k_stride, v_
                     stream) -> int:
     return int(load().gdn_attn_prompt(q, k, v, cu_seqlens, out, lse, scale, q_stride, k_stride, v_stride, T, R, Hq,
                                       Hkv, D, dtype, stream))
+
+
+def gdn_attn_prompt_bwd_workspace_bytes(T, Hq, Hkv, D) -> int:
+    return int(load().gdn_attn_prompt_bwd_workspace_bytes(T, Hq, Hkv, D))
+
+
+def gdn_attn_prompt_bwd(q, k, v, out, lse, grad_out, cu_seqlens, grad_q, grad_k, grad_v, scale, q_stride, k_stride,
+                        v_stride, grad_out_stride, grad_q_stride, grad_k_stride, grad_v_stride, T, R, Hq, Hkv, D, dtype,
+                        workspace, workspace_bytes, stream) -> int:
+    return int(load().gdn_attn_prompt_bwd(q, k, v, out, lse, grad_out, cu_seqlens, grad_q, grad_k, grad_v, scale,
+                                          q_stride, k_stride, v_stride, grad_out_stride, grad_q_stride, grad_k_stride,
+                                          grad_v_stride, T, R, Hq, Hkv, D, dtype, workspace, workspace_bytes, stream))
 
 
 # ------------------------------------------------------------- torch helpers

@@ -125,6 +125,35 @@ def test_prompt_of_nothing_is_noop():
     assert prompt(R=0, **none) == raw.GDN_OK
 
 
+def prompt_bwd(**kw):
+    args = dict(q=A, k=A, v=A, out=A, lse=A, grad_out=A, cu_seqlens=A, grad_q=A, grad_k=A, grad_v=A, scale=0.125,
+                q_stride=512, k_stride=256, v_stride=256, grad_out_stride=512, grad_q_stride=512, grad_k_stride=256,
+                grad_v_stride=256, T=100, R=3, Hq=8, Hkv=4, D=64, dtype=gdn.GDN_BF16, workspace=A,
+                workspace_bytes=1 << 40, stream=None)
+    args.update(kw)
+    return gdn.gdn_attn_prompt_bwd(**args)
+
+
+@pytest.mark.parametrize("kw,status", PROMPT_ERRORS + [
+    *((dict([(n + "_stride", 508)]), raw.GDN_ERR_SHAPE) for n in ("grad_out", "grad_q")),
+    *((dict([(n + "_stride", 248)]), raw.GDN_ERR_SHAPE) for n in ("grad_k", "grad_v")),
+    *((dict([(n, None)]), raw.GDN_ERR_NULL) for n in ("q", "k", "v", "out", "lse", "grad_out", "cu_seqlens", "grad_q",
+                                                      "grad_k", "grad_v")),
+    *((dict([(n, A + 8)]), raw.GDN_ERR_ALIGN) for n in ("q", "k", "v", "out", "lse", "grad_out", "cu_seqlens", "grad_q",
+                                                        "grad_k", "grad_v", "workspace")),
+    (dict(workspace=None), raw.GDN_ERR_WORKSPACE), (dict(workspace_bytes=2 * 100 * 8 * 4 - 1), raw.GDN_ERR_WORKSPACE),
+])
+def test_prompt_bwd_argument_errors(kw, status):
+    assert prompt_bwd(**kw) == status
+
+
+def test_prompt_bwd_workspace():
+    assert gdn.gdn_attn_prompt_bwd_workspace_bytes(100, 8, 4, 64) == 2 * 100 * 8 * 4  # lse and delta
+    assert gdn.gdn_attn_prompt_bwd_workspace_bytes(100, 8, 3, 64) == 0
+    none = {n: None for n in ("q", "k", "v", "out", "lse", "grad_out", "cu_seqlens", "grad_q", "grad_k", "grad_v", "workspace")}
+    assert prompt_bwd(T=0, **none) == raw.GDN_OK and prompt_bwd(R=0, **none) == raw.GDN_OK
+
+
 def test_cache_helpers_refuse_on_cpu():
     torch = pytest.importorskip("torch")
     i = torch.zeros(4, dtype=torch.int32)
@@ -137,3 +166,5 @@ def test_cache_helpers_refuse_on_cpu():
         gdn.attn_decode(x, c, c, s, s, i.view(4, 1), i)
     with pytest.raises(ValueError, match="HIP device"):
         gdn.attn_prompt(x, x, x, i)
+    with pytest.raises(ValueError, match="HIP device"):
+        gdn.attn_prompt_bwd(x, x, x, x, s, x, i)

@@ -1,0 +1,174 @@
+"""Gradients of attention over packed prompts on the GPU against the 64-bit oracle's, and against differences.
+
+Tolerances, element by element, with u = 2^-8 (half a bf16 step).  dv: every weight p is rounded to bf16 once and the
+sum once, u (sum p |do| + |dv|).  delta is summed from the rounded output, so it errs by u sum |do o|; ds = p (dp -
+delta) is rounded once, u |ds| + p u sum |do o|, and reaches dq and dk through |k| and |q|; these are rounded once.
+float32 exponents and sums add 2^-12 of the same sums with |dp| + |delta| in place of |dp - delta| (scores here are below
+2^6, so exponents err by less than 2^-17; sums of 700 terms by less than 2^-14).
+"""
+import numpy as np
+import pytest
+
+from gpu_util import note, torch_dev
+from oracle import attention as ref
+from test_gpu_attn_cache import ints
+from test_gpu_attn_prompt import RAGGED, host, make, offsets
+
+pytestmark = pytest.mark.gpu
+U, F = 2.0 ** -8, 2.0 ** -12
+
+
+def bounds(q, k, v, do, cu, scale, grads):
+    T, Hq, D = q.shape
+    G = Hq // k.shape[1]
+    tq, tk, tv = (np.abs(x) * U + 1e-30 for x in grads)
+    for a, b in zip(cu[:-1], cu[1:]):
+        for h in range(Hq if b > a else 0):
+            s = q[a:b, h] @ k[a:b, h // G].T * scale
+            s = np.where(np.tril(np.ones_like(s, dtype=bool)), s, -np.inf)
+            p = np.exp(s - s.max(1, keepdims=True))
+            p /= p.sum(1, keepdims=True)
+            o, dp = p @ v[a:b, h // G], do[a:b, h] @ v[a:b, h // G].T
+            delta, off = (do[a:b, h] * o).sum(1, keepdims=True), np.abs(do[a:b, h] * o).sum(1, keepdims=True)
+            e = abs(scale) * p * (U * np.abs(dp - delta) + U * off + F * (np.abs(dp) + np.abs(delta)))
+            tq[a:b, h] += e @ np.abs(k[a:b, h // G])
+            tk[a:b, h // G] += e.T @ np.abs(q[a:b, h])
+            tv[a:b, h // G] += (U + F) * p.T @ np.abs(do[a:b, h])
+    return tq, tk, tv
+
+
+def check(torch, q, k, v, cu, scale=None, do=None, seed=0, into=None):
+    import linear_attention_sequence_gated_amd as gdn
+    T, Hq, D = q.shape
+    H = k.shape[1]
+    if do is None:
+        do = torch.from_numpy(np.random.default_rng(seed + 99).standard_normal((T, Hq, D)).astype(np.float32)).to(torch.bfloat16).cuda()
+    c = ints(torch, cu)
+    out, lse = gdn.attn_prompt(q, k, v, c, scale)
+    grads = into or [torch.full((T, n, D), 7.0, dtype=torch.bfloat16, device="cuda") for n in (Hq, H, H)]
+    got = gdn.attn_prompt_bwd(q, k, v, out, lse, do, c, scale, *grads)
+    torch.cuda.synchronize()
+    x = [np.nan_to_num(y, nan=0, posinf=0, neginf=0) for y in host(q, k, v, do)]
+    scale = D ** -0.5 if scale is None else scale
+    want = ref.prompt(x[0], x[1], x[2], cu, scale, x[3])[2:]
+    tol = bounds(*x, cu, scale, want)
+    inside = np.zeros(T, bool)
+    for a, b in zip(cu[:-1], cu[1:]):
+        inside[a:b] = True
+    worst = []
+    for g, w, t in zip(host(*got), want, tol):
+        assert np.all(g[~inside] == 7), "rows of no sequence are left as they were"
+        worst.append((np.abs(g - w) / t)[inside].max(initial=0))
+    print("worst share of the tolerance: dq %.2f dk %.2f dv %.2f" % tuple(worst))
+    assert max(worst) <= 1
+    return got
+
+
+@pytest.mark.parametrize("L", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 257, 300, 513, 700])
+@pytest.mark.parametrize("Hq,H,D", [(2, 2, 64), (2, 1, 128)])
+def test_one_prompt(L, Hq, H, D):
+    torch = torch_dev()
+    note(f"bwd L{L} Hq{Hq} H{H} D{D}")
+    check(torch, *make(torch, np.random.default_rng(L), L, Hq, H, D), offsets([L]))
+
+
+@pytest.mark.parametrize("lens", RAGGED.values(), ids=RAGGED.keys())
+@pytest.mark.parametrize("Hq,H,D,fused", [(3, 1, 64, True), (4, 4, 64, False), (4, 2, 128, True), (8, 1, 128, False)])
+def test_packed_prompts(lens, Hq, H, D, fused):
+    torch = torch_dev()
+    note(f"bwd packed {len(lens)} sequences Hq{Hq} H{H} D{D}")
+    check(torch, *make(torch, np.random.default_rng(len(lens)), sum(lens), Hq, H, D, fused), offsets(lens))
+
+
+def test_gradients_into_one_projection():
+    """q, k, v and their gradients as parts of fused tensors; grad_out with room between its rows."""
+    torch = torch_dev()
+    rng = np.random.default_rng(5)
+    lens, Hq, H, D = [40, 100, 3], 4, 2, 64
+    q, k, v = make(torch, rng, sum(lens), Hq, H, D)
+    wide = torch.from_numpy(rng.standard_normal((sum(lens), 2 * Hq, D)).astype(np.float32)).to(torch.bfloat16).cuda()
+    d = torch.full((sum(lens), Hq + 2 * H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    note("bwd into one projection")
+    check(torch, q, k, v, offsets(lens), do=wide[:, Hq:], into=list(d.split([Hq, H, H], 1)))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_outside_may_hold_anything(D):
+    torch = torch_dev()
+    lens, rng = [70, 30, 90], np.random.default_rng(6)
+    cu = offsets(lens, before=9)
+    T = cu[-1] + 60
+    q, k, v = make(torch, rng, T, 2, 1, D)
+    do = torch.from_numpy(rng.standard_normal((T, 2, D)).astype(np.float32)).to(torch.bfloat16).cuda()
+    for x in (q, k, v, do):
+        x[:9], x[cu[-1]:] = float("nan"), float("inf")
+    note(f"bwd outside D{D}")
+    good = check(torch, q, k, v, cu, do=do)
+    # a neighbour that is not finite changes nothing elsewhere, and shows in its own gradients
+    import linear_attention_sequence_gated_amd as gdn
+    for bad in range(4):
+        x = [t.clone() for t in (q, k, v, do)]
+        x[bad][cu[1] + 12] = float("nan")
+        c = ints(torch, cu)
+        out, lse = gdn.attn_prompt(*x[:3], c)
+        got = gdn.attn_prompt_bwd(*x[:3], out, lse, x[3], c)
+        keep = np.r_[cu[0]:cu[1], cu[2]:cu[3]]
+        for a, b in zip(got, good):
+            assert torch.equal(a[keep], b[keep])
+        # dv = sum p do does not contain v
+        assert all(g[cu[1]:cu[2]].isnan().any() for g in (got[:2] if bad == 2 else got))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scale,size", [(0.0, 1.0), (-0.2, 1.0), (1.0, 2.0), (1e-3, 30.0)])
+def test_scales(D, scale, size):
+    torch = torch_dev()
+    note(f"bwd scale {scale} size {size} D{D}")
+    check(torch, *make(torch, np.random.default_rng(7), 300, 2, 2, D, size=size), offsets([150, 150]), scale)
+
+
+def test_same_gradients_every_time():
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    q, k, v = make(torch, np.random.default_rng(8), 900, 8, 2, 64)
+    c, do = ints(torch, [0, 400, 900]), torch.ones(900, 8, 64, dtype=torch.bfloat16, device="cuda")
+    out, lse = gdn.attn_prompt(q, k, v, c)
+    a, b = (gdn.attn_prompt_bwd(q, k, v, out, lse, do, c) for _ in range(2))
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_against_differences():
+    """Along random directions, sum grad . direction against a central difference of the oracle's forward."""
+    torch = torch_dev()
+    lens, D = [50, 90], 64
+    q, k, v = make(torch, np.random.default_rng(9), sum(lens), 4, 2, D)
+    cu = offsets(lens)
+    note("bwd differences")
+    got = host(*check(torch, q, k, v, cu, seed=1))
+    do = np.random.default_rng(1 + 99).standard_normal((sum(lens), 4, D)).astype(np.float32)
+    do = torch.from_numpy(do).to(torch.bfloat16).float().numpy().astype(np.float64)
+    x = host(q, k, v)
+    want = ref.prompt(*x, cu, D ** -0.5, do)[2:]
+    tol = bounds(*x, do, cu, D ** -0.5, want)
+    for i in range(3):
+        for seed in range(3):
+            d = np.random.default_rng(seed).standard_normal(x[i].shape)
+            ends = []
+            for eps in (1e-5, -1e-5):
+                y = list(x)
+                y[i] = y[i] + eps * d
+                ends.append((ref.prompt(*y, cu, D ** -0.5)[0] * do).sum())
+            diff = (ends[0] - ends[1]) / 2e-5
+            assert abs((got[i] * d).sum() - diff) <= (tol[i] * np.abs(d)).sum() + 1e-4 * abs(diff) + 1e-3
+
+
+@pytest.mark.parametrize("cu", [[-5, 40, 30, 100000, 2 ** 31 - 1], [100, 50, 0], [-2 ** 31, -1, 2 ** 31 - 1], [7], [64, 64, 64]])
+def test_offsets_out_of_order(cu):
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    q, k, v = make(torch, np.random.default_rng(9), 200, 2, 1, 64)
+    c = ints(torch, cu)
+    note(f"bwd offsets {cu}")
+    out, lse = gdn.attn_prompt(q, k, v, c)
+    gdn.attn_prompt_bwd(q, k, v, out, lse, out, c)
+    torch.cuda.synchronize()
