@@ -21,7 +21,7 @@ template <int D, int QT, int NW> struct Fwd {
     __bf16 v[2][kN * D];
     int beg[BM];
     int window[BM + 1];
-    int lo[NW];
+    int lo[NW], hi[NW];
   };
 };
 
@@ -37,18 +37,30 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
   const int r0 = (tiles - 1 - rank) * BM, kvh = hq / (a.Hq / a.Hkv);
 
   find_rows<BM, NT>(a.cu, a.R, a.T, r0, lds.window, lds.beg, nullptr);
-  int first = a.T;  // first key that any row of the tile sees
+  int first = a.T, last = -1;  // the keys that the tile's rows see
   for (int i = tid; i < BM; i += NT)
-    if (lds.beg[i] >= 0) first = min(first, lds.beg[i]);
+    if (lds.beg[i] >= 0) {
+      first = min(first, lds.beg[i]);
+      last = max(last, r0 + i + 1);
+    }
 #pragma unroll
-  for (int d = 32; d; d >>= 1) first = min(first, __shfl_xor(first, d));
-  if (lane == 0) lds.lo[wave] = first;
+  for (int d = 32; d; d >>= 1) {
+    first = min(first, __shfl_xor(first, d));
+    last = max(last, __shfl_xor(last, d));
+  }
+  if (lane == 0) {
+    lds.lo[wave] = first;
+    lds.hi[wave] = last;
+  }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < NW; ++w) first = min(first, lds.lo[w]);
+  for (int w = 0; w < NW; ++w) {
+    first = min(first, lds.lo[w]);
+    last = max(last, lds.hi[w]);
+  }
   first = __builtin_amdgcn_readfirstlane(first);
-  if (first >= a.T) return;  // no row of the tile is in a sequence
-  const int last = min(r0 + BM, a.T);
+  last = __builtin_amdgcn_readfirstlane(last);
+  if (last < 0) return;  // no row of the tile is in a sequence
 
   // queries: operands for the wave's rows, their sign turned for a negative scale
   const int w0 = r0 + wave * 32 * QT;
@@ -100,14 +112,10 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
     sk.load(lds.k[buf], rows_rsrc(kp, a.ks, kv, n, D), wave);
     sv.load(lds.v[buf], rows_rsrc(vp, a.vs, kv, n, D), wave);
   };
-  stage(0, first);
-  int buf = 0;
-  for (int kv = first; kv < last; kv += kN, buf ^= 1) {
-    staged_barrier();
-    if (kv + kN < last) stage(buf ^ 1, kv + kN);
-    if (kv > w0 + 32 * QT - 1 || kv + kN <= lowest) continue;  // nothing of it is seen by the wave's rows
-    const bool masked = kv + kN - 1 > w0 || kv < highest || kv + kN > last;
-    const __bf16 *K = lds.k[buf], *V = lds.v[buf];
+  int dirty_lo = last, dirty_hi = 0;  // the tiles with non-finite values that were left out
+  // one tile of keys; MASKED: some of its keys are not seen by some of the rows
+  auto step = [&](auto masked_, const __bf16* K, const __bf16* V, int kv) {
+    constexpr bool MASKED = decltype(masked_)::value;
     f32x16 s[QT][2];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
@@ -123,14 +131,16 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
     u32x4 p[QT][4];
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      if (masked) {
+      unsigned seen = 0;  // bit 16 n + e
+      if constexpr (MASKED) {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int key = kv + 32 * n + 8 * (e / 4) + 4 * hl + e % 4;
-            const bool seen = beg[t] >= 0 && key >= beg[t] && key <= row[t];
-            s[t][n][e] = seen ? s[t][n][e] : -INFINITY;
+            const bool x = beg[t] >= 0 && key >= beg[t] && key <= row[t];
+            seen |= (x ? 1u : 0u) << (16 * n + e);
+            s[t][n][e] = x ? s[t][n][e] : -INFINITY;
           }
       }
       float top = s[t][0][0];
@@ -152,7 +162,7 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][n][e], c, -m[t]));
-          if (masked) x = s[t][n][e] == -INFINITY ? 0.f : x;
+          if constexpr (MASKED) x = (seen >> (16 * n + e)) & 1u ? x : 0.f;
           s[t][n][e] = x;
           sum += x;
         }
@@ -162,18 +172,7 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
       l[t] += sum;
     }
     bool clean = true;
-    if (masked) {  // values that no row sees must not reach the sums, whatever they are
-      unsigned w = 0;
-#pragma unroll
-      for (int i = 0; i < DT; ++i)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const u32x4 f = col_frag<D>(V, vb, 16 * b, i);
-          w = worst(worst(w, f[0]), f[1]);
-          w = worst(worst(w, f[2]), f[3]);
-        }
-      clean = __all(finite(w));
-    }
+    if constexpr (MASKED) clean = clean_tile<D, kN>(V);
     if (clean) {
 #pragma unroll
       for (int i = 0; i < DT; ++i)
@@ -184,21 +183,28 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
           for (int t = 0; t < QT; ++t) o[t][i] = mma(f, p[t][b], o[t][i]);
         }
     } else {
-      // finite values as ever; the others through the sum of the weights that meet them
-#pragma unroll 1
-      for (int kind = 0; kind < 4; ++kind)
+      // values that some row does not see must not reach its sums: they are left
+      // out here, and added to the rows that see them when all is written
+      dirty_lo = min(dirty_lo, kv);
+      dirty_hi = kv + kN;
 #pragma unroll
-        for (int i = 0; i < DT; ++i)
+      for (int i = 0; i < DT; ++i)
 #pragma unroll
-          for (int t = 0; t < QT; ++t) {
-            f32x16 x = kind ? zero16() : o[t][i];
+        for (int b = 0; b < 4; ++b) {
+          const u32x4 f = finite_only(col_frag<D>(V, vb, 16 * b, i));
 #pragma unroll
-            for (int b = 0; b < 4; ++b) x = mma(pick(col_frag<D>(V, vb, 16 * b, i), kind), p[t][b], x);
-            const float bad = kind == 1 ? INFINITY : kind == 2 ? -INFINITY : __builtin_nanf("");
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[t][i][e] = kind == 0 ? x[e] : x[e] > 0.f ? o[t][i][e] + bad : o[t][i][e];
-          }
+          for (int t = 0; t < QT; ++t) o[t][i] = mma(f, p[t][b], o[t][i]);
+        }
     }
+  };
+  stage(0, first);
+  int buf = 0;
+  for (int kv = first; kv < last; kv += kN, buf ^= 1) {
+    staged_barrier();
+    if (kv + kN < last) stage(buf ^ 1, kv + kN);
+    if (kv > w0 + 32 * QT - 1 || kv + kN <= lowest) continue;  // nothing of it is seen by the wave's rows
+    if (kv + kN - 1 > w0 || kv < highest || kv + kN > last) step(std::true_type{}, lds.k[buf], lds.v[buf], kv);
+    else step(std::false_type{}, lds.k[buf], lds.v[buf], kv);
   }
 
 #pragma unroll
@@ -213,6 +219,19 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
           *reinterpret_cast<u32x2*>(dst + 32 * i + 8 * e) = pipe::cvt4(
               f32x4{o[t][i][4 * e] * inv, o[t][i][4 * e + 1] * inv, o[t][i][4 * e + 2] * inv, o[t][i][4 * e + 3] * inv});
       if (hl == 0) a.lse[(size_t)hq * a.T + row[t]] = (m[t] + __builtin_amdgcn_logf(z)) * kLn2;
+    }
+  }  if (dirty_hi == 0) return;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    if (beg[t] < 0) continue;
+    __bf16* dst = static_cast<__bf16*>(a.out) + ((size_t)row[t] * a.Hq + hq) * D;
+    for (int key = max(beg[t], dirty_lo); key <= row[t] && key < dirty_hi; ++key) {
+      const __bf16* src = static_cast<const __bf16*>(a.v) + (long long)key * a.vs + (long long)kvh * D;
+      for (int d = 32 * hl; d < D; d += 64)
+        for (int i = 0; i < 32; ++i) {
+          const float x = (float)src[d + i];
+          if (!__builtin_isfinite(x)) dst[d + i] = (__bf16)((float)dst[d + i] + x);
+        }
     }
   }
 }

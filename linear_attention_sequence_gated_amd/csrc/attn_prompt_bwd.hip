@@ -48,18 +48,6 @@ __device__ __forceinline__ void add_columns(f32x16 (&acc)[D / 32], const __bf16*
   }
 }
 
-// Whether all of a staged tile is finite.
-template <int D> __device__ __forceinline__ bool clean_tile(const __bf16* tile) {
-  unsigned w = 0;
-  const u32x4* p = reinterpret_cast<const u32x4*>(tile);
-#pragma unroll
-  for (int i = 0; i < kN * D / 512; ++i) {
-    const u32x4 x = p[i * 64 + (threadIdx.x & 63)];
-    w = worst(worst(worst(worst(w, x[0]), x[1]), x[2]), x[3]);
-  }
-  return __all(finite(w));
-}
-
 template <int D> __device__ __forceinline__ void store_rows(__bf16* dst, const f32x16 (&acc)[D / 32], float f, int hl) {
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
@@ -150,7 +138,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
     if (kv + kN < last) stage(buf ^ 1, kv + kN);
     if (kv > w0 + 31 || kv + kN <= lowest) continue;
     const bool masked = kv + kN - 1 > w0 || kv < highest || kv + kN > last;
-    const bool clean = !masked || clean_tile<D>(kt[buf]);
+    const bool clean = !masked || clean_tile<D, kN>(kt[buf]);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       f32x16 s = zero16(), dp = zero16();
@@ -255,7 +243,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
     i0 = ni;
     if (i1 + kN - 1 < w0 || i1 >= highest) continue;
     const bool masked = i1 < w0 + 31 || i1 + kN > lowest;
-    const bool clean = !masked || (clean_tile<D>(qt[buf]) && clean_tile<D>(gt[buf]));
+    const bool clean = !masked || (clean_tile<D, kN>(qt[buf]) && clean_tile<D, kN>(gt[buf]));
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       f32x16 s = zero16(), dp = zero16();

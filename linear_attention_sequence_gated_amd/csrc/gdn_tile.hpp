@@ -153,6 +153,20 @@ __device__ __forceinline__ u32x4 pick(const u32x4& w, int kind) {
   return u32x4{pick(w[0], kind), pick(w[1], kind), pick(w[2], kind), pick(w[3], kind)};
 }
 
+__device__ __forceinline__ u32x4 finite_only(const u32x4& w) { return pick(w, 0); }
+
+// Whether all of a staged tile of N rows is finite.
+template <int D, int N> __device__ __forceinline__ bool clean_tile(const __bf16* tile) {
+  unsigned w = 0;
+  const u32x4* p = reinterpret_cast<const u32x4*>(tile);
+#pragma unroll
+  for (int i = 0; i < N * D / 512; ++i) {
+    const u32x4 x = p[i * 64 + (threadIdx.x & 63)];
+    w = worst(worst(worst(worst(w, x[0]), x[1]), x[2]), x[3]);
+  }
+  return __all(finite(w));
+}
+
 // ------------------------------------------------------------------ sequences
 // The largest s in [lo, hi] with at(s) <= row, given at(lo) <= row.
 template <class At> __device__ __forceinline__ int last_at_most(At at, int lo, int hi, int row) {
