@@ -432,13 +432,13 @@ int gdn_attn_decode(const void *q, const void *k_cache, const void *v_cache, con
  *   out        [T, Hq, D] written;  lse [Hq, T] written
  *
  * Rows in no sequence (before cu_seqlens[0], from cu_seqlens[R] on) are left
- * as they were, in out and lse.  Values of masked
- * keys and rows never reach a result, whatever they are.  T * Hq and the row
- * strides are below 2^28 and 2^24.
+ * as they were in out and lse, or, where zero_rest is not 0, set to zero.
+ * Values of masked keys and rows never reach a result, whatever they are.
+ * T * Hq and the row strides are below 2^28 and 2^24.
  */
 int gdn_attn_prompt(const void *q, const void *k, const void *v, const int *cu_seqlens, void *out, float *lse,
                     float scale, long long q_stride, long long k_stride, long long v_stride, int T, int R, int Hq,
-                    int Hkv, int D, int dtype, void *stream);
+                    int Hkv, int D, int dtype, int zero_rest, void *stream);
 
 /*
  * Gradients of sum(out * grad_out) for gdn_attn_prompt's forward, from the out
@@ -449,7 +449,7 @@ int gdn_attn_prompt(const void *q, const void *k, const void *v, const int *cu_s
  *
  * Each gradient is summed in float32 in a fixed order and rounded once, to
  * bf16; probabilities and score gradients are rounded to bf16 where they enter
- * a product.  Rows in no sequence are left as they were.  A non-finite value
+ * a product.  Rows in no sequence: as for the forward.  A non-finite value
  * of a row gives non-finite gradients where its row's probabilities reach, and
  * none outside its sequence.  Workspace: gdn_attn_prompt_bwd_workspace_bytes,
  * scratch on entry and exit, no clearing needed.
@@ -459,8 +459,8 @@ int gdn_attn_prompt_bwd(const void *q, const void *k, const void *v, const void 
                         const void *grad_out, const int *cu_seqlens, void *grad_q, void *grad_k, void *grad_v,
                         float scale, long long q_stride, long long k_stride, long long v_stride,
                         long long grad_out_stride, long long grad_q_stride, long long grad_k_stride,
-                        long long grad_v_stride, int T, int R, int Hq, int Hkv, int D, int dtype, void *workspace,
-                        size_t workspace_bytes, void *stream);
+                        long long grad_v_stride, int T, int R, int Hq, int Hkv, int D, int dtype, int zero_rest,
+                        void *workspace, size_t workspace_bytes, void *stream);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *gdn_status_str(int status);

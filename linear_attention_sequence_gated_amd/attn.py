@@ -167,17 +167,18 @@ def attn_prompt(q, k, v, cu_seqlens, scale: float | None = None, out=None, lse=N
     allocated here hold zeros there.
     """
     dev, t, r, hq, hkv, d, strides = _prompt(q, k, v, cu_seqlens, "attn_prompt")
+    zero_rest = out is None and lse is None
     if out is None:
-        out = torch.zeros((t, hq, d), dtype=_BF16, device=dev)
+        out = (torch.empty if zero_rest else torch.zeros)((t, hq, d), dtype=_BF16, device=dev)
     else:
         _dense(out, "out", (t, hq, d), _BF16, dev)
     if lse is None:
-        lse = torch.zeros((hq, t), dtype=_F32, device=dev)
+        lse = (torch.empty if zero_rest else torch.zeros)((hq, t), dtype=_F32, device=dev)
     else:
         _dense(lse, "lse", (hq, t), _F32, dev)
     _call(dev, stream, raw.load().gdn_attn_prompt, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
           out.data_ptr(), lse.data_ptr(), d ** -0.5 if scale is None else scale, *strides, t, r, hq, hkv, d,
-          raw.GDN_BF16)
+          raw.GDN_BF16, zero_rest)
     return out, lse
 
 
@@ -193,13 +194,16 @@ def attn_prompt_bwd(q, k, v, out, lse, grad_out, cu_seqlens, scale: float | None
     _dense(out, "out", (t, hq, d), _BF16, dev)
     _dense(lse, "lse", (hq, t), _F32, dev)
     shapes = {"grad_q": (t, hq, d), "grad_k": (t, hkv, d), "grad_v": (t, hkv, d)}
-    grads = [torch.zeros(s, dtype=_BF16, device=dev) if g is None else g for g, s in zip((grad_q, grad_k, grad_v), shapes.values())]
+    grads = (grad_q, grad_k, grad_v)
+    zero_rest = all(g is None for g in grads)
+    make = torch.empty if zero_rest else torch.zeros
+    grads = [make(s, dtype=_BF16, device=dev) if g is None else g for g, s in zip(grads, shapes.values())]
     gstrides = [_rows(g, n, s, dev) for g, (n, s) in zip(grads, shapes.items())]
     gos = _rows(grad_out, "grad_out", (t, hq, d), dev)
     lib = raw.load()
     ws = torch.empty(lib.gdn_attn_prompt_bwd_workspace_bytes(t, hq, hkv, d), dtype=torch.uint8, device=dev)
     _call(dev, stream, lib.gdn_attn_prompt_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
           lse.data_ptr(), grad_out.data_ptr(), cu_seqlens.data_ptr(), *(g.data_ptr() for g in grads),
-          d ** -0.5 if scale is None else scale, *strides, gos, *gstrides, t, r, hq, hkv, d, raw.GDN_BF16,
+          d ** -0.5 if scale is None else scale, *strides, gos, *gstrides, t, r, hq, hkv, d, raw.GDN_BF16, zero_rest,
           ws.data_ptr(), ws.numel())
     return tuple(grads)

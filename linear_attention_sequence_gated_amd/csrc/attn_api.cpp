@@ -126,18 +126,19 @@ int gdn_attn_decode(const void* q, const void* k_cache, const void* v_cache, con
 
 int gdn_attn_prompt(const void* q, const void* k, const void* v, const int* cu_seqlens, void* out, float* lse,
                     float scale, long long q_stride, long long k_stride, long long v_stride, int T, int R, int Hq,
-                    int Hkv, int D, int dtype, void* stream) {
+                    int Hkv, int D, int dtype, int zero_rest, void* stream) {
   if (!known_dtype(dtype)) return GDN_ERR_DTYPE;
   if (const int s = prompt_shape(T, R, Hq, Hkv, D)) return s;
   if (dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
   const long long qrow = (long long)Hq * D, krow = (long long)Hkv * D;
   if (!near_ok(q_stride, qrow) || !near_ok(k_stride, krow) || !near_ok(v_stride, krow)) return GDN_ERR_SHAPE;
-  if (T == 0 || R == 0) return GDN_OK;
+  if (T == 0) return GDN_OK;
   if (!q || !k || !v || !cu_seqlens || !out || !lse) return GDN_ERR_NULL;
   const void* ptrs[] = {q, k, v, cu_seqlens, out, lse};
   if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
   return status(gdn::launch_attn_prompt(
-      {q, k, v, cu_seqlens, out, lse, scale, q_stride, k_stride, v_stride, T, R, Hq, Hkv, D, stream}));
+      {q, k, v, cu_seqlens, out, lse, scale, q_stride, k_stride, v_stride, T, R, Hq, Hkv, D,
+       zero_rest, stream}));
 }
 
 size_t gdn_attn_prompt_bwd_workspace_bytes(int T, int Hq, int Hkv, int D) {
@@ -148,8 +149,8 @@ int gdn_attn_prompt_bwd(const void* q, const void* k, const void* v, const void*
                         const void* grad_out, const int* cu_seqlens, void* grad_q, void* grad_k, void* grad_v,
                         float scale, long long q_stride, long long k_stride, long long v_stride,
                         long long grad_out_stride, long long grad_q_stride, long long grad_k_stride,
-                        long long grad_v_stride, int T, int R, int Hq, int Hkv, int D, int dtype, void* workspace,
-                        size_t workspace_bytes, void* stream) {
+                        long long grad_v_stride, int T, int R, int Hq, int Hkv, int D, int dtype, int zero_rest,
+                        void* workspace, size_t workspace_bytes, void* stream) {
   if (!known_dtype(dtype)) return GDN_ERR_DTYPE;
   if (const int s = prompt_shape(T, R, Hq, Hkv, D)) return s;
   if (dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
@@ -158,7 +159,7 @@ int gdn_attn_prompt_bwd(const void* q, const void* k, const void* v, const void*
     if (!near_ok(s, qrow)) return GDN_ERR_SHAPE;
   for (const long long s : {k_stride, v_stride, grad_k_stride, grad_v_stride})
     if (!near_ok(s, krow)) return GDN_ERR_SHAPE;
-  if (T == 0 || R == 0) return GDN_OK;
+  if (T == 0) return GDN_OK;
   if (!q || !k || !v || !out || !lse || !grad_out || !cu_seqlens || !grad_q || !grad_k || !grad_v) return GDN_ERR_NULL;
   const void* ptrs[] = {q, k, v, out, lse, grad_out, cu_seqlens, grad_q, grad_k, grad_v, workspace};
   if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
@@ -166,7 +167,7 @@ int gdn_attn_prompt_bwd(const void* q, const void* k, const void* v, const void*
   return status(gdn::launch_attn_prompt_bwd({q, k, v, out, lse, grad_out, cu_seqlens, grad_q, grad_k, grad_v,
                                              static_cast<float*>(workspace), scale, q_stride, k_stride, v_stride,
                                              grad_out_stride, grad_q_stride, grad_k_stride, grad_v_stride, T, R, Hq,
-                                             Hkv, D, stream}));
+                                             Hkv, D, zero_rest, stream}));
 }
 
 }  // extern "C"

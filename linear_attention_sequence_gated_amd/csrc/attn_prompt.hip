@@ -60,14 +60,20 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
   }
   first = __builtin_amdgcn_readfirstlane(first);
   last = __builtin_amdgcn_readfirstlane(last);
-  if (last < 0) return;  // no row of the tile is in a sequence
+  if (last < 0) {  // no row of the tile is in a sequence
+    if (a.zero_rest) zero_rows<D>(static_cast<__bf16*>(a.out) + (long long)hq * D, (long long)a.Hq * D, r0, min(BM, a.T - r0), NT);
+    if (a.zero_rest)
+      for (int i = tid; i < BM && r0 + i < a.T; i += NT) a.lse[(size_t)hq * a.T + r0 + i] = 0.f;
+    return;
+  }
 
   // queries: operands for the wave's rows, their sign turned for a negative scale
   const int w0 = r0 + wave * 32 * QT;
   u32x4 q[QT][KS];
   int row[QT], beg[QT];
   int lowest = a.T, highest = -1;  // the range of beg over the wave's rows
-  const float c = __builtin_fabsf(a.scale) * kLog2e;
+  // a scale of zero stays just above it, so that masked scores, -infinity, keep a weight of zero
+  const float c = fmaxf(__builtin_fabsf(a.scale) * kLog2e, 1e-37f);
   const unsigned flip = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
@@ -91,6 +97,12 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
   lowest = __builtin_amdgcn_readfirstlane(lowest);
   highest = __builtin_amdgcn_readfirstlane(highest);
 
+  int from[QT], upto[QT];  // the keys that the lane's row sees, less 4 hl
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    from[t] = beg[t] - 4 * hl;
+    upto[t] = beg[t] < 0 ? -8 : row[t] - 4 * hl;
+  }
   f32x16 o[QT][DT];
   float m[QT], l[QT];
 #pragma unroll
@@ -131,16 +143,13 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
     u32x4 p[QT][4];
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      unsigned seen = 0;  // bit 16 n + e
       if constexpr (MASKED) {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const int key = kv + 32 * n + 8 * (e / 4) + 4 * hl + e % 4;
-            const bool x = beg[t] >= 0 && key >= beg[t] && key <= row[t];
-            seen |= (x ? 1u : 0u) << (16 * n + e);
-            s[t][n][e] = x ? s[t][n][e] : -INFINITY;
+            const int key = 32 * n + 8 * (e / 4) + e % 4;  // from kv + 4 hl on
+            s[t][n][e] = key >= from[t] - kv && key <= upto[t] - kv ? s[t][n][e] : -INFINITY;
           }
       }
       float top = s[t][0][0];
@@ -161,8 +170,7 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
       for (int n = 0; n < 2; ++n) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][n][e], c, -m[t]));
-          if constexpr (MASKED) x = (seen >> (16 * n + e)) & 1u ? x : 0.f;
+          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][n][e], c, -m[t]));
           s[t][n][e] = x;
           sum += x;
         }
@@ -199,18 +207,33 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
   };
   stage(0, first);
   int buf = 0;
-  for (int kv = first; kv < last; kv += kN, buf ^= 1) {
+  int kv = first;
+  auto next = [&] {
     staged_barrier();
     if (kv + kN < last) stage(buf ^ 1, kv + kN);
-    if (kv > w0 + 32 * QT - 1 || kv + kN <= lowest) continue;  // nothing of it is seen by the wave's rows
-    if (kv + kN - 1 > w0 || kv < highest || kv + kN > last) step(std::true_type{}, lds.k[buf], lds.v[buf], kv);
-    else step(std::false_type{}, lds.k[buf], lds.v[buf], kv);
+  };
+  // tiles of which some row misses some key, at both ends of the range, and
+  // those between, which all rows see whole (loops apart: one loop with both
+  // bodies takes more registers than there are)
+  auto edge = [&](int end) {
+    for (; kv < end; kv += kN, buf ^= 1) {
+      next();
+      if (kv <= w0 + 32 * QT - 1 && kv + kN > lowest) step(std::true_type{}, lds.k[buf], lds.v[buf], kv);
+    }
+  };
+  edge(min(highest, last));
+  for (; kv + kN - 1 <= w0; kv += kN, buf ^= 1) {
+    next();
+    step(std::false_type{}, lds.k[buf], lds.v[buf], kv);
   }
+  edge(last);
 
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    const float z = sum_halves(l[t]), inv = 1.f / z;
-    if (beg[t] >= 0) {
+    const float z = sum_halves(l[t]);
+    const bool rest = beg[t] < 0 && row[t] < a.T && a.zero_rest;
+    const float inv = rest ? 0.f : 1.f / z;
+    if (beg[t] >= 0 || rest) {
       __bf16* dst = static_cast<__bf16*>(a.out) + ((size_t)row[t] * a.Hq + hq) * D + 4 * hl;
 #pragma unroll
       for (int i = 0; i < DT; ++i)
@@ -218,7 +241,7 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
         for (int e = 0; e < 4; ++e)
           *reinterpret_cast<u32x2*>(dst + 32 * i + 8 * e) = pipe::cvt4(
               f32x4{o[t][i][4 * e] * inv, o[t][i][4 * e + 1] * inv, o[t][i][4 * e + 2] * inv, o[t][i][4 * e + 3] * inv});
-      if (hl == 0) a.lse[(size_t)hq * a.T + row[t]] = (m[t] + __builtin_amdgcn_logf(z)) * kLn2;
+      if (hl == 0) a.lse[(size_t)hq * a.T + row[t]] = rest ? 0.f : (m[t] + __builtin_amdgcn_logf(z)) * kLn2;
     }
   }  if (dirty_hi == 0) return;
 #pragma unroll
@@ -227,8 +250,8 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
     __bf16* dst = static_cast<__bf16*>(a.out) + ((size_t)row[t] * a.Hq + hq) * D;
     for (int key = max(beg[t], dirty_lo); key <= row[t] && key < dirty_hi; ++key) {
       const __bf16* src = static_cast<const __bf16*>(a.v) + (long long)key * a.vs + (long long)kvh * D;
-      for (int d = 32 * hl; d < D; d += 64)
-        for (int i = 0; i < 32; ++i) {
+      for (int d = 4 * hl; d < D; d += 8)  // the entries that this lane stored
+        for (int i = 0; i < 4; ++i) {
           const float x = (float)src[d + i];
           if (!__builtin_isfinite(x)) dst[d + i] = (__bf16)((float)dst[d + i] + x);
         }

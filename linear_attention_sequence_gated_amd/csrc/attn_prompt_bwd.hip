@@ -25,26 +25,14 @@ constexpr float kLog2e = 1.44269504088896f;
 constexpr int kN = 64;  // rows of a staged tile
 
 // acc[t] += (columns 32 t of a staged tile, rows r0 .. r0 + 15)^T w, as kept in
-// acc's registers.  Where the tile is not clean (a value that no weight may
-// meet is not finite, see masked tiles) its non-finite values count as zero and
-// as NaN where a weight other than zero meets them.
-template <int D>
-__device__ __forceinline__ void add_columns(f32x16 (&acc)[D / 32], const __bf16* tile, int base, int r0, const u32x4& w,
-                                            bool clean) {
+// acc's registers.  DIRTY: the tile holds values that are not finite, which
+// some weights, zeros, must not meet: such values are left out.
+template <bool DIRTY, int D>
+__device__ __forceinline__ void add_columns(f32x16 (&acc)[D / 32], const __bf16* tile, int base, int r0, const u32x4& w) {
 #pragma unroll
   for (int t = 0; t < D / 32; ++t) {
     const u32x4 f = col_frag<D>(tile, base, r0, t);
-    if (clean) {
-      acc[t] = mma(f, w, acc[t]);
-    } else {
-      acc[t] = mma(pick(f, 0), w, acc[t]);
-      const u32x4 size{w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu, w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu};
-      f32x16 bad = zero16();
-#pragma unroll
-      for (int kind = 1; kind < 4; ++kind) bad = mma(pick(f, kind), size, bad);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[t][e] = bad[e] > 0.f ? __builtin_nanf("") : acc[t][e];
-    }
+    acc[t] = mma(DIRTY ? finite_only(f) : f, w, acc[t]);
   }
 }
 
@@ -57,29 +45,57 @@ template <int D> __device__ __forceinline__ void store_rows(__bf16* dst, const f
           pipe::cvt4(f32x4{acc[i][4 * e] * f, acc[i][4 * e + 1] * f, acc[i][4 * e + 2] * f, acc[i][4 * e + 3] * f});
 }
 
+// NaN into a gradient row's entries wherever rows [lo, hi) of src hold a value
+// that is not finite: what add_columns left out, for the rows that it concerns.
+// Each lane sees to the entries that it stored.
+template <int D>
+__device__ __forceinline__ void spoil(__bf16* dst, const void* src, long long stride, int lo, int hi, int hl) {
+  for (int i = lo; i < hi; ++i) {
+    const __bf16* x = static_cast<const __bf16*>(src) + (long long)i * stride;
+    for (int d = 4 * hl; d < D; d += 8)
+      for (int j = 0; j < 4; ++j)
+        if (!__builtin_isfinite((float)x[d + j])) dst[d + j] = (__bf16)__builtin_nanf("");
+  }
+}
+
 // ---------------------------------------------------------------------- dq
 template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(PromptBwdArgs a) {
   constexpr int BM = 32 * NW, NT = 64 * NW, KS = D / 16;
   __shared__ __bf16 kt[2][kN * D], vt[2][kN * D];
-  __shared__ int begs[BM], window[BM + 1], lows[NW];
+  __shared__ int begs[BM], window[BM + 1], lows[NW], tops[NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const int tiles = (a.T + BM - 1) / BM;
   const int rank = blockIdx.x / a.Hq, hq = blockIdx.x - rank * a.Hq;
   const int r0 = (tiles - 1 - rank) * BM, kvh = hq / (a.Hq / a.Hkv);
 
   find_rows<BM, NT>(a.cu, a.R, a.T, r0, window, begs, nullptr);
-  int first = a.T;
+  int first = a.T, last = -1;  // the keys that the tile's rows see
   for (int i = tid; i < BM; i += NT)
-    if (begs[i] >= 0) first = min(first, begs[i]);
+    if (begs[i] >= 0) {
+      first = min(first, begs[i]);
+      last = max(last, r0 + i + 1);
+    }
 #pragma unroll
-  for (int d = 32; d; d >>= 1) first = min(first, __shfl_xor(first, d));
-  if (lane == 0) lows[wave] = first;
+  for (int d = 32; d; d >>= 1) {
+    first = min(first, __shfl_xor(first, d));
+    last = max(last, __shfl_xor(last, d));
+  }
+  if (lane == 0) {
+    lows[wave] = first;
+    tops[wave] = last;
+  }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < NW; ++w) first = min(first, lows[w]);
+  for (int w = 0; w < NW; ++w) {
+    first = min(first, lows[w]);
+    last = max(last, tops[w]);
+  }
   first = __builtin_amdgcn_readfirstlane(first);
-  if (first >= a.T) return;
-  const int last = min(r0 + BM, a.T);
+  last = __builtin_amdgcn_readfirstlane(last);
+  if (last < 0) {  // no row of the tile is in a sequence
+    if (a.zero_rest) zero_rows<D>(static_cast<__bf16*>(a.grad_q) + (long long)hq * D, a.gqs, r0, min(BM, a.T - r0), NT);
+    return;
+  }
 
   const int w0 = r0 + wave * 32, row = w0 + (lane & 31), beg = begs[row - r0];
   const int at = min(row, a.T - 1);
@@ -131,51 +147,84 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
     sk.load(kt[buf], rows_rsrc(kp, a.ks, kv, n, D), wave);
     sv.load(vt[buf], rows_rsrc(vp, a.vs, kv, n, D), wave);
   };
-  stage(0, first);
-  int buf = 0;
-  for (int kv = first; kv < last; kv += kN, buf ^= 1) {
-    staged_barrier();
-    if (kv + kN < last) stage(buf ^ 1, kv + kN);
-    if (kv > w0 + 31 || kv + kN <= lowest) continue;
-    const bool masked = kv + kN - 1 > w0 || kv < highest || kv + kN > last;
-    const bool clean = !masked || clean_tile<D, kN>(kt[buf]);
-#pragma unroll
+  const int from = beg - 4 * hl, upto = beg < 0 ? -8 : row - 4 * hl;  // the keys that the lane's row sees
+  int dirty_lo = last, dirty_hi = 0;                                   // keys of tiles in which values were left out
+  int buf = 0, kv = first;
+  auto step = [&](auto masked_, auto dirty_, const __bf16* K, const __bf16* V) {
+    constexpr bool MASKED = decltype(masked_)::value, DIRTY = decltype(dirty_)::value;
+#pragma unroll 1
     for (int n = 0; n < 2; ++n) {
       f32x16 s = zero16(), dp = zero16();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        s = mma(row_frag<D>(kt[buf], rb, 32 * n, ks), q[ks], s);
-        dp = mma(row_frag<D>(vt[buf], rb, 32 * n, ks), g[ks], dp);
+        s = mma(row_frag<D>(K, rb, 32 * n, ks), q[ks], s);
+        dp = mma(row_frag<D>(V, rb, 32 * n, ks), g[ks], dp);
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -lse2));
         s[e] = p * (dp[e] - delta);
-      }
-      if (masked) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int key = kv + 32 * n + 8 * (e / 4) + 4 * hl + e % 4;
-          s[e] = beg >= 0 && key >= beg && key <= row ? s[e] : 0.f;
-        }
+        const int key = 32 * n + 8 * (e / 4) + e % 4;  // from kv + 4 hl on
+        if constexpr (MASKED) s[e] = key >= from - kv && key <= upto - kv ? s[e] : 0.f;
       }
 #pragma unroll
-      for (int b = 0; b < 2; ++b) add_columns<D>(dq, kt[buf], cb, 32 * n + 16 * b, operand(s, b), clean);
+      for (int b = 0; b < 2; ++b) add_columns<DIRTY, D>(dq, K, cb, 32 * n + 16 * b, operand(s, b));
     }
+  };
+  stage(0, first);
+  auto next = [&] {
+    staged_barrier();
+    if (kv + kN < last) stage(buf ^ 1, kv + kN);
+  };
+  // tiles of which some row misses some key, at both ends, and those between
+  auto edge = [&](int end) {
+    for (; kv < end; kv += kN, buf ^= 1) {
+      next();
+      if (kv > w0 + 31 || kv + kN <= lowest) continue;
+      if (clean_tile<D, kN>(kt[buf])) {
+        step(std::true_type{}, std::false_type{}, kt[buf], vt[buf]);
+      } else {
+        step(std::true_type{}, std::true_type{}, kt[buf], vt[buf]);
+        dirty_lo = min(dirty_lo, kv);
+        dirty_hi = kv + kN;
+      }
+    }
+  };
+  edge(min(highest, last));
+  for (; kv + kN - 1 <= w0; kv += kN, buf ^= 1) {
+    next();
+    step(std::false_type{}, std::false_type{}, kt[buf], vt[buf]);
   }
-  if (beg >= 0) store_rows<D>(static_cast<__bf16*>(a.grad_q) + (long long)row * a.gqs + (long long)hq * D, dq, a.scale, hl);
+  edge(last);
+  const bool rest = beg < 0 && row < a.T && a.zero_rest;
+  if (beg >= 0 || rest)
+    store_rows<D>(static_cast<__bf16*>(a.grad_q) + (long long)row * a.gqs + (long long)hq * D, dq, rest ? 0.f : a.scale, hl);
+  if (dirty_hi && beg >= 0) {
+    spoil<D>(static_cast<__bf16*>(a.grad_q) + (long long)row * a.gqs + (long long)hq * D, kp, a.ks, max(beg, dirty_lo),
+             min(row + 1, dirty_hi), hl);
+  }
 }
 
 // ------------------------------------------------------------------ dk, dv
-template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(PromptBwdArgs a) {
-  constexpr int BN = 32 * NW, NT = 64 * NW, KS = D / 16;
+// Two waves to 32 keys: one computes the scores and dv, the other do . v and
+// dk.  Either holds one operand and one accumulator for its keys (96 registers
+// at D = 128, where one wave for both would need 192 before its first score),
+// both run the same code on Q and dO in turned roles, and all that passes
+// between them are the probabilities, through LDS, lane by lane, in float32.
+template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv_kernel(PromptBwdArgs a) {
+  constexpr int BN = 32 * NP, NW = 2 * NP, NT = 64 * NW, KS = D / 16;
   __shared__ __bf16 qt[2][kN * D], gt[2][kN * D];
   __shared__ float lt[2][kN], dt[2][kN];
+  __shared__ f32x4 hand[NP][8][64];
   __shared__ int begs[BN], ends[BN], window[BN + 1], most[NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
+  const int pair = wave % NP;
+  const bool second = wave >= NP;  // do . v and dk
   // the first tiles of a long sequence meet the most rows
   const int rank = blockIdx.x / a.Hkv, kvh = blockIdx.x - rank * a.Hkv;
   const int r0 = rank * BN, G = a.Hq / a.Hkv;
+  __bf16* grad = static_cast<__bf16*>(second ? a.grad_k : a.grad_v) + (long long)kvh * D;
+  const long long gs = second ? a.gks : a.gvs;
 
   find_rows<BN, NT>(a.cu, a.R, a.T, r0, window, begs, ends);
   int last = -1;  // the row behind the last that attends to a key of the tile
@@ -187,22 +236,24 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
 #pragma unroll
   for (int w = 0; w < NW; ++w) last = max(last, most[w]);
   last = __builtin_amdgcn_readfirstlane(last);
-  if (last < 0) return;
-
-  const int w0 = r0 + wave * 32, key = w0 + (lane & 31), end = ends[key - r0];
-  const int at = min(key, a.T - 1);
-  const float c = a.scale * kLog2e;
-  u32x4 k[KS], v[KS];
-  {
-    const __bf16* kp = static_cast<const __bf16*>(a.k) + (long long)at * a.ks + (long long)kvh * D + 8 * hl;
-    const __bf16* vp = static_cast<const __bf16*>(a.v) + (long long)at * a.vs + (long long)kvh * D + 8 * hl;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      k[ks] = *reinterpret_cast<const u32x4*>(kp + 16 * ks);
-      v[ks] = *reinterpret_cast<const u32x4*>(vp + 16 * ks);
-    }
+  if (last < 0) {
+    if (a.zero_rest && pair == 0)
+      for (int i = lane; i < BN * (D / 8); i += 64)
+        if (r0 + i / (D / 8) < a.T)
+          *reinterpret_cast<u32x4*>(grad + (long long)(r0 + i / (D / 8)) * gs + i % (D / 8) * 8) = u32x4{0u, 0u, 0u, 0u};
+    return;
   }
-  int lowest = end, highest = end;  // the range of end over the wave's keys
+
+  const int w0 = r0 + pair * 32, key = w0 + (lane & 31), end = ends[key - r0];
+  const float c = a.scale * kLog2e;
+  u32x4 kv[KS];
+  {
+    const __bf16* src = static_cast<const __bf16*>(second ? a.v : a.k) + (long long)min(key, a.T - 1) * (second ? a.vs : a.ks) +
+                        (long long)kvh * D + 8 * hl;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) kv[ks] = *reinterpret_cast<const u32x4*>(src + 16 * ks);
+  }
+  int lowest = end, highest = end;  // the range of end over the pair's keys
 #pragma unroll
   for (int d = 32; d; d >>= 1) {
     lowest = min(lowest, __shfl_xor(lowest, d));
@@ -211,78 +262,116 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
   lowest = __builtin_amdgcn_readfirstlane(lowest);
   highest = __builtin_amdgcn_readfirstlane(highest);
 
-  f32x16 dk[D / 32], dv[D / 32];
+  f32x16 acc[D / 32];
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) dk[i] = dv[i] = zero16();
+  for (int i = 0; i < D / 32; ++i) acc[i] = zero16();
   const int rb = row_base<D>(lane), cb = col_base<D>(lane);
-  Stage<D, kN, NW> sq, sg;
-  sq.init(a.qs, wave);
-  sg.init(a.gos, wave);
   const __bf16* qp = static_cast<const __bf16*>(a.q);
   const __bf16* gp = static_cast<const __bf16*>(a.grad_out);
+  // Q is staged by the first waves, dO by the second
+  Stage<D, kN, NP> st;
+  st.init(second ? a.gos : a.qs, pair);
   auto stage = [&](int buf, int hq, int i0) {
     const int n = min(kN, last - i0);
-    sq.load(qt[buf], rows_rsrc(qp + (long long)hq * D, a.qs, i0, n, D), wave);
-    sg.load(gt[buf], rows_rsrc(gp + (long long)hq * D, a.gos, i0, n, D), wave);
+    if (second) st.load(gt[buf], rows_rsrc(gp + (long long)hq * D, a.gos, i0, n, D), pair);
+    else st.load(qt[buf], rows_rsrc(qp + (long long)hq * D, a.qs, i0, n, D), pair);
     if (wave == 0) stage_words(lt[buf], pipe::make_rsrc(a.ws + (size_t)hq * a.T + i0, n * 4));
-    if (wave == 1) stage_words(dt[buf], pipe::make_rsrc(a.ws + (size_t)(a.Hq + hq) * a.T + i0, n * 4));
+    if (wave == NP) stage_words(dt[buf], pipe::make_rsrc(a.ws + (size_t)(a.Hq + hq) * a.T + i0, n * 4));
   };
-  const int steps = (last - r0 + kN - 1) / kN, total = steps * G;
-  stage(0, kvh * G, r0);
-  int buf = 0, head = 0, i0 = r0;
-  for (int it = 0; it < total; ++it, buf ^= 1) {
-    staged_barrier();
-    int nh = head, ni = i0 + kN;
-    if (ni >= last) {
-      nh = head + 1;
-      ni = r0;
-    }
-    if (it + 1 < total) stage(buf ^ 1, kvh * G + nh, ni);
-    const int i1 = i0;
-    head = nh;
-    i0 = ni;
-    if (i1 + kN - 1 < w0 || i1 >= highest) continue;
-    const bool masked = i1 < w0 + 31 || i1 + kN > lowest;
-    const bool clean = !masked || (clean_tile<D, kN>(qt[buf]) && clean_tile<D, kN>(gt[buf]));
+  // the two halves of a tile of rows that the pair's keys may be seen by
+  f32x16 s[2];
+  auto scores = [&](auto masked_, int buf, int i1) {
+    constexpr bool MASKED = decltype(masked_)::value;
+    const __bf16* X = second ? gt[buf] : qt[buf];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      f32x16 s = zero16(), dp = zero16();
+      s[n] = zero16();
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        s = mma(row_frag<D>(qt[buf], rb, 32 * n, ks), k[ks], s);
-        dp = mma(row_frag<D>(gt[buf], rb, 32 * n, ks), v[ks], dp);
-      }
+      for (int ks = 0; ks < KS; ++ks) s[n] = mma(row_frag<D>(X, rb, 32 * n, ks), kv[ks], s[n]);
+    }
+    if (second) return;
+    const int from = key - i1 - 4 * hl, upto = end - 1 - i1 - 4 * hl;  // the rows that see the lane's key
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int e4 = 0; e4 < 4; ++e4) {
         const f32x4 l = *reinterpret_cast<const f32x4*>(&lt[buf][32 * n + 8 * e4 + 4 * hl]);
-        const f32x4 d = *reinterpret_cast<const f32x4*>(&dt[buf][32 * n + 8 * e4 + 4 * hl]);
+        f32x4 p;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int e = 4 * e4 + j;
-          s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -l[j]));
-          dp[e] = s[e] * (dp[e] - d[j]);
+          const int i = 32 * n + 8 * e4 + j;  // from i1 + 4 hl on
+          p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][4 * e4 + j], c, -l[j]));
+          if constexpr (MASKED) p[j] = i >= from && i <= upto ? p[j] : 0.f;
+          s[n][4 * e4 + j] = p[j];
         }
+        hand[pair][4 * n + e4][lane] = p;
       }
-      if (masked) {
+  };
+  auto products = [&](auto masked_, auto dirty_, int buf, int i1) {
+    constexpr bool MASKED = decltype(masked_)::value, DIRTY = decltype(dirty_)::value;
+    const __bf16* Y = second ? qt[buf] : gt[buf];
+    if (second) {
+      const int from = key - i1 - 4 * hl, upto = end - 1 - i1 - 4 * hl;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int i = i1 + 32 * n + 8 * (e / 4) + 4 * hl + e % 4;
-          const bool seen = i >= key && i < end;
-          s[e] = seen ? s[e] : 0.f;
-          dp[e] = seen ? dp[e] : 0.f;
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+          const f32x4 p = hand[pair][4 * n + e4][lane];
+          const f32x4 d = *reinterpret_cast<const f32x4*>(&dt[buf][32 * n + 8 * e4 + 4 * hl]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int i = 32 * n + 8 * e4 + j;
+            float x = p[j] * (s[n][4 * e4 + j] - d[j]);
+            if constexpr (MASKED) x = i >= from && i <= upto ? x : 0.f;
+            s[n][4 * e4 + j] = x;
+          }
         }
-      }
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        add_columns<D>(dv, gt[buf], cb, 32 * n + 16 * b, operand(s, b), clean);
-        add_columns<D>(dk, qt[buf], cb, 32 * n + 16 * b, operand(dp, b), clean);
-      }
     }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) add_columns<DIRTY, D>(acc, Y, cb, 32 * n + 16 * b, operand(s[n], b));
+  };
+  bool dirty = false;  // values were left out
+  stage(0, kvh * G, r0);
+  int buf = 0;
+  for (int head = 0; head < G; ++head) {
+    int i1 = r0;
+    auto next = [&] {
+      staged_barrier();
+      if (i1 + kN < last) stage(buf ^ 1, kvh * G + head, i1 + kN);
+      else if (head + 1 < G) stage(buf ^ 1, kvh * G + head + 1, r0);
+    };
+    // tiles of which some row misses some key, at both ends, and those between
+    auto edge = [&](int stop) {
+      for (; i1 < stop; i1 += kN, buf ^= 1) {
+        const bool met = i1 + kN - 1 >= w0 && i1 < highest;
+        next();
+        if (met) scores(std::true_type{}, buf, i1);
+        pipe::stage_barrier();
+        if (!met) continue;
+        if (clean_tile<D, kN>(second ? qt[buf] : gt[buf])) {
+          products(std::true_type{}, std::false_type{}, buf, i1);
+        } else {
+          products(std::true_type{}, std::true_type{}, buf, i1);
+          dirty = true;
+        }
+      }
+    };
+    edge(min(w0 + 31, last));
+    for (; i1 + kN <= lowest; i1 += kN, buf ^= 1) {
+      next();
+      scores(std::false_type{}, buf, i1);
+      pipe::stage_barrier();
+      products(std::false_type{}, std::false_type{}, buf, i1);
+    }
+    edge(last);
   }
-  if (end >= 0) {
-    store_rows<D>(static_cast<__bf16*>(a.grad_k) + (long long)key * a.gks + (long long)kvh * D, dk, a.scale, hl);
-    store_rows<D>(static_cast<__bf16*>(a.grad_v) + (long long)key * a.gvs + (long long)kvh * D, dv, 1.f, hl);
-  }
+  const bool rest = end < 0 && key < a.T && a.zero_rest;
+  if (end >= 0 || rest) store_rows<D>(grad + (long long)key * gs, acc, rest ? 0.f : (second ? a.scale : 1.f), hl);
+  if (dirty && end >= 0)
+    for (int h = kvh * G; h < (kvh + 1) * G; ++h)
+      spoil<D>(grad + (long long)key * gs, (second ? qp : gp) + (long long)h * D, second ? a.qs : a.gos, key, end, hl);
 }
 
 template <int D> hipError_t launch(const PromptBwdArgs& a) {
@@ -291,7 +380,7 @@ template <int D> hipError_t launch(const PromptBwdArgs& a) {
   hipStream_t st = static_cast<hipStream_t>(a.stream);
   const hipError_t e = launch_kernel(attn_dq_kernel<D, NW>, dim3(tiles * a.Hq), dim3(64 * NW), st, a);
   if (e != hipSuccess) return e;
-  return launch_kernel(attn_dkv_kernel<D, NW>, dim3(tiles * a.Hkv), dim3(64 * NW), st, a);
+  return launch_kernel(attn_dkv_kernel<D, 4>, dim3(tiles * a.Hkv), dim3(512), st, a);
 }
 
 }  // namespace

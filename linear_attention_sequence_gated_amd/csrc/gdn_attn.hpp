@@ -65,7 +65,7 @@ struct PromptArgs {
   float* lse;
   float scale;
   long long qs, ks, vs;
-  int T, R, Hq, Hkv, D;
+  int T, R, Hq, Hkv, D, zero_rest;
   void* stream;
 };
 hipError_t launch_attn_prompt(const PromptArgs& a);
@@ -84,7 +84,7 @@ struct PromptBwdArgs {
   float* ws;
   float scale;
   long long qs, ks, vs, gos, gqs, gks, gvs;
-  int T, R, Hq, Hkv, D;
+  int T, R, Hq, Hkv, D, zero_rest;
   void* stream;
 };
 size_t attn_prompt_bwd_workspace_bytes(int T, int Hq);

@@ -126,6 +126,12 @@ __device__ __forceinline__ void staged_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// Sets rows [r0, r0 + n) of one head to zero, by NT threads.
+template <int D> __device__ __forceinline__ void zero_rows(__bf16* dst, long long stride, int r0, int n, int NT) {
+  for (int i = threadIdx.x; i < n * (D / 8); i += NT)
+    *reinterpret_cast<u32x4*>(dst + (long long)(r0 + i / (D / 8)) * stride + i % (D / 8) * 8) = u32x4{0u, 0u, 0u, 0u};
+}
+
 // ----------------------------------------------------------- non-finite values
 // Non-finite bf16 values have all exponent bits set; the larger of a word's
 // halves without their signs, over words.
@@ -159,7 +165,7 @@ __device__ __forceinline__ u32x4 finite_only(const u32x4& w) { return pick(w, 0)
 template <int D, int N> __device__ __forceinline__ bool clean_tile(const __bf16* tile) {
   unsigned w = 0;
   const u32x4* p = reinterpret_cast<const u32x4*>(tile);
-#pragma unroll
+#pragma unroll 4
   for (int i = 0; i < N * D / 512; ++i) {
     const u32x4 x = p[i * 64 + (threadIdx.x & 63)];
     w = worst(worst(worst(worst(w, x[0]), x[1]), x[2]), x[3]);

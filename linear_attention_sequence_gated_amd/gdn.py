@@ -76,11 +76,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.gdn_attn_decode_workspace_bytes.restype = sz
     lib.gdn_attn_decode.argtypes = [vp] * 9 + [fl, ll] + [ci] * 9 + [vp, sz, vp]
     lib.gdn_attn_decode.restype = ci
-    lib.gdn_attn_prompt.argtypes = [vp] * 6 + [fl] + [ll] * 3 + [ci] * 6 + [vp]
+    lib.gdn_attn_prompt.argtypes = [vp] * 6 + [fl] + [ll] * 3 + [ci] * 7 + [vp]
     lib.gdn_attn_prompt.restype = ci
     lib.gdn_attn_prompt_bwd_workspace_bytes.argtypes = [ci] * 4
     lib.gdn_attn_prompt_bwd_workspace_bytes.restype = sz
-    lib.gdn_attn_prompt_bwd.argtypes = [vp] * 10 + [fl] + [ll] * 7 + [ci] * 6 + [vp, sz, vp]
+    lib.gdn_attn_prompt_bwd.argtypes = [vp] * 10 + [fl] + [ll] * 7 + [ci] * 7 + [vp, sz, vp]
     lib.gdn_attn_prompt_bwd.restype = ci
     lib.gdn_status_str.argtypes = [ci]
     lib.gdn_status_str.restype = ctypes.c_char_p
@@ -163,9 +163,9 @@ def gdn_attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
 
 
 def gdn_attn_prompt(q, k, v, cu_seqlens, out, lse, scale, q_stride, k_stride, v_stride, T, R, Hq, Hkv, D, dtype,
-                    stream) -> int:
+                    zero_rest, stream) -> int:
     return int(load().gdn_attn_prompt(q, k, v, cu_seqlens, out, lse, scale, q_stride, k_stride, v_stride, T, R, Hq,
-                                      Hkv, D, dtype, stream))
+                                      Hkv, D, dtype, zero_rest, stream))
 
 
 def gdn_attn_prompt_bwd_workspace_bytes(T, Hq, Hkv, D) -> int:
@@ -174,10 +174,11 @@ def gdn_attn_prompt_bwd_workspace_bytes(T, Hq, Hkv, D) -> int:
 
 def gdn_attn_prompt_bwd(q, k, v, out, lse, grad_out, cu_seqlens, grad_q, grad_k, grad_v, scale, q_stride, k_stride,
                         v_stride, grad_out_stride, grad_q_stride, grad_k_stride, grad_v_stride, T, R, Hq, Hkv, D, dtype,
-                        workspace, workspace_bytes, stream) -> int:
+                        zero_rest, workspace, workspace_bytes, stream) -> int:
     return int(load().gdn_attn_prompt_bwd(q, k, v, out, lse, grad_out, cu_seqlens, grad_q, grad_k, grad_v, scale,
                                           q_stride, k_stride, v_stride, grad_out_stride, grad_q_stride, grad_k_stride,
-                                          grad_v_stride, T, R, Hq, Hkv, D, dtype, workspace, workspace_bytes, stream))
+                                          grad_v_stride, T, R, Hq, Hkv, D, dtype, zero_rest, workspace,
+                                          workspace_bytes, stream))
 
 
 # ------------------------------------------------------------- torch helpers

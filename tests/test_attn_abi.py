@@ -96,7 +96,7 @@ def test_decode_workspace():
 
 def prompt(**kw):
     args = dict(q=A, k=A, v=A, cu_seqlens=A, out=A, lse=A, scale=0.125, q_stride=512, k_stride=256, v_stride=256, T=100,
-                R=3, Hq=8, Hkv=4, D=64, dtype=gdn.GDN_BF16, stream=None)
+                R=3, Hq=8, Hkv=4, D=64, dtype=gdn.GDN_BF16, zero_rest=0, stream=None)
     args.update(kw)
     return gdn.gdn_attn_prompt(**args)
 
@@ -122,14 +122,13 @@ def test_prompt_argument_errors(kw, status):
 def test_prompt_of_nothing_is_noop():
     none = dict(q=None, k=None, v=None, cu_seqlens=None, out=None, lse=None)
     assert prompt(T=0, **none) == raw.GDN_OK
-    assert prompt(R=0, **none) == raw.GDN_OK
 
 
 def prompt_bwd(**kw):
     args = dict(q=A, k=A, v=A, out=A, lse=A, grad_out=A, cu_seqlens=A, grad_q=A, grad_k=A, grad_v=A, scale=0.125,
                 q_stride=512, k_stride=256, v_stride=256, grad_out_stride=512, grad_q_stride=512, grad_k_stride=256,
-                grad_v_stride=256, T=100, R=3, Hq=8, Hkv=4, D=64, dtype=gdn.GDN_BF16, workspace=A,
-                workspace_bytes=1 << 40, stream=None)
+                grad_v_stride=256, T=100, R=3, Hq=8, Hkv=4, D=64, dtype=gdn.GDN_BF16, zero_rest=0,
+                workspace=A, workspace_bytes=1 << 40, stream=None)
     args.update(kw)
     return gdn.gdn_attn_prompt_bwd(**args)
 
@@ -151,7 +150,7 @@ def test_prompt_bwd_workspace():
     assert gdn.gdn_attn_prompt_bwd_workspace_bytes(100, 8, 4, 64) == 2 * 100 * 8 * 4  # lse and delta
     assert gdn.gdn_attn_prompt_bwd_workspace_bytes(100, 8, 3, 64) == 0
     none = {n: None for n in ("q", "k", "v", "out", "lse", "grad_out", "cu_seqlens", "grad_q", "grad_k", "grad_v", "workspace")}
-    assert prompt_bwd(T=0, **none) == raw.GDN_OK and prompt_bwd(R=0, **none) == raw.GDN_OK
+    assert prompt_bwd(T=0, **none) == raw.GDN_OK
 
 
 def test_cache_helpers_refuse_on_cpu():
