@@ -142,7 +142,7 @@ int gdn_attn_prompt(const void* q, const void* k, const void* v, const int* cu_s
 }
 
 size_t gdn_attn_prompt_bwd_workspace_bytes(int T, int Hq, int Hkv, int D) {
-  return prompt_shape(T, 0, Hq, Hkv, D) ? 0 : gdn::attn_prompt_bwd_workspace_bytes(T, Hq);
+  return prompt_shape(T, 0, Hq, Hkv, D) ? 0 : gdn::attn_prompt_bwd_workspace_bytes(T, Hq, Hkv, D);
 }
 
 int gdn_attn_prompt_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse,
@@ -163,7 +163,7 @@ int gdn_attn_prompt_bwd(const void* q, const void* k, const void* v, const void*
   if (!q || !k || !v || !out || !lse || !grad_out || !cu_seqlens || !grad_q || !grad_k || !grad_v) return GDN_ERR_NULL;
   const void* ptrs[] = {q, k, v, out, lse, grad_out, cu_seqlens, grad_q, grad_k, grad_v, workspace};
   if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
-  if (!workspace || workspace_bytes < gdn::attn_prompt_bwd_workspace_bytes(T, Hq)) return GDN_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < gdn::attn_prompt_bwd_workspace_bytes(T, Hq, Hkv, D)) return GDN_ERR_WORKSPACE;
   return status(gdn::launch_attn_prompt_bwd({q, k, v, out, lse, grad_out, cu_seqlens, grad_q, grad_k, grad_v,
                                              static_cast<float*>(workspace), scale, q_stride, k_stride, v_stride,
                                              grad_out_stride, grad_q_stride, grad_k_stride, grad_v_stride, T, R, Hq,

@@ -6,11 +6,12 @@
 //   dq_i = scale sum_j ds_ij k_j,     dk_j = scale sum_i ds_ij q_i,
 // dk and dv summed over the query heads that share key head j's.
 //
-// Two launches, each of which owns the gradients it writes, so that nothing is
-// added through memory and the order of every sum is fixed: one per tile of
-// rows for dq (three products for a pair of tiles), one per tile of keys for dk
-// and dv (four).  The probabilities are computed in both; the first launch
-// leaves lse and delta, in powers of two, in the workspace for the second.
+// One launch by tiles of rows for dq (three products for a pair of tiles), one
+// by tiles of keys for dk and dv (four), each of which owns the sums it writes,
+// so that their order is fixed.  The probabilities are computed in both; the
+// first launch leaves lse (times log2 e) and delta in the workspace for the
+// second.  Where there are few keys to share out, the query heads of a key head
+// are shared out too, and a third launch adds their sums.
 #include "../../include/gdn.h"
 #include "gdn_attn.hpp"
 #include "gdn_launch.hpp"
@@ -48,13 +49,13 @@ template <int D> __device__ __forceinline__ void store_rows(__bf16* dst, const f
 // NaN into a gradient row's entries wherever rows [lo, hi) of src hold a value
 // that is not finite: what add_columns left out, for the rows that it concerns.
 // Each lane sees to the entries that it stored.
-template <int D>
-__device__ __forceinline__ void spoil(__bf16* dst, const void* src, long long stride, int lo, int hi, int hl) {
+template <int D, class T>
+__device__ __forceinline__ void spoil(T* dst, const void* src, long long stride, int lo, int hi, int hl) {
   for (int i = lo; i < hi; ++i) {
     const __bf16* x = static_cast<const __bf16*>(src) + (long long)i * stride;
     for (int d = 4 * hl; d < D; d += 8)
       for (int j = 0; j < 4; ++j)
-        if (!__builtin_isfinite((float)x[d + j])) dst[d + j] = (__bf16)__builtin_nanf("");
+        if (!__builtin_isfinite((float)x[d + j])) dst[d + j] = (T)__builtin_nanf("");
   }
 }
 
@@ -206,25 +207,84 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
 }
 
 // ------------------------------------------------------------------ dk, dv
-// Two waves to 32 keys: one computes the scores and dv, the other do . v and
-// dk.  Either holds one operand and one accumulator for its keys (96 registers
-// at D = 128, where one wave for both would need 192 before its first score),
-// both run the same code on Q and dO in turned roles, and all that passes
-// between them are the probabilities, through LDS, lane by lane, in float32.
-template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv_kernel(PromptBwdArgs a) {
-  constexpr int BN = 32 * NP, NW = 2 * NP, NT = 64 * NW, KS = D / 16;
+// A workgroup's part: a tile of keys of one key head, and of the query heads
+// that share it all (shares = 1) or an equal share.  Shares write float32 sums
+// to the workspace, [share][dk, dv][T][Hkv][D], which a last launch adds.
+struct Share {
+  int tile, kvh, h0, heads, at;
+};
+__device__ __forceinline__ Share share_of(const PromptBwdArgs& a) {
+  // the first tiles of a long sequence meet the most rows
+  const int per = a.Hkv * a.shares, tile = blockIdx.x / per, x = blockIdx.x - tile * per;
+  const int heads = a.Hq / per;
+  return {tile, x / a.shares, x * heads, heads, x % a.shares};
+}
+__host__ __device__ inline size_t sums_at(int T, int Hq) { return ((size_t)2 * T * Hq + 3) / 4 * 4; }  // behind lse, delta
+__device__ __forceinline__ float* sums_row(const PromptBwdArgs& a, int D, int at, bool values, int row, int kvh) {
+  return a.ws + sums_at(a.T, a.Hq) + ((((size_t)at * 2 + values) * a.T + row) * a.Hkv + kvh) * D;
+}
+
+template <int D>
+__device__ __forceinline__ void write_grad(const PromptBwdArgs& a, const Share& sh, bool values, int key, int end,
+                                           const f32x16 (&acc)[D / 32], float f, int hl) {
+  if (a.shares > 1) {
+    if (end < 0) return;
+    float* dst = sums_row(a, D, sh.at, values, key, sh.kvh);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<f32x4*>(dst + 32 * i + 8 * e + 4 * hl) =
+            f32x4{acc[i][4 * e] * f, acc[i][4 * e + 1] * f, acc[i][4 * e + 2] * f, acc[i][4 * e + 3] * f};
+    return;
+  }
+  const bool rest = end < 0 && key < a.T && a.zero_rest;
+  if (end >= 0 || rest)
+    store_rows<D>(static_cast<__bf16*>(values ? a.grad_v : a.grad_k) + (long long)key * (values ? a.gvs : a.gks) + (long long)sh.kvh * D,
+                  acc, rest ? 0.f : f, hl);
+}
+
+template <int D>
+__device__ __forceinline__ void spoil_grad(const PromptBwdArgs& a, const Share& sh, bool values, int key, int end, int hl) {
+  for (int h = sh.h0; h < sh.h0 + sh.heads; ++h) {
+    const __bf16* src = static_cast<const __bf16*>(values ? a.grad_out : a.q) + (long long)h * D;
+    const long long stride = values ? a.gos : a.qs;
+    if (a.shares > 1)
+      spoil<D>(sums_row(a, D, sh.at, values, key, sh.kvh), src, stride, key, end, hl);
+    else
+      spoil<D>(static_cast<__bf16*>(values ? a.grad_v : a.grad_k) + (long long)key * (values ? a.gvs : a.gks) + (long long)sh.kvh * D,
+               src, stride, key, end, hl);
+  }
+}
+
+// Adds the shares of 32 keys of one key head, in their order.
+template <int D> __global__ __launch_bounds__(256) void attn_dkv_sum_kernel(PromptBwdArgs a) {
+  __shared__ int begs[32], window[33];
+  const int tile = blockIdx.x / a.Hkv, kvh = blockIdx.x - tile * a.Hkv;
+  find_rows<32, 256>(a.cu, a.R, a.T, tile * 32, window, begs, nullptr);
+  for (int x = threadIdx.x; x < 2 * 32 * (D / 4); x += 256) {
+    const bool values = x >= 32 * (D / 4);
+    const int i = x % (32 * (D / 4)) / (D / 4), d = x % (D / 4) * 4, row = tile * 32 + i;
+    const bool in = begs[i] >= 0;
+    if (row >= a.T || (!in && !a.zero_rest)) continue;
+    f32x4 sum = pipe::zero4();
+    if (in)
+      for (int s = 0; s < a.shares; ++s) sum += *reinterpret_cast<const f32x4*>(sums_row(a, D, s, values, row, kvh) + d);
+    *reinterpret_cast<u32x2*>(static_cast<__bf16*>(values ? a.grad_v : a.grad_k) + (long long)row * (values ? a.gvs : a.gks) +
+                              (long long)kvh * D + d) = pipe::cvt4(sum);
+  }
+}
+
+// One wave to 32 keys, D = 64.
+template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(PromptBwdArgs a) {
+  constexpr int BN = 32 * NW, NT = 64 * NW, KS = D / 16;
   __shared__ __bf16 qt[2][kN * D], gt[2][kN * D];
   __shared__ float lt[2][kN], dt[2][kN];
-  __shared__ f32x4 hand[NP][8][64];
   __shared__ int begs[BN], ends[BN], window[BN + 1], most[NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
-  const int pair = wave % NP;
-  const bool second = wave >= NP;  // do . v and dk
   // the first tiles of a long sequence meet the most rows
-  const int rank = blockIdx.x / a.Hkv, kvh = blockIdx.x - rank * a.Hkv;
-  const int r0 = rank * BN, G = a.Hq / a.Hkv;
-  __bf16* grad = static_cast<__bf16*>(second ? a.grad_k : a.grad_v) + (long long)kvh * D;
-  const long long gs = second ? a.gks : a.gvs;
+  const Share sh = share_of(a);
+  const int r0 = sh.tile * BN, kvh = sh.kvh, h0 = sh.h0, heads = sh.heads;
 
   find_rows<BN, NT>(a.cu, a.R, a.T, r0, window, begs, ends);
   int last = -1;  // the row behind the last that attends to a key of the tile
@@ -237,10 +297,160 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
   for (int w = 0; w < NW; ++w) last = max(last, most[w]);
   last = __builtin_amdgcn_readfirstlane(last);
   if (last < 0) {
-    if (a.zero_rest && pair == 0)
-      for (int i = lane; i < BN * (D / 8); i += 64)
-        if (r0 + i / (D / 8) < a.T)
-          *reinterpret_cast<u32x4*>(grad + (long long)(r0 + i / (D / 8)) * gs + i % (D / 8) * 8) = u32x4{0u, 0u, 0u, 0u};
+    if (a.zero_rest && a.shares == 1) {
+      zero_rows<D>(static_cast<__bf16*>(a.grad_k) + (long long)kvh * D, a.gks, r0, min(BN, a.T - r0), NT);
+      zero_rows<D>(static_cast<__bf16*>(a.grad_v) + (long long)kvh * D, a.gvs, r0, min(BN, a.T - r0), NT);
+    }
+    return;
+  }
+
+  const int w0 = r0 + wave * 32, key = w0 + (lane & 31), end = ends[key - r0];
+  const int at = min(key, a.T - 1);
+  const float c = a.scale * kLog2e;
+  u32x4 k[KS], v[KS];
+  {
+    const __bf16* kp = static_cast<const __bf16*>(a.k) + (long long)at * a.ks + (long long)kvh * D + 8 * hl;
+    const __bf16* vp = static_cast<const __bf16*>(a.v) + (long long)at * a.vs + (long long)kvh * D + 8 * hl;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      k[ks] = *reinterpret_cast<const u32x4*>(kp + 16 * ks);
+      v[ks] = *reinterpret_cast<const u32x4*>(vp + 16 * ks);
+    }
+  }
+  int lowest = end, highest = end;  // the range of end over the wave's keys
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    lowest = min(lowest, __shfl_xor(lowest, d));
+    highest = max(highest, __shfl_xor(highest, d));
+  }
+  lowest = __builtin_amdgcn_readfirstlane(lowest);
+  highest = __builtin_amdgcn_readfirstlane(highest);
+
+  f32x16 dk[D / 32], dv[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) dk[i] = dv[i] = zero16();
+  const int rb = row_base<D>(lane), cb = col_base<D>(lane);
+  Stage<D, kN, NW> sq, sg;
+  sq.init(a.qs, wave);
+  sg.init(a.gos, wave);
+  const __bf16* qp = static_cast<const __bf16*>(a.q);
+  const __bf16* gp = static_cast<const __bf16*>(a.grad_out);
+  auto stage = [&](int buf, int hq, int i0) {
+    const int n = min(kN, last - i0);
+    sq.load(qt[buf], rows_rsrc(qp + (long long)hq * D, a.qs, i0, n, D), wave);
+    sg.load(gt[buf], rows_rsrc(gp + (long long)hq * D, a.gos, i0, n, D), wave);
+    if (wave == 0) stage_words(lt[buf], pipe::make_rsrc(a.ws + (size_t)hq * a.T + i0, n * 4));
+    if (wave == 1) stage_words(dt[buf], pipe::make_rsrc(a.ws + (size_t)(a.Hq + hq) * a.T + i0, n * 4));
+  };
+  bool dirty = false;  // values were left out
+  // a tile of rows that the wave's keys may be seen by
+  auto step = [&](auto masked_, auto dirty_, int buf, int i1) {
+    constexpr bool MASKED = decltype(masked_)::value, DIRTY = decltype(dirty_)::value;
+    const __bf16 *Q = qt[buf], *O = gt[buf];
+    const int from = key - i1 - 4 * hl, upto = end - 1 - i1 - 4 * hl;  // the rows that see the lane's key
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        s = mma(row_frag<D>(Q, rb, 32 * n, ks), k[ks], s);
+        dp = mma(row_frag<D>(O, rb, 32 * n, ks), v[ks], dp);
+      }
+#pragma unroll
+      for (int e4 = 0; e4 < 4; ++e4) {
+        const f32x4 l = *reinterpret_cast<const f32x4*>(&lt[buf][32 * n + 8 * e4 + 4 * hl]);
+        const f32x4 d = *reinterpret_cast<const f32x4*>(&dt[buf][32 * n + 8 * e4 + 4 * hl]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int e = 4 * e4 + j;
+          s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -l[j]));
+          dp[e] = s[e] * (dp[e] - d[j]);
+          const int i = 32 * n + 8 * e4 + j;  // from i1 + 4 hl on
+          if constexpr (MASKED) {
+            const bool seen = i >= from && i <= upto;
+            s[e] = seen ? s[e] : 0.f;
+            dp[e] = seen ? dp[e] : 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        add_columns<DIRTY, D>(dv, O, cb, 32 * n + 16 * b, operand(s, b));
+        add_columns<DIRTY, D>(dk, Q, cb, 32 * n + 16 * b, operand(dp, b));
+      }
+    }
+  };
+  stage(0, h0, r0);
+  int buf = 0;
+  for (int head = 0; head < heads; ++head) {
+    int i1 = r0;
+    auto next = [&] {
+      staged_barrier();
+      if (i1 + kN < last) stage(buf ^ 1, h0 + head, i1 + kN);
+      else if (head + 1 < heads) stage(buf ^ 1, h0 + head + 1, r0);
+    };
+    // tiles of which some row misses some key, at both ends, and those between
+    auto edge = [&](int stop) {
+      for (; i1 < stop; i1 += kN, buf ^= 1) {
+        next();
+        if (i1 + kN - 1 < w0 || i1 >= highest) continue;
+        if (clean_tile<D, kN>(qt[buf]) && clean_tile<D, kN>(gt[buf])) {
+          step(std::true_type{}, std::false_type{}, buf, i1);
+        } else {
+          step(std::true_type{}, std::true_type{}, buf, i1);
+          dirty = true;
+        }
+      }
+    };
+    edge(min(w0 + 31, last));
+    for (; i1 + kN <= lowest; i1 += kN, buf ^= 1) {
+      next();
+      step(std::false_type{}, std::false_type{}, buf, i1);
+    }
+    edge(last);
+  }
+  write_grad<D>(a, sh, false, key, end, dk, a.scale, hl);
+  write_grad<D>(a, sh, true, key, end, dv, 1.f, hl);
+  if (dirty && end >= 0) {
+    spoil_grad<D>(a, sh, false, key, end, hl);
+    spoil_grad<D>(a, sh, true, key, end, hl);
+  }
+}
+
+// Two waves to 32 keys, D = 128: one computes the scores and dv, the other
+// do . v and dk.  Either holds one operand and one accumulator for its keys (96
+// registers, where one wave for both would need 192 before its first score and
+// spills), both run the same code on Q and dO in turned roles, and all that
+// passes between them are the probabilities, through LDS, lane by lane, in
+// float32.
+template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv_pair_kernel(PromptBwdArgs a) {
+  constexpr int BN = 32 * NP, NW = 2 * NP, NT = 64 * NW, KS = D / 16;
+  __shared__ __bf16 qt[2][kN * D], gt[2][kN * D];
+  __shared__ float lt[2][kN], dt[2][kN];
+  __shared__ f32x4 hand[NP][8][64];
+  __shared__ int begs[BN], ends[BN], window[BN + 1], most[NW];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
+  const int pair = wave % NP;
+  const bool second = wave >= NP;  // do . v and dk
+  // the first tiles of a long sequence meet the most rows
+  const Share sh = share_of(a);
+  const int r0 = sh.tile * BN, kvh = sh.kvh, h0 = sh.h0, heads = sh.heads;
+
+  find_rows<BN, NT>(a.cu, a.R, a.T, r0, window, begs, ends);
+  int last = -1;  // the row behind the last that attends to a key of the tile
+  for (int i = tid; i < BN; i += NT) last = max(last, ends[i]);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) last = max(last, __shfl_xor(last, d));
+  if (lane == 0) most[wave] = last;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < NW; ++w) last = max(last, most[w]);
+  last = __builtin_amdgcn_readfirstlane(last);
+  if (last < 0) {
+    if (a.zero_rest && a.shares == 1) {
+      zero_rows<D>(static_cast<__bf16*>(a.grad_k) + (long long)kvh * D, a.gks, r0, min(BN, a.T - r0), NT);
+      zero_rows<D>(static_cast<__bf16*>(a.grad_v) + (long long)kvh * D, a.gvs, r0, min(BN, a.T - r0), NT);
+    }
     return;
   }
 
@@ -333,14 +543,14 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
       for (int b = 0; b < 2; ++b) add_columns<DIRTY, D>(acc, Y, cb, 32 * n + 16 * b, operand(s[n], b));
   };
   bool dirty = false;  // values were left out
-  stage(0, kvh * G, r0);
+  stage(0, h0, r0);
   int buf = 0;
-  for (int head = 0; head < G; ++head) {
+  for (int head = 0; head < heads; ++head) {
     int i1 = r0;
     auto next = [&] {
       staged_barrier();
-      if (i1 + kN < last) stage(buf ^ 1, kvh * G + head, i1 + kN);
-      else if (head + 1 < G) stage(buf ^ 1, kvh * G + head + 1, r0);
+      if (i1 + kN < last) stage(buf ^ 1, h0 + head, i1 + kN);
+      else if (head + 1 < heads) stage(buf ^ 1, h0 + head + 1, r0);
     };
     // tiles of which some row misses some key, at both ends, and those between
     auto edge = [&](int stop) {
@@ -367,26 +577,47 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
     }
     edge(last);
   }
-  const bool rest = end < 0 && key < a.T && a.zero_rest;
-  if (end >= 0 || rest) store_rows<D>(grad + (long long)key * gs, acc, rest ? 0.f : (second ? a.scale : 1.f), hl);
-  if (dirty && end >= 0)
-    for (int h = kvh * G; h < (kvh + 1) * G; ++h)
-      spoil<D>(grad + (long long)key * gs, (second ? qp : gp) + (long long)h * D, second ? a.qs : a.gos, key, end, hl);
+  write_grad<D>(a, sh, !second, key, end, acc, second ? a.scale : 1.f, hl);
+  if (dirty && end >= 0) spoil_grad<D>(a, sh, !second, key, end, hl);
+}
+
+// Shares of the query heads that read one key head: as few as give the CUs
+// kEnough tiles of keys to choose from (the first tiles of a sequence meet many
+// more rows than its last, so few tiles leave most CUs waiting for the longest),
+// at most one head each.
+constexpr int kEnough = 1024;
+int shares_of(int T, int Hq, int Hkv) {
+  const int G = Hq / Hkv;
+  const long long tiles = ((long long)T + 127) / 128 * Hkv;
+  for (int s = 1; s < G; ++s)
+    if (G % s == 0 && tiles * s >= kEnough) return s;
+  return G;
 }
 
 template <int D> hipError_t launch(const PromptBwdArgs& a) {
-  constexpr int NW = 4;
-  const unsigned tiles = (unsigned)((a.T + 32 * NW - 1) / (32 * NW));
+  const unsigned tiles = (unsigned)((a.T + 127) / 128);
   hipStream_t st = static_cast<hipStream_t>(a.stream);
-  const hipError_t e = launch_kernel(attn_dq_kernel<D, NW>, dim3(tiles * a.Hq), dim3(64 * NW), st, a);
+  hipError_t e = launch_kernel(attn_dq_kernel<D, 4>, dim3(tiles * a.Hq), dim3(256), st, a);
   if (e != hipSuccess) return e;
-  return launch_kernel(attn_dkv_kernel<D, 4>, dim3(tiles * a.Hkv), dim3(512), st, a);
+  const dim3 grid(tiles * a.Hkv * a.shares);
+  if constexpr (D == 64) e = launch_kernel(attn_dkv_kernel<D, 4>, grid, dim3(256), st, a);
+  else e = launch_kernel(attn_dkv_pair_kernel<D, 4>, grid, dim3(512), st, a);
+  if (e != hipSuccess || a.shares == 1) return e;
+  return launch_kernel(attn_dkv_sum_kernel<D>, dim3((unsigned)((a.T + 31) / 32) * a.Hkv), dim3(256), st, a);
 }
 
 }  // namespace
 
-size_t attn_prompt_bwd_workspace_bytes(int T, int Hq) { return ((size_t)2 * T * Hq * sizeof(float) + 15) / 16 * 16; }
+size_t attn_prompt_bwd_workspace_bytes(int T, int Hq, int Hkv, int D) {
+  const int shares = shares_of(T, Hq, Hkv);
+  const size_t sums = shares > 1 ? (size_t)shares * 2 * T * Hkv * D : 0;
+  return (sums_at(T, Hq) + sums) * sizeof(float);
+}
 
-hipError_t launch_attn_prompt_bwd(const PromptBwdArgs& a) { return a.D == 64 ? launch<64>(a) : launch<128>(a); }
+hipError_t launch_attn_prompt_bwd(const PromptBwdArgs& args) {
+  PromptBwdArgs a = args;
+  a.shares = shares_of(a.T, a.Hq, a.Hkv);
+  return a.D == 64 ? launch<64>(a) : launch<128>(a);
+}
 
 }  // namespace gdn

@@ -86,8 +86,9 @@ struct PromptBwdArgs {
   long long qs, ks, vs, gos, gqs, gks, gvs;
   int T, R, Hq, Hkv, D, zero_rest;
   void* stream;
+  int shares = 1;  // set by the launch: shares of the query heads of a key head
 };
-size_t attn_prompt_bwd_workspace_bytes(int T, int Hq);
+size_t attn_prompt_bwd_workspace_bytes(int T, int Hq, int Hkv, int D);
 hipError_t launch_attn_prompt_bwd(const PromptBwdArgs& a);
 
 }  // namespace gdn

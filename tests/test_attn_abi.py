@@ -124,6 +124,10 @@ def test_prompt_of_nothing_is_noop():
     assert prompt(T=0, **none) == raw.GDN_OK
 
 
+# lse and delta [8, 100], and the sums of two shares of the query heads of a key head [2, 2, 100, 4, 64]
+BWD_NEED = 2 * 100 * 8 * 4 + 2 * 2 * 100 * 4 * 64 * 4
+
+
 def prompt_bwd(**kw):
     args = dict(q=A, k=A, v=A, out=A, lse=A, grad_out=A, cu_seqlens=A, grad_q=A, grad_k=A, grad_v=A, scale=0.125,
                 q_stride=512, k_stride=256, v_stride=256, grad_out_stride=512, grad_q_stride=512, grad_k_stride=256,
@@ -140,14 +144,17 @@ def prompt_bwd(**kw):
                                                       "grad_k", "grad_v")),
     *((dict([(n, A + 8)]), raw.GDN_ERR_ALIGN) for n in ("q", "k", "v", "out", "lse", "grad_out", "cu_seqlens", "grad_q",
                                                         "grad_k", "grad_v", "workspace")),
-    (dict(workspace=None), raw.GDN_ERR_WORKSPACE), (dict(workspace_bytes=2 * 100 * 8 * 4 - 1), raw.GDN_ERR_WORKSPACE),
+    (dict(workspace=None), raw.GDN_ERR_WORKSPACE), (dict(workspace_bytes=BWD_NEED - 1), raw.GDN_ERR_WORKSPACE),
 ])
 def test_prompt_bwd_argument_errors(kw, status):
     assert prompt_bwd(**kw) == status
 
 
 def test_prompt_bwd_workspace():
-    assert gdn.gdn_attn_prompt_bwd_workspace_bytes(100, 8, 4, 64) == 2 * 100 * 8 * 4  # lse and delta
+    assert gdn.gdn_attn_prompt_bwd_workspace_bytes(100, 8, 4, 64) == BWD_NEED
+    # a key head per query head, or tiles enough for one workgroup each: no shares
+    assert gdn.gdn_attn_prompt_bwd_workspace_bytes(100, 8, 8, 64) == 2 * 100 * 8 * 4
+    assert gdn.gdn_attn_prompt_bwd_workspace_bytes(1 << 20, 8, 4, 64) == 2 * (1 << 20) * 8 * 4
     assert gdn.gdn_attn_prompt_bwd_workspace_bytes(100, 8, 3, 64) == 0
     none = {n: None for n in ("q", "k", "v", "out", "lse", "grad_out", "cu_seqlens", "grad_q", "grad_k", "grad_v", "workspace")}
     assert prompt_bwd(T=0, **none) == raw.GDN_OK
