@@ -20,7 +20,7 @@ template <int D, int QT, int NW> struct Fwd {
     __bf16 k[2][kN * D];
     __bf16 v[2][kN * D];
     int beg[BM];
-    int window[BM + 1];
+    int window[kWindow];
     int lo[NW], hi[NW];
   };
 };
@@ -36,6 +36,18 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
   const int rank = blockIdx.x / a.Hq, hq = blockIdx.x - rank * a.Hq;
   const int r0 = (tiles - 1 - rank) * BM, kvh = hq / (a.Hq / a.Hkv);
 
+  // queries: operands for the wave's rows, on their way while the sequences are found
+  const int w0 = r0 + wave * 32 * QT;
+  u32x4 q[QT][KS];
+  int row[QT], beg[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    row[t] = w0 + 32 * t + (lane & 31);
+    const __hip_bfloat16* src =
+        static_cast<const __hip_bfloat16*>(a.q) + (long long)min(row[t], a.T - 1) * a.qs + (long long)hq * D + 8 * hl;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) q[t][ks] = *reinterpret_cast<const u32x4*>(src + 16 * ks);
+  }
   find_rows<BM, NT>(a.cu, a.R, a.T, r0, lds.window, lds.beg, nullptr);
   int first = a.T, last = -1;  // the keys that the tile's rows see
   for (int i = tid; i < BM; i += NT)
@@ -67,25 +79,16 @@ __global__ __launch_bounds__(64 * NW, QT == 2 && D == 128 ? 1 : 2) void attn_pro
     return;
   }
 
-  // queries: operands for the wave's rows, their sign turned for a negative scale
-  const int w0 = r0 + wave * 32 * QT;
-  u32x4 q[QT][KS];
-  int row[QT], beg[QT];
   int lowest = a.T, highest = -1;  // the range of beg over the wave's rows
-  // a scale of zero stays just above it, so that masked scores, -infinity, keep a weight of zero
+  // a scale of zero stays just above it, so that masked scores, -infinity, keep
+  // a weight of zero; for a negative one the queries' signs are turned
   const float c = fmaxf(__builtin_fabsf(a.scale) * kLog2e, 1e-37f);
   const unsigned flip = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    row[t] = w0 + 32 * t + (lane & 31);
     beg[t] = lds.beg[row[t] - r0];
-    const __hip_bfloat16* src =
-        static_cast<const __hip_bfloat16*>(a.q) + (long long)min(row[t], a.T - 1) * a.qs + (long long)hq * D + 8 * hl;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      q[t][ks] = *reinterpret_cast<const u32x4*>(src + 16 * ks);
-      q[t][ks] ^= flip;
-    }
+    for (int ks = 0; ks < KS; ++ks) q[t][ks] ^= flip;
     lowest = min(lowest, beg[t] < 0 ? a.T : beg[t]);
     highest = max(highest, beg[t] < 0 ? a.T : beg[t]);
   }

@@ -63,7 +63,7 @@ __device__ __forceinline__ void spoil(T* dst, const void* src, long long stride,
 template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(PromptBwdArgs a) {
   constexpr int BM = 32 * NW, NT = 64 * NW, KS = D / 16;
   __shared__ __bf16 kt[2][kN * D], vt[2][kN * D];
-  __shared__ int begs[BM], window[BM + 1], lows[NW], tops[NW];
+  __shared__ int begs[BM], window[kWindow], lows[NW], tops[NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const int tiles = (a.T + BM - 1) / BM;
   const int rank = blockIdx.x / a.Hq, hq = blockIdx.x - rank * a.Hq;
@@ -259,7 +259,7 @@ __device__ __forceinline__ void spoil_grad(const PromptBwdArgs& a, const Share& 
 
 // Adds the shares of 32 keys of one key head, in their order.
 template <int D> __global__ __launch_bounds__(256) void attn_dkv_sum_kernel(PromptBwdArgs a) {
-  __shared__ int begs[32], window[33];
+  __shared__ int begs[32], window[kWindow];
   const int tile = blockIdx.x / a.Hkv, kvh = blockIdx.x - tile * a.Hkv;
   find_rows<32, 256>(a.cu, a.R, a.T, tile * 32, window, begs, nullptr);
   for (int x = threadIdx.x; x < 2 * 32 * (D / 4); x += 256) {
@@ -280,7 +280,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
   constexpr int BN = 32 * NW, NT = 64 * NW, KS = D / 16;
   __shared__ __bf16 qt[2][kN * D], gt[2][kN * D];
   __shared__ float lt[2][kN], dt[2][kN];
-  __shared__ int begs[BN], ends[BN], window[BN + 1], most[NW];
+  __shared__ int begs[BN], ends[BN], window[kWindow], most[NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   // the first tiles of a long sequence meet the most rows
   const Share sh = share_of(a);
@@ -428,7 +428,7 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
   __shared__ __bf16 qt[2][kN * D], gt[2][kN * D];
   __shared__ float lt[2][kN], dt[2][kN];
   __shared__ f32x4 hand[NP][8][64];
-  __shared__ int begs[BN], ends[BN], window[BN + 1], most[NW];
+  __shared__ int begs[BN], ends[BN], window[kWindow], most[NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const int pair = wave % NP;
   const bool second = wave >= NP;  // do . v and dk

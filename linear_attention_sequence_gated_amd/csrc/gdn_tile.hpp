@@ -187,31 +187,35 @@ template <class At> __device__ __forceinline__ int last_at_most(At at, int lo, i
 // Of rows [r0, r0 + N), by NT threads: their sequence's first row in beg[] and
 // the row behind its last in end[] (which may be NULL); rows of no sequence get
 // beg = end = -1.  0 <= beg <= row < end <= T whatever cu holds.  Ends with a
-// barrier.  The sequence of r0 is found NT probes at a time; the offsets behind
-// it are staged in `window` (N + 1 entries), where the other rows look theirs up.
+// barrier.  Offsets are looked up in LDS, in `window` (kWindow entries): all of
+// them where they fit, which costs one round trip to memory; otherwise those
+// from r0's sequence on, which is found NT probes at a time first.
+constexpr int kWindow = 512;
 template <int N, int NT>
 __device__ __forceinline__ void find_rows(const int* cu, int R, int T, int r0, int* window, int* beg, int* end) {
   const int t = threadIdx.x;
   int lo = 0;
-  for (int n = R + 1;;) {
-    const int step = (n + NT - 1) / NT, i = t * step;
-    const int cnt = __syncthreads_count(i < n && cu[lo + i] <= r0);
-    if (cnt > 1) lo += (cnt - 1) * step;
-    if (cnt == 0 || step == 1) break;
-    n = min(step, R + 1 - lo);
+  if (R >= kWindow) {
+    for (int n = R + 1;;) {
+      const int step = (n + NT - 1) / NT, i = t * step;
+      const int cnt = __syncthreads_count(i < n && cu[lo + i] <= r0);
+      if (cnt > 1) lo += (cnt - 1) * step;
+      if (cnt == 0 || step == 1) break;
+      n = min(step, R + 1 - lo);
+    }
   }
-  // cu[lo] is the last offset at or before r0 (or lo = 0 and there is none)
-  const int last = min(R - lo, N);
+  // cu[lo] is the last offset at or before r0, or lo = 0
+  const int last = min(R - lo, kWindow - 1);
   for (int i = t; i <= last; i += NT) window[i] = cu[lo + i];
   __syncthreads();
   for (int i = t; i < N; i += NT) {
     const int row = r0 + i;
     int s = last_at_most([&](int x) { return window[x]; }, 0, last, row) + lo;
-    if (s == lo + last) s = last_at_most([&](int x) { return cu[x]; }, s, R, row);
+    if (s == lo + last && s < R) s = last_at_most([&](int x) { return cu[x]; }, s, R, row);
     int b = -1, e = -1;
     if (s < R && row < T) {
-      b = cu[s];
-      e = min(cu[s + 1], T);
+      b = s - lo <= last ? window[s - lo] : cu[s];
+      e = min(s + 1 - lo <= last ? window[s + 1 - lo] : cu[s + 1], T);
       if (b > row || e <= row) b = e = -1;
       else b = max(b, 0);
     }
