@@ -37,6 +37,14 @@ __device__ __forceinline__ void add_columns(f32x16 (&acc)[D / 32], const __bf16*
   }
 }
 
+// Whether all waves found their part of a tile finite.
+template <int NW> __device__ __forceinline__ bool all_clean(const int (&bad)[NW]) {
+  int x = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) x |= bad[w];
+  return __builtin_amdgcn_readfirstlane(x) == 0;
+}
+
 template <int D> __device__ __forceinline__ void store_rows(__bf16* dst, const f32x16 (&acc)[D / 32], float f, int hl) {
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
@@ -63,54 +71,61 @@ __device__ __forceinline__ void spoil(T* dst, const void* src, long long stride,
 template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(PromptBwdArgs a) {
   constexpr int BM = 32 * NW, NT = 64 * NW, KS = D / 16;
   __shared__ __bf16 kt[2][kN * D], vt[2][kN * D];
-  __shared__ int begs[BM], window[kWindow], lows[NW], tops[NW];
+  __shared__ int begs[BM], window[kWindow], ranges[3][NW], bad[2][NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const int tiles = (a.T + BM - 1) / BM;
   const int rank = blockIdx.x / a.Hq, hq = blockIdx.x - rank * a.Hq;
   const int r0 = (tiles - 1 - rank) * BM, kvh = hq / (a.Hq / a.Hkv);
 
-  find_rows<BM, NT>(a.cu, a.R, a.T, r0, window, begs, nullptr);
-  int first = a.T, last = -1;  // the keys that the tile's rows see
-  for (int i = tid; i < BM; i += NT)
-    if (begs[i] >= 0) {
-      first = min(first, begs[i]);
-      last = max(last, r0 + i + 1);
+  const int w0 = r0 + wave * 32, row = w0 + (lane & 31), at = min(row, a.T - 1);
+  const float c = a.scale * kLog2e;
+  u32x4 q[KS], g[KS];
+  find_rows<BM, NT>(a.cu, a.R, a.T, r0, window, begs, nullptr, [&] {
+    const __bf16* qp = static_cast<const __bf16*>(a.q) + (long long)at * a.qs + (long long)hq * D + 8 * hl;
+    const __bf16* gp = static_cast<const __bf16*>(a.grad_out) + (long long)at * a.gos + (long long)hq * D + 8 * hl;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      q[ks] = *reinterpret_cast<const u32x4*>(qp + 16 * ks);
+      g[ks] = *reinterpret_cast<const u32x4*>(gp + 16 * ks);
     }
+  });
+  // the keys that the tile's rows see, and the last beginning of a sequence among them
+  const int beg = begs[row - r0];
+  int lowest = beg < 0 ? a.T : beg, highest = lowest, last = beg < 0 ? -1 : row + 1;
 #pragma unroll
   for (int d = 32; d; d >>= 1) {
-    first = min(first, __shfl_xor(first, d));
+    lowest = min(lowest, __shfl_xor(lowest, d));
+    highest = max(highest, __shfl_xor(highest, d));
     last = max(last, __shfl_xor(last, d));
   }
   if (lane == 0) {
-    lows[wave] = first;
-    tops[wave] = last;
+    ranges[0][wave] = lowest;
+    ranges[1][wave] = highest;
+    ranges[2][wave] = last;
   }
   __syncthreads();
+  int first = a.T, latest = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    first = min(first, lows[w]);
-    last = max(last, tops[w]);
+    first = min(first, ranges[0][w]);
+    latest = max(latest, ranges[1][w]);
+    last = max(last, ranges[2][w]);
   }
+  lowest = __builtin_amdgcn_readfirstlane(lowest);  // of the wave's rows
+  highest = __builtin_amdgcn_readfirstlane(highest);
   first = __builtin_amdgcn_readfirstlane(first);
+  latest = __builtin_amdgcn_readfirstlane(latest);
   last = __builtin_amdgcn_readfirstlane(last);
   if (last < 0) {  // no row of the tile is in a sequence
     if (a.zero_rest) zero_rows<D>(static_cast<__bf16*>(a.grad_q) + (long long)hq * D, a.gqs, r0, min(BM, a.T - r0), NT);
     return;
   }
 
-  const int w0 = r0 + wave * 32, row = w0 + (lane & 31), beg = begs[row - r0];
-  const int at = min(row, a.T - 1);
-  const float c = a.scale * kLog2e;
-  u32x4 q[KS], g[KS];
   float delta = 0.f;
   {
-    const __bf16* qp = static_cast<const __bf16*>(a.q) + (long long)at * a.qs + (long long)hq * D + 8 * hl;
-    const __bf16* gp = static_cast<const __bf16*>(a.grad_out) + (long long)at * a.gos + (long long)hq * D + 8 * hl;
     const __bf16* op = static_cast<const __bf16*>(a.out) + ((long long)at * a.Hq + hq) * D + 8 * hl;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      q[ks] = *reinterpret_cast<const u32x4*>(qp + 16 * ks);
-      g[ks] = *reinterpret_cast<const u32x4*>(gp + 16 * ks);
       const u32x4 o = *reinterpret_cast<const u32x4*>(op + 16 * ks);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -125,14 +140,6 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
     a.ws[(size_t)hq * a.T + row] = lse2;
     a.ws[(size_t)(a.Hq + hq) * a.T + row] = delta;
   }
-  int lowest = beg < 0 ? a.T : beg, highest = lowest;
-#pragma unroll
-  for (int d = 32; d; d >>= 1) {
-    lowest = min(lowest, __shfl_xor(lowest, d));
-    highest = max(highest, __shfl_xor(highest, d));
-  }
-  lowest = __builtin_amdgcn_readfirstlane(lowest);
-  highest = __builtin_amdgcn_readfirstlane(highest);
 
   f32x16 dq[D / 32];
 #pragma unroll
@@ -155,6 +162,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
     constexpr bool MASKED = decltype(masked_)::value, DIRTY = decltype(dirty_)::value;
 #pragma unroll 1
     for (int n = 0; n < 2; ++n) {
+      const unsigned seen = bits(from - kv - 32 * n, upto - kv - 32 * n);
       f32x16 s = zero16(), dp = zero16();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
@@ -165,8 +173,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
       for (int e = 0; e < 16; ++e) {
         const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -lse2));
         s[e] = p * (dp[e] - delta);
-        const int key = 32 * n + 8 * (e / 4) + e % 4;  // from kv + 4 hl on
-        if constexpr (MASKED) s[e] = key >= from - kv && key <= upto - kv ? s[e] : 0.f;
+        if constexpr (MASKED) s[e] = where_seen<true>(s[e], seen, e);
       }
 #pragma unroll
       for (int b = 0; b < 2; ++b) add_columns<DIRTY, D>(dq, K, cb, 32 * n + 16 * b, operand(s, b));
@@ -174,6 +181,12 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
   };
   stage(0, first);
   auto next = [&] {
+    // a tile that is masked for some wave: each looks at the keys it loaded
+    if (kv + kN - 1 > r0 || kv < latest || kv + kN > last) {
+      wait_staged();
+      const bool ok = Stage<D, kN, NW>::clean(kt[buf], wave);
+      if (lane == 0) bad[buf][wave] = !ok;
+    }
     staged_barrier();
     if (kv + kN < last) stage(buf ^ 1, kv + kN);
   };
@@ -182,7 +195,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
     for (; kv < end; kv += kN, buf ^= 1) {
       next();
       if (kv > w0 + 31 || kv + kN <= lowest) continue;
-      if (clean_tile<D, kN>(kt[buf])) {
+      if (all_clean(bad[buf])) {
         step(std::true_type{}, std::false_type{}, kt[buf], vt[buf]);
       } else {
         step(std::true_type{}, std::true_type{}, kt[buf], vt[buf]);
@@ -261,7 +274,7 @@ __device__ __forceinline__ void spoil_grad(const PromptBwdArgs& a, const Share& 
 template <int D> __global__ __launch_bounds__(256) void attn_dkv_sum_kernel(PromptBwdArgs a) {
   __shared__ int begs[32], window[kWindow];
   const int tile = blockIdx.x / a.Hkv, kvh = blockIdx.x - tile * a.Hkv;
-  find_rows<32, 256>(a.cu, a.R, a.T, tile * 32, window, begs, nullptr);
+  find_rows<32, 256>(a.cu, a.R, a.T, tile * 32, window, begs, nullptr, [] {});
   for (int x = threadIdx.x; x < 2 * 32 * (D / 4); x += 256) {
     const bool values = x >= 32 * (D / 4);
     const int i = x % (32 * (D / 4)) / (D / 4), d = x % (D / 4) * 4, row = tile * 32 + i;
@@ -280,22 +293,35 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
   constexpr int BN = 32 * NW, NT = 64 * NW, KS = D / 16;
   __shared__ __bf16 qt[2][kN * D], gt[2][kN * D];
   __shared__ float lt[2][kN], dt[2][kN];
-  __shared__ int begs[BN], ends[BN], window[kWindow], most[NW];
+  __shared__ int begs[BN], ends[BN], window[kWindow], most[2][NW], bad[2][NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   // the first tiles of a long sequence meet the most rows
   const Share sh = share_of(a);
   const int r0 = sh.tile * BN, kvh = sh.kvh, h0 = sh.h0, heads = sh.heads;
 
-  find_rows<BN, NT>(a.cu, a.R, a.T, r0, window, begs, ends);
-  int last = -1;  // the row behind the last that attends to a key of the tile
-  for (int i = tid; i < BN; i += NT) last = max(last, ends[i]);
+  find_rows<BN, NT>(a.cu, a.R, a.T, r0, window, begs, ends, [] {});
+  int last = -1, soonest = a.T;  // the rows behind the last that attend to the tile's keys: the most, the least
+  for (int i = tid; i < BN; i += NT) {
+    last = max(last, ends[i]);
+    soonest = min(soonest, ends[i]);
+  }
 #pragma unroll
-  for (int d = 32; d; d >>= 1) last = max(last, __shfl_xor(last, d));
-  if (lane == 0) most[wave] = last;
+  for (int d = 32; d; d >>= 1) {
+    last = max(last, __shfl_xor(last, d));
+    soonest = min(soonest, __shfl_xor(soonest, d));
+  }
+  if (lane == 0) {
+    most[0][wave] = last;
+    most[1][wave] = soonest;
+  }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < NW; ++w) last = max(last, most[w]);
+  for (int w = 0; w < NW; ++w) {
+    last = max(last, most[0][w]);
+    soonest = min(soonest, most[1][w]);
+  }
   last = __builtin_amdgcn_readfirstlane(last);
+  soonest = __builtin_amdgcn_readfirstlane(soonest);
   if (last < 0) {
     if (a.zero_rest && a.shares == 1) {
       zero_rows<D>(static_cast<__bf16*>(a.grad_k) + (long long)kvh * D, a.gks, r0, min(BN, a.T - r0), NT);
@@ -348,8 +374,9 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
     constexpr bool MASKED = decltype(masked_)::value, DIRTY = decltype(dirty_)::value;
     const __bf16 *Q = qt[buf], *O = gt[buf];
     const int from = key - i1 - 4 * hl, upto = end - 1 - i1 - 4 * hl;  // the rows that see the lane's key
-#pragma unroll
+#pragma unroll MASKED ? 1 : 2
     for (int n = 0; n < 2; ++n) {
+      const unsigned seen = bits(from - 32 * n, upto - 32 * n);
       f32x16 s = zero16(), dp = zero16();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
@@ -365,11 +392,9 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
           const int e = 4 * e4 + j;
           s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -l[j]));
           dp[e] = s[e] * (dp[e] - d[j]);
-          const int i = 32 * n + 8 * e4 + j;  // from i1 + 4 hl on
           if constexpr (MASKED) {
-            const bool seen = i >= from && i <= upto;
-            s[e] = seen ? s[e] : 0.f;
-            dp[e] = seen ? dp[e] : 0.f;
+            s[e] = where_seen<true>(s[e], seen, e);
+            dp[e] = where_seen<true>(dp[e], seen, e);
           }
         }
       }
@@ -385,6 +410,12 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
   for (int head = 0; head < heads; ++head) {
     int i1 = r0;
     auto next = [&] {
+      // a tile that is masked for some wave: each looks at what it loaded
+      if (i1 < r0 + BN - 1 || i1 + kN > soonest) {
+        wait_staged();
+        const bool ok = Stage<D, kN, NW>::clean(qt[buf], wave) && Stage<D, kN, NW>::clean(gt[buf], wave);
+        if (lane == 0) bad[buf][wave] = !ok;
+      }
       staged_barrier();
       if (i1 + kN < last) stage(buf ^ 1, h0 + head, i1 + kN);
       else if (head + 1 < heads) stage(buf ^ 1, h0 + head + 1, r0);
@@ -394,7 +425,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
       for (; i1 < stop; i1 += kN, buf ^= 1) {
         next();
         if (i1 + kN - 1 < w0 || i1 >= highest) continue;
-        if (clean_tile<D, kN>(qt[buf]) && clean_tile<D, kN>(gt[buf])) {
+        if (all_clean(bad[buf])) {
           step(std::true_type{}, std::false_type{}, buf, i1);
         } else {
           step(std::true_type{}, std::true_type{}, buf, i1);
@@ -428,7 +459,7 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
   __shared__ __bf16 qt[2][kN * D], gt[2][kN * D];
   __shared__ float lt[2][kN], dt[2][kN];
   __shared__ f32x4 hand[NP][8][64];
-  __shared__ int begs[BN], ends[BN], window[kWindow], most[NW];
+  __shared__ int begs[BN], ends[BN], window[kWindow], most[2][NW], bad[2][NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const int pair = wave % NP;
   const bool second = wave >= NP;  // do . v and dk
@@ -436,16 +467,29 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
   const Share sh = share_of(a);
   const int r0 = sh.tile * BN, kvh = sh.kvh, h0 = sh.h0, heads = sh.heads;
 
-  find_rows<BN, NT>(a.cu, a.R, a.T, r0, window, begs, ends);
-  int last = -1;  // the row behind the last that attends to a key of the tile
-  for (int i = tid; i < BN; i += NT) last = max(last, ends[i]);
+  find_rows<BN, NT>(a.cu, a.R, a.T, r0, window, begs, ends, [] {});
+  int last = -1, soonest = a.T;  // the rows behind the last that attend to the tile's keys: the most, the least
+  for (int i = tid; i < BN; i += NT) {
+    last = max(last, ends[i]);
+    soonest = min(soonest, ends[i]);
+  }
 #pragma unroll
-  for (int d = 32; d; d >>= 1) last = max(last, __shfl_xor(last, d));
-  if (lane == 0) most[wave] = last;
+  for (int d = 32; d; d >>= 1) {
+    last = max(last, __shfl_xor(last, d));
+    soonest = min(soonest, __shfl_xor(soonest, d));
+  }
+  if (lane == 0) {
+    most[0][wave] = last;
+    most[1][wave] = soonest;
+  }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < NW; ++w) last = max(last, most[w]);
+  for (int w = 0; w < NW; ++w) {
+    last = max(last, most[0][w]);
+    soonest = min(soonest, most[1][w]);
+  }
   last = __builtin_amdgcn_readfirstlane(last);
+  soonest = __builtin_amdgcn_readfirstlane(soonest);
   if (last < 0) {
     if (a.zero_rest && a.shares == 1) {
       zero_rows<D>(static_cast<__bf16*>(a.grad_k) + (long long)kvh * D, a.gks, r0, min(BN, a.T - r0), NT);
@@ -509,9 +553,8 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
         f32x4 p;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int i = 32 * n + 8 * e4 + j;  // from i1 + 4 hl on
           p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][4 * e4 + j], c, -l[j]));
-          if constexpr (MASKED) p[j] = i >= from && i <= upto ? p[j] : 0.f;
+          if constexpr (MASKED) p[j] = where_seen<true>(p[j], bits(from - 32 * n, upto - 32 * n), 4 * e4 + j);
           s[n][4 * e4 + j] = p[j];
         }
         hand[pair][4 * n + e4][lane] = p;
@@ -530,9 +573,8 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
           const f32x4 d = *reinterpret_cast<const f32x4*>(&dt[buf][32 * n + 8 * e4 + 4 * hl]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int i = 32 * n + 8 * e4 + j;
             float x = p[j] * (s[n][4 * e4 + j] - d[j]);
-            if constexpr (MASKED) x = i >= from && i <= upto ? x : 0.f;
+            if constexpr (MASKED) x = where_seen<true>(x, bits(from - 32 * n, upto - 32 * n), 4 * e4 + j);
             s[n][4 * e4 + j] = x;
           }
         }
@@ -548,6 +590,12 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
   for (int head = 0; head < heads; ++head) {
     int i1 = r0;
     auto next = [&] {
+      // a tile that is masked for some wave: each looks at what it loaded
+      if (i1 < r0 + BN - 1 || i1 + kN > soonest) {
+        wait_staged();
+        const bool ok = Stage<D, kN, NP>::clean(second ? gt[buf] : qt[buf], pair);
+        if (lane == 0) bad[buf][wave] = !ok;
+      }
       staged_barrier();
       if (i1 + kN < last) stage(buf ^ 1, h0 + head, i1 + kN);
       else if (head + 1 < heads) stage(buf ^ 1, h0 + head + 1, r0);
@@ -560,7 +608,7 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
         if (met) scores(std::true_type{}, buf, i1);
         pipe::stage_barrier();
         if (!met) continue;
-        if (clean_tile<D, kN>(second ? qt[buf] : gt[buf])) {
+        if (all_clean(bad[buf])) {
           products(std::true_type{}, std::false_type{}, buf, i1);
         } else {
           products(std::true_type{}, std::true_type{}, buf, i1);

@@ -60,6 +60,49 @@ __device__ __forceinline__ u32x4 operand(const f32x16& x, int b) {
                pipe::cvt2(x[8 * b + 4], x[8 * b + 5]), pipe::cvt2(x[8 * b + 6], x[8 * b + 7])};
 }
 
+// ----------------------------------------------------------- non-finite values
+// Non-finite bf16 values have all exponent bits set; the larger of a word's
+// halves without their signs, over words.
+__device__ __forceinline__ unsigned worst(unsigned m, unsigned w) {
+  typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
+  const u16x2 a = __builtin_bit_cast(u16x2, m), b = __builtin_bit_cast(u16x2, w & 0x7fff7fffu);
+  return __builtin_bit_cast(unsigned, __builtin_elementwise_max(a, b));
+}
+__device__ __forceinline__ bool finite(unsigned m) { return (m & 0xffffu) < 0x7f80u && (m >> 16) < 0x7f80u; }
+
+// A word with its non-finite halves replaced: by zero, or (kind 1, 2, 3) one
+// where the half is +infinity, -infinity, NaN and zero elsewhere.
+__device__ __forceinline__ unsigned pick(unsigned w, int kind) {
+  unsigned r = 0;
+#pragma unroll
+  for (int s = 0; s < 32; s += 16) {
+    const unsigned x = (w >> s) & 0xffffu, a = x & 0x7fffu;
+    const bool bad = a >= 0x7f80u;
+    const bool hit = kind == 1 ? x == 0x7f80u : kind == 2 ? x == 0xff80u : a > 0x7f80u;
+    r |= (kind == 0 ? (bad ? 0u : x) : (hit ? 0x3f80u : 0u)) << s;
+  }
+  return r;
+}
+__device__ __forceinline__ u32x4 pick(const u32x4& w, int kind) {
+  return u32x4{pick(w[0], kind), pick(w[1], kind), pick(w[2], kind), pick(w[3], kind)};
+}
+
+__device__ __forceinline__ u32x4 finite_only(const u32x4& w) { return pick(w, 0); }
+
+// The score e of a half-tile (of 32 keys, element e) where bit 8 (e / 4) + e % 4
+// of `seen` is set, otherwise -infinity (ZERO: zero).
+template <bool ZERO> __device__ __forceinline__ float where_seen(float x, unsigned seen, int e) {
+  const int bit = 8 * (e / 4) + e % 4, all = (int)(seen << (31 - bit)) >> 31;
+  const int other = ZERO ? 0 : (int)0xff800000u;
+  return __builtin_bit_cast(float, (all & __builtin_bit_cast(int, x)) | (~all & other));
+}
+// Bits lo .. hi of a word, those outside it left out.
+__device__ __forceinline__ unsigned bits(int lo, int hi) {
+  lo = lo < 0 ? 0 : lo;
+  hi = hi > 31 ? 31 : hi;
+  return lo > hi ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
+}
+
 // Rows [r0, r0 + n) of a [rows, heads, D] array whose rows are `stride`
 // elements apart, seen through a buffer resource that ends with them: what lies
 // behind reads as zero.
@@ -98,6 +141,16 @@ template <int D, int N, int NW> struct Stage {
     for (int i = 0; i < LOADS; ++i)
       stage_pieces(lds + (wave * LOADS + i) * 512, rsrc, off[i]);
   }
+  // Whether the part that this wave loaded is finite (its loads have arrived).
+  static __device__ __forceinline__ bool clean(const __bf16* lds, int wave) {
+    unsigned m = 0;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(lds + (wave * LOADS + i) * 512 + (threadIdx.x & 63) * 8);
+      m = worst(worst(worst(worst(m, x[0]), x[1]), x[2]), x[3]);
+    }
+    return __all(finite(m));
+  }
 };
 
 // Operand rows: row r0 + l % 32 of a staged tile, its values 16 ks + 8 h .. + 7.
@@ -119,7 +172,14 @@ template <int D> __device__ __forceinline__ u32x4 col_frag(const __bf16* lds, in
   return pipe::pair(a, b);
 }
 
-// Waits until this wave's loads into LDS have arrived, then for the others.
+// Until this wave's loads into LDS have arrived.
+__device__ __forceinline__ void wait_staged() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// The same, then for the others' too.
 __device__ __forceinline__ void staged_barrier() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -130,47 +190,6 @@ __device__ __forceinline__ void staged_barrier() {
 template <int D> __device__ __forceinline__ void zero_rows(__bf16* dst, long long stride, int r0, int n, int NT) {
   for (int i = threadIdx.x; i < n * (D / 8); i += NT)
     *reinterpret_cast<u32x4*>(dst + (long long)(r0 + i / (D / 8)) * stride + i % (D / 8) * 8) = u32x4{0u, 0u, 0u, 0u};
-}
-
-// ----------------------------------------------------------- non-finite values
-// Non-finite bf16 values have all exponent bits set; the larger of a word's
-// halves without their signs, over words.
-__device__ __forceinline__ unsigned worst(unsigned m, unsigned w) {
-  typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
-  const u16x2 a = __builtin_bit_cast(u16x2, m), b = __builtin_bit_cast(u16x2, w & 0x7fff7fffu);
-  return __builtin_bit_cast(unsigned, __builtin_elementwise_max(a, b));
-}
-__device__ __forceinline__ bool finite(unsigned m) { return (m & 0xffffu) < 0x7f80u && (m >> 16) < 0x7f80u; }
-
-// A word with its non-finite halves replaced: by zero, or (kind 1, 2, 3) one
-// where the half is +infinity, -infinity, NaN and zero elsewhere.
-__device__ __forceinline__ unsigned pick(unsigned w, int kind) {
-  unsigned r = 0;
-#pragma unroll
-  for (int s = 0; s < 32; s += 16) {
-    const unsigned x = (w >> s) & 0xffffu, a = x & 0x7fffu;
-    const bool bad = a >= 0x7f80u;
-    const bool hit = kind == 1 ? x == 0x7f80u : kind == 2 ? x == 0xff80u : a > 0x7f80u;
-    r |= (kind == 0 ? (bad ? 0u : x) : (hit ? 0x3f80u : 0u)) << s;
-  }
-  return r;
-}
-__device__ __forceinline__ u32x4 pick(const u32x4& w, int kind) {
-  return u32x4{pick(w[0], kind), pick(w[1], kind), pick(w[2], kind), pick(w[3], kind)};
-}
-
-__device__ __forceinline__ u32x4 finite_only(const u32x4& w) { return pick(w, 0); }
-
-// Whether all of a staged tile of N rows is finite.
-template <int D, int N> __device__ __forceinline__ bool clean_tile(const __bf16* tile) {
-  unsigned w = 0;
-  const u32x4* p = reinterpret_cast<const u32x4*>(tile);
-#pragma unroll 4
-  for (int i = 0; i < N * D / 512; ++i) {
-    const u32x4 x = p[i * 64 + (threadIdx.x & 63)];
-    w = worst(worst(worst(worst(w, x[0]), x[1]), x[2]), x[3]);
-  }
-  return __all(finite(w));
 }
 
 // ------------------------------------------------------------------ sequences
@@ -191,8 +210,11 @@ template <class At> __device__ __forceinline__ int last_at_most(At at, int lo, i
 // them where they fit, which costs one round trip to memory; otherwise those
 // from r0's sequence on, which is found NT probes at a time first.
 constexpr int kWindow = 512;
-template <int N, int NT>
-__device__ __forceinline__ void find_rows(const int* cu, int R, int T, int r0, int* window, int* beg, int* end) {
+// meanwhile() issues other loads, behind the first of these.
+template <int N, int NT, class F>
+__device__ __forceinline__ void find_rows(const int* cu, int R, int T, int r0, int* window, int* beg, int* end,
+                                          F meanwhile) {
+  static_assert(2 * NT >= kWindow, "two loads per thread");
   const int t = threadIdx.x;
   int lo = 0;
   if (R >= kWindow) {
@@ -206,7 +228,10 @@ __device__ __forceinline__ void find_rows(const int* cu, int R, int T, int r0, i
   }
   // cu[lo] is the last offset at or before r0, or lo = 0
   const int last = min(R - lo, kWindow - 1);
-  for (int i = t; i <= last; i += NT) window[i] = cu[lo + i];
+  const int one = t <= last ? cu[lo + t] : 0, two = t + NT <= last ? cu[lo + t + NT] : 0;
+  meanwhile();
+  if (t <= last) window[t] = one;
+  if (t + NT <= last) window[t + NT] = two;
   __syncthreads();
   for (int i = t; i < N; i += NT) {
     const int row = r0 + i;
