@@ -20,9 +20,11 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_prom
   __shared__ int begs[BM], window[kWindow], ranges[3][NW], bad[2][NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const int tiles = (a.T + BM - 1) / BM;
-  // the tiles with the most keys of a long sequence first, all heads of a tile side by side
+  // the tiles with the most keys (of a long sequence: the last) first, all heads of a tile side by side
   const int rank = blockIdx.x / a.Hq, hq = blockIdx.x - rank * a.Hq;
-  const int r0 = (tiles - 1 - rank) * BM, kvh = hq / (a.Hq / a.Hkv);
+  int tile = tiles - 1 - rank;
+  if (a.by_length) tile = tile_by_length<BM, NT, false>(a.cu, a.R, a.T, tiles, rank, window, reinterpret_cast<int*>(kt));
+  const int r0 = tile * BM, kvh = hq / (a.Hq / a.Hkv);
 
   // queries: operands for the wave's rows
   const int w0 = r0 + wave * 32, row = w0 + (lane & 31);
@@ -219,6 +221,10 @@ template <int D> hipError_t launch(const PromptArgs& a) {
 
 }  // namespace
 
-hipError_t launch_attn_prompt(const PromptArgs& a) { return a.D == 64 ? launch<64>(a) : launch<128>(a); }
+hipError_t launch_attn_prompt(const PromptArgs& args) {
+  PromptArgs a = args;
+  a.by_length = rank_tiles(a.T, a.R, a.Hq);
+  return a.D == 64 ? launch<64>(a) : launch<128>(a);
+}
 
 }  // namespace gdn

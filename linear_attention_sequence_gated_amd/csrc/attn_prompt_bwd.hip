@@ -75,7 +75,9 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const int tiles = (a.T + BM - 1) / BM;
   const int rank = blockIdx.x / a.Hq, hq = blockIdx.x - rank * a.Hq;
-  const int r0 = (tiles - 1 - rank) * BM, kvh = hq / (a.Hq / a.Hkv);
+  int tile = tiles - 1 - rank;
+  if (a.by_length) tile = tile_by_length<BM, NT, false>(a.cu, a.R, a.T, tiles, rank, window, reinterpret_cast<int*>(kt));
+  const int r0 = tile * BM, kvh = hq / (a.Hq / a.Hkv);
 
   const int w0 = r0 + wave * 32, row = w0 + (lane & 31), at = min(row, a.T - 1);
   const float c = a.scale * kLog2e;
@@ -296,7 +298,9 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
   __shared__ int begs[BN], ends[BN], window[kWindow], most[2][NW], bad[2][NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   // the first tiles of a long sequence meet the most rows
-  const Share sh = share_of(a);
+  Share sh = share_of(a);
+  if (a.keys_by_length)
+    sh.tile = tile_by_length<BN, NT, true>(a.cu, a.R, a.T, (a.T + BN - 1) / BN, sh.tile, window, reinterpret_cast<int*>(qt));
   const int r0 = sh.tile * BN, kvh = sh.kvh, h0 = sh.h0, heads = sh.heads;
 
   find_rows<BN, NT>(a.cu, a.R, a.T, r0, window, begs, ends, [] {});
@@ -464,7 +468,9 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
   const int pair = wave % NP;
   const bool second = wave >= NP;  // do . v and dk
   // the first tiles of a long sequence meet the most rows
-  const Share sh = share_of(a);
+  Share sh = share_of(a);
+  if (a.keys_by_length)
+    sh.tile = tile_by_length<BN, NT, true>(a.cu, a.R, a.T, (a.T + BN - 1) / BN, sh.tile, window, reinterpret_cast<int*>(qt));
   const int r0 = sh.tile * BN, kvh = sh.kvh, h0 = sh.h0, heads = sh.heads;
 
   find_rows<BN, NT>(a.cu, a.R, a.T, r0, window, begs, ends, [] {});
@@ -665,6 +671,8 @@ size_t attn_prompt_bwd_workspace_bytes(int T, int Hq, int Hkv, int D) {
 hipError_t launch_attn_prompt_bwd(const PromptBwdArgs& args) {
   PromptBwdArgs a = args;
   a.shares = shares_of(a.T, a.Hq, a.Hkv);
+  a.by_length = rank_tiles(a.T, a.R, a.Hq);
+  a.keys_by_length = rank_tiles(a.T, a.R, a.Hkv * a.shares);
   return a.D == 64 ? launch<64>(a) : launch<128>(a);
 }
 

@@ -67,7 +67,14 @@ struct PromptArgs {
   long long qs, ks, vs;
   int T, R, Hq, Hkv, D, zero_rest;
   void* stream;
+  bool by_length = false;  // set by the launch: tiles taken by their length
 };
+// Whether the tiles of 128 rows are ranked by length (tile_by_length): several
+// sequences, and more workgroups than run at once (512, two to a CU).
+inline bool rank_tiles(int T, int R, int per_tile) {
+  const int tiles = (T + 127) / 128;
+  return R > 1 && R < 512 && tiles <= 256 && (long long)tiles * per_tile > 512;
+}
 hipError_t launch_attn_prompt(const PromptArgs& a);
 
 struct PromptBwdArgs {
@@ -87,6 +94,7 @@ struct PromptBwdArgs {
   int T, R, Hq, Hkv, D, zero_rest;
   void* stream;
   int shares = 1;  // set by the launch: shares of the query heads of a key head
+  bool by_length = false, keys_by_length = false;
 };
 size_t attn_prompt_bwd_workspace_bytes(int T, int Hq, int Hkv, int D);
 hipError_t launch_attn_prompt_bwd(const PromptBwdArgs& a);

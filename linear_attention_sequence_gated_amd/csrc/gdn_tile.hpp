@@ -250,5 +250,41 @@ __device__ __forceinline__ void find_rows(const int* cu, int R, int T, int r0, i
   __syncthreads();
 }
 
+// The rank-th longest of the tiles of N rows, by one of NT threads each: as long
+// as the keys that its rows see (KEYS: the rows that see its keys), by its first
+// (last) row.  Workgroups are started in the order of their numbers, and the
+// last ones to end are short ones if they were started by length; with few
+// tiles of sequences of many lengths that is worth more than the microsecond
+// that the ranking costs every workgroup (61 tiles of 13 sequences of up to
+// 1201 rows, 16 heads of 128: MEASURED).  Needs tiles <= NT, R < kWindow;
+// `window` (kWindow) and `keys` (NT entries) are scratch.  Ends with a barrier.
+template <int N, int NT, bool KEYS>
+__device__ __forceinline__ int tile_by_length(const int* cu, int R, int T, int tiles, int rank, int* window, int* keys) {
+  const int t = threadIdx.x;
+  const int one = t <= R ? cu[t] : 0, two = t + NT <= R ? cu[t + NT] : 0;
+  if (t <= R) window[t] = one;
+  if (t + NT <= R) window[t + NT] = two;
+  __syncthreads();
+  const int first = t * N, end = min(first + N, T), row = KEYS ? end - 1 : first;
+  const int s = last_at_most([&](int x) { return window[x]; }, 0, R, row);
+  int len = N;
+  if (s < R) len = KEYS ? min(window[s + 1], T) - first : end - max(window[s], 0);
+  // unique: longer first, then the later (KEYS: earlier) tile
+  const int mine = t < tiles ? (min(max(len, 0), T) / 16) * NT + (KEYS ? NT - 1 - t : t) : -1;
+  keys[t] = mine;
+  __syncthreads();
+  int above = 0;
+  for (int i = 0; i < tiles; i += 4) {
+    const int4 x = *reinterpret_cast<const int4*>(keys + i);
+    above += (x.x > mine) + (x.y > mine) + (x.z > mine) + (x.w > mine);
+  }
+  __syncthreads();
+  if (t < tiles && above == rank) window[0] = t;
+  __syncthreads();
+  const int found = window[0];
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(found);
+}
+
 }  // namespace tile
 }  // namespace gdn
