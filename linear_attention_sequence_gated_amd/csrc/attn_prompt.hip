@@ -94,7 +94,10 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_prom
     sk.load(kt[buf], rows_rsrc(kp, a.ks, kv, n, D), wave);
     sv.load(vt[buf], rows_rsrc(vp, a.vs, kv, n, D), wave);
   };
-  int dirty_lo = last, dirty_hi = 0;  // the tiles with non-finite values that were left out
+  // the tiles whose non-finite values were left out: some row may not see them,
+  // and its weight of zero must not meet them; they are added to the rows that
+  // see them when all is written
+  int dirty_lo = last, dirty_hi = 0;
   // one tile of keys; MASKED: some of its keys are not seen by some of the rows
   auto step = [&](auto masked_, int buf, int kv) {
     constexpr bool MASKED = decltype(masked_)::value;
@@ -139,39 +142,25 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_prom
       p[2 * n + 1] = operand(s[n], 1);
     }
     l += sum;
-    bool clean = true;
-    if constexpr (MASKED) {
-      int x = 0;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) x |= bad[buf][w];
-      clean = __builtin_amdgcn_readfirstlane(x) == 0;
-    }
-    if (clean) {
+    for (int i = 0; i < DT; ++i)
 #pragma unroll
-      for (int i = 0; i < DT; ++i)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) o[i] = mma(col_frag<D>(vt[buf], vb, 16 * b, i), p[b], o[i]);
-    } else {
-      // values that some row does not see must not reach its sums: they are left
-      // out here, and added to the rows that see them when all is written
-      dirty_lo = min(dirty_lo, kv);
-      dirty_hi = kv + kN;
-#pragma unroll
-      for (int i = 0; i < DT; ++i)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) o[i] = mma(finite_only(col_frag<D>(vt[buf], vb, 16 * b, i)), p[b], o[i]);
-    }
+      for (int b = 0; b < 4; ++b) o[i] = mma(col_frag<D>(vt[buf], vb, 16 * b, i), p[b], o[i]);
   };
   stage(0, first);
   int buf = 0, kv = first;
   auto next = [&] {
-    // a tile that is masked for some wave: each looks at the values it loaded
-    if (kv + kN - 1 > r0 || kv < latest || kv + kN > last) {
+    const bool masked = kv + kN - 1 > r0 || kv < latest || kv + kN > last;  // for some wave
+    if (masked) {
       wait_staged();
-      const bool ok = Stage<D, kN, NW>::clean(vt[buf], wave);
+      const bool ok = Stage<D, kN, NW>::scrub(vt[buf], wave);
       if (lane == 0) bad[buf][wave] = !ok;
     }
     staged_barrier();
+    if (masked && !all_clean(bad[buf])) {
+      dirty_lo = min(dirty_lo, kv);
+      dirty_hi = kv + kN;
+    }
     if (kv + kN < last) stage(buf ^ 1, kv + kN);
   };
   // tiles of which some row misses some key, at both ends of the range, and

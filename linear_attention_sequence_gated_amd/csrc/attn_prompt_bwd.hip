@@ -26,23 +26,11 @@ constexpr float kLog2e = 1.44269504088896f;
 constexpr int kN = 64;  // rows of a staged tile
 
 // acc[t] += (columns 32 t of a staged tile, rows r0 .. r0 + 15)^T w, as kept in
-// acc's registers.  DIRTY: the tile holds values that are not finite, which
-// some weights, zeros, must not meet: such values are left out.
-template <bool DIRTY, int D>
+// acc's registers.
+template <int D>
 __device__ __forceinline__ void add_columns(f32x16 (&acc)[D / 32], const __bf16* tile, int base, int r0, const u32x4& w) {
 #pragma unroll
-  for (int t = 0; t < D / 32; ++t) {
-    const u32x4 f = col_frag<D>(tile, base, r0, t);
-    acc[t] = mma(DIRTY ? finite_only(f) : f, w, acc[t]);
-  }
-}
-
-// Whether all waves found their part of a tile finite.
-template <int NW> __device__ __forceinline__ bool all_clean(const int (&bad)[NW]) {
-  int x = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) x |= bad[w];
-  return __builtin_amdgcn_readfirstlane(x) == 0;
+  for (int t = 0; t < D / 32; ++t) acc[t] = mma(col_frag<D>(tile, base, r0, t), w, acc[t]);
 }
 
 template <int D> __device__ __forceinline__ void store_rows(__bf16* dst, const f32x16 (&acc)[D / 32], float f, int hl) {
@@ -54,16 +42,19 @@ template <int D> __device__ __forceinline__ void store_rows(__bf16* dst, const f
           pipe::cvt4(f32x4{acc[i][4 * e] * f, acc[i][4 * e + 1] * f, acc[i][4 * e + 2] * f, acc[i][4 * e + 3] * f});
 }
 
-// NaN into a gradient row's entries wherever rows [lo, hi) of src hold a value
-// that is not finite: what add_columns left out, for the rows that it concerns.
-// Each lane sees to the entries that it stored.
+// What scrubbing left out of a gradient row: NaN into its entries where rows
+// [lo, hi) of src hold a value that is not finite, or, with `all`, into all of
+// them if there is any.  Each lane sees to the entries that it stored.
 template <int D, class T>
-__device__ __forceinline__ void spoil(T* dst, const void* src, long long stride, int lo, int hi, int hl) {
+__device__ __forceinline__ void spoil(T* dst, const void* src, long long stride, int lo, int hi, bool all, int hl) {
   for (int i = lo; i < hi; ++i) {
     const __bf16* x = static_cast<const __bf16*>(src) + (long long)i * stride;
+    bool any = false;
+    if (all)
+      for (int d = 0; d < D; ++d) any |= !__builtin_isfinite((float)x[d]);
     for (int d = 4 * hl; d < D; d += 8)
       for (int j = 0; j < 4; ++j)
-        if (!__builtin_isfinite((float)x[d + j])) dst[d + j] = (T)__builtin_nanf("");
+        if (any || !__builtin_isfinite((float)x[d + j])) dst[d + j] = (T)__builtin_nanf("");
   }
 }
 
@@ -146,7 +137,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
   f32x16 dq[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) dq[i] = zero16();
-  const int rb = row_base<D>(lane), cb = col_base<D>(lane);
+  const int rb0 = row_base<D>(lane), cb0 = col_base<D>(lane);
   Stage<D, kN, NW> sk, sv;
   sk.init(a.ks, wave);
   sv.init(a.vs, wave);
@@ -158,10 +149,11 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
     sv.load(vt[buf], rows_rsrc(vp, a.vs, kv, n, D), wave);
   };
   const int from = beg - 4 * hl, upto = beg < 0 ? -8 : row - 4 * hl;  // the keys that the lane's row sees
-  int dirty_lo = last, dirty_hi = 0;                                   // keys of tiles in which values were left out
+  int dirty_lo = last, dirty_hi = 0;  // keys of tiles that held values that are not finite
   int buf = 0, kv = first;
-  auto step = [&](auto masked_, auto dirty_, const __bf16* K, const __bf16* V) {
-    constexpr bool MASKED = decltype(masked_)::value, DIRTY = decltype(dirty_)::value;
+  auto step = [&](auto masked_, const __bf16* K, const __bf16* V) {
+    constexpr bool MASKED = decltype(masked_)::value;
+    const int rb = fresh(rb0), cb = fresh(cb0);
 #pragma unroll 1
     for (int n = 0; n < 2; ++n) {
       const unsigned seen = bits(from - kv - 32 * n, upto - kv - 32 * n);
@@ -178,47 +170,43 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
         if constexpr (MASKED) s[e] = where_seen<true>(s[e], seen, e);
       }
 #pragma unroll
-      for (int b = 0; b < 2; ++b) add_columns<DIRTY, D>(dq, K, cb, 32 * n + 16 * b, operand(s, b));
+      for (int b = 0; b < 2; ++b) add_columns<D>(dq, K, cb, 32 * n + 16 * b, operand(s, b));
     }
   };
   stage(0, first);
   auto next = [&] {
-    // a tile that is masked for some wave: each looks at the keys it loaded
-    if (kv + kN - 1 > r0 || kv < latest || kv + kN > last) {
+    const bool masked = kv + kN - 1 > r0 || kv < latest || kv + kN > last;  // for some wave
+    if (masked) {
       wait_staged();
-      const bool ok = Stage<D, kN, NW>::clean(kt[buf], wave);
+      const bool ok = Stage<D, kN, NW>::scrub(kt[buf], wave);
       if (lane == 0) bad[buf][wave] = !ok;
     }
     staged_barrier();
+    if (masked && !all_clean(bad[buf])) {
+      dirty_lo = min(dirty_lo, kv);
+      dirty_hi = kv + kN;
+    }
     if (kv + kN < last) stage(buf ^ 1, kv + kN);
   };
   // tiles of which some row misses some key, at both ends, and those between
   auto edge = [&](int end) {
     for (; kv < end; kv += kN, buf ^= 1) {
       next();
-      if (kv > w0 + 31 || kv + kN <= lowest) continue;
-      if (all_clean(bad[buf])) {
-        step(std::true_type{}, std::false_type{}, kt[buf], vt[buf]);
-      } else {
-        step(std::true_type{}, std::true_type{}, kt[buf], vt[buf]);
-        dirty_lo = min(dirty_lo, kv);
-        dirty_hi = kv + kN;
-      }
+      if (kv <= w0 + 31 && kv + kN > lowest) step(std::true_type{}, kt[buf], vt[buf]);
     }
   };
   edge(min(highest, last));
   for (; kv + kN - 1 <= w0; kv += kN, buf ^= 1) {
     next();
-    step(std::false_type{}, std::false_type{}, kt[buf], vt[buf]);
+    step(std::false_type{}, kt[buf], vt[buf]);
   }
   edge(last);
   const bool rest = beg < 0 && row < a.T && a.zero_rest;
   if (beg >= 0 || rest)
     store_rows<D>(static_cast<__bf16*>(a.grad_q) + (long long)row * a.gqs + (long long)hq * D, dq, rest ? 0.f : a.scale, hl);
-  if (dirty_hi && beg >= 0) {
+  if (dirty_hi && beg >= 0)  // a key that is not finite spoils the weights of all rows that see it
     spoil<D>(static_cast<__bf16*>(a.grad_q) + (long long)row * a.gqs + (long long)hq * D, kp, a.ks, max(beg, dirty_lo),
-             min(row + 1, dirty_hi), hl);
-  }
+             min(row + 1, dirty_hi), true, hl);
 }
 
 // ------------------------------------------------------------------ dk, dv
@@ -259,16 +247,20 @@ __device__ __forceinline__ void write_grad(const PromptBwdArgs& a, const Share& 
                   acc, rest ? 0.f : f, hl);
 }
 
+// Rows of q that are not finite spoil the weights of their keys, dk and dv
+// whole; rows of do that are not finite dk whole and dv where they are not.
 template <int D>
 __device__ __forceinline__ void spoil_grad(const PromptBwdArgs& a, const Share& sh, bool values, int key, int end, int hl) {
-  for (int h = sh.h0; h < sh.h0 + sh.heads; ++h) {
-    const __bf16* src = static_cast<const __bf16*>(values ? a.grad_out : a.q) + (long long)h * D;
-    const long long stride = values ? a.gos : a.qs;
+  for (int x = 0; x < 2 * sh.heads; ++x) {
+    const bool outer = x & 1;  // do
+    const __bf16* src = static_cast<const __bf16*>(outer ? a.grad_out : a.q) + (long long)(sh.h0 + x / 2) * D;
+    const long long stride = outer ? a.gos : a.qs;
+    const bool all = !(outer && values);
     if (a.shares > 1)
-      spoil<D>(sums_row(a, D, sh.at, values, key, sh.kvh), src, stride, key, end, hl);
+      spoil<D>(sums_row(a, D, sh.at, values, key, sh.kvh), src, stride, key, end, all, hl);
     else
       spoil<D>(static_cast<__bf16*>(values ? a.grad_v : a.grad_k) + (long long)key * (values ? a.gvs : a.gks) + (long long)sh.kvh * D,
-               src, stride, key, end, hl);
+               src, stride, key, end, all, hl);
   }
 }
 
@@ -359,7 +351,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
   f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) dk[i] = dv[i] = zero16();
-  const int rb = row_base<D>(lane), cb = col_base<D>(lane);
+  const int rb0 = row_base<D>(lane), cb0 = col_base<D>(lane);
   Stage<D, kN, NW> sq, sg;
   sq.init(a.qs, wave);
   sg.init(a.gos, wave);
@@ -372,10 +364,11 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
     if (wave == 0) stage_words(lt[buf], pipe::make_rsrc(a.ws + (size_t)hq * a.T + i0, n * 4));
     if (wave == 1) stage_words(dt[buf], pipe::make_rsrc(a.ws + (size_t)(a.Hq + hq) * a.T + i0, n * 4));
   };
-  bool dirty = false;  // values were left out
+  bool dirty = false;  // a tile held values that are not finite
   // a tile of rows that the wave's keys may be seen by
-  auto step = [&](auto masked_, auto dirty_, int buf, int i1) {
-    constexpr bool MASKED = decltype(masked_)::value, DIRTY = decltype(dirty_)::value;
+  auto step = [&](auto masked_, int buf, int i1) {
+    constexpr bool MASKED = decltype(masked_)::value;
+    const int rb = fresh(rb0), cb = fresh(cb0);
     const __bf16 *Q = qt[buf], *O = gt[buf];
     const int from = key - i1 - 4 * hl, upto = end - 1 - i1 - 4 * hl;  // the rows that see the lane's key
 #pragma unroll MASKED ? 1 : 2
@@ -404,8 +397,8 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
       }
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        add_columns<DIRTY, D>(dv, O, cb, 32 * n + 16 * b, operand(s, b));
-        add_columns<DIRTY, D>(dk, Q, cb, 32 * n + 16 * b, operand(dp, b));
+        add_columns<D>(dv, O, cb, 32 * n + 16 * b, operand(s, b));
+        add_columns<D>(dk, Q, cb, 32 * n + 16 * b, operand(dp, b));
       }
     }
   };
@@ -414,13 +407,14 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
   for (int head = 0; head < heads; ++head) {
     int i1 = r0;
     auto next = [&] {
-      // a tile that is masked for some wave: each looks at what it loaded
-      if (i1 < r0 + BN - 1 || i1 + kN > soonest) {
+      const bool masked = i1 < r0 + BN - 1 || i1 + kN > soonest;  // for some wave
+      if (masked) {
         wait_staged();
-        const bool ok = Stage<D, kN, NW>::clean(qt[buf], wave) && Stage<D, kN, NW>::clean(gt[buf], wave);
-        if (lane == 0) bad[buf][wave] = !ok;
+        const bool q_ok = Stage<D, kN, NW>::scrub(qt[buf], wave), g_ok = Stage<D, kN, NW>::scrub(gt[buf], wave);
+        if (lane == 0) bad[buf][wave] = !(q_ok && g_ok);
       }
       staged_barrier();
+      if (masked && !all_clean(bad[buf])) dirty = true;
       if (i1 + kN < last) stage(buf ^ 1, h0 + head, i1 + kN);
       else if (head + 1 < heads) stage(buf ^ 1, h0 + head + 1, r0);
     };
@@ -428,19 +422,13 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
     auto edge = [&](int stop) {
       for (; i1 < stop; i1 += kN, buf ^= 1) {
         next();
-        if (i1 + kN - 1 < w0 || i1 >= highest) continue;
-        if (all_clean(bad[buf])) {
-          step(std::true_type{}, std::false_type{}, buf, i1);
-        } else {
-          step(std::true_type{}, std::true_type{}, buf, i1);
-          dirty = true;
-        }
+        if (i1 + kN - 1 >= w0 && i1 < highest) step(std::true_type{}, buf, i1);
       }
     };
     edge(min(w0 + 31, last));
     for (; i1 + kN <= lowest; i1 += kN, buf ^= 1) {
       next();
-      step(std::false_type{}, std::false_type{}, buf, i1);
+      step(std::false_type{}, buf, i1);
     }
     edge(last);
   }
@@ -525,7 +513,7 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
   f32x16 acc[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) acc[i] = zero16();
-  const int rb = row_base<D>(lane), cb = col_base<D>(lane);
+  const int rb0 = row_base<D>(lane), cb0 = col_base<D>(lane);
   const __bf16* qp = static_cast<const __bf16*>(a.q);
   const __bf16* gp = static_cast<const __bf16*>(a.grad_out);
   // Q is staged by the first waves, dO by the second
@@ -543,6 +531,7 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
   auto scores = [&](auto masked_, int buf, int i1) {
     constexpr bool MASKED = decltype(masked_)::value;
     const __bf16* X = second ? gt[buf] : qt[buf];
+    const int rb = fresh(rb0);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       s[n] = zero16();
@@ -566,8 +555,9 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
         hand[pair][4 * n + e4][lane] = p;
       }
   };
-  auto products = [&](auto masked_, auto dirty_, int buf, int i1) {
-    constexpr bool MASKED = decltype(masked_)::value, DIRTY = decltype(dirty_)::value;
+  auto products = [&](auto masked_, int buf, int i1) {
+    constexpr bool MASKED = decltype(masked_)::value;
+    const int cb = fresh(cb0);
     const __bf16* Y = second ? qt[buf] : gt[buf];
     if (second) {
       const int from = key - i1 - 4 * hl, upto = end - 1 - i1 - 4 * hl;
@@ -588,21 +578,22 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) add_columns<DIRTY, D>(acc, Y, cb, 32 * n + 16 * b, operand(s[n], b));
+      for (int b = 0; b < 2; ++b) add_columns<D>(acc, Y, cb, 32 * n + 16 * b, operand(s[n], b));
   };
-  bool dirty = false;  // values were left out
+  bool dirty = false;  // a tile held values that are not finite
   stage(0, h0, r0);
   int buf = 0;
   for (int head = 0; head < heads; ++head) {
     int i1 = r0;
     auto next = [&] {
-      // a tile that is masked for some wave: each looks at what it loaded
-      if (i1 < r0 + BN - 1 || i1 + kN > soonest) {
+      const bool masked = i1 < r0 + BN - 1 || i1 + kN > soonest;  // for some wave
+      if (masked) {
         wait_staged();
-        const bool ok = Stage<D, kN, NP>::clean(second ? gt[buf] : qt[buf], pair);
+        const bool ok = Stage<D, kN, NP>::scrub(second ? gt[buf] : qt[buf], pair);
         if (lane == 0) bad[buf][wave] = !ok;
       }
       staged_barrier();
+      if (masked && !all_clean(bad[buf])) dirty = true;
       if (i1 + kN < last) stage(buf ^ 1, h0 + head, i1 + kN);
       else if (head + 1 < heads) stage(buf ^ 1, h0 + head + 1, r0);
     };
@@ -613,13 +604,7 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
         next();
         if (met) scores(std::true_type{}, buf, i1);
         pipe::stage_barrier();
-        if (!met) continue;
-        if (all_clean(bad[buf])) {
-          products(std::true_type{}, std::false_type{}, buf, i1);
-        } else {
-          products(std::true_type{}, std::true_type{}, buf, i1);
-          dirty = true;
-        }
+        if (met) products(std::true_type{}, buf, i1);
       }
     };
     edge(min(w0 + 31, last));
@@ -627,7 +612,7 @@ template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv
       next();
       scores(std::false_type{}, buf, i1);
       pipe::stage_barrier();
-      products(std::false_type{}, std::false_type{}, buf, i1);
+      products(std::false_type{}, buf, i1);
     }
     edge(last);
   }

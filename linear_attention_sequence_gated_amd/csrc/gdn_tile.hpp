@@ -70,24 +70,15 @@ __device__ __forceinline__ unsigned worst(unsigned m, unsigned w) {
 }
 __device__ __forceinline__ bool finite(unsigned m) { return (m & 0xffffu) < 0x7f80u && (m >> 16) < 0x7f80u; }
 
-// A word with its non-finite halves replaced: by zero, or (kind 1, 2, 3) one
-// where the half is +infinity, -infinity, NaN and zero elsewhere.
-__device__ __forceinline__ unsigned pick(unsigned w, int kind) {
-  unsigned r = 0;
+// Words with their non-finite halves set to zero.
+__device__ __forceinline__ u32x4 finite_only(u32x4 w) {
 #pragma unroll
-  for (int s = 0; s < 32; s += 16) {
-    const unsigned x = (w >> s) & 0xffffu, a = x & 0x7fffu;
-    const bool bad = a >= 0x7f80u;
-    const bool hit = kind == 1 ? x == 0x7f80u : kind == 2 ? x == 0xff80u : a > 0x7f80u;
-    r |= (kind == 0 ? (bad ? 0u : x) : (hit ? 0x3f80u : 0u)) << s;
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+    if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
   }
-  return r;
+  return w;
 }
-__device__ __forceinline__ u32x4 pick(const u32x4& w, int kind) {
-  return u32x4{pick(w[0], kind), pick(w[1], kind), pick(w[2], kind), pick(w[3], kind)};
-}
-
-__device__ __forceinline__ u32x4 finite_only(const u32x4& w) { return pick(w, 0); }
 
 // The score e of a half-tile (of 32 keys, element e) where bit 8 (e / 4) + e % 4
 // of `seen` is set, otherwise -infinity (ZERO: zero).
@@ -141,17 +132,39 @@ template <int D, int N, int NW> struct Stage {
     for (int i = 0; i < LOADS; ++i)
       stage_pieces(lds + (wave * LOADS + i) * 512, rsrc, off[i]);
   }
-  // Whether the part that this wave loaded is finite (its loads have arrived).
-  static __device__ __forceinline__ bool clean(const __bf16* lds, int wave) {
+  // Sets the values that are not finite, of the part that this wave loaded, to
+  // zero; false if there were any.  Its loads have arrived.
+  static __device__ __forceinline__ bool scrub(__bf16* lds, int wave) {
     unsigned m = 0;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
       const u32x4 x = *reinterpret_cast<const u32x4*>(lds + (wave * LOADS + i) * 512 + (threadIdx.x & 63) * 8);
       m = worst(worst(worst(worst(m, x[0]), x[1]), x[2]), x[3]);
     }
-    return __all(finite(m));
+    if (__all(finite(m))) return true;
+#pragma unroll 1
+    for (int i = 0; i < LOADS; ++i) {
+      u32x4* x = reinterpret_cast<u32x4*>(lds + (wave * LOADS + i) * 512 + (threadIdx.x & 63) * 8);
+      *x = finite_only(*x);
+    }
+    return false;
   }
 };
+
+// Whether no wave found anything to scrub.
+template <int NW> __device__ __forceinline__ bool all_clean(const int (&bad)[NW]) {
+  int x = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) x |= bad[w];
+  return __builtin_amdgcn_readfirstlane(x) == 0;
+}
+
+// x, which the compiler takes for a new value: what is computed from it is
+// computed where it is used, not kept in registers over a loop.
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
 
 // Operand rows: row r0 + l % 32 of a staged tile, its values 16 ks + 8 h .. + 7.
 template <int D> __device__ __forceinline__ int row_base(int lane) { return pipe::row_off<D>(lane & 31, 8 * (lane >> 5)) * 2; }
