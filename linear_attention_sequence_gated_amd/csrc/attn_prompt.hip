@@ -14,7 +14,7 @@ constexpr float kLowest = -1e30f;  // running maximum before the first token
 constexpr float kSlack = 8.f;      // the maximum in use may lie this far (powers of two) below the true one
 constexpr int kN = 64;             // keys of a tile
 
-template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_kernel(PromptArgs a) {
+template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 2) void attn_prompt_kernel(PromptArgs a) {
   constexpr int BM = 32 * NW, NT = 64 * NW, KS = D / 16, DT = D / 32;
   __shared__ __bf16 kt[2][kN * D], vt[2][kN * D];
   __shared__ int begs[BM], window[kWindow], ranges[3][NW], bad[2][NW];
@@ -83,7 +83,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_prom
 #pragma unroll
   for (int i = 0; i < DT; ++i) o[i] = zero16();
 
-  const int kb = row_base<D>(lane), vb = col_base<D>(lane);
+  const int kb0 = row_base<D>(lane), vb0 = col_base<D>(lane);
   Stage<D, kN, NW> sk, sv;
   sk.init(a.ks, wave);
   sv.init(a.vs, wave);
@@ -101,6 +101,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_prom
   // one tile of keys; MASKED: some of its keys are not seen by some of the rows
   auto step = [&](auto masked_, int buf, int kv) {
     constexpr bool MASKED = decltype(masked_)::value;
+    const int kb = fresh(kb0), vb = fresh(vb0);
     f32x16 s[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
