@@ -7,6 +7,8 @@ side by side; the distance between rows is free, so that q, k and v can be parts
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import gdn as raw
@@ -23,24 +25,20 @@ def _device(t, who):
 
 
 def _dense(t, name, shape, dtype, dev):
-    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev.index or not t.is_contiguous():
         raw._check(t, name, shape, dtype, dev)
 
 
 def _rows(t, name, shape, dev):
     """Distance between the rows of t [tokens, heads, D], whose rows are dense."""
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != _BF16:
-        raise TypeError(f"{name}: expected {_BF16}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name}: expected device {dev}, got {t.device}")
     tokens, heads, d = shape
-    row, head, one = t.stride()
-    if one != 1 or (head != d and heads != 1):
+    row, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if t.shape != shape or t.dtype is not _BF16 or t.get_device() != dev.index:
+        raw._check(t.contiguous(), name, shape, _BF16, dev)
+    if d > 1 and one != 1 or heads > 1 and head != d:
         raise ValueError(f"{name}: the heads of a row must be contiguous")
     if tokens <= 1:
-        return max(row, heads * d) // 8 * 8 if row % 8 else max(row, heads * d)
+        return heads * d
     if row < heads * d or row % 8:
         raise ValueError(f"{name}: rows must be a multiple of 8 elements apart and not overlap")
     return row
@@ -49,7 +47,7 @@ def _rows(t, name, shape, dev):
 def _call(dev, stream, fn, *args):
     """fn(*args, stream) with `dev` as the current device."""
     if torch.cuda.current_device() == dev.index:
-        s = fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else stream)
+        s = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream)
     else:
         with torch.cuda.device(dev):
             s = fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else stream)
@@ -112,6 +110,11 @@ def cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=None
           raw.GDN_BF16, fmt)
 
 
+@functools.lru_cache(maxsize=None)
+def _decode_workspace(*sizes):
+    return raw.gdn_attn_decode_workspace_bytes(*sizes)
+
+
 def attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale: float | None = None, out=None,
                 lse=None, workspace=None, stream=None):
     """Attention of one new token per request, q [R, Hq, D] bf16, over the first seq_lens [R] tokens of its blocks
@@ -136,9 +139,8 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, sc
     else:
         _dense(lse, "lse", (r, hq), _F32, dev)
     lib = raw.load()
-    need = lib.gdn_attn_decode_workspace_bytes(r, hq, hkv, d, bt, width)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(_decode_workspace(r, hq, hkv, d, bt, width), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous on the device of q")
     _call(dev, stream, lib.gdn_attn_decode, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),

@@ -47,6 +47,10 @@ constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
 constexpr float kLowest = -3e38f;  // running maximum before the first token
 constexpr float kCodeUp = 1024.f;  // int8 codes enter the products times 2^-10
 
+// Shares of the work: what the CUs hold at once (three workgroups of the 139
+// registers that d = 64 takes, two at d = 128).
+constexpr int most_shares(int D) { return 256 * (D == 64 ? 3 : 2); }
+
 struct DecodeSizes {
   int R, Hq, Hkv, G, NG, Gc, bt, width, num_blocks, W;
 };
@@ -269,32 +273,53 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
     found[1] = at;
   }
   __syncthreads();
+  // the part of one (request, key head) that a share covers: units [ua, ub)
+  struct Part {
+    int r, n, nu, h, q0, cols, ua, ub;
+  };
   int r = __builtin_amdgcn_readfirstlane(found[0]);
   long long base = (long long)__builtin_amdgcn_readfirstlane(found[1]) * heads;  // first unit of request r
+  auto part_at = [&](long long u) {
+    Part p;
+    p.r = r;
+    p.n = tokens_of(a.seq_lens, r, z);
+    p.nu = units_of(p.n);
+    const int hh = (int)((u - base) / p.nu);
+    p.h = hh / z.NG;
+    p.q0 = p.h * z.G + (hh - p.h * z.NG) * 16;
+    p.cols = min(16, (p.h + 1) * z.G - p.q0);
+    p.ua = (int)(u - base - (long long)hh * p.nu);
+    p.ub = (int)min((long long)p.nu, p.ua + (u1 - u));
+    return p;
+  };
+  Tile<D> t0, t1;
+  u32x4 qw[D / 32];
+  // its queries and first tile, on their way while the part before it is joined
+  auto begin = [&](const Part& p) {
+    const __hip_bfloat16* src =
+        static_cast<const __hip_bfloat16*>(a.q) + (long long)p.r * a.qs + (long long)(p.q0 + min(c, p.cols - 1)) * D;
+#pragma unroll
+    for (int ks = 0; ks < D / 32; ++ks) qw[ks] = *reinterpret_cast<const u32x4*>(src + (D / 4) * g + 8 * ks);
+    const int tok = p.ua * kUnit + wave * kTile, end = min(p.n, p.ub * kUnit);
+    if (tok < end) load_tile<D>(t0, tok, end, a.block_table + (size_t)p.r * z.width, p.h, a, z);
+  };
 
   bool first = true;
-  for (long long u = u0; u < u1;) {
-    const int n = tokens_of(a.seq_lens, r, z), nu = units_of(n);
-    const int hh = (int)((u - base) / nu), h = hh / z.NG, q0 = h * z.G + (hh - h * z.NG) * 16;
-    const int cols = min(16, (h + 1) * z.G - q0);
-    const int ua = (int)(u - base - (long long)hh * nu);                       // units of (r, hh): [ua, ub)
-    const int ub = (int)min((long long)nu, ua + (u1 - u));
-    const int* row = a.block_table + (size_t)r * z.width;
+  Part cur = part_at(u0);
+  begin(cur);
+  for (long long u = u0;;) {
+    const int nu = cur.nu, h = cur.h, q0 = cur.q0, cols = cur.cols, ua = cur.ua, ub = cur.ub, rr = cur.r;
+    const int* row = a.block_table + (size_t)rr * z.width;
 
     // query operands, moved into fp16's range
     f16x8 q[D / 32];
     float qfac;
     {
-      const __hip_bfloat16* src =
-          static_cast<const __hip_bfloat16*>(a.q) + (long long)r * a.qs + (long long)(q0 + min(c, cols - 1)) * D;
-      u32x4 w[D / 32];
       float top = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < D / 32; ++ks) {
-        w[ks] = *reinterpret_cast<const u32x4*>(src + (D / 4) * g + 8 * ks);
+      for (int ks = 0; ks < D / 32; ++ks)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(pipe::lo_f(w[ks][e])), fabsf(pipe::hi_f(w[ks][e]))));
-      }
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(pipe::lo_f(qw[ks][e])), fabsf(pipe::hi_f(qw[ks][e]))));
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const int e2 = __builtin_amdgcn_frexp_expf(top);
@@ -304,8 +329,8 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
       for (int ks = 0; ks < D / 32; ++ks)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          q[ks][2 * e] = (_Float16)(pipe::lo_f(w[ks][e]) * down);
-          q[ks][2 * e + 1] = (_Float16)(pipe::hi_f(w[ks][e]) * down);
+          q[ks][2 * e] = (_Float16)(pipe::lo_f(qw[ks][e]) * down);
+          q[ks][2 * e + 1] = (_Float16)(pipe::hi_f(qw[ks][e]) * down);
         }
     }
 
@@ -314,11 +339,9 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
     s.l = 0.f;
 #pragma unroll
     for (int i = 0; i < NB; ++i) s.acc[i] = pipe::zero4();
-    const int end = min(n, ub * kUnit);
-    Tile<D> t0, t1;
+    const int end = min(cur.n, ub * kUnit);
     int tok = ua * kUnit + wave * kTile;
     if (tok < end) {
-      load_tile<D>(t0, tok, end, row, h, a, z);
       for (;;) {
         if (tok + kUnit < end) load_tile<D>(t1, tok + kUnit, end, row, h, a, z);
         take_tile<D, FMT>(s, t0, q, qfac);
@@ -329,6 +352,24 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
         tok += kUnit;
         if (tok >= end) break;
       }
+    }
+
+    u += ub - ua;
+    const bool more = u < u1;
+    if (more) {
+      if (u >= base + (long long)nu * heads) {  // the next request that has tokens
+        base += (long long)nu * heads;
+        for (++r;; r += 64) {
+          const unsigned long long some = __ballot(r + lane < z.R && tokens_of(a.seq_lens, min(r + lane, z.R - 1), z) > 0);
+          if (some) {
+            r += __builtin_ctzll(some);
+            break;
+          }
+        }
+        r = __builtin_amdgcn_readfirstlane(r);
+      }
+      cur = part_at(u);
+      begin(cur);
     }
 
     // join the waves
@@ -360,7 +401,7 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
     float* o_ws = a.ws + slot * z.Gc * (D + 2);
     if (wave == 0 && lane < cols) {
       if (whole) {
-        if (a.lse) a.lse[(size_t)r * z.Hq + q0 + lane] = L > 0.f ? (M + __builtin_amdgcn_logf(L)) * kLn2 : -INFINITY;
+        if (a.lse) a.lse[(size_t)rr * z.Hq + q0 + lane] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
       } else {
         o_ws[z.Gc * D + 2 * lane] = M;
         o_ws[z.Gc * D + 2 * lane + 1] = L;
@@ -378,38 +419,26 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
         for (int w = 1; w < kWaves; ++w) Mc = fmaxf(Mc, ml[w][0][col]);
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) Lc += ml[w][1][col] * __builtin_amdgcn_exp2f(ml[w][0][col] - Mc);
-        const float inv = Lc > 0.f ? 1.f / Lc : 0.f;
+        const float inv = Lc == 0.f ? 0.f : 1.f / Lc;
         o *= inv;
-        *reinterpret_cast<u32x2*>(static_cast<__bf16*>(a.out) + ((size_t)r * z.Hq + q0 + col) * D + d) = pipe::cvt4(o);
+        *reinterpret_cast<u32x2*>(static_cast<__bf16*>(a.out) + ((size_t)rr * z.Hq + q0 + col) * D + d) = pipe::cvt4(o);
       } else {
         *reinterpret_cast<f32x4*>(o_ws + col * D + d) = o;
       }
     }
+    if (!more) return;
     __syncthreads();
     first = false;
-    u += ub - ua;
-    if (u < u1 && u >= base + (long long)nu * heads) {  // the next request that has tokens
-      base += (long long)nu * heads;
-      for (++r;; r += 64) {
-        const unsigned long long some = __ballot(r + lane < z.R && tokens_of(a.seq_lens, min(r + lane, z.R - 1), z) > 0);
-        if (some) {
-          r += __builtin_ctzll(some);
-          break;
-        }
-      }
-      r = __builtin_amdgcn_readfirstlane(r);
-    }
   }
 }
 
 // Joins the shares of one (request, query head), in the order of the tokens;
 // heads that one workgroup covered are done already.  Requests without tokens
 // get their zeros here.
-template <int D> __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs a, DecodeSizes z) {
-  constexpr int NP = 256 / (D / 4);  // shares taken side by side
-  __shared__ float sum[NP][D];
-  __shared__ float red[4];
-  __shared__ int scan[2][kWaves];
+template <int D> __global__ __launch_bounds__(512) void attn_decode_join_kernel(DecodeArgs a, DecodeSizes z) {
+  constexpr int NT = 512, NP = NT / (D / 4);  // shares taken side by side
+  __shared__ float sum[NP][D], ls[NP], weight[most_shares(D)], part_l[most_shares(D)], red[NT / 64];
+  __shared__ int scan[2][NT / 64];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int r = blockIdx.x / z.Hq, hq = blockIdx.x % z.Hq, h = hq / z.G, in = hq - h * z.G, hh = h * z.NG + in / 16, col = in % 16;
   const int n = tokens_of(a.seq_lens, r, z), nu = units_of(n), heads = z.Hkv * z.NG;
@@ -420,7 +449,7 @@ template <int D> __global__ __launch_bounds__(256) void attn_decode_join_kernel(
     return;
   }
   int all = 0, pre = 0;
-  for (int i = tid; i < z.R; i += 256) {
+  for (int i = tid; i < z.R; i += NT) {
     const int x = units_of(tokens_of(a.seq_lens, i, z));
     all += x;
     pre += i < r ? x : 0;
@@ -435,8 +464,12 @@ template <int D> __global__ __launch_bounds__(256) void attn_decode_join_kernel(
     scan[1][wave] = pre;
   }
   __syncthreads();
-  all = scan[0][0] + scan[0][1] + scan[0][2] + scan[0][3];
-  pre = scan[1][0] + scan[1][1] + scan[1][2] + scan[1][3];
+  all = pre = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) {
+    all += scan[0][w];
+    pre += scan[1][w];
+  }
   const long long U = (long long)all * heads, P = (long long)pre * heads + (long long)hh * nu;
   // the workgroup that takes unit x: the first whose share ends past it
   auto taker = [&](long long x) { return (int)(((x + 1) * z.W + U - 1) / U - 1); };
@@ -446,27 +479,35 @@ template <int D> __global__ __launch_bounds__(256) void attn_decode_join_kernel(
     const bool head_of_share = U * i / z.W >= P;
     return a.ws + (2 * (size_t)i + (head_of_share ? 0 : 1)) * z.Gc * (D + 2);
   };
+  // maxima and sums of the shares first, as weights; then the outputs, their
+  // loads independent of one another
+  const int n_parts = i1 - i0 + 1;
   float M = kLowest;
-  for (int i = i0 + tid; i <= i1; i += 256)
-    if (U * i / z.W < U * (i + 1) / z.W) M = fmaxf(M, at(i)[z.Gc * D + 2 * col]);
+  for (int i = tid; i < n_parts; i += NT) {
+    const bool any = U * (i0 + i) / z.W < U * (i0 + i + 1) / z.W;  // a share may be without units
+    const float2 x = any ? *reinterpret_cast<const float2*>(at(i0 + i) + z.Gc * D + 2 * col) : make_float2(kLowest, 0.f);
+    weight[i] = x.x;
+    part_l[i] = x.y;
+    M = fmaxf(M, x.x);
+  }
 #pragma unroll
   for (int d = 32; d; d >>= 1) M = fmaxf(M, __shfl_xor(M, d));
   if (lane == 0) red[wave] = M;
   __syncthreads();
-  M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) M = fmaxf(M, red[w]);
+  for (int i = tid; i < n_parts; i += NT) weight[i] = part_l[i] == 0.f ? 0.f : __builtin_amdgcn_exp2f(weight[i] - M);
+  __syncthreads();
   const int part = tid / (D / 4), d = 4 * (tid % (D / 4));
   f32x4 o = pipe::zero4();
   float L = 0.f;
 #pragma unroll 4
-  for (int i = i0 + part; i <= i1; i += NP) {
-    if (U * i / z.W >= U * (i + 1) / z.W) continue;  // a share without units
-    const float* w = at(i);
-    const float e = __builtin_amdgcn_exp2f(w[z.Gc * D + 2 * col] - M);
-    L += e * w[z.Gc * D + 2 * col + 1];
-    o += *reinterpret_cast<const f32x4*>(w + col * D + d) * e;
+  for (int i = part; i < n_parts; i += NP) {
+    const float e = weight[i];
+    L += e * part_l[i];
+    if (e != 0.f) o += *reinterpret_cast<const f32x4*>(at(i0 + i) + col * D + d) * e;
   }
   *reinterpret_cast<f32x4*>(&sum[part][d]) = o;
-  __shared__ float ls[NP];
   if (d == 0) ls[part] = L;
   __syncthreads();
   if (tid < D / 4) {
@@ -477,9 +518,9 @@ template <int D> __global__ __launch_bounds__(256) void attn_decode_join_kernel(
       L += ls[p];
       o += *reinterpret_cast<const f32x4*>(&sum[p][4 * tid]);
     }
-    o *= L > 0.f ? 1.f / L : 0.f;
+    o *= L == 0.f ? 0.f : 1.f / L;
     *reinterpret_cast<u32x2*>(out + 4 * tid) = pipe::cvt4(o);
-    if (tid == 0 && a.lse) a.lse[(size_t)r * z.Hq + hq] = L > 0.f ? (M + __builtin_amdgcn_logf(L)) * kLn2 : -INFINITY;
+    if (tid == 0 && a.lse) a.lse[(size_t)r * z.Hq + hq] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
   }
 }
 
@@ -494,10 +535,9 @@ DecodeSizes sizes(int R, int Hq, int Hkv, int D, int bt, int width, int num_bloc
   z.bt = bt;
   z.width = width;
   z.num_blocks = num_blocks;
-  // what the CUs hold at once (three workgroups of the 139 registers that
-  // d = 64 takes, two at d = 128), and no more than there can be units
+  // no more shares than there can be units
   const long long units = ((long long)width * bt + kUnit - 1) / kUnit * R * Hkv * z.NG;
-  const int most = 256 * (D == 64 ? 3 : 2);
+  const int most = most_shares(D);
   z.W = units < most ? (int)units : most;
   return z;
 }
@@ -508,7 +548,7 @@ template <int D, int FMT> hipError_t launch(const DecodeArgs& a, const DecodeSiz
     const hipError_t e = launch_kernel(attn_decode_kernel<D, FMT>, dim3(z.W), dim3(256), st, a, z);
     if (e != hipSuccess) return e;
   }
-  return launch_kernel(attn_decode_join_kernel<D>, dim3(z.R * z.Hq), dim3(256), st, a, z);
+  return launch_kernel(attn_decode_join_kernel<D>, dim3(z.R * z.Hq), dim3(512), st, a, z);
 }
 
 }  // namespace

@@ -168,3 +168,20 @@ def test_decode_blocks_of_zeros_beside_others():
         x[table[2, 0]], s[table[2, 0]] = 0, 2.0 ** -100
     note("decode zeros")
     check(torch, q, kc, vc, ks, vs, table, lens)
+
+
+@pytest.mark.parametrize("lens", [[40], [5000, 40, 0]])
+def test_decode_queries_that_are_not_finite(lens):
+    """A head whose query is not finite gets NaN, and no other head does; a request without tokens gets zeros even so."""
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    q, kc, vc, ks, vs, table, lens = make(torch, np.random.default_rng(12), lens, 4, 2, 64, 16, "int8")
+    dev = [x.cuda() for x in (kc, vc, ks, vs)] + [ints(torch, table), ints(torch, lens)]
+    good, _ = gdn.attn_decode(q.cuda(), *dev)
+    for bad in (float("nan"), float("inf")):
+        x = q.clone()
+        x[:, 2, 7] = bad
+        out, lse = gdn.attn_decode(x.cuda(), *dev)
+        some = torch.from_numpy(lens > 0)
+        assert out[some][:, 2].isnan().all() and lse[some][:, 2].isnan().all()
+        assert torch.equal(out[:, [0, 1, 3]], good[:, [0, 1, 3]]) and (out[~some] == 0).all()
