@@ -435,24 +435,27 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
 // Joins the shares of one (request, query head), in the order of the tokens;
 // heads that one workgroup covered are done already.  Requests without tokens
 // get their zeros here.
-template <int D> __global__ __launch_bounds__(512) void attn_decode_join_kernel(DecodeArgs a, DecodeSizes z) {
-  constexpr int NT = 512, NP = NT / (D / 4);  // shares taken side by side
-  __shared__ float sum[NP][D], ls[NP], weight[most_shares(D)], part_l[most_shares(D)], red[NT / 64];
+// DS workgroups of C = D / DS columns each.
+template <int D, int DS> __global__ __launch_bounds__(128 * (DS == 1 ? 2 : 4)) void attn_decode_join_kernel(DecodeArgs a, DecodeSizes z) {
+  constexpr int NT = DS == 1 ? 256 : 512, C = D / DS, NP = NT / (C / 4);  // shares taken side by side
+  __shared__ float sum[NT / 64][C], ls[NT / 64], weight[most_shares(D)], part_l[most_shares(D)], red[NT / 64];
   __shared__ int scan[2][NT / 64];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int r = blockIdx.x / z.Hq, hq = blockIdx.x % z.Hq, h = hq / z.G, in = hq - h * z.G, hh = h * z.NG + in / 16, col = in % 16;
+  const int x = blockIdx.x / DS, d0 = blockIdx.x % DS * C;
+  const int r = x / z.Hq, hq = x - r * z.Hq, h = hq / z.G, in = hq - h * z.G, hh = h * z.NG + in / 16, col = in % 16;
   const int n = tokens_of(a.seq_lens, r, z), nu = units_of(n), heads = z.Hkv * z.NG;
-  __bf16* out = static_cast<__bf16*>(a.out) + ((size_t)r * z.Hq + hq) * D;
+  __bf16* out = static_cast<__bf16*>(a.out) + ((size_t)r * z.Hq + hq) * D + d0;
+  const bool writes_lse = tid == 0 && d0 == 0 && a.lse;
   if (nu == 0) {
-    if (tid < D / 4) *reinterpret_cast<u32x2*>(out + 4 * tid) = u32x2{0u, 0u};
-    if (tid == 0 && a.lse) a.lse[(size_t)r * z.Hq + hq] = -INFINITY;
+    if (tid < C / 4) *reinterpret_cast<u32x2*>(out + 4 * tid) = u32x2{0u, 0u};
+    if (writes_lse) a.lse[(size_t)r * z.Hq + hq] = -INFINITY;
     return;
   }
   int all = 0, pre = 0;
   for (int i = tid; i < z.R; i += NT) {
-    const int x = units_of(tokens_of(a.seq_lens, i, z));
-    all += x;
-    pre += i < r ? x : 0;
+    const int nu_i = units_of(tokens_of(a.seq_lens, i, z));
+    all += nu_i;
+    pre += i < r ? nu_i : 0;
   }
 #pragma unroll
   for (int d = 32; d; d >>= 1) {
@@ -498,29 +501,35 @@ template <int D> __global__ __launch_bounds__(512) void attn_decode_join_kernel(
   for (int w = 0; w < NT / 64; ++w) M = fmaxf(M, red[w]);
   for (int i = tid; i < n_parts; i += NT) weight[i] = part_l[i] == 0.f ? 0.f : __builtin_amdgcn_exp2f(weight[i] - M);
   __syncthreads();
-  const int part = tid / (D / 4), d = 4 * (tid % (D / 4));
+  const int part = tid / (C / 4), d = 4 * (tid % (C / 4));
   f32x4 o = pipe::zero4();
   float L = 0.f;
 #pragma unroll 4
   for (int i = part; i < n_parts; i += NP) {
     const float e = weight[i];
     L += e * part_l[i];
-    if (e != 0.f) o += *reinterpret_cast<const f32x4*>(at(i0 + i) + col * D + d) * e;
+    if (e != 0.f) o += *reinterpret_cast<const f32x4*>(at(i0 + i) + col * D + d0 + d) * e;
   }
-  *reinterpret_cast<f32x4*>(&sum[part][d]) = o;
-  if (d == 0) ls[part] = L;
+#pragma unroll
+  for (int x = C / 4; x < 64; x <<= 1) {  // over the shares of a wave
+    L += __shfl_xor(L, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], x);
+  }
+  if (lane < C / 4) *reinterpret_cast<f32x4*>(&sum[wave][d]) = o;
+  if (lane == 0) ls[wave] = L;
   __syncthreads();
-  if (tid < D / 4) {
+  if (tid < C / 4) {
     L = 0.f;
     o = pipe::zero4();
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      L += ls[p];
-      o += *reinterpret_cast<const f32x4*>(&sum[p][4 * tid]);
+    for (int w = 0; w < NT / 64; ++w) {
+      L += ls[w];
+      o += *reinterpret_cast<const f32x4*>(&sum[w][4 * tid]);
     }
     o *= L == 0.f ? 0.f : 1.f / L;
     *reinterpret_cast<u32x2*>(out + 4 * tid) = pipe::cvt4(o);
-    if (tid == 0 && a.lse) a.lse[(size_t)r * z.Hq + hq] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
+    if (writes_lse) a.lse[(size_t)r * z.Hq + hq] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
   }
 }
 
@@ -548,7 +557,10 @@ template <int D, int FMT> hipError_t launch(const DecodeArgs& a, const DecodeSiz
     const hipError_t e = launch_kernel(attn_decode_kernel<D, FMT>, dim3(z.W), dim3(256), st, a, z);
     if (e != hipSuccess) return e;
   }
-  return launch_kernel(attn_decode_join_kernel<D>, dim3(z.R * z.Hq), dim3(512), st, a, z);
+  // few rows: a row's columns over four workgroups, so that a long request's
+  // many shares are read by more of them
+  if (z.R * z.Hq < 256) return launch_kernel(attn_decode_join_kernel<D, 4>, dim3(z.R * z.Hq * 4), dim3(512), st, a, z);
+  return launch_kernel(attn_decode_join_kernel<D, 1>, dim3(z.R * z.Hq), dim3(256), st, a, z);
 }
 
 }  // namespace

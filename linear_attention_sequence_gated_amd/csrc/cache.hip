@@ -200,9 +200,10 @@ __global__ __launch_bounds__(kThreads) void block_tables_kernel(TablesArgs a) {
 // the new scale, code = rne(code s_old / s).  The codes are the rounding of
 // 32-bit products (by the reciprocal and by the ratio).
 //
-// One wave per run (the tokens of one call that fall into one block), head and
-// tensor: a run's rows fit its registers (NL 16-byte pieces per lane), so that
-// they are read once and the largest magnitude needs no other wave.
+// One workgroup per run (the tokens of one call that fall into one block), head
+// and tensor: a run's rows fit the registers of its four waves (NL 16-byte
+// pieces per lane), so that they are read once and the largest magnitude takes
+// one exchange through LDS.  Bound by HBM: 2 bytes read and 1 written per value.
 template <int FMT> constexpr float kMost = FMT == GDN_CACHE_I8 ? 127.f : 448.f;
 constexpr float kLeastScale = 7.88860905e-31f;   // 2^-100: a block of zeros keeps a finite reciprocal
 constexpr float kMostAbs = 3.38953139e38f;       // infinities count as the largest bf16 value
@@ -240,35 +241,33 @@ template <int FMT> __device__ __forceinline__ void decode4(unsigned w, float (&y
 
 template <int FMT, int D, int NL>
 __device__ __forceinline__ void append_run(const __hip_bfloat16* __restrict__ x, long long stride, char* tile,
-                                           float* scale, int first, int n) {
-  constexpr int LR = D / 8, RL = 64 / LR;  // lanes per row, rows per load
-  const int lane = threadIdx.x & 63, row = lane / LR, col = lane % LR;
+                                           float* scale, int first, int n, float* red) {
+  constexpr int LR = D / 8, RL = 256 / LR;  // lanes per row, rows per load of the workgroup
+  const int t = threadIdx.x, row = t / LR, col = t % LR;
   u32x4 w[NL];
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
     w[i] = u32x4{0u, 0u, 0u, 0u};
-    if (i * RL < n) {
-      const int r = i * RL + row;
-      if (r < n) w[i] = *reinterpret_cast<const u32x4*>(x + (long long)r * stride + 8 * col);
-    }
+    const int r = i * RL + row;
+    if (r < n) w[i] = *reinterpret_cast<const u32x4*>(x + (long long)r * stride + 8 * col);
   }
   const float old = first ? *scale : 0.f;
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    if (i * RL < n) {
+  for (int i = 0; i < NL; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(lo_f(w[i][e])), fabsf(hi_f(w[i][e]))));
-    }
-  }
+    for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(lo_f(w[i][e])), fabsf(hi_f(w[i][e]))));
 #pragma unroll
   for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  if ((t & 63) == 0) red[t >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   const float s = fmaxf(fmaxf(old, fminf(top, kMostAbs) * (1.f / kMost<FMT>)), kLeastScale);
   const float inv = 1.f / s;
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
     const int r = i * RL + row;
-    if (i * RL < n && r < n) {
+    if (r < n) {
       unsigned c[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -281,7 +280,7 @@ __device__ __forceinline__ void append_run(const __hip_bfloat16* __restrict__ x,
   }
   if (first && s != old) {
     const float ratio = old / s;
-    for (int o = lane * 16; o < first * D; o += 64 * 16) {
+    for (int o = t * 16; o < first * D; o += 256 * 16) {
       u32x4 c = *reinterpret_cast<const u32x4*>(tile + o);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -294,59 +293,71 @@ __device__ __forceinline__ void append_run(const __hip_bfloat16* __restrict__ x,
       *reinterpret_cast<u32x4*>(tile + o) = c;
     }
   }
-  if (lane == 0) *scale = s;
+  if (t == 0) *scale = s;
 }
 
-// A wave looks at `window` consecutive slots (a power of two, at most 64) and
-// writes the runs that begin there.
+// A workgroup looks at `window` consecutive slots (a power of two, at most 64)
+// and writes the runs that begin there, for one head of one tensor.
 template <int FMT, int D, int NL> __global__ __launch_bounds__(256) void cache_append_kernel(AppendArgs a, int window) {
+  __shared__ float red[2][4];
   const int lane = threadIdx.x & 63;
-  const long long unit = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
-  const int which = unit & 1, h = (int)((unit >> 1) % a.H);
-  const long long t0 = (unit >> 1) / a.H * window;
-  if (t0 >= a.T) return;
+  const int unit = blockIdx.x, which = unit & 1, h = (unit >> 1) % a.H;
+  const long long t0 = (long long)((unit >> 1) / a.H) * window;
   const int sh = __builtin_ctz(a.bt), slots = a.num_blocks << sh;
   auto slot_at = [&](long long t) {
     const int s = t >= 0 && t < a.T ? a.slot_map[t] : -1;
     return s >= 0 && s < slots ? s : -1;
   };
-  const int mine = lane < window ? slot_at(t0 + lane) : -1;
-  const int before = lane < window ? slot_at(t0 + lane - 1) : -1;
-  const bool begins = mine >= 0 && (before < 0 || before != mine - 1 || (mine & (a.bt - 1)) == 0);
+  // slots t0 - 1 .. t0 + 126 or so: this lane's, the one before it, and 64 on
+  const int mine = slot_at(t0 + lane), far = slot_at(t0 + 64 + lane);
+  int before = __shfl_up(mine, 1);
+  if (lane == 0) before = slot_at(t0 - 1);
+  const bool begins = lane < window && mine >= 0 && (before != mine - 1 || (mine & (a.bt - 1)) == 0);
   unsigned long long todo = __ballot(begins);
-  while (todo) {
+  for (int k = 0; todo; k ^= 1) {
     const int i = __builtin_ctzll(todo);
     todo &= todo - 1;
     const int s = __builtin_amdgcn_readlane(mine, i), first = s & (a.bt - 1);
-    // its length: the slots that follow one another, up to the block's end
-    const unsigned long long m0 = __ballot(slot_at(t0 + i + lane) == s + lane && first + lane < a.bt);
-    int n = m0 == ~0ull ? 64 : __builtin_ctzll(~m0);
-    if (n == 64 && first + 64 < a.bt) {
-      const unsigned long long m1 =
-          __ballot(slot_at(t0 + i + 64 + lane) == s + 64 + lane && first + 64 + lane < a.bt);
-      n = m1 == ~0ull ? 128 : 64 + __builtin_ctzll(~m1);
+    // its length: the slots that follow one another, up to the block's end; 128
+    // at most, of which the last may lie past the slots at hand
+    const unsigned long long near_ = __ballot(lane >= i && mine == s + lane - i && first + lane - i < a.bt) >> i;
+    const int in_near = 64 - i;
+    int n = ~near_ ? __builtin_ctzll(~near_) : 64;
+    if (n >= in_near) {
+      n = in_near;
+      const unsigned long long m = __ballot(far == s + in_near + lane && first + in_near + lane < a.bt);
+      const int more = ~m ? __builtin_ctzll(~m) : 64;
+      n += more;
+      if (more == 64 && first + n < a.bt) {
+        const unsigned long long l = __ballot(slot_at(t0 + 128 + lane) == s + n + lane && first + n + lane < a.bt);
+        n += ~l ? __builtin_ctzll(~l) : 64;
+      }
     }
     const long long tile = (long long)(s >> sh) * a.H + h;
     const __hip_bfloat16* x = static_cast<const __hip_bfloat16*>(which ? a.v : a.k);
     const long long stride = which ? a.vs : a.ks;
     append_run<FMT, D, NL>(x + (t0 + i) * stride + (long long)h * D, stride,
                            static_cast<char*>(which ? a.v_cache : a.k_cache) + tile * a.bt * D,
-                           (which ? a.v_scale : a.k_scale) + tile, first, n);
+                           (which ? a.v_scale : a.k_scale) + tile, first, n, red[k]);
   }
 }
 
 template <int FMT, int D> hipError_t append_nl(const AppendArgs& a) {
-  const int window = a.T <= 2048 ? 1 : 16;
-  const long long units = ((long long)a.T + window - 1) / window * a.H * 2;
-  const dim3 grid((unsigned)((units + 3) / 4)), block(256);
+  // A window of one slot spreads single tokens best; a wider one keeps the
+  // workgroups that find nothing to begin from being the most of the work.
+  int window = 1;
+  while (window < 64 && (long long)(a.T + window - 1) / window * a.H * 2 > 8192) window *= 2;
+  const dim3 grid((unsigned)((a.T + window - 1) / window * a.H * 2)), block(256);
   hipStream_t st = static_cast<hipStream_t>(a.stream);
-  switch (a.bt * D / 512) {
+  switch (a.bt * D / 2048) {  // loads of 256 lanes x 8 values to a block
+    case 0:
+    case 1: return launch_kernel(cache_append_kernel<FMT, D, 1>, grid, block, st, a, window);
     case 2: return launch_kernel(cache_append_kernel<FMT, D, 2>, grid, block, st, a, window);
     case 4: return launch_kernel(cache_append_kernel<FMT, D, 4>, grid, block, st, a, window);
-    case 8: return launch_kernel(cache_append_kernel<FMT, D, 8>, grid, block, st, a, window);
-    case 16: return launch_kernel(cache_append_kernel<FMT, D, 16>, grid, block, st, a, window);
-    default: return launch_kernel(cache_append_kernel<FMT, D, 32>, grid, block, st, a, window);
+    default:
+      if constexpr (D == 128) return launch_kernel(cache_append_kernel<FMT, D, 8>, grid, block, st, a, window);
   }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
