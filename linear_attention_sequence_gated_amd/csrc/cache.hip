@@ -54,8 +54,7 @@ __device__ __forceinline__ bool granted(const Req& q, long long cu, long long of
 
 __global__ __launch_bounds__(kThreads) void block_tables_kernel(TablesArgs a) {
   __shared__ long long red[2][kThreads / 64];
-  __shared__ long long cus[kRows + 1], offs[kRows];
-  __shared__ int held[kRows], have[kRows], ok[kRows];
+  __shared__ int cus[kRows + 1], offs[kRows], held[kRows], have[kRows], ok[kRows];
   const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
   const int groups = (a.R + kRows - 1) / kRows;
   if ((int)blockIdx.x < groups) {
@@ -94,12 +93,12 @@ __global__ __launch_bounds__(kThreads) void block_tables_kernel(TablesArgs a) {
       const long long cu = st + pt - q.tokens, off = sb + pb - q.need;
       const bool g = here && granted(q, cu, off, a);
       if (lane < kRows) {
-        cus[lane] = cu < a.T ? cu : a.T;
-        offs[lane] = off;
+        cus[lane] = cu < a.T ? (int)cu : a.T;
+        offs[lane] = (int)off;  // used where granted: below n_free
         held[lane] = n;
         have[lane] = (int)(((long long)n + a.bt - 1) >> __builtin_ctz(a.bt));
         ok[lane] = g;
-        if (lane == kRows - 1) cus[kRows] = st + pt < a.T ? st + pt : a.T;
+        if (lane == kRows - 1) cus[kRows] = st + pt < a.T ? (int)(st + pt) : a.T;
       }
       if (here) {
         a.cu_seqlens[r + 1] = (int)(st + pt < a.T ? st + pt : a.T);
@@ -111,35 +110,65 @@ __global__ __launch_bounds__(kThreads) void block_tables_kernel(TablesArgs a) {
     // fresh entries of the table rows: one wave per request
     for (int i = wave; i < kRows && r0 + i < a.R; i += kThreads / 64) {
       if (!ok[i]) continue;
-      const int m = (int)(cus[i + 1] - cus[i]);
+      const int m = cus[i + 1] - cus[i];
       const int all = (int)(((long long)held[i] + m + a.bt - 1) >> __builtin_ctz(a.bt));
       int* row = a.block_table + (size_t)(r0 + i) * a.width;
       for (int c = have[i] + lane; c < all; c += 64) row[c] = a.free_blocks[offs[i] + c - have[i]];
     }
     // slots of the tokens of these requests: a contiguous stretch of the map
     const int sh = __builtin_ctz(a.bt);
-    for (long long x = cus[0] + t; x < cus[kRows]; x += kThreads) {
-      int i = 0;
+    const int end = cus[kRows];
+    for (int base = cus[0]; base < end; base += 4 * kThreads) {
+      int slot[4];
 #pragma unroll
-      for (int s = kRows / 2; s; s >>= 1)
-        if (cus[i + s] <= x) i += s;
-      int slot = -1;
-      if (ok[i]) {
-        const int pos = held[i] + (int)(x - cus[i]), c = pos >> sh;
-        const int id = c < have[i] ? a.block_table[(size_t)(r0 + i) * a.width + c] : a.free_blocks[offs[i] + c - have[i]];
-        if (id >= 0 && id < a.num_blocks) slot = (id << sh) + (pos & (a.bt - 1));
+      for (int k = 0; k < 4; ++k) {  // four at a time, for their reads to overlap
+        const int x = base + k * kThreads + t;
+        int i = 0;
+#pragma unroll
+        for (int s = kRows / 2; s; s >>= 1)
+          if (cus[i + s] <= x) i += s;
+        slot[k] = -1;
+        if (x < end && ok[i]) {
+          const int pos = held[i] + (x - cus[i]), c = pos >> sh;
+          const int id = c < have[i] ? a.block_table[(size_t)(r0 + i) * a.width + c] : a.free_blocks[offs[i] + c - have[i]];
+          if (id >= 0 && id < a.num_blocks) slot[k] = (id << sh) + (pos & (a.bt - 1));
+        }
       }
-      a.slot_map[x] = slot;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (base + k * kThreads + t < end) a.slot_map[base + k * kThreads + t] = slot[k];
     }
     return;
   }
-  // totals: rounds of kThreads requests, the running sums carried along
+  // totals: rounds of kPer requests per thread, the running sums carried along
+  constexpr int kPer = 16;
   long long ct = 0, cb = 0, used = 0, refused = 0;
-  for (int base = 0; base < a.R; base += kThreads) {
-    const int r = base + t;
-    const bool here = r < a.R;
-    const Req q = request(here ? a.seq_lens[r] : 0, here ? a.new_lens[r] : 0, a);
-    long long pt = q.tokens, pb = q.need;
+  for (int base = 0; base < a.R; base += kThreads * kPer) {
+    int n[kPer], m[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; i += 4) {
+      const int r = base + t * kPer + i;
+      const bool four = r + 3 < a.R;
+      const int4 x = four ? *reinterpret_cast<const int4*>(a.seq_lens + r) : make_int4(0, 0, 0, 0);
+      const int4 y = four ? *reinterpret_cast<const int4*>(a.new_lens + r) : make_int4(0, 0, 0, 0);
+      n[i] = x.x, n[i + 1] = x.y, n[i + 2] = x.z, n[i + 3] = x.w;
+      m[i] = y.x, m[i + 1] = y.y, m[i + 2] = y.z, m[i + 3] = y.w;
+      if (!four)
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          if (r + j < a.R) {
+            n[i + j] = a.seq_lens[r + j];
+            m[i + j] = a.new_lens[r + j];
+          }
+    }
+    long long mt = 0, mb = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const Req q = request(n[i], m[i], a);
+      mt += q.tokens;
+      mb += q.need;
+    }
+    long long pt = mt, pb = mb;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const long long x = __shfl_up(pt, d), y = __shfl_up(pb, d);
@@ -153,20 +182,27 @@ __global__ __launch_bounds__(kThreads) void block_tables_kernel(TablesArgs a) {
       red[1][wave] = pb;
     }
     __syncthreads();
-    long long bt_ = ct, bb = cb;
+    pt += ct - mt;
+    pb += cb - mb;
 #pragma unroll
     for (int w = 0; w < kThreads / 64; ++w) {
       if (w < wave) {
-        bt_ += red[0][w];
-        bb += red[1][w];
+        pt += red[0][w];
+        pb += red[1][w];
       }
       ct += red[0][w];
       cb += red[1][w];
     }
     __syncthreads();
-    if (here) {
-      if (!granted(q, bt_ + pt - q.tokens, bb + pb - q.need, a)) ++refused;
-      else if (q.need) used = bb + pb;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const Req q = request(n[i], m[i], a);
+      if (base + t * kPer + i < a.R) {
+        if (!granted(q, pt, pb, a)) ++refused;
+        else if (q.need) used = pb + q.need;
+      }
+      pt += q.tokens;
+      pb += q.need;
     }
   }
 #pragma unroll

@@ -44,7 +44,7 @@ def run_tables(torch, held, new, table, free, bt, nb, T):
 
 @pytest.mark.parametrize("R,bt,longest,prompts,pad", [
     (1, 16, 0, 0, 0), (1, 16, 15, 1, 3), (1, 64, 1, 0, 5), (5, 32, 100, 2, 0), (16, 16, 64, 0, 1), (17, 128, 300, 5, 2),
-    (64, 16, 33, 64, 700), (255, 64, 500, 3, 0), (257, 32, 129, 20, 1), (1000, 16, 400, 10, 300)])
+    (64, 16, 33, 64, 700), (255, 64, 500, 3, 0), (257, 32, 129, 20, 1), (1000, 16, 400, 10, 300), (4095, 16, 90, 9, 3), (4097, 32, 90, 9, 3), (9001, 16, 40, 3, 0)])
 def test_tables(R, bt, longest, prompts, pad):
     torch = torch_dev()
     rng = np.random.default_rng(R + bt)
@@ -155,6 +155,22 @@ def test_append_many_tokens(kind):
     _, slots, *_ = ref.block_tables(held, new, table, free, 64, nb, T)
     note(f"append many {kind} T{T}")
     check_append(torch, rng, rng.standard_normal((T, 2, 64)), slots, nb, 1, 64, 64, kind)
+
+
+@pytest.mark.parametrize("T,H", [(5000, 1), (6000, 3), (9000, 8)])
+def test_append_runs_of_whole_blocks(T, H):
+    """Blocks of 128 tokens whose rows begin anywhere among the slots that a workgroup looks at."""
+    torch = torch_dev()
+    rng = np.random.default_rng(T)
+    new, held = [], []
+    while sum(new) < T:
+        new.append(int(rng.choice([1, 2, 5, 127, 128, 129, 256, 300])))
+        held.append(int(rng.choice([0, 0, 1, 63, 64, 127])))
+    new, held = np.array(new), np.array(held)
+    table, free, nb = make_table(rng, held, new, 128)
+    _, slots, *_ = ref.block_tables(held, new, table, free, 128, nb, int(new.sum()))
+    note(f"append whole blocks T{T} H{H}")
+    check_append(torch, rng, rng.standard_normal((int(new.sum()), 2 * H, 64)), slots, nb, H, 128, 64, "int8")
 
 
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
