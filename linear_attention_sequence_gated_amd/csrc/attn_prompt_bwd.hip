@@ -129,10 +129,6 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
   }
   delta = sum_halves(delta);
   const float lse2 = a.lse[(size_t)hq * a.T + at] * kLog2e;
-  if (beg >= 0 && hl == 0) {
-    a.ws[(size_t)hq * a.T + row] = lse2;
-    a.ws[(size_t)(a.Hq + hq) * a.T + row] = delta;
-  }
 
   f32x16 dq[D / 32];
 #pragma unroll
@@ -149,6 +145,10 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
     sv.load(vt[buf], rows_rsrc(vp, a.vs, kv, n, D), wave);
   };
   const int from = beg - 4 * hl, upto = beg < 0 ? -8 : row - 4 * hl;  // the keys that the lane's row sees
+  // delta comes from the rounded output.  The ds of a row add up to zero, but for
+  // that rounding: what they add up to is its error, and the second launch gets
+  // delta without it.
+  float rest = 0.f;
   int dirty_lo = last, dirty_hi = 0;  // keys of tiles that held values that are not finite
   int buf = 0, kv = first;
   auto step = [&](auto masked_, const __bf16* K, const __bf16* V) {
@@ -168,6 +168,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
         const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -lse2));
         s[e] = p * (dp[e] - delta);
         if constexpr (MASKED) s[e] = where_seen<true>(s[e], seen, e);
+        rest += s[e];
       }
 #pragma unroll
       for (int b = 0; b < 2; ++b) add_columns<D>(dq, K, cb, 32 * n + 16 * b, operand(s, b));
@@ -201,9 +202,14 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
     step(std::false_type{}, kt[buf], vt[buf]);
   }
   edge(last);
-  const bool rest = beg < 0 && row < a.T && a.zero_rest;
-  if (beg >= 0 || rest)
-    store_rows<D>(static_cast<__bf16*>(a.grad_q) + (long long)row * a.gqs + (long long)hq * D, dq, rest ? 0.f : a.scale, hl);
+  const float off = sum_halves(rest);
+  if (beg >= 0 && hl == 0) {
+    a.ws[(size_t)hq * a.T + row] = lse2;
+    a.ws[(size_t)(a.Hq + hq) * a.T + row] = delta + off;
+  }
+  const bool outside = beg < 0 && row < a.T && a.zero_rest;
+  if (beg >= 0 || outside)
+    store_rows<D>(static_cast<__bf16*>(a.grad_q) + (long long)row * a.gqs + (long long)hq * D, dq, outside ? 0.f : a.scale, hl);
   if (dirty_hi && beg >= 0)  // a key that is not finite spoils the weights of all rows that see it
     spoil<D>(static_cast<__bf16*>(a.grad_q) + (long long)row * a.gqs + (long long)hq * D, kp, a.ks, max(beg, dirty_lo),
              min(row + 1, dirty_hi), true, hl);
