@@ -46,7 +46,7 @@ def _rows(t, name, shape, dev):
 
 def _call(dev, stream, fn, *args):
     """fn(*args, stream) with `dev` as the current device."""
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         s = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream)
     else:
         with torch.cuda.device(dev):
@@ -71,14 +71,10 @@ def block_tables(seq_lens, new_lens, block_table, free_blocks, block_tokens: int
     _dense(free_blocks, "free_blocks", (free_blocks.numel(),), _I32, dev)
     if tokens < 0:
         raise ValueError("block_tables: tokens is negative")
-    # one allocation, each part 16-byte aligned
-    a, b, c = -(-tokens // 4) * 4, (r + 4) // 4 * 4, -(-r // 4) * 4
-    buf = torch.empty(a + b + c + 2, dtype=_I32, device=dev)
-    slot_map, cu, after, used = buf[:tokens], buf[a:a + r + 1], buf[a + b:a + b + r], buf[a + b + c:]
-    p = buf.data_ptr()
+    slot_map, cu, after, used = (seq_lens.new_empty(n) for n in (tokens, r + 1, r, 2))
     _call(dev, stream, raw.load().gdn_block_tables, seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
-          free_blocks.data_ptr(), p, p + 4 * a, p + 4 * (a + b), p + 4 * (a + b + c), r, width, free_blocks.numel(),
-          block_tokens, num_blocks, tokens)
+          free_blocks.data_ptr(), slot_map.data_ptr(), cu.data_ptr(), after.data_ptr(), used.data_ptr(), r, width,
+          free_blocks.numel(), block_tokens, num_blocks, tokens)
     return slot_map, cu, after, used
 
 
@@ -131,16 +127,16 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, sc
     _dense(block_table, "block_table", (r, width), _I32, dev)
     _dense(seq_lens, "seq_lens", (r,), _I32, dev)
     if out is None:
-        out = torch.empty((r, hq, d), dtype=_BF16, device=dev)
+        out = q.new_empty((r, hq, d))
     else:
         _dense(out, "out", (r, hq, d), _BF16, dev)
     if lse is None:
-        lse = torch.empty((r, hq), dtype=_F32, device=dev)
+        lse = k_scale.new_empty((r, hq))
     else:
         _dense(lse, "lse", (r, hq), _F32, dev)
     lib = raw.load()
     if workspace is None:
-        workspace = torch.empty(_decode_workspace(r, hq, hkv, d, bt, width), dtype=torch.uint8, device=dev)
+        workspace = k_scale.new_empty(_decode_workspace(r, hq, hkv, d, bt, width) // 4)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous on the device of q")
     _call(dev, stream, lib.gdn_attn_decode, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),

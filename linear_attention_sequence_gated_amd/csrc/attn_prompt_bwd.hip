@@ -9,8 +9,8 @@
 // One launch by tiles of rows for dq (three products for a pair of tiles), one
 // by tiles of keys for dk and dv (four), each of which owns the sums it writes,
 // so that their order is fixed.  The probabilities are computed in both; the
-// first launch leaves lse (times log2 e) and delta in the workspace for the
-// second.  Where there are few keys to share out, the query heads of a key head
+// first launch leaves lse (times log2 e) and -delta, which the second's products
+// start from, in the workspace.  Where there are few keys to share out, the query heads of a key head
 // are shared out too, and a third launch adds their sums.
 #include "../../include/gdn.h"
 #include "gdn_attn.hpp"
@@ -205,7 +205,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
   const float off = sum_halves(rest);
   if (beg >= 0 && hl == 0) {
     a.ws[(size_t)hq * a.T + row] = lse2;
-    a.ws[(size_t)(a.Hq + hq) * a.T + row] = delta + off;
+    a.ws[(size_t)(a.Hq + hq) * a.T + row] = -(delta + off);
   }
   const bool outside = beg < 0 && row < a.T && a.zero_rest;
   if (beg >= 0 || outside)
@@ -288,11 +288,20 @@ template <int D> __global__ __launch_bounds__(256) void attn_dkv_sum_kernel(Prom
   }
 }
 
-// One wave to 32 keys, D = 64.
-template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(PromptBwdArgs a) {
+// One wave to 32 keys, rows in tiles of NR.  At D = 64 a wave holds K and V of
+// its keys as operands beside both accumulators (243 registers).  At D = 128
+// that would be 192 registers before the first score: V stays in LDS (VLDS),
+// which takes tiles of half as many rows, and every tile goes through the masked
+// body, since two bodies of this size take more registers than there are (237
+// with one; a bit mask per score costs less than a spill, whose reload waits for
+// the loads that stage the next tile).  4 x 2 heads of two waves sharing the work
+// of 32 keys, scores handed over through LDS, took 260 us where this takes 155
+// (13 documents of up to 1201 rows, 16 / 4 heads of 128).
+template <int D, int NW, int NR, bool VLDS> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(PromptBwdArgs a) {
   constexpr int BN = 32 * NW, NT = 64 * NW, KS = D / 16;
-  __shared__ __bf16 qt[2][kN * D], gt[2][kN * D];
-  __shared__ float lt[2][kN], dt[2][kN];
+  __shared__ __bf16 qt[2][NR * D], gt[2][NR * D];
+  __shared__ float lt[2][64], dt[2][64];
+  __shared__ __bf16 vt[VLDS ? BN * D : 8];
   __shared__ int begs[BN], ends[BN], window[kWindow], most[2][NW], bad[2][NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   // the first tiles of a long sequence meet the most rows
@@ -342,7 +351,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       k[ks] = *reinterpret_cast<const u32x4*>(kp + 16 * ks);
-      v[ks] = *reinterpret_cast<const u32x4*>(vp + 16 * ks);
+      if (!VLDS) v[ks] = *reinterpret_cast<const u32x4*>(vp + 16 * ks);
     }
   }
   int lowest = end, highest = end;  // the range of end over the wave's keys
@@ -358,13 +367,13 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) dk[i] = dv[i] = zero16();
   const int rb0 = row_base<D>(lane), cb0 = col_base<D>(lane);
-  Stage<D, kN, NW> sq, sg;
+  Stage<D, NR, NW> sq, sg;
   sq.init(a.qs, wave);
   sg.init(a.gos, wave);
   const __bf16* qp = static_cast<const __bf16*>(a.q);
   const __bf16* gp = static_cast<const __bf16*>(a.grad_out);
   auto stage = [&](int buf, int hq, int i0) {
-    const int n = min(kN, last - i0);
+    const int n = min(NR, last - i0);
     sq.load(qt[buf], rows_rsrc(qp + (long long)hq * D, a.qs, i0, n, D), wave);
     sg.load(gt[buf], rows_rsrc(gp + (long long)hq * D, a.gos, i0, n, D), wave);
     if (wave == 0) stage_words(lt[buf], pipe::make_rsrc(a.ws + (size_t)hq * a.T + i0, n * 4));
@@ -377,24 +386,29 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
     const int rb = fresh(rb0), cb = fresh(cb0);
     const __bf16 *Q = qt[buf], *O = gt[buf];
     const int from = key - i1 - 4 * hl, upto = end - 1 - i1 - 4 * hl;  // the rows that see the lane's key
-#pragma unroll MASKED ? 1 : 2
-    for (int n = 0; n < 2; ++n) {
+#pragma unroll MASKED ? 1 : NR / 32
+    for (int n = 0; n < NR / 32; ++n) {
       const unsigned seen = bits(from - 32 * n, upto - 32 * n);
-      f32x16 s = zero16(), dp = zero16();
+      f32x16 s = zero16(), dp;
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        s = mma(row_frag<D>(Q, rb, 32 * n, ks), k[ks], s);
-        dp = mma(row_frag<D>(O, rb, 32 * n, ks), v[ks], dp);
+      for (int ks = 0; ks < KS; ++ks) s = mma(row_frag<D>(Q, rb, 32 * n, ks), k[ks], s);
+#pragma unroll
+      for (int e4 = 0; e4 < 4; ++e4) {
+        const f32x4 d = *reinterpret_cast<const f32x4*>(&dt[buf][32 * n + 8 * e4 + 4 * hl]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dp[4 * e4 + j] = d[j];
       }
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        dp = mma(row_frag<D>(O, rb, 32 * n, ks), VLDS ? row_frag<D>(vt, rb, 32 * wave, ks) : v[ks], dp);
 #pragma unroll
       for (int e4 = 0; e4 < 4; ++e4) {
         const f32x4 l = *reinterpret_cast<const f32x4*>(&lt[buf][32 * n + 8 * e4 + 4 * hl]);
-        const f32x4 d = *reinterpret_cast<const f32x4*>(&dt[buf][32 * n + 8 * e4 + 4 * hl]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int e = 4 * e4 + j;
           s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -l[j]));
-          dp[e] = s[e] * (dp[e] - d[j]);
+          dp[e] = s[e] * dp[e];
           if constexpr (MASKED) {
             s[e] = where_seen<true>(s[e], seen, e);
             dp[e] = where_seen<true>(dp[e], seen, e);
@@ -408,33 +422,40 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
       }
     }
   };
+  if constexpr (VLDS) {
+    Stage<D, BN, NW> sv;
+    sv.init(a.vs, wave);
+    sv.load(vt, rows_rsrc(static_cast<const __bf16*>(a.v) + (long long)kvh * D, a.vs, r0, min(BN, a.T - r0), D), wave);
+  }
   stage(0, h0, r0);
   int buf = 0;
   for (int head = 0; head < heads; ++head) {
     int i1 = r0;
     auto next = [&] {
-      const bool masked = i1 < r0 + BN - 1 || i1 + kN > soonest;  // for some wave
+      const bool masked = i1 < r0 + BN - 1 || i1 + NR > soonest;  // for some wave
       if (masked) {
         wait_staged();
-        const bool q_ok = Stage<D, kN, NW>::scrub(qt[buf], wave), g_ok = Stage<D, kN, NW>::scrub(gt[buf], wave);
+        const bool q_ok = Stage<D, NR, NW>::scrub(qt[buf], wave), g_ok = Stage<D, NR, NW>::scrub(gt[buf], wave);
         if (lane == 0) bad[buf][wave] = !(q_ok && g_ok);
       }
       staged_barrier();
       if (masked && !all_clean(bad[buf])) dirty = true;
-      if (i1 + kN < last) stage(buf ^ 1, h0 + head, i1 + kN);
+      if (i1 + NR < last) stage(buf ^ 1, h0 + head, i1 + NR);
       else if (head + 1 < heads) stage(buf ^ 1, h0 + head + 1, r0);
     };
     // tiles of which some row misses some key, at both ends, and those between
     auto edge = [&](int stop) {
-      for (; i1 < stop; i1 += kN, buf ^= 1) {
+      for (; i1 < stop; i1 += NR, buf ^= 1) {
         next();
-        if (i1 + kN - 1 >= w0 && i1 < highest) step(std::true_type{}, buf, i1);
+        if (i1 + NR - 1 >= w0 && i1 < highest) step(std::true_type{}, buf, i1);
       }
     };
-    edge(min(w0 + 31, last));
-    for (; i1 + kN <= lowest; i1 += kN, buf ^= 1) {
-      next();
-      step(std::false_type{}, buf, i1);
+    if constexpr (!VLDS) {
+      edge(min(w0 + 31, last));
+      for (; i1 + NR <= lowest; i1 += NR, buf ^= 1) {
+        next();
+        step(std::false_type{}, buf, i1);
+      }
     }
     edge(last);
   }
@@ -444,186 +465,6 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
     spoil_grad<D>(a, sh, false, key, end, hl);
     spoil_grad<D>(a, sh, true, key, end, hl);
   }
-}
-
-// Two waves to 32 keys, D = 128: one computes the scores and dv, the other
-// do . v and dk.  Either holds one operand and one accumulator for its keys (96
-// registers, where one wave for both would need 192 before its first score and
-// spills), both run the same code on Q and dO in turned roles, and all that
-// passes between them are the probabilities, through LDS, lane by lane, in
-// float32.
-template <int D, int NP> __global__ __launch_bounds__(128 * NP, 2) void attn_dkv_pair_kernel(PromptBwdArgs a) {
-  constexpr int BN = 32 * NP, NW = 2 * NP, NT = 64 * NW, KS = D / 16;
-  __shared__ __bf16 qt[2][kN * D], gt[2][kN * D];
-  __shared__ float lt[2][kN], dt[2][kN];
-  __shared__ f32x4 hand[NP][8][64];
-  __shared__ int begs[BN], ends[BN], window[kWindow], most[2][NW], bad[2][NW];
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
-  const int pair = wave % NP;
-  const bool second = wave >= NP;  // do . v and dk
-  // the first tiles of a long sequence meet the most rows
-  Share sh = share_of(a);
-  if (a.keys_by_length)
-    sh.tile = tile_by_length<BN, NT, true>(a.cu, a.R, a.T, (a.T + BN - 1) / BN, sh.tile, window, reinterpret_cast<int*>(qt));
-  const int r0 = sh.tile * BN, kvh = sh.kvh, h0 = sh.h0, heads = sh.heads;
-
-  find_rows<BN, NT>(a.cu, a.R, a.T, r0, window, begs, ends, [] {});
-  int last = -1, soonest = a.T;  // the rows behind the last that attend to the tile's keys: the most, the least
-  for (int i = tid; i < BN; i += NT) {
-    last = max(last, ends[i]);
-    soonest = min(soonest, ends[i]);
-  }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) {
-    last = max(last, __shfl_xor(last, d));
-    soonest = min(soonest, __shfl_xor(soonest, d));
-  }
-  if (lane == 0) {
-    most[0][wave] = last;
-    most[1][wave] = soonest;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    last = max(last, most[0][w]);
-    soonest = min(soonest, most[1][w]);
-  }
-  last = __builtin_amdgcn_readfirstlane(last);
-  soonest = __builtin_amdgcn_readfirstlane(soonest);
-  if (last < 0) {
-    if (a.zero_rest && a.shares == 1) {
-      zero_rows<D>(static_cast<__bf16*>(a.grad_k) + (long long)kvh * D, a.gks, r0, min(BN, a.T - r0), NT);
-      zero_rows<D>(static_cast<__bf16*>(a.grad_v) + (long long)kvh * D, a.gvs, r0, min(BN, a.T - r0), NT);
-    }
-    return;
-  }
-
-  const int w0 = r0 + pair * 32, key = w0 + (lane & 31), end = ends[key - r0];
-  const float c = a.scale * kLog2e;
-  u32x4 kv[KS];
-  {
-    const __bf16* src = static_cast<const __bf16*>(second ? a.v : a.k) + (long long)min(key, a.T - 1) * (second ? a.vs : a.ks) +
-                        (long long)kvh * D + 8 * hl;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) kv[ks] = *reinterpret_cast<const u32x4*>(src + 16 * ks);
-  }
-  int lowest = end, highest = end;  // the range of end over the pair's keys
-#pragma unroll
-  for (int d = 32; d; d >>= 1) {
-    lowest = min(lowest, __shfl_xor(lowest, d));
-    highest = max(highest, __shfl_xor(highest, d));
-  }
-  lowest = __builtin_amdgcn_readfirstlane(lowest);
-  highest = __builtin_amdgcn_readfirstlane(highest);
-
-  f32x16 acc[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) acc[i] = zero16();
-  const int rb0 = row_base<D>(lane), cb0 = col_base<D>(lane);
-  const __bf16* qp = static_cast<const __bf16*>(a.q);
-  const __bf16* gp = static_cast<const __bf16*>(a.grad_out);
-  // Q is staged by the first waves, dO by the second
-  Stage<D, kN, NP> st;
-  st.init(second ? a.gos : a.qs, pair);
-  auto stage = [&](int buf, int hq, int i0) {
-    const int n = min(kN, last - i0);
-    if (second) st.load(gt[buf], rows_rsrc(gp + (long long)hq * D, a.gos, i0, n, D), pair);
-    else st.load(qt[buf], rows_rsrc(qp + (long long)hq * D, a.qs, i0, n, D), pair);
-    if (wave == 0) stage_words(lt[buf], pipe::make_rsrc(a.ws + (size_t)hq * a.T + i0, n * 4));
-    if (wave == NP) stage_words(dt[buf], pipe::make_rsrc(a.ws + (size_t)(a.Hq + hq) * a.T + i0, n * 4));
-  };
-  // the two halves of a tile of rows that the pair's keys may be seen by
-  f32x16 s[2];
-  auto scores = [&](auto masked_, int buf, int i1) {
-    constexpr bool MASKED = decltype(masked_)::value;
-    const __bf16* X = second ? gt[buf] : qt[buf];
-    const int rb = fresh(rb0);
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      s[n] = zero16();
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) s[n] = mma(row_frag<D>(X, rb, 32 * n, ks), kv[ks], s[n]);
-    }
-    if (second) return;
-    const int from = key - i1 - 4 * hl, upto = end - 1 - i1 - 4 * hl;  // the rows that see the lane's key
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int e4 = 0; e4 < 4; ++e4) {
-        const f32x4 l = *reinterpret_cast<const f32x4*>(&lt[buf][32 * n + 8 * e4 + 4 * hl]);
-        f32x4 p;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][4 * e4 + j], c, -l[j]));
-          if constexpr (MASKED) p[j] = where_seen<true>(p[j], bits(from - 32 * n, upto - 32 * n), 4 * e4 + j);
-          s[n][4 * e4 + j] = p[j];
-        }
-        hand[pair][4 * n + e4][lane] = p;
-      }
-  };
-  auto products = [&](auto masked_, int buf, int i1) {
-    constexpr bool MASKED = decltype(masked_)::value;
-    const int cb = fresh(cb0);
-    const __bf16* Y = second ? qt[buf] : gt[buf];
-    if (second) {
-      const int from = key - i1 - 4 * hl, upto = end - 1 - i1 - 4 * hl;
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e4 = 0; e4 < 4; ++e4) {
-          const f32x4 p = hand[pair][4 * n + e4][lane];
-          const f32x4 d = *reinterpret_cast<const f32x4*>(&dt[buf][32 * n + 8 * e4 + 4 * hl]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float x = p[j] * (s[n][4 * e4 + j] - d[j]);
-            if constexpr (MASKED) x = where_seen<true>(x, bits(from - 32 * n, upto - 32 * n), 4 * e4 + j);
-            s[n][4 * e4 + j] = x;
-          }
-        }
-    }
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) add_columns<D>(acc, Y, cb, 32 * n + 16 * b, operand(s[n], b));
-  };
-  bool dirty = false;  // a tile held values that are not finite
-  stage(0, h0, r0);
-  int buf = 0;
-  for (int head = 0; head < heads; ++head) {
-    int i1 = r0;
-    auto next = [&] {
-      const bool masked = i1 < r0 + BN - 1 || i1 + kN > soonest;  // for some wave
-      if (masked) {
-        wait_staged();
-        const bool ok = Stage<D, kN, NP>::scrub(second ? gt[buf] : qt[buf], pair);
-        if (lane == 0) bad[buf][wave] = !ok;
-      }
-      staged_barrier();
-      if (masked && !all_clean(bad[buf])) dirty = true;
-      if (i1 + kN < last) stage(buf ^ 1, h0 + head, i1 + kN);
-      else if (head + 1 < heads) stage(buf ^ 1, h0 + head + 1, r0);
-    };
-    // tiles of which some row misses some key, at both ends, and those between
-    auto edge = [&](int stop) {
-      for (; i1 < stop; i1 += kN, buf ^= 1) {
-        const bool met = i1 + kN - 1 >= w0 && i1 < highest;
-        next();
-        if (met) scores(std::true_type{}, buf, i1);
-        pipe::stage_barrier();
-        if (met) products(std::true_type{}, buf, i1);
-      }
-    };
-    edge(min(w0 + 31, last));
-    for (; i1 + kN <= lowest; i1 += kN, buf ^= 1) {
-      next();
-      scores(std::false_type{}, buf, i1);
-      pipe::stage_barrier();
-      products(std::false_type{}, buf, i1);
-    }
-    edge(last);
-  }
-  write_grad<D>(a, sh, !second, key, end, acc, second ? a.scale : 1.f, hl);
-  if (dirty && end >= 0) spoil_grad<D>(a, sh, !second, key, end, hl);
 }
 
 // Shares of the query heads that read one key head: as few as give the CUs
@@ -645,8 +486,8 @@ template <int D> hipError_t launch(const PromptBwdArgs& a) {
   hipError_t e = launch_kernel(attn_dq_kernel<D, 4>, dim3(tiles * a.Hq), dim3(256), st, a);
   if (e != hipSuccess) return e;
   const dim3 grid(tiles * a.Hkv * a.shares);
-  if constexpr (D == 64) e = launch_kernel(attn_dkv_kernel<D, 4>, grid, dim3(256), st, a);
-  else e = launch_kernel(attn_dkv_pair_kernel<D, 4>, grid, dim3(512), st, a);
+  if constexpr (D == 64) e = launch_kernel(attn_dkv_kernel<D, 4, 64, false>, grid, dim3(256), st, a);
+  else e = launch_kernel(attn_dkv_kernel<D, 4, 32, true>, grid, dim3(256), st, a);
   if (e != hipSuccess || a.shares == 1) return e;
   return launch_kernel(attn_dkv_sum_kernel<D>, dim3((unsigned)((a.T + 31) / 32) * a.Hkv), dim3(256), st, a);
 }
