@@ -2,7 +2,7 @@
 single-token read, attention over whole prompts and its gradients.
 
 They check dtypes, shapes, strides and devices, allocate what is not passed in, pass ``data_ptr()`` and the current
-HIP stream of the tensors' device, and raise on a non-OK status.  Rows are [tokens, heads, D] with the heads of a row
+HIP stream of the tensors' device (or ``stream``), and raise on a non-OK status.  Rows are [tokens, heads, D] with the heads of a row
 side by side; the distance between rows is free, so that q, k and v can be parts of one fused projection.
 """
 from __future__ import annotations
@@ -44,19 +44,37 @@ def _rows(t, name, shape, dev):
     return row
 
 
-def _call(dev, stream, fn, *args):
-    """fn(*args, stream) with `dev` as the current device."""
+def _call(dev, fn, *args):
+    """fn(*args, the current stream of dev), with dev as the current device."""
     if torch._C._cuda_getDevice() == dev.index:
-        s = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream)
+        s = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
-            s = fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else stream)
+            s = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     if s != raw.GDN_OK:
         raise raw.GdnError(s)
 
 
-def block_tables(seq_lens, new_lens, block_table, free_blocks, block_tokens: int, num_blocks: int, tokens: int,
-                 stream=None):
+def _on_stream(f):
+    """Adds the argument stream (a hipStream_t as a number; the current stream unless given).  Another stream is made
+    the current one for the call, so that what is allocated in it belongs to that stream."""
+
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        dev = (args[0] if args else next(iter(kw.values()))).device
+        if dev.type != "cuda" or stream == torch._C._cuda_getCurrentRawStream(dev.index):
+            return f(*args, **kw)
+        s = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+        with torch.cuda.stream(s):
+            return f(*args, **kw)
+
+    return call
+
+
+@_on_stream
+def block_tables(seq_lens, new_lens, block_table, free_blocks, block_tokens: int, num_blocks: int, tokens: int):
     """Extends block_table [R, width] in place by the blocks that new_lens [R] more tokens need beyond seq_lens [R],
     taken from the front of free_blocks.  All int32.  tokens: the length of the slot map, at least the sum of new_lens
     (what is over is filled with -1).
@@ -72,7 +90,7 @@ def block_tables(seq_lens, new_lens, block_table, free_blocks, block_tokens: int
     if tokens < 0:
         raise ValueError("block_tables: tokens is negative")
     slot_map, cu, after, used = (seq_lens.new_empty(n) for n in (tokens, r + 1, r, 2))
-    _call(dev, stream, raw.load().gdn_block_tables, seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
+    _call(dev, raw.load().gdn_block_tables, seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
           free_blocks.data_ptr(), slot_map.data_ptr(), cu.data_ptr(), after.data_ptr(), used.data_ptr(), r, width,
           free_blocks.numel(), block_tokens, num_blocks, tokens)
     return slot_map, cu, after, used
@@ -90,7 +108,8 @@ def _cache(k_cache, v_cache, k_scale, v_scale, dev):
     return nb, hkv, bt, d, fmt
 
 
-def cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=None):
+@_on_stream
+def cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale):
     """Writes the rows k, v [T, Hkv, D] bf16 into the cache at slot_map [T] int32 (see block_tables), in place.
 
     k_cache, v_cache [num_blocks, Hkv, block_tokens, D] int8 or float8_e4m3fn; k_scale, v_scale [num_blocks, Hkv]
@@ -101,7 +120,7 @@ def cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=None
     t = k.shape[0]
     ks, vs = _rows(k, "k", (t, hkv, d), dev), _rows(v, "v", (t, hkv, d), dev)
     _dense(slot_map, "slot_map", (t,), _I32, dev)
-    _call(dev, stream, raw.load().gdn_cache_append, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(),
+    _call(dev, raw.load().gdn_cache_append, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), ks, vs, t, hkv, d, bt, nb,
           raw.GDN_BF16, fmt)
 
@@ -111,8 +130,9 @@ def _decode_workspace(*sizes):
     return raw.gdn_attn_decode_workspace_bytes(*sizes)
 
 
+@_on_stream
 def attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale: float | None = None, out=None,
-                lse=None, workspace=None, stream=None):
+                lse=None, workspace=None):
     """Attention of one new token per request, q [R, Hq, D] bf16, over the first seq_lens [R] tokens of its blocks
     block_table [R, width] (int32) in the cache (see cache_append).  scale: 1 / sqrt(D) unless given.
 
@@ -139,7 +159,7 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, sc
         workspace = k_scale.new_empty(_decode_workspace(r, hq, hkv, d, bt, width) // 4)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous on the device of q")
-    _call(dev, stream, lib.gdn_attn_decode, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+    _call(dev, lib.gdn_attn_decode, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
           v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
           d ** -0.5 if scale is None else scale, qs, r, hq, hkv, d, bt, nb, width, raw.GDN_BF16, fmt,
           workspace.data_ptr(), workspace.numel() * workspace.element_size())
@@ -157,7 +177,8 @@ def _prompt(q, k, v, cu_seqlens, who):
     return dev, t, cu_seqlens.numel() - 1, hq, hkv, d, strides
 
 
-def attn_prompt(q, k, v, cu_seqlens, scale: float | None = None, out=None, lse=None, stream=None):
+@_on_stream
+def attn_prompt(q, k, v, cu_seqlens, scale: float | None = None, out=None, lse=None):
     """Causal attention over packed prompts: q [T, Hq, D], k, v [T, Hkv, D] bf16, cu_seqlens [R + 1] int32 the offsets
     of the sequences.  scale: 1 / sqrt(D) unless given.
 
@@ -174,14 +195,15 @@ def attn_prompt(q, k, v, cu_seqlens, scale: float | None = None, out=None, lse=N
         lse = (torch.empty if zero_rest else torch.zeros)((hq, t), dtype=_F32, device=dev)
     else:
         _dense(lse, "lse", (hq, t), _F32, dev)
-    _call(dev, stream, raw.load().gdn_attn_prompt, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
+    _call(dev, raw.load().gdn_attn_prompt, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
           out.data_ptr(), lse.data_ptr(), d ** -0.5 if scale is None else scale, *strides, t, r, hq, hkv, d,
           raw.GDN_BF16, zero_rest)
     return out, lse
 
 
+@_on_stream
 def attn_prompt_bwd(q, k, v, out, lse, grad_out, cu_seqlens, scale: float | None = None, grad_q=None, grad_k=None,
-                    grad_v=None, stream=None):
+                    grad_v=None):
     """Gradients of sum(out * grad_out) for attn_prompt's forward, from the out and lse that it returned.
 
     Returns (grad_q, grad_k, grad_v) bf16, the latter two summed over the query heads that share them.  Passed in, they
@@ -200,7 +222,7 @@ def attn_prompt_bwd(q, k, v, out, lse, grad_out, cu_seqlens, scale: float | None
     gos = _rows(grad_out, "grad_out", (t, hq, d), dev)
     lib = raw.load()
     ws = torch.empty(lib.gdn_attn_prompt_bwd_workspace_bytes(t, hq, hkv, d), dtype=torch.uint8, device=dev)
-    _call(dev, stream, lib.gdn_attn_prompt_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+    _call(dev, lib.gdn_attn_prompt_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
           lse.data_ptr(), grad_out.data_ptr(), cu_seqlens.data_ptr(), *(g.data_ptr() for g in grads),
           d ** -0.5 if scale is None else scale, *strides, gos, *gstrides, t, r, hq, hkv, d, raw.GDN_BF16, zero_rest,
           ws.data_ptr(), ws.numel())
