@@ -12,9 +12,9 @@ using namespace tile;
 constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
 constexpr float kLowest = -1e30f;  // running maximum before the first token
 constexpr float kSlack = 8.f;      // the maximum in use may lie this far (powers of two) below the true one
-constexpr int kN = 64;             // keys of a tile
 
-template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 2) void attn_prompt_kernel(PromptArgs a) {
+template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 3) void attn_prompt_kernel(PromptArgs a) {
+  constexpr int kN = D == 64 ? 64 : 32, NH = kN / 32;  // keys of a staged tile
   constexpr int BM = 32 * NW, NT = 64 * NW, KS = D / 16, DT = D / 32;
   __shared__ __bf16 kt[2][kN * D], vt[2][kN * D];
   __shared__ int begs[BM], window[kWindow], ranges[3][NW], bad[2][NW];
@@ -102,16 +102,16 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 2) 
   auto step = [&](auto masked_, int buf, int kv) {
     constexpr bool MASKED = decltype(masked_)::value;
     const int kb = fresh(kb0), vb = fresh(vb0);
-    f32x16 s[2];
+    f32x16 s[NH];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int n = 0; n < NH; ++n) {
       s[n] = zero16();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) s[n] = mma(row_frag<D>(kt[buf], kb, 32 * n, ks), q[ks], s[n]);
     }
     if constexpr (MASKED) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+      for (int n = 0; n < NH; ++n) {
         const unsigned seen = bits(from - kv - 32 * n, upto - kv - 32 * n);
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[n][e] = where_seen<false>(s[n][e], seen, e);
@@ -119,7 +119,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 2) 
     }
     float top = s[0][0];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < NH; ++n)
 #pragma unroll
       for (int e = 0; e < 16; ++e) top = fmaxf(top, s[n][e]);
     top = max_halves(top) * c;
@@ -130,10 +130,10 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 2) 
 #pragma unroll
       for (int i = 0; i < DT; ++i) o[i] *= f;
     }
-    u32x4 p[4];
+    u32x4 p[2 * NH];
     float sum = 0.f;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int n = 0; n < NH; ++n) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         s[n][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][e], c, -m));
@@ -146,7 +146,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 2) 
 #pragma unroll
     for (int i = 0; i < DT; ++i)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) o[i] = mma(col_frag<D>(vt[buf], vb, 16 * b, i), p[b], o[i]);
+      for (int b = 0; b < 2 * NH; ++b) o[i] = mma(col_frag<D>(vt[buf], vb, 16 * b, i), p[b], o[i]);
   };
   stage(0, first);
   int buf = 0, kv = first;
