@@ -87,10 +87,11 @@ def test_decode_argument_errors(kw, status):
 
 
 def test_decode_workspace():
-    need = gdn.gdn_attn_decode_workspace_bytes(3, 8, 4, 64, 16, 9)  # 2 units of 128 tokens x 3 x 4, two shares each
-    assert need == 2 * 24 * 2 * 66 * 4
+    need = gdn.gdn_attn_decode_workspace_bytes(3, 8, 4, 64, 16, 9)  # 2 units of 128 tokens and one ahead of them x 3 x 4, two shares each
+    assert need == 2 * 36 * 2 * 66 * 4
     assert decode(workspace_bytes=need - 1) == raw.GDN_ERR_WORKSPACE
     assert gdn.gdn_attn_decode_workspace_bytes(3, 8, 3, 64, 16, 9) == 0  # unsupported arguments
+    assert gdn.gdn_attn_decode_workspace_bytes(3, 8, 4, 64, 16, 0) == 0  # no blocks
     assert decode(R=0, q=None, seq_lens=None, out=None) == raw.GDN_OK
 
 
