@@ -331,6 +331,8 @@ int gdn_recurrent_step(const void *q, const void *k, const void *v, const float 
  *     other; the distance between rows is an argument, in elements, at least
  *     the row's length and a multiple of 8, so that the parts of one fused
  *     projection can be passed as they are.
+ *   - Scores (scale q.k) are float32 numbers and below 2^30 in magnitude: as
+ *     they grow, their exponentials lose what their fraction does.
  *   - Softmax statistics and every sum are float32; probabilities are rounded
  *     to 16 bits where they enter a matrix product.
  *   - lse is the natural logarithm of a row's sum of exp(scale q.k), float32.
@@ -341,6 +343,8 @@ int gdn_recurrent_step(const void *q, const void *k, const void *v, const float 
  *     or 128), stored [num_blocks, Hkv, block_tokens, D] in 8 bits with one
  *     float32 scale per (block, key head), stored [num_blocks, Hkv]; a value
  *     is its code times its scale.  num_blocks * block_tokens is below 2^31.
+ *   - What a call writes overlaps nothing that it reads, but for the tables and
+ *     caches that it updates in place.
  *   - Errors as for gdn_chunk_fwd.
  * ------------------------------------------------------------------------ */
 
@@ -388,6 +392,7 @@ int gdn_block_tables(const int *seq_lens, const int *new_lens, int *block_table,
  * and M = 127 (int8) or 448 (e4m3):
  *     s = max(a / M, old scale if older rows stand before the new ones, 2^-100)
  *     code = rne(x / s);   older codes = rne(code * old / s) if s grew.
+ * x / s is the float32 product x * (1 / s); old / s is a float32 quotient.
  * Rows behind the new ones are left as they were.  A block whose first row is
  * new starts a scale of its own, whatever its scale was.  NaN is stored as
  * zero, infinities as the largest code of the largest bf16 value's scale.
@@ -412,8 +417,10 @@ int gdn_cache_append(const void *k, const void *v, const int *slot_map, void *k_
  *
  * A request without tokens gets zeros and an lse of -infinity.  What the cache
  * holds behind a request's last token is never used, whatever its bits.
- * Scales are positive and finite.  Workspace: gdn_attn_decode_workspace_bytes;
- * scratch on entry and exit, no clearing needed.  R below 2^20.
+ * Scales are positive normal numbers.  Workspace:
+ * gdn_attn_decode_workspace_bytes; scratch on entry and exit, no clearing
+ * needed.  R is below 2^20, R * Hq below 2^23, width * block_tokens below 2^31,
+ * and so is R times the table's 128-token units and one.
  */
 size_t gdn_attn_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int block_tokens, int width);
 int gdn_attn_decode(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,

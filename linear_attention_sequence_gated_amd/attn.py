@@ -63,7 +63,7 @@ def _on_stream(f):
     def call(*args, stream=None, **kw):
         if stream is None:
             return f(*args, **kw)
-        dev = (args[0] if args else next(iter(kw.values()))).device
+        dev = next(x for x in (*args, *kw.values()) if isinstance(x, torch.Tensor)).device
         if dev.type != "cuda" or stream == torch._C._cuda_getCurrentRawStream(dev.index):
             return f(*args, **kw)
         s = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
@@ -125,7 +125,7 @@ def cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale):
           raw.GDN_BF16, fmt)
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=1024)
 def _decode_workspace(*sizes):
     return raw.gdn_attn_decode_workspace_bytes(*sizes)
 

@@ -42,7 +42,8 @@ int heads_shape(int Hq, int Hkv, int D) {
   return D == 64 || D == 128 ? GDN_OK : GDN_ERR_UNSUPPORTED;
 }
 
-// A row stride of which 64 rows stay inside 32-bit byte offsets.
+// A row stride of which 128 rows, the most that a buffer resource covers, stay
+// inside 32-bit byte offsets.
 bool near_ok(long long s, long long row) { return stride_ok(s, row) && s < (1LL << 24); }
 
 int prompt_shape(int T, int R, int Hq, int Hkv, int D) {

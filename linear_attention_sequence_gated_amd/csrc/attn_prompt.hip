@@ -1,4 +1,30 @@
 // attn_prompt.hip -- causal attention over packed prompts, forward.
+//
+// For row i and the keys j of its sequence up to itself,
+//   s_ij = scale q_i.k_j,   o_i = sum_j e^(s_ij) v_j / sum_j e^(s_ij),   lse_i = log sum_j e^(s_ij),
+// in one pass over the keys with a running maximum m and sum.  The maximum in
+// use is renewed only once a score lies 2^8 above it: sums and weights are then
+// at most 2^8, which float32 and bf16 hold as well as 1, and most tiles skip the
+// rescaling of the accumulators.
+//
+// A workgroup takes 128 rows of one head, a wave 32 of them; S^T = K Q^T and
+// O^T = V^T P^T by 32x32x16 products, so that a row is a lane's column: its
+// maximum and sum take one exchange of half-waves, and the weights, rounded to
+// bf16 (2^-8 of each, the operands' own precision), go from accumulator to
+// operand in place.  K and V are staged in LDS by direct loads, one tile ahead,
+// and read there by rows (K) and transposed (V).  Rows are cut into tiles where
+// they lie, whatever sequences they belong to: tiles that some row sees in part
+// are masked, those that all rows see whole are not.  The workgroups of the
+// heads that share keys are neighbours.
+//
+// What bounds it is the matrix and the vector unit together: 32 keys of a wave's
+// 32 rows are 4 D / 32 products of 32 cycles and 16 lanes' exponentials, with as
+// many multiply-adds, sums and maxima.  1 x 16384 x 16/4 x 64 takes 578 us, 950
+// TFLOP/s of the 1600 that the largest library products reach here; 8 x 2048 x
+// 12/4 x 64 70 us; 1 x 16384 x 16/4 x 128 1030 us, 1060 TFLOP/s.  Without the softmax the same
+// loop reaches 1190, without the reads of LDS 1215.  Two tiles of rows to a wave,
+// the next scores beside the softmax, eight waves, orders set by hand and other
+// wave priorities were all slower or the same.
 #include "../../include/gdn.h"
 #include "gdn_attn.hpp"
 #include "gdn_launch.hpp"
@@ -10,13 +36,17 @@ namespace {
 using namespace tile;
 
 constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
-constexpr float kLowest = -1e30f;  // running maximum before the first token
+constexpr float kLowest = -3e38f;  // running maximum before the first token
 constexpr float kSlack = 8.f;      // the maximum in use may lie this far (powers of two) below the true one
 
 template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 3) void attn_prompt_kernel(PromptArgs a) {
-  constexpr int kN = D == 64 ? 64 : 32, NH = kN / 32;  // keys of a staged tile
+  // keys of a staged tile: 64 at D = 64, where 125 registers let four workgroups
+  // share a CU (578 us for 1 x 16384 x 16/4 x 64; with 32 keys 620); 32 at
+  // D = 128, where that takes 158 registers and three workgroups a CU (67.7 us for
+  // 13 prompts of up to 1201 rows x 16/4 x 128; with 64 keys and two 70.5)
+  constexpr int kN = D == 64 ? 64 : 32, NH = kN / 32;
   constexpr int BM = 32 * NW, NT = 64 * NW, KS = D / 16, DT = D / 32;
-  __shared__ __bf16 kt[2][kN * D], vt[2][kN * D];
+  __shared__ alignas(16) __bf16 kt[2][kN * D], vt[2][kN * D];
   __shared__ int begs[BM], window[kWindow], ranges[3][NW], bad[2][NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const int tiles = (a.T + BM - 1) / BM;

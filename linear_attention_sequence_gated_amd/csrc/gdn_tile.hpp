@@ -268,8 +268,8 @@ __device__ __forceinline__ void find_rows(const int* cu, int R, int T, int r0, i
 // (last) row.  Workgroups are started in the order of their numbers, and the
 // last ones to end are short ones if they were started by length; with few
 // tiles of sequences of many lengths that is worth more than the microsecond
-// that the ranking costs every workgroup (61 tiles of 13 sequences of up to
-// 1201 rows, 16 heads of 128: MEASURED).  Needs tiles <= NT, R < kWindow;
+// that the ranking costs every workgroup (13 sequences of up to 1201 rows x 16/4 x
+// 128, forward: 73 us for 80; 8 of 2048 x 12/4 x 64: 75 for 84).  Needs tiles <= NT, R < kWindow;
 // `window` (kWindow) and `keys` (NT entries) are scratch.  Ends with a barrier.
 template <int N, int NT, bool KEYS>
 __device__ __forceinline__ int tile_by_length(const int* cu, int R, int T, int tiles, int rank, int* window, int* keys) {

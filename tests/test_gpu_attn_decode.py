@@ -106,6 +106,18 @@ def test_decode_many_requests():
     check(torch, *make(torch, rng, lens, 2, 1, 64, 16, "e4m3"))
 
 
+@pytest.mark.parametrize("D,H", [(64, 3), (128, 2)])
+@pytest.mark.parametrize("R", [70, 300, 800])
+def test_decode_shares_that_begin_and_end_anywhere(R, D, H):
+    """Lengths around whole units of 128 tokens, many more units than workgroups and about as many: shares that begin
+    or end with a request's first unit, its last, or between two requests."""
+    torch = torch_dev()
+    rng = np.random.default_rng(R + D)
+    lens = rng.choice([0, 1, 127, 128, 129, 256, 257, 900], R)
+    note(f"decode shares R{R} D{D}")
+    check(torch, *make(torch, rng, lens, 2 * H, H, D, 128, "int8"))
+
+
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
 def test_decode_ignores_what_lies_behind(kind):
     """Bits behind a request's last token, unused blocks and their scales may be anything, NaN codes included."""

@@ -139,6 +139,17 @@ def test_growing_scores():
     check_forward(torch, q, k, v, offsets([520]))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_equal_scores_at_the_end_of_their_range(D):
+    """-2^29 and 2^29: exponents have no fraction left, but equal scores have equal weights."""
+    torch = torch_dev()
+    q, k, v = make(torch, np.random.default_rng(9), 200, 1, 1, D, fused=False)
+    note(f"equal scores D{D}")
+    for sign in (-1, 1):
+        q[:], k[:] = 2.0 ** 13, sign * 2.0 ** 13
+        check_forward(torch, q, k, v, offsets([140, 60]), 8.0 / D)
+
+
 @pytest.mark.parametrize("cu", [[-5, 40, 30, 100000, 2 ** 31 - 1], [100, 50, 0], [-2 ** 31, -1, 2 ** 31 - 1], [7], [64, 64, 64]])
 def test_offsets_out_of_order(cu):
     """Offsets that are no offsets lead to no access outside the buffers, and only to rows' results that mean nothing."""

@@ -221,8 +221,10 @@ def test_other_streams():
         # the default stream, given by its number (zero), from another current one
         s.synchronize()
         o = gdn.attn_prompt(q, k, v, cu, stream=torch.cuda.default_stream().cuda_stream)
+    named = gdn.attn_prompt(scale=None, cu_seqlens=cu, v=v, k=k, q=q, stream=s.cuda_stream)
     s.synchronize()
     torch.cuda.synchronize()
+    got.append((*named, *grads))
     for r in got:
         for a, b in zip((*want, *grads), r):
             assert torch.equal(a, b)
