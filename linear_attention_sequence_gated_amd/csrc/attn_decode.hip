@@ -249,6 +249,47 @@ __device__ __forceinline__ void take_tile(Sums<D>& s, const Tile<D>& t, const f1
   }
 }
 
+// The request that unit u = at(U) lies in, of U units over all (request, head)s,
+// and its own first unit (both undefined if u is not below U).  By 256 threads;
+// scan and found are scratch in LDS.
+struct Place {
+  long long U, u, base;
+  int r;
+};
+template <class At> __device__ __forceinline__ Place place_of(const DecodeArgs& a, const DecodeSizes& z, int* scan, int* found, At at) {
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), heads = z.Hkv * z.NG;
+  const int per = (z.R + 255) / 256, ra = tid * per;
+  int mine = 0;
+  for (int i = 0; i < per; ++i)
+    if (ra + i < z.R) mine += cost_of(tokens_of(a.seq_lens, ra + i, z));
+  const int incl = wave_scan(mine);
+  if ((tid & 63) == 63) scan[wave] = incl;
+  __syncthreads();
+  int before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if (w < wave) before += scan[w];
+    total += scan[w];
+  }
+  Place p;
+  p.U = (long long)total * heads;
+  p.u = at(p.U);
+  if (p.u >= (long long)before * heads && p.u < (long long)(before + mine) * heads) {
+    int r = ra, first = before;
+    for (;; ++r) {
+      const int n = cost_of(tokens_of(a.seq_lens, r, z));
+      if (p.u < (long long)(first + n) * heads) break;
+      first += n;
+    }
+    found[0] = r;
+    found[1] = first;
+  }
+  __syncthreads();
+  p.r = __builtin_amdgcn_readfirstlane(found[0]);
+  p.base = (long long)__builtin_amdgcn_readfirstlane(found[1]) * heads;
+  return p;
+}
+
 template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a, DecodeSizes z) {
   constexpr int NB = D / 16, LD = D + 4;
   __shared__ alignas(16) float part[kWaves][16][LD];
@@ -258,40 +299,16 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
   const int heads = z.Hkv * z.NG;
 
   // this workgroup's share [u0, u1) of the units, and the request it starts in
-  const int per = (z.R + 255) / 256, ra = tid * per;
-  int mine = 0;
-  for (int i = 0; i < per; ++i)
-    if (ra + i < z.R) mine += cost_of(tokens_of(a.seq_lens, ra + i, z));
-  const int incl = wave_scan(mine);
-  if (lane == 63) scan[wave] = incl;
-  __syncthreads();
-  int before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) before += scan[w];
-    total += scan[w];
-  }
-  const long long U = (long long)total * heads;
-  const long long u0 = U * blockIdx.x / z.W, u1 = U * (blockIdx.x + 1) / z.W;
+  const Place at = place_of(a, z, scan, found, [&](long long U) { return U * blockIdx.x / z.W; });
+  const long long u0 = at.u, u1 = at.U * (blockIdx.x + 1) / z.W;
   if (u0 >= u1) return;
-  if (u0 >= (long long)before * heads && u0 < (long long)(before + mine) * heads) {
-    int r = ra, at = before;
-    for (;; ++r) {
-      const int nu = cost_of(tokens_of(a.seq_lens, r, z));
-      if (u0 < (long long)(at + nu) * heads) break;
-      at += nu;
-    }
-    found[0] = r;
-    found[1] = at;
-  }
-  __syncthreads();
   // the part of one (request, key head) that a share covers: units [ua, ub)
   struct Part {
     int r, n, nu, cost, h, q0, cols, ua, ub;  // ub <= ua: nothing but of what stands ahead
     long long next;
   };
-  int r = __builtin_amdgcn_readfirstlane(found[0]);
-  long long base = (long long)__builtin_amdgcn_readfirstlane(found[1]) * heads;  // first unit of request r
+  int r = at.r;
+  long long base = at.base;  // first unit of request r
   auto part_at = [&](long long u) {
     Part p;
     p.r = r;
@@ -302,10 +319,10 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
     p.h = hh / z.NG;
     p.q0 = p.h * z.G + (hh - p.h * z.NG) * 16;
     p.cols = min(16, (p.h + 1) * z.G - p.q0);
-    const int at = (int)(u - base - (long long)hh * p.cost) - kAhead;
-    p.ua = max(at, 0);
-    p.ub = (int)min((long long)p.nu, at + (u1 - u));
-    p.next = u + (p.ub - at);
+    const int from = (int)(u - base - (long long)hh * p.cost) - kAhead;
+    p.ua = max(from, 0);
+    p.ub = (int)min((long long)p.nu, from + (u1 - u));
+    p.next = u + (p.ub - from);
     return p;
   };
   Tile<D> t0, t1;
@@ -450,52 +467,91 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
   }
 }
 
+// The workgroup that takes unit x of U: the first whose share ends past it.
+__device__ __forceinline__ int taker(long long x, long long U, const DecodeSizes& z) {
+  return (int)(((x + 1) * z.W + U - 1) / U - 1);
+}
+
 // Joins the shares of one (request, query head), in the order of the tokens;
 // heads that one workgroup covered are done already.  Requests without tokens
-// get their zeros here.
-// DS workgroups of C = D / DS columns each.
-template <int D, int DS> __global__ __launch_bounds__(128 * (DS == 1 ? 2 : 4)) void attn_decode_join_kernel(DecodeArgs a, DecodeSizes z) {
+// get their zeros here.  Either a workgroup (DS of them, for D / DS columns
+// each) sees to one row of the output, or (CUTS) to a column of the head that
+// the end of one share lies in, if no share before it ends there too.
+template <int D, int DS, bool CUTS> __global__ __launch_bounds__(128 * (DS == 1 ? 2 : 4)) void attn_decode_join_kernel(DecodeArgs a, DecodeSizes z) {
   constexpr int NT = DS == 1 ? 256 : 512, C = D / DS, NP = NT / (C / 4);  // shares taken side by side
+  static_assert(!CUTS || DS == 1, "");
   __shared__ alignas(16) float sum[NT / 64][C], ls[NT / 64], weight[most_shares(D)], part_l[most_shares(D)], red[NT / 64];
   __shared__ int scan[2][NT / 64];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int x = blockIdx.x / DS, d0 = blockIdx.x % DS * C;
-  const int r = x / z.Hq, hq = x - r * z.Hq, h = hq / z.G, in = hq - h * z.G, hh = h * z.NG + in / 16, col = in % 16;
-  const int n = tokens_of(a.seq_lens, r, z), nu = units_of(n), cost = cost_of(n), heads = z.Hkv * z.NG;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, heads = z.Hkv * z.NG;
+  int r, hq, col, d0 = 0, i0, i1;
+  long long U, P;  // P: the row's first unit
+  if constexpr (CUTS) {
+    const int cuts = (z.W - 1) * z.Gc;
+    if ((int)blockIdx.x >= cuts) {  // zeros, sixteen requests to a workgroup
+      const int r0 = (blockIdx.x - cuts) * 16;
+      for (int i = r0; i < min(r0 + 16, z.R); ++i) {
+        if (tokens_of(a.seq_lens, i, z)) continue;
+        for (int x = tid; x < z.Hq * (D / 8); x += NT)
+          reinterpret_cast<u32x4*>(static_cast<__bf16*>(a.out) + (size_t)i * z.Hq * D)[x] = u32x4{0u, 0u, 0u, 0u};
+        for (int x = tid; a.lse && x < z.Hq; x += NT) a.lse[(size_t)i * z.Hq + x] = -INFINITY;
+      }
+      return;
+    }
+    i0 = blockIdx.x / z.Gc;
+    col = blockIdx.x - i0 * z.Gc;
+    const Place at = place_of(a, z, scan[0], scan[1], [&](long long all) { return all * (i0 + 1) / z.W; });
+    if (at.u >= at.U) return;
+    U = at.U;
+    r = at.r;
+    const int cost = cost_of(tokens_of(a.seq_lens, r, z)), hh = (int)((at.u - at.base) / cost), h = hh / z.NG;
+    P = at.base + (long long)hh * cost;
+    hq = h * z.G + (hh - h * z.NG) * 16 + col;
+    if (at.u <= P + kAhead || U * i0 / z.W > P + kAhead || hq >= (h + 1) * z.G) return;
+    i1 = taker(P + cost - 1, U, z);
+  } else {
+    const int x = blockIdx.x / DS;
+    d0 = blockIdx.x % DS * C;
+    r = x / z.Hq;
+    hq = x - r * z.Hq;
+    const int h = hq / z.G, in = hq - h * z.G, hh = h * z.NG + in / 16;
+    col = in % 16;
+    const int n = tokens_of(a.seq_lens, r, z), cost = cost_of(n);
+    if (n == 0) {
+      if (tid < C / 4)
+        *reinterpret_cast<u32x2*>(static_cast<__bf16*>(a.out) + ((size_t)r * z.Hq + hq) * D + d0 + 4 * tid) = u32x2{0u, 0u};
+      if (tid == 0 && d0 == 0 && a.lse) a.lse[(size_t)r * z.Hq + hq] = -INFINITY;
+      return;
+    }
+    int all = 0, pre = 0;
+    for (int i = tid; i < z.R; i += NT) {
+      const int c = cost_of(tokens_of(a.seq_lens, i, z));
+      all += c;
+      pre += i < r ? c : 0;
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+      all += __shfl_xor(all, d);
+      pre += __shfl_xor(pre, d);
+    }
+    if (lane == 0) {
+      scan[0][wave] = all;
+      scan[1][wave] = pre;
+    }
+    __syncthreads();
+    all = pre = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) {
+      all += scan[0][w];
+      pre += scan[1][w];
+    }
+    U = (long long)all * heads;
+    P = (long long)pre * heads + (long long)hh * cost;
+    i0 = taker(P + kAhead, U, z);
+    i1 = taker(P + cost - 1, U, z);
+    if (i0 == i1) return;
+  }
   __bf16* out = static_cast<__bf16*>(a.out) + ((size_t)r * z.Hq + hq) * D + d0;
   const bool writes_lse = tid == 0 && d0 == 0 && a.lse;
-  if (nu == 0) {
-    if (tid < C / 4) *reinterpret_cast<u32x2*>(out + 4 * tid) = u32x2{0u, 0u};
-    if (writes_lse) a.lse[(size_t)r * z.Hq + hq] = -INFINITY;
-    return;
-  }
-  int all = 0, pre = 0;
-  for (int i = tid; i < z.R; i += NT) {
-    const int nu_i = cost_of(tokens_of(a.seq_lens, i, z));
-    all += nu_i;
-    pre += i < r ? nu_i : 0;
-  }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) {
-    all += __shfl_xor(all, d);
-    pre += __shfl_xor(pre, d);
-  }
-  if (lane == 0) {
-    scan[0][wave] = all;
-    scan[1][wave] = pre;
-  }
-  __syncthreads();
-  all = pre = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 64; ++w) {
-    all += scan[0][w];
-    pre += scan[1][w];
-  }
-  const long long U = (long long)all * heads, P = (long long)pre * heads + (long long)hh * cost;
-  // the workgroup that takes unit x: the first whose share ends past it
-  auto taker = [&](long long x) { return (int)(((x + 1) * z.W + U - 1) / U - 1); };
-  const int i0 = taker(P + kAhead), i1 = taker(P + cost - 1);
-  if (i0 == i1) return;
   auto at = [&](int i) {
     const bool head_of_share = U * i / z.W >= P;
     return a.ws + (2 * (size_t)i + (head_of_share ? 0 : 1)) * z.Gc * (D + 2);
@@ -577,8 +633,12 @@ template <int D, int FMT> hipError_t launch(const DecodeArgs& a, const DecodeSiz
   }
   // few rows: a row's columns over four workgroups, so that a long request's
   // many shares are read by more of them
-  if (z.R * z.Hq < 256) return launch_kernel(attn_decode_join_kernel<D, 4>, dim3(z.R * z.Hq * 4), dim3(512), st, a, z);
-  return launch_kernel(attn_decode_join_kernel<D, 1>, dim3(z.R * z.Hq), dim3(256), st, a, z);
+  const int rows = z.R * z.Hq, cuts = z.W ? (z.W - 1) * z.Gc : 0;
+  if (rows < 256) return launch_kernel(attn_decode_join_kernel<D, 4, false>, dim3(rows * 4), dim3(512), st, a, z);
+  // by rows or by the ends of shares, whichever is fewer (700 requests of up to
+  // 100 tokens x 16/4 x 128: 33.7 us for 43.9 by rows)
+  if (rows <= cuts + (z.R + 15) / 16) return launch_kernel(attn_decode_join_kernel<D, 1, false>, dim3(rows), dim3(256), st, a, z);
+  return launch_kernel(attn_decode_join_kernel<D, 1, true>, dim3(cuts + (z.R + 15) / 16), dim3(256), st, a, z);
 }
 
 }  // namespace

@@ -118,6 +118,14 @@ def test_decode_shares_that_begin_and_end_anywhere(R, D, H):
     check(torch, *make(torch, rng, lens, 2 * H, H, D, 128, "int8"))
 
 
+def test_decode_many_requests_of_many_heads():
+    """More query heads to a key head than columns, the last group in part, more rows than ends of shares."""
+    torch = torch_dev()
+    rng = np.random.default_rng(4)
+    note("decode many heads")
+    check(torch, *make(torch, rng, rng.choice([0, 3, 128, 300, 700], 500), 46, 2, 64, 64, "e4m3"))
+
+
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
 def test_decode_ignores_what_lies_behind(kind):
     """Bits behind a request's last token, unused blocks and their scales may be anything, NaN codes included."""
