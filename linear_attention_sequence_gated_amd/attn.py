@@ -156,7 +156,8 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, sc
         _dense(lse, "lse", (r, hq), _F32, dev)
     lib = raw.load()
     if workspace is None:
-        workspace = k_scale.new_empty(_decode_workspace(r, hq, hkv, d, bt, width) // 4)
+        size = _decode_workspace(r, hq, hkv, d, bt, width)
+        workspace = k_scale.new_empty(size // 4) if size else lse
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous on the device of q")
     _call(dev, lib.gdn_attn_decode, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),

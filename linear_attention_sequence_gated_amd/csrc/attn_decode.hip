@@ -7,8 +7,9 @@
 // The cache is read once (2 D bytes per token and head); everything else is
 // small, so the kernel is bound by HBM and is built to keep loads in flight.
 //
-// Work is counted in units of 128 tokens of one (request, head), one more for
-// its beginning and end, and dealt out in equal contiguous shares to a fixed
+// Where no request can be long, by the width of the table, a workgroup takes all
+// of one (request, head).  Otherwise work is counted in units of 128 tokens of one
+// (request, head), one more for its beginning and end, and dealt out in equal contiguous shares to a fixed
 // number of workgroups, whatever the lengths: a long request is split over many workgroups and short ones are
 // taken several to a workgroup.  The shares follow from the lengths, which
 // only the device knows, so every workgroup finds its own with a prefix sum.
@@ -47,7 +48,7 @@ using pipe::u32x4;
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 
-constexpr int kUnit = 128, kWaves = 4, kTile = kUnit / kWaves;  // tokens of a unit, of a wave's tile
+constexpr int kUnit = 128, kTile = 32;  // tokens of a unit, of a wave's tile
 // To begin a (request, head) and to end it take about the time of a unit.  Counted
 // so, 64 ragged requests x 16/4 x 128 take 28.9 us for 34.3 uncounted, 256 of up
 // to 1000 tokens 46.3 for 51.7; 4 x 65521 tokens 61.6 for 60.9.
@@ -61,7 +62,7 @@ constexpr float kCodeUp = 1024.f;  // int8 codes enter the products times 2^-10
 constexpr int most_shares(int D) { return 256 * (D == 64 ? 3 : 2); }
 
 struct DecodeSizes {
-  int R, Hq, Hkv, G, NG, Gc, bt, width, num_blocks, W;
+  int R, Hq, Hkv, G, NG, Gc, bt, width, num_blocks, W, whole;  // whole: waves of a workgroup that takes a whole (request, key head), or 0
 };
 
 // Tokens of a request that its table row can hold.
@@ -290,24 +291,30 @@ template <class At> __device__ __forceinline__ Place place_of(const DecodeArgs& 
   return p;
 }
 
-template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a, DecodeSizes z) {
-  constexpr int NB = D / 16, LD = D + 4;
-  __shared__ alignas(16) float part[kWaves][16][LD];
-  __shared__ float ml[kWaves][2][16];
-  __shared__ int scan[kWaves], found[2];
+template <int D, int FMT, int NW, bool WHOLE> __global__ __launch_bounds__(64 * NW, 2) void attn_decode_kernel(DecodeArgs a, DecodeSizes z) {
+  constexpr int NB = D / 16, LD = D + 4, kStep = NW * kTile;
+  static_assert(WHOLE || kStep == kUnit, "");
+  __shared__ alignas(16) float part[NW][16][LD];
+  __shared__ float ml[NW][2][16];
+  __shared__ int scan[4], found[2];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, c = lane & 15;
   const int heads = z.Hkv * z.NG;
 
   // this workgroup's share [u0, u1) of the units, and the request it starts in
-  const Place at = place_of(a, z, scan, found, [&](long long U) { return U * blockIdx.x / z.W; });
-  const long long u0 = at.u, u1 = at.U * (blockIdx.x + 1) / z.W;
-  if (u0 >= u1) return;
+  Place at{};
+  long long u0 = 0, u1 = 0;
+  if constexpr (!WHOLE) {
+    at = place_of(a, z, scan, found, [&](long long U) { return U * blockIdx.x / z.W; });
+    u0 = at.u;
+    u1 = at.U * (blockIdx.x + 1) / z.W;
+    if (u0 >= u1) return;
+  }
   // the part of one (request, key head) that a share covers: units [ua, ub)
   struct Part {
     int r, n, nu, cost, h, q0, cols, ua, ub;  // ub <= ua: nothing but of what stands ahead
     long long next;
   };
-  int r = at.r;
+  int r = WHOLE ? (int)blockIdx.x / heads : at.r;
   long long base = at.base;  // first unit of request r
   auto part_at = [&](long long u) {
     Part p;
@@ -315,10 +322,15 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
     p.n = tokens_of(a.seq_lens, r, z);
     p.nu = units_of(p.n);
     p.cost = kAhead + p.nu;
-    const int hh = (int)((u - base) / p.cost);
+    const int hh = WHOLE ? (int)u : (int)((u - base) / p.cost);
     p.h = hh / z.NG;
     p.q0 = p.h * z.G + (hh - p.h * z.NG) * 16;
     p.cols = min(16, (p.h + 1) * z.G - p.q0);
+    if constexpr (WHOLE) {
+      p.ua = 0;
+      p.ub = p.nu;
+      return p;
+    }
     const int from = (int)(u - base - (long long)hh * p.cost) - kAhead;
     p.ua = max(from, 0);
     p.ub = (int)min((long long)p.nu, from + (u1 - u));
@@ -338,8 +350,8 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
   };
 
   bool first = true;
-  Part cur = part_at(u0);
-  if (cur.ub <= cur.ua) return;
+  Part cur = part_at(WHOLE ? blockIdx.x - r * heads : u0);
+  if (!WHOLE && cur.ub <= cur.ua) return;
   begin(cur);
   for (;;) {
     const int nu = cur.nu, h = cur.h, q0 = cur.q0, cols = cur.cols, ua = cur.ua, ub = cur.ub, rr = cur.r;
@@ -377,19 +389,19 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
     int tok = ua * kUnit + wave * kTile;
     if (tok < end) {
       for (;;) {
-        if (tok + kUnit < end) load_tile<D>(t1, tok + kUnit, end, row, h, a, z);
+        if (tok + kStep < end) load_tile<D>(t1, tok + kStep, end, row, h, a, z);
         take_tile<D, FMT>(s, t0, q, qfac);
-        tok += kUnit;
+        tok += kStep;
         if (tok >= end) break;
-        if (tok + kUnit < end) load_tile<D>(t0, tok + kUnit, end, row, h, a, z);
+        if (tok + kStep < end) load_tile<D>(t0, tok + kStep, end, row, h, a, z);
         take_tile<D, FMT>(s, t1, q, qfac);
-        tok += kUnit;
+        tok += kStep;
         if (tok >= end) break;
       }
     }
 
     const long long u = cur.next;
-    bool more = u < u1;
+    bool more = !WHOLE && u < u1;
     if (more) {
       if (u >= base + (long long)cur.cost * heads) {  // the next request that has tokens
         base += (long long)cur.cost * heads;
@@ -417,10 +429,10 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
     __syncthreads();
     float M = ml[0][0][c];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) M = fmaxf(M, ml[w][0][c]);
+    for (int w = 1; w < NW; ++w) M = fmaxf(M, ml[w][0][c]);
     float L = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) L += ml[w][1][c] * __builtin_amdgcn_exp2f(ml[w][0][c] - M);
+    for (int w = 0; w < NW; ++w) L += ml[w][1][c] * __builtin_amdgcn_exp2f(ml[w][0][c] - M);
     const float mine_w = __builtin_amdgcn_exp2f(s.m - M) * (FMT == GDN_CACHE_I8 ? kCodeUp : 1.f);
     if (c < cols) {
 #pragma unroll
@@ -443,17 +455,17 @@ template <int D, int FMT> __global__ __launch_bounds__(256, 2) void attn_decode_
       }
     }
     __syncthreads();
-    for (int x = tid; x < cols * D / 4; x += 256) {
+    for (int x = tid; x < cols * D / 4; x += 64 * NW) {
       const int col = x / (D / 4), d = 4 * (x % (D / 4));
       f32x4 o = pipe::zero4();
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) o += *reinterpret_cast<const f32x4*>(&part[w][col][d]);
+      for (int w = 0; w < NW; ++w) o += *reinterpret_cast<const f32x4*>(&part[w][col][d]);
       if (whole) {
         float Mc = ml[0][0][col], Lc = 0.f;
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) Mc = fmaxf(Mc, ml[w][0][col]);
+        for (int w = 1; w < NW; ++w) Mc = fmaxf(Mc, ml[w][0][col]);
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) Lc += ml[w][1][col] * __builtin_amdgcn_exp2f(ml[w][0][col] - Mc);
+        for (int w = 0; w < NW; ++w) Lc += ml[w][1][col] * __builtin_amdgcn_exp2f(ml[w][0][col] - Mc);
         const float inv = Lc == 0.f ? 0.f : 1.f / Lc;
         o *= inv;
         *reinterpret_cast<u32x2*>(static_cast<__bf16*>(a.out) + ((size_t)rr * z.Hq + q0 + col) * D + d) = pipe::cvt4(o);
@@ -622,13 +634,30 @@ DecodeSizes sizes(int R, int Hq, int Hkv, int D, int bt, int width, int num_bloc
   const long long units = width ? (((long long)width * bt + kUnit - 1) / kUnit + kAhead) * R * Hkv * z.NG : 0;
   const int most = most_shares(D);
   z.W = units < most ? (int)units : most;
+  // one workgroup to a (request, key head), and no join, if none can be long; the
+  // more of them there are, the longer they may be before the longest is what the
+  // call takes.  Both ways, us: 1 x 777 x 12/4 x 64 6.6 for 9.4, 64 ragged of up
+  // to 1500 x 16/4 x 128 14.9 for 20.2, 300 of up to 120 9.8 for 20.4, of up to
+  // 2000 60.6 for 78.4, of up to 8000 229 for 243; 16 of 2000 16.4 for 13.8, 64 of
+  // 4099 31.1 for 29.6.
+  const long long groups = (long long)R * Hkv * z.NG, cap = ((long long)width * bt + kUnit - 1) / kUnit;
+  z.whole = cap <= (groups < 256 ? 8 : groups < 1024 ? 24 : 64);
+  // eight waves to each where that leaves none waiting for a CU, and for the long
+  // ones: 64 ragged of up to 777 x 16/4 x 128 9.4 for 10.5 with four, 300 of up to
+  // 777 36 for 26
+  if (z.whole) z.whole = cap > 4 && (groups <= (D == 64 ? 512 : 256) || cap > 16) ? 8 : 4;
   return z;
 }
 
 template <int D, int FMT> hipError_t launch(const DecodeArgs& a, const DecodeSizes& z) {
   hipStream_t st = static_cast<hipStream_t>(a.stream);
+  if (z.whole) {
+    const dim3 grid(z.R * z.Hkv * z.NG);
+    if (z.whole == 8) return launch_kernel(attn_decode_kernel<D, FMT, 8, true>, grid, dim3(512), st, a, z);
+    return launch_kernel(attn_decode_kernel<D, FMT, 4, true>, grid, dim3(256), st, a, z);
+  }
   if (z.W) {
-    const hipError_t e = launch_kernel(attn_decode_kernel<D, FMT>, dim3(z.W), dim3(256), st, a, z);
+    const hipError_t e = launch_kernel(attn_decode_kernel<D, FMT, 4, false>, dim3(z.W), dim3(256), st, a, z);
     if (e != hipSuccess) return e;
   }
   // few rows: a row's columns over four workgroups, so that a long request's
@@ -645,6 +674,7 @@ template <int D, int FMT> hipError_t launch(const DecodeArgs& a, const DecodeSiz
 
 size_t attn_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int bt, int width) {
   const DecodeSizes z = sizes(R, Hq, Hkv, D, bt, width, 0);
+  if (z.whole) return 0;
   return ((size_t)2 * z.W * z.Gc * (D + 2) * sizeof(float) + 15) / 16 * 16;
 }
 

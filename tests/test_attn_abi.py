@@ -65,7 +65,7 @@ def test_append_of_nothing_is_noop():
 
 def decode(**kw):
     args = dict(q=A, k_cache=A, v_cache=A, k_scale=A, v_scale=A, block_table=A, seq_lens=A, out=A, lse=A, scale=0.125,
-                q_stride=512, R=3, Hq=8, Hkv=4, D=64, block_tokens=16, num_blocks=64, width=9, dtype=gdn.GDN_BF16,
+                q_stride=512, R=3, Hq=8, Hkv=4, D=64, block_tokens=16, num_blocks=64, width=72, dtype=gdn.GDN_BF16,
                 cache_format=gdn.GDN_CACHE_I8, workspace=A, workspace_bytes=1 << 40, stream=None)
     args.update(kw)
     return gdn.gdn_attn_decode(**args)
@@ -87,11 +87,11 @@ def test_decode_argument_errors(kw, status):
 
 
 def test_decode_workspace():
-    need = gdn.gdn_attn_decode_workspace_bytes(3, 8, 4, 64, 16, 9)  # 2 units of 128 tokens and one ahead of them x 3 x 4, two shares each
-    assert need == 2 * 36 * 2 * 66 * 4
+    need = gdn.gdn_attn_decode_workspace_bytes(3, 8, 4, 64, 16, 72)  # 9 units of 128 tokens and one ahead of them x 3 x 4, two shares each
+    assert need == 2 * 120 * 2 * 66 * 4
     assert decode(workspace_bytes=need - 1) == raw.GDN_ERR_WORKSPACE
-    assert gdn.gdn_attn_decode_workspace_bytes(3, 8, 3, 64, 16, 9) == 0  # unsupported arguments
-    assert gdn.gdn_attn_decode_workspace_bytes(3, 8, 4, 64, 16, 0) == 0  # no blocks
+    assert gdn.gdn_attn_decode_workspace_bytes(3, 8, 3, 64, 16, 72) == 0  # unsupported arguments
+    assert gdn.gdn_attn_decode_workspace_bytes(3, 8, 4, 64, 16, 9) == 0  # short: nothing to join
     assert decode(R=0, q=None, seq_lens=None, out=None) == raw.GDN_OK
 
 

@@ -14,6 +14,16 @@ from oracle import attention as ref
 from test_gpu_attn_cache import ints, make_cache, values
 
 pytestmark = pytest.mark.gpu
+WIDE = [False]  # whether tables have room for many more tokens than their requests have
+
+
+@pytest.fixture(params=[False, True], ids=["narrow", "wide"], autouse=True)
+def wide(request):
+    """Both ways to deal out the work: by the width of the table no request is long, or some could be."""
+    WIDE[0] = request.param
+    yield
+    WIDE[0] = False
+
 
 
 def make(torch, rng, lens, Hq, H, D, bt, kind, extra_width=0, spread=1.0):
@@ -21,6 +31,7 @@ def make(torch, rng, lens, Hq, H, D, bt, kind, extra_width=0, spread=1.0):
     blocks = -(-np.maximum(lens, 0) // bt)
     nb = int(blocks.sum()) + 2
     ids = rng.permutation(nb)
+    extra_width += 65 * 128 // bt if WIDE[0] else 0
     table = np.full((len(lens), max(1, int(blocks.max(initial=0))) + extra_width), -1)
     at = 0
     for r, b in enumerate(blocks):

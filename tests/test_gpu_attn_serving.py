@@ -237,7 +237,7 @@ def test_buffers_of_the_caller():
     torch = torch_dev()
     import linear_attention_sequence_gated_amd as gdn
     from test_gpu_attn_decode import make
-    q, kc, vc, ks, vs, table, lens = make(torch, np.random.default_rng(4), [100, 3], 4, 2, 64, 16, "int8")
+    q, kc, vc, ks, vs, table, lens = make(torch, np.random.default_rng(4), [100, 3], 4, 2, 64, 16, "int8", extra_width=600)
     dev = [t.cuda() for t in (q, kc, vc, ks, vs)] + [ints(torch, table), ints(torch, lens)]
     want = gdn.attn_decode(*dev)
     out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
