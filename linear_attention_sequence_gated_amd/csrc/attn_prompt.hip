@@ -39,6 +39,77 @@ constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
 constexpr float kLowest = -3e38f;  // running maximum before the first token
 constexpr float kSlack = 8.f;      // the maximum in use may lie this far (powers of two) below the true one
 
+// What a wave carries over the keys: lane l has row l % 32, its output columns
+// as in the accumulators; m is shared by the two lanes of a row, l is the lane's
+// own part.
+template <int D> struct Rows {
+  f32x16 o[D / 32];
+  float m, l;
+  __device__ __forceinline__ void clear() {
+    m = kLowest;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = zero16();
+  }
+};
+
+// One staged tile of 32 NH keys; MASKED: only keys from .. upto (less 4 hl) of it
+// are seen by the lane's row.
+// keys_done() is called when the keys have been read, values_due() before the values are.
+template <int D, int NH, bool MASKED, class F, class G>
+__device__ __forceinline__ void take_keys(Rows<D>& x, const __bf16* kt, const __bf16* vt, int kb0, int vb0,
+                                          const u32x4 (&q)[D / 16], float c, int from, int upto, F keys_done, G values_due) {
+  constexpr int KS = D / 16, DT = D / 32;
+  const int kb = fresh(kb0), vb = fresh(vb0);
+  f32x16 s[NH];
+#pragma unroll
+  for (int n = 0; n < NH; ++n) {
+    s[n] = zero16();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) s[n] = mma(row_frag<D>(kt, kb, 32 * n, ks), q[ks], s[n]);
+  }
+  keys_done();
+  if constexpr (MASKED) {
+#pragma unroll
+    for (int n = 0; n < NH; ++n) {
+      const unsigned seen = bits(from - 32 * n, upto - 32 * n);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[n][e] = where_seen<false>(s[n][e], seen, e);
+    }
+  }
+  float top = s[0][0];
+#pragma unroll
+  for (int n = 0; n < NH; ++n)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = fmaxf(top, s[n][e]);
+  top = max_halves(top) * c;
+  if (__any(top > x.m + kSlack)) {
+    const float to = fmaxf(x.m, top), f = __builtin_amdgcn_exp2f(x.m - to);
+    x.m = to;
+    x.l *= f;
+#pragma unroll
+    for (int i = 0; i < DT; ++i) x.o[i] *= f;
+  }
+  u32x4 p[2 * NH];
+  float sum = 0.f;
+#pragma unroll
+  for (int n = 0; n < NH; ++n) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      s[n][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][e], c, -x.m));
+      sum += s[n][e];
+    }
+    p[2 * n] = operand(s[n], 0);
+    p[2 * n + 1] = operand(s[n], 1);
+  }
+  x.l += sum;
+  values_due();
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int b = 0; b < 2 * NH; ++b) x.o[i] = mma(col_frag<D>(vt, vb, 16 * b, i), p[b], x.o[i]);
+}
+
 template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 3) void attn_prompt_kernel(PromptArgs a) {
   // keys of a staged tile: 64 at D = 64, where 125 registers let four workgroups
   // share a CU (578 us for 1 x 16384 x 16/4 x 64; with 32 keys 620); 32 at
@@ -108,10 +179,8 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 3) 
   for (int ks = 0; ks < KS; ++ks) q[ks] ^= flip;
   const int from = beg - 4 * hl, upto = beg < 0 ? -8 : row - 4 * hl;  // the keys that the lane's row sees, less 4 hl
 
-  f32x16 o[DT];
-  float m = kLowest, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < DT; ++i) o[i] = zero16();
+  Rows<D> x;
+  x.clear();
 
   const int kb0 = row_base<D>(lane), vb0 = col_base<D>(lane);
   Stage<D, kN, NW> sk, sv;
@@ -128,56 +197,6 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 3) 
   // and its weight of zero must not meet them; they are added to the rows that
   // see them when all is written
   int dirty_lo = last, dirty_hi = 0;
-  // one tile of keys; MASKED: some of its keys are not seen by some of the rows
-  auto step = [&](auto masked_, int buf, int kv) {
-    constexpr bool MASKED = decltype(masked_)::value;
-    const int kb = fresh(kb0), vb = fresh(vb0);
-    f32x16 s[NH];
-#pragma unroll
-    for (int n = 0; n < NH; ++n) {
-      s[n] = zero16();
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) s[n] = mma(row_frag<D>(kt[buf], kb, 32 * n, ks), q[ks], s[n]);
-    }
-    if constexpr (MASKED) {
-#pragma unroll
-      for (int n = 0; n < NH; ++n) {
-        const unsigned seen = bits(from - kv - 32 * n, upto - kv - 32 * n);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[n][e] = where_seen<false>(s[n][e], seen, e);
-      }
-    }
-    float top = s[0][0];
-#pragma unroll
-    for (int n = 0; n < NH; ++n)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[n][e]);
-    top = max_halves(top) * c;
-    if (__any(top > m + kSlack)) {
-      const float to = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - to);
-      m = to;
-      l *= f;
-#pragma unroll
-      for (int i = 0; i < DT; ++i) o[i] *= f;
-    }
-    u32x4 p[2 * NH];
-    float sum = 0.f;
-#pragma unroll
-    for (int n = 0; n < NH; ++n) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        s[n][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][e], c, -m));
-        sum += s[n][e];
-      }
-      p[2 * n] = operand(s[n], 0);
-      p[2 * n + 1] = operand(s[n], 1);
-    }
-    l += sum;
-#pragma unroll
-    for (int i = 0; i < DT; ++i)
-#pragma unroll
-      for (int b = 0; b < 2 * NH; ++b) o[i] = mma(col_frag<D>(vt[buf], vb, 16 * b, i), p[b], o[i]);
-  };
   stage(0, first);
   int buf = 0, kv = first;
   auto next = [&] {
@@ -200,17 +219,17 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 3) 
   auto edge = [&](int end) {
     for (; kv < end; kv += kN, buf ^= 1) {
       next();
-      if (kv <= w0 + 31 && kv + kN > lowest) step(std::true_type{}, buf, kv);
+      if (kv <= w0 + 31 && kv + kN > lowest) take_keys<D, NH, true>(x, kt[buf], vt[buf], kb0, vb0, q, c, from - kv, upto - kv, [] {}, [] {});
     }
   };
   edge(min(highest, last));
   for (; kv + kN - 1 <= w0; kv += kN, buf ^= 1) {
     next();
-    step(std::false_type{}, buf, kv);
+    take_keys<D, NH, false>(x, kt[buf], vt[buf], kb0, vb0, q, c, 0, 0, [] {}, [] {});
   }
   edge(last);
 
-  const float z = sum_halves(l);
+  const float z = sum_halves(x.l);
   const bool rest = beg < 0 && row < a.T && a.zero_rest;
   if (beg < 0 && !rest) return;
   const float inv = rest ? 0.f : 1.f / z;
@@ -220,23 +239,177 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 3) 
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       *reinterpret_cast<u32x2*>(dst + 32 * i + 8 * e + 4 * hl) =
-          pipe::cvt4(f32x4{o[i][4 * e] * inv, o[i][4 * e + 1] * inv, o[i][4 * e + 2] * inv, o[i][4 * e + 3] * inv});
-  if (hl == 0) a.lse[(size_t)hq * a.T + row] = rest ? 0.f : (m + __builtin_amdgcn_logf(z)) * kLn2;
+          pipe::cvt4(f32x4{x.o[i][4 * e] * inv, x.o[i][4 * e + 1] * inv, x.o[i][4 * e + 2] * inv, x.o[i][4 * e + 3] * inv});
+  if (hl == 0) a.lse[(size_t)hq * a.T + row] = rest ? 0.f : (x.m + __builtin_amdgcn_logf(z)) * kLn2;
   if (rest) return;
   for (int key = max(beg, dirty_lo); key <= row && key < dirty_hi; ++key) {
     const __bf16* src = static_cast<const __bf16*>(a.v) + (long long)key * a.vs + (long long)kvh * D;
     for (int d = 4 * hl; d < D; d += 8)  // the entries that this lane stored
       for (int i = 0; i < 4; ++i) {
-        const float x = (float)src[d + i];
-        if (!__builtin_isfinite(x)) dst[d + i] = (__bf16)((float)dst[d + i] + x);
+        const float y = (float)src[d + i];
+        if (!__builtin_isfinite(y)) dst[d + i] = (__bf16)((float)dst[d + i] + y);
       }
+  }
+}
+
+// Few rows: a workgroup takes 32 rows of one head and its waves every NW-th tile
+// of their keys, each staging its own and waiting for nobody; what they have is
+// joined through LDS at the end.  A row's chain of tiles is a quarter as long for
+// four times the reads of keys: 1 x 1000 x 16/4 x 128 15.6 us for 36.2, 1 x 2500
+// x 12/4 x 64 25 for 50, 1 x 131 5.2 for 6.6; 8 x 2048 112 for 75.
+template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_split_kernel(PromptArgs a) {
+  constexpr int kN = 32, NT = 64 * NW, KS = D / 16, DT = D / 32, LD = D + 4;
+  __shared__ union alignas(16) {
+    __bf16 staged[NW][2][kN * D];
+    float part[NW][32][LD];
+  } mem;
+  auto& part = mem.part;
+  __shared__ float ml[NW][2][32];
+  __shared__ int begs[32], window[kWindow], dirty[2][NW];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
+  const int tiles = (a.T + 31) / 32;
+  const int rank = blockIdx.x / a.Hq, hq = blockIdx.x - rank * a.Hq;
+  const int r0 = (tiles - 1 - rank) * 32, kvh = hq / (a.Hq / a.Hkv);
+
+  const int row = r0 + (lane & 31);
+  u32x4 q[KS];
+  find_rows<32, NT>(a.cu, a.R, a.T, r0, window, begs, nullptr, [&] {
+    const __hip_bfloat16* src =
+        static_cast<const __hip_bfloat16*>(a.q) + (long long)min(row, a.T - 1) * a.qs + (long long)hq * D + 8 * hl;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) q[ks] = *reinterpret_cast<const u32x4*>(src + 16 * ks);
+  });
+  const int beg = begs[row - r0];
+  const KeyRange range = key_range(beg, row, a.T);
+  const int first = range.first, latest = range.latest, last = range.last;
+  if (last < 0) {  // no row of the tile is in a sequence
+    if (a.zero_rest) {
+      zero_rows<D>(static_cast<__bf16*>(a.out) + (long long)hq * D, (long long)a.Hq * D, r0, min(32, a.T - r0), NT);
+      if (tid < 32 && r0 + tid < a.T) a.lse[(size_t)hq * a.T + r0 + tid] = 0.f;
+    }
+    return;
+  }
+  const float c = fmaxf(__builtin_fabsf(a.scale) * kLog2e, 1e-37f);
+  const unsigned flip = a.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) q[ks] ^= flip;
+  const int from = beg - 4 * hl, upto = beg < 0 ? -8 : row - 4 * hl;
+
+  Rows<D> x;
+  x.clear();
+  const int kb0 = row_base<D>(lane), vb0 = col_base<D>(lane);
+  Stage<D, kN, 1> sk, sv;
+  sk.init(a.ks, 0);
+  sv.init(a.vs, 0);
+  const __hip_bfloat16* kp = static_cast<const __hip_bfloat16*>(a.k) + (long long)kvh * D;
+  const __hip_bfloat16* vp = static_cast<const __hip_bfloat16*>(a.v) + (long long)kvh * D;
+  // one buffer each: the next keys are on their way while the values are used,
+  // the next values while the keys are, so that more workgroups share a CU
+  __bf16 *kt = mem.staged[wave][0], *vt = mem.staged[wave][1];
+  auto stage_keys = [&](int kv) { sk.load(kt, rows_rsrc(kp, a.ks, kv, min(kN, last - kv), D), 0); };
+  auto stage_values = [&](int kv) { sv.load(vt, rows_rsrc(vp, a.vs, kv, min(kN, last - kv), D), 0); };
+  constexpr int kLoads = Stage<D, kN, 1>::LOADS;
+  int dirty_lo = last, dirty_hi = 0, kv = first + kN * wave;
+  if (kv < last) {
+    stage_keys(kv);
+    stage_values(kv);
+  }
+  for (; kv < last; kv += kN * NW) {
+    const int to = kv + kN * NW;
+    wait_all_but<kLoads>();
+    auto keys_done = [&] {
+      if (to < last) {
+        wait_read();
+        stage_keys(to);
+      }
+    };
+    auto values_due = [&] {
+      if (to < last) wait_all_but<kLoads>();
+      else wait_all_but<0>();
+    };
+    if (kv + kN - 1 > r0 || kv < latest || kv + kN > last) {
+      take_keys<D, 1, true>(x, kt, vt, kb0, vb0, q, c, from - kv, upto - kv, keys_done, [&] {
+        values_due();
+        if (!Stage<D, kN, 1>::scrub(vt, 0)) {
+          dirty_lo = min(dirty_lo, kv);
+          dirty_hi = kv + kN;
+        }
+      });
+    } else {
+      take_keys<D, 1, false>(x, kt, vt, kb0, vb0, q, c, 0, 0, keys_done, values_due);
+    }
+    if (to < last) {
+      wait_read();
+      stage_values(to);
+    }
+  }
+
+  const float z = sum_halves(x.l);
+  if (lane < 32) {
+    ml[wave][0][lane] = x.m;
+    ml[wave][1][lane] = z;
+  }
+  if (lane == 0) {
+    dirty[0][wave] = dirty_lo;
+    dirty[1][wave] = dirty_hi;
+  }
+  __syncthreads();
+  {
+    float M = ml[0][0][lane & 31];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) M = fmaxf(M, ml[w][0][lane & 31]);
+    const float f = __builtin_amdgcn_exp2f(x.m - M);
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<f32x4*>(&part[wave][lane & 31][32 * i + 8 * e + 4 * hl]) =
+            f32x4{x.o[i][4 * e] * f, x.o[i][4 * e + 1] * f, x.o[i][4 * e + 2] * f, x.o[i][4 * e + 3] * f};
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    dirty_lo = min(dirty_lo, dirty[0][w]);
+    dirty_hi = max(dirty_hi, dirty[1][w]);
+  }
+  for (int i = tid; i < 32 * (D / 4); i += NT) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4, b = begs[r];
+    if (r0 + r >= a.T || (b < 0 && !a.zero_rest)) continue;
+    float M = ml[0][0][r], L = 0.f;
+#pragma unroll
+    for (int w = 1; w < NW; ++w) M = fmaxf(M, ml[w][0][r]);
+    f32x4 o = pipe::zero4();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      L += ml[w][1][r] * __builtin_amdgcn_exp2f(ml[w][0][r] - M);
+      o += *reinterpret_cast<const f32x4*>(&part[w][r][d]);
+    }
+    o *= 1.f / L;
+    if (b >= 0)
+      for (int key = max(b, dirty_lo); key <= r0 + r && key < dirty_hi; ++key) {
+        const __bf16* src = static_cast<const __bf16*>(a.v) + (long long)key * a.vs + (long long)kvh * D + d;
+        for (int j = 0; j < 4; ++j)
+          if (!__builtin_isfinite((float)src[j])) o[j] += (float)src[j];
+      }
+    if (b < 0) o = pipe::zero4();
+    *reinterpret_cast<u32x2*>(static_cast<__bf16*>(a.out) + ((size_t)(r0 + r) * a.Hq + hq) * D + d) = pipe::cvt4(o);
+    if (d == 0) a.lse[(size_t)hq * a.T + r0 + r] = b < 0 ? 0.f : (M + __builtin_amdgcn_logf(L)) * kLn2;
   }
 }
 
 template <int D> hipError_t launch(const PromptArgs& a) {
   constexpr int NW = 4;
+  hipStream_t st = static_cast<hipStream_t>(a.stream);
+  if (split_keys(a.T, a.R, a.Hq, D)) {
+    const dim3 grid((unsigned)((a.T + 31) / 32 * a.Hq));
+    if constexpr (D == 64)
+      // few workgroups with long chains: eight waves (1 x 600 x 12/4 x 64 6.9 us for
+      // 8.3 with four, 4 x 512 13.3 for 10.3)
+      if (grid.x <= 512 && a.T >= 256LL * a.R) return launch_kernel(attn_prompt_split_kernel<D, 8>, grid, dim3(512), st, a);
+    return launch_kernel(attn_prompt_split_kernel<D, 4>, grid, dim3(256), st, a);
+  }
   const unsigned tiles = (unsigned)((a.T + 32 * NW - 1) / (32 * NW));
-  return launch_kernel(attn_prompt_kernel<D, NW>, dim3(tiles * a.Hq), dim3(64 * NW), static_cast<hipStream_t>(a.stream), a);
+  return launch_kernel(attn_prompt_kernel<D, NW>, dim3(tiles * a.Hq), dim3(64 * NW), st, a);
 }
 
 }  // namespace

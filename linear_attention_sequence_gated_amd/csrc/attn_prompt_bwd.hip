@@ -24,6 +24,8 @@
 // Bound by the matrix and the vector unit together, as the forward: 8 x 2048 x
 // 12 x 64 takes 106 us for dq and 151 for dk and dv, 2 x 4096 x 16/4 x 128
 // with the forward 670 us, 930 TFLOP/s.
+#include <algorithm>
+
 #include "../../include/gdn.h"
 #include "gdn_attn.hpp"
 #include "gdn_launch.hpp"
@@ -70,7 +72,79 @@ __device__ __forceinline__ void spoil(T* dst, const void* src, long long stride,
   }
 }
 
+// The waves' sums of 32 rows (a lane's row: l % 32), one beside the other in LDS,
+// and what they add up to.  The first begins and ends with a barrier.
+template <int D, int NW> using Parts = float[NW][32][D + 4];
+template <int D, int NW>
+__device__ __forceinline__ void join_rows(Parts<D, NW>& part, const f32x16 (&acc)[D / 32], int wave, int lane) {
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<f32x4*>(&part[wave][lane & 31][32 * i + 8 * e + 4 * (lane >> 5)]) =
+          f32x4{acc[i][4 * e], acc[i][4 * e + 1], acc[i][4 * e + 2], acc[i][4 * e + 3]};
+  __syncthreads();
+}
+template <int D, int NW> __device__ __forceinline__ f32x4 joined(const Parts<D, NW>& part, int r, int d) {
+  f32x4 o = *reinterpret_cast<const f32x4*>(&part[0][r][d]);
+#pragma unroll
+  for (int w = 1; w < NW; ++w) o += *reinterpret_cast<const f32x4*>(&part[w][r][d]);
+  return o;
+}
+
+// Whether rows [lo, hi) of src hold a value that is not finite.
+template <int D> __device__ __forceinline__ bool spoiled(const void* src, long long stride, int lo, int hi) {
+  bool any = false;
+  for (int i = lo; i < hi; ++i)
+    for (int d = 0; d < D; ++d) any |= !__builtin_isfinite((float)(static_cast<const __bf16*>(src) + (long long)i * stride)[d]);
+  return any;
+}
+
 // ---------------------------------------------------------------------- dq
+// do . o of a row, of which each half-wave holds half of do as operands.
+template <int D>
+__device__ __forceinline__ float delta_of(const PromptBwdArgs& a, int row, int hq, const u32x4 (&g)[D / 16], int hl) {
+  const __bf16* op = static_cast<const __bf16*>(a.out) + ((long long)row * a.Hq + hq) * D + 8 * hl;
+  float delta = 0.f;
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const u32x4 o = *reinterpret_cast<const u32x4*>(op + 16 * ks);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      delta = __builtin_fmaf(pipe::lo_f(g[ks][e]), pipe::lo_f(o[e]), delta);
+      delta = __builtin_fmaf(pipe::hi_f(g[ks][e]), pipe::hi_f(o[e]), delta);
+    }
+  }
+  return sum_halves(delta);
+}
+
+// 32 keys, rows n0 .. of the staged K and V, for a wave's 32 rows, of which the
+// lane's sees keys from .. upto (less 4 hl) if MASKED; values_done() is called
+// when V has been read.
+template <int D, bool MASKED, class F>
+__device__ __forceinline__ void dq_tile(f32x16 (&dq)[D / 32], float& rest, const __bf16* K, const __bf16* V, int rb, int cb,
+                                        int n0, const u32x4 (&q)[D / 16], const u32x4 (&g)[D / 16], float c, float lse2,
+                                        float delta, int from, int upto, F values_done) {
+  const unsigned seen = bits(from, upto);
+  f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    s = mma(row_frag<D>(K, rb, n0, ks), q[ks], s);
+    dp = mma(row_frag<D>(V, rb, n0, ks), g[ks], dp);
+  }
+  values_done();
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -lse2));
+    s[e] = p * (dp[e] - delta);
+    if constexpr (MASKED) s[e] = where_seen<true>(s[e], seen, e);
+    rest += s[e];
+  }
+#pragma unroll
+  for (int b = 0; b < 2; ++b) add_columns<D>(dq, K, cb, n0 + 16 * b, operand(s, b));
+}
+
 template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(PromptBwdArgs a) {
   constexpr int BM = 32 * NW, NT = 64 * NW, KS = D / 16;
   __shared__ alignas(16) __bf16 kt[2][kN * D], vt[2][kN * D];
@@ -126,20 +200,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
     return;
   }
 
-  float delta = 0.f;
-  {
-    const __bf16* op = static_cast<const __bf16*>(a.out) + ((long long)at * a.Hq + hq) * D + 8 * hl;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const u32x4 o = *reinterpret_cast<const u32x4*>(op + 16 * ks);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        delta = __builtin_fmaf(pipe::lo_f(g[ks][e]), pipe::lo_f(o[e]), delta);
-        delta = __builtin_fmaf(pipe::hi_f(g[ks][e]), pipe::hi_f(o[e]), delta);
-      }
-    }
-  }
-  delta = sum_halves(delta);
+  const float delta = delta_of<D>(a, at, hq, g, hl);
   const float lse2 = a.lse[(size_t)hq * a.T + at] * kLog2e;
 
   f32x16 dq[D / 32];
@@ -167,24 +228,8 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
     constexpr bool MASKED = decltype(masked_)::value;
     const int rb = fresh(rb0), cb = fresh(cb0);
 #pragma unroll 1
-    for (int n = 0; n < 2; ++n) {
-      const unsigned seen = bits(from - kv - 32 * n, upto - kv - 32 * n);
-      f32x16 s = zero16(), dp = zero16();
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        s = mma(row_frag<D>(K, rb, 32 * n, ks), q[ks], s);
-        dp = mma(row_frag<D>(V, rb, 32 * n, ks), g[ks], dp);
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -lse2));
-        s[e] = p * (dp[e] - delta);
-        if constexpr (MASKED) s[e] = where_seen<true>(s[e], seen, e);
-        rest += s[e];
-      }
-#pragma unroll
-      for (int b = 0; b < 2; ++b) add_columns<D>(dq, K, cb, 32 * n + 16 * b, operand(s, b));
-    }
+    for (int n = 0; n < 2; ++n)
+      dq_tile<D, MASKED>(dq, rest, K, V, rb, cb, 32 * n, q, g, c, lse2, delta, from - kv - 32 * n, upto - kv - 32 * n, [] {});
   };
   stage(0, first);
   auto next = [&] {
@@ -225,6 +270,115 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
   if (dirty_hi && beg >= 0)  // a key that is not finite spoils the weights of all rows that see it
     spoil<D>(static_cast<__bf16*>(a.grad_q) + (long long)row * a.gqs + (long long)hq * D, kp, a.ks, max(beg, dirty_lo),
              min(row + 1, dirty_hi), true, hl);
+}
+
+// Few rows, as in the forward: a workgroup takes 32 rows and its waves every
+// NW-th tile of 32 keys, each staging its own; their sums are added at the end.
+// With the same for dk and dv: forward and gradients of 1 x 1000 x 12/4 x 64 41 us
+// for 76, 1 x 2500 x 16/4 x 128 211 for 297.
+template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_split_kernel(PromptBwdArgs a) {
+  constexpr int NT = 64 * NW, KS = D / 16, LD = D + 4;
+  __shared__ union alignas(16) {
+    __bf16 staged[NW][2][32 * D];
+    float part[NW][32][LD];
+  } mem;
+  __shared__ float rests[NW][32];
+  __shared__ int begs[32], window[kWindow], dirty[2][NW];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
+  const int tiles = (a.T + 31) / 32;
+  const int rank = blockIdx.x / a.Hq, hq = blockIdx.x - rank * a.Hq;
+  const int r0 = (tiles - 1 - rank) * 32, kvh = hq / (a.Hq / a.Hkv);
+
+  const int row = r0 + (lane & 31), at = min(row, a.T - 1);
+  const float c = a.scale * kLog2e;
+  u32x4 q[KS], g[KS];
+  find_rows<32, NT>(a.cu, a.R, a.T, r0, window, begs, nullptr, [&] {
+    const __bf16* qp = static_cast<const __bf16*>(a.q) + (long long)at * a.qs + (long long)hq * D + 8 * hl;
+    const __bf16* gp = static_cast<const __bf16*>(a.grad_out) + (long long)at * a.gos + (long long)hq * D + 8 * hl;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      q[ks] = *reinterpret_cast<const u32x4*>(qp + 16 * ks);
+      g[ks] = *reinterpret_cast<const u32x4*>(gp + 16 * ks);
+    }
+  });
+  const int beg = begs[row - r0];
+  const KeyRange range = key_range(beg, row, a.T);
+  const int first = range.first, latest = range.latest, last = range.last;
+  if (last < 0) {  // no row of the tile is in a sequence
+    if (a.zero_rest) zero_rows<D>(static_cast<__bf16*>(a.grad_q) + (long long)hq * D, a.gqs, r0, min(32, a.T - r0), NT);
+    return;
+  }
+  const float delta = delta_of<D>(a, at, hq, g, hl), lse2 = a.lse[(size_t)hq * a.T + at] * kLog2e;
+
+  f32x16 dq[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) dq[i] = zero16();
+  const int rb0 = row_base<D>(lane), cb0 = col_base<D>(lane);
+  Stage<D, 32, 1> sk, sv;
+  sk.init(a.ks, 0);
+  sv.init(a.vs, 0);
+  const __bf16* kp = static_cast<const __bf16*>(a.k) + (long long)kvh * D;
+  const __bf16* vp = static_cast<const __bf16*>(a.v) + (long long)kvh * D;
+  __bf16 *kt = mem.staged[wave][0], *vt = mem.staged[wave][1];
+  const int from = beg - 4 * hl, upto = beg < 0 ? -8 : row - 4 * hl;
+  float rest = 0.f;
+  int dirty_lo = last, dirty_hi = 0, kv = first + 32 * wave;
+  auto stage_keys = [&](int kv) { sk.load(kt, rows_rsrc(kp, a.ks, kv, min(32, last - kv), D), 0); };
+  auto stage_values = [&](int kv) { sv.load(vt, rows_rsrc(vp, a.vs, kv, min(32, last - kv), D), 0); };
+  if (kv < last) {
+    stage_keys(kv);
+    stage_values(kv);
+  }
+  for (; kv < last; kv += 32 * NW) {
+    const int to = kv + 32 * NW, rb = fresh(rb0), cb = fresh(cb0);
+    wait_staged();
+    auto values_done = [&] {
+      if (to < last) {
+        wait_read();
+        stage_values(to);
+      }
+    };
+    if (kv + 31 > r0 || kv < latest || kv + 32 > last) {
+      if (!Stage<D, 32, 1>::scrub(kt, 0)) {
+        dirty_lo = min(dirty_lo, kv);
+        dirty_hi = kv + 32;
+      }
+      dq_tile<D, true>(dq, rest, kt, vt, rb, cb, 0, q, g, c, lse2, delta, from - kv, upto - kv, values_done);
+    } else {
+      dq_tile<D, false>(dq, rest, kt, vt, rb, cb, 0, q, g, c, lse2, delta, 0, 0, values_done);
+    }
+    if (to < last) {
+      wait_read();
+      stage_keys(to);
+    }
+  }
+  const float off = sum_halves(rest);
+  if (hl == 0) rests[wave][lane] = off;
+  if (lane == 0) {
+    dirty[0][wave] = dirty_lo;
+    dirty[1][wave] = dirty_hi;
+  }
+  join_rows<D, NW>(mem.part, dq, wave, lane);
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    dirty_lo = min(dirty_lo, dirty[0][w]);
+    dirty_hi = max(dirty_hi, dirty[1][w]);
+  }
+  if (wave == 0 && hl == 0 && beg >= 0) {
+    float more = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) more += rests[w][lane];
+    a.ws[(size_t)hq * a.T + row] = lse2;
+    a.ws[(size_t)(a.Hq + hq) * a.T + row] = -(delta + more);
+  }
+  for (int i = tid; i < 32 * (D / 4); i += NT) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4, b = begs[r];
+    if (r0 + r >= a.T || (b < 0 && !a.zero_rest)) continue;
+    f32x4 o = joined<D, NW>(mem.part, r, d) * (b < 0 ? 0.f : a.scale);
+    if (b < 0) o = pipe::zero4();
+    if (b >= 0 && spoiled<D>(kp, a.ks, max(b, dirty_lo), min(r0 + r + 1, dirty_hi))) o += __builtin_nanf("");
+    *reinterpret_cast<u32x2*>(static_cast<__bf16*>(a.grad_q) + (long long)(r0 + r) * a.gqs + (long long)hq * D + d) = pipe::cvt4(o);
+  }
 }
 
 // ------------------------------------------------------------------ dk, dv
@@ -282,14 +436,28 @@ __device__ __forceinline__ void spoil_grad(const PromptBwdArgs& a, const Share& 
   }
 }
 
-// Adds the shares of 32 keys of one key head, in their order.
+// The same for four entries, d on, of a key's sums.
+template <int D>
+__device__ __forceinline__ void spoil_sums(f32x4& o, const PromptBwdArgs& a, const Share& sh, bool values, int key, int end, int d) {
+  for (int h = sh.h0; h < sh.h0 + sh.heads; ++h) {
+    const __bf16 *q = static_cast<const __bf16*>(a.q) + (long long)h * D, *g = static_cast<const __bf16*>(a.grad_out) + (long long)h * D;
+    if (spoiled<D>(q, a.qs, key, end) || (!values && spoiled<D>(g, a.gos, key, end))) o += __builtin_nanf("");
+    if (values)
+      for (int i = key; i < end; ++i)
+        for (int j = 0; j < 4; ++j)
+          if (!__builtin_isfinite((float)g[(long long)i * a.gos + d + j])) o[j] = __builtin_nanf("");
+  }
+}
+
+// Adds the shares of kSumRows keys of one key head, in their order.
+constexpr int kSumRows = 8;
 template <int D> __global__ __launch_bounds__(256) void attn_dkv_sum_kernel(PromptBwdArgs a) {
-  __shared__ int begs[32], window[kWindow];
+  __shared__ int begs[kSumRows], window[kWindow];
   const int tile = blockIdx.x / a.Hkv, kvh = blockIdx.x - tile * a.Hkv;
-  find_rows<32, 256>(a.cu, a.R, a.T, tile * 32, window, begs, nullptr, [] {});
-  for (int x = threadIdx.x; x < 2 * 32 * (D / 4); x += 256) {
-    const bool values = x >= 32 * (D / 4);
-    const int i = x % (32 * (D / 4)) / (D / 4), d = x % (D / 4) * 4, row = tile * 32 + i;
+  find_rows<kSumRows, 256>(a.cu, a.R, a.T, tile * kSumRows, window, begs, nullptr, [] {});
+  for (int x = threadIdx.x; x < 2 * kSumRows * (D / 4); x += 256) {
+    const bool values = x >= kSumRows * (D / 4);
+    const int i = x % (kSumRows * (D / 4)) / (D / 4), d = x % (D / 4) * 4, row = tile * kSumRows + i;
     const bool in = begs[i] >= 0;
     if (row >= a.T || (!in && !a.zero_rest)) continue;
     f32x4 sum = pipe::zero4();
@@ -300,11 +468,52 @@ template <int D> __global__ __launch_bounds__(256) void attn_dkv_sum_kernel(Prom
   }
 }
 
+// 32 rows, n0 .. of the staged Q and dO with their lse and -delta, for a wave's
+// 32 keys: k their operands, v those of V or (VLDS) vt its rows from v0 on; the lane's key is seen by rows
+// from .. upto (less 4 hl) if MASKED.
+template <int D, bool MASKED, bool VLDS>
+__device__ __forceinline__ void dkv_tile(f32x16 (&dk)[D / 32], f32x16 (&dv)[D / 32], const __bf16* Q, const __bf16* O,
+                                         const float* lt, const float* dt, int rb, int cb, int n0,
+                                         const u32x4 (&k)[D / 16], const u32x4 (&v)[D / 16], const __bf16* vt, int v0, float c, int from, int upto, int hl) {
+  const unsigned seen = bits(from, upto);
+  f32x16 s = zero16(), dp;
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) s = mma(row_frag<D>(Q, rb, n0, ks), k[ks], s);
+#pragma unroll
+  for (int e4 = 0; e4 < 4; ++e4) {
+    const f32x4 d = *reinterpret_cast<const f32x4*>(&dt[n0 + 8 * e4 + 4 * hl]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dp[4 * e4 + j] = d[j];
+  }
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks)
+    dp = mma(row_frag<D>(O, rb, n0, ks), VLDS ? row_frag<D>(vt, rb, v0, ks) : v[ks], dp);
+#pragma unroll
+  for (int e4 = 0; e4 < 4; ++e4) {
+    const f32x4 l = *reinterpret_cast<const f32x4*>(&lt[n0 + 8 * e4 + 4 * hl]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = 4 * e4 + j;
+      s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -l[j]));
+      dp[e] = s[e] * dp[e];
+      if constexpr (MASKED) {
+        s[e] = where_seen<true>(s[e], seen, e);
+        dp[e] = where_seen<true>(dp[e], seen, e);
+      }
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    add_columns<D>(dv, O, cb, n0 + 16 * b, operand(s, b));
+    add_columns<D>(dk, Q, cb, n0 + 16 * b, operand(dp, b));
+  }
+}
+
 // One wave to 32 keys, rows in tiles of NR.  At D = 64 a wave holds K and V of
 // its keys as operands beside both accumulators (243 registers).  At D = 128
 // that would be 192 registers before the first score: V stays in LDS (VLDS),
 // which takes tiles of half as many rows, and every tile goes through the masked
-// body, since two bodies of this size take more registers than there are (237
+// body, since two bodies of this size take more registers than there are (256
 // with one; a bit mask per score costs less than a spill, whose reload waits for
 // the loads that stage the next tile).  Two waves that share the work of 32 keys
 // and hand the scores over through LDS took 260 us where this takes 155 (13
@@ -400,38 +609,8 @@ template <int D, int NW, int NR, bool VLDS> __global__ __launch_bounds__(64 * NW
     const int from = key - i1 - 4 * hl, upto = end - 1 - i1 - 4 * hl;  // the rows that see the lane's key
 #pragma unroll MASKED ? 1 : NR / 32
     for (int n = 0; n < NR / 32; ++n) {
-      const unsigned seen = bits(from - 32 * n, upto - 32 * n);
-      f32x16 s = zero16(), dp;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) s = mma(row_frag<D>(Q, rb, 32 * n, ks), k[ks], s);
-#pragma unroll
-      for (int e4 = 0; e4 < 4; ++e4) {
-        const f32x4 d = *reinterpret_cast<const f32x4*>(&dt[buf][32 * n + 8 * e4 + 4 * hl]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dp[4 * e4 + j] = d[j];
-      }
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-        dp = mma(row_frag<D>(O, rb, 32 * n, ks), VLDS ? row_frag<D>(vt, rb, 32 * wave, ks) : v[ks], dp);
-#pragma unroll
-      for (int e4 = 0; e4 < 4; ++e4) {
-        const f32x4 l = *reinterpret_cast<const f32x4*>(&lt[buf][32 * n + 8 * e4 + 4 * hl]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int e = 4 * e4 + j;
-          s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -l[j]));
-          dp[e] = s[e] * dp[e];
-          if constexpr (MASKED) {
-            s[e] = where_seen<true>(s[e], seen, e);
-            dp[e] = where_seen<true>(dp[e], seen, e);
-          }
-        }
-      }
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        add_columns<D>(dv, O, cb, 32 * n + 16 * b, operand(s, b));
-        add_columns<D>(dk, Q, cb, 32 * n + 16 * b, operand(dp, b));
-      }
+      dkv_tile<D, MASKED, VLDS>(dk, dv, Q, O, lt[buf], dt[buf], rb, cb, 32 * n, k,
+                          v, vt, 32 * wave, c, from - 32 * n, upto - 32 * n, hl);
     }
   };
   if constexpr (VLDS) {
@@ -479,45 +658,162 @@ template <int D, int NW, int NR, bool VLDS> __global__ __launch_bounds__(64 * NW
   }
 }
 
+// Few keys: a workgroup takes 32 of one key head, and its waves every NW-th tile
+// of 32 rows of the share's query heads, one head after the other.
+template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_split_kernel(PromptBwdArgs a) {
+  constexpr int NT = 64 * NW, KS = D / 16;
+  constexpr bool VLDS = D == 128;
+  __shared__ union alignas(16) {
+    __bf16 staged[NW][2][32 * D];
+    Parts<D, NW> part;
+  } mem;
+  __shared__ alignas(16) float lt[NW][64], dt[NW][64];
+  __shared__ alignas(16) __bf16 vt[VLDS ? 32 * D : 8];
+  __shared__ int begs[32], ends[32], window[kWindow], dirty[NW];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
+  const Share sh = share_of(a);
+  const int r0 = sh.tile * 32, kvh = sh.kvh;
+  find_rows<32, NT>(a.cu, a.R, a.T, r0, window, begs, ends, [] {});
+  const int key = r0 + (lane & 31), end = ends[lane & 31], at = min(key, a.T - 1);
+  int last = end, soonest = end;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    last = max(last, __shfl_xor(last, d));
+    soonest = min(soonest, __shfl_xor(soonest, d));
+  }
+  last = __builtin_amdgcn_readfirstlane(last);
+  soonest = __builtin_amdgcn_readfirstlane(soonest);
+  if (last < 0) {
+    if (a.zero_rest && a.shares == 1) {
+      zero_rows<D>(static_cast<__bf16*>(a.grad_k) + (long long)kvh * D, a.gks, r0, min(32, a.T - r0), NT);
+      zero_rows<D>(static_cast<__bf16*>(a.grad_v) + (long long)kvh * D, a.gvs, r0, min(32, a.T - r0), NT);
+    }
+    return;
+  }
+  const float c = a.scale * kLog2e;
+  u32x4 k[KS], v[KS];
+  {
+    const __bf16* kp = static_cast<const __bf16*>(a.k) + (long long)at * a.ks + (long long)kvh * D + 8 * hl;
+    const __bf16* vp = static_cast<const __bf16*>(a.v) + (long long)at * a.vs + (long long)kvh * D + 8 * hl;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      k[ks] = *reinterpret_cast<const u32x4*>(kp + 16 * ks);
+      if (!VLDS) v[ks] = *reinterpret_cast<const u32x4*>(vp + 16 * ks);
+    }
+  }
+  if constexpr (VLDS) {
+    Stage<D, 32, NW> sv;
+    sv.init(a.vs, wave);
+    sv.load(vt, rows_rsrc(static_cast<const __bf16*>(a.v) + (long long)kvh * D, a.vs, r0, min(32, a.T - r0), D), wave);
+    staged_barrier();
+  }
+  f32x16 dk[D / 32], dv[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) dk[i] = dv[i] = zero16();
+  const int rb0 = row_base<D>(lane), cb0 = col_base<D>(lane);
+  Stage<D, 32, 1> sq, sg;
+  sq.init(a.qs, 0);
+  sg.init(a.gos, 0);
+  auto stage = [&](int head, int i1) {
+    const int n = min(32, last - i1), hq = sh.h0 + head;
+    sq.load(mem.staged[wave][0], rows_rsrc(static_cast<const __bf16*>(a.q) + (long long)hq * D, a.qs, i1, n, D), 0);
+    sg.load(mem.staged[wave][1], rows_rsrc(static_cast<const __bf16*>(a.grad_out) + (long long)hq * D, a.gos, i1, n, D), 0);
+    stage_words(lt[wave], pipe::make_rsrc(a.ws + (size_t)hq * a.T + i1, n * 4));
+    stage_words(dt[wave], pipe::make_rsrc(a.ws + (size_t)(a.Hq + hq) * a.T + i1, n * 4));
+  };
+  const int nt = (last - r0 + 31) / 32;  // tiles of rows to a head
+  bool bad = false;
+  int head = wave / nt, i = wave - head * nt;
+  __bf16 *Q = mem.staged[wave][0], *O = mem.staged[wave][1];
+  if (head < sh.heads) stage(head, r0 + 32 * i);
+  while (head < sh.heads) {
+    const int i1 = r0 + 32 * i, rb = fresh(rb0), cb = fresh(cb0);
+    for (i += NW; i >= nt && head < sh.heads; i -= nt) ++head;
+    wait_staged();
+    if (VLDS || i1 < r0 + 31 || i1 + 32 > soonest) {
+      if (i1 < r0 + 31 || i1 + 32 > soonest) {
+        const bool q_ok = Stage<D, 32, 1>::scrub(Q, 0), g_ok = Stage<D, 32, 1>::scrub(O, 0);
+        bad |= !(q_ok && g_ok);
+      }
+      dkv_tile<D, true, VLDS>(dk, dv, Q, O, lt[wave], dt[wave], rb, cb, 0, k, v, vt, 0, c, key - i1 - 4 * hl,
+                              end - 1 - i1 - 4 * hl, hl);
+    } else {
+      dkv_tile<D, false, VLDS>(dk, dv, Q, O, lt[wave], dt[wave], rb, cb, 0, k, v, vt, 0, c, 0, 0, hl);
+    }
+    if (head < sh.heads) {
+      wait_read();
+      stage(head, r0 + 32 * i);
+    }
+  }
+  if (lane == 0) dirty[wave] = bad;
+  for (int values = 0; values < 2; ++values) {
+    if (values) join_rows<D, NW>(mem.part, dv, wave, lane);
+    else join_rows<D, NW>(mem.part, dk, wave, lane);
+    const bool any = !all_clean(dirty);
+    for (int x = tid; x < 32 * (D / 4); x += NT) {
+      const int r = x / (D / 4), d = x % (D / 4) * 4, e = ends[r];
+      if (r0 + r >= a.T || (e < 0 && (!a.zero_rest || a.shares > 1))) continue;
+      f32x4 o = joined<D, NW>(mem.part, r, d) * (values ? 1.f : a.scale);
+      if (e < 0) o = pipe::zero4();
+      if (any && e >= 0) spoil_sums<D>(o, a, sh, values, r0 + r, e, d);
+      if (a.shares > 1)
+        *reinterpret_cast<f32x4*>(sums_row(a, D, sh.at, values, r0 + r, kvh) + d) = o;
+      else
+        *reinterpret_cast<u32x2*>(static_cast<__bf16*>(values ? a.grad_v : a.grad_k) +
+                                  (long long)(r0 + r) * (values ? a.gvs : a.gks) + (long long)kvh * D + d) = pipe::cvt4(o);
+    }
+  }
+}
+
 // Shares of the query heads that read one key head: as few as give the CUs
 // kEnough tiles of keys to choose from (the first tiles of a sequence meet many
 // more rows than its last, so few tiles leave most CUs waiting for the longest),
-// at most one head each.
+// at most one head each.  Half as many where tiles are small and their rows split
+// over waves (1 x 1000 x 16/4 x 128 67 us for 74 with a quarter), and no shares
+// where all heads together are a few tiles to a wave (4 x 128 x 12/4 x 64 19.4 us
+// for 20.7).
 constexpr int kEnough = 1024;
-int shares_of(int T, int Hq, int Hkv) {
+int shares_of(int T, int R, int Hq, int Hkv, int D) {
   const int G = Hq / Hkv;
-  const long long tiles = ((long long)T + 127) / 128 * Hkv;
+  const bool split = split_keys(T, R, Hq, D);
+  if (split && (long long)G * T <= 512LL * std::max(R, 1)) return 1;
+  const long long tiles = split ? ((long long)T + 31) / 32 * Hkv : ((long long)T + 127) / 128 * Hkv;
   for (int s = 1; s < G; ++s)
-    if (G % s == 0 && tiles * s >= kEnough) return s;
+    if (G % s == 0 && tiles * s >= (split ? kEnough / 2 : kEnough)) return s;
   return G;
 }
 
-template <int D> hipError_t launch(const PromptBwdArgs& a) {
-  const unsigned tiles = (unsigned)((a.T + 127) / 128);
+template <int D> hipError_t launch(const PromptBwdArgs& a, bool split) {
+  const unsigned tiles = (unsigned)((a.T + 127) / 128), fine = (unsigned)((a.T + 31) / 32);
   hipStream_t st = static_cast<hipStream_t>(a.stream);
-  hipError_t e = launch_kernel(attn_dq_kernel<D, 4>, dim3(tiles * a.Hq), dim3(256), st, a);
+  hipError_t e;
+  if (split) e = launch_kernel(attn_dq_split_kernel<D, 4>, dim3(fine * a.Hq), dim3(256), st, a);
+  else e = launch_kernel(attn_dq_kernel<D, 4>, dim3(tiles * a.Hq), dim3(256), st, a);
   if (e != hipSuccess) return e;
-  const dim3 grid(tiles * a.Hkv * a.shares);
-  if constexpr (D == 64) e = launch_kernel(attn_dkv_kernel<D, 4, 64, false>, grid, dim3(256), st, a);
+  const dim3 grid((split ? fine : tiles) * a.Hkv * a.shares);
+  if (split) e = launch_kernel(attn_dkv_split_kernel<D, 4>, grid, dim3(256), st, a);
+  else if constexpr (D == 64) e = launch_kernel(attn_dkv_kernel<D, 4, 64, false>, grid, dim3(256), st, a);
   else e = launch_kernel(attn_dkv_kernel<D, 4, 32, true>, grid, dim3(256), st, a);
   if (e != hipSuccess || a.shares == 1) return e;
-  return launch_kernel(attn_dkv_sum_kernel<D>, dim3((unsigned)((a.T + 31) / 32) * a.Hkv), dim3(256), st, a);
+  return launch_kernel(attn_dkv_sum_kernel<D>, dim3((unsigned)((a.T + kSumRows - 1) / kSumRows) * a.Hkv), dim3(256), st, a);
 }
 
 }  // namespace
 
 size_t attn_prompt_bwd_workspace_bytes(int T, int Hq, int Hkv, int D) {
-  const int shares = shares_of(T, Hq, Hkv);
+  // the most that any number of sequences takes
+  const int shares = std::max(shares_of(T, 1, Hq, Hkv, D), shares_of(T, T + 1, Hq, Hkv, D));
   const size_t sums = shares > 1 ? (size_t)shares * 2 * T * Hkv * D : 0;
   return (sums_at(T, Hq) + sums) * sizeof(float);
 }
 
 hipError_t launch_attn_prompt_bwd(const PromptBwdArgs& args) {
   PromptBwdArgs a = args;
-  a.shares = shares_of(a.T, a.Hq, a.Hkv);
+  const bool split = split_keys(a.T, a.R, a.Hq, a.D);
+  a.shares = shares_of(a.T, a.R, a.Hq, a.Hkv, a.D);
   a.by_length = rank_tiles(a.T, a.R, a.Hq);
   a.keys_by_length = rank_tiles(a.T, a.R, a.Hkv * a.shares);
-  return a.D == 64 ? launch<64>(a) : launch<128>(a);
+  return a.D == 64 ? launch<64>(a, split) : launch<128>(a, split);
 }
 
 }  // namespace gdn

@@ -75,6 +75,18 @@ inline bool rank_tiles(int T, int R, int per_tile) {
   const int tiles = (T + 127) / 128;
   return R > 1 && R < 512 && tiles <= 256 && (long long)tiles * per_tile > 512;
 }
+// Whether tiles of 32 rows, their keys split over the waves of a workgroup, are
+// faster than tiles of 128 that a workgroup's waves share the keys of: where the
+// chain of tiles that the last rows of a sequence go through counts for more than
+// the keys' being read four times as often.  With L keys to a sequence (their
+// mean), the chain is shorter by something like L, and the work larger by
+// something like T Hq (600 + L).  Both ways, us: 1 x 6000 x 12/4 x 64 97 for 117,
+// 2 x 4000 90 for 83, 4 x 512 10.3 for 11.7, 8 x 512 18.6 for 15.1; 1 x 3000 x 16/4
+// x 128 69 for 100, 1 x 6000 240 for 217, 16 x 64 8.8 for 9.6, 8 x 256 18.8 for 13.5.
+inline bool split_keys(int T, int R, int Hq, int D) {
+  const long long L = T / (R > 0 ? R : 1);
+  return (long long)T * Hq * (600 + L) < (D == 64 ? 82000 : 62000) * L;
+}
 hipError_t launch_attn_prompt(const PromptArgs& a);
 
 struct PromptBwdArgs {

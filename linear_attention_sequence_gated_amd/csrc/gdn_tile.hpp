@@ -199,6 +199,36 @@ __device__ __forceinline__ void staged_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// Until all but the last N of this wave's loads have arrived.
+template <int N> __device__ __forceinline__ void wait_all_but() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Until what this wave reads from LDS has arrived.
+__device__ __forceinline__ void wait_read() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// The keys that 32 rows (a lane's: l % 32) see, [first, last), and the last
+// beginning of a sequence among them; last < 0 if none is in a sequence.
+struct KeyRange {
+  int first, latest, last;
+};
+__device__ __forceinline__ KeyRange key_range(int beg, int row, int T) {
+  int first = beg < 0 ? T : beg, latest = first, last = beg < 0 ? -1 : row + 1;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    first = min(first, __shfl_xor(first, d));
+    latest = max(latest, __shfl_xor(latest, d));
+    last = max(last, __shfl_xor(last, d));
+  }
+  return {__builtin_amdgcn_readfirstlane(first), __builtin_amdgcn_readfirstlane(latest), __builtin_amdgcn_readfirstlane(last)};
+}
+
 // Sets rows [r0, r0 + n) of one head to zero, by NT threads.
 template <int D> __device__ __forceinline__ void zero_rows(__bf16* dst, long long stride, int r0, int n, int NT) {
   for (int i = threadIdx.x; i < n * (D / 8); i += NT)

@@ -12,6 +12,19 @@ from oracle import attention as ref
 from test_gpu_attn_cache import ints
 
 pytestmark = pytest.mark.gpu
+PAD = [False]
+
+
+@pytest.fixture(params=[False, True], ids=["as given", "padded"], autouse=True)
+def padded(request):
+    """With many sequences of no rows behind the others: few rows to a sequence choose the other tiles."""
+    PAD[0] = request.param
+    yield
+    PAD[0] = False
+
+
+def cu_of(torch, cu):
+    return ints(torch, np.concatenate([cu, np.repeat(cu[-1:], 260)]) if PAD[0] else cu)
 
 
 def make(torch, rng, T, Hq, H, D, fused=True, size=1.0):
@@ -30,7 +43,7 @@ def check_forward(torch, q, k, v, cu, scale=None):
     T, Hq, D = q.shape
     out = torch.full((T, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((Hq, T), 7.0, device="cuda")
-    gdn.attn_prompt(q, k, v, ints(torch, cu), scale, out=out, lse=lse)
+    gdn.attn_prompt(q, k, v, cu_of(torch, cu), scale, out=out, lse=lse)
     torch.cuda.synchronize()
     scale = D ** -0.5 if scale is None else scale
     qs, ks, vs = host(q, k, v)
@@ -104,7 +117,7 @@ def test_rows_outside_and_what_they_hold(D):
         x[cu[1]:cu[2]] = float("nan")
     v[cu[0] + 50, 0, 3], v[cu[0] + 60, 0, 4], k[cu[0] + 65] = float("inf"), -float("inf"), float("nan")
     import linear_attention_sequence_gated_amd as gdn
-    out2, lse2 = gdn.attn_prompt(q, k, v, ints(torch, cu))
+    out2, lse2 = gdn.attn_prompt(q, k, v, cu_of(torch, cu))
     keep = np.r_[cu[0]:cu[0] + 50, cu[2]:cu[3]]
     assert torch.equal(out2[keep], out[keep]) and torch.equal(lse2[:, keep], lse[:, keep])
     assert out2[cu[1]:cu[2]].isnan().all()
@@ -114,7 +127,7 @@ def test_rows_outside_and_what_they_hold(D):
     assert (late[..., 3] == float("inf")).all() and (late[..., 4] == -float("inf")).all()
     assert out2[cu[0] + 65:cu[1]].isnan().all()
     v[cu[0] + 62, 1 - 1, 3] = float("nan")
-    out3, _ = gdn.attn_prompt(q, k, v, ints(torch, cu))
+    out3, _ = gdn.attn_prompt(q, k, v, cu_of(torch, cu))
     assert out3[cu[0] + 62:cu[0] + 65, :, 3].isnan().all() and torch.equal(out3[cu[0]:cu[0] + 62], out2[cu[0]:cu[0] + 62])
 
 
@@ -157,5 +170,5 @@ def test_offsets_out_of_order(cu):
     import linear_attention_sequence_gated_amd as gdn
     q, k, v = make(torch, np.random.default_rng(9), 200, 2, 1, 64)
     note(f"offsets {cu}")
-    gdn.attn_prompt(q, k, v, ints(torch, cu))
+    gdn.attn_prompt(q, k, v, cu_of(torch, cu))
     torch.cuda.synchronize()

@@ -11,8 +11,7 @@ import pytest
 
 from gpu_util import note, torch_dev
 from oracle import attention as ref
-from test_gpu_attn_cache import ints
-from test_gpu_attn_prompt import RAGGED, host, make, offsets
+from test_gpu_attn_prompt import RAGGED, cu_of, host, make, offsets, padded  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 U, F = 2.0 ** -8, 2.0 ** -12
@@ -43,7 +42,7 @@ def check(torch, q, k, v, cu, scale=None, do=None, seed=0, into=None):
     H = k.shape[1]
     if do is None:
         do = torch.from_numpy(np.random.default_rng(seed + 99).standard_normal((T, Hq, D)).astype(np.float32)).to(torch.bfloat16).cuda()
-    c = ints(torch, cu)
+    c = cu_of(torch, cu)
     out, lse = gdn.attn_prompt(q, k, v, c, scale)
     grads = into or [torch.full((T, n, D), 7.0, dtype=torch.bfloat16, device="cuda") for n in (Hq, H, H)]
     got = gdn.attn_prompt_bwd(q, k, v, out, lse, do, c, scale, *grads)
@@ -109,7 +108,7 @@ def test_rows_outside_may_hold_anything(D):
     for bad in range(4):
         x = [t.clone() for t in (q, k, v, do)]
         x[bad][cu[1] + 12] = float("nan")
-        c = ints(torch, cu)
+        c = cu_of(torch, cu)
         out, lse = gdn.attn_prompt(*x[:3], c)
         got = gdn.attn_prompt_bwd(*x[:3], out, lse, x[3], c)
         keep = np.r_[cu[0]:cu[1], cu[2]:cu[3]]
@@ -131,7 +130,7 @@ def test_same_gradients_every_time():
     torch = torch_dev()
     import linear_attention_sequence_gated_amd as gdn
     q, k, v = make(torch, np.random.default_rng(8), 900, 8, 2, 64)
-    c, do = ints(torch, [0, 400, 900]), torch.ones(900, 8, 64, dtype=torch.bfloat16, device="cuda")
+    c, do = cu_of(torch, [0, 400, 900]), torch.ones(900, 8, 64, dtype=torch.bfloat16, device="cuda")
     out, lse = gdn.attn_prompt(q, k, v, c)
     a, b = (gdn.attn_prompt_bwd(q, k, v, out, lse, do, c) for _ in range(2))
     assert all(torch.equal(x, y) for x, y in zip(a, b))
@@ -167,7 +166,7 @@ def test_offsets_out_of_order(cu):
     torch = torch_dev()
     import linear_attention_sequence_gated_amd as gdn
     q, k, v = make(torch, np.random.default_rng(9), 200, 2, 1, 64)
-    c = ints(torch, cu)
+    c = cu_of(torch, cu)
     note(f"bwd offsets {cu}")
     out, lse = gdn.attn_prompt(q, k, v, c)
     gdn.attn_prompt_bwd(q, k, v, out, lse, out, c)
