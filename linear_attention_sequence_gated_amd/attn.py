@@ -130,6 +130,11 @@ def _decode_workspace(*sizes):
     return raw.gdn_attn_decode_workspace_bytes(*sizes)
 
 
+@functools.lru_cache(maxsize=1024)
+def _bwd_workspace(*sizes):
+    return raw.gdn_attn_prompt_bwd_workspace_bytes(*sizes)
+
+
 @_on_stream
 def attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale: float | None = None, out=None,
                 lse=None, workspace=None):
@@ -189,11 +194,11 @@ def attn_prompt(q, k, v, cu_seqlens, scale: float | None = None, out=None, lse=N
     dev, t, r, hq, hkv, d, strides = _prompt(q, k, v, cu_seqlens, "attn_prompt")
     zero_rest = out is None and lse is None
     if out is None:
-        out = (torch.empty if zero_rest else torch.zeros)((t, hq, d), dtype=_BF16, device=dev)
+        out = q.new_empty((t, hq, d)) if zero_rest else q.new_zeros((t, hq, d))
     else:
         _dense(out, "out", (t, hq, d), _BF16, dev)
     if lse is None:
-        lse = (torch.empty if zero_rest else torch.zeros)((hq, t), dtype=_F32, device=dev)
+        lse = q.new_empty((hq, t), dtype=_F32) if zero_rest else q.new_zeros((hq, t), dtype=_F32)
     else:
         _dense(lse, "lse", (hq, t), _F32, dev)
     _call(dev, raw.load().gdn_attn_prompt, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
@@ -214,17 +219,21 @@ def attn_prompt_bwd(q, k, v, out, lse, grad_out, cu_seqlens, scale: float | None
     dev, t, r, hq, hkv, d, strides = _prompt(q, k, v, cu_seqlens, "attn_prompt_bwd")
     _dense(out, "out", (t, hq, d), _BF16, dev)
     _dense(lse, "lse", (hq, t), _F32, dev)
-    shapes = {"grad_q": (t, hq, d), "grad_k": (t, hkv, d), "grad_v": (t, hkv, d)}
+    shapes = (t, hq, d), (t, hkv, d), (t, hkv, d)
     grads = (grad_q, grad_k, grad_v)
     zero_rest = all(g is None for g in grads)
-    make = torch.empty if zero_rest else torch.zeros
-    grads = [make(s, dtype=_BF16, device=dev) if g is None else g for g, s in zip(grads, shapes.values())]
-    gstrides = [_rows(g, n, s, dev) for g, (n, s) in zip(grads, shapes.items())]
+    if zero_rest:
+        grads = [q.new_empty(s) for s in shapes]
+        gstrides = hq * d, hkv * d, hkv * d
+    else:
+        grads = [q.new_zeros(s) if g is None else g for g, s in zip(grads, shapes)]
+        gstrides = [_rows(g, n, s, dev) for g, n, s in zip(grads, ("grad_q", "grad_k", "grad_v"), shapes)]
     gos = _rows(grad_out, "grad_out", (t, hq, d), dev)
     lib = raw.load()
-    ws = torch.empty(lib.gdn_attn_prompt_bwd_workspace_bytes(t, hq, hkv, d), dtype=torch.uint8, device=dev)
+    size = _bwd_workspace(t, hq, hkv, d)
+    ws = lse.new_empty(size // 4)
     _call(dev, lib.gdn_attn_prompt_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
           lse.data_ptr(), grad_out.data_ptr(), cu_seqlens.data_ptr(), *(g.data_ptr() for g in grads),
           d ** -0.5 if scale is None else scale, *strides, gos, *gstrides, t, r, hq, hkv, d, raw.GDN_BF16, zero_rest,
-          ws.data_ptr(), ws.numel())
+          ws.data_ptr(), size)
     return tuple(grads)
