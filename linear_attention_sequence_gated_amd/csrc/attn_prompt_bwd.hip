@@ -449,22 +449,45 @@ __device__ __forceinline__ void spoil_sums(f32x4& o, const PromptBwdArgs& a, con
   }
 }
 
-// Adds the shares of kSumRows keys of one key head, in their order.
+// Adds the shares of kSumRows keys of one key head, in their order.  The sums are
+// read before it is known which rows are in a sequence: those of the others are
+// what the workspace held, and left out.
 constexpr int kSumRows = 8;
 template <int D> __global__ __launch_bounds__(256) void attn_dkv_sum_kernel(PromptBwdArgs a) {
+  constexpr int kItems = 2 * kSumRows * (D / 4) / 256;
+  static_assert(kItems * 256 == 2 * kSumRows * (D / 4), "");
   __shared__ int begs[kSumRows], window[kWindow];
   const int tile = blockIdx.x / a.Hkv, kvh = blockIdx.x - tile * a.Hkv;
-  find_rows<kSumRows, 256>(a.cu, a.R, a.T, tile * kSumRows, window, begs, nullptr, [] {});
-  for (int x = threadIdx.x; x < 2 * kSumRows * (D / 4); x += 256) {
-    const bool values = x >= kSumRows * (D / 4);
-    const int i = x % (kSumRows * (D / 4)) / (D / 4), d = x % (D / 4) * 4, row = tile * kSumRows + i;
+  auto place = [&](int n, bool& values, int& i, int& d) {
+    const int x = threadIdx.x + 256 * n;
+    values = x >= kSumRows * (D / 4);
+    i = x % (kSumRows * (D / 4)) / (D / 4);
+    d = x % (D / 4) * 4;
+  };
+  f32x4 sum[kItems];
+  find_rows<kSumRows, 256>(a.cu, a.R, a.T, tile * kSumRows, window, begs, nullptr, [&] {
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) sum[n] = pipe::zero4();
+#pragma unroll 2
+    for (int s = 0; s < a.shares; ++s)
+#pragma unroll
+      for (int n = 0; n < kItems; ++n) {
+        bool values;
+        int i, d;
+        place(n, values, i, d);
+        sum[n] += *reinterpret_cast<const f32x4*>(sums_row(a, D, s, values, min(tile * kSumRows + i, a.T - 1), kvh) + d);
+      }
+  });
+#pragma unroll
+  for (int n = 0; n < kItems; ++n) {
+    bool values;
+    int i, d;
+    place(n, values, i, d);
+    const int row = tile * kSumRows + i;
     const bool in = begs[i] >= 0;
     if (row >= a.T || (!in && !a.zero_rest)) continue;
-    f32x4 sum = pipe::zero4();
-    if (in)
-      for (int s = 0; s < a.shares; ++s) sum += *reinterpret_cast<const f32x4*>(sums_row(a, D, s, values, row, kvh) + d);
     *reinterpret_cast<u32x2*>(static_cast<__bf16*>(values ? a.grad_v : a.grad_k) + (long long)row * (values ? a.gvs : a.gks) +
-                              (long long)kvh * D + d) = pipe::cvt4(sum);
+                              (long long)kvh * D + d) = pipe::cvt4(in ? sum[n] : pipe::zero4());
   }
 }
 
@@ -768,18 +791,18 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
 // Shares of the query heads that read one key head: as few as give the CUs
 // kEnough tiles of keys to choose from (the first tiles of a sequence meet many
 // more rows than its last, so few tiles leave most CUs waiting for the longest),
-// at most one head each.  Half as many where tiles are small and their rows split
-// over waves (1 x 1000 x 16/4 x 128 67 us for 74 with a quarter), and no shares
-// where all heads together are a few tiles to a wave (4 x 128 x 12/4 x 64 19.4 us
-// for 20.7).
-constexpr int kEnough = 1024;
+// at most one head each.  (13 documents of up to 1201 rows x 16/4 x 128, forward and
+// gradients: 331 us with two shares, 335 with four; 1 x 1000 x 16/4 x 128, in
+// small tiles, 67 for 74 with 256.)  No shares where all heads together are a few
+// small tiles to a wave: 4 x 128 x 12/4 x 64 19.4 us for 20.7.
+constexpr int kEnough = 600, kEnoughSplit = 512;
 int shares_of(int T, int R, int Hq, int Hkv, int D) {
   const int G = Hq / Hkv;
   const bool split = split_keys(T, R, Hq, D);
   if (split && (long long)G * T <= 512LL * std::max(R, 1)) return 1;
   const long long tiles = split ? ((long long)T + 31) / 32 * Hkv : ((long long)T + 127) / 128 * Hkv;
   for (int s = 1; s < G; ++s)
-    if (G % s == 0 && tiles * s >= (split ? kEnough / 2 : kEnough)) return s;
+    if (G % s == 0 && tiles * s >= (split ? kEnoughSplit : kEnough)) return s;
   return G;
 }
 
