@@ -28,10 +28,10 @@
 // most one whatever the blocks' scales; the denominator sums 2^(s_j - m) in
 // float32.
 //
-// 4 x 65521 tokens x 16/4 x 128 take 48 us, 5.6 TB/s, and 5 us to join; 64
-// requests of up to 4099 tokens 24 us; one of 777 x 12/4 x 64 5.7 us and 5.3 to
-// join, most of it the chain of lengths, table, codes.  Three waves to a SIMD and
-// more shares than the CUs hold at once were slower.
+// 4 x 65521 tokens x 16/4 x 128 take 49 us, 5.4 TB/s, and 5 us to join; 64
+// requests of up to 4099 tokens 25 us, 4.7 TB/s, and 5 to join; one of 777 x 12/4
+// x 64 6.6 us, the chain of lengths, table, codes and four tiles a wave.  More
+// shares than the CUs hold at once, and eight waves to a share, were slower.
 #include <hip/hip_bf16.h>
 
 #include "../../include/gdn.h"
