@@ -110,14 +110,25 @@ __device__ __forceinline__ void take_keys(Rows<D>& x, const __bf16* kt, const __
     for (int b = 0; b < 2 * NH; ++b) x.o[i] = mma(col_frag<D>(vt, vb, 16 * b, i), p[b], x.o[i]);
 }
 
-template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 3) void attn_prompt_kernel(PromptArgs a) {
+// NW / KP waves of a workgroup take 32 rows each; KP = 2: the others the same rows
+// and the second half of each tile's keys, added at the end.  That halves a row's
+// chain of tiles for twice the reads of keys (1 x 5000 x 16/4 x 128 140 us for 174,
+// 2 x 2000 55 for 75, 1 x 8000 319 for 301).
+template <int D, int NW, int KP> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : KP == 1 ? 3 : 2) void attn_prompt_kernel(PromptArgs a) {
   // keys of a staged tile: 64 at D = 64, where 125 registers let four workgroups
   // share a CU (578 us for 1 x 16384 x 16/4 x 64; with 32 keys 620); 32 at
   // D = 128, where that takes 158 registers and three workgroups a CU (67.7 us for
   // 13 prompts of up to 1201 rows x 16/4 x 128; with 64 keys and two 70.5)
-  constexpr int kN = D == 64 ? 64 : 32, NH = kN / 32;
-  constexpr int BM = 32 * NW, NT = 64 * NW, KS = D / 16, DT = D / 32;
-  __shared__ alignas(16) __bf16 kt[2][kN * D], vt[2][kN * D];
+  constexpr int kN = D == 64 ? 64 : 32 * KP, NH = kN / 32 / KP;
+  constexpr int RW = NW / KP, BM = 32 * RW, NT = 64 * NW, KS = D / 16, DT = D / 32;
+  __shared__ union alignas(16) {
+    struct {
+      __bf16 k[2][kN * D], v[2][kN * D];
+    } staged;
+    float part[KP == 2 ? RW : 1][32][D + 4];
+  } mem;
+  auto &kt = mem.staged.k, &vt = mem.staged.v;
+  __shared__ float ml[2][BM];
   __shared__ int begs[BM], window[kWindow], ranges[3][NW], bad[2][NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const int tiles = (a.T + BM - 1) / BM;
@@ -128,7 +139,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 3) 
   const int r0 = tile * BM, kvh = hq / (a.Hq / a.Hkv);
 
   // queries: operands for the wave's rows
-  const int w0 = r0 + wave * 32, row = w0 + (lane & 31);
+  const int part = wave / RW, ko = 32 * NH * part, w0 = r0 + (wave - part * RW) * 32, row = w0 + (lane & 31);
   u32x4 q[KS];
   find_rows<BM, NT>(a.cu, a.R, a.T, r0, window, begs, nullptr, [&] {
     const __hip_bfloat16* src =
@@ -219,17 +230,47 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 3) 
   auto edge = [&](int end) {
     for (; kv < end; kv += kN, buf ^= 1) {
       next();
-      if (kv <= w0 + 31 && kv + kN > lowest) take_keys<D, NH, true>(x, kt[buf], vt[buf], kb0, vb0, q, c, from - kv, upto - kv, [] {}, [] {});
+      const int at = kv + ko;
+      if (at <= w0 + 31 && at + 32 * NH > lowest) take_keys<D, NH, true>(x, kt[buf] + ko * D, vt[buf] + ko * D, kb0, vb0, q, c, from - at, upto - at, [] {}, [] {});
     }
   };
   edge(min(highest, last));
   for (; kv + kN - 1 <= w0; kv += kN, buf ^= 1) {
     next();
-    take_keys<D, NH, false>(x, kt[buf], vt[buf], kb0, vb0, q, c, 0, 0, [] {}, [] {});
+    take_keys<D, NH, false>(x, kt[buf] + ko * D, vt[buf] + ko * D, kb0, vb0, q, c, 0, 0, [] {}, [] {});
   }
   edge(last);
 
-  const float z = sum_halves(x.l);
+  float z = sum_halves(x.l);
+  if constexpr (KP == 2) {  // the second half of each tile's keys, handed to the waves of the first
+    const int r = row - r0;
+    __syncthreads();
+    if (part) {
+      if (hl == 0) {
+        ml[0][r] = x.m;
+        ml[1][r] = z;
+      }
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<f32x4*>(&mem.part[r / 32][r % 32][32 * i + 8 * e + 4 * hl]) =
+              f32x4{x.o[i][4 * e], x.o[i][4 * e + 1], x.o[i][4 * e + 2], x.o[i][4 * e + 3]};
+    }
+    __syncthreads();
+    if (part) return;
+    const float m = fmaxf(x.m, ml[0][r]), f = __builtin_amdgcn_exp2f(x.m - m), g = __builtin_amdgcn_exp2f(ml[0][r] - m);
+    x.m = m;
+    z = z * f + ml[1][r] * g;
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f32x4 y = *reinterpret_cast<const f32x4*>(&mem.part[r / 32][r % 32][32 * i + 8 * e + 4 * hl]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x.o[i][4 * e + j] = x.o[i][4 * e + j] * f + y[j] * g;
+      }
+  }
   const bool rest = beg < 0 && row < a.T && a.zero_rest;
   if (beg < 0 && !rest) return;
   const float inv = rest ? 0.f : 1.f / z;
@@ -408,8 +449,14 @@ template <int D> hipError_t launch(const PromptArgs& a) {
       if (grid.x <= 512 && a.T >= 256LL * a.R) return launch_kernel(attn_prompt_split_kernel<D, 8>, grid, dim3(512), st, a);
     return launch_kernel(attn_prompt_split_kernel<D, 4>, grid, dim3(256), st, a);
   }
+  if constexpr (D == 128)
+    if (split_halves(a.T, a.R, a.Hq)) {
+      PromptArgs b = a;
+      b.by_length = false;
+      return launch_kernel(attn_prompt_kernel<D, NW, 2>, dim3((unsigned)((a.T + 63) / 64 * a.Hq)), dim3(64 * NW), st, b);
+    }
   const unsigned tiles = (unsigned)((a.T + 32 * NW - 1) / (32 * NW));
-  return launch_kernel(attn_prompt_kernel<D, NW>, dim3(tiles * a.Hq), dim3(64 * NW), st, a);
+  return launch_kernel(attn_prompt_kernel<D, NW, 1>, dim3(tiles * a.Hq), dim3(64 * NW), st, a);
 }
 
 }  // namespace

@@ -87,6 +87,12 @@ inline bool split_keys(int T, int R, int Hq, int D) {
   const long long L = T / (R > 0 ? R : 1);
   return (long long)T * Hq * (600 + L) < (D == 64 ? 82000 : 62000) * L;
 }
+// The same for tiles of 64 rows with their keys in two halves, D = 128: between
+// the two (at D = 64 it gains nothing but for single sequences of about 8000).
+inline bool split_halves(int T, int R, int Hq) {
+  const long long L = T / (R > 0 ? R : 1);
+  return (long long)T * Hq * (600 + L) < 108000 * L;
+}
 hipError_t launch_attn_prompt(const PromptArgs& a);
 
 struct PromptBwdArgs {

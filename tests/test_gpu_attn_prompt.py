@@ -98,6 +98,39 @@ def test_thousands_of_sequences():
     check_forward(torch, *make(torch, np.random.default_rng(2), int(lens.sum()), 1, 1, 64), offsets(lens))
 
 
+@pytest.mark.parametrize("lens", [[300, 300, 300, 300], [1, 511, 64, 65, 0, 600], [1200], [1000, 31, 33, 100]])
+def test_tiles_with_keys_in_halves(lens):
+    """Work and chains of tiles in between: the form that halves the keys; rows outside, and values there that are not finite."""
+    torch = torch_dev()
+    heads = {4: 24, 6: 17, 1: 40}[len(lens)]
+    cu = offsets(lens, 7)
+    T = int(cu[-1]) + 9
+    mean = T // len(lens)
+    assert 62000 * mean <= T * heads * (600 + mean) < 108000 * mean
+    q, k, v = make(torch, np.random.default_rng(len(lens)), T, heads, 1, 128)
+    note(f"halves {lens}")
+    out, lse = check_forward(torch, q, k, v, cu)
+    v[:7], v[-9:], k[:7], k[-9:] = float("inf"), float("nan"), float("nan"), float("nan")
+    again, lse2 = check_forward(torch, q, k, v, cu)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    row = int(cu[0] + cu[1]) // 2  # a row of the first sequence: those before it and those of the others do not see it
+    v[row, 0, 3] = float("-inf")
+    bad = check_nothing_else(torch, q, k, v, cu, out)
+    assert torch.equal(bad[row:int(cu[1]), :, 3], torch.full_like(bad[row:int(cu[1]), :, 3], float("-inf")))
+
+
+def check_nothing_else(torch, q, k, v, cu, good):
+    """The forward's output, which is the given one but for column 3 of the first sequence."""
+    import linear_attention_sequence_gated_amd as gdn
+    out = torch.full_like(good, 7.0)
+    lse = torch.full((q.shape[1], q.shape[0]), 7.0, device="cuda")
+    gdn.attn_prompt(q, k, v, cu_of(torch, cu), out=out, lse=lse)
+    a, b = out.clone(), good.clone()
+    a[cu[0]:cu[1], :, 3] = b[cu[0]:cu[1], :, 3] = 0
+    assert torch.equal(a, b)
+    return out
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_rows_outside_and_what_they_hold(D):
     """Rows before the first and behind the last sequence hold NaN and infinities; so may a sequence's own later rows
