@@ -457,7 +457,7 @@ int gdn_attn_prompt(const void *q, const void *k, const void *v, const int *cu_s
  *
  * Each gradient is summed in float32 in a fixed order and rounded once, to
  * bf16; probabilities and score gradients are rounded to bf16 where they enter
- * a product.  Rows in no sequence: as for the forward.  A non-finite value
+ * a product (grad_q: score gradients in two parts, to 2^-16).  Rows in no sequence: as for the forward.  A non-finite value
  * of a row gives non-finite gradients where its row's probabilities reach, and
  * none outside its sequence.  Workspace: gdn_attn_prompt_bwd_workspace_bytes,
  * scratch on entry and exit, no clearing needed.

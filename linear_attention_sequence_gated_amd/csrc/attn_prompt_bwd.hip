@@ -15,11 +15,11 @@
 // sums.  (Five products in one launch, dq added up with atomics, would read and
 // exponentiate half as often but make the order of dq's sums one of arrival.)
 //
-// p and ds are rounded to bf16 where they enter a product, 2^-8 of each.  In dq
-// and dk that costs as much again as the rounding of the result: their relative
-// error is 2.4e-3 where float32 operands would leave 1.7e-3.  Two bf16 parts of
-// ds would bring dq to 1.9e-3 for 6 to 9 % of the time of forward and gradients;
-// the sums over thousands of rows that follow in training do not notice.
+// p and ds are rounded to bf16 where they enter a product, 2^-8 of each; for dq, ds
+// is taken in two parts, the rounded and what the rounding left (2^-16 of it):
+// with one, dq's relative error is 2.5e-3, half as much again as that of rounding
+// the result (1.7e-3), with two 1.9e-3, for a fourth product in place of three (4
+// to 8 % of the time of forward and gradients).  dk has 2.4e-3 and dv 2.3e-3 with one.
 //
 // Bound by the matrix and the vector unit together, as the forward: 8 x 2048 x
 // 12 x 64 takes 106 us for dq and 151 for dk and dv, 2 x 4096 x 16/4 x 128
@@ -121,17 +121,17 @@ __device__ __forceinline__ float delta_of(const PromptBwdArgs& a, int row, int h
 
 // 32 keys, rows n0 .. of the staged K and V, for a wave's 32 rows, of which the
 // lane's sees keys from .. upto (less 4 hl) if MASKED; values_done() is called
-// when V has been read.
-template <int D, bool MASKED, class F>
+// when V has been read.  GLDS: do comes from LDS, gt, not from g.
+template <int D, bool MASKED, bool GLDS, class F>
 __device__ __forceinline__ void dq_tile(f32x16 (&dq)[D / 32], float& rest, const __bf16* K, const __bf16* V, int rb, int cb,
-                                        int n0, const u32x4 (&q)[D / 16], const u32x4 (&g)[D / 16], float c, float lse2,
+                                        int n0, const u32x4 (&q)[D / 16], const u32x4 (&g)[D / 16], const __bf16* gt, int gb, float c, float lse2,
                                         float delta, int from, int upto, F values_done) {
   const unsigned seen = bits(from, upto);
   f32x16 s = zero16(), dp = zero16();
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
     s = mma(row_frag<D>(K, rb, n0, ks), q[ks], s);
-    dp = mma(row_frag<D>(V, rb, n0, ks), g[ks], dp);
+    dp = mma(row_frag<D>(V, rb, n0, ks), GLDS ? row_frag<D>(gt, gb, 0, ks) : g[ks], dp);
   }
   values_done();
 #pragma unroll
@@ -142,7 +142,20 @@ __device__ __forceinline__ void dq_tile(f32x16 (&dq)[D / 32], float& rest, const
     rest += s[e];
   }
 #pragma unroll
-  for (int b = 0; b < 2; ++b) add_columns<D>(dq, K, cb, n0 + 16 * b, operand(s, b));
+  for (int b = 0; b < 2; ++b) {
+    const u32x4 hi = operand(s, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[8 * b + 2 * i] -= pipe::lo_f(hi[i]);
+      s[8 * b + 2 * i + 1] -= pipe::hi_f(hi[i]);
+    }
+    const u32x4 lo = operand(s, b);
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t) {
+      const u32x4 k = col_frag<D>(K, cb, n0 + 16 * b, t);
+      dq[t] = mma(k, lo, mma(k, hi, dq[t]));
+    }
+  }
 }
 
 template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(PromptBwdArgs a) {
@@ -229,7 +242,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
     const int rb = fresh(rb0), cb = fresh(cb0);
 #pragma unroll 1
     for (int n = 0; n < 2; ++n)
-      dq_tile<D, MASKED>(dq, rest, K, V, rb, cb, 32 * n, q, g, c, lse2, delta, from - kv - 32 * n, upto - kv - 32 * n, [] {});
+      dq_tile<D, MASKED, false>(dq, rest, K, V, rb, cb, 32 * n, q, g, nullptr, 0, c, lse2, delta, from - kv - 32 * n, upto - kv - 32 * n, [] {});
   };
   stage(0, first);
   auto next = [&] {
@@ -282,6 +295,8 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_s
     __bf16 staged[NW][2][32 * D];
     float part[NW][32][LD];
   } mem;
+  constexpr bool GLDS = D == 128;  // do, the same rows for all waves, from LDS: there are no registers for it
+  __shared__ alignas(16) __bf16 gt[GLDS ? 32 * D : 8];
   __shared__ float rests[NW][32];
   __shared__ int begs[32], window[kWindow], dirty[2][NW];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
@@ -310,6 +325,12 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_s
   }
   const float delta = delta_of<D>(a, at, hq, g, hl), lse2 = a.lse[(size_t)hq * a.T + at] * kLog2e;
 
+  if constexpr (GLDS) {
+    Stage<D, 32, NW> sg;
+    sg.init(a.gos, wave);
+    sg.load(gt, rows_rsrc(static_cast<const __bf16*>(a.grad_out) + (long long)hq * D, a.gos, r0, min(32, a.T - r0), D), wave);
+    staged_barrier();
+  }
   f32x16 dq[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) dq[i] = zero16();
@@ -343,9 +364,9 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_s
         dirty_lo = min(dirty_lo, kv);
         dirty_hi = kv + 32;
       }
-      dq_tile<D, true>(dq, rest, kt, vt, rb, cb, 0, q, g, c, lse2, delta, from - kv, upto - kv, values_done);
+      dq_tile<D, true, GLDS>(dq, rest, kt, vt, rb, cb, 0, q, g, gt, rb, c, lse2, delta, from - kv, upto - kv, values_done);
     } else {
-      dq_tile<D, false>(dq, rest, kt, vt, rb, cb, 0, q, g, c, lse2, delta, 0, 0, values_done);
+      dq_tile<D, false, GLDS>(dq, rest, kt, vt, rb, cb, 0, q, g, gt, rb, c, lse2, delta, 0, 0, values_done);
     }
     if (to < last) {
       wait_read();

@@ -2,7 +2,8 @@
 
 Tolerances, element by element, with u = 2^-8 (half a bf16 step).  dv: every weight p is rounded to bf16 once and the
 sum once, u (sum p |do| + |dv|).  delta is summed from the rounded output, so it errs by u sum |do o|; ds = p (dp -
-delta) is rounded once, u |ds| + p u sum |do o|, and reaches dq and dk through |k| and |q|; these are rounded once.
+delta) errs by p u sum |do o| and, rounded once where it enters dk, by u |ds| more; for dq it enters in two parts, 2^-16 |ds|,
+which float32's share covers.  It reaches dq and dk through |k| and |q|; these are rounded once.
 float32 exponents and sums add 2^-12 of the same sums with |dp| + |delta| in place of |dp - delta| (scores here are below
 2^6, so exponents err by less than 2^-17; sums of 700 terms by less than 2^-14).
 """
@@ -29,9 +30,9 @@ def bounds(q, k, v, do, cu, scale, grads):
             p /= p.sum(1, keepdims=True)
             o, dp = p @ v[a:b, h // G], do[a:b, h] @ v[a:b, h // G].T
             delta, off = (do[a:b, h] * o).sum(1, keepdims=True), np.abs(do[a:b, h] * o).sum(1, keepdims=True)
-            e = abs(scale) * p * (U * np.abs(dp - delta) + U * off + F * (np.abs(dp) + np.abs(delta)))
+            e = abs(scale) * p * (U * off + F * (np.abs(dp) + np.abs(delta)))
             tq[a:b, h] += e @ np.abs(k[a:b, h // G])
-            tk[a:b, h // G] += e.T @ np.abs(q[a:b, h])
+            tk[a:b, h // G] += (e + abs(scale) * p * U * np.abs(dp - delta)).T @ np.abs(q[a:b, h])
             tv[a:b, h // G] += (U + F) * p.T @ np.abs(do[a:b, h])
     return tq, tk, tv
 
