@@ -22,8 +22,8 @@
 // to 8 % of the time of forward and gradients).  dk has 2.4e-3 and dv 2.3e-3 with one.
 //
 // Bound by the matrix and the vector unit together, as the forward: 8 x 2048 x
-// 12 x 64 takes 106 us for dq and 151 for dk and dv, 2 x 4096 x 16/4 x 128
-// with the forward 670 us, 930 TFLOP/s.
+// 12 x 64 takes 125 us for dq and 151 for dk and dv, 2 x 4096 x 16/4 x 128
+// with the forward 735 us, 650 TFLOP/s.
 #include <algorithm>
 
 #include "../../include/gdn.h"
@@ -288,7 +288,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
 // Few rows, as in the forward: a workgroup takes 32 rows and its waves every
 // NW-th tile of 32 keys, each staging its own; their sums are added at the end.
 // With the same for dk and dv: forward and gradients of 1 x 1000 x 12/4 x 64 41 us
-// for 76, 1 x 2500 x 16/4 x 128 211 for 297.
+// for 76, 1 x 2500 x 16/4 x 128 217 for 297.
 template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_split_kernel(PromptBwdArgs a) {
   constexpr int NT = 64 * NW, KS = D / 16, LD = D + 4;
   __shared__ union alignas(16) {
