@@ -79,7 +79,8 @@ def block_tables(seq_lens, new_lens, block_table, free_blocks, block_tokens: int
     taken from the front of free_blocks.  All int32.  tokens: the length of the slot map, at least the sum of new_lens
     (what is over is filled with -1).
 
-    Returns (slot_map [tokens], cu_seqlens [R + 1], lens_after [R], used [2]: free blocks taken, requests refused).
+    Returns (slot_map [tokens], cu_seqlens [R + 1], lens_after [R], used [2]: free blocks taken, requests refused), parts of
+    one allocation.
     """
     dev = _device(seq_lens, "block_tables")
     r, width = block_table.shape
@@ -89,7 +90,10 @@ def block_tables(seq_lens, new_lens, block_table, free_blocks, block_tokens: int
     _dense(free_blocks, "free_blocks", (free_blocks.numel(),), _I32, dev)
     if tokens < 0:
         raise ValueError("block_tables: tokens is negative")
-    slot_map, cu, after, used = (seq_lens.new_empty(n) for n in (tokens, r + 1, r, 2))
+    # one allocation, its parts 16 bytes aligned (four take 1.5 us more)
+    a, b = -(r + 1) % 4, -r % 4
+    used, _, cu, _, after, _, slot_map = seq_lens.new_empty(4 + r + 1 + a + r + b + tokens).split_with_sizes(
+        (2, 2, r + 1, a, r, b, tokens))
     _call(dev, raw.load().gdn_block_tables, seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
           free_blocks.data_ptr(), slot_map.data_ptr(), cu.data_ptr(), after.data_ptr(), used.data_ptr(), r, width,
           free_blocks.numel(), block_tokens, num_blocks, tokens)
