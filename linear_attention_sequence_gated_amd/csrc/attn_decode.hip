@@ -636,16 +636,19 @@ DecodeSizes sizes(int R, int Hq, int Hkv, int D, int bt, int width, int num_bloc
   z.W = units < most ? (int)units : most;
   // one workgroup to a (request, key head), and no join, if none can be long; the
   // more of them there are, the longer they may be before the longest is what the
-  // call takes.  Both ways, us: 1 x 777 x 12/4 x 64 6.6 for 9.4, 64 ragged of up
-  // to 1500 x 16/4 x 128 14.9 for 20.2, 300 of up to 120 9.8 for 20.4, of up to
-  // 2000 60.6 for 78.4, of up to 8000 229 for 243; 16 of 2000 16.4 for 13.8, 64 of
-  // 4099 31.1 for 29.6.
+  // call takes.  Both ways, us on the GPU: 1 x 777 x 12/4 x 64 6.6 for 9.4, 64
+  // ragged of up to 1500 x 16/4 x 128 14.9 for 20.2, 300 of up to 120 9.8 for 20.4,
+  // of up to 2000 60.6 for 78.4, of up to 8000 229 for 243; 16 of 2000 16.4 for
+  // 13.8.  With cold caches, calls: 64 of up to 4099 34.4 for 36.4, 64 of 4000 x
+  // 16/4 x 64 30 for 38, but 64 of up to 4099 x 12/4 x 64 25.8 for 24.4 and 128 of
+  // up to 4099 x 16/4 x 128, more than run at once, 66.5 for 63.3.
   const long long groups = (long long)R * Hkv * z.NG, cap = ((long long)width * bt + kUnit - 1) / kUnit;
-  z.whole = cap <= (groups < 256 ? 8 : groups < 1024 ? 24 : 64);
+  const long long at_once = D == 64 ? 512 : 256;  // of eight waves
+  z.whole = cap <= (groups < 256 ? 8 : groups <= at_once ? 40 : groups < 1024 ? 24 : 64);
   // eight waves to each where that leaves none waiting for a CU, and for the long
   // ones: 64 ragged of up to 777 x 16/4 x 128 9.4 for 10.5 with four, 300 of up to
   // 777 36 for 26
-  if (z.whole) z.whole = cap > 4 && (groups <= (D == 64 ? 512 : 256) || cap > 16) ? 8 : 4;
+  if (z.whole) z.whole = cap > 4 && (groups <= at_once || cap > 16) ? 8 : 4;
   return z;
 }
 
