@@ -29,9 +29,10 @@
 // float32.
 //
 // 4 x 65521 tokens x 16/4 x 128 take 49 us, 5.4 TB/s, and 5 us to join; 64
-// requests of up to 4099 tokens 25 us, 4.7 TB/s, and 5 to join; one of 777 x 12/4
-// x 64 6.6 us, the chain of lengths, table, codes and four tiles a wave.  More
-// shares than the CUs hold at once, and eight waves to a share, were slower.
+// requests of up to 4099 tokens 29 us, 4.0 TB/s, the longest's tiles on one CU; one
+// of 777 x 12/4 x 64 6.6 us, the chain of lengths, table, codes and four tiles a
+// wave.  More shares than the CUs hold at once, and eight waves to a share, were
+// slower.
 #include <hip/hip_bf16.h>
 
 #include "../../include/gdn.h"
@@ -147,17 +148,25 @@ template <int D> struct Tile {
   int n[2];  // tokens of the half that count
 };
 
+// The blocks that a wave's tile lies in (any where it has no tokens).
+struct Blocks {
+  int id[2];
+};
+__device__ __forceinline__ Blocks blocks_of(int tok, int n, const int* row, int bt) {
+  const int sh = __builtin_ctz(bt);
+  return {{tok < n ? row[tok >> sh] : 0, tok + 16 < n ? row[(tok + 16) >> sh] : 0}};
+}
+
 template <int D>
-__device__ __forceinline__ void load_tile(Tile<D>& t, int tok, int n, const int* row, int h, const DecodeArgs& a,
+__device__ __forceinline__ void load_tile(Tile<D>& t, const Blocks& b, int tok, int n, int h, const DecodeArgs& a,
                                           const DecodeSizes& z) {
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  const int sh = __builtin_ctz(z.bt);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int p = tok + 16 * j;
     int left = n - p;
     left = left < 0 ? 0 : (left > 16 ? 16 : left);
-    int id = left ? row[p >> sh] : 0;
+    int id = b.id[j];
     if (id < 0 || id >= z.num_blocks) left = 0;
     if (!left) id = 0;
     const size_t tile = (size_t)id * z.Hkv + h;
@@ -338,6 +347,9 @@ template <int D, int FMT, int NW, bool WHOLE> __global__ __launch_bounds__(64 * 
     return p;
   };
   Tile<D> t0, t1;
+  // of the tile after next: the table is read a tile before the codes that it leads
+  // to (64 x 4000 x 16/4 x 64 27.4 us for 30; a third tile on its way costs 3 %)
+  Blocks ahead;
   u32x4 qw[D / 32];
   // its queries and first tile, on their way while the part before it is joined
   auto begin = [&](const Part& p) {
@@ -346,7 +358,11 @@ template <int D, int FMT, int NW, bool WHOLE> __global__ __launch_bounds__(64 * 
 #pragma unroll
     for (int ks = 0; ks < D / 32; ++ks) qw[ks] = *reinterpret_cast<const u32x4*>(src + (D / 4) * g + 8 * ks);
     const int tok = p.ua * kUnit + wave * kTile, end = min(p.n, p.ub * kUnit);
-    if (tok < end) load_tile<D>(t0, tok, end, a.block_table + (size_t)p.r * z.width, p.h, a, z);
+    if (tok < end) {
+      const int* row = a.block_table + (size_t)p.r * z.width;
+      load_tile<D>(t0, blocks_of(tok, end, row, z.bt), tok, end, p.h, a, z);
+      ahead = blocks_of(tok + kStep, end, row, z.bt);
+    }
   };
 
   bool first = true;
@@ -389,11 +405,13 @@ template <int D, int FMT, int NW, bool WHOLE> __global__ __launch_bounds__(64 * 
     int tok = ua * kUnit + wave * kTile;
     if (tok < end) {
       for (;;) {
-        if (tok + kStep < end) load_tile<D>(t1, tok + kStep, end, row, h, a, z);
+        if (tok + kStep < end) load_tile<D>(t1, ahead, tok + kStep, end, h, a, z);
+        ahead = blocks_of(tok + 2 * kStep, end, row, z.bt);
         take_tile<D, FMT>(s, t0, q, qfac);
         tok += kStep;
         if (tok >= end) break;
-        if (tok + kStep < end) load_tile<D>(t0, tok + kStep, end, row, h, a, z);
+        if (tok + kStep < end) load_tile<D>(t0, ahead, tok + kStep, end, h, a, z);
+        ahead = blocks_of(tok + 2 * kStep, end, row, z.bt);
         take_tile<D, FMT>(s, t1, q, qfac);
         tok += kStep;
         if (tok >= end) break;
