@@ -374,7 +374,7 @@ enum { GDN_CACHE_I8 = 0,   /* signed integers in [-127, 127]                  */
  * blocks (the needs of every request before it count, refused or not, unless
  * their own lengths are at fault).  A refused request keeps its table row and
  * its length; a negative new length counts as no tokens.  A block outside
- * [0, num_blocks) gets slot -1.  R below 2^20.  One launch.
+ * [0, num_blocks) gets slot -1.  R below 2^20, T below 2^31 - 2^12.  One launch.
  */
 int gdn_block_tables(const int *seq_lens, const int *new_lens, int *block_table, const int *free_blocks,
                      int *slot_map, int *cu_seqlens, int *lens_after, int *used, int R, int width, int n_free,

@@ -27,6 +27,9 @@ bool block_ok(int bt) { return bt == 16 || bt == 32 || bt == 64 || bt == 128; }
 bool stride_ok(long long s, long long row) { return s >= row && s % 8 == 0 && s < (1LL << 40); }
 
 constexpr int kMaxRequests = 1 << 20;
+// Slots and tokens are counted in 32 bits by loops that step up to 2048 past the
+// last one; their numbers stay below this.
+constexpr long long kMostTokens = (1LL << 31) - 4096;
 
 // Sizes of a cache and of the heads that read it.
 int cache_shape(int Hkv, int D, int bt, int num_blocks) {
@@ -71,6 +74,7 @@ int gdn_block_tables(const int* seq_lens, const int* new_lens, int* block_table,
   if (R < 0 || width < 0 || n_free < 0 || num_blocks < 0 || T < 0 || block_tokens <= 0) return GDN_ERR_SHAPE;
   if (R >= kMaxRequests || (long long)num_blocks * block_tokens >= (1LL << 31) || (long long)width * block_tokens >= (1LL << 31))
     return GDN_ERR_SHAPE;
+  if (T >= kMostTokens) return GDN_ERR_SHAPE;
   if (!block_ok(block_tokens)) return GDN_ERR_UNSUPPORTED;
   if (!cu_seqlens || !used || (T && !slot_map) || (n_free && !free_blocks)) return GDN_ERR_NULL;
   if (R && (!seq_lens || !new_lens || !lens_after || (width && !block_table))) return GDN_ERR_NULL;

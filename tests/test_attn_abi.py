@@ -30,6 +30,12 @@ def test_tables_argument_errors(kw, status):
     assert tables(**kw) == status
 
 
+def test_tables_largest_slot_map():
+    """Slots are counted in 32 bits, some way past the last: the longest maps are refused, whatever fits below them."""
+    assert tables(T=2 ** 31 - 1) == raw.GDN_ERR_SHAPE and tables(T=2 ** 31 - 4096) == raw.GDN_ERR_SHAPE
+    assert tables(T=2 ** 31 - 4097, slot_map=None) == raw.GDN_ERR_NULL  # past the check of sizes
+
+
 def append(**kw):
     args = dict(k=A, v=A, slot_map=A, k_cache=A, v_cache=A, k_scale=A, v_scale=A, k_stride=256, v_stride=256, T=10,
                 Hkv=4, D=64, block_tokens=16, num_blocks=64, dtype=gdn.GDN_BF16, cache_format=gdn.GDN_CACHE_I8, stream=None)
