@@ -420,8 +420,8 @@ int gdn_cache_append(const void *k, const void *v, const int *slot_map, void *k_
  * Scales are positive normal numbers.  Workspace:
  * gdn_attn_decode_workspace_bytes, which is 0 where the table is narrow;
  * scratch on entry and exit, no clearing needed.  R is below 2^20, R * Hq below
- * 2^23, width * block_tokens below 2^31, and so is R times the table's 128-token
- * units and one.
+ * 2^23, width * block_tokens below 2^31 - 2^12, R times the table's 128-token
+ * units and one below 2^31.
  */
 size_t gdn_attn_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int block_tokens, int width);
 int gdn_attn_decode(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,

@@ -56,7 +56,7 @@ int prompt_shape(int T, int R, int Hq, int Hkv, int D) {
 }
 
 int decode_shape(int R, int Hq, int Hkv, int D, int bt, int width) {
-  if (R < 0 || width < 0 || bt <= 0 || R >= kMaxRequests || (long long)width * bt >= (1LL << 31)) return GDN_ERR_SHAPE;
+  if (R < 0 || width < 0 || bt <= 0 || R >= kMaxRequests || (long long)width * bt >= kMostTokens) return GDN_ERR_SHAPE;
   if (const int s = heads_shape(Hq, Hkv, D)) return s;
   if ((long long)R * Hq >= (1LL << 23)) return GDN_ERR_SHAPE;  // one workgroup of 512 joins one (request, head)
   // the units of 128 tokens over all requests, and one more for each, stay 32-bit numbers

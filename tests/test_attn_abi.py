@@ -101,6 +101,17 @@ def test_decode_workspace():
     assert decode(R=0, q=None, seq_lens=None, out=None) == raw.GDN_OK
 
 
+def test_decode_longest_tables():
+    """A length on the device may be anything and is cut to the table's width; tokens are counted in 32 bits, some way
+    past that, so the widest tables are refused."""
+    for bt in (16, 128):
+        for w in ((2 ** 31 - 1) // bt, (2 ** 31 - 4096) // bt):
+            assert decode(R=1, block_tokens=bt, width=w) == raw.GDN_ERR_SHAPE
+            assert gdn.gdn_attn_decode_workspace_bytes(1, 8, 4, 64, bt, w) == 0
+        w = (2 ** 31 - 4096) // bt - 1
+        assert decode(R=1, block_tokens=bt, width=w, workspace=None) == raw.GDN_ERR_WORKSPACE  # past the check of sizes
+
+
 def prompt(**kw):
     args = dict(q=A, k=A, v=A, cu_seqlens=A, out=A, lse=A, scale=0.125, q_stride=512, k_stride=256, v_stride=256, T=100,
                 R=3, Hq=8, Hkv=4, D=64, dtype=gdn.GDN_BF16, zero_rest=0, stream=None)
