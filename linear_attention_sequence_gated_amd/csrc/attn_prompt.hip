@@ -224,6 +224,10 @@ template <int D, int NW, int KP> __global__ __launch_bounds__(64 * NW, D == 64 ?
     }
     if (kv + kN < last) stage(buf ^ 1, kv + kN);
   };
+  // where the tiles that the wave's rows see whole end (a wave none of whose rows is
+  // in a sequence may lie behind the last tile: it takes no more than the others,
+  // with whom it shares the barriers)
+  const int whole = min(w0 + 1, last);
   // tiles of which some row misses some key, at both ends of the range, and
   // those between, which all rows see whole (loops apart: one loop with both
   // bodies takes more registers than there are)
@@ -235,7 +239,7 @@ template <int D, int NW, int KP> __global__ __launch_bounds__(64 * NW, D == 64 ?
     }
   };
   edge(min(highest, last));
-  for (; kv + kN - 1 <= w0; kv += kN, buf ^= 1) {
+  for (; kv + kN <= whole; kv += kN, buf ^= 1) {
     next();
     take_keys<D, NH, false>(x, kt[buf] + ko * D, vt[buf] + ko * D, kb0, vb0, q, c, 0, 0, [] {}, [] {});
   }

@@ -259,6 +259,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
     }
     if (kv + kN < last) stage(buf ^ 1, kv + kN);
   };
+  const int whole = min(w0 + 1, last);  // waves behind the last tile take no more than the others
   // tiles of which some row misses some key, at both ends, and those between
   auto edge = [&](int end) {
     for (; kv < end; kv += kN, buf ^= 1) {
@@ -267,7 +268,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
     }
   };
   edge(min(highest, last));
-  for (; kv + kN - 1 <= w0; kv += kN, buf ^= 1) {
+  for (; kv + kN <= whole; kv += kN, buf ^= 1) {
     next();
     step(std::false_type{}, kt[buf], vt[buf]);
   }

@@ -164,6 +164,29 @@ def test_rows_outside_and_what_they_hold(D):
     assert out3[cu[0] + 62:cu[0] + 65, :, 3].isnan().all() and torch.equal(out3[cu[0]:cu[0] + 62], out2[cu[0]:cu[0] + 62])
 
 
+BEHIND = [(0, 129), (5, 133), (5, 135), (0, 140), (1, 161), (100, 290), (0, 1), (3, 5)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("first,end", BEHIND)
+def test_waves_behind_the_last_key(first, end, D):
+    """Waves of a tile that no sequence reaches any more: their rows are zeros, whatever rows outside hold."""
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    T = -(-end // 128) * 128 + 70
+    q, k, v = make(torch, np.random.default_rng(end), T, 4, 2, D, fused=False)
+    cu = np.array([first, end])
+    note(f"behind {first} {end} D{D}")
+    good, glse = check_forward(torch, q, k, v, cu)
+    outside = np.r_[0:first, end:T]
+    for bad in ("nan", "inf"):
+        for x in (q, k, v):
+            x[outside] = float(bad)
+        out, lse = gdn.attn_prompt(q, k, v, cu_of(torch, cu))
+        assert (out[outside] == 0).all() and (lse[:, outside] == 0).all()
+        assert torch.equal(out[first:end], good[first:end]) and torch.equal(lse[:, first:end], glse[:, first:end])
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("scale,size", [(0.0, 1.0), (-0.2, 1.0), (1.0, 3.0), (1e-3, 30.0), (30.0, 0.2)])
 def test_scales(D, scale, size):

@@ -12,7 +12,7 @@ import pytest
 
 from gpu_util import note, torch_dev
 from oracle import attention as ref
-from test_gpu_attn_prompt import RAGGED, cu_of, host, make, offsets, padded  # noqa: F401
+from test_gpu_attn_prompt import BEHIND, RAGGED, cu_of, host, make, offsets, padded  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 U, F = 2.0 ** -8, 2.0 ** -12
@@ -117,6 +117,27 @@ def test_rows_outside_may_hold_anything(D):
             assert torch.equal(a[keep], b[keep])
         # dv = sum p do does not contain v
         assert all(g[cu[1]:cu[2]].isnan().any() for g in (got[:2] if bad == 2 else got))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("first,end", BEHIND)
+def test_waves_behind_the_last_key(first, end, D):
+    """Waves of a tile that no sequence reaches any more: their rows' gradients are zeros, whatever rows outside hold."""
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    T = -(-end // 128) * 128 + 70
+    q, k, v = make(torch, np.random.default_rng(end), T, 4, 2, D, fused=False)
+    do = torch.from_numpy(np.random.default_rng(end + 1).standard_normal((T, 4, D)).astype(np.float32)).to(torch.bfloat16).cuda()
+    cu = np.array([first, end])
+    note(f"bwd behind {first} {end} D{D}")
+    good = check(torch, q, k, v, cu, do=do)
+    outside, c = np.r_[0:first, end:T], cu_of(torch, cu)
+    for bad in ("nan", "inf"):
+        for x in (q, k, v, do):
+            x[outside] = float(bad)
+        out, lse = gdn.attn_prompt(q, k, v, c)
+        for a, b in zip(gdn.attn_prompt_bwd(q, k, v, out, lse, do, c), good):
+            assert (a[outside] == 0).all() and torch.equal(a[first:end], b[first:end])
 
 
 @pytest.mark.parametrize("D", [64, 128])
