@@ -398,8 +398,10 @@ int gdn_block_tables(const int *seq_lens, const int *new_lens, int *block_table,
  * zero, infinities as the largest code of the largest bf16 value's scale.
  *
  * No two tokens may have the same slot, and the tokens of one block must
- * follow one another in the call with ascending slots, as gdn_block_tables
- * gives them; otherwise the block's contents are undefined.
+ * follow one another in the call with consecutive slots (each one more than the
+ * one before it, none left out between), as gdn_block_tables gives them;
+ * otherwise that block's contents and scale are undefined: rows behind a gap are
+ * taken for a write of their own, at the same time as those before it.
  * T * Hkv below 2^28.
  */
 int gdn_cache_append(const void *k, const void *v, const int *slot_map, void *k_cache, void *v_cache,

@@ -117,7 +117,8 @@ def cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale):
     """Writes the rows k, v [T, Hkv, D] bf16 into the cache at slot_map [T] int32 (see block_tables), in place.
 
     k_cache, v_cache [num_blocks, Hkv, block_tokens, D] int8 or float8_e4m3fn; k_scale, v_scale [num_blocks, Hkv]
-    float32: a value is its code times the scale of its block and head.
+    float32: a value is its code times the scale of its block and head.  The tokens of one block follow one another in
+    the call with consecutive slots; a token whose slot lies outside the cache is skipped.
     """
     dev = _device(k, "cache_append")
     nb, hkv, bt, d, fmt = _cache(k_cache, v_cache, k_scale, v_scale, dev)

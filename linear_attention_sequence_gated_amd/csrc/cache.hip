@@ -238,8 +238,10 @@ __global__ __launch_bounds__(kThreads) void block_tables_kernel(TablesArgs a) {
 // the new scale, code = rne(code s_old / s).  The codes are the rounding of
 // 32-bit products (by the reciprocal and by the ratio).
 //
-// One workgroup per run (the tokens of one call that fall into one block), head
-// and tensor: a run's rows fit the registers of its four waves (NL 16-byte
+// One workgroup per run (the tokens of one call that fall into one block: as they
+// follow one another with consecutive slots, a run ends where a slot is not one more
+// than that before it, and no other run of the call has the same scale), head and
+// tensor: a run's rows fit the registers of its four waves (NL 16-byte
 // pieces per lane), so that they are read once and the largest magnitude takes
 // one exchange through LDS.  Bound by HBM, 2 bytes read and 1 written per value:
 // 9869 tokens x 16 heads of 128, 121 MB, take 22.5 us, 5.4 TB/s; 256 single tokens
