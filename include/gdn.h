@@ -419,7 +419,10 @@ int gdn_cache_append(const void *k, const void *v, const int *slot_map, void *k_
  *
  * A request without tokens gets zeros and an lse of -infinity.  What the cache
  * holds behind a request's last token is never used, whatever its bits.
- * Scales are positive normal numbers.  Workspace:
+ * A token's probability times its v scale is rounded to fp16: to 2^-11 of itself,
+ * or 2^-40 of the request's largest where that is more (below e^-20 of it).
+ * Scales are positive normal numbers; where scores pass 2^23, those of v lie
+ * between 2^-16 and 2^16.  Workspace:
  * gdn_attn_decode_workspace_bytes, which is 0 where the table is narrow;
  * scratch on entry and exit, no clearing needed.  R is below 2^20, R * Hq below
  * 2^23, width * block_tokens below 2^31 - 2^12, R times the table's 128-token

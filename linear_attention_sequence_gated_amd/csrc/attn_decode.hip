@@ -23,9 +23,11 @@
 // never leave their lane.  Codes are exact in fp16 (int8 through u 2^-10 -
 // 128 2^-10, one packed multiply-add for two); q is moved into fp16's range by
 // a power of two per head, which is exact down to 2^-28 of its largest entry.
-// The running maximum m is that of s_j + log2 vs_j, so that the weights
-// p_j = 2^(s_j - m) vs_j that are rounded to fp16 (half an ulp: 2^-12) are at
-// most one whatever the blocks' scales; the denominator sums 2^(s_j - m) in
+// The running maximum m is that of s_j + log2 vs_j less 15, so that the weights
+// p_j = 2^(s_j - m) vs_j that are rounded to fp16 are at most 2^15 whatever the
+// blocks' scales: half an ulp, 2^-11 of each that is at least e^-20 of the largest,
+// 2^-40 of the largest of those below.  (At most one, they lost a flat tail 17 below
+// one high score, whose value may be zero.)  The denominator sums 2^(s_j - m) in
 // float32.
 //
 // 4 x 65521 tokens x 16/4 x 128 take 49 us, 5.4 TB/s, and 5 us to join; 64
@@ -57,6 +59,17 @@ constexpr int kAhead = 1;
 constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
 constexpr float kLowest = -3e38f;  // running maximum before the first token
 constexpr float kCodeUp = 1024.f;  // int8 codes enter the products times 2^-10
+// The maximum in use lies kUp below the true one, so that the largest weights are
+// 2^15 and those down to 2^-29 of it (e^-20) normal numbers of fp16, which ends at
+// 65504.  Not where scores pass 2^24: their sums with log2 vs_j are off by more
+// than a power of two, and the room is needed for that.
+constexpr float kUp = 15.f, kUpBelow = 16777216.f;
+// What the denominator sums is 2^(s_j - m), 2^kUp / vs_j where vs_j's token has the
+// maximum: for the scales' whole range (2^-126 to 2^121) to fit float32 with 2^31
+// tokens, log2 vs_j counts as kLeastLog at least in m (the largest weights of
+// smaller scales are below 2^15, still normal), and the sums are taken times 2^-kDown.
+constexpr float kLeastLog = -97.f, kDown = 16.f;
+constexpr float kDownBy = 1.f / 65536;  // 2^-kDown
 
 // Shares of the work: what the CUs hold at once (three workgroups of the at most
 // 168 registers that d = 64 takes, two at d = 128).
@@ -216,7 +229,7 @@ __device__ __forceinline__ void take_tile(Sums<D>& s, const Tile<D>& t, const f1
     for (int ks = 0; ks < D / 32; ++ks)
       y = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes8<FMT>(t.k[j][2 * ks], t.k[j][2 * ks + 1]), q[ks], y, 0, 0, 0);
     const float f = qfac * t.ks[j];
-    const float lv = __builtin_amdgcn_logf(t.vs[j]);
+    const float lv = fmaxf(__builtin_amdgcn_logf(t.vs[j]), kLeastLog);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[j][i] = 4 * g + i < t.n[j] ? y[i] * f : -INFINITY;
@@ -225,7 +238,7 @@ __device__ __forceinline__ void take_tile(Sums<D>& s, const Tile<D>& t, const f1
   }
   top = fmaxf(top, __shfl_xor(top, 16));
   top = fmaxf(top, __shfl_xor(top, 32));
-  const float m = fmaxf(s.m, top);
+  const float m = fmaxf(s.m, fabsf(top) < kUpBelow ? top - kUp : top);
   if (__any(m != s.m)) {
     const float c = __builtin_amdgcn_exp2f(s.m - m);
     s.l *= c;
@@ -239,7 +252,7 @@ __device__ __forceinline__ void take_tile(Sums<D>& s, const Tile<D>& t, const f1
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float e = __builtin_amdgcn_exp2f(x[j][i] - m);
-      s.l += e;
+      s.l = __builtin_fmaf(e, kDownBy, s.l);
       p[4 * j + i] = (_Float16)(e * t.vs[j]);
     }
   }
@@ -451,7 +464,7 @@ template <int D, int FMT, int NW, bool WHOLE> __global__ __launch_bounds__(64 * 
     float L = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) L += ml[w][1][c] * __builtin_amdgcn_exp2f(ml[w][0][c] - M);
-    const float mine_w = __builtin_amdgcn_exp2f(s.m - M) * (FMT == GDN_CACHE_I8 ? kCodeUp : 1.f);
+    const float mine_w = __builtin_amdgcn_exp2f(s.m - M) * (FMT == GDN_CACHE_I8 ? kCodeUp * kDownBy : kDownBy);
     if (c < cols) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -466,7 +479,7 @@ template <int D, int FMT, int NW, bool WHOLE> __global__ __launch_bounds__(64 * 
     float* o_ws = a.ws + slot * z.Gc * (D + 2);
     if (wave == 0 && lane < cols) {
       if (whole) {
-        if (a.lse) a.lse[(size_t)rr * z.Hq + q0 + lane] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
+        if (a.lse) a.lse[(size_t)rr * z.Hq + q0 + lane] = L == 0.f ? -INFINITY : (M + (kDown + __builtin_amdgcn_logf(L))) * kLn2;
       } else {
         o_ws[z.Gc * D + 2 * lane] = M;
         o_ws[z.Gc * D + 2 * lane + 1] = L;
@@ -633,7 +646,7 @@ template <int D, int DS, bool CUTS> __global__ __launch_bounds__(128 * (DS == 1 
     }
     o *= L == 0.f ? 0.f : 1.f / L;
     *reinterpret_cast<u32x2*>(out + 4 * tid) = pipe::cvt4(o);
-    if (writes_lse) a.lse[(size_t)r * z.Hq + hq] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
+    if (writes_lse) a.lse[(size_t)r * z.Hq + hq] = L == 0.f ? -INFINITY : (M + (kDown + __builtin_amdgcn_logf(L))) * kLn2;
   }
 }
 

@@ -201,6 +201,47 @@ def test_decode_blocks_of_zeros_beside_others():
     check(torch, q, kc, vc, ks, vs, table, lens)
 
 
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("gap", [8.0, 12.0, 16.0, 19.5])
+def test_decode_one_token_far_above_the_others(gap, D, kind):
+    """One token's score lies far above those of the others, which are equal, and its value is zero: the output is that
+    of the others, whose weights are small numbers (down to e^-19.5 of the largest)."""
+    torch = torch_dev()
+    q, kc, vc, ks, vs, table, lens = make(torch, np.random.default_rng(15), [20, 300, 2000, 2000], 4, 2, D, 32, kind)
+    most = 127 if kind == "int8" else 448
+    q[:], ks[:] = 1.0, 1.0
+    kc.view(torch.int8)[:] = 0
+    for r, at in enumerate((0, 299, 1000, 0)):
+        kc[table[r, at // 32], :, at % 32] = torch.full((D,), float(most)).to(kc.dtype)
+        vc.view(torch.int8)[table[r, at // 32], :, at % 32] = 0
+    note(f"decode far above {gap} D{D} {kind}")
+    check(torch, q, kc, vc, ks, vs, table, lens, scale=gap / (most * D))
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("power", [-126, -118, -100, -60, 60, 100, 120])
+def test_decode_scales_at_the_ends_of_their_range(power, kind):
+    """All values' scales next to the smallest or largest that there are: the denominator's sums stay numbers.
+
+    lse is that of any other scales; it is put together from numbers as large as log2 of the scale (below 2^7) plus
+    scores and lengths (2^6), which err by half an ulp, 2^-18, where they are added: 2^-15 covers eight such.  Where
+    neither they nor their products leave the range of normal bf16 numbers, outputs are those of scales of one, moved."""
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    q, kc, vc, ks, vs, table, lens = make(torch, np.random.default_rng(14), [1, 30, 700, 9000], 4, 2, 64, 64, kind)
+    vs[:] = 1.0
+    rest = ints(torch, table), ints(torch, lens)
+    x = (q.float().numpy().astype(np.float64), values(kc), values(vc), ks.numpy(), vs.numpy(), table, lens, 64 ** -0.5)
+    want, wlse = ref.decode(*x)
+    to, tl = bounds(*x, want, wlse)
+    note(f"decode scales of 2^{power} {kind}")
+    out, lse = gdn.attn_decode(q.cuda(), kc.cuda(), vc.cuda(), ks.cuda(), torch.full_like(vs, 2.0 ** power).cuda(), *rest)
+    assert (np.abs(lse.cpu().numpy() - wlse) <= tl + 2.0 ** -15).all()
+    if abs(power) <= 100:
+        assert (np.abs(np.ldexp(out.double().cpu().numpy(), -power) - want) <= to).all()
+
+
 @pytest.mark.parametrize("lens", [[40], [5000, 40, 0]])
 def test_decode_queries_that_are_not_finite(lens):
     """A head whose query is not finite gets NaN, and no other head does; a request without tokens gets zeros even so."""
