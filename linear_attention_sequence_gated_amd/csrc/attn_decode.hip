@@ -313,6 +313,16 @@ template <class At> __device__ __forceinline__ Place place_of(const DecodeArgs& 
   return p;
 }
 
+// The workspace: two slots to a share, outputs [2 W][Gc][D] and behind them maxima
+// and sums [2 W][Gc][2], so that each is aligned to what it is read by (a slot of
+// both would begin 8 bytes off for every other odd Gc).
+__device__ __forceinline__ float* outputs_at(const DecodeArgs& a, const DecodeSizes& z, int D, size_t slot) {
+  return a.ws + slot * z.Gc * D;
+}
+__device__ __forceinline__ float* sums_at(const DecodeArgs& a, const DecodeSizes& z, int D, size_t slot) {
+  return a.ws + (size_t)2 * z.W * z.Gc * D + slot * z.Gc * 2;
+}
+
 template <int D, int FMT, int NW, bool WHOLE> __global__ __launch_bounds__(64 * NW, 2) void attn_decode_kernel(DecodeArgs a, DecodeSizes z) {
   constexpr int NB = D / 16, LD = D + 4, kStep = NW * kTile;
   static_assert(WHOLE || kStep == kUnit, "");
@@ -476,13 +486,13 @@ template <int D, int FMT, int NW, bool WHOLE> __global__ __launch_bounds__(64 * 
     }
     const bool whole = ua == 0 && ub == nu;
     const size_t slot = 2 * (size_t)blockIdx.x + (first ? 0 : 1);
-    float* o_ws = a.ws + slot * z.Gc * (D + 2);
+    float *o_ws = outputs_at(a, z, D, slot), *m_ws = sums_at(a, z, D, slot);
     if (wave == 0 && lane < cols) {
       if (whole) {
         if (a.lse) a.lse[(size_t)rr * z.Hq + q0 + lane] = L == 0.f ? -INFINITY : (M + (kDown + __builtin_amdgcn_logf(L))) * kLn2;
       } else {
-        o_ws[z.Gc * D + 2 * lane] = M;
-        o_ws[z.Gc * D + 2 * lane + 1] = L;
+        m_ws[2 * lane] = M;
+        m_ws[2 * lane + 1] = L;
       }
     }
     __syncthreads();
@@ -597,7 +607,7 @@ template <int D, int DS, bool CUTS> __global__ __launch_bounds__(128 * (DS == 1 
   const bool writes_lse = tid == 0 && d0 == 0 && a.lse;
   auto at = [&](int i) {
     const bool head_of_share = U * i / z.W >= P;
-    return a.ws + (2 * (size_t)i + (head_of_share ? 0 : 1)) * z.Gc * (D + 2);
+    return 2 * (size_t)i + (head_of_share ? 0 : 1);
   };
   // maxima and sums of the shares first, as weights; then the outputs, their
   // loads independent of one another
@@ -605,7 +615,7 @@ template <int D, int DS, bool CUTS> __global__ __launch_bounds__(128 * (DS == 1 
   float M = kLowest;
   for (int i = tid; i < n_parts; i += NT) {
     const bool any = U * (i0 + i) / z.W < U * (i0 + i + 1) / z.W;  // a share may be without units
-    const float2 x = any ? *reinterpret_cast<const float2*>(at(i0 + i) + z.Gc * D + 2 * col) : make_float2(kLowest, 0.f);
+    const float2 x = any ? *reinterpret_cast<const float2*>(sums_at(a, z, D, at(i0 + i)) + 2 * col) : make_float2(kLowest, 0.f);
     weight[i] = x.x;
     part_l[i] = x.y;
     M = fmaxf(M, x.x);
@@ -625,7 +635,7 @@ template <int D, int DS, bool CUTS> __global__ __launch_bounds__(128 * (DS == 1 
   for (int i = part; i < n_parts; i += NP) {
     const float e = weight[i];
     L += e * part_l[i];
-    if (e != 0.f) o += *reinterpret_cast<const f32x4*>(at(i0 + i) + col * D + d0 + d) * e;
+    if (e != 0.f) o += *reinterpret_cast<const f32x4*>(outputs_at(a, z, D, at(i0 + i)) + col * D + d0 + d) * e;
   }
 #pragma unroll
   for (int x = C / 4; x < 64; x <<= 1) {  // over the shares of a wave
