@@ -110,6 +110,23 @@ __device__ __forceinline__ void take_keys(Rows<D>& x, const __bf16* kt, const __
     for (int b = 0; b < 2 * NH; ++b) x.o[i] = mma(col_frag<D>(vt, vb, 16 * b, i), p[b], x.o[i]);
 }
 
+// Where rows lo .. hi - 1 of V hold values that are not finite.
+template <int D, int N, int NT>
+__device__ __forceinline__ void mark_values(Marks<D, N>& up, Marks<D, N>& down, const void* v, long long stride, int lo,
+                                            int hi, int r0) {
+  up.template clear<NT>();
+  down.template clear<NT>();
+  __syncthreads();
+  up.template look<NT, Kind::up>(v, stride, lo, hi, r0);
+  down.template look<NT, Kind::down>(v, stride, lo, hi, r0);
+  __syncthreads();
+}
+__device__ __forceinline__ float with_infinities(float x, bool up, bool down) {
+  if (up) x += INFINITY;
+  if (down) x -= INFINITY;
+  return x;
+}
+
 // NW / KP waves of a workgroup take 32 rows each; KP = 2: the others the same rows
 // and the second half of each tile's keys, added at the end.  That halves a row's
 // chain of tiles for twice the reads of keys (1 x 5000 x 16/4 x 128 140 us for 174,
@@ -130,6 +147,7 @@ template <int D, int NW, int KP> __global__ __launch_bounds__(64 * NW, D == 64 ?
   auto &kt = mem.staged.k, &vt = mem.staged.v;
   __shared__ float ml[2][BM];
   __shared__ int begs[BM], window[kWindow], ranges[3][NW], bad[2][NW];
+  __shared__ Marks<D, BM> up, down;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const int tiles = (a.T + BM - 1) / BM;
   // the tiles with the most keys (of a long sequence: the last) first, all heads of a tile side by side
@@ -244,6 +262,7 @@ template <int D, int NW, int KP> __global__ __launch_bounds__(64 * NW, D == 64 ?
     take_keys<D, NH, false>(x, kt[buf] + ko * D, vt[buf] + ko * D, kb0, vb0, q, c, 0, 0, [] {}, [] {});
   }
   edge(last);
+  if (dirty_hi) mark_values<D, BM, NT>(up, down, vp, a.vs, dirty_lo, min(dirty_hi, last), r0);
 
   float z = sum_halves(x.l);
   if constexpr (KP == 2) {  // the second half of each tile's keys, handed to the waves of the first
@@ -286,14 +305,13 @@ template <int D, int NW, int KP> __global__ __launch_bounds__(64 * NW, D == 64 ?
       *reinterpret_cast<u32x2*>(dst + 32 * i + 8 * e + 4 * hl) =
           pipe::cvt4(f32x4{x.o[i][4 * e] * inv, x.o[i][4 * e + 1] * inv, x.o[i][4 * e + 2] * inv, x.o[i][4 * e + 3] * inv});
   if (hl == 0) a.lse[(size_t)hq * a.T + row] = rest ? 0.f : (x.m + __builtin_amdgcn_logf(z)) * kLn2;
-  if (rest) return;
-  for (int key = max(beg, dirty_lo); key <= row && key < dirty_hi; ++key) {
-    const __bf16* src = static_cast<const __bf16*>(a.v) + (long long)key * a.vs + (long long)kvh * D;
-    for (int d = 4 * hl; d < D; d += 8)  // the entries that this lane stored
-      for (int i = 0; i < 4; ++i) {
-        const float y = (float)src[d + i];
-        if (!__builtin_isfinite(y)) dst[d + i] = (__bf16)((float)dst[d + i] + y);
-      }
+  if (rest || !dirty_hi) return;
+  const int lo = max(beg - r0, 0), hi = row - r0 + 1;
+  for (int w = 0; w < DT; ++w) {
+    const unsigned u = up.columns(w, lo, hi, beg < r0), n = down.columns(w, lo, hi, beg < r0);
+    if (u | n)
+      for (int d = 4 * hl; d < 32; d += 8)  // the entries that this lane stored
+        for (int i = d; i < d + 4; ++i) dst[32 * w + i] = (__bf16)with_infinities((float)dst[32 * w + i], u >> i & 1, n >> i & 1);
   }
 }
 
@@ -302,7 +320,7 @@ template <int D, int NW, int KP> __global__ __launch_bounds__(64 * NW, D == 64 ?
 // joined through LDS at the end.  A row's chain of tiles is a quarter as long for
 // four times the reads of keys: 1 x 1000 x 16/4 x 128 15.6 us for 36.2, 1 x 2500
 // x 12/4 x 64 25 for 50, 1 x 131 5.2 for 6.6; 8 x 2048 112 for 75.
-template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_split_kernel(PromptArgs a) {
+template <int D, int NW> __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : 2) void attn_prompt_split_kernel(PromptArgs a) {
   constexpr int kN = 32, NT = 64 * NW, KS = D / 16, DT = D / 32, LD = D + 4;
   __shared__ union alignas(16) {
     __bf16 staged[NW][2][kN * D];
@@ -311,6 +329,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_prom
   auto& part = mem.part;
   __shared__ float ml[NW][2][32];
   __shared__ int begs[32], window[kWindow], dirty[2][NW];
+  __shared__ Marks<D, 32> up, down;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const int tiles = (a.T + 31) / 32;
   const int rank = blockIdx.x / a.Hq, hq = blockIdx.x - rank * a.Hq;
@@ -417,6 +436,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_prom
     dirty_lo = min(dirty_lo, dirty[0][w]);
     dirty_hi = max(dirty_hi, dirty[1][w]);
   }
+  if (dirty_hi) mark_values<D, 32, NT>(up, down, vp, a.vs, dirty_lo, min(dirty_hi, last), r0);
   for (int i = tid; i < 32 * (D / 4); i += NT) {
     const int r = i / (D / 4), d = i % (D / 4) * 4, b = begs[r];
     if (r0 + r >= a.T || (b < 0 && !a.zero_rest)) continue;
@@ -430,12 +450,11 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_prom
       o += *reinterpret_cast<const f32x4*>(&part[w][r][d]);
     }
     o *= 1.f / L;
-    if (b >= 0)
-      for (int key = max(b, dirty_lo); key <= r0 + r && key < dirty_hi; ++key) {
-        const __bf16* src = static_cast<const __bf16*>(a.v) + (long long)key * a.vs + (long long)kvh * D + d;
-        for (int j = 0; j < 4; ++j)
-          if (!__builtin_isfinite((float)src[j])) o[j] += (float)src[j];
-      }
+    if (dirty_hi && b >= 0) {
+      const int lo = max(b - r0, 0);
+      const unsigned u = up.columns(d / 32, lo, r + 1, b < r0), n = down.columns(d / 32, lo, r + 1, b < r0);
+      for (int j = 0; j < 4; ++j) o[j] = with_infinities(o[j], u >> (d % 32 + j) & 1, n >> (d % 32 + j) & 1);
+    }
     if (b < 0) o = pipe::zero4();
     *reinterpret_cast<u32x2*>(static_cast<__bf16*>(a.out) + ((size_t)(r0 + r) * a.Hq + hq) * D + d) = pipe::cvt4(o);
     if (d == 0) a.lse[(size_t)hq * a.T + r0 + r] = b < 0 ? 0.f : (M + __builtin_amdgcn_logf(L)) * kLn2;

@@ -56,20 +56,22 @@ template <int D> __device__ __forceinline__ void store_rows(__bf16* dst, const f
           pipe::cvt4(f32x4{acc[i][4 * e] * f, acc[i][4 * e + 1] * f, acc[i][4 * e + 2] * f, acc[i][4 * e + 3] * f});
 }
 
-// What scrubbing left out of a gradient row: NaN into its entries where rows
-// [lo, hi) of src hold a value that is not finite, or, with `all`, into all of
-// them if there is any.  Each lane sees to the entries that it stored.
-template <int D, class T>
-__device__ __forceinline__ void spoil(T* dst, const void* src, long long stride, int lo, int hi, bool all, int hl) {
-  for (int i = lo; i < hi; ++i) {
-    const __bf16* x = static_cast<const __bf16*>(src) + (long long)i * stride;
-    bool any = false;
-    if (all)
-      for (int d = 0; d < D; ++d) any |= !__builtin_isfinite((float)x[d]);
-    for (int d = 4 * hl; d < D; d += 8)
-      for (int j = 0; j < 4; ++j)
-        if (any || !__builtin_isfinite((float)x[d + j])) dst[d + j] = (T)__builtin_nanf("");
-  }
+// What scrubbing left out of a gradient row: NaN into those of its columns 32 w ..
+// whose bit is set.  Each lane sees to the entries that it stored.
+template <class T> __device__ __forceinline__ void spoil(T* dst, int w, unsigned columns, int hl) {
+  if (columns)
+    for (int d = 4 * hl; d < 32; d += 8)
+      for (int i = d; i < d + 4; ++i)
+        if (columns >> i & 1) dst[32 * w + i] = (T)__builtin_nanf("");
+}
+
+// Which of rows lo .. hi - 1 of K hold values that are not finite.
+template <int D, int N, int NT>
+__device__ __forceinline__ void mark_keys(Marks<D, N>& marks, const void* k, long long stride, int lo, int hi, int r0) {
+  marks.template clear<NT>();
+  __syncthreads();
+  marks.template look<NT, Kind::not_finite>(k, stride, lo, hi, r0);
+  __syncthreads();
 }
 
 // The waves' sums of 32 rows (a lane's row: l % 32), one beside the other in LDS,
@@ -91,14 +93,6 @@ template <int D, int NW> __device__ __forceinline__ f32x4 joined(const Parts<D, 
 #pragma unroll
   for (int w = 1; w < NW; ++w) o += *reinterpret_cast<const f32x4*>(&part[w][r][d]);
   return o;
-}
-
-// Whether rows [lo, hi) of src hold a value that is not finite.
-template <int D> __device__ __forceinline__ bool spoiled(const void* src, long long stride, int lo, int hi) {
-  bool any = false;
-  for (int i = lo; i < hi; ++i)
-    for (int d = 0; d < D; ++d) any |= !__builtin_isfinite((float)(static_cast<const __bf16*>(src) + (long long)i * stride)[d]);
-  return any;
 }
 
 // ---------------------------------------------------------------------- dq
@@ -162,6 +156,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
   constexpr int BM = 32 * NW, NT = 64 * NW, KS = D / 16;
   __shared__ alignas(16) __bf16 kt[2][kN * D], vt[2][kN * D];
   __shared__ int begs[BM], window[kWindow], ranges[3][NW], bad[2][NW];
+  __shared__ Marks<D, BM> marks;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const int tiles = (a.T + BM - 1) / BM;
   const int rank = blockIdx.x / a.Hq, hq = blockIdx.x - rank * a.Hq;
@@ -281,9 +276,12 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
   const bool outside = beg < 0 && row < a.T && a.zero_rest;
   if (beg >= 0 || outside)
     store_rows<D>(static_cast<__bf16*>(a.grad_q) + (long long)row * a.gqs + (long long)hq * D, dq, outside ? 0.f : a.scale, hl);
-  if (dirty_hi && beg >= 0)  // a key that is not finite spoils the weights of all rows that see it
-    spoil<D>(static_cast<__bf16*>(a.grad_q) + (long long)row * a.gqs + (long long)hq * D, kp, a.ks, max(beg, dirty_lo),
-             min(row + 1, dirty_hi), true, hl);
+  if (dirty_hi) {  // a key that is not finite spoils the weights of all rows that see it
+    mark_keys<D, BM, NT>(marks, kp, a.ks, dirty_lo, min(dirty_hi, last), r0);
+    if (beg >= 0 && marks.any(max(beg - r0, 0), row - r0 + 1, beg < r0))
+      for (int w = 0; w < D / 32; ++w)
+        spoil(static_cast<__bf16*>(a.grad_q) + (long long)row * a.gqs + (long long)hq * D, w, ~0u, hl);
+  }
 }
 
 // Few rows, as in the forward: a workgroup takes 32 rows and its waves every
@@ -300,6 +298,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_s
   __shared__ alignas(16) __bf16 gt[GLDS ? 32 * D : 8];
   __shared__ float rests[NW][32];
   __shared__ int begs[32], window[kWindow], dirty[2][NW];
+  __shared__ Marks<D, 32> marks;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const int tiles = (a.T + 31) / 32;
   const int rank = blockIdx.x / a.Hq, hq = blockIdx.x - rank * a.Hq;
@@ -393,12 +392,13 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_s
     a.ws[(size_t)hq * a.T + row] = lse2;
     a.ws[(size_t)(a.Hq + hq) * a.T + row] = -(delta + more);
   }
+  if (dirty_hi) mark_keys<D, 32, NT>(marks, kp, a.ks, dirty_lo, min(dirty_hi, last), r0);
   for (int i = tid; i < 32 * (D / 4); i += NT) {
     const int r = i / (D / 4), d = i % (D / 4) * 4, b = begs[r];
     if (r0 + r >= a.T || (b < 0 && !a.zero_rest)) continue;
     f32x4 o = joined<D, NW>(mem.part, r, d) * (b < 0 ? 0.f : a.scale);
     if (b < 0) o = pipe::zero4();
-    if (b >= 0 && spoiled<D>(kp, a.ks, max(b, dirty_lo), min(r0 + r + 1, dirty_hi))) o += __builtin_nanf("");
+    if (dirty_hi && b >= 0 && marks.any(max(b - r0, 0), r + 1, b < r0)) o += __builtin_nanf("");
     *reinterpret_cast<u32x2*>(static_cast<__bf16*>(a.grad_q) + (long long)(r0 + r) * a.gqs + (long long)hq * D + d) = pipe::cvt4(o);
   }
 }
@@ -441,33 +441,38 @@ __device__ __forceinline__ void write_grad(const PromptBwdArgs& a, const Share& 
                   acc, rest ? 0.f : f, hl);
 }
 
-// Rows of q that are not finite spoil the weights of their keys, dk and dv
-// whole; rows of do that are not finite dk whole and dv where they are not.
-template <int D>
-__device__ __forceinline__ void spoil_grad(const PromptBwdArgs& a, const Share& sh, bool values, int key, int end, int hl) {
-  for (int x = 0; x < 2 * sh.heads; ++x) {
-    const bool outer = x & 1;  // do
-    const __bf16* src = static_cast<const __bf16*>(outer ? a.grad_out : a.q) + (long long)(sh.h0 + x / 2) * D;
-    const long long stride = outer ? a.gos : a.qs;
-    const bool all = !(outer && values);
-    if (a.shares > 1)
-      spoil<D>(sums_row(a, D, sh.at, values, key, sh.kvh), src, stride, key, end, all, hl);
-    else
-      spoil<D>(static_cast<__bf16*>(values ? a.grad_v : a.grad_k) + (long long)key * (values ? a.gvs : a.gks) + (long long)sh.kvh * D,
-               src, stride, key, end, all, hl);
+// Which rows of q and of do, of the share's heads, hold values that are not finite.
+// Those of q spoil the weights of their keys, dk and dv whole; those of do dk whole
+// and dv where they are.
+template <int D, int N> struct RowMarks {
+  Marks<D, N> q, g;
+  template <int NT> __device__ __forceinline__ void look(const PromptBwdArgs& a, const Share& sh, int r0, int last) {
+    q.template clear<NT>();
+    g.template clear<NT>();
+    __syncthreads();
+    for (int h = sh.h0; h < sh.h0 + sh.heads; ++h) {
+      q.template look<NT, Kind::not_finite>(static_cast<const __bf16*>(a.q) + (long long)h * D, a.qs, r0, last, r0);
+      g.template look<NT, Kind::not_finite>(static_cast<const __bf16*>(a.grad_out) + (long long)h * D, a.gos, r0, last, r0);
+    }
+    __syncthreads();
   }
-}
-
-// The same for four entries, d on, of a key's sums.
-template <int D>
-__device__ __forceinline__ void spoil_sums(f32x4& o, const PromptBwdArgs& a, const Share& sh, bool values, int key, int end, int d) {
-  for (int h = sh.h0; h < sh.h0 + sh.heads; ++h) {
-    const __bf16 *q = static_cast<const __bf16*>(a.q) + (long long)h * D, *g = static_cast<const __bf16*>(a.grad_out) + (long long)h * D;
-    if (spoiled<D>(q, a.qs, key, end) || (!values && spoiled<D>(g, a.gos, key, end))) o += __builtin_nanf("");
-    if (values)
-      for (int i = key; i < end; ++i)
-        for (int j = 0; j < 4; ++j)
-          if (!__builtin_isfinite((float)g[(long long)i * a.gos + d + j])) o[j] = __builtin_nanf("");
+  // Columns 32 w .. of dk (of dv) that the rows from lo to hi - 1 (from r0), and with
+  // `others` those behind the tile, spoil.
+  __device__ __forceinline__ unsigned columns(bool values, int w, int lo, int hi, bool others) const {
+    if (q.any(lo, hi, others)) return ~0u;
+    if (values) return g.columns(w, lo, hi, others);
+    return g.any(lo, hi, others) ? ~0u : 0u;
+  }
+};
+template <int D, int N>
+__device__ __forceinline__ void spoil_grad(const PromptBwdArgs& a, const Share& sh, const RowMarks<D, N>& marks, bool values,
+                                           int key, int r0, int end, int hl) {
+  for (int w = 0; w < D / 32; ++w) {
+    const unsigned m = marks.columns(values, w, key - r0, min(end - r0, N), end > r0 + N);
+    if (a.shares > 1)
+      spoil(sums_row(a, D, sh.at, values, key, sh.kvh), w, m, hl);
+    else
+      spoil(static_cast<__bf16*>(values ? a.grad_v : a.grad_k) + (long long)key * (values ? a.gvs : a.gks) + (long long)sh.kvh * D, w, m, hl);
   }
 }
 
@@ -569,6 +574,7 @@ template <int D, int NW, int NR, bool VLDS> __global__ __launch_bounds__(64 * NW
   __shared__ alignas(16) float lt[2][64], dt[2][64];
   __shared__ alignas(16) __bf16 vt[VLDS ? BN * D : 8];
   __shared__ int begs[BN], ends[BN], window[kWindow], most[2][NW], bad[2][NW];
+  __shared__ RowMarks<D, BN> marks;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   // the first tiles of a long sequence meet the most rows
   Share sh = share_of(a);
@@ -697,9 +703,9 @@ template <int D, int NW, int NR, bool VLDS> __global__ __launch_bounds__(64 * NW
   }
   write_grad<D>(a, sh, false, key, end, dk, a.scale, hl);
   write_grad<D>(a, sh, true, key, end, dv, 1.f, hl);
-  if (dirty && end >= 0) {
-    spoil_grad<D>(a, sh, false, key, end, hl);
-    spoil_grad<D>(a, sh, true, key, end, hl);
+  if (dirty) {
+    marks.template look<NT>(a, sh, r0, last);
+    for (int values = 0; values < 2 && end >= 0; ++values) spoil_grad<D, BN>(a, sh, marks, values, key, r0, end, hl);
   }
 }
 
@@ -715,6 +721,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
   __shared__ alignas(16) float lt[NW][64], dt[NW][64];
   __shared__ alignas(16) __bf16 vt[VLDS ? 32 * D : 8];
   __shared__ int begs[32], ends[32], window[kWindow], dirty[NW];
+  __shared__ RowMarks<D, 32> marks;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const Share sh = share_of(a);
   const int r0 = sh.tile * 32, kvh = sh.kvh;
@@ -791,16 +798,22 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_
     }
   }
   if (lane == 0) dirty[wave] = bad;
+  __syncthreads();
+  const bool any = !all_clean(dirty);
+  if (any) marks.template look<NT>(a, sh, r0, last);
   for (int values = 0; values < 2; ++values) {
     if (values) join_rows<D, NW>(mem.part, dv, wave, lane);
     else join_rows<D, NW>(mem.part, dk, wave, lane);
-    const bool any = !all_clean(dirty);
     for (int x = tid; x < 32 * (D / 4); x += NT) {
       const int r = x / (D / 4), d = x % (D / 4) * 4, e = ends[r];
       if (r0 + r >= a.T || (e < 0 && (!a.zero_rest || a.shares > 1))) continue;
       f32x4 o = joined<D, NW>(mem.part, r, d) * (values ? 1.f : a.scale);
       if (e < 0) o = pipe::zero4();
-      if (any && e >= 0) spoil_sums<D>(o, a, sh, values, r0 + r, e, d);
+      if (any && e >= 0) {
+        const unsigned m = marks.columns(values, d / 32, r, min(e - r0, 32), e > r0 + 32);
+        for (int j = 0; j < 4; ++j)
+          if (m >> (d % 32 + j) & 1) o[j] = __builtin_nanf("");
+      }
       if (a.shares > 1)
         *reinterpret_cast<f32x4*>(sums_row(a, D, sh.at, values, r0 + r, kvh) + d) = o;
       else

@@ -185,6 +185,53 @@ template <int D> __device__ __forceinline__ u32x4 col_frag(const __bf16* lds, in
   return pipe::pair(a, b);
 }
 
+// Which columns of rows r0 .. r0 + N - 1 of an array hold values of a kind, and
+// which of the rows before or behind those, taken together: a tile of rows (keys)
+// sees either all of the keys before it (rows behind it) that are of its first
+// (last) sequence, or none.  For what was left out of masked tiles: a workgroup
+// reads the rows once, whatever they hold, and each lane then a word per row of the
+// tile from LDS.  In LDS; look() and clear() by NT threads, with barriers between.
+enum class Kind { not_finite, up, down };  // up, down: infinities of that sign, and NaN
+template <int D, int N> struct Marks {
+  unsigned row[N][D / 32], rest[D / 32];
+  static __device__ __forceinline__ unsigned is(unsigned h, Kind kind) {  // of the lower half
+    const unsigned size = h & 0x7fffu;
+    if (kind == Kind::not_finite) return size >= 0x7f80u;
+    return size > 0x7f80u || (h & 0xffffu) == (kind == Kind::up ? 0x7f80u : 0xff80u);
+  }
+  template <int NT> __device__ __forceinline__ void clear() {
+    for (int i = threadIdx.x; i < (N + 1) * (D / 32); i += NT) (&row[0][0])[i] = 0u;
+  }
+  template <int NT, Kind KIND>
+  __device__ __forceinline__ void look(const void* src, long long stride, int lo, int hi, int r0) {
+    constexpr int NU = D / 8;  // pieces of eight to a row
+    static_assert(NT % NU == 0, "");
+    const int u = threadIdx.x % NU, shift = 8 * (u % 4);
+    unsigned others = 0;
+#pragma unroll 4
+    for (int i = lo + (int)threadIdx.x / NU; i < hi; i += NT / NU) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const __hip_bfloat16*>(src) + (long long)i * stride + 8 * u);
+      unsigned m = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m |= is(w[e], KIND) << (2 * e) | is(w[e] >> 16, KIND) << (2 * e + 1);
+      if (i < r0 || i >= r0 + N) others |= m;
+      else if (m) atomicOr(&row[i - r0][u / 4], m << shift);
+    }
+    if (others) atomicOr(&rest[u / 4], others << shift);
+  }
+  // Columns 32 w .. of rows lo .. hi - 1 (from r0), and of the others.
+  __device__ __forceinline__ unsigned columns(int w, int lo, int hi, bool others) const {
+    unsigned m = others ? rest[w] : 0u;
+    for (int i = lo; i < hi; ++i) m |= row[i][w];
+    return m;
+  }
+  __device__ __forceinline__ bool any(int lo, int hi, bool others) const {
+    unsigned m = 0;
+    for (int w = 0; w < D / 32; ++w) m |= columns(w, lo, hi, others);
+    return m != 0;
+  }
+};
+
 // Until this wave's loads into LDS have arrived.
 __device__ __forceinline__ void wait_staged() {
   __builtin_amdgcn_sched_barrier(0);
