@@ -37,6 +37,8 @@
 // slower.
 #include <hip/hip_bf16.h>
 
+#include <algorithm>
+
 #include "../../include/gdn.h"
 #include "gdn_attn.hpp"
 #include "gdn_launch.hpp"
@@ -675,20 +677,23 @@ DecodeSizes sizes(int R, int Hq, int Hkv, int D, int bt, int width, int num_bloc
   const long long units = width ? (((long long)width * bt + kUnit - 1) / kUnit + kAhead) * R * Hkv * z.NG : 0;
   const int most = most_shares(D);
   z.W = units < most ? (int)units : most;
-  // one workgroup to a (request, key head), and no join, if none can be long; the
-  // more of them there are, the longer they may be before the longest is what the
-  // call takes.  Both ways, us on the GPU: 1 x 777 x 12/4 x 64 6.6 for 9.4, 64
-  // ragged of up to 1500 x 16/4 x 128 14.9 for 20.2, 300 of up to 120 9.8 for 20.4,
-  // of up to 2000 60.6 for 78.4, of up to 8000 229 for 243; 16 of 2000 16.4 for
-  // 13.8.  With cold caches, calls: 64 of up to 4099 34.4 for 36.4, 64 of 4000 x
-  // 16/4 x 64 30 for 38, but 64 of up to 4099 x 12/4 x 64 25.8 for 24.4 and 128 of
-  // up to 4099 x 16/4 x 128, more than run at once, 66.5 for 63.3.
-  const long long groups = (long long)R * Hkv * z.NG, cap = ((long long)width * bt + kUnit - 1) / kUnit;
-  const long long at_once = D == 64 ? 512 : 256;  // of eight waves
-  z.whole = cap <= (groups < 256 ? 8 : groups <= at_once ? 40 : groups < 1024 ? 24 : 64);
+  // one workgroup to a (request, key head), and no join, if none can be long.  Such a
+  // call takes as long as the longest of them, the shares what all together and a join
+  // take: where each has a CU of its own, the more there are, the longer they may be;
+  // beyond that the last ones wait for a CU, and the length that may be grows again as
+  // there are more to fill in.  Both ways, us on the GPU, x 16/4 heads, uniformly
+  // ragged.  128: 8 of up to 1000 10.9 for 12.5, 32 of 2000 17.8 for 16.5, 56 of 4200 31.5
+  // for 32.9, 63 of 5100 37.9 for 38.4, 64 of 4200 32.6 for 34.4, 65 of 4200 36.0 for
+  // 36.0, 80 of 2000 27.1 for 28.7, of 4200 46.6 for 43.0, 128 of 4200 62 for 66, 256 of
+  // 8000 209 for 220.  64: 8 of 1000 7.9 for 11.4, 48 of 2900 17.4 for 18.6, 64 of 4200
+  // 22.5 for 23.3, of 5100 26.5 for 25.4, 65 of 2000 17.6 for 18.3, of 4200 28.8 for
+  // 24.3, 128 of 5100 38 for 42, 256 of 8000 118 for 124.
+  const long long groups = (long long)R * Hkv * z.NG, cap = ((long long)width * bt + kUnit - 1) / kUnit, cus = 256;
+  z.whole = cap <= (groups <= cus ? std::max(8LL, groups / 7) : std::min(64LL, std::max(24LL, groups / 16)));
   // eight waves to each where that leaves none waiting for a CU, and for the long
   // ones: 64 ragged of up to 777 x 16/4 x 128 9.4 for 10.5 with four, 300 of up to
   // 777 36 for 26
+  const long long at_once = D == 64 ? 512 : 256;  // of eight waves
   if (z.whole) z.whole = cap > 4 && (groups <= at_once || cap > 16) ? 8 : 4;
   return z;
 }

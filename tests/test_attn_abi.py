@@ -101,6 +101,21 @@ def test_decode_workspace():
     assert decode(R=0, q=None, seq_lens=None, out=None) == raw.GDN_OK
 
 
+def test_decode_forms_follow_groups_and_widths():
+    """The longest table, in units of 128 tokens, that one workgroup to a request and key head takes: it grows with
+    their number while each has a CU, whatever the head size, and again with how many wait for one."""
+    for D in (64, 128):
+        def whole(groups):
+            units = 0
+            while gdn.gdn_attn_decode_workspace_bytes(groups, 1, 1, D, 128, units + 1) == 0:
+                units += 1
+            return units
+        few = [whole(g) for g in range(1, 257)]
+        assert few == sorted(few) and few[0] == 8 and max(b - a for a, b in zip(few, few[1:])) == 1
+        many = [whole(g) for g in range(257, 1200, 7)]
+        assert many == sorted(many) and many[-1] == 64 and max(b - a for a, b in zip(many, many[1:])) == 1
+
+
 def test_decode_longest_tables():
     """A length on the device may be anything and is cut to the table's width; tokens are counted in 32 bits, some way
     past that, so the widest tables are refused."""

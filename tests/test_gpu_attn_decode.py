@@ -129,6 +129,25 @@ def test_decode_shares_that_begin_and_end_anywhere(R, D, H):
     check(torch, *make(torch, rng, lens, 2 * H, H, D, 128, "int8"))
 
 
+def forms(R, H, longest):
+    """Whether one workgroup takes all of a request and key head (there is nothing to join) for tables of `longest`."""
+    import linear_attention_sequence_gated_amd as gdn
+    return gdn.gdn_attn_decode_workspace_bytes(R, 2 * H, H, 64, 16, -(-longest // 16)) == 0
+
+
+@pytest.mark.parametrize("D,kind", [(64, "int8"), (128, "e4m3")])
+@pytest.mark.parametrize("R,H,longest", [(60, 4, 4000), (63, 4, 4500), (64, 4, 4600), (65, 4, 2500), (126, 2, 3400), (1030, 1, 5200), (40, 9, 2900)])
+def test_decode_long_requests_in_one_workgroup(R, H, longest, D, kind):
+    """Long requests that one workgroup takes each, many of them: a few of the longest among short ones."""
+    torch = torch_dev()
+    rng = np.random.default_rng(R + longest)
+    lens = rng.choice([0, 1, 33, 128, 300, 511], R)
+    lens[rng.permutation(R)[:5]] = [longest, longest - 1, longest - 15, longest // 2 + 7, 1025]
+    note(f"decode whole R{R} H{H} {longest} D{D} {kind}")
+    assert forms(R, H, longest)
+    check(torch, *make(torch, rng, lens, 2 * H, H, D, 16, kind))
+
+
 def test_decode_many_requests_of_many_heads():
     """More query heads to a key head than columns, the last group in part, more rows than ends of shares."""
     torch = torch_dev()
