@@ -91,6 +91,33 @@ def test_packed_prompts(lens, Hq, H, D, fused):
     check_forward(torch, *make(torch, np.random.default_rng(len(lens)), sum(lens), Hq, H, D, fused), offsets(lens))
 
 
+RANKED = {
+    "equal": [350] * 13,
+    "ragged": [1201, 0, 700, 3, 0, 512, 640, 1, 900, 128, 127, 129, 261],
+    "one long": [1900] + [5, 200, 64, 0, 131] * 7,
+    "many": [17, 40, 3, 128, 0, 60] * 19,
+}
+
+
+def ranked(T, R, heads):
+    """Whether tiles of 128 rows are taken by their length: several sequences, more workgroups than run at once."""
+    tiles = -(-T // 128)
+    mean = T // R
+    return 1 < R < 512 and tiles <= 256 and tiles * heads > 512 and T * heads * (600 + mean) >= 108000 * mean
+
+
+@pytest.mark.parametrize("lens", RANKED.values(), ids=RANKED.keys())
+@pytest.mark.parametrize("H,D", [(16, 64), (4, 128)])
+def test_tiles_taken_by_length(lens, H, D):
+    """Every tile is taken once, whatever the lengths: ties, empty sequences, rows outside, tiles no multiple of four."""
+    torch = torch_dev()
+    cu = offsets(lens, 37)
+    T = int(cu[-1]) + 150
+    assert ranked(T, len(lens), 16) and ranked(T, len(lens) + 260, 16)
+    note(f"by length {len(lens)} sequences H{H} D{D}")
+    check_forward(torch, *make(torch, np.random.default_rng(len(lens)), T, 16, H, D), cu)
+
+
 def test_thousands_of_sequences():
     torch = torch_dev()
     lens = np.random.default_rng(1).integers(0, 4, 5000)

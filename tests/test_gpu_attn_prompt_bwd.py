@@ -12,7 +12,7 @@ import pytest
 
 from gpu_util import note, torch_dev
 from oracle import attention as ref
-from test_gpu_attn_prompt import BEHIND, RAGGED, cu_of, host, make, offsets, padded  # noqa: F401
+from test_gpu_attn_prompt import BEHIND, RAGGED, RANKED, cu_of, host, make, offsets, padded, ranked  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 U, F = 2.0 ** -8, 2.0 ** -12
@@ -78,6 +78,29 @@ def test_packed_prompts(lens, Hq, H, D, fused):
     torch = torch_dev()
     note(f"bwd packed {len(lens)} sequences Hq{Hq} H{H} D{D}")
     check(torch, *make(torch, np.random.default_rng(len(lens)), sum(lens), Hq, H, D, fused), offsets(lens))
+
+
+@pytest.mark.parametrize("lens", RANKED.values(), ids=RANKED.keys())
+@pytest.mark.parametrize("H,D", [(16, 64), (4, 64), (16, 128), (4, 128)])
+def test_tiles_taken_by_length(lens, H, D):
+    """Rows and keys: four key heads are shared out by query heads, so that there are as many workgroups."""
+    torch = torch_dev()
+    cu = offsets(lens, 37)
+    T = int(cu[-1]) + 150
+    assert ranked(T, len(lens), 16) and ranked(T, len(lens) + 260, 16)
+    note(f"bwd by length {len(lens)} sequences H{H} D{D}")
+    check(torch, *make(torch, np.random.default_rng(len(lens)), T, 16, H, D), cu)
+
+
+@pytest.mark.parametrize("R,most", [(511, 9), (512, 9), (1400, 4)])
+@pytest.mark.parametrize("Hq,H,D", [(4, 4, 64), (4, 1, 64), (2, 2, 128), (4, 1, 128)])
+def test_more_sequences_than_a_window(R, most, Hq, H, D):
+    """More offsets than are looked up at once, for dq, for dk and dv, and for the sums of shared heads."""
+    torch = torch_dev()
+    lens = np.random.default_rng(R).integers(0, most + 1, R)
+    lens[R // 2] = 150
+    note(f"bwd {R} sequences Hq{Hq} H{H} D{D}")
+    check(torch, *make(torch, np.random.default_rng(R + D), int(lens.sum()), Hq, H, D), offsets(lens))
 
 
 def test_gradients_into_one_projection():
