@@ -331,8 +331,9 @@ int gdn_recurrent_step(const void *q, const void *k, const void *v, const float 
  *     other; the distance between rows is an argument, in elements, at least
  *     the row's length and a multiple of 8, so that the parts of one fused
  *     projection can be passed as they are.
- *   - Scores (scale q.k) are float32 numbers and below 2^30 in magnitude: as
- *     they grow, their exponentials lose what their fraction does.
+ *   - scale is finite, of either sign (others GDN_ERR_SHAPE).  Scores (scale
+ *     q.k) are float32 numbers and below 2^30 in magnitude: as they grow, their
+ *     exponentials lose what their fraction does.
  *   - Softmax statistics and every sum are float32; probabilities are rounded
  *     to 16 bits where they enter a matrix product.
  *   - lse is the natural logarithm of a row's sum of exp(scale q.k), float32.

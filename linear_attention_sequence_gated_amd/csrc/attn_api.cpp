@@ -2,6 +2,7 @@
 // validates every argument before anything is enqueued, then launches.
 #include <stdint.h>
 
+#include <cmath>
 #include <initializer_list>
 
 #include "../../include/gdn.h"
@@ -22,6 +23,9 @@ int status(hipError_t e) { return e == hipSuccess ? GDN_OK : GDN_ERR_HIP; }
 bool known_dtype(int d) { return d == GDN_F32 || d == GDN_BF16 || d == GDN_C64; }
 
 bool block_ok(int bt) { return bt == 16 || bt == 32 || bt == 64 || bt == 128; }
+
+// A scale that is a number: the forward's running maximum would take others for zero.
+bool scale_ok(float s) { return std::isfinite(s); }
 
 // A row stride: room for the row, 16-byte aligned rows, no offset past 2^62.
 bool stride_ok(long long s, long long row) { return s >= row && s % 8 == 0 && s < (1LL << 40); }
@@ -116,7 +120,7 @@ int gdn_attn_decode(const void* q, const void* k_cache, const void* v_cache, con
   if (const int s = cache_shape(Hkv, D, block_tokens, num_blocks)) return s;
   if (const int s = decode_shape(R, Hq, Hkv, D, block_tokens, width)) return s;
   if (dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
-  if (!stride_ok(q_stride, (long long)Hq * D)) return GDN_ERR_SHAPE;
+  if (!stride_ok(q_stride, (long long)Hq * D) || !scale_ok(scale)) return GDN_ERR_SHAPE;
   if (R == 0) return GDN_OK;
   if (!q || !seq_lens || !out || (width && !block_table)) return GDN_ERR_NULL;
   if (num_blocks && (!k_cache || !v_cache || !k_scale || !v_scale)) return GDN_ERR_NULL;
@@ -135,6 +139,7 @@ int gdn_attn_prompt(const void* q, const void* k, const void* v, const int* cu_s
   if (!known_dtype(dtype)) return GDN_ERR_DTYPE;
   if (const int s = prompt_shape(T, R, Hq, Hkv, D)) return s;
   if (dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+  if (!scale_ok(scale)) return GDN_ERR_SHAPE;
   const long long qrow = (long long)Hq * D, krow = (long long)Hkv * D;
   if (!near_ok(q_stride, qrow) || !near_ok(k_stride, krow) || !near_ok(v_stride, krow)) return GDN_ERR_SHAPE;
   if (T == 0) return GDN_OK;
@@ -159,6 +164,7 @@ int gdn_attn_prompt_bwd(const void* q, const void* k, const void* v, const void*
   if (!known_dtype(dtype)) return GDN_ERR_DTYPE;
   if (const int s = prompt_shape(T, R, Hq, Hkv, D)) return s;
   if (dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+  if (!scale_ok(scale)) return GDN_ERR_SHAPE;
   const long long qrow = (long long)Hq * D, krow = (long long)Hkv * D;
   for (const long long s : {q_stride, grad_out_stride, grad_q_stride})
     if (!near_ok(s, qrow)) return GDN_ERR_SHAPE;

@@ -193,6 +193,13 @@ def test_prompt_bwd_workspace():
     assert prompt_bwd(T=0, **none) == raw.GDN_OK
 
 
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf"), 1e39])
+@pytest.mark.parametrize("call", [decode, prompt, prompt_bwd])
+def test_scales_that_are_no_numbers(call, scale):
+    assert call(scale=scale) == raw.GDN_ERR_SHAPE
+    assert call(scale=-0.125, q=None) == raw.GDN_ERR_NULL  # past the check
+
+
 def test_cache_helpers_refuse_on_cpu():
     torch = pytest.importorskip("torch")
     i = torch.zeros(4, dtype=torch.int32)
