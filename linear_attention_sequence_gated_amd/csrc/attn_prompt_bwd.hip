@@ -155,7 +155,7 @@ __device__ __forceinline__ void dq_tile(f32x16 (&dq)[D / 32], float& rest, const
 template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(PromptBwdArgs a) {
   constexpr int BM = 32 * NW, NT = 64 * NW, KS = D / 16;
   __shared__ alignas(16) __bf16 kt[2][kN * D], vt[2][kN * D];
-  __shared__ int begs[BM], window[kWindow], ranges[3][NW], bad[2][NW];
+  __shared__ int begs[BM], window[kWindow], ranges[3][NW], dirty;  // dirty: a tile held values that are not finite
   __shared__ Marks<D, BM> marks;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   const int tiles = (a.T + BM - 1) / BM;
@@ -167,6 +167,7 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
   const int w0 = r0 + wave * 32, row = w0 + (lane & 31), at = min(row, a.T - 1);
   const float c = a.scale * kLog2e;
   u32x4 q[KS], g[KS];
+  if (tid == 0) dirty = 0;
   find_rows<BM, NT>(a.cu, a.R, a.T, r0, window, begs, nullptr, [&] {
     const __bf16* qp = static_cast<const __bf16*>(a.q) + (long long)at * a.qs + (long long)hq * D + 8 * hl;
     const __bf16* gp = static_cast<const __bf16*>(a.grad_out) + (long long)at * a.gos + (long long)hq * D + 8 * hl;
@@ -230,7 +231,6 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
   // that rounding: what they add up to is its error, and the second launch gets
   // delta without it.
   float rest = 0.f;
-  int dirty_lo = last, dirty_hi = 0;  // keys of tiles that held values that are not finite
   int buf = 0, kv = first;
   auto step = [&](auto masked_, const __bf16* K, const __bf16* V) {
     constexpr bool MASKED = decltype(masked_)::value;
@@ -245,13 +245,9 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
     if (masked) {
       wait_staged();
       const bool ok = Stage<D, kN, NW>::scrub(kt[buf], wave);
-      if (lane == 0) bad[buf][wave] = !ok;
+      if (lane == 0 && !ok) dirty = 1;
     }
     staged_barrier();
-    if (masked && !all_clean(bad[buf])) {
-      dirty_lo = min(dirty_lo, kv);
-      dirty_hi = kv + kN;
-    }
     if (kv + kN < last) stage(buf ^ 1, kv + kN);
   };
   const int whole = min(w0 + 1, last);  // waves behind the last tile take no more than the others
@@ -276,8 +272,9 @@ template <int D, int NW> __global__ __launch_bounds__(64 * NW, 2) void attn_dq_k
   const bool outside = beg < 0 && row < a.T && a.zero_rest;
   if (beg >= 0 || outside)
     store_rows<D>(static_cast<__bf16*>(a.grad_q) + (long long)row * a.gqs + (long long)hq * D, dq, outside ? 0.f : a.scale, hl);
-  if (dirty_hi) {  // a key that is not finite spoils the weights of all rows that see it
-    mark_keys<D, BM, NT>(marks, kp, a.ks, dirty_lo, min(dirty_hi, last), r0);
+  __syncthreads();
+  if (dirty) {  // a key that is not finite spoils the weights of all rows that see it
+    mark_keys<D, BM, NT>(marks, kp, a.ks, first, last, r0);
     if (beg >= 0 && marks.any(max(beg - r0, 0), row - r0 + 1, beg < r0))
       for (int w = 0; w < D / 32; ++w)
         spoil(static_cast<__bf16*>(a.grad_q) + (long long)row * a.gqs + (long long)hq * D, w, ~0u, hl);
@@ -573,7 +570,7 @@ template <int D, int NW, int NR, bool VLDS> __global__ __launch_bounds__(64 * NW
   __shared__ alignas(16) __bf16 qt[2][NR * D], gt[2][NR * D];
   __shared__ alignas(16) float lt[2][64], dt[2][64];
   __shared__ alignas(16) __bf16 vt[VLDS ? BN * D : 8];
-  __shared__ int begs[BN], ends[BN], window[kWindow], most[2][NW], bad[2][NW];
+  __shared__ int begs[BN], ends[BN], window[kWindow], most[2][NW], dirty;  // dirty: a tile held values that are not finite
   __shared__ RowMarks<D, BN> marks;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hl = lane >> 5;
   // the first tiles of a long sequence meet the most rows
@@ -582,6 +579,7 @@ template <int D, int NW, int NR, bool VLDS> __global__ __launch_bounds__(64 * NW
     sh.tile = tile_by_length<BN, NT, true>(a.cu, a.R, a.T, (a.T + BN - 1) / BN, sh.tile, window, reinterpret_cast<int*>(qt));
   const int r0 = sh.tile * BN, kvh = sh.kvh, h0 = sh.h0, heads = sh.heads;
 
+  if (tid == 0) dirty = 0;
   find_rows<BN, NT>(a.cu, a.R, a.T, r0, window, begs, ends, [] {});
   int last = -1, soonest = a.T;  // the rows behind the last that attend to the tile's keys: the most, the least
   for (int i = tid; i < BN; i += NT) {
@@ -651,7 +649,6 @@ template <int D, int NW, int NR, bool VLDS> __global__ __launch_bounds__(64 * NW
     if (wave == 0) stage_words(lt[buf], pipe::make_rsrc(a.ws + (size_t)hq * a.T + i0, n * 4));
     if (wave == 1) stage_words(dt[buf], pipe::make_rsrc(a.ws + (size_t)(a.Hq + hq) * a.T + i0, n * 4));
   };
-  bool dirty = false;  // a tile held values that are not finite
   // a tile of rows that the wave's keys may be seen by
   auto step = [&](auto masked_, int buf, int i1) {
     constexpr bool MASKED = decltype(masked_)::value;
@@ -678,10 +675,9 @@ template <int D, int NW, int NR, bool VLDS> __global__ __launch_bounds__(64 * NW
       if (masked) {
         wait_staged();
         const bool q_ok = Stage<D, NR, NW>::scrub(qt[buf], wave), g_ok = Stage<D, NR, NW>::scrub(gt[buf], wave);
-        if (lane == 0) bad[buf][wave] = !(q_ok && g_ok);
+        if (lane == 0 && !(q_ok && g_ok)) dirty = 1;
       }
       staged_barrier();
-      if (masked && !all_clean(bad[buf])) dirty = true;
       if (i1 + NR < last) stage(buf ^ 1, h0 + head, i1 + NR);
       else if (head + 1 < heads) stage(buf ^ 1, h0 + head + 1, r0);
     };
@@ -703,6 +699,7 @@ template <int D, int NW, int NR, bool VLDS> __global__ __launch_bounds__(64 * NW
   }
   write_grad<D>(a, sh, false, key, end, dk, a.scale, hl);
   write_grad<D>(a, sh, true, key, end, dv, 1.f, hl);
+  __syncthreads();
   if (dirty) {
     marks.template look<NT>(a, sh, r0, last);
     for (int values = 0; values < 2 && end >= 0; ++values) spoil_grad<D, BN>(a, sh, marks, values, key, r0, end, hl);

@@ -163,6 +163,90 @@ def test_waves_behind_the_last_key(first, end, D):
             assert (a[outside] == 0).all() and torch.equal(a[first:end], b[first:end])
 
 
+def reached(lens, bad, Hq, H):
+    """Where results cannot be finite, given where q, k, v and do are not: by the formulas, every row for itself."""
+    q, k, v, do = bad
+    G, cu = Hq // H, offsets(lens)
+    out, dq, dk, dv = (np.zeros_like(x) for x in (q, q, k, v))
+    for a, b in zip(cu[:-1], cu[1:]):
+        for h in range(Hq):
+            kv = h // G
+            keys = np.logical_or.accumulate(k[a:b, kv].any(1))  # a key that row i sees is not finite
+            values = np.logical_or.accumulate(v[a:b, kv], 0)
+            weights = q[a:b, h].any(1) | keys  # the row's scores, its lse
+            out[a:b, h] = weights[:, None] | values
+            scores = weights | do[a:b, h].any(1) | values.any(1)  # the gradients of the row's scores
+            dq[a:b, h] = scores[:, None]
+            dk[a:b, kv] |= np.logical_or.accumulate(scores[::-1])[::-1][:, None]
+            dv[a:b, kv] |= np.logical_or.accumulate((weights[:, None] | do[a:b, h])[::-1], 0)[::-1]
+    return out, dq, dk, dv
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,H", [(4, 2), (3, 3)])
+@pytest.mark.parametrize("lens", [[300, 5, 400, 200], [900], [130, 640, 1, 129]])
+def test_values_that_are_not_finite_reach_what_the_formulas_say(lens, Hq, H, D):
+    """A value that is not finite in one tensor, at rows of every part of a tile, in a column: results that depend on it
+    are not finite, through however many tiles, and the others are bit for bit what they were."""
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    rng = np.random.default_rng(len(lens) + D)
+    T = sum(lens)
+    good = [t.contiguous() for t in make(torch, rng, T, Hq, H, D, fused=False)]
+    good.append(torch.from_numpy(rng.standard_normal((T, Hq, D)).astype(np.float32)).to(torch.bfloat16).cuda())
+    c = cu_of(torch, offsets(lens))
+
+    def run(x):
+        out, lse = gdn.attn_prompt(*x[:3], c)
+        return [out, *gdn.attn_prompt_bwd(*x[:3], out, lse, x[3], c)]
+
+    want = run(good)
+    for which, value in [(0, "nan"), (1, "nan"), (2, "nan"), (2, "inf"), (2, "-inf"), (3, "nan"), (3, "inf")]:
+        for rows in ([T // 2], [0], [T - 1], [127, 128], [31, 300], [5, T - 40]):
+            x, bad = [t.clone() for t in good], [np.zeros(tuple(t.shape), bool) for t in good]
+            for row in rows:
+                h, d = rng.integers(x[which].shape[1]), rng.integers(D)
+                x[which][row, h, d], bad[which][row, h, d] = float(value), True
+            note(f"bwd not finite {lens} Hq{Hq} H{H} D{D}: {which} {value} {rows}")
+            for name, got, clean, no in zip(("out", "dq", "dk", "dv"), run(x), want, reached(lens, bad, Hq, H)):
+                assert np.array_equal(~got.isfinite().cpu().numpy(), no), name
+                no = torch.from_numpy(no).cuda()
+                assert torch.equal(got.masked_fill(no, 0), clean.masked_fill(no, 0)), name
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[4096], [2050, 2046]])
+def test_a_step_that_diverged_is_no_slower_by_orders(lens, D):
+    """All of one tensor not finite: the forward and the gradients stay within ten times their usual time (rows that every
+    lane looked through by itself took 600 times as long)."""
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    T, c = sum(lens), cu_of(torch, offsets(lens))
+    good = [t.contiguous() for t in make(torch, np.random.default_rng(3), T, 8, 2, D, fused=False)]
+    good.append(torch.ones(T, 8, D, dtype=torch.bfloat16, device="cuda"))
+
+    def time(x):
+        best = []
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            out, lse = gdn.attn_prompt(*x[:3], c)
+            gdn.attn_prompt_bwd(*x[:3], out, lse, x[3], c)
+            b.record()
+            torch.cuda.synchronize()
+            best.append(a.elapsed_time(b))
+        return min(best)
+
+    usual = time(good)
+    for which in range(4):
+        x = list(good)
+        x[which] = torch.full_like(x[which], float("nan"))
+        note(f"bwd diverged {lens} D{D}: {which}")
+        took = time(x)
+        print("%.3f ms, usually %.3f" % (took, usual))
+        assert took <= 10 * usual
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("scale,size", [(0.0, 1.0), (-0.2, 1.0), (1.0, 2.0), (1e-3, 30.0)])
 def test_scales(D, scale, size):
