@@ -391,9 +391,14 @@ int gdn_block_tables(const int *seq_lens, const int *new_lens, int *block_table,
  *
  * For each (block, head) that new rows fall into, with a = max |x| over them
  * and M = 127 (int8) or 448 (e4m3):
- *     s = max(a / M, old scale if older rows stand before the new ones, 2^-100)
+ *     s = max(a (1 / M), old scale if older rows stand before the new ones, 2^-100)
  *     code = rne(x / s);   older codes = rne(code * old / s) if s grew.
- * x / s is the float32 product x * (1 / s); old / s is a float32 quotient.
+ * a (1 / M) is the float32 product with the float32 reciprocal, x / s the float32
+ * product x * (1 / s); old / s is a float32 quotient.
+ * A value of int8 is off by at most s / 2 when it is written, and by as much
+ * again, of the scale then, for each later call in which its block's scale grows:
+ * k growths leave at most (k + 1) s / 2, or s where each at least doubles it.  For
+ * e4m3 each of these roundings is 2^-4 of the value, or 2^-10 s if that is more.
  * Rows behind the new ones are left as they were.  A block whose first row is
  * new starts a scale of its own, whatever its scale was.  NaN is stored as
  * zero, infinities as the largest code of the largest bf16 value's scale.

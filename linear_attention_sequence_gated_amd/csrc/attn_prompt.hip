@@ -19,9 +19,10 @@
 //
 // What bounds it is the matrix and the vector unit together: 32 keys of a wave's
 // 32 rows are 4 D / 32 products of 32 cycles and 16 lanes' exponentials, with as
-// many multiply-adds, sums and maxima.  1 x 16384 x 16/4 x 64 takes 578 us, 950
-// TFLOP/s of the 1600 that the largest library products reach here; 8 x 2048 x
-// 12/4 x 64 70 us; 1 x 16384 x 16/4 x 128 1030 us, 1060 TFLOP/s.  Without the softmax the same
+// many multiply-adds, sums and maxima.  1 x 16384 x 16/4 x 64 takes 578 to 605 us, 910
+// to 950 TFLOP/s of the 1600 that the largest library products reach here; 8 x 2048 x
+// 12/4 x 64 71 to 79 us (a fifth of the CUs' time goes by waiting for the longest
+// tiles); 1 x 16384 x 16/4 x 128 1030 to 1130 us, 970 to 1060 TFLOP/s.  Without the softmax the same
 // loop reaches 1190, without the reads of LDS 1215.  Two tiles of rows to a wave,
 // the next scores beside the softmax, eight waves, orders set by hand and other
 // wave priorities were all slower or the same.

@@ -22,8 +22,10 @@
 // to 8 % of the time of forward and gradients).  dk has 2.4e-3 and dv 2.3e-3 with one.
 //
 // Bound by the matrix and the vector unit together, as the forward: 8 x 2048 x
-// 12 x 64 takes 125 us for dq and 151 for dk and dv, 2 x 4096 x 16/4 x 128
-// with the forward 735 us, 650 TFLOP/s.
+// 12 x 64 takes 125 us for dq and 149 for dk and dv, 2 x 4096 x 16/4 x 128
+// with the forward 735 to 775 us, 620 to 650 TFLOP/s.  Packed sequences of many
+// lengths are bound by the longest workgroups: of the time of dk and dv of 13
+// documents of up to 1201 rows x 16/4 x 128, 146 us, the CUs are busy 0.70.
 #include <algorithm>
 
 #include "../../include/gdn.h"
@@ -563,7 +565,7 @@ __device__ __forceinline__ void dkv_tile(f32x16 (&dk)[D / 32], f32x16 (&dv)[D / 
 // body, since two bodies of this size take more registers than there are (256
 // with one; a bit mask per score costs less than a spill, whose reload waits for
 // the loads that stage the next tile).  Two waves that share the work of 32 keys
-// and hand the scores over through LDS took 260 us where this takes 155 (13
+// and hand the scores over through LDS took 260 us where this takes 146 (13
 // documents of up to 1201 rows, 16/4 heads of 128).
 template <int D, int NW, int NR, bool VLDS> __global__ __launch_bounds__(64 * NW, 2) void attn_dkv_kernel(PromptBwdArgs a) {
   constexpr int BN = 32 * NW, NT = 64 * NW, KS = D / 16;

@@ -233,7 +233,7 @@ __global__ __launch_bounds__(kThreads) void block_tables_kernel(TablesArgs a) {
 
 // -------------------------------------------------------------- cache append
 // Codes of a block's rows for one head share one scale:
-//   s = max(s_old, max |x| / M),  code = rne(x / s),  M = 127 or 448,
+//   s = max(s_old, max |x| (1 / M)),  code = rne(x / s),  M = 127 or 448,
 // s_old only where the block holds older rows, whose codes are then moved to
 // the new scale, code = rne(code s_old / s).  The codes are the rounding of
 // 32-bit products (by the reciprocal and by the ratio).
@@ -246,7 +246,9 @@ __global__ __launch_bounds__(kThreads) void block_tables_kernel(TablesArgs a) {
 // one exchange through LDS.  Bound by HBM, 2 bytes read and 1 written per value:
 // 9869 tokens x 16 heads of 128, 121 MB, take 22.5 us, 5.4 TB/s; 256 single tokens
 // x 4 x 64 5.6 us, the chain of slot, scale and codes.  The rounding to 8 bits is
-// the operator itself: half a step of a code, s / 2 (int8) or 2^-4 (e4m3).
+// the operator itself: half a step of a code, s / 2 (int8) or 2^-4 (e4m3), when a row
+// is written, and again whenever its block's scale grows after that (k times: at most
+// (k + 1) s / 2; a block filled token by token can grow bt - 1 times).
 template <int FMT> constexpr float kMost = FMT == GDN_CACHE_I8 ? 127.f : 448.f;
 constexpr float kLeastScale = 7.88860905e-31f;   // 2^-100: a block of zeros keeps a finite reciprocal
 constexpr float kMostAbs = 3.38953139e38f;       // infinities count as the largest bf16 value
