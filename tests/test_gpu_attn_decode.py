@@ -208,6 +208,15 @@ def test_decode_strided_queries_scale_and_large_numbers():
         check(torch, q, kc, vc, ks, vs, table, lens, scale=0.3 / size, qdev=wide.cuda()[:, 6:])
 
 
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("scale", [0.0, -0.125, -0.4, 1e-30])
+def test_decode_scales_of_scores(scale, kind):
+    """Uniform weights, turned signs; a scale of nearly nothing."""
+    torch = torch_dev()
+    note(f"decode scale {scale} {kind}")
+    check(torch, *make(torch, np.random.default_rng(9), [1, 40, 0, 700, 2100], 4, 2, 64, 32, kind), scale=scale)
+
+
 def test_decode_blocks_of_zeros_beside_others():
     """A block of zeros has the smallest scale, 2^-100: its tokens still count in the denominator."""
     torch = torch_dev()
