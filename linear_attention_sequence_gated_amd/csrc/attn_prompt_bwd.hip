@@ -19,7 +19,8 @@
 // is taken in two parts, the rounded and what the rounding left (2^-16 of it):
 // with one, dq's relative error is 2.5e-3, half as much again as that of rounding
 // the result (1.7e-3), with two 1.9e-3, for a fourth product in place of three (4
-// to 8 % of the time of forward and gradients).  dk has 2.4e-3 and dv 2.3e-3 with one.
+// to 8 % of the time of forward and gradients).  dk has 2.4e-3 and dv 2.3e-3 with one:
+// two for both of them are six products for four, 15 to 26 % of the gradients' time.
 //
 // Bound by the matrix and the vector unit together, as the forward: 8 x 2048 x
 // 12 x 64 takes 125 us for dq and 149 for dk and dv, 2 x 4096 x 16/4 x 128
