@@ -481,6 +481,133 @@ int gdn_attn_prompt_bwd(const void *q, const void *k, const void *v, const void 
                         long long grad_v_stride, int T, int R, int Hq, int Hkv, int D, int dtype, int zero_rest,
                         void *workspace, size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * What stands around a recurrent layer's state update: the norm before its
+ * projections, the short convolution behind them, and a selective state space
+ * scan in the delta rule's place.
+ *
+ * Shared by the entry points below
+ *   - Rows are packed: T tokens, one after the other; the distance between rows
+ *     is an argument, in elements, at least the row's length and a multiple of 8,
+ *     so that parts of one fused projection can be passed as they are.  Outputs
+ *     without a stride are dense.
+ *   - Rows are bf16 or float32 (dtype), parameters of the same type or float32
+ *     (weight_dtype; float32 rows have float32 parameters).  All arithmetic is
+ *     float32; results are rounded once, to nearest even.
+ *   - cu_seqlens [R + 1] int32, ascending: sequence r is the rows cu_seqlens[r]
+ *     to cu_seqlens[r + 1] - 1.  Lengths of zero are fine.  The values are not
+ *     known to the call: what would lead outside the T rows is clamped.
+ *     Rows in no sequence are left as they were, or, where zero_rest is not 0,
+ *     set to zero; nothing that they hold reaches a result.
+ *   - Sums over rows (gradients of parameters) are made in a fixed order.
+ *   - What a call writes overlaps nothing that it reads, but for the states that
+ *     a step updates in place.
+ *   - Errors as for gdn_chunk_fwd.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition:
+ *
+ *     s = round(x + residual),   out = s weight / sqrt(mean(s^2) + eps)
+ *
+ *   x, residual [T] rows of C values, x_stride and residual_stride apart;
+ *              residual may be NULL: s is x
+ *   weight     [C]
+ *   out        [T, C] written;  sum [T, C] written: s (not without a residual)
+ *
+ * s is rounded to the rows' type before it is normalised: the norm is that of
+ * what the next block reads.  C is a multiple of 8 and at most 16384, T below
+ * 2^24; eps is finite and not negative.  Squares are summed in float32: rows
+ * whose squares add up past its range come out as zeros.
+ */
+int gdn_rms_norm(const void *x, const void *residual, const void *weight, void *out, void *sum, float eps,
+                 long long x_stride, long long residual_stride, int T, int C, int dtype, int weight_dtype,
+                 void *stream);
+
+/*
+ * The same with an output in 8 bits (format: the codes of a cache), for a
+ * product in 8 bits: a value is its code times its scale.
+ *
+ *   codes [T, C] written;  scale written: [T, C / 128] where block is 128 (C a
+ *   multiple of it), [T] where block is 0 (a scale to a row)
+ *
+ * With y the value that gdn_rms_norm would round, a = max |y| over a scale's
+ * values and M = 127 (int8) or 448 (e4m3):
+ *     scale = max(a (1 / M), 2^-100),   code = rne(y (1 / scale)).
+ * Where a value is infinite or NaN so is the scale, and the values that it stands
+ * for are NaN.
+ */
+int gdn_rms_norm_quant(const void *x, const void *residual, const void *weight, void *codes, float *scale,
+                       void *sum, float eps, long long x_stride, long long residual_stride, int T, int C,
+                       int block, int dtype, int weight_dtype, int format, void *stream);
+
+/*
+ * Gradients of gdn_rms_norm: of sum(out * grad_out) + sum(s * grad_sum).
+ *
+ *   sum        [T] rows, sum_stride apart: s as the forward wrote it (x without
+ *              a residual)
+ *   grad_out, grad_sum  [T] rows, their strides apart; grad_sum may be NULL
+ *   grad_x     [T, C] written: the gradient of x, and of the residual
+ *   grad_weight [C] written, of the weight's type
+ *
+ * Workspace: gdn_rms_norm_bwd_workspace_bytes (0 where T is 0), scratch on entry
+ * and exit, no clearing needed.
+ */
+size_t gdn_rms_norm_bwd_workspace_bytes(int T, int C, int dtype);
+int gdn_rms_norm_bwd(const void *sum, const void *weight, const void *grad_out, const void *grad_sum,
+                     void *grad_x, void *grad_weight, float eps, long long sum_stride, long long grad_out_stride,
+                     long long grad_sum_stride, int T, int C, int dtype, int weight_dtype, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * Depthwise causal convolution over packed sequences: with z the rows of a
+ * sequence behind the W - 1 rows of its state,
+ *
+ *     p_t = bias + sum_j weight[:, j] z_{t + j},   out_t = p_t sigmoid(p_t), or p_t without silu
+ *
+ * so that tap W - 1 meets row t and tap 0 the row W - 1 before it.
+ *
+ *   x          [T] rows of C values, x_stride apart
+ *   weight     [C, W], W from 2 to 4;  bias [C], may be NULL
+ *   state      [R, W - 1, C] of the rows' type: the rows before each sequence,
+ *              the latest last; may be NULL (zeros)
+ *   out        [T, C] written
+ *   state_final [R, W - 1, C] written: the last rows of z; may be NULL
+ *
+ * C is a multiple of 8 and at most 65536, T C below 2^34, R below 2^20, R C below
+ * 2^31.
+ */
+int gdn_short_conv(const void *x, const void *weight, const void *bias, const int *cu_seqlens, const void *state,
+                   void *out, void *state_final, long long x_stride, int T, int R, int C, int W, int dtype,
+                   int weight_dtype, int silu, int zero_rest, void *stream);
+
+/*
+ * Its gradients: of sum(out * grad_out) + sum(state_final * grad_state_final).
+ *
+ *   grad_out   [T] rows, grad_out_stride apart;  grad_state_final [R, W - 1, C],
+ *              may be NULL
+ *   grad_x [T, C], grad_weight [C, W], grad_bias [C], grad_state [R, W - 1, C]
+ *              written, each of the type of what it is the gradient of; the last
+ *              two may be NULL
+ *
+ * Workspace: gdn_short_conv_bwd_workspace_bytes (0 where T is 0), scratch on
+ * entry and exit, no clearing needed.
+ */
+size_t gdn_short_conv_bwd_workspace_bytes(int T, int C, int W);
+int gdn_short_conv_bwd(const void *x, const void *weight, const void *bias, const void *grad_out,
+                       const int *cu_seqlens, const void *state, const void *grad_state_final, void *grad_x,
+                       void *grad_weight, void *grad_bias, void *grad_state, long long x_stride,
+                       long long grad_out_stride, int T, int R, int C, int W, int dtype, int weight_dtype, int silu,
+                       int zero_rest, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One new row for each of R sequences: out [R, C] from x (R rows) and the state
+ * [R, W - 1, C], which is moved on in place.
+ */
+int gdn_short_conv_step(const void *x, const void *weight, const void *bias, void *state, void *out,
+                        long long x_stride, int R, int C, int W, int dtype, int weight_dtype, int silu,
+                        void *stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *gdn_status_str(int status);
 

@@ -1,0 +1,235 @@
+"""Torch helpers of what stands around a recurrent layer's state update (include/gdn.h): the root-mean-square norm with
+the residual's addition, also with an output in 8 bits, and the short causal convolution.
+
+They check dtypes, shapes, strides and devices, allocate what is not passed in, pass ``data_ptr()`` and the current
+HIP stream of the tensors' device (or ``stream``), and raise on a non-OK status.  Rows are [tokens, channels] with the
+channels of a row side by side; the distance between rows is free, so that x can be a part of one fused projection.
+"""
+from __future__ import annotations
+
+import functools
+
+import torch
+
+from . import gdn as raw
+from .attn import _FORMATS, _I32, _call, _dense, _device, _on_stream
+
+_CODES = {torch.bfloat16: raw.GDN_BF16, torch.float32: raw.GDN_F32}
+
+
+def _types(x, weight, who):
+    """The codes of the rows' and the parameters' types."""
+    code, wcode = _CODES.get(x.dtype), _CODES.get(weight.dtype)
+    if code is None:
+        raise TypeError(f"{who}: unsupported dtype {x.dtype}; use bfloat16 or float32")
+    if wcode is None or (code == raw.GDN_F32 and wcode != code):
+        raise TypeError(f"{who}: parameters must have the rows' dtype or float32, got {weight.dtype}")
+    return code, wcode
+
+
+def _rows(t, name, shape, dtype, dev):
+    """Distance between the rows of t [tokens, channels], whose rows are dense."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev.index:
+        raw._check(t.contiguous(), name, shape, dtype, dev)
+    row, one = t.stride()
+    if shape[0] and shape[1] > 1 and one != 1:
+        raise ValueError(f"{name}: the channels of a row must be contiguous")
+    if shape[0] <= 1:
+        return -(-shape[1] // 8) * 8
+    if row < shape[1] or row % 8:
+        raise ValueError(f"{name}: rows must be a multiple of 8 elements apart and not overlap")
+    return row
+
+
+def _given(t, name, shape, dtype, dev):
+    """The address of an optional dense tensor."""
+    if t is None:
+        return None
+    _dense(t, name, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _norm_inputs(x, weight, residual, who):
+    dev = _device(x, who)
+    t, c = x.shape
+    code, wcode = _types(x, weight, who)
+    xs = _rows(x, "x", (t, c), x.dtype, dev)
+    _dense(weight, "weight", (c,), weight.dtype, dev)
+    rs = 0 if residual is None else _rows(residual, "residual", (t, c), x.dtype, dev)
+    return dev, t, c, code, wcode, xs, rs
+
+
+def _sum_of(x, residual, out):
+    """Where the sum goes: x itself without a residual."""
+    if residual is None:
+        if out is not None:
+            raise ValueError("sum_out: there is no sum without a residual")
+        return x, None
+    t, c = x.shape
+    if out is None:
+        out = x.new_empty((t, c))
+    else:
+        _dense(out, "sum_out", (t, c), x.dtype, x.device)
+    return out, out.data_ptr()
+
+
+@_on_stream
+def rms_norm(x, weight, residual=None, eps: float = 1e-6, out=None, sum_out=None):
+    """Root-mean-square norm of the rows s = x + residual: s weight / sqrt(mean(s^2) + eps).
+
+    x, residual [T, C] bfloat16 or float32, C a multiple of 8; weight [C] of that dtype or float32.  Returns (out [T, C],
+    s [T, C], rounded to x's dtype before it is normalised; x itself without a residual).
+    """
+    dev, t, c, code, wcode, xs, rs = _norm_inputs(x, weight, residual, "rms_norm")
+    if out is None:
+        out = x.new_empty((t, c))
+    else:
+        _dense(out, "out", (t, c), x.dtype, dev)
+    total, to = _sum_of(x, residual, sum_out)
+    _call(dev, raw.load().gdn_rms_norm, x.data_ptr(), raw._ptr(residual), weight.data_ptr(), out.data_ptr(), to, eps, xs, rs,
+          t, c, code, wcode)
+    return out, total
+
+
+@_on_stream
+def rms_norm_quant(x, weight, residual=None, eps: float = 1e-6, dtype=torch.float8_e4m3fn, block: int = 128, codes=None,
+                   scale=None, sum_out=None):
+    """rms_norm with an output in 8 bits, for a product in 8 bits: codes [T, C] of dtype (int8 or float8_e4m3fn), and a
+    float32 scale for each block of 128 columns [T, C / 128] or, with block = 0, for each row [T, 1].
+
+    Returns (codes, scale, s): a value is its code times its scale.
+    """
+    dev, t, c, code, wcode, xs, rs = _norm_inputs(x, weight, residual, "rms_norm_quant")
+    fmt = _FORMATS.get(dtype)
+    if fmt is None:
+        raise TypeError(f"unsupported dtype {dtype} of the codes; use int8 or float8_e4m3fn")
+    if block not in (0, 128) or block and c % block:
+        raise ValueError("block: 128 columns, of which a row is a multiple, or 0 for a scale to a row")
+    if codes is None:
+        codes = x.new_empty((t, c), dtype=dtype)
+    else:
+        _dense(codes, "codes", (t, c), dtype, dev)
+    shape = (t, c // block if block else 1)
+    if scale is None:
+        scale = x.new_empty(shape, dtype=torch.float32)
+    else:
+        _dense(scale, "scale", shape, torch.float32, dev)
+    total, to = _sum_of(x, residual, sum_out)
+    _call(dev, raw.load().gdn_rms_norm_quant, x.data_ptr(), raw._ptr(residual), weight.data_ptr(), codes.data_ptr(),
+          scale.data_ptr(), to, eps, xs, rs, t, c, block, code, wcode, fmt)
+    return codes, scale, total
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace(*sizes):
+    return raw.gdn_rms_norm_bwd_workspace_bytes(*sizes)
+
+
+@_on_stream
+def rms_norm_bwd(sum, weight, grad_out, eps: float = 1e-6, grad_sum=None):
+    """Gradients of sum(out * grad_out) + sum(s * grad_sum) for rms_norm's forward, from the s that it returned.
+
+    Returns (grad_x [T, C], which is the residual's gradient too, grad_weight [C] of the weight's dtype).  The workspace
+    is allocated here with torch.
+    """
+    dev = _device(sum, "rms_norm_bwd")
+    t, c = sum.shape
+    code, wcode = _types(sum, weight, "rms_norm_bwd")
+    ss = _rows(sum, "sum", (t, c), sum.dtype, dev)
+    _dense(weight, "weight", (c,), weight.dtype, dev)
+    gs = _rows(grad_out, "grad_out", (t, c), sum.dtype, dev)
+    gss = 0 if grad_sum is None else _rows(grad_sum, "grad_sum", (t, c), sum.dtype, dev)
+    grad_x, grad_weight = sum.new_empty((t, c)), torch.empty_like(weight)
+    size = _norm_workspace(t, c, code)
+    ws = weight.new_empty(size // 4, dtype=torch.float32)
+    _call(dev, raw.load().gdn_rms_norm_bwd, sum.data_ptr(), weight.data_ptr(), grad_out.data_ptr(), raw._ptr(grad_sum),
+          grad_x.data_ptr(), grad_weight.data_ptr(), eps, ss, gs, gss, t, c, code, wcode, ws.data_ptr(), size)
+    return grad_x, grad_weight
+
+
+def _conv_inputs(x, weight, bias, who):
+    dev = _device(x, who)
+    t, c = x.shape
+    code, wcode = _types(x, weight, who)
+    if weight.dim() != 2:
+        raise ValueError("weight: expected [channels, taps]")
+    w = weight.shape[1]
+    xs = _rows(x, "x", (t, c), x.dtype, dev)
+    _dense(weight, "weight", (c, w), weight.dtype, dev)
+    return dev, t, c, w, code, wcode, xs, _given(bias, "bias", (c,), weight.dtype, dev)
+
+
+def _sequences(cu_seqlens, dev):
+    _dense(cu_seqlens, "cu_seqlens", (cu_seqlens.numel(),), _I32, dev)
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens: needs at least one entry")
+    return cu_seqlens.numel() - 1
+
+
+@_on_stream
+def short_conv(x, weight, cu_seqlens, bias=None, state=None, silu: bool = True, out=None, state_final=None):
+    """Depthwise causal convolution over packed sequences, with SiLU: x [T, C] bfloat16 or float32, weight [C, W] with W
+    from 2 to 4 (the last tap meets the row itself) and bias [C] of x's dtype or float32, cu_seqlens [R + 1] int32 the
+    offsets of the sequences, state [R, W - 1, C] the rows before each (zeros unless given).
+
+    Returns (out [T, C], state_final [R, W - 1, C]).  Rows in no sequence are not written; an out that is allocated here
+    holds zeros there.
+    """
+    dev, t, c, w, code, wcode, xs, bp = _conv_inputs(x, weight, bias, "short_conv")
+    r = _sequences(cu_seqlens, dev)
+    sp = _given(state, "state", (r, w - 1, c), x.dtype, dev)
+    zero_rest = out is None
+    if out is None:
+        out = x.new_empty((t, c))
+    else:
+        _dense(out, "out", (t, c), x.dtype, dev)
+    if state_final is None:
+        state_final = x.new_empty((r, w - 1, c))
+    else:
+        _dense(state_final, "state_final", (r, w - 1, c), x.dtype, dev)
+    _call(dev, raw.load().gdn_short_conv, x.data_ptr(), weight.data_ptr(), bp, cu_seqlens.data_ptr(), sp, out.data_ptr(),
+          state_final.data_ptr(), xs, t, r, c, w, code, wcode, silu, zero_rest)
+    return out, state_final
+
+
+@functools.lru_cache(maxsize=1024)
+def _conv_workspace(*sizes):
+    return raw.gdn_short_conv_bwd_workspace_bytes(*sizes)
+
+
+@_on_stream
+def short_conv_bwd(x, weight, grad_out, cu_seqlens, bias=None, state=None, silu: bool = True, grad_state_final=None):
+    """Gradients of sum(out * grad_out) + sum(state_final * grad_state_final) for short_conv's forward.
+
+    Returns (grad_x [T, C], zeros in rows of no sequence; grad_weight [C, W]; grad_bias [C] or None without a bias;
+    grad_state [R, W - 1, C] or None without a state), each of the dtype of what it is the gradient of.  The workspace is
+    allocated here with torch.
+    """
+    dev, t, c, w, code, wcode, xs, bp = _conv_inputs(x, weight, bias, "short_conv_bwd")
+    r = _sequences(cu_seqlens, dev)
+    gs = _rows(grad_out, "grad_out", (t, c), x.dtype, dev)
+    sp = _given(state, "state", (r, w - 1, c), x.dtype, dev)
+    gsp = _given(grad_state_final, "grad_state_final", (r, w - 1, c), x.dtype, dev)
+    grad_x, grad_weight = x.new_empty((t, c)), torch.empty_like(weight)
+    grad_bias = None if bias is None else torch.empty_like(bias)
+    grad_state = None if state is None else torch.empty_like(state)
+    size = _conv_workspace(t, c, w)
+    ws = x.new_empty(size // 4, dtype=torch.float32)
+    _call(dev, raw.load().gdn_short_conv_bwd, x.data_ptr(), weight.data_ptr(), bp, grad_out.data_ptr(),
+          cu_seqlens.data_ptr(), sp, gsp, grad_x.data_ptr(), grad_weight.data_ptr(), raw._ptr(grad_bias),
+          raw._ptr(grad_state), xs, gs, t, r, c, w, code, wcode, silu, True, ws.data_ptr(), size)
+    return grad_x, grad_weight, grad_bias, grad_state
+
+
+@_on_stream
+def short_conv_step(x, weight, state, bias=None, silu: bool = True, out=None):
+    """One new row x [R, C] for each of R sequences: returns out [R, C] and moves state [R, W - 1, C] on in place."""
+    dev, r, c, w, code, wcode, xs, bp = _conv_inputs(x, weight, bias, "short_conv_step")
+    _dense(state, "state", (r, w - 1, c), x.dtype, dev)
+    if out is None:
+        out = x.new_empty((r, c))
+    else:
+        _dense(out, "out", (r, c), x.dtype, dev)
+    _call(dev, raw.load().gdn_short_conv_step, x.data_ptr(), weight.data_ptr(), bp, state.data_ptr(), out.data_ptr(), xs, r,
+          c, w, code, wcode, silu)
+    return out

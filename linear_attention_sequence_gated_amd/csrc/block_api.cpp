@@ -1,0 +1,152 @@
+// block_api.cpp -- the C ABI of what stands around a recurrent layer's state
+// update (declared in include/gdn.h): validates every argument before anything is
+// enqueued, then launches.
+#include <stdint.h>
+
+#include <cmath>
+
+#include "../../include/gdn.h"
+#include "gdn_block.hpp"
+
+namespace {
+
+template <int N> bool all_aligned(const void* const (&ptrs)[N]) {
+  for (const void* p : ptrs)
+    if (p && (reinterpret_cast<uintptr_t>(p) & 15u)) return false;
+  return true;
+}
+
+int status(hipError_t e) { return e == hipSuccess ? GDN_OK : GDN_ERR_HIP; }
+
+bool known_dtype(int d) { return d == GDN_F32 || d == GDN_BF16 || d == GDN_C64; }
+
+// Types of rows and of parameters: bf16 or float32; float32 rows have float32
+// parameters.
+int types(int dtype, int param_dtype) {
+  if (!known_dtype(dtype) || !known_dtype(param_dtype)) return GDN_ERR_DTYPE;
+  if (dtype == GDN_C64 || param_dtype == GDN_C64 || (dtype == GDN_F32 && param_dtype != GDN_F32)) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+// A row stride: room for the row, 16-byte aligned rows, no offset past 2^62.
+bool stride_ok(long long s, long long row) { return s >= row && s % 8 == 0 && s < (1LL << 32); }
+
+// Rows of a norm: their pieces fit a workgroup's registers.
+int norm_shape(int T, int C, int dtype) {
+  if (T < 0 || C <= 0 || T >= (1 << 24)) return GDN_ERR_SHAPE;
+  return C % 8 == 0 && C <= 16384 && dtype != GDN_C64 ? GDN_OK : GDN_ERR_UNSUPPORTED;
+}
+
+// Sizes of a convolution, which keep its launches under 2^32 work-items.
+int conv_shape(int T, int R, int C, int W) {
+  if (T < 0 || R < 0 || C <= 0 || W <= 0 || R >= (1 << 20) || T >= (1 << 28)) return GDN_ERR_SHAPE;
+  if ((long long)T * C >= (1LL << 34) || (long long)R * C >= (1LL << 31)) return GDN_ERR_SHAPE;
+  return C % 8 == 0 && C <= 65536 && W >= 2 && W <= 4 ? GDN_OK : GDN_ERR_UNSUPPORTED;
+}
+
+int norm(const void* x, const void* residual, const void* weight, void* out, void* sum, float* scale, float eps,
+         long long xs, long long rs, int T, int C, int fmt, int block, int dtype, int weight_dtype, void* stream) {
+  if (const int s = types(dtype, weight_dtype)) return s;
+  if (const int s = norm_shape(T, C, dtype)) return s;
+  if (!std::isfinite(eps) || eps < 0.f || !stride_ok(xs, C) || (residual && !stride_ok(rs, C))) return GDN_ERR_SHAPE;
+  if (T == 0) return GDN_OK;
+  if (!x || !weight || !out || (residual && !sum) || (fmt >= 0 && !scale)) return GDN_ERR_NULL;
+  const void* ptrs[] = {x, residual, weight, out, sum, scale};
+  if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
+  return status(gdn::launch_rms_norm({x, residual, weight, out, sum, scale, xs, rs, eps, T, C, dtype == GDN_F32,
+                                      weight_dtype == GDN_F32, fmt, block, stream}));
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdn_rms_norm(const void* x, const void* residual, const void* weight, void* out, void* sum, float eps,
+                 long long x_stride, long long residual_stride, int T, int C, int dtype, int weight_dtype, void* stream) {
+  return norm(x, residual, weight, out, sum, nullptr, eps, x_stride, residual_stride, T, C, -1, 0, dtype, weight_dtype, stream);
+}
+
+int gdn_rms_norm_quant(const void* x, const void* residual, const void* weight, void* codes, float* scale, void* sum,
+                       float eps, long long x_stride, long long residual_stride, int T, int C, int block, int dtype,
+                       int weight_dtype, int format, void* stream) {
+  if (format != GDN_CACHE_I8 && format != GDN_CACHE_E4M3) return GDN_ERR_DTYPE;
+  if (block < 0) return GDN_ERR_SHAPE;
+  if (block != 0 && (block != 128 || C % 128)) return GDN_ERR_UNSUPPORTED;
+  return norm(x, residual, weight, codes, sum, scale, eps, x_stride, residual_stride, T, C, format, block, dtype, weight_dtype,
+              stream);
+}
+
+size_t gdn_rms_norm_bwd_workspace_bytes(int T, int C, int dtype) {
+  return types(dtype, GDN_F32) || norm_shape(T, C, dtype) ? 0 : gdn::rms_norm_bwd_workspace_bytes(T, C, dtype == GDN_F32);
+}
+
+int gdn_rms_norm_bwd(const void* sum, const void* weight, const void* grad_out, const void* grad_sum, void* grad_x,
+                     void* grad_weight, float eps, long long sum_stride, long long grad_out_stride,
+                     long long grad_sum_stride, int T, int C, int dtype, int weight_dtype, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (const int s = types(dtype, weight_dtype)) return s;
+  if (const int s = norm_shape(T, C, dtype)) return s;
+  if (!std::isfinite(eps) || eps < 0.f || !stride_ok(sum_stride, C) || !stride_ok(grad_out_stride, C)) return GDN_ERR_SHAPE;
+  if (grad_sum && !stride_ok(grad_sum_stride, C)) return GDN_ERR_SHAPE;
+  if (!weight || !grad_weight || (T && (!sum || !grad_out || !grad_x))) return GDN_ERR_NULL;
+  const void* ptrs[] = {sum, weight, grad_out, grad_sum, grad_x, grad_weight, workspace};
+  if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
+  const size_t need = gdn::rms_norm_bwd_workspace_bytes(T, C, dtype == GDN_F32);
+  if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+  return status(gdn::launch_rms_norm_bwd({sum, weight, grad_out, grad_sum, grad_x, grad_weight, static_cast<float*>(workspace),
+                                          sum_stride, grad_out_stride, grad_sum_stride, eps, T, C, dtype == GDN_F32,
+                                          weight_dtype == GDN_F32, stream}));
+}
+
+int gdn_short_conv(const void* x, const void* weight, const void* bias, const int* cu_seqlens, const void* state, void* out,
+                   void* state_final, long long x_stride, int T, int R, int C, int W, int dtype, int weight_dtype,
+                   int silu, int zero_rest, void* stream) {
+  if (const int s = types(dtype, weight_dtype)) return s;
+  if (const int s = conv_shape(T, R, C, W)) return s;
+  if (!stride_ok(x_stride, C)) return GDN_ERR_SHAPE;
+  if (T == 0 && (R == 0 || !state_final)) return GDN_OK;
+  if (!weight || !cu_seqlens || (T && (!x || !out))) return GDN_ERR_NULL;
+  const void* ptrs[] = {x, weight, bias, cu_seqlens, state, out, state_final};
+  if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
+  return status(gdn::launch_short_conv({x, weight, bias, cu_seqlens, state, out, state_final, x_stride, T, R, C, W,
+                                        dtype == GDN_F32, weight_dtype == GDN_F32, silu != 0, zero_rest != 0, stream}));
+}
+
+size_t gdn_short_conv_bwd_workspace_bytes(int T, int C, int W) {
+  return conv_shape(T, 0, C, W) ? 0 : gdn::short_conv_bwd_workspace_bytes(T, C, W);
+}
+
+int gdn_short_conv_bwd(const void* x, const void* weight, const void* bias, const void* grad_out, const int* cu_seqlens,
+                       const void* state, const void* grad_state_final, void* grad_x, void* grad_weight, void* grad_bias,
+                       void* grad_state, long long x_stride, long long grad_out_stride, int T, int R, int C, int W,
+                       int dtype, int weight_dtype, int silu, int zero_rest, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  if (const int s = types(dtype, weight_dtype)) return s;
+  if (const int s = conv_shape(T, R, C, W)) return s;
+  if (!stride_ok(x_stride, C) || !stride_ok(grad_out_stride, C)) return GDN_ERR_SHAPE;
+  if (!weight || !cu_seqlens || !grad_weight || (T && (!x || !grad_out || !grad_x))) return GDN_ERR_NULL;
+  const void* ptrs[] = {x, weight, bias, grad_out, cu_seqlens, state, grad_state_final, grad_x, grad_weight, grad_bias, grad_state,
+                        workspace};
+  if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
+  const size_t need = gdn::short_conv_bwd_workspace_bytes(T, C, W);
+  if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+  return status(gdn::launch_short_conv_bwd({x, weight, bias, grad_out, cu_seqlens, state, grad_state_final, grad_x, grad_weight,
+                                            grad_bias, grad_state, static_cast<float*>(workspace), x_stride, grad_out_stride,
+                                            T, R, C, W, dtype == GDN_F32, weight_dtype == GDN_F32, silu != 0, zero_rest != 0,
+                                            stream}));
+}
+
+int gdn_short_conv_step(const void* x, const void* weight, const void* bias, void* state, void* out, long long x_stride,
+                        int R, int C, int W, int dtype, int weight_dtype, int silu, void* stream) {
+  if (const int s = types(dtype, weight_dtype)) return s;
+  if (const int s = conv_shape(R, R, C, W)) return s;
+  if (!stride_ok(x_stride, C)) return GDN_ERR_SHAPE;
+  if (R == 0) return GDN_OK;
+  if (!x || !weight || !state || !out) return GDN_ERR_NULL;
+  const void* ptrs[] = {x, weight, bias, state, out};
+  if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
+  return status(gdn::launch_short_conv_step({x, weight, bias, state, out, x_stride, R, C, W, dtype == GDN_F32,
+                                             weight_dtype == GDN_F32, silu != 0, stream}));
+}
+
+}  // extern "C"

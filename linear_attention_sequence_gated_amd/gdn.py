@@ -28,7 +28,9 @@ EXPORTS = ("gdn_chunk_fwd_workspace_bytes", "gdn_chunk_fwd", "gdn_chunk_fwd_prol
            "gdn_chunk_fwd_prologue", "gdn_chunk_bwd_workspace_bytes",
            "gdn_chunk_bwd", "gdn_fwd_channel_decay", "gdn_recurrent_step", "gdn_status_str", "gdn_chunk_fwd_noalloc",
            "gdn_block_tables", "gdn_cache_append", "gdn_attn_decode_workspace_bytes", "gdn_attn_decode",
-           "gdn_attn_prompt", "gdn_attn_prompt_bwd_workspace_bytes", "gdn_attn_prompt_bwd")
+           "gdn_attn_prompt", "gdn_attn_prompt_bwd_workspace_bytes", "gdn_attn_prompt_bwd",
+           "gdn_rms_norm", "gdn_rms_norm_quant", "gdn_rms_norm_bwd_workspace_bytes", "gdn_rms_norm_bwd", "gdn_short_conv",
+           "gdn_short_conv_bwd_workspace_bytes", "gdn_short_conv_bwd", "gdn_short_conv_step")
 
 _lib = None
 
@@ -82,6 +84,22 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.gdn_attn_prompt_bwd_workspace_bytes.restype = sz
     lib.gdn_attn_prompt_bwd.argtypes = [vp] * 10 + [fl] + [ll] * 7 + [ci] * 7 + [vp, sz, vp]
     lib.gdn_attn_prompt_bwd.restype = ci
+    lib.gdn_rms_norm.argtypes = [vp] * 5 + [fl] + [ll] * 2 + [ci] * 4 + [vp]
+    lib.gdn_rms_norm.restype = ci
+    lib.gdn_rms_norm_quant.argtypes = [vp] * 6 + [fl] + [ll] * 2 + [ci] * 6 + [vp]
+    lib.gdn_rms_norm_quant.restype = ci
+    lib.gdn_rms_norm_bwd_workspace_bytes.argtypes = [ci] * 3
+    lib.gdn_rms_norm_bwd_workspace_bytes.restype = sz
+    lib.gdn_rms_norm_bwd.argtypes = [vp] * 6 + [fl] + [ll] * 3 + [ci] * 4 + [vp, sz, vp]
+    lib.gdn_rms_norm_bwd.restype = ci
+    lib.gdn_short_conv.argtypes = [vp] * 7 + [ll] + [ci] * 8 + [vp]
+    lib.gdn_short_conv.restype = ci
+    lib.gdn_short_conv_bwd_workspace_bytes.argtypes = [ci] * 3
+    lib.gdn_short_conv_bwd_workspace_bytes.restype = sz
+    lib.gdn_short_conv_bwd.argtypes = [vp] * 11 + [ll] * 2 + [ci] * 8 + [vp, sz, vp]
+    lib.gdn_short_conv_bwd.restype = ci
+    lib.gdn_short_conv_step.argtypes = [vp] * 5 + [ll] + [ci] * 6 + [vp]
+    lib.gdn_short_conv_step.restype = ci
     lib.gdn_status_str.argtypes = [ci]
     lib.gdn_status_str.restype = ctypes.c_char_p
     if path is None:
@@ -179,6 +197,50 @@ def gdn_attn_prompt_bwd(q, k, v, out, lse, grad_out, cu_seqlens, grad_q, grad_k,
                                           q_stride, k_stride, v_stride, grad_out_stride, grad_q_stride, grad_k_stride,
                                           grad_v_stride, T, R, Hq, Hkv, D, dtype, zero_rest, workspace,
                                           workspace_bytes, stream))
+
+
+def gdn_rms_norm(x, residual, weight, out, sum, eps, x_stride, residual_stride, T, C, dtype, weight_dtype, stream) -> int:
+    return int(load().gdn_rms_norm(x, residual, weight, out, sum, eps, x_stride, residual_stride, T, C, dtype,
+                                   weight_dtype, stream))
+
+
+def gdn_rms_norm_quant(x, residual, weight, codes, scale, sum, eps, x_stride, residual_stride, T, C, block, dtype,
+                       weight_dtype, format, stream) -> int:
+    return int(load().gdn_rms_norm_quant(x, residual, weight, codes, scale, sum, eps, x_stride, residual_stride, T, C,
+                                         block, dtype, weight_dtype, format, stream))
+
+
+def gdn_rms_norm_bwd_workspace_bytes(T, C, dtype) -> int:
+    return int(load().gdn_rms_norm_bwd_workspace_bytes(T, C, dtype))
+
+
+def gdn_rms_norm_bwd(sum, weight, grad_out, grad_sum, grad_x, grad_weight, eps, sum_stride, grad_out_stride,
+                     grad_sum_stride, T, C, dtype, weight_dtype, workspace, workspace_bytes, stream) -> int:
+    return int(load().gdn_rms_norm_bwd(sum, weight, grad_out, grad_sum, grad_x, grad_weight, eps, sum_stride,
+                                       grad_out_stride, grad_sum_stride, T, C, dtype, weight_dtype, workspace,
+                                       workspace_bytes, stream))
+
+
+def gdn_short_conv(x, weight, bias, cu_seqlens, state, out, state_final, x_stride, T, R, C, W, dtype, weight_dtype, silu,
+                   zero_rest, stream) -> int:
+    return int(load().gdn_short_conv(x, weight, bias, cu_seqlens, state, out, state_final, x_stride, T, R, C, W, dtype,
+                                     weight_dtype, silu, zero_rest, stream))
+
+
+def gdn_short_conv_bwd_workspace_bytes(T, C, W) -> int:
+    return int(load().gdn_short_conv_bwd_workspace_bytes(T, C, W))
+
+
+def gdn_short_conv_bwd(x, weight, bias, grad_out, cu_seqlens, state, grad_state_final, grad_x, grad_weight, grad_bias,
+                       grad_state, x_stride, grad_out_stride, T, R, C, W, dtype, weight_dtype, silu, zero_rest, workspace,
+                       workspace_bytes, stream) -> int:
+    return int(load().gdn_short_conv_bwd(x, weight, bias, grad_out, cu_seqlens, state, grad_state_final, grad_x,
+                                         grad_weight, grad_bias, grad_state, x_stride, grad_out_stride, T, R, C, W, dtype,
+                                         weight_dtype, silu, zero_rest, workspace, workspace_bytes, stream))
+
+
+def gdn_short_conv_step(x, weight, bias, state, out, x_stride, R, C, W, dtype, weight_dtype, silu, stream) -> int:
+    return int(load().gdn_short_conv_step(x, weight, bias, state, out, x_stride, R, C, W, dtype, weight_dtype, silu, stream))
 
 
 # ------------------------------------------------------------- torch helpers

@@ -1,0 +1,170 @@
+"""Refusals of the norm's and the short convolution's entry points, on the CPU: no call here reaches a kernel (each fails
+validation or has nothing to do)."""
+import pytest
+
+import linear_attention_sequence_gated_amd as gdn
+from linear_attention_sequence_gated_amd import gdn as raw
+
+A = 0x10000  # a 16-byte aligned fake address; validation rejects before any use
+NAN = float("nan")
+
+
+def each(names, value, status):
+    return [(dict([(n, value)]), status) for n in names]
+
+
+TYPES = [(dict(dtype=7), raw.GDN_ERR_DTYPE), (dict(weight_dtype=-1), raw.GDN_ERR_DTYPE),
+         (dict(dtype=raw.GDN_C64), raw.GDN_ERR_UNSUPPORTED), (dict(weight_dtype=raw.GDN_C64), raw.GDN_ERR_UNSUPPORTED),
+         (dict(dtype=raw.GDN_F32, weight_dtype=raw.GDN_BF16), raw.GDN_ERR_UNSUPPORTED)]
+NORM = TYPES + [(dict(T=-1), raw.GDN_ERR_SHAPE), (dict(T=1 << 24), raw.GDN_ERR_SHAPE), (dict(C=0), raw.GDN_ERR_SHAPE),
+                (dict(eps=NAN), raw.GDN_ERR_SHAPE), (dict(eps=-1e-6), raw.GDN_ERR_SHAPE), (dict(eps=float("inf")), raw.GDN_ERR_SHAPE)]
+
+
+def norm(**kw):
+    args = dict(x=A, residual=A, weight=A, out=A, sum=A, eps=1e-6, x_stride=256, residual_stride=256, T=4, C=256,
+                dtype=raw.GDN_BF16, weight_dtype=raw.GDN_BF16, stream=None)
+    args.update(kw)
+    return gdn.gdn_rms_norm(**args)
+
+
+@pytest.mark.parametrize("kw,status", NORM + [
+    (dict(C=252, x_stride=256), raw.GDN_ERR_UNSUPPORTED), (dict(C=16392, x_stride=16392, residual_stride=16392), raw.GDN_ERR_UNSUPPORTED),
+    (dict(x_stride=248), raw.GDN_ERR_SHAPE), (dict(x_stride=260), raw.GDN_ERR_SHAPE), (dict(residual_stride=248), raw.GDN_ERR_SHAPE),
+    (dict(x_stride=1 << 32), raw.GDN_ERR_SHAPE),
+    *each(("x", "weight", "out", "sum"), None, raw.GDN_ERR_NULL),
+    *each(("x", "residual", "weight", "out", "sum"), A + 8, raw.GDN_ERR_ALIGN)])
+def test_norm_argument_errors(kw, status):
+    assert norm(**kw) == status
+
+
+def test_norm_of_nothing_is_noop():
+    assert norm(T=0, x=None, residual=None, weight=None, out=None, sum=None) == raw.GDN_OK
+
+
+def quant(**kw):
+    args = dict(x=A, residual=A, weight=A, codes=A, scale=A, sum=A, eps=1e-6, x_stride=256, residual_stride=256, T=4,
+                C=256, block=128, dtype=raw.GDN_BF16, weight_dtype=raw.GDN_BF16, format=raw.GDN_CACHE_E4M3, stream=None)
+    args.update(kw)
+    return gdn.gdn_rms_norm_quant(**args)
+
+
+@pytest.mark.parametrize("kw,status", NORM + [
+    (dict(format=2), raw.GDN_ERR_DTYPE), (dict(format=-1), raw.GDN_ERR_DTYPE), (dict(block=-1), raw.GDN_ERR_SHAPE),
+    (dict(block=64), raw.GDN_ERR_UNSUPPORTED), (dict(C=192), raw.GDN_ERR_UNSUPPORTED),
+    *each(("x", "weight", "codes", "scale", "sum"), None, raw.GDN_ERR_NULL),
+    *each(("x", "residual", "weight", "codes", "scale", "sum"), A + 4, raw.GDN_ERR_ALIGN)])
+def test_quant_argument_errors(kw, status):
+    assert quant(**kw) == status
+
+
+def norm_bwd(**kw):
+    args = dict(sum=A, weight=A, grad_out=A, grad_sum=A, grad_x=A, grad_weight=A, eps=1e-6, sum_stride=256,
+                grad_out_stride=256, grad_sum_stride=256, T=4, C=256, dtype=raw.GDN_BF16, weight_dtype=raw.GDN_BF16,
+                workspace=A, workspace_bytes=1 << 40, stream=None)
+    args.update(kw)
+    return gdn.gdn_rms_norm_bwd(**args)
+
+
+@pytest.mark.parametrize("kw,status", NORM + [
+    (dict(sum_stride=248), raw.GDN_ERR_SHAPE), (dict(grad_out_stride=260), raw.GDN_ERR_SHAPE), (dict(grad_sum_stride=0), raw.GDN_ERR_SHAPE),
+    *each(("sum", "weight", "grad_out", "grad_x", "grad_weight"), None, raw.GDN_ERR_NULL),
+    *each(("sum", "weight", "grad_out", "grad_sum", "grad_x", "grad_weight", "workspace"), A + 8, raw.GDN_ERR_ALIGN),
+    (dict(workspace=None), raw.GDN_ERR_WORKSPACE), (dict(workspace_bytes=0), raw.GDN_ERR_WORKSPACE)])
+def test_norm_bwd_argument_errors(kw, status):
+    assert norm_bwd(**kw) == status
+
+
+def test_norm_bwd_workspace():
+    need = gdn.gdn_rms_norm_bwd_workspace_bytes(4, 256, raw.GDN_BF16)
+    assert need > 0 and norm_bwd(workspace_bytes=need - 1) == raw.GDN_ERR_WORKSPACE
+    assert gdn.gdn_rms_norm_bwd_workspace_bytes(0, 256, raw.GDN_BF16) == 0
+    assert gdn.gdn_rms_norm_bwd_workspace_bytes(4, 252, raw.GDN_BF16) == 0  # unsupported arguments
+    assert gdn.gdn_rms_norm_bwd_workspace_bytes(4, 256, raw.GDN_C64) == 0
+
+
+CONV = TYPES + [(dict(C=0), raw.GDN_ERR_SHAPE), (dict(W=0), raw.GDN_ERR_SHAPE), (dict(R=-1), raw.GDN_ERR_SHAPE),
+                (dict(R=1 << 20), raw.GDN_ERR_SHAPE), (dict(W=1), raw.GDN_ERR_UNSUPPORTED), (dict(W=5), raw.GDN_ERR_UNSUPPORTED),
+                (dict(C=60, x_stride=64), raw.GDN_ERR_UNSUPPORTED), (dict(C=65544, x_stride=65544), raw.GDN_ERR_UNSUPPORTED),
+                (dict(x_stride=56), raw.GDN_ERR_SHAPE), (dict(x_stride=68), raw.GDN_ERR_SHAPE)]
+
+
+def conv(**kw):
+    args = dict(x=A, weight=A, bias=A, cu_seqlens=A, state=A, out=A, state_final=A, x_stride=64, T=9, R=2, C=64, W=4,
+                dtype=raw.GDN_BF16, weight_dtype=raw.GDN_BF16, silu=1, zero_rest=1, stream=None)
+    args.update(kw)
+    return gdn.gdn_short_conv(**args)
+
+
+@pytest.mark.parametrize("kw,status", CONV + [
+    (dict(T=-1), raw.GDN_ERR_SHAPE), (dict(T=1 << 28), raw.GDN_ERR_SHAPE), (dict(T=1 << 27, C=1024, x_stride=1024), raw.GDN_ERR_SHAPE),
+    (dict(R=1 << 19, C=8192, x_stride=8192), raw.GDN_ERR_SHAPE),
+    *each(("x", "weight", "cu_seqlens", "out"), None, raw.GDN_ERR_NULL),
+    *each(("x", "weight", "bias", "cu_seqlens", "state", "out", "state_final"), A + 8, raw.GDN_ERR_ALIGN)])
+def test_conv_argument_errors(kw, status):
+    assert conv(**kw) == status
+
+
+def test_conv_of_nothing_is_noop():
+    none = dict(x=None, weight=None, bias=None, cu_seqlens=None, state=None, out=None)
+    assert conv(T=0, R=0, **none) == raw.GDN_OK
+    assert conv(T=0, state_final=None, **none) == raw.GDN_OK
+
+
+def conv_bwd(**kw):
+    args = dict(x=A, weight=A, bias=A, grad_out=A, cu_seqlens=A, state=A, grad_state_final=A, grad_x=A, grad_weight=A,
+                grad_bias=A, grad_state=A, x_stride=64, grad_out_stride=64, T=9, R=2, C=64, W=4, dtype=raw.GDN_BF16,
+                weight_dtype=raw.GDN_BF16, silu=1, zero_rest=1, workspace=A, workspace_bytes=1 << 40, stream=None)
+    args.update(kw)
+    return gdn.gdn_short_conv_bwd(**args)
+
+
+@pytest.mark.parametrize("kw,status", CONV + [
+    (dict(T=-1), raw.GDN_ERR_SHAPE), (dict(grad_out_stride=56), raw.GDN_ERR_SHAPE),
+    *each(("x", "weight", "grad_out", "cu_seqlens", "grad_x", "grad_weight"), None, raw.GDN_ERR_NULL),
+    *each(("x", "weight", "bias", "grad_out", "cu_seqlens", "state", "grad_state_final", "grad_x", "grad_weight", "grad_bias",
+           "grad_state", "workspace"), A + 8, raw.GDN_ERR_ALIGN),
+    (dict(workspace=None), raw.GDN_ERR_WORKSPACE), (dict(workspace_bytes=0), raw.GDN_ERR_WORKSPACE)])
+def test_conv_bwd_argument_errors(kw, status):
+    assert conv_bwd(**kw) == status
+
+
+def test_conv_bwd_workspace():
+    need = gdn.gdn_short_conv_bwd_workspace_bytes(9, 64, 4)
+    assert need == 64 * 5 * 4 and conv_bwd(workspace_bytes=need - 1) == raw.GDN_ERR_WORKSPACE
+    assert gdn.gdn_short_conv_bwd_workspace_bytes(0, 64, 4) == 0
+    assert gdn.gdn_short_conv_bwd_workspace_bytes(9, 64, 5) == 0  # unsupported arguments
+
+
+def conv_step(**kw):
+    args = dict(x=A, weight=A, bias=A, state=A, out=A, x_stride=64, R=2, C=64, W=4, dtype=raw.GDN_BF16,
+                weight_dtype=raw.GDN_BF16, silu=1, stream=None)
+    args.update(kw)
+    return gdn.gdn_short_conv_step(**args)
+
+
+@pytest.mark.parametrize("kw,status", CONV + [
+    *each(("x", "weight", "state", "out"), None, raw.GDN_ERR_NULL),
+    *each(("x", "weight", "bias", "state", "out"), A + 8, raw.GDN_ERR_ALIGN)])
+def test_conv_step_argument_errors(kw, status):
+    assert conv_step(**kw) == status
+
+
+def test_conv_step_of_nothing_is_noop():
+    assert conv_step(R=0, x=None, weight=None, state=None, out=None) == raw.GDN_OK
+
+
+def test_helpers_refuse_host_tensors():
+    torch = pytest.importorskip("torch")
+    x, w, cu = torch.zeros(4, 64), torch.ones(64), torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(ValueError, match="HIP device"):
+        gdn.rms_norm(x, w)
+    with pytest.raises(ValueError, match="HIP device"):
+        gdn.rms_norm_quant(x, w)
+    with pytest.raises(ValueError, match="HIP device"):
+        gdn.rms_norm_bwd(x, w, x)
+    with pytest.raises(ValueError, match="HIP device"):
+        gdn.short_conv(x, torch.zeros(64, 4), cu)
+    with pytest.raises(ValueError, match="HIP device"):
+        gdn.short_conv_bwd(x, torch.zeros(64, 4), x, cu)
+    with pytest.raises(ValueError, match="HIP device"):
+        gdn.short_conv_step(x, torch.zeros(64, 4), torch.zeros(4, 3, 64))
