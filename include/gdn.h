@@ -608,6 +608,49 @@ int gdn_short_conv_step(const void *x, const void *weight, const void *bias, voi
                         long long x_stride, int R, int C, int W, int dtype, int weight_dtype, int silu,
                         void *stream);
 
+/*
+ * Selective state space scan.  For every head, with d = softplus(dt + dt_bias) and
+ * a state S [N, P]:
+ *
+ *     S_t = exp(a d_t) S_{t-1} + d_t B_t x_t^T,   out_t = S_t^T C_t + D x_t
+ *
+ *   x          [T] rows of H * P bf16 values (dtype), x_stride apart
+ *   dt         [T] rows of H values, bf16 or float32 (dt_dtype), dt_stride apart
+ *              (any, from H on)
+ *   a          [H], negative: the rate of decay;  D, dt_bias [H], may be NULL
+ *              (zeros); all of param_dtype, bf16 or float32
+ *   B, C       [T] rows of G * N bf16 values, B_stride and C_stride apart; head h
+ *              reads group h / (H / G), H a multiple of G
+ *   cu_seqlens [R + 1]
+ *   S0         [R, H, N, P] float32: the states before, may be NULL (zeros)
+ *   out        [T, H, P] bf16, written
+ *   S_final    [R, H, N, P] float32, written; may be NULL
+ *
+ * P and N are 64 or 128 each.  States and every sum are float32; weights of rows and
+ * the state are rounded to bf16 where they enter a product whose result is out, and
+ * taken in three bf16 parts (2^-25) where it is a state.  A decay of less than 2^-160
+ * a token is taken for that.  Inputs are finite and a <= 0: others give results that
+ * are undefined, typically non-finite, in their own sequence and nowhere else.
+ * Workspace: gdn_ssm_scan_workspace_bytes (0 for short T), scratch on entry and
+ * exit, no clearing needed.  T is below 2^26, T * H below 2^31, R below 2^20, R * H
+ * below 2^22, the strides of x, B and C below 2^24.
+ */
+size_t gdn_ssm_scan_workspace_bytes(int T, int H, int P, int G, int N);
+int gdn_ssm_scan(const void *x, const void *dt, const void *a, const void *B, const void *C, const void *D,
+                 const void *dt_bias, const int *cu_seqlens, const float *S0, void *out, float *S_final,
+                 long long x_stride, long long dt_stride, long long B_stride, long long C_stride, int T, int R,
+                 int H, int P, int G, int N, int dtype, int dt_dtype, int param_dtype, int zero_rest,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token for each of R sequences, in place on their states S [R, H, N, P]
+ * float32; x, dt, B, C have R rows.  The state and its sums are float32.
+ */
+int gdn_ssm_step(const void *x, const void *dt, const void *a, const void *B, const void *C, const void *D,
+                 const void *dt_bias, float *S, void *out, long long x_stride, long long dt_stride,
+                 long long B_stride, long long C_stride, int R, int H, int P, int G, int N, int dtype, int dt_dtype,
+                 int param_dtype, void *stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *gdn_status_str(int status);
 

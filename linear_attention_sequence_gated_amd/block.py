@@ -1,5 +1,5 @@
 """Torch helpers of what stands around a recurrent layer's state update (include/gdn.h): the root-mean-square norm with
-the residual's addition, also with an output in 8 bits, and the short causal convolution.
+the residual's addition, also with an output in 8 bits, the short causal convolution, and the selective state space scan.
 
 They check dtypes, shapes, strides and devices, allocate what is not passed in, pass ``data_ptr()`` and the current
 HIP stream of the tensors' device (or ``stream``), and raise on a non-OK status.  Rows are [tokens, channels] with the
@@ -232,4 +232,94 @@ def short_conv_step(x, weight, state, bias=None, silu: bool = True, out=None):
         _dense(out, "out", (r, c), x.dtype, dev)
     _call(dev, raw.load().gdn_short_conv_step, x.data_ptr(), weight.data_ptr(), bp, state.data_ptr(), out.data_ptr(), xs, r,
           c, w, code, wcode, silu)
+    return out
+
+
+def _heads(t, name, shape, dev):
+    """Distance between the rows of t [tokens, heads, D] bf16, whose heads lie side by side."""
+    if t.shape != shape or t.dtype is not torch.bfloat16 or t.get_device() != dev.index:
+        raw._check(t.contiguous(), name, shape, torch.bfloat16, dev)
+    n, h, d = shape
+    row, head, one = t.stride()
+    if n and (d > 1 and one != 1 or h > 1 and head != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    if n <= 1:
+        return h * d
+    if row < h * d or row % 8:
+        raise ValueError(f"{name}: rows must be a multiple of 8 elements apart and not overlap")
+    return row
+
+
+def _scan_inputs(x, dt, a, B, C, D, dt_bias, who):
+    """(device, addresses of the seven inputs, strides, sizes, types)."""
+    dev = _device(x, who)
+    if x.dim() != 3 or B.dim() != 3:
+        raise ValueError(f"{who}: x and B must be [tokens, heads, size]")
+    t, h, p = x.shape
+    _, g, n = B.shape
+    xs, bs, cs = _heads(x, "x", (t, h, p), dev), _heads(B, "B", (t, g, n), dev), _heads(C, "C", (t, g, n), dev)
+    dcode, pcode = _CODES.get(dt.dtype), _CODES.get(a.dtype)
+    if dcode is None or pcode is None:
+        raise TypeError(f"{who}: dt and the parameters must be bfloat16 or float32")
+    if dt.shape != (t, h) or dt.get_device() != dev.index:
+        raw._check(dt.contiguous(), "dt", (t, h), dt.dtype, dev)
+    row, one = dt.stride()
+    if t and h > 1 and one != 1:
+        raise ValueError("dt: the heads of a row must be contiguous")
+    if t > 1 and row < h:
+        raise ValueError("dt: rows must not overlap")
+    _dense(a, "a", (h,), a.dtype, dev)
+    ptrs = (x.data_ptr(), dt.data_ptr(), a.data_ptr(), B.data_ptr(), C.data_ptr(), _given(D, "D", (h,), a.dtype, dev),
+            _given(dt_bias, "dt_bias", (h,), a.dtype, dev))
+    return dev, ptrs, (xs, row if t > 1 else h, bs, cs), (t, h, p, g, n), (raw.GDN_BF16, dcode, pcode)
+
+
+@functools.lru_cache(maxsize=1024)
+def _scan_workspace(*sizes):
+    return raw.gdn_ssm_scan_workspace_bytes(*sizes)
+
+
+@_on_stream
+def ssm_scan(x, dt, a, B, C, cu_seqlens, D=None, dt_bias=None, S0=None, out=None, S_final=None):
+    """Selective state space scan over packed sequences: with d = softplus(dt + dt_bias), per head
+
+        S_t = exp(a d_t) S_{t-1} + d_t B_t x_t^T,    out_t = S_t^T C_t + D x_t.
+
+    x [T, H, P] bf16 and B, C [T, G, N] bf16 (P, N 64 or 128; head h reads group h // (H / G)), each of which may be a part
+    of wider rows; dt [T, H] bf16 or float32; a (negative), D, dt_bias [H] bf16 or float32, one dtype; cu_seqlens [R + 1]
+    int32 the offsets of the sequences; S0 [R, H, N, P] float32 the states before (zeros unless given).
+
+    Returns (out [T, H, P] bf16, S_final [R, H, N, P] float32).  Rows in no sequence are not written; an out that is
+    allocated here holds zeros there.  The workspace is allocated here with torch.
+    """
+    dev, ptrs, strides, (t, h, p, g, n), types = _scan_inputs(x, dt, a, B, C, D, dt_bias, "ssm_scan")
+    r = _sequences(cu_seqlens, dev)
+    sp = _given(S0, "S0", (r, h, n, p), torch.float32, dev)
+    zero_rest = out is None
+    if out is None:
+        out = x.new_empty((t, h, p))
+    else:
+        _dense(out, "out", (t, h, p), torch.bfloat16, dev)
+    if S_final is None:
+        S_final = x.new_empty((r, h, n, p), dtype=torch.float32)
+    else:
+        _dense(S_final, "S_final", (r, h, n, p), torch.float32, dev)
+    size = _scan_workspace(t, h, p, g, n)
+    ws = S_final.new_empty(size // 4) if size else None
+    _call(dev, raw.load().gdn_ssm_scan, *ptrs, cu_seqlens.data_ptr(), sp, out.data_ptr(), S_final.data_ptr(), *strides, t, r,
+          h, p, g, n, *types, zero_rest, raw._ptr(ws), size)
+    return out, S_final
+
+
+@_on_stream
+def ssm_step(x, dt, a, B, C, S, D=None, dt_bias=None, out=None):
+    """One token for each of R sequences of ssm_scan: x [R, H, P], dt [R, H], B, C [R, G, N], in place on S [R, H, N, P]
+    float32.  Returns out [R, H, P] bf16."""
+    dev, ptrs, strides, (r, h, p, g, n), types = _scan_inputs(x, dt, a, B, C, D, dt_bias, "ssm_step")
+    _dense(S, "S", (r, h, n, p), torch.float32, dev)
+    if out is None:
+        out = x.new_empty((r, h, p))
+    else:
+        _dense(out, "out", (r, h, p), torch.bfloat16, dev)
+    _call(dev, raw.load().gdn_ssm_step, *ptrs, S.data_ptr(), out.data_ptr(), *strides, r, h, p, g, n, *types)
     return out

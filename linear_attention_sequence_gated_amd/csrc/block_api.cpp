@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <cmath>
+#include <initializer_list>
 
 #include "../../include/gdn.h"
 #include "gdn_block.hpp"
@@ -55,6 +56,26 @@ int norm(const void* x, const void* residual, const void* weight, void* out, voi
   if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
   return status(gdn::launch_rms_norm({x, residual, weight, out, sum, scale, xs, rs, eps, T, C, dtype == GDN_F32,
                                       weight_dtype == GDN_F32, fmt, block, stream}));
+}
+
+// Sizes and types of a scan.  64 rows of x, B and C, the most that a buffer
+// resource covers, stay inside 32-bit byte offsets.
+int scan_shape(int T, int R, int H, int P, int G, int N) {
+  if (T < 0 || R < 0 || H <= 0 || P <= 0 || G <= 0 || N <= 0 || H % G || T >= (1 << 26) || R >= (1 << 20)) return GDN_ERR_SHAPE;
+  if (H >= (1 << 16) || (long long)T * H >= (1LL << 31) || (long long)R * H >= (1LL << 22)) return GDN_ERR_SHAPE;
+  return (P == 64 || P == 128) && (N == 64 || N == 128) ? GDN_OK : GDN_ERR_UNSUPPORTED;
+}
+bool near_ok(long long s, long long row) { return stride_ok(s, row) && s < (1LL << 24); }
+// dt and the parameters of heads may begin anywhere, as columns of a projection do.
+bool params_aligned(std::initializer_list<const void*> ptrs, int dtype) {
+  for (const void* p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p) % (dtype == GDN_F32 ? 4 : 2)) return false;
+  return true;
+}
+int scan_types(int dtype, int dt_dtype, int param_dtype) {
+  for (const int d : {dtype, dt_dtype, param_dtype})
+    if (!known_dtype(d)) return GDN_ERR_DTYPE;
+  return dtype == GDN_BF16 && dt_dtype != GDN_C64 && param_dtype != GDN_C64 ? GDN_OK : GDN_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -147,6 +168,48 @@ int gdn_short_conv_step(const void* x, const void* weight, const void* bias, voi
   if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
   return status(gdn::launch_short_conv_step({x, weight, bias, state, out, x_stride, R, C, W, dtype == GDN_F32,
                                              weight_dtype == GDN_F32, silu != 0, stream}));
+}
+
+size_t gdn_ssm_scan_workspace_bytes(int T, int H, int P, int G, int N) {
+  return scan_shape(T, 0, H, P, G, N) ? 0 : gdn::ssm_scan_workspace_bytes(T, H, P, G, N);
+}
+
+int gdn_ssm_scan(const void* x, const void* dt, const void* a, const void* B, const void* C, const void* D,
+                 const void* dt_bias, const int* cu_seqlens, const float* S0, void* out, float* S_final, long long x_stride,
+                 long long dt_stride, long long B_stride, long long C_stride, int T, int R, int H, int P, int G, int N,
+                 int dtype, int dt_dtype, int param_dtype, int zero_rest, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+  if (const int s = scan_types(dtype, dt_dtype, param_dtype)) return s;
+  if (const int s = scan_shape(T, R, H, P, G, N)) return s;
+  if (!near_ok(x_stride, (long long)H * P) || !near_ok(B_stride, (long long)G * N) || !near_ok(C_stride, (long long)G * N))
+    return GDN_ERR_SHAPE;
+  if (dt_stride < H || dt_stride >= (1LL << 32)) return GDN_ERR_SHAPE;
+  if (T == 0 && (R == 0 || !S_final)) return GDN_OK;
+  if (!a || !cu_seqlens || (T && (!x || !dt || !B || !C || !out))) return GDN_ERR_NULL;
+  const void* ptrs[] = {x, B, C, cu_seqlens, S0, out, S_final, workspace};
+  if (!all_aligned(ptrs) || !params_aligned({dt}, dt_dtype) || !params_aligned({a, D, dt_bias}, param_dtype)) return GDN_ERR_ALIGN;
+  const size_t need = gdn::ssm_scan_workspace_bytes(T, H, P, G, N);
+  if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+  return status(gdn::launch_ssm_scan({x, dt, a, B, C, D, dt_bias, cu_seqlens, S0, out, S_final, static_cast<float*>(workspace),
+                                      x_stride, dt_stride, B_stride, C_stride,
+                                      {T, R, H, P, G, N, dt_dtype == GDN_F32, param_dtype == GDN_F32}, zero_rest != 0, stream}));
+}
+
+int gdn_ssm_step(const void* x, const void* dt, const void* a, const void* B, const void* C, const void* D,
+                 const void* dt_bias, float* S, void* out, long long x_stride, long long dt_stride, long long B_stride,
+                 long long C_stride, int R, int H, int P, int G, int N, int dtype, int dt_dtype, int param_dtype,
+                 void* stream) {
+  if (const int s = scan_types(dtype, dt_dtype, param_dtype)) return s;
+  if (const int s = scan_shape(0, R, H, P, G, N)) return s;
+  if (!stride_ok(x_stride, (long long)H * P) || !stride_ok(B_stride, (long long)G * N) || !stride_ok(C_stride, (long long)G * N))
+    return GDN_ERR_SHAPE;
+  if (dt_stride < H || dt_stride >= (1LL << 32)) return GDN_ERR_SHAPE;
+  if (R == 0) return GDN_OK;
+  if (!x || !dt || !a || !B || !C || !S || !out) return GDN_ERR_NULL;
+  const void* ptrs[] = {x, B, C, S, out};
+  if (!all_aligned(ptrs) || !params_aligned({dt}, dt_dtype) || !params_aligned({a, D, dt_bias}, param_dtype)) return GDN_ERR_ALIGN;
+  return status(gdn::launch_ssm_step({x, dt, a, B, C, D, dt_bias, S, out, x_stride, dt_stride, B_stride, C_stride,
+                                      {R, R, H, P, G, N, dt_dtype == GDN_F32, param_dtype == GDN_F32}, stream}));
 }
 
 }  // extern "C"

@@ -93,4 +93,48 @@ struct ConvStepArgs {
 };
 hipError_t launch_short_conv_step(const ConvStepArgs& a);
 
+// Types and sizes of a scan: H heads of P channels read G groups of B and C of N
+// values.  dt is float32 or bf16, and so are the parameters.
+struct ScanShape {
+  int T, R, H, P, G, N;
+  bool dt_f32, p_f32;
+};
+
+struct ScanArgs {
+  const void* x;
+  const void* dt;
+  const void* a;
+  const void* B;
+  const void* C;
+  const void* D;     // may be NULL
+  const void* bias;  // may be NULL
+  const int* cu;
+  const float* S0;  // may be NULL
+  void* out;
+  float* S_final;  // may be NULL
+  float* ws;
+  long long xs, dts, bs, cs;
+  ScanShape n;
+  bool zero_rest;
+  void* stream;
+};
+size_t ssm_scan_workspace_bytes(int T, int H, int P, int G, int N);
+hipError_t launch_ssm_scan(const ScanArgs& a);
+
+struct ScanStepArgs {
+  const void* x;
+  const void* dt;
+  const void* a;
+  const void* B;
+  const void* C;
+  const void* D;
+  const void* bias;
+  float* S;
+  void* out;
+  long long xs, dts, bs, cs;
+  ScanShape n;
+  void* stream;
+};
+hipError_t launch_ssm_step(const ScanStepArgs& a);
+
 }  // namespace gdn

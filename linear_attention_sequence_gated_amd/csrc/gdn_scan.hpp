@@ -1,0 +1,190 @@
+// gdn_scan.hpp -- parts of the selective state space scan shared by its forward
+// and its gradients: steps and decays of a piece of rows, how heads are dealt to
+// workgroups, and the walk over the sequences of a segment of rows.
+#pragma once
+
+#include "gdn_block.hpp"
+#include "gdn_rows.hpp"
+
+namespace gdn {
+namespace scan {
+
+using namespace rows;
+using tile::f32x16;
+
+constexpr int Q = 64;             // rows to a piece
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// log(1 + e^z), to float32's own precision also where it is small.
+__device__ __forceinline__ float softplus(float z) { return z > 20.f ? z : log1pf(__expf(z)); }
+
+// What a row does to the state, in powers of two: steps of less than 2^-160 are
+// taken for that, since 2^-160 of any float32 number is below the smallest; so the
+// sums over a piece stay below 2^14 and their differences exact to 2^-10.
+__device__ __forceinline__ float log2_keep(float a, float delta) { return fmaxf(a * kLog2e * delta, -160.f); }
+
+// Columns of x are taken 64 at a time ("strips"): a head of P = 64 or half of one of
+// 128, whose recurrence runs by itself.  Workgroups take NS neighbouring strips of
+// one group of heads; a group's last workgroup may have fewer.
+struct Strips {
+  int per_group;  // strips to a group
+  int sets;       // workgroups to a group
+};
+__host__ __device__ inline Strips strips(int H, int P, int G, int NS) {
+  const int per = H / G * (P / 64);
+  return {per, (per + NS - 1) / NS};
+}
+
+// ----------------------------------------------------------------- sequences
+// cu[i], in LDS where all of them fit.
+struct Offsets {
+  const int* cu;
+  const int* window;  // NULL: not there
+  __device__ __forceinline__ int operator()(int i) const {
+    return __builtin_amdgcn_readfirstlane(window ? window[i] : cu[i]);
+  }
+  // How many of the first n offsets are below row.
+  __device__ __forceinline__ int below(int n, int row) const {
+    int lo = 0;
+    while (lo < n) {
+      const int mid = lo + (n - lo) / 2;
+      if ((*this)(mid) < row) lo = mid + 1;
+      else n = mid;
+    }
+    return lo;
+  }
+};
+
+// Offsets ready for use by NT threads; ends with a barrier.
+template <int NT> __device__ __forceinline__ Offsets offsets(const int* cu, int R, int* window) {
+  if (R >= kWindow) return {cu, nullptr};
+  for (int i = threadIdx.x; i <= R; i += NT) window[i] = cu[i];
+  __syncthreads();
+  return {cu, window};
+}
+
+// A run of rows of one sequence, at most Q.
+struct Piece {
+  int row, n, seq;
+  bool first, last;  // of its sequence
+};
+
+// The pieces of rows [s0, s1), in order: of the sequence that goes on into them,
+// if any, then of those that begin in them.  The rows that it gives ascend, and
+// every call ends, whatever cu holds.
+struct Walk {
+  Offsets cu;
+  int T, s1, r, rend, beg, pos, end;
+  __device__ __forceinline__ void init(const Offsets& c, int R, int T_, int s0, int s1_) {
+    cu = c, T = T_, s1 = s1_;
+    const int k = cu.below(R, s0);
+    rend = cu.below(R, s1);
+    r = k - 1;
+    beg = pos = end = s0;
+    if (k > 0) {
+      beg = min(max(cu(k - 1), 0), s0);
+      end = min(max(cu(k), s0), T);
+    }
+  }
+  // Whether rows before s0 belong to the first piece's sequence.
+  __device__ __forceinline__ bool goes_on() const { return pos < min(end, s1); }
+  __device__ __forceinline__ bool next(Piece& p) {
+    for (;;) {
+      const int e = min(end, s1);
+      if (pos < e) {
+        p.row = pos, p.n = min(Q, e - pos), p.seq = r;
+        p.first = pos == beg;
+        pos += p.n;
+        p.last = pos == end;
+        return true;
+      }
+      if (++r >= rend) return false;
+      beg = pos = min(max(cu(r), pos), T);
+      end = min(max(cu(r + 1), beg), T);
+    }
+  }
+};
+
+// ------------------------------------------------------------ steps of a piece
+// Of the piece's rows (a lane each), for one head: in LDS, for a wave.
+struct Steps {
+  float G[Q];  // sums of the log2 decays up to and including the row
+  float u[Q];  // log2(delta) - G
+  float v[32];  // delta 2^(G_31 - G) of the first 32
+  float w[Q];  // delta 2^(sum of the decays behind the row)
+};
+
+__device__ __forceinline__ float dt_at(const void* dt, bool f32, long long i) { return param(dt, f32, i); }
+
+// Returns the sum over the piece.  No barrier: the wave reads what it wrote.
+__device__ __forceinline__ float steps(Steps& s, float z, float a, bool in) {
+  const int lane = threadIdx.x & 63;
+  const float delta = in ? softplus(z) : 0.f;
+  const float g = in ? log2_keep(a, delta) : 0.f;
+  const float G = pipe::wave_prefix_sum(g);
+  // the sums behind each row, from the last row back: no difference of large numbers
+  const float back = pipe::wave_prefix_sum(__shfl(g, 63 - lane));
+  const float after = __shfl(back, (62 - lane) & 63);
+  const float G31 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, G), 31));
+  s.G[lane] = G;
+  s.u[lane] = __builtin_amdgcn_logf(delta) - G;
+  if (lane < 32) s.v[lane] = delta * exp2_(G31 - G);
+  s.w[lane] = delta * exp2_(lane == 63 ? 0.f : after);
+  pipe::issue_fence();  // read as vectors from here on
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, G), 63));
+}
+
+// ------------------------------------------------------------------- products
+// The state of a strip's 32 columns, [N][32]: tile t holds rows 32 t ..; a tile's row
+// i stands for n = i with bits 2 and 3 exchanged, so that elements 8 b .. 8 b + 7 of
+// a lane are the eight n from 16 b + 8 (l / 32) on: an operand of the products with
+// rows of C (and B) read eight values at a time.
+__device__ __forceinline__ int state_row(int e, int half) { return 16 * (e / 8) + 8 * half + e % 8; }
+
+// Transposed operand whose row l % 32 of the tile is that n.
+template <int D> __device__ __forceinline__ int col_base_state(int lane) {
+  const int c = lane & 15, m = c & 3;
+  return pipe::row_off<D>(4 * (lane >> 5) + (c >> 2), 16 * ((lane >> 4) & 1) + 8 * (m & 1) + 4 * (m >> 1)) * 2;
+}
+
+// Eight bf16 values (of rows k) times eight numbers w, as PARTS bf16 operands that
+// add up to the products: to 2^-8, 2^-17 and 2^-25 of them.
+template <int PARTS> struct Split {
+  u32x4 part[PARTS];
+  __device__ __forceinline__ void make(const u32x4& x, const float* w0, const float* w1) {
+    const float4 a = *reinterpret_cast<const float4*>(w0), b = *reinterpret_cast<const float4*>(w1);
+    float f[8] = {pipe::lo_f(x[0]) * a.x, pipe::hi_f(x[0]) * a.y, pipe::lo_f(x[1]) * a.z, pipe::hi_f(x[1]) * a.w,
+                  pipe::lo_f(x[2]) * b.x, pipe::hi_f(x[2]) * b.y, pipe::lo_f(x[3]) * b.z, pipe::hi_f(x[3]) * b.w};
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const unsigned c = pipe::cvt2(f[2 * i], f[2 * i + 1]);
+        part[p][i] = c;
+        f[2 * i] -= pipe::lo_f(c);
+        f[2 * i + 1] -= pipe::hi_f(c);
+      }
+    }
+  }
+};
+
+// States in memory, [N][P] float32: the part of a wave's 32 columns.
+template <int NT> __device__ __forceinline__ void load_state(f32x16 (&S)[NT], const float* src, int P) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) S[t][e] = src[(long long)(32 * t + state_row(e, lane >> 5)) * P + (lane & 31)];
+}
+template <int NT> __device__ __forceinline__ void store_state(const f32x16 (&S)[NT], float* dst, int P) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) dst[(long long)(32 * t + state_row(e, lane >> 5)) * P + (lane & 31)] = S[t][e];
+}
+
+}  // namespace scan
+}  // namespace gdn

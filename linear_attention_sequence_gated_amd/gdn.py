@@ -30,7 +30,8 @@ EXPORTS = ("gdn_chunk_fwd_workspace_bytes", "gdn_chunk_fwd", "gdn_chunk_fwd_prol
            "gdn_block_tables", "gdn_cache_append", "gdn_attn_decode_workspace_bytes", "gdn_attn_decode",
            "gdn_attn_prompt", "gdn_attn_prompt_bwd_workspace_bytes", "gdn_attn_prompt_bwd",
            "gdn_rms_norm", "gdn_rms_norm_quant", "gdn_rms_norm_bwd_workspace_bytes", "gdn_rms_norm_bwd", "gdn_short_conv",
-           "gdn_short_conv_bwd_workspace_bytes", "gdn_short_conv_bwd", "gdn_short_conv_step")
+           "gdn_short_conv_bwd_workspace_bytes", "gdn_short_conv_bwd", "gdn_short_conv_step",
+           "gdn_ssm_scan_workspace_bytes", "gdn_ssm_scan", "gdn_ssm_step")
 
 _lib = None
 
@@ -100,6 +101,12 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.gdn_short_conv_bwd.restype = ci
     lib.gdn_short_conv_step.argtypes = [vp] * 5 + [ll] + [ci] * 6 + [vp]
     lib.gdn_short_conv_step.restype = ci
+    lib.gdn_ssm_scan_workspace_bytes.argtypes = [ci] * 5
+    lib.gdn_ssm_scan_workspace_bytes.restype = sz
+    lib.gdn_ssm_scan.argtypes = [vp] * 11 + [ll] * 4 + [ci] * 10 + [vp, sz, vp]
+    lib.gdn_ssm_scan.restype = ci
+    lib.gdn_ssm_step.argtypes = [vp] * 9 + [ll] * 4 + [ci] * 8 + [vp]
+    lib.gdn_ssm_step.restype = ci
     lib.gdn_status_str.argtypes = [ci]
     lib.gdn_status_str.restype = ctypes.c_char_p
     if path is None:
@@ -241,6 +248,23 @@ def gdn_short_conv_bwd(x, weight, bias, grad_out, cu_seqlens, state, grad_state_
 
 def gdn_short_conv_step(x, weight, bias, state, out, x_stride, R, C, W, dtype, weight_dtype, silu, stream) -> int:
     return int(load().gdn_short_conv_step(x, weight, bias, state, out, x_stride, R, C, W, dtype, weight_dtype, silu, stream))
+
+
+def gdn_ssm_scan_workspace_bytes(T, H, P, G, N) -> int:
+    return int(load().gdn_ssm_scan_workspace_bytes(T, H, P, G, N))
+
+
+def gdn_ssm_scan(x, dt, a, B, C, D, dt_bias, cu_seqlens, S0, out, S_final, x_stride, dt_stride, B_stride, C_stride, T, R, H,
+                 P, G, N, dtype, dt_dtype, param_dtype, zero_rest, workspace, workspace_bytes, stream) -> int:
+    return int(load().gdn_ssm_scan(x, dt, a, B, C, D, dt_bias, cu_seqlens, S0, out, S_final, x_stride, dt_stride, B_stride,
+                                   C_stride, T, R, H, P, G, N, dtype, dt_dtype, param_dtype, zero_rest, workspace,
+                                   workspace_bytes, stream))
+
+
+def gdn_ssm_step(x, dt, a, B, C, D, dt_bias, S, out, x_stride, dt_stride, B_stride, C_stride, R, H, P, G, N, dtype,
+                 dt_dtype, param_dtype, stream) -> int:
+    return int(load().gdn_ssm_step(x, dt, a, B, C, D, dt_bias, S, out, x_stride, dt_stride, B_stride, C_stride, R, H, P, G,
+                                   N, dtype, dt_dtype, param_dtype, stream))
 
 
 # ------------------------------------------------------------- torch helpers

@@ -89,3 +89,62 @@ def short_conv_bwd(x, weight, bias, cu, g, state=None, g_last=None, act=True):
         size[2] += np.abs(q).sum(0)
         got[0][b:e], got[3][r], size[0][b:e], size[3][r] = gz[W - 1:], gz[:W - 1], az[W - 1:], az[:W - 1]
     return got, size
+
+
+def softplus(z):
+    return np.where(z > 30, z, np.log1p(np.exp(np.minimum(z, 30.0))))
+
+
+def ssm_scan(x, dt, a, B, C, D, bias, cu, S0=None):
+    """Token after token.  x [T, H, P], dt [T, H], B, C [T, G, N]; D, bias [H].  Returns (out, S_final [R, H, N, P])."""
+    T, H, P = x.shape
+    rep, N, R = H // B.shape[1], B.shape[2], len(cu) - 1
+    Bh, Ch = np.repeat(B, rep, 1), np.repeat(C, rep, 1)
+    d = softplus(dt + bias)
+    keep = np.exp(a * d)
+    out, last = np.zeros((T, H, P)), np.zeros((R, H, N, P))
+    for r, b, e in _sequences(cu, T):
+        S = np.zeros((H, N, P)) if S0 is None else S0[r].copy()
+        for t in range(b, e):
+            S = keep[t][:, None, None] * S + (d[t][:, None] * Bh[t])[:, :, None] * x[t][:, None]
+            out[t] = np.einsum("hn,hnp->hp", Ch[t], S) + D[:, None] * x[t]
+        last[r] = S
+    return out, last
+
+
+def ssm_scan_bwd(x, dt, a, B, C, D, bias, cu, g, S0=None, g_last=None):
+    """Gradients of sum(out * g) + sum(S_final * g_last), in the order x, dt, a, B, C, D, bias, S0."""
+    T, H, P = x.shape
+    G, N, R = B.shape[1], B.shape[2], len(cu) - 1
+    rep = H // G
+    Bh, Ch = np.repeat(B, rep, 1), np.repeat(C, rep, 1)
+    z = dt + bias
+    d = softplus(z)
+    keep = np.exp(a * d)
+    gx, gd, ga, gB, gC = np.zeros_like(x), np.zeros_like(dt), np.zeros(H), np.zeros_like(Bh), np.zeros_like(Ch)
+    gS0 = np.zeros((R, H, N, P))
+    gx += D[:, None] * g
+    for r, b, e in _sequences(cu, T):
+        S = [np.zeros((H, N, P)) if S0 is None else S0[r]]
+        for t in range(b, e):
+            S.append(keep[t][:, None, None] * S[-1] + (d[t][:, None] * Bh[t])[:, :, None] * x[t][:, None])
+        gS = np.zeros((H, N, P)) if g_last is None else g_last[r].copy()
+        for t in range(e - 1, b - 1, -1):
+            new, old = S[t - b + 1], S[t - b]
+            gC[t] = np.einsum("hnp,hp->hn", new, g[t])
+            gS = gS + Ch[t][:, :, None] * g[t][:, None]
+            bx = np.einsum("hnp,hp->hn", gS, x[t])
+            gB[t] = d[t][:, None] * bx
+            gx[t] += d[t][:, None] * np.einsum("hn,hnp->hp", Bh[t], gS)
+            gk = (gS * old).sum((1, 2)) * keep[t]
+            gd[t] = a * gk + (Bh[t] * bx).sum(1)
+            ga += d[t] * gk
+            gS = keep[t][:, None, None] * gS
+        gS0[r] = gS
+    gz = gd / (1.0 + np.exp(-z))
+    inside = np.zeros(T, bool)
+    for _, b, e in _sequences(cu, T):
+        inside[b:e] = True
+    gx[~inside] = 0
+    g = np.where(inside[:, None, None], g, 0.0)
+    return [gx, gz, ga, gB.reshape(T, G, rep, N).sum(2), gC.reshape(T, G, rep, N).sum(2), (g * x).sum((0, 2)), gz.sum(0), gS0]

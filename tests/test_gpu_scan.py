@@ -1,0 +1,151 @@
+"""The selective state space scan on the GPU against its fp64 reference.
+
+Tolerances, element by element, relative to SIZE: what the same recurrence gives for the inputs' magnitudes, so the sum of
+the magnitudes of a result's terms.
+  out  Each term is rounded to bf16 once (its weight, or the state that it is part of): 2^-8 of SIZE; float32 sums of N + 64
+       terms and their weights' exponents, (N + 128) 2^-24 and 16 2^-24 of the largest sum of decays in a piece; then the
+       result to bf16, 2^-8 of itself.
+  S    A term is kept to 2^-25, and each piece's sum of 64 and the decays' exponents to (64 + 64 E) 2^-24, where E is
+       the largest sum of decays in a piece (up to the 160 where what it multiplies is gone); the products with a piece's
+       decay add 2 2^-24 a piece.
+A second, normwise bound tells random rounding from a wrong row: independent errors of at most half a bf16 step are, in the
+root of their mean square, 2^-8 / sqrt(3) of the values; two of them (term and result) 3.2e-3; 4e-3 is asked."""
+import numpy as np
+import pytest
+
+from gpu_util import down, note, torch_dev
+from oracle import block as ref
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+class Case:
+    """Seeded inputs on the device (strided as parts of projections), and the numbers that they hold."""
+
+    def __init__(self, torch, cu, t, h, p, g, n, seed=0, dt="bf16", param="bf16", state=True, spread=1.0, slow=False):
+        import numpy as np
+        self.torch, self.cu, self.shape = torch, cu, (t, h, p, g, n)
+        rng = np.random.default_rng([seed, t, h])
+        types = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+        def make(shape, kind="bf16", f=None):
+            v = rng.standard_normal(shape) if f is None else f
+            return torch.from_numpy(np.asarray(v, np.float32)).to(types[kind]).cuda()
+
+        rows = make((t, h * p + 2 * g * n + 8))
+        self.x = rows[:, 8:8 + h * p].view(t, h, p)
+        self.B = rows[:, 8 + h * p:8 + h * p + g * n].view(t, g, n)
+        self.C = rows[:, 8 + h * p + g * n:].view(t, g, n)
+        self.dt = make((t, h + 3), dt, spread * rng.standard_normal((t, h + 3)))[:, 3:]
+        step = np.exp(rng.uniform(np.log(1e-3), np.log(1e-2 if slow else 1e-1), h))
+        self.bias = make(h, param, np.log(np.expm1(step)))
+        self.a = make(h, param, -rng.uniform(1, 2 if slow else 16, h))
+        self.D = make(h, param)
+        self.S0 = make((len(cu) - 1, h, n, p), "f32") if state else None
+        self.offsets = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        self.names = ("x", "dt", "a", "B", "C")
+
+    def args(self):
+        return [getattr(self, k) for k in self.names]
+
+    def numbers(self):
+        f = lambda t: None if t is None else down(t).astype(np.float64)  # noqa: E731
+        return [f(v) for v in (*self.args(), self.D, self.bias)], f(self.S0)
+
+    def exponents(self):
+        """The largest sum of log2 decays over a piece of 64 rows, at most."""
+        (x, dt, a, B, C, D, bias), _ = self.numbers()
+        g = np.minimum(-a * ref.softplus(dt + bias) * 1.4427, 160.0)
+        return float(max((g[i:i + 64].sum(0).max() for i in range(0, len(g), 32)), default=0.0))
+
+
+def check(c, out, last, pieces):
+    ins, S0 = c.numbers()
+    x, dt, a, B, C, D, bias = ins
+    t, h, p, g, n = c.shape
+    want, want_last = ref.ssm_scan(*ins, c.cu, S0)
+    size, size_last = ref.ssm_scan(np.abs(x), dt, a, np.abs(B), np.abs(C), np.abs(D), bias, c.cu, None if S0 is None else np.abs(S0))
+    E = c.exponents()
+    got, got_last = down(out).astype(np.float64), down(last).astype(np.float64)
+    assert np.isfinite(got).all() and np.isfinite(got_last).all()
+    room = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + (n + 128 + 16 * E) * U) * 1.01 * size + 1e-30
+    room_last = (64 + 64 * min(E, 160) + 2 * pieces) * U * size_last + 1e-30
+    worst = np.abs(got - want).max(initial=0) and float((np.abs(got - want) / room).max())
+    worst_last = float((np.abs(got_last - want_last) / room_last).max(initial=0))
+    norm = np.linalg.norm(want)
+    rel = np.linalg.norm(got - want) / norm if norm else 0.0
+    nl = np.linalg.norm(want_last)
+    print(f"[parity] out {worst:.3f} of its room, norm {rel:.2e}; S {worst_last:.3f}, norm {np.linalg.norm(got_last - want_last) / max(nl, 1e-300):.2e}", flush=True)
+    assert worst <= 1 and worst_last <= 1 and rel <= 4e-3
+
+
+SHAPES = [(2, 64, 1, 64), (3, 64, 1, 128), (4, 64, 2, 128), (6, 64, 2, 64), (2, 128, 1, 128), (3, 128, 3, 64), (1, 64, 1, 128)]
+RUNS = [("one row", [0, 1], 1), ("a piece", [0, 64], 64), ("short", [0, 2, 3, 3, 7], 7), ("odd", [0, 131], 131), ("empty", [0, 0, 0], 0),
+        ("no sequences", [0], 5), ("rows outside", [3, 40, 41, 90], 101), ("ends", [0, 63, 64, 127, 128, 130, 193], 193), ("ragged", [0, 300, 301, 517], 517),
+        ("singles", list(range(70)), 69)]
+
+
+@pytest.mark.parametrize("name,cu,t", RUNS, ids=[r[0] for r in RUNS])
+@pytest.mark.parametrize("h,p,g,n", SHAPES)
+def test_scan(name, cu, t, h, p, g, n):
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    for state in (True, False):
+        note(f"scan {name} t{t} h{h} p{p} g{g} n{n} state={state}")
+        c = Case(torch, cu, t, h, p, g, n, state=state, dt="bf16" if state else "f32", param="f32" if state else "bf16")
+        out, last = gdn.ssm_scan(*c.args(), c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0)
+        check(c, out, last, 2 + t // 64)
+        inside = np.zeros(t, bool)
+        for lo, hi in zip(cu, cu[1:]):
+            inside[lo:hi] = True
+        assert not down(out)[~inside].any()
+
+
+@pytest.mark.parametrize("dt,param", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")])
+@pytest.mark.parametrize("r,h,p,g,n", [(1, 1, 64, 1, 64), (3, 6, 64, 3, 128), (5, 4, 128, 2, 64), (40, 24, 64, 1, 128), (2, 5, 128, 1, 128)])
+def test_step(r, h, p, g, n, dt, param):
+    """out is rounded once; a state's element takes one product and one sum, the sum over N elements N + 8."""
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    note(f"step r{r} h{h} p{p} g{g} n{n} {dt} {param}")
+    cu = list(range(r + 1))
+    c = Case(torch, cu, r, h, p, g, n, dt=dt, param=param)
+    ins, S0 = c.numbers()
+    want, want_last = ref.ssm_scan(*ins, cu, S0)
+    x, d, a, B, C, D, bias = ins
+    size, size_last = ref.ssm_scan(np.abs(x), d, a, np.abs(B), np.abs(C), np.abs(D), bias, cu, np.abs(S0))
+    S = c.S0.clone()
+    out = gdn.ssm_step(*c.args(), S, D=c.D, dt_bias=c.bias)
+    assert (np.abs(down(out) - want) <= 2.0 ** -8 * np.abs(want) + 1.01 * (n + 24 + c.exponents()) * U * size).all()
+    assert (np.abs(down(S) - want_last) <= (16 + c.exponents()) * U * size_last).all()
+
+
+def test_steps_follow_the_prompt():
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    r, steps = 3, 70
+    cu = [i * steps for i in range(r + 1)]
+    c = Case(torch, cu, r * steps, 4, 64, 2, 128)
+    want, last = gdn.ssm_scan(*c.args(), c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0)
+    S, rows = c.S0.clone(), torch.arange(r, device="cuda") * steps
+    got = torch.empty_like(want)
+    for i in range(steps):
+        got[rows + i] = gdn.ssm_step(*(v if k == "a" else v[rows + i] for k, v in zip(c.names, c.args())), S, D=c.D, dt_bias=c.bias)
+    assert (S - last).norm() <= 2e-6 * last.norm()
+    assert (got.float() - want.float()).norm() <= 4e-3 * want.float().norm()
+
+
+def test_prompt_in_pieces_is_the_whole_prompt():
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    c = Case(torch, [0, 400], 400, 3, 64, 1, 64, state=False, slow=True)
+    whole, last = gdn.ssm_scan(*c.args(), c.offsets, D=c.D, dt_bias=c.bias)
+    S, got = None, []
+    for lo, hi in ((0, 1), (1, 130), (130, 130), (130, 400)):
+        part = [v if k == "a" else v[lo:hi] for k, v in zip(c.names, c.args())]
+        o, S = gdn.ssm_scan(*part, torch.tensor([0, hi - lo], dtype=torch.int32, device="cuda"), D=c.D, dt_bias=c.bias, S0=S)
+        got.append(o)
+    assert (S - last).norm() <= 2e-6 * last.norm()
+    assert (torch.cat(got).float() - whole.float()).norm() <= 4e-3 * whole.float().norm()

@@ -54,3 +54,30 @@ def test_conv_gradients_are_differences(W, act):
     got, _ = ref.short_conv_bwd(x, w, b, cu, g, st, gl, act)
     for a, v in zip(got, (x, w, b, st)):
         assert np.allclose(a, numeric(loss, v), atol=1e-7)
+
+
+def test_scan_of_a_hand_worked_column():
+    """One head, one state, one channel; softplus(0) = ln 2, so that a = -1 halves the state."""
+    one = np.ones((3, 1, 1))
+    x, dt = np.array([1.0, 2.0, 4.0]).reshape(3, 1, 1), np.zeros((3, 1))
+    out, last = ref.ssm_scan(x, dt, np.array([-1.0]), one, 2 * one, np.array([10.0]), np.zeros(1), [0, 0, 2, 3], np.full((3, 1, 1, 1), 8.0))
+    d = np.log(2.0)
+    S = [4 + d, (4 + d) / 2 + 2 * d, 4 + 4 * d]
+    assert np.allclose(out[:, 0, 0], [2 * S[0] + 10, 2 * S[1] + 20, 2 * S[2] + 40])
+    assert np.allclose(last.reshape(-1), [8, S[1], S[2]])
+
+
+def test_scan_gradients_are_differences():
+    rng = np.random.default_rng(5)
+    H, P, G, N, T, cu = 4, 2, 2, 3, 9, [1, 5, 5, 6, 8]
+    x, dt, B, C, g = (rng.standard_normal(s) for s in ((T, H, P), (T, H), (T, G, N), (T, G, N), (T, H, P)))
+    a, D, bias = -np.exp(rng.standard_normal(H)), rng.standard_normal(H), rng.standard_normal(H)
+    S0, gl = rng.standard_normal((4, H, N, P)), rng.standard_normal((4, H, N, P))
+
+    def loss():
+        out, last = ref.ssm_scan(x, dt, a, B, C, D, bias, cu, S0)
+        return (out * g).sum() + (last * gl).sum()
+
+    got = ref.ssm_scan_bwd(x, dt, a, B, C, D, bias, cu, g, S0, gl)
+    for v, w in zip(got, (x, dt, a, B, C, D, bias, S0)):
+        assert np.allclose(v, numeric(loss, w), atol=2e-7)
