@@ -643,6 +643,35 @@ int gdn_ssm_scan(const void *x, const void *dt, const void *a, const void *B, co
                  void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Gradients of gdn_ssm_scan: of sum(out * grad_out) + sum(S_final * grad_S_final).
+ * The states are computed again inside the call.
+ *
+ *   grad_out, grad_x  [T] rows of H * P bf16 values, their strides apart
+ *   grad_B, grad_C    [T] rows of G * N bf16 values, their strides apart, summed over
+ *              the heads that share them
+ *   grad_dt    [T, H] of dt_dtype
+ *   grad_a, grad_D, grad_dt_bias [H] of param_dtype; the latter two may be NULL
+ *   grad_S_final, grad_S0 [R, H, N, P] float32; may be NULL
+ *
+ * Sums are float32, in a fixed order, and rounded once.  Weights, states and gradients
+ * of states are rounded to bf16 where they enter a product (grad_S0: as states of the
+ * forward are); grad_dt, grad_a and grad_dt_bias, sums of many terms that may cancel,
+ * are as exact as that leaves their terms (2^-8 of each).  Rows in no sequence: as for
+ * the forward.  Workspace: gdn_ssm_scan_bwd_workspace_bytes, scratch on entry and exit,
+ * no clearing needed; it holds two bf16 states for each head and 64 tokens, and for
+ * each head and sequence.
+ */
+size_t gdn_ssm_scan_bwd_workspace_bytes(int T, int R, int H, int P, int G, int N);
+int gdn_ssm_scan_bwd(const void *x, const void *dt, const void *a, const void *B, const void *C, const void *D,
+                     const void *dt_bias, const void *grad_out, const int *cu_seqlens, const float *S0,
+                     const float *grad_S_final, void *grad_x, void *grad_dt, void *grad_a, void *grad_B,
+                     void *grad_C, void *grad_D, void *grad_dt_bias, float *grad_S0, long long x_stride,
+                     long long dt_stride, long long B_stride, long long C_stride, long long grad_out_stride,
+                     long long grad_x_stride, long long grad_B_stride, long long grad_C_stride, int T, int R, int H,
+                     int P, int G, int N, int dtype, int dt_dtype, int param_dtype, int zero_rest, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
  * One token for each of R sequences, in place on their states S [R, H, N, P]
  * float32; x, dt, B, C have R rows.  The state and its sums are float32.
  */

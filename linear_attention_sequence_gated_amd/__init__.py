@@ -11,12 +11,12 @@ from .gdn import (GDN_BF16, GDN_C64, GDN_CACHE_E4M3, GDN_CACHE_I8, GDN_F32, GDN_
                   gdn_chunk_fwd_workspace_bytes, gdn_fwd_channel_decay, gdn_recurrent_step,
                   gdn_rms_norm, gdn_rms_norm_bwd, gdn_rms_norm_bwd_workspace_bytes, gdn_rms_norm_quant, gdn_short_conv,
                   gdn_short_conv_bwd, gdn_short_conv_bwd_workspace_bytes, gdn_short_conv_step,
-                  gdn_ssm_scan, gdn_ssm_scan_workspace_bytes, gdn_ssm_step,
+                  gdn_ssm_scan, gdn_ssm_scan_bwd, gdn_ssm_scan_bwd_workspace_bytes, gdn_ssm_scan_workspace_bytes, gdn_ssm_step,
                   gdn_status_str, load, recurrent_step)
 
 _ATTN = ("attn_decode", "attn_prompt", "attn_prompt_bwd", "block_tables", "cache_append")
 _BLOCK = ("rms_norm", "rms_norm_bwd", "rms_norm_quant", "short_conv", "short_conv_bwd", "short_conv_step",
-          "ssm_scan", "ssm_step")
+          "ssm_scan", "ssm_scan_bwd", "ssm_step")
 
 
 def __getattr__(name):

@@ -311,6 +311,43 @@ def ssm_scan(x, dt, a, B, C, cu_seqlens, D=None, dt_bias=None, S0=None, out=None
     return out, S_final
 
 
+@functools.lru_cache(maxsize=1024)
+def _scan_bwd_workspace(*sizes):
+    return raw.gdn_ssm_scan_bwd_workspace_bytes(*sizes)
+
+
+@_on_stream
+def ssm_scan_bwd(x, dt, a, B, C, grad_out, cu_seqlens, D=None, dt_bias=None, S0=None, grad_S_final=None, grad_x=None,
+                 grad_B=None, grad_C=None):
+    """Gradients of sum(out * grad_out) + sum(S_final * grad_S_final) for ssm_scan's forward, which is computed again.
+
+    Returns (grad_x [T, H, P], grad_dt [T, H], grad_a [H], grad_B, grad_C [T, G, N], grad_D [H] or None without D,
+    grad_dt_bias [H] or None without dt_bias, grad_S0 [R, H, N, P] or None without S0), each of the dtype of what it is the
+    gradient of; grad_B and grad_C are summed over the heads that share them.  grad_x, grad_B and grad_C may be passed in,
+    as parts of one tensor; rows in no sequence are not written then, and hold zeros in gradients that are allocated here.
+    The workspace is allocated here with torch.
+    """
+    dev, ptrs, strides, (t, h, p, g, n), types = _scan_inputs(x, dt, a, B, C, D, dt_bias, "ssm_scan_bwd")
+    r = _sequences(cu_seqlens, dev)
+    gs = _heads(grad_out, "grad_out", (t, h, p), dev)
+    sp = _given(S0, "S0", (r, h, n, p), torch.float32, dev)
+    gsp = _given(grad_S_final, "grad_S_final", (r, h, n, p), torch.float32, dev)
+    zero_rest = grad_x is None and grad_B is None and grad_C is None
+    rows, gstrides = [], []
+    for v, name, shape in ((grad_x, "grad_x", (t, h, p)), (grad_B, "grad_B", (t, g, n)), (grad_C, "grad_C", (t, g, n))):
+        rows.append((x.new_empty if zero_rest else x.new_zeros)(shape) if v is None else v)
+        gstrides.append(shape[1] * shape[2] if v is None else _heads(v, name, shape, dev))
+    grad_dt = dt.new_empty((t, h)) if zero_rest else dt.new_zeros((t, h))
+    grad_a = torch.empty_like(a)
+    grad_D, grad_bias, grad_S0 = (None if v is None else torch.empty_like(v) for v in (D, dt_bias, S0))
+    size = _scan_bwd_workspace(t, r, h, p, g, n)
+    ws = x.new_empty(size // 2)
+    _call(dev, raw.load().gdn_ssm_scan_bwd, *ptrs, grad_out.data_ptr(), cu_seqlens.data_ptr(), sp, gsp, rows[0].data_ptr(),
+          grad_dt.data_ptr(), grad_a.data_ptr(), rows[1].data_ptr(), rows[2].data_ptr(), raw._ptr(grad_D), raw._ptr(grad_bias),
+          raw._ptr(grad_S0), *strides, gs, *gstrides, t, r, h, p, g, n, *types, zero_rest, ws.data_ptr(), size)
+    return rows[0], grad_dt, grad_a, rows[1], rows[2], grad_D, grad_bias, grad_S0
+
+
 @_on_stream
 def ssm_step(x, dt, a, B, C, S, D=None, dt_bias=None, out=None):
     """One token for each of R sequences of ssm_scan: x [R, H, P], dt [R, H], B, C [R, G, N], in place on S [R, H, N, P]

@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libgdn.so")
 PEAK_LIB = os.path.join(PKG, "libgdn_peak.so")
 PEAK_SOURCES = ["peak.hip"]
 SOURCES = ["chunk_fwd.hip", "chunk_pipe.hip", "chunk_two.hip", "chunk_cx.hip", "chunk_bwd.hip", "tok_bwd.hip", "chunk_grad.hip", "channel_decay.hip", "channel_chunk.hip", "decode.hip", "noalloc.hip", "prologue.hip", "cache.hip", "attn_decode.hip", "attn_prompt.hip",
-           "attn_prompt_bwd.hip", "norm.hip", "short_conv.hip", "ssm_scan.hip", "ssm_step.hip",
+           "attn_prompt_bwd.hip", "norm.hip", "short_conv.hip", "ssm_scan.hip", "ssm_scan_bwd.hip", "ssm_step.hip",
            "gdn_api.cpp", "attn_api.cpp", "block_api.cpp"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

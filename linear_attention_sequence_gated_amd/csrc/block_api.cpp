@@ -195,6 +195,39 @@ int gdn_ssm_scan(const void* x, const void* dt, const void* a, const void* B, co
                                       {T, R, H, P, G, N, dt_dtype == GDN_F32, param_dtype == GDN_F32}, zero_rest != 0, stream}));
 }
 
+size_t gdn_ssm_scan_bwd_workspace_bytes(int T, int R, int H, int P, int G, int N) {
+  return scan_shape(T, R, H, P, G, N) ? 0 : gdn::ssm_scan_bwd_workspace_bytes(T, R, H, P, G, N);
+}
+
+int gdn_ssm_scan_bwd(const void* x, const void* dt, const void* a, const void* B, const void* C, const void* D,
+                     const void* dt_bias, const void* grad_out, const int* cu_seqlens, const float* S0,
+                     const float* grad_S_final, void* grad_x, void* grad_dt, void* grad_a, void* grad_B, void* grad_C,
+                     void* grad_D, void* grad_dt_bias, float* grad_S0, long long x_stride, long long dt_stride,
+                     long long B_stride, long long C_stride, long long grad_out_stride, long long grad_x_stride,
+                     long long grad_B_stride, long long grad_C_stride, int T, int R, int H, int P, int G, int N, int dtype,
+                     int dt_dtype, int param_dtype, int zero_rest, void* workspace, size_t workspace_bytes, void* stream) {
+  if (const int s = scan_types(dtype, dt_dtype, param_dtype)) return s;
+  if (const int s = scan_shape(T, R, H, P, G, N)) return s;
+  for (const long long s : {x_stride, grad_out_stride, grad_x_stride})
+    if (!near_ok(s, (long long)H * P)) return GDN_ERR_SHAPE;
+  for (const long long s : {B_stride, C_stride, grad_B_stride, grad_C_stride})
+    if (!near_ok(s, (long long)G * N)) return GDN_ERR_SHAPE;
+  if (dt_stride < H || dt_stride >= (1LL << 32)) return GDN_ERR_SHAPE;
+  if (!a || !cu_seqlens || !grad_a || (T && (!x || !dt || !B || !C || !grad_out || !grad_x || !grad_dt || !grad_B || !grad_C)))
+    return GDN_ERR_NULL;
+  const void* ptrs[] = {x, B, C, grad_out, cu_seqlens, S0, grad_S_final, grad_x, grad_dt, grad_B, grad_C, grad_S0, workspace};
+  if (!all_aligned(ptrs) || !params_aligned({dt}, dt_dtype) ||
+      !params_aligned({a, D, dt_bias, grad_a, grad_D, grad_dt_bias}, param_dtype))
+    return GDN_ERR_ALIGN;
+  const size_t need = gdn::ssm_scan_bwd_workspace_bytes(T, R, H, P, G, N);
+  if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+  return status(gdn::launch_ssm_scan_bwd({x, dt, a, B, C, D, dt_bias, grad_out, cu_seqlens, S0, grad_S_final, grad_x, grad_dt,
+                                          grad_a, grad_B, grad_C, grad_D, grad_dt_bias, grad_S0, workspace, x_stride, dt_stride,
+                                          B_stride, C_stride, grad_out_stride, grad_x_stride, grad_B_stride, grad_C_stride,
+                                          {T, R, H, P, G, N, dt_dtype == GDN_F32, param_dtype == GDN_F32}, zero_rest != 0,
+                                          stream}));
+}
+
 int gdn_ssm_step(const void* x, const void* dt, const void* a, const void* B, const void* C, const void* D,
                  const void* dt_bias, float* S, void* out, long long x_stride, long long dt_stride, long long B_stride,
                  long long C_stride, int R, int H, int P, int G, int N, int dtype, int dt_dtype, int param_dtype,

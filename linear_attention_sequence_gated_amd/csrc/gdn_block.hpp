@@ -121,6 +121,35 @@ struct ScanArgs {
 size_t ssm_scan_workspace_bytes(int T, int H, int P, int G, int N);
 hipError_t launch_ssm_scan(const ScanArgs& a);
 
+struct ScanBwdArgs {
+  const void* x;
+  const void* dt;
+  const void* a;
+  const void* B;
+  const void* C;
+  const void* D;
+  const void* bias;
+  const void* grad_out;
+  const int* cu;
+  const float* S0;
+  const float* grad_S_final;  // may be NULL
+  void* grad_x;
+  void* grad_dt;
+  void* grad_a;
+  void* grad_B;
+  void* grad_C;
+  void* grad_D;     // may be NULL
+  void* grad_bias;  // may be NULL
+  float* grad_S0;   // may be NULL
+  void* ws;
+  long long xs, dts, bs, cs, gs, gxs, gbs, gcs;
+  ScanShape n;
+  bool zero_rest;
+  void* stream;
+};
+size_t ssm_scan_bwd_workspace_bytes(int T, int R, int H, int P, int G, int N);
+hipError_t launch_ssm_scan_bwd(const ScanBwdArgs& a);
+
 struct ScanStepArgs {
   const void* x;
   const void* dt;

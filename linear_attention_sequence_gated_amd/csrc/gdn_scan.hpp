@@ -71,10 +71,14 @@ struct Piece {
   bool first, last;  // of its sequence
 };
 
+// Whose pieces end at multiples of Q as well: a piece of sequence r with rows of the
+// c-th Q then has a number of its own, c + r.
+__device__ __forceinline__ int piece_id(const Piece& p) { return p.row / Q + p.seq; }
+
 // The pieces of rows [s0, s1), in order: of the sequence that goes on into them,
 // if any, then of those that begin in them.  The rows that it gives ascend, and
 // every call ends, whatever cu holds.
-struct Walk {
+template <bool ALIGNED> struct Walk {
   Offsets cu;
   int T, s1, r, rend, beg, pos, end;
   __device__ __forceinline__ void init(const Offsets& c, int R, int T_, int s0, int s1_) {
@@ -94,7 +98,7 @@ struct Walk {
     for (;;) {
       const int e = min(end, s1);
       if (pos < e) {
-        p.row = pos, p.n = min(Q, e - pos), p.seq = r;
+        p.row = pos, p.n = min(ALIGNED ? Q - pos % Q : Q, e - pos), p.seq = r;
         p.first = pos == beg;
         pos += p.n;
         p.last = pos == end;
@@ -103,6 +107,38 @@ struct Walk {
       if (++r >= rend) return false;
       beg = pos = min(max(cu(r), pos), T);
       end = min(max(cu(r + 1), beg), T);
+    }
+  }
+};
+
+// The same pieces from the last to the first, cut at multiples of Q.
+struct WalkBack {
+  Offsets cu;
+  int T, s0, r, rlow, beg, pos, end;
+  __device__ __forceinline__ void take(int top) {  // sequence r, rows below `top`
+    beg = min(max(cu(r), 0), top);
+    end = min(max(cu(r + 1), beg), T);
+    pos = min(end, top);
+  }
+  __device__ __forceinline__ void init(const Offsets& c, int R, int T_, int s0_, int s1) {
+    cu = c, T = T_, s0 = s0_;
+    rlow = max(cu.below(R, s0) - 1, 0);
+    r = cu.below(R, s1) - 1;
+    beg = pos = end = s0;
+    if (r >= rlow) take(s1);
+  }
+  __device__ __forceinline__ bool next(Piece& p) {
+    for (;;) {
+      const int b = max(beg, s0);
+      if (pos > b) {
+        const int row = max(b, (pos - 1) / Q * Q);
+        p.row = row, p.n = pos - row, p.seq = r;
+        p.first = row == beg, p.last = pos == end;
+        pos = row;
+        return true;
+      }
+      if (--r < rlow) return false;
+      take(pos);
     }
   }
 };
@@ -149,6 +185,19 @@ template <int D> __device__ __forceinline__ int col_base_state(int lane) {
   return pipe::row_off<D>(4 * (lane >> 5) + (c >> 2), 16 * ((lane >> 4) & 1) + 8 * (m & 1) + 4 * (m >> 1)) * 2;
 }
 
+// Transposed operands with eight consecutive k to a lane: column 32 t + l % 32 of a
+// staged tile, rows r0 + 8 (l / 32) on (r0 a multiple of 16).
+template <int D> __device__ __forceinline__ int col_base8(int lane) {
+  const int c = lane & 15;
+  return pipe::row_off<D>(8 * (lane >> 5) + (c >> 2), 16 * ((lane >> 4) & 1) + 4 * (c & 3)) * 2;
+}
+template <int D> __device__ __forceinline__ u32x4 col_frag8(const __bf16* lds, int base, int r0, int t) {
+  const char* p = reinterpret_cast<const char*>(lds);
+  const u32x2 a = pipe::ld4_tr(reinterpret_cast<const __bf16*>(p + ((base ^ (64 * t)) + r0 * D * 2)));
+  const u32x2 b = pipe::ld4_tr(reinterpret_cast<const __bf16*>(p + ((base ^ (64 * t) ^ 16) + (r0 + 4) * D * 2)));
+  return pipe::pair(a, b);
+}
+
 // Eight bf16 values (of rows k) times eight numbers w, as PARTS bf16 operands that
 // add up to the products: to 2^-8, 2^-17 and 2^-25 of them.
 template <int PARTS> struct Split {
@@ -184,6 +233,32 @@ template <int NT> __device__ __forceinline__ void store_state(const f32x16 (&S)[
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int e = 0; e < 16; ++e) dst[(long long)(32 * t + state_row(e, lane >> 5)) * P + (lane & 31)] = S[t][e];
+}
+
+// Adds up states of segments along the sequences, [slots][strips][N][64] and behind
+// them [slots][strips] of what each segment keeps of the state before it (log2):
+// kNone where no sequence crosses the slot's border, kFresh where the one that does
+// began (ended) in the segment.  Slot s becomes the state at the border; `back` from
+// the last to the first.
+constexpr float kNone = 1.f, kFresh = 2.f;
+template <int N> __device__ __forceinline__ void join(float* ws, int nstrips, int slots, int strip, int i, bool back) {
+  const ptrdiff_t step = (ptrdiff_t)nstrips * N * 64;
+  const float* kept = ws + slots * step + strip + (back ? (ptrdiff_t)(slots - 1) * nstrips : 0);
+  float* at = ws + (ptrdiff_t)strip * N * 64 + i + (back ? (slots - 1) * step : 0);
+  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < slots; ++s, at += back ? -step : step, kept += back ? -nstrips : nstrips) {
+    const float k = *kept;
+    if (k == kNone) continue;
+    float4 v = *reinterpret_cast<const float4*>(at);
+    if (k != kFresh) {
+      const float f = exp2_(k);
+      v.x = __builtin_fmaf(f, S.x, v.x), v.y = __builtin_fmaf(f, S.y, v.y);
+      v.z = __builtin_fmaf(f, S.z, v.z), v.w = __builtin_fmaf(f, S.w, v.w);
+      *reinterpret_cast<float4*>(at) = v;
+    }
+    S = v;
+  }
 }
 
 }  // namespace scan

@@ -50,12 +50,8 @@ struct ScanParams {
   bool dt_f32, p_f32, zero_rest;
 };
 
-// The workspace: the states of [segments - 1][strips][N][64], then a float for each
-// [segments - 1][strips]: the log2 of what the segment keeps of the state before it,
-// or kNone where no sequence crosses its end, or kFresh where the one that does began
-// in it.
-constexpr float kNone = 1.f, kFresh = 2.f;
-
+// The workspace: the states of [segments - 1][strips][N][64], then what each segment
+// keeps (see join).
 template <int N, bool OUT>
 __global__ __launch_bounds__(kThreads) void scan_kernel(ScanParams p) {
   constexpr int NT = N / 32;
@@ -87,7 +83,7 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(ScanParams p) {
   f32x16 S[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) S[t] = zero16();
-  Walk walk;
+  Walk<false> walk;
   walk.init(cu, p.R, p.T, s0, s1);
   float whole = 0.f;  // log2 of what the segment keeps of a state (not OUT)
   bool fresh = false;
@@ -262,26 +258,8 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(ScanParams p) {
   }
 }
 
-// Adds up along the sequences: slot s becomes the state in front of segment s + 1.
 template <int N> __global__ __launch_bounds__(256) void join_kernel(float* ws, int nstrips, int slots) {
-  const int strip = blockIdx.y, i = (blockIdx.x * 256 + threadIdx.x) * 4;
-  const float* kept = ws + (size_t)slots * nstrips * N * 64 + strip;
-  float* at = ws + (size_t)strip * N * 64 + i;
-  const size_t step = (size_t)nstrips * N * 64;
-  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = 0; s < slots; ++s, at += step, kept += nstrips) {
-    const float k = *kept;
-    if (k == kNone) continue;
-    float4 v = *reinterpret_cast<const float4*>(at);
-    if (k != kFresh) {
-      const float f = exp2_(k);
-      v.x = __builtin_fmaf(f, S.x, v.x), v.y = __builtin_fmaf(f, S.y, v.y);
-      v.z = __builtin_fmaf(f, S.z, v.z), v.w = __builtin_fmaf(f, S.w, v.w);
-      *reinterpret_cast<float4*>(at) = v;
-    }
-    S = v;
-  }
+  join<N>(ws, nstrips, slots, blockIdx.y, (blockIdx.x * 256 + threadIdx.x) * 4, false);
 }
 
 // Rows to a segment: enough workgroups for the CUs, and at least four pieces each.

@@ -31,7 +31,7 @@ EXPORTS = ("gdn_chunk_fwd_workspace_bytes", "gdn_chunk_fwd", "gdn_chunk_fwd_prol
            "gdn_attn_prompt", "gdn_attn_prompt_bwd_workspace_bytes", "gdn_attn_prompt_bwd",
            "gdn_rms_norm", "gdn_rms_norm_quant", "gdn_rms_norm_bwd_workspace_bytes", "gdn_rms_norm_bwd", "gdn_short_conv",
            "gdn_short_conv_bwd_workspace_bytes", "gdn_short_conv_bwd", "gdn_short_conv_step",
-           "gdn_ssm_scan_workspace_bytes", "gdn_ssm_scan", "gdn_ssm_step")
+           "gdn_ssm_scan_workspace_bytes", "gdn_ssm_scan", "gdn_ssm_scan_bwd_workspace_bytes", "gdn_ssm_scan_bwd", "gdn_ssm_step")
 
 _lib = None
 
@@ -105,6 +105,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.gdn_ssm_scan_workspace_bytes.restype = sz
     lib.gdn_ssm_scan.argtypes = [vp] * 11 + [ll] * 4 + [ci] * 10 + [vp, sz, vp]
     lib.gdn_ssm_scan.restype = ci
+    lib.gdn_ssm_scan_bwd_workspace_bytes.argtypes = [ci] * 6
+    lib.gdn_ssm_scan_bwd_workspace_bytes.restype = sz
+    lib.gdn_ssm_scan_bwd.argtypes = [vp] * 19 + [ll] * 8 + [ci] * 10 + [vp, sz, vp]
+    lib.gdn_ssm_scan_bwd.restype = ci
     lib.gdn_ssm_step.argtypes = [vp] * 9 + [ll] * 4 + [ci] * 8 + [vp]
     lib.gdn_ssm_step.restype = ci
     lib.gdn_status_str.argtypes = [ci]
@@ -259,6 +263,20 @@ def gdn_ssm_scan(x, dt, a, B, C, D, dt_bias, cu_seqlens, S0, out, S_final, x_str
     return int(load().gdn_ssm_scan(x, dt, a, B, C, D, dt_bias, cu_seqlens, S0, out, S_final, x_stride, dt_stride, B_stride,
                                    C_stride, T, R, H, P, G, N, dtype, dt_dtype, param_dtype, zero_rest, workspace,
                                    workspace_bytes, stream))
+
+
+def gdn_ssm_scan_bwd_workspace_bytes(T, R, H, P, G, N) -> int:
+    return int(load().gdn_ssm_scan_bwd_workspace_bytes(T, R, H, P, G, N))
+
+
+def gdn_ssm_scan_bwd(x, dt, a, B, C, D, dt_bias, grad_out, cu_seqlens, S0, grad_S_final, grad_x, grad_dt, grad_a, grad_B,
+                     grad_C, grad_D, grad_dt_bias, grad_S0, x_stride, dt_stride, B_stride, C_stride, grad_out_stride,
+                     grad_x_stride, grad_B_stride, grad_C_stride, T, R, H, P, G, N, dtype, dt_dtype, param_dtype, zero_rest,
+                     workspace, workspace_bytes, stream) -> int:
+    return int(load().gdn_ssm_scan_bwd(x, dt, a, B, C, D, dt_bias, grad_out, cu_seqlens, S0, grad_S_final, grad_x, grad_dt,
+                                       grad_a, grad_B, grad_C, grad_D, grad_dt_bias, grad_S0, x_stride, dt_stride, B_stride,
+                                       C_stride, grad_out_stride, grad_x_stride, grad_B_stride, grad_C_stride, T, R, H, P, G,
+                                       N, dtype, dt_dtype, param_dtype, zero_rest, workspace, workspace_bytes, stream))
 
 
 def gdn_ssm_step(x, dt, a, B, C, D, dt_bias, S, out, x_stride, dt_stride, B_stride, C_stride, R, H, P, G, N, dtype,

@@ -149,3 +149,75 @@ def test_prompt_in_pieces_is_the_whole_prompt():
         got.append(o)
     assert (S - last).norm() <= 2e-6 * last.norm()
     assert (torch.cat(got).float() - whole.float()).norm() <= 4e-3 * whole.float().norm()
+
+
+# ------------------------------------------------------------------- gradients
+def gradients(c, g, gl):
+    """The oracle's gradients, and what its recurrence gives for the inputs' magnitudes, whose terms add up."""
+    (x, dt, a, B, C, D, bias), S0 = c.numbers()
+    want = ref.ssm_scan_bwd(x, dt, a, B, C, D, bias, c.cu, g, S0, gl)
+    m = lambda v: None if v is None else np.abs(v)  # noqa: E731
+    size = ref.ssm_scan_bwd(m(x), dt, -np.abs(a), m(B), m(C), m(D), bias, c.cu, m(g), m(S0), m(gl))
+    # of dt and what is summed from it: direct terms and those by the decay have opposite signs there (a < 0)
+    x, B, C, g, S0, gl = m(x), m(B), m(C), m(g), m(S0), m(gl)
+    up = ref.ssm_scan_bwd(x, dt, a, B, C, 0 * D, bias, c.cu, g, S0, gl)
+    z = dt + bias
+    d, sig = ref.softplus(z), 1 / (1 + np.exp(-z))
+    rep = x.shape[1] // B.shape[1]
+    by_x = (up[0] * x).sum(2)  # what d_t multiplies, times d_t: x_t . gx_t
+    direct = by_x / np.maximum(d, 1e-300)
+    by_a = np.abs(up[1] / sig - direct)  # a gg_t
+    size[1] = (direct + by_a) * sig
+    size[6] = size[1].sum(0)
+    size[2] = (by_a / np.abs(a) * d).sum(0)
+    return want, size
+
+
+NAMES = ("x", "dt", "a", "B", "C", "D", "bias", "S0")
+
+
+def check_gradients(c, got, g, gl):
+    """Element by element: a term has a weight or a state rounded to bf16, 2^-8 of it, and for C and B the sum over heads
+    none more; dt's terms have a state rounded in one factor and its gradient in the other at most, 2 2^-8 (the products
+    <Z, S>).  The result is rounded to its type.  S0 is a state (see above).  Normwise: as for out, 4e-3; the parameters'
+    gradients, whose terms cancel, of their terms' size.  dt's terms have random signs here, so that its norm is of the order
+    of the root of their squares' sum, and their independent errors, 2^-8 / sqrt(3) in each of two factors and the result,
+    leave 3.9e-3 of that; three times as much is asked, since a decay takes some terms from the norm."""
+    want, size = gradients(c, g, gl)
+    E = c.exponents()
+    T = c.shape[0]
+    for k, name in enumerate(NAMES):
+        if got[k] is None:
+            continue
+        v = down(got[k]).astype(np.float64)
+        assert v.shape == want[k].shape and np.isfinite(v).all(), name
+        half = 2.0 ** -8 if got[k].dtype.itemsize == 2 else U
+        term = {"S0": 0.0, "D": 0.0, "dt": 2.0 ** -7, "a": 2.0 ** -7, "bias": 2.0 ** -7}.get(name, 2.0 ** -8)
+        chain = 64 + 64 * min(E, 160) + 2 * (T // 64 + 2) if name == "S0" else 384 + 16 * E + T / 64
+        room = half * np.abs(want[k]) + (term + chain * U) * 1.02 * size[k] + 1e-30
+        worst = float((np.abs(v - want[k]) / room).max(initial=0))
+        norm = np.linalg.norm(want[k])
+        rel = np.linalg.norm(v - want[k]) / norm if norm else 0.0
+        of_size = np.linalg.norm(v - want[k]) / max(np.linalg.norm(size[k]), 1e-300)
+        print(f"[parity] {name}: {worst:.3f} of its room, norm {rel:.2e}, of its terms {of_size:.2e}", flush=True)
+        assert worst <= 1, (name, worst)
+        assert (rel if name in ("x", "B", "C", "S0") else of_size) <= 4e-3, (name, rel)
+        assert name != "dt" or rel <= 1.2e-2, (name, rel)
+
+
+@pytest.mark.parametrize("name,cu,t", RUNS, ids=[r[0] for r in RUNS])
+@pytest.mark.parametrize("h,p,g,n", SHAPES)
+def test_scan_gradients(name, cu, t, h, p, g, n):
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    for state in (True, False):
+        note(f"scan gradients {name} t{t} h{h} p{p} g{g} n{n} state={state}")
+        c = Case(torch, cu, t, h, p, g, n, state=state, dt="bf16" if state else "f32", param="f32" if state else "bf16")
+        go = torch.randn(t, h * p + 8, device="cuda", dtype=torch.bfloat16)[:, :h * p].view(t, h, p)
+        gl = torch.randn(len(cu) - 1, h, n, p, device="cuda") if state else None
+        got = gdn.ssm_scan_bwd(*c.args(), go, c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0, grad_S_final=gl)
+        check_gradients(c, got, down(go).astype(np.float64), None if gl is None else down(gl).astype(np.float64))
+        inside = np.zeros(t, bool)
+        for lo, hi in zip(cu, cu[1:]):
+            inside[lo:hi] = True
+        assert not any(down(got[k])[~inside].any() for k in (0, 1, 3, 4))
