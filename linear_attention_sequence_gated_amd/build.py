@@ -32,10 +32,13 @@ CFLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno
 
 # Per-source flags.  channel_chunk.hip rescales its matrix-core accumulators with
 # vector instructions every step; the VGPR form of the MFMA instructions keeps
-# them in VGPRs instead of copying them to and from AGPRs each time.
+# them in VGPRs instead of copying them to and from AGPRs each time; so do the
+# state space scan and its gradients.
 # peak.hip needs the same form for its loop of chained accumulations, or the
 # register allocator shuffles the accumulators through AGPR copies every round.
 EXTRA = {"channel_chunk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "ssm_scan.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "ssm_scan_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "peak.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 

@@ -17,8 +17,17 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// log(1 + e^z), to float32's own precision also where it is small.
-__device__ __forceinline__ float softplus(float z) { return z > 20.f ? z : log1pf(__expf(z)); }
+// log(1 + e^z), to a few units of float32's last place also where it is small: the
+// series of log(1 + e) for e below 1/16, otherwise the logarithm of u = 1 + e with what
+// the sum's rounding lost.
+__device__ __forceinline__ float softplus(float z) {
+  const float e = exp2_(fminf(z, 20.f) * kLog2e), u = 1.f + e;
+  const float large = __builtin_fmaf(__builtin_amdgcn_logf(u), 0.6931471805599453f, (e - (u - 1.f)) * __builtin_amdgcn_rcpf(u));
+  float small = -1.f / 8;
+#pragma unroll
+  for (int n = 7; n; --n) small = __builtin_fmaf(small, e, n % 2 ? 1.f / n : -1.f / n);
+  return z > 20.f ? z : e < 0.0625f ? small * e : large;
+}
 
 // What a row does to the state, in powers of two: steps of less than 2^-160 are
 // taken for that, since 2^-160 of any float32 number is below the smallest; so the
@@ -36,6 +45,38 @@ __host__ __device__ inline Strips strips(int H, int P, int G, int NS) {
   const int per = H / G * (P / 64);
   return {per, (per + NS - 1) / NS};
 }
+
+// ------------------------------------------------------------------- staging
+// Rows of D values to LDS as tile::Stage puts them, one load (of LOADS) at a time.  As
+// assembly: a load to LDS that the compiler knows of makes it wait for all such loads
+// before whatever it reads from LDS next, of another buffer too, so that nothing would
+// run beside them (7 pieces of 64 rows x 4 x 64 channels, N = 128, a workgroup: 66 us
+// for 37).  The load has no result in a register; its arrival is waited for by
+// tile::staged_barrier().  M0, which nothing else here is kept in, is the address in LDS.
+struct Source {
+  u32x4 rsrc;
+};
+__device__ __forceinline__ Source source(const void* base, long long stride, long long r0, int n, int D) {
+  const unsigned long long at = reinterpret_cast<unsigned long long>(static_cast<const __bf16*>(base) + r0 * stride);
+  const unsigned bytes = n > 0 ? (unsigned)((n - 1) * stride + D) * 2u : 0u;
+  return {u32x4{(unsigned)__builtin_amdgcn_readfirstlane((int)at), (unsigned)__builtin_amdgcn_readfirstlane((int)(at >> 32)) & 0xffffu,
+                (unsigned)__builtin_amdgcn_readfirstlane((int)bytes), (unsigned)pipe::kRsrcWord3}};
+}
+template <int D, int N, int NW> struct Stage : tile::Stage<D, N, NW> {
+  typedef tile::Stage<D, N, NW> Base;
+  __device__ __forceinline__ void load_one(__bf16* lds, const Source& src, int wave, int i) const {
+    const unsigned at = (unsigned)__builtin_amdgcn_readfirstlane(
+        (int)(unsigned)(unsigned long long)(tile::lds_void*)(lds + (wave * Base::LOADS + i) * 512));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(at), "v"(Base::off[i]), "s"(src.rsrc)
+                 : "memory");
+  }
+  __device__ __forceinline__ void load(__bf16* lds, const Source& src, int wave) const {
+#pragma unroll
+    for (int i = 0; i < Base::LOADS; ++i) load_one(lds, src, wave, i);
+  }
+};
 
 // ----------------------------------------------------------------- sequences
 // cu[i], in LDS where all of them fit.
@@ -144,12 +185,13 @@ struct WalkBack {
 };
 
 // ------------------------------------------------------------ steps of a piece
-// Of the piece's rows (a lane each), for one head: in LDS, for a wave.
-struct Steps {
+// Of the piece's rows (a lane each), for one head: in LDS, by one wave.
+struct alignas(16) Steps {
   float G[Q];  // sums of the log2 decays up to and including the row
   float u[Q];  // log2(delta) - G
   float v[32];  // delta 2^(G_31 - G) of the first 32
   float w[Q];  // delta 2^(sum of the decays behind the row)
+  float total;  // sum of the log2 decays
 };
 
 __device__ __forceinline__ float dt_at(const void* dt, bool f32, long long i) { return param(dt, f32, i); }
@@ -168,8 +210,10 @@ __device__ __forceinline__ float steps(Steps& s, float z, float a, bool in) {
   s.u[lane] = __builtin_amdgcn_logf(delta) - G;
   if (lane < 32) s.v[lane] = delta * exp2_(G31 - G);
   s.w[lane] = delta * exp2_(lane == 63 ? 0.f : after);
+  const float total = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, G), 63));
+  if (lane == 0) s.total = total;
   pipe::issue_fence();  // read as vectors from here on
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, G), 63));
+  return total;
 }
 
 // ------------------------------------------------------------------- products
@@ -219,20 +263,27 @@ template <int PARTS> struct Split {
   }
 };
 
-// States in memory, [N][P] float32: the part of a wave's 32 columns.
+// States in memory, [N][P] float32: the part of a wave's 32 columns.  Addresses are
+// computed here, not kept in registers over a loop.
 template <int NT> __device__ __forceinline__ void load_state(f32x16 (&S)[NT], const float* src, int P) {
-  const int lane = threadIdx.x & 63;
+  const int lane = tile::fresh(threadIdx.x & 63), step = tile::fresh(P);
+  const float* at = src + (lane >> 5) * 8 * step + (lane & 31);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) S[t][e] = src[(long long)(32 * t + state_row(e, lane >> 5)) * P + (lane & 31)];
+    for (int b = 0; b < 2; ++b, at += 16 * step)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) S[t][8 * b + j] = at[j * step];
 }
 template <int NT> __device__ __forceinline__ void store_state(const f32x16 (&S)[NT], float* dst, int P) {
-  const int lane = threadIdx.x & 63;
+  const int lane = tile::fresh(threadIdx.x & 63), step = tile::fresh(P);
+  float* at = dst + (lane >> 5) * 8 * step + (lane & 31);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) dst[(long long)(32 * t + state_row(e, lane >> 5)) * P + (lane & 31)] = S[t][e];
+    for (int b = 0; b < 2; ++b, at += 16 * step)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) at[j * step] = S[t][8 * b + j];
 }
 
 // Adds up states of segments along the sequences, [slots][strips][N][64] and behind
@@ -246,18 +297,31 @@ template <int N> __device__ __forceinline__ void join(float* ws, int nstrips, in
   const float* kept = ws + slots * step + strip + (back ? (ptrdiff_t)(slots - 1) * nstrips : 0);
   float* at = ws + (ptrdiff_t)strip * N * 64 + i + (back ? (slots - 1) * step : 0);
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = 0; s < slots; ++s, at += back ? -step : step, kept += back ? -nstrips : nstrips) {
-    const float k = *kept;
-    if (k == kNone) continue;
-    float4 v = *reinterpret_cast<const float4*>(at);
-    if (k != kFresh) {
-      const float f = exp2_(k);
-      v.x = __builtin_fmaf(f, S.x, v.x), v.y = __builtin_fmaf(f, S.y, v.y);
-      v.z = __builtin_fmaf(f, S.z, v.z), v.w = __builtin_fmaf(f, S.w, v.w);
-      *reinterpret_cast<float4*>(at) = v;
+  constexpr int U = 8;  // slots whose loads are issued together
+  for (int s0 = 0; s0 < slots; s0 += U) {
+    float k[U];
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      k[u] = kNone;
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s0 + u < slots) {
+        k[u] = kept[u * (back ? -nstrips : nstrips)];
+        v[u] = *reinterpret_cast<const float4*>(at + u * (back ? -step : step));
+      }
     }
-    S = v;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k[u] == kNone) continue;  // what the slot holds is not to be used
+      if (k[u] != kFresh) {
+        const float f = exp2_(k[u]);
+        v[u].x = __builtin_fmaf(f, S.x, v[u].x), v[u].y = __builtin_fmaf(f, S.y, v[u].y);
+        v[u].z = __builtin_fmaf(f, S.z, v[u].z), v[u].w = __builtin_fmaf(f, S.w, v[u].w);
+        *reinterpret_cast<float4*>(at + u * (back ? -step : step)) = v[u];
+      }
+      S = v[u];
+    }
+    at += (back ? -U : U) * step, kept += (back ? -U : U) * nstrips;
   }
 }
 

@@ -28,8 +28,6 @@ using namespace scan;
 using tile::operand;
 using tile::zero16;
 
-constexpr int kStrips = 2;  // strips to a workgroup
-constexpr int kThreads = 128 * kStrips, kWaves = 2 * kStrips;
 constexpr int kParts = 3;
 
 struct ScanParams {
@@ -47,25 +45,30 @@ struct ScanParams {
   float* ws;
   long long xs, dts, bs, cs;
   int T, R, H, P, G, seg, nseg;
-  bool dt_f32, p_f32, zero_rest;
+  bool dt_f32, p_f32, zero_rest, joined;
 };
 
 // The workspace: the states of [segments - 1][strips][N][64], then what each segment
 // keeps (see join).
-template <int N, bool OUT>
-__global__ __launch_bounds__(kThreads) void scan_kernel(ScanParams p) {
-  constexpr int NT = N / 32;
-  constexpr int kTile = Q * N, kX = Q * 128 * (kStrips / 2);
+// Where four values (j a multiple of 4) of a row i of C B^T lie in LDS: 16-byte pieces
+// are moved by the row, so that neither 16 rows' nor 16 pieces' meet in a bank.
+__device__ __forceinline__ int cb_off(int i, int j) { return i * Q + ((j / 4) ^ (i & 15)) * 4; }
+
+template <int N, int NS, bool OUT>
+__global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanParams p) {
+  constexpr int NT = N / 32, kThreads = 128 * NS, kWaves = 2 * NS;
+  constexpr int kTile = Q * N, kX = Q * 64 * NS;
   constexpr int kBuf = (OUT ? 2 : 1) * kTile + kX;
   __shared__ __attribute__((aligned(1024))) __bf16 buf[2][kBuf];
-  __shared__ Steps st_all[kWaves];
+  __shared__ Steps st_all[NS][2];
+  __shared__ __attribute__((aligned(1024))) float cbs[OUT ? Q * Q : 4];  // C B^T: [i][j], see cb_off
+  __shared__ __attribute__((aligned(16))) __bf16 yts[OUT && N == 64 ? NS * 64 * 32 : 8];
   __shared__ int window[kWindow];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, col = lane & 31;
-  Steps& st = st_all[wave];
 
-  const Strips sp = strips(p.H, p.P, p.G, kStrips);
+  const Strips sp = strips(p.H, p.P, p.G, NS);
   const int group = blockIdx.x / sp.sets, set = blockIdx.x % sp.sets, seg = blockIdx.y;
-  const int in_group = set * kStrips, here = min(kStrips, sp.per_group - in_group);
+  const int in_group = set * NS, here = min(NS, sp.per_group - in_group);
   const int strip0 = group * sp.per_group + in_group;
   const bool mine = wave / 2 < here;  // otherwise the wave follows the first strip and writes nothing
   const int strip = strip0 + (mine ? wave / 2 : 0);
@@ -78,7 +81,8 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(ScanParams p) {
   float* const local = p.ws;
   float* const kept = p.ws + (size_t)(p.nseg - 1) * nstrips * N * 64;
   auto state_at = [&](const float* base, int seq) { return base + (((long long)seq * p.H + head) * N) * p.P + hcol; };
-  auto slot = [&](int s) { return local + ((size_t)s * nstrips + strip) * N * 64 + (wave & 1) * 32; };
+  // a slot holds the accumulators as they are, four values of each lane together
+  auto slot = [&](int s) { return reinterpret_cast<f32x4*>(local + ((size_t)s * nstrips + strip) * N * 64 + (wave & 1) * N * 32) + lane; };
 
   f32x16 S[NT];
 #pragma unroll
@@ -87,7 +91,77 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(ScanParams p) {
   walk.init(cu, p.R, p.T, s0, s1);
   float whole = 0.f;  // log2 of what the segment keeps of a state (not OUT)
   bool fresh = false;
+  const bool goes_on = seg && walk.goes_on();
+  if constexpr (!OUT) {
+    // only the sequence that crosses the segment's end
+    const int r = walk.rend - 1;
+    const int b = r >= 0 ? min(max(cu(r), 0), p.T) : p.T, e = r >= 0 ? min(cu(r + 1), p.T) : 0;
+    if (e <= s1 || b >= s1) {
+      if (threadIdx.x < here) kept[(size_t)seg * nstrips + strip0 + threadIdx.x] = kNone;
+      return;
+    }
+    walk.r = r, walk.beg = b, walk.pos = max(b, s0), walk.end = e;
+    fresh = b >= s0;
+  }
+
+  // staging: rows of C, B and x
+  Stage<N, Q, kWaves> sc, sb;
+  Stage<128, Q, kWaves> sx;  // two strips at a time
+  if constexpr (OUT) sc.init(p.cs, wave);
+  sb.init(p.bs, wave);
+  sx.init(p.xs, wave);
+  const __bf16* xg = static_cast<const __bf16*>(p.x) + strip0 * 64;
+  const __bf16* bg = static_cast<const __bf16*>(p.B) + group * N;
+  const __bf16* cg = static_cast<const __bf16*>(p.C) + group * N;
+  // One of the kLoads parts of a piece's staging: they are spread over the work on the piece before, since the loads of
+  // eight waves in a row wait for each other.
+  constexpr int kLx = decltype(sx)::LOADS, kLb = decltype(sb)::LOADS, kLoads = NS / 2 * kLx + (OUT ? 2 : 1) * kLb;
+  auto stage = [&](int b, const Piece& pc, int i) {
+    if (i < NS / 2 * kLx) {
+      const int pair = i / kLx;
+      if (2 * pair < here)
+        sx.load_one(buf[b] + kTile + pair * Q * 128,
+                    source(xg + 128 * pair, p.xs, pc.row, pc.n, 64 * min(2, here - 2 * pair)), wave, i % kLx);
+    } else if (i < NS / 2 * kLx + kLb) {
+      sb.load_one(buf[b], source(bg, p.bs, pc.row, pc.n, N), wave, i - NS / 2 * kLx);
+    } else if (OUT) {
+      sc.load_one(buf[b] + kTile + kX, source(cg, p.cs, pc.row, pc.n, N), wave, i - NS / 2 * kLx - kLb);
+    }
+  };
+  auto raw_dt = [&](const Piece& pc) {
+    return lane < pc.n ? dt_at(p.dt, p.dt_f32, (long long)(pc.row + lane) * p.dts + head) + bias : 0.f;
+  };
+  const int rb = tile::row_base<N>(lane), cb = col_base_state<N>(lane), xb = tile::col_base<128>(lane);
+  const float dskip = OUT && p.D ? param(p.D, p.p_f32, head) : 0.f;
+
+  Piece cur, nxt;
+  bool more = walk.next(cur);
+  float z0 = 0.f;
+  // One wave of a strip computes its steps: waves 0, 3, 5 and 6, one on each SIMD.
+  const bool steps_mine = wave % 2 == ((wave / 2 ^ wave / 4) & 1);
+  if (more) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) stage(0, cur, i);
+    if (steps_mine) z0 = raw_dt(cur);
+  }
   if constexpr (OUT) {
+    if (goes_on) {  // the state at the border, added up here where that was not done before
+      float f = 1.f;
+      for (int k = seg - 1;; --k) {
+        const f32x4* at = slot(k);
+        const float keeps = p.joined ? kFresh : kept[(size_t)k * nstrips + strip];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 v = at[(4 * t + q) * 64];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[t][4 * q + j] = __builtin_fmaf(f, v[j], S[t][4 * q + j]);
+          }
+        if (keeps == kFresh || k == 0) break;
+        f *= exp2_(keeps);
+      }
+    }
     // rows of no sequence, and the states of sequences without rows
     const int lead = p.R ? min(max(cu(0), 0), p.T) : p.T, tail = p.R ? min(max(cu(p.R), 0), p.T) : p.T;
     if (p.zero_rest) {
@@ -109,54 +183,19 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(ScanParams p) {
         for (int n = half; n < N; n += 2) dst[(long long)n * p.P + col] = src ? src[(long long)n * p.P + col] : 0.f;
       }
     }
-    if (seg && walk.goes_on()) load_state<NT>(S, slot(seg - 1), 64);
-  } else {
-    // only the sequence that crosses the segment's end
-    const int r = walk.rend - 1;
-    const int b = r >= 0 ? min(max(cu(r), 0), p.T) : p.T, e = r >= 0 ? min(cu(r + 1), p.T) : 0;
-    if (e <= s1 || b >= s1) {
-      if (threadIdx.x < here) kept[(size_t)seg * nstrips + strip0 + threadIdx.x] = kNone;
-      return;
-    }
-    walk.r = r, walk.beg = b, walk.pos = max(b, s0), walk.end = e;
-    fresh = b >= s0;
   }
-
-  // staging: rows of C, B and x
-  tile::Stage<N, Q, kWaves> sc, sb;
-  tile::Stage<128, Q, kWaves> sx;
-  if constexpr (OUT) sc.init(p.cs, wave);
-  sb.init(p.bs, wave);
-  sx.init(p.xs, wave);
-  const __bf16* xg = static_cast<const __bf16*>(p.x) + strip0 * 64;
-  const __bf16* bg = static_cast<const __bf16*>(p.B) + group * N;
-  const __bf16* cg = static_cast<const __bf16*>(p.C) + group * N;
-  auto stage = [&](int b, const Piece& pc) {
-    if constexpr (OUT) sc.load(buf[b] + kTile + kX, tile::rows_rsrc(cg, p.cs, pc.row, pc.n, N), wave);
-    sb.load(buf[b], tile::rows_rsrc(bg, p.bs, pc.row, pc.n, N), wave);
-    sx.load(buf[b] + kTile, tile::rows_rsrc(xg, p.xs, pc.row, pc.n, 64 * here), wave);
-  };
-  auto raw_dt = [&](const Piece& pc) {
-    return lane < pc.n ? dt_at(p.dt, p.dt_f32, (long long)(pc.row + lane) * p.dts + head) + bias : 0.f;
-  };
-  const int rb = tile::row_base<N>(lane), cb = col_base_state<N>(lane), xb = tile::col_base<128>(lane);
-  const float dskip = OUT && p.D ? param(p.D, p.p_f32, head) : 0.f;
-
-  Piece cur, nxt;
-  bool more = walk.next(cur);
-  float z = 0.f;
-  if (more) {
-    stage(0, cur);
-    z = raw_dt(cur);
-  }
+  if (more && steps_mine) steps(st_all[wave / 2][0], z0, a, lane < cur.n);
   for (int b = 0; more; b ^= 1) {
     tile::staged_barrier();  // this piece's rows are here, and the other buffer is free
     more = walk.next(nxt);
-    float z_next = 0.f;
-    if (more) {
-      stage(b ^ 1, nxt);
-      z_next = raw_dt(nxt);
-    }
+    if (!more) nxt.row = nxt.n = 0;
+    const float z = steps_mine ? raw_dt(nxt) : 0.f;
+    auto stage_some = [&](int part) {  // of four
+      if (more)
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          if (i * 4 / kLoads == part) stage(b ^ 1, nxt, i);
+    };
     if (cur.first) {
       if (p.S0) load_state<NT>(S, state_at(p.S0, cur.seq), p.P);
       else {
@@ -164,95 +203,155 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(ScanParams p) {
         for (int t = 0; t < NT; ++t) S[t] = zero16();
       }
     }
-    const float total = steps(st, z, a, lane < cur.n);
-    whole += total;
-    const __bf16 *Bt = buf[b], *Xt = buf[b] + kTile, *Ct = buf[b] + kTile + kX;
-    const int xcol = wave;  // 32-column block of the tile of x
-    u32x4 xf[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) xf[k] = tile::col_frag<128>(Xt, xb, 16 * k, xcol);
+    const Steps& st = st_all[wave / 2][b];
+    const __bf16 *Bt = buf[b], *Xt = buf[b] + kTile + wave / 4 * Q * 128, *Ct = buf[b] + kTile + kX;
+    const int xcol = wave % 4;  // 32-column block of the pair of strips
 
+    f32x16 y[2] = {zero16(), zero16()};
+    float k0 = 0.f, k1 = 0.f;  // of the lane's two rows
     if constexpr (OUT) {
-      f32x16 y[2] = {zero16(), zero16()}, m[3] = {zero16(), zero16(), zero16()};
+      // C B^T, once for all strips: the ten 16 x 16 blocks at or under the diagonal, rows j by lanes i
+      const int lane = tile::fresh(threadIdx.x & 63);
+#pragma unroll 1
+      for (int tile = kWaves - 1 - wave; tile < 10; tile += kWaves) {
+        const int ib = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, jb = tile - ib * (ib + 1) / 2;
+        f32x4 acc = pipe::zero4();
+#pragma unroll
+        for (int ks = 0; ks < N / 32; ++ks)
+          acc = pipe::mma32(*reinterpret_cast<const u32x4*>(Bt + pipe::row_off<N>(16 * jb + lane % 16, 32 * ks + lane / 16 * 8)),
+                            *reinterpret_cast<const u32x4*>(Ct + pipe::row_off<N>(16 * ib + lane % 16, 32 * ks + lane / 16 * 8)), acc);
+        *reinterpret_cast<f32x4*>(cbs + cb_off(16 * ib + lane % 16, 16 * jb + lane / 16 * 4)) = acc;
+      }
 #pragma unroll
       for (int ks = 0; ks < N / 16; ++ks) {
-        const u32x4 c0 = tile::row_frag<N>(Ct, rb, 0, ks), c1 = tile::row_frag<N>(Ct, rb, 32, ks);
-        const u32x4 b0 = tile::row_frag<N>(Bt, rb, 0, ks), b1 = tile::row_frag<N>(Bt, rb, 32, ks);
         const u32x4 s = operand(S[ks / 2], ks % 2);
-        m[0] = tile::mma(b0, c0, m[0]);
-        m[1] = tile::mma(b0, c1, m[1]);
-        m[2] = tile::mma(b1, c1, m[2]);
-        y[0] = tile::mma(s, c0, y[0]);
-        y[1] = tile::mma(s, c1, y[1]);
+        y[0] = tile::mma(s, tile::row_frag<N>(Ct, rb, 0, ks), y[0]);
+        y[1] = tile::mma(s, tile::row_frag<N>(Ct, rb, 32, ks), y[1]);
       }
-      const float g0 = st.G[col], g1 = st.G[32 + col], g31 = st.G[31];
-      const float k0 = exp2_(g0), k1 = exp2_(g1), off = exp2_(g1 - g31);
+      k0 = st.G[col], k1 = st.G[32 + col];
+      lds_barrier();
+    }
+    auto state = [&] {  // the state behind the piece
+      const float keep = exp2_(st.total);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) y[0][e] *= k0, y[1][e] *= k1;
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 ua = *reinterpret_cast<const float4*>(st.u + 8 * q + 4 * half);
-        const float4 ub = *reinterpret_cast<const float4*>(st.u + 32 + 8 * q + 4 * half);
-        const float4 v = *reinterpret_cast<const float4*>(st.v + 8 * q + 4 * half);
-        const float fa[4] = {ua.x, ua.y, ua.z, ua.w}, fb[4] = {ub.x, ub.y, ub.z, ub.w}, fv[4] = {v.x, v.y, v.z, v.w};
+        for (int e = 0; e < 16; ++e) S[t][e] *= keep;
+      // each 16 rows' operands are read beside the products of the 16 before
+      u32x4 bt[2][NT], xk[2];
+      xk[0] = tile::col_frag<128>(Xt, xb, 0, xcol);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool seen = 8 * q + 4 * half + j <= col;
-          m[0][4 * q + j] *= seen ? exp2_(g0 + fa[j]) : 0.f;
-          m[2][4 * q + j] *= seen ? exp2_(g1 + fb[j]) : 0.f;
-          m[1][4 * q + j] *= off * fv[j];
+      for (int t = 0; t < NT; ++t) bt[0][t] = tile::col_frag<N>(Bt, cb, 0, t);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        Split<kParts> xw;
+        xw.make(xk[k & 1], st.w + 16 * k + 4 * half, st.w + 16 * k + 8 + 4 * half);
+        __builtin_amdgcn_sched_barrier(0);
+        if (k < 3) {
+          xk[(k + 1) & 1] = tile::col_frag<128>(Xt, xb, 16 * (k + 1), xcol);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) bt[(k + 1) & 1][t] = tile::col_frag<N>(Bt, cb, 16 * (k + 1), t);
         }
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) S[t] = tile::mma(bt[k & 1][t], xw.part[q], S[t]);
+        stage_some(k);
+        __builtin_amdgcn_sched_barrier(0);
       }
+    };
+    auto result = [&] {
+      // addresses and masks are computed here, not kept over the loop
+      const int lane = tile::fresh(threadIdx.x & 63), half = lane >> 5, col = lane & 31;
+      const unsigned seen = col < 4 * half ? 0u : 0xffffffffu >> (31 - (col - 4 * half));  // bit 8 q + j: row 8 q + 4 half + j <= col
+      const float g0 = k0, g1 = k1, off = exp2_(g1 - st.G[31]);
+      const float f0 = exp2_(g0), f1 = exp2_(g1);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[0][e] *= f0, y[1][e] *= f1;
+      // the weights of rows: tiles of rows j (elements) by rows i (lanes), 16 rows j at a time, as operands
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        y[0] = tile::mma(xf[k], operand(m[0], k), y[0]);
-        y[1] = tile::mma(xf[k], operand(m[1], k), y[1]);
-        y[1] = tile::mma(xf[2 + k], operand(m[2], k), y[1]);
-      }
-      // y tile: columns are rows of the piece, elements channels 8 q + 4 half + j
+        float f[3][8];
 #pragma unroll
-      for (int it = 0; it < 2; ++it) {
-        const int i = 32 * it + col;
-        if (mine && i < cur.n) {
-          __bf16* o = static_cast<__bf16*>(p.out) + (long long)(cur.row + i) * p.H * p.P + strip * 64 + (wave & 1) * 32 + 4 * half;
+        for (int u = 0; u < 2; ++u) {
+          const int j0 = 16 * k + 8 * u + 4 * half;
+          const float4 ua = *reinterpret_cast<const float4*>(st.u + j0), ub = *reinterpret_cast<const float4*>(st.u + 32 + j0);
+          const float4 v = *reinterpret_cast<const float4*>(st.v + j0);
+          const f32x4 c00 = *reinterpret_cast<const f32x4*>(cbs + cb_off(col, j0));
+          const f32x4 c10 = *reinterpret_cast<const f32x4*>(cbs + cb_off(32 + col, j0));
+          const f32x4 c11 = *reinterpret_cast<const f32x4*>(cbs + cb_off(32 + col, 32 + j0));
+          const float fa[4] = {ua.x, ua.y, ua.z, ua.w}, fb[4] = {ub.x, ub.y, ub.z, ub.w}, fv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const u32x2 xv = pipe::ld4(Xt + pipe::row_off<128>(i, xcol * 32 + 8 * q + 4 * half));
-            u32x2 w;
-            w[0] = pipe::cvt2(__builtin_fmaf(dskip, pipe::lo_f(xv[0]), y[it][4 * q]), __builtin_fmaf(dskip, pipe::hi_f(xv[0]), y[it][4 * q + 1]));
-            w[1] = pipe::cvt2(__builtin_fmaf(dskip, pipe::lo_f(xv[1]), y[it][4 * q + 2]), __builtin_fmaf(dskip, pipe::hi_f(xv[1]), y[it][4 * q + 3]));
-            *reinterpret_cast<u32x2*>(o + 8 * q) = w;
+          for (int j = 0; j < 4; ++j) {
+            // blocks over the diagonal hold anything: left out by bits
+            const int in = (int)(seen << (31 - (8 * (2 * k + u) + j))) >> 31;
+            f[0][4 * u + j] = __builtin_bit_cast(float, __builtin_bit_cast(int, c00[j] * exp2_(g0 + fa[j])) & in);
+            f[1][4 * u + j] = c10[j] * (off * fv[j]);
+            f[2][4 * u + j] = __builtin_bit_cast(float, __builtin_bit_cast(int, c11[j] * exp2_(g1 + fb[j])) & in);
           }
         }
+        u32x4 w[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[i][e] = pipe::cvt2(f[i][2 * e], f[i][2 * e + 1]);
+        const u32x4 x0 = tile::col_frag<128>(Xt, xb, 16 * k, xcol), x1 = tile::col_frag<128>(Xt, xb, 32 + 16 * k, xcol);
+        y[0] = tile::mma(x0, w[0], y[0]);
+        y[1] = tile::mma(x0, w[1], y[1]);
+        y[1] = tile::mma(x1, w[2], y[1]);
+        __builtin_amdgcn_sched_barrier(0);
       }
-    }
-
-    // the state behind the piece
-    const float keep = exp2_(total);
+      // y: columns are rows of the piece, elements channels 8 q + 4 half + j.  Added to D x, and by 32 rows through a part
+      // of LDS that is this wave's alone, where C was, to memory in pieces of 16 bytes.
+      char* const yt = reinterpret_cast<char*>(N == 128 ? const_cast<__bf16*>(Ct) : yts) + wave * 2048;
+      const int hp = p.H * p.P;
+      __bf16* o = static_cast<__bf16*>(p.out) + (long long)(cur.row + lane / 4) * hp + strip * 64 + (wave & 1) * 32 + lane % 4 * 8;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+      for (int it = 0; it < 2; ++it) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) S[t][e] *= keep;
+        for (int q = 0; q < 4; ++q) {
+          const u32x2 xv = pipe::ld4(Xt + pipe::row_off<128>(32 * it + col, xcol * 32 + 8 * q + 4 * half));
+          u32x2 w;
+          w[0] = pipe::cvt2(__builtin_fmaf(dskip, pipe::lo_f(xv[0]), y[it][4 * q]), __builtin_fmaf(dskip, pipe::hi_f(xv[0]), y[it][4 * q + 1]));
+          w[1] = pipe::cvt2(__builtin_fmaf(dskip, pipe::lo_f(xv[1]), y[it][4 * q + 2]), __builtin_fmaf(dskip, pipe::hi_f(xv[1]), y[it][4 * q + 3]));
+          *reinterpret_cast<u32x2*>(yt + col * 64 + ((q ^ (col >> 1 & 3)) * 16 + half * 8)) = w;
+        }
+        pipe::issue_fence();
+        const int left = mine ? cur.n - 32 * it - lane / 4 : 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      Split<kParts> xw;
-      xw.make(xf[k], st.w + 16 * k + 4 * half, st.w + 16 * k + 8 + 4 * half);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const u32x4 bt = tile::col_frag<N>(Bt, cb, 16 * k, t);
-#pragma unroll
-        for (int q = 0; q < kParts; ++q) S[t] = tile::mma(bt, xw.part[q], S[t]);
+        for (int r = 0; r < 2; ++r, o += 16 * hp) {
+          const int row = 16 * r + lane / 4;
+          const u32x4 v = *reinterpret_cast<const u32x4*>(yt + row * 64 + (lane % 4 ^ (row >> 1 & 3)) * 16);
+          if (16 * r < left) *reinterpret_cast<u32x4*>(o) = v;
+        }
+        pipe::issue_fence();
       }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    whole += st.total;
+    // The waves of a SIMD take the two in different orders, so that one's products run beside the other's arithmetic.
+    if constexpr (OUT) {
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        if (i == wave / (kWaves / 2)) result();
+        else state();
+      }
+    } else {
+      state();
     }
+    if (steps_mine) steps(st_all[wave / 2][b ^ 1], z, a, lane < nxt.n);
     if constexpr (OUT) {
       if (cur.last && p.S_final && mine) store_state<NT>(S, const_cast<float*>(state_at(p.S_final, cur.seq)), p.P);
     }
     cur = nxt;
-    z = z_next;
   }
   if constexpr (!OUT) {
     if (mine) {
-      store_state<NT>(S, slot(seg), 64);
+      f32x4* at = slot(seg);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) at[(4 * t + q) * 64] = f32x4{S[t][4 * q], S[t][4 * q + 1], S[t][4 * q + 2], S[t][4 * q + 3]};
       if (threadIdx.x % 128 == 0) kept[(size_t)seg * nstrips + strip] = fresh ? kFresh : whole;
     }
   }
@@ -262,43 +361,59 @@ template <int N> __global__ __launch_bounds__(256) void join_kernel(float* ws, i
   join<N>(ws, nstrips, slots, blockIdx.y, (blockIdx.x * 256 + threadIdx.x) * 4, false);
 }
 
-// Rows to a segment: enough workgroups for the CUs, and at least four pieces each.
-int segment_rows(int T, int H, int P, int G) {
-  const int sets = G * strips(H, P, G, kStrips).sets;
-  const int want = sets >= 256 ? 1 : 256 / sets;
+// How the work is cut.  Strips to a workgroup: four, so that eight waves share C B^T
+// and its operands, where that still leaves a workgroup for every second CU; otherwise
+// two, whose four waves are done sooner.  Rows to a segment: a workgroup to each CU,
+// none waiting, and at least four pieces.
+struct Cut {
+  int ns, sets, seg, nseg;
+};
+Cut cut(int T, int H, int P, int G) {
+  Cut c;
   const int pieces = (T + Q - 1) / Q;
-  int per = (pieces + want - 1) / want;
-  if (per < 4) per = 4;
-  return per * Q;
+  for (c.ns = 4;; c.ns = 2) {
+    c.sets = G * strips(H, P, G, c.ns).sets;
+    const int want = c.sets >= 256 ? 1 : 256 / c.sets;
+    int per = (pieces + want - 1) / want;
+    if (per < 4) per = 4;
+    c.seg = per * Q;
+    c.nseg = T > c.seg ? (T + c.seg - 1) / c.seg : 1;
+    if (c.ns == 2 || (H / G * (P / 64) > 2 && c.sets * c.nseg >= 128)) return c;
+  }
 }
-int segments(int T, int seg) { return T > seg ? (T + seg - 1) / seg : 1; }
+// Whether a launch of its own adds the segments up: a workgroup that does it for itself reads all those before it in its
+// sequence, half of a sequence's on average (8 x 2048 rows in 37 segments, 24 strips: 11 us for the launch).
+bool joins(int T, int R, int seg) { return (long long)T > 8LL * seg * (R > 1 ? R : 1); }
 
 }  // namespace
 
 size_t ssm_scan_workspace_bytes(int T, int H, int P, int G, int N) {
-  const size_t slots = segments(T, segment_rows(T, H, P, G)) - 1, nstrips = (size_t)H * (P / 64);
+  const size_t slots = cut(T, H, P, G).nseg - 1, nstrips = (size_t)H * (P / 64);
   return slots * nstrips * (N * 64 + 1) * sizeof(float);
 }
 
 hipError_t launch_ssm_scan(const ScanArgs& a) {
   hipStream_t st = static_cast<hipStream_t>(a.stream);
   const ScanShape& n = a.n;
-  const int seg = segment_rows(n.T, n.H, n.P, n.G), nseg = segments(n.T, seg);
-  const int sets = n.G * strips(n.H, n.P, n.G, kStrips).sets, nstrips = n.H * (n.P / 64);
+  const Cut c = cut(n.T, n.H, n.P, n.G);
+  const int nseg = c.nseg, nstrips = n.H * (n.P / 64);
   const ScanParams p = {a.x, a.dt, a.a, a.B, a.C, a.D, a.bias, a.cu, a.S0, a.out, a.S_final, a.ws, a.xs, a.dts, a.bs, a.cs,
-                        n.T, n.R, n.H, n.P, n.G, seg, nseg, n.dt_f32, n.p_f32, a.zero_rest};
-  auto go = [&](auto nn) {
-    constexpr int N = decltype(nn)::value;
+                        n.T, n.R, n.H, n.P, n.G, c.seg, nseg, n.dt_f32, n.p_f32, a.zero_rest, joins(n.T, n.R, c.seg)};
+  auto go = [&](auto nn, auto per) {
+    constexpr int N = decltype(nn)::value, NS = decltype(per)::value;
     if (nseg > 1) {
-      hipLaunchKernelGGL((scan_kernel<N, false>), dim3(sets, nseg - 1), dim3(kThreads), 0, st, p);
+      hipLaunchKernelGGL((scan_kernel<N, NS, false>), dim3(c.sets, nseg - 1), dim3(128 * NS), 0, st, p);
       if (const hipError_t e = hipGetLastError()) return e;
-      hipLaunchKernelGGL((join_kernel<N>), dim3(N * 64 / 1024, nstrips), dim3(256), 0, st, a.ws, nstrips, nseg - 1);
-      if (const hipError_t e = hipGetLastError()) return e;
+      if (p.joined) {
+        hipLaunchKernelGGL((join_kernel<N>), dim3(N * 64 / 1024, nstrips), dim3(256), 0, st, a.ws, nstrips, nseg - 1);
+        if (const hipError_t e = hipGetLastError()) return e;
+      }
     }
-    hipLaunchKernelGGL((scan_kernel<N, true>), dim3(sets, nseg), dim3(kThreads), 0, st, p);
+    hipLaunchKernelGGL((scan_kernel<N, NS, true>), dim3(c.sets, nseg), dim3(128 * NS), 0, st, p);
     return hipGetLastError();
   };
-  return n.N == 64 ? go(pipe::ic<64>{}) : go(pipe::ic<128>{});
+  auto sized = [&](auto nn) { return c.ns == 4 ? go(nn, pipe::ic<4>{}) : go(nn, pipe::ic<2>{}); };
+  return n.N == 64 ? sized(pipe::ic<64>{}) : sized(pipe::ic<128>{});
 }
 
 }  // namespace gdn

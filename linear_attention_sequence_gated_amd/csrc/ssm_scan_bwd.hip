@@ -163,16 +163,16 @@ __global__ __launch_bounds__(256) void states_kernel(BwdParams p) {
     load(slot(seg - 1), 64);
   }
 
-  tile::Stage<N, Q, 4> sk;
-  tile::Stage<64, Q, 4> sv;
+  Stage<N, Q, 4> sk;
+  Stage<64, Q, 4> sv;
   const __bf16* kg = (up ? static_cast<const __bf16*>(p.C) : static_cast<const __bf16*>(p.B)) + group * N;
   const __bf16* vg = (up ? static_cast<const __bf16*>(p.go) : static_cast<const __bf16*>(p.x)) + strip * 64;
   const long long ks = up ? p.cs : p.bs, vs = up ? p.gs : p.xs;
   sk.init(ks, wave);
   sv.init(vs, wave);
   auto stage = [&](int b, const Piece& pc) {
-    sk.load(buf[b], tile::rows_rsrc(kg, ks, pc.row, pc.n, N), wave);
-    sv.load(buf[b] + Q * N, tile::rows_rsrc(vg, vs, pc.row, pc.n, 64), wave);
+    sk.load(buf[b], source(kg, ks, pc.row, pc.n, N), wave);
+    sv.load(buf[b] + Q * N, source(vg, vs, pc.row, pc.n, 64), wave);
   };
   auto raw_dt = [&](const Piece& pc) {
     return lane < pc.n ? dt_at(p.dt, p.dt_f32, (long long)(pc.row + lane) * p.dts + head) + bias : 0.f;
@@ -325,9 +325,9 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdParams p) {
     zero(max(tail, c0), c1);
   }
 
-  tile::Stage<N, Q, 4> sc, sb;
-  tile::Stage<64, Q, 4> sx, sh;
-  tile::Stage<64, N, 4> ss;
+  Stage<N, Q, 4> sc, sb;
+  Stage<64, Q, 4> sx, sh;
+  Stage<64, N, 4> ss;
   sc.init(p.cs, wave);
   sb.init(p.bs, wave);
   sx.init(p.xs, wave);
@@ -344,13 +344,13 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdParams p) {
     __syncthreads();  // the piece before is done with its buffers
     auto stage = [&](int b, int strip) {
       const long long at = ((long long)piece_id(pc) * nstrips + strip) * N * 64;
-      ss.load(L.strip[b].S, tile::rows_rsrc(p.states[0] + at, 64, 0, N, 64), wave);
-      ss.load(L.strip[b].Z, tile::rows_rsrc(p.states[1] + at, 64, 0, N, 64), wave);
-      sx.load(L.strip[b].x, tile::rows_rsrc(static_cast<const __bf16*>(p.x) + strip * 64, p.xs, pc.row, pc.n, 64), wave);
-      sh.load(L.strip[b].h, tile::rows_rsrc(static_cast<const __bf16*>(p.go) + strip * 64, p.gs, pc.row, pc.n, 64), wave);
+      ss.load(L.strip[b].S, source(p.states[0] + at, 64, 0, N, 64), wave);
+      ss.load(L.strip[b].Z, source(p.states[1] + at, 64, 0, N, 64), wave);
+      sx.load(L.strip[b].x, source(static_cast<const __bf16*>(p.x) + strip * 64, p.xs, pc.row, pc.n, 64), wave);
+      sh.load(L.strip[b].h, source(static_cast<const __bf16*>(p.go) + strip * 64, p.gs, pc.row, pc.n, 64), wave);
     };
-    sc.load(L.C, tile::rows_rsrc(static_cast<const __bf16*>(p.C) + group * N, p.cs, pc.row, pc.n, N), wave);
-    sb.load(L.B, tile::rows_rsrc(static_cast<const __bf16*>(p.B) + group * N, p.bs, pc.row, pc.n, N), wave);
+    sc.load(L.C, source(static_cast<const __bf16*>(p.C) + group * N, p.cs, pc.row, pc.n, N), wave);
+    sb.load(L.B, source(static_cast<const __bf16*>(p.B) + group * N, p.bs, pc.row, pc.n, N), wave);
     stage(0, strip0);
 
     f32x16 gB[NR], gC[NR], cb = zero16();
