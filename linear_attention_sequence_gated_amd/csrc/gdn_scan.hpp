@@ -64,19 +64,54 @@ __device__ __forceinline__ Source source(const void* base, long long stride, lon
 }
 template <int D, int N, int NW> struct Stage : tile::Stage<D, N, NW> {
   typedef tile::Stage<D, N, NW> Base;
-  __device__ __forceinline__ void load_one(__bf16* lds, const Source& src, int wave, int i) const {
+  // `ahead`: bytes behind src that the loads begin at.
+  __device__ __forceinline__ void load_one(__bf16* lds, const Source& src, int wave, int i, int ahead = 0) const {
     const unsigned at = (unsigned)__builtin_amdgcn_readfirstlane(
         (int)(unsigned)(unsigned long long)(tile::lds_void*)(lds + (wave * Base::LOADS + i) * 512));
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
-                 : "s"(at), "v"(Base::off[i]), "s"(src.rsrc)
+                 : "s"(at), "v"(Base::off[i]), "s"(src.rsrc), "s"(ahead)
                  : "memory");
   }
-  __device__ __forceinline__ void load(__bf16* lds, const Source& src, int wave) const {
+  __device__ __forceinline__ void load(__bf16* lds, const Source& src, int wave, int ahead = 0) const {
 #pragma unroll
-    for (int i = 0; i < Base::LOADS; ++i) load_one(lds, src, wave, i);
+    for (int i = 0; i < Base::LOADS; ++i) load_one(lds, src, wave, i, ahead);
   }
 };
+
+// The same for one wave that loads R rows of 64 values by itself: the swizzle repeats
+// after 16 rows, two loads, so that two offsets serve them all.
+struct Stage64 {
+  unsigned off[2];
+  int step;  // bytes between rows 16 apart
+  __device__ __forceinline__ void init(long long stride) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 8 * i + lane / 8;
+      off[i] = (unsigned)(r * stride * 2) + (pipe::row_off<64>(r, 8 * (lane % 8)) - r * 64) * 2;
+    }
+    step = (int)(stride * 32);
+  }
+  template <int R> __device__ __forceinline__ void load(__bf16* lds, const Source& src, int ahead) const {
+    const unsigned at = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(unsigned long long)(tile::lds_void*)lds);
+#pragma unroll
+    for (int i = 0; i < R / 8; ++i)
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                   :
+                   : "s"(at + i * 1024), "v"(off[i & 1]), "s"(src.rsrc), "s"(ahead + (i >> 1) * step)
+                   : "memory");
+  }
+};
+
+// x, which has arrived when this is reached.  What a load brought has to be asked for
+// before the next loads to LDS are issued: the compiler, which does not know of those,
+// would wait for them too.
+template <class T> __device__ __forceinline__ T arrived(T x) {
+  static_assert(sizeof(T) == 4, "");
+  asm volatile("" : "+v"(x));
+  return x;
+}
 
 // ----------------------------------------------------------------- sequences
 // cu[i], in LDS where all of them fit.
@@ -195,6 +230,11 @@ struct alignas(16) Steps {
 };
 
 __device__ __forceinline__ float dt_at(const void* dt, bool f32, long long i) { return param(dt, f32, i); }
+// The same in two parts, so that nothing waits for the load: its bits, and their number.
+__device__ __forceinline__ unsigned dt_bits(const void* dt, bool f32, long long i) {
+  return f32 ? static_cast<const unsigned*>(dt)[i] : static_cast<const unsigned short*>(dt)[i];
+}
+__device__ __forceinline__ float dt_of(unsigned bits, bool f32) { return number(f32 ? bits : bits << 16); }
 
 // Returns the sum over the piece.  No barrier: the wave reads what it wrote.
 __device__ __forceinline__ float steps(Steps& s, float z, float a, bool in) {

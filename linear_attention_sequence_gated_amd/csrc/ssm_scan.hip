@@ -60,7 +60,7 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
   constexpr int kTile = Q * N, kX = Q * 64 * NS;
   constexpr int kBuf = (OUT ? 2 : 1) * kTile + kX;
   __shared__ __attribute__((aligned(1024))) __bf16 buf[2][kBuf];
-  __shared__ Steps st_all[NS][2];
+  __shared__ Steps st_all[NS];
   __shared__ __attribute__((aligned(1024))) float cbs[OUT ? Q * Q : 4];  // C B^T: [i][j], see cb_off
   __shared__ __attribute__((aligned(16))) __bf16 yts[OUT && N == 64 ? NS * 64 * 32 : 8];
   __shared__ int window[kWindow];
@@ -184,12 +184,13 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
       }
     }
   }
-  if (more && steps_mine) steps(st_all[wave / 2][0], z0, a, lane < cur.n);
+  float z = z0;
   for (int b = 0; more; b ^= 1) {
     tile::staged_barrier();  // this piece's rows are here, and the other buffer is free
+    z = arrived(z);
     more = walk.next(nxt);
     if (!more) nxt.row = nxt.n = 0;
-    const float z = steps_mine ? raw_dt(nxt) : 0.f;
+    const float z_next = steps_mine ? raw_dt(nxt) : 0.f;
     auto stage_some = [&](int part) {  // of four
       if (more)
 #pragma unroll
@@ -203,17 +204,19 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
         for (int t = 0; t < NT; ++t) S[t] = zero16();
       }
     }
-    const Steps& st = st_all[wave / 2][b];
+    Steps& st = st_all[wave / 2];
     const __bf16 *Bt = buf[b], *Xt = buf[b] + kTile + wave / 4 * Q * 128, *Ct = buf[b] + kTile + kX;
     const int xcol = wave % 4;  // 32-column block of the pair of strips
 
+    if (steps_mine) steps(st, z, a, lane < cur.n);
     f32x16 y[2] = {zero16(), zero16()};
     float k0 = 0.f, k1 = 0.f;  // of the lane's two rows
     if constexpr (OUT) {
-      // C B^T, once for all strips: the ten 16 x 16 blocks at or under the diagonal, rows j by lanes i
+      // C B^T, once for all strips: the ten 16 x 16 blocks at or under the diagonal, rows j by lanes i, by the waves that
+      // have no steps to compute
       const int lane = tile::fresh(threadIdx.x & 63);
 #pragma unroll 1
-      for (int tile = kWaves - 1 - wave; tile < 10; tile += kWaves) {
+      for (int tile = steps_mine ? 10 : NS == 4 ? (wave < 3 ? wave - 1 : wave < 7 ? 2 : 3) : wave - 1; tile < 10; tile += NS) {
         const int ib = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, jb = tile - ib * (ib + 1) / 2;
         f32x4 acc = pipe::zero4();
 #pragma unroll
@@ -228,9 +231,9 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
         y[0] = tile::mma(s, tile::row_frag<N>(Ct, rb, 0, ks), y[0]);
         y[1] = tile::mma(s, tile::row_frag<N>(Ct, rb, 32, ks), y[1]);
       }
-      k0 = st.G[col], k1 = st.G[32 + col];
-      lds_barrier();
     }
+    lds_barrier();
+    if constexpr (OUT) k0 = st.G[col], k1 = st.G[32 + col];
     auto state = [&] {  // the state behind the piece
       const float keep = exp2_(st.total);
 #pragma unroll
@@ -339,11 +342,11 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
     } else {
       state();
     }
-    if (steps_mine) steps(st_all[wave / 2][b ^ 1], z, a, lane < nxt.n);
     if constexpr (OUT) {
       if (cur.last && p.S_final && mine) store_state<NT>(S, const_cast<float*>(state_at(p.S_final, cur.seq)), p.P);
     }
     cur = nxt;
+    z = z_next;
   }
   if constexpr (!OUT) {
     if (mine) {

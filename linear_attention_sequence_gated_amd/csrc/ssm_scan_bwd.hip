@@ -189,11 +189,12 @@ __global__ __launch_bounds__(256) void states_kernel(BwdParams p) {
   }
   for (int b = 0; more; b ^= 1) {
     tile::staged_barrier();
+    z = arrived(z);
     more = next(nxt);
     float z_next = 0.f;
     if (more) {
-      stage(b ^ 1, nxt);
       z_next = raw_dt(nxt);
+      stage(b ^ 1, nxt);
     }
     if (up ? cur.last : cur.first) {
       const float* src = up ? p.gSf : p.S0;
@@ -251,50 +252,91 @@ template <int N> __global__ __launch_bounds__(256) void join_both_kernel(float* 
 }
 
 // -------------------------------------------------------------- gradients
-// Sums of 16 elements over the 32 lanes of each half: lane l gets that of element l % 16.
-__device__ __forceinline__ float column_sums(f32x16 v) {
+template <int CTRL> __device__ __forceinline__ float dpp(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+// Sums of four elements over the 16 lanes of a row of lanes: lane l gets that of element l % 4.
+__device__ __forceinline__ float column_sums(const f32x4& v) {
   const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1, n = 8; n; d *= 2, n /= 2) {
-    const bool odd = lane & d;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float mine = odd ? v[2 * i + 1] : v[2 * i], other = odd ? v[2 * i] : v[2 * i + 1];
-      v[i] = mine + __shfl_xor(other, d);
-    }
-  }
-  return v[0] + __shfl_xor(v[0], 16);
+  const bool b0 = lane & 1, b1 = lane & 2;
+  const float p = (b0 ? v[1] : v[0]) + dpp<0xB1>(b0 ? v[0] : v[1]), q = (b0 ? v[3] : v[2]) + dpp<0xB1>(b0 ? v[2] : v[3]);  // quad_perm [1, 0, 3, 2]
+  float r = (b1 ? q : p) + dpp<0x4E>(b1 ? p : q);  // quad_perm [2, 3, 0, 1]
+  r += dpp<0x128>(r);  // row_ror:8
+  return r + dpp<0x124>(r);  // row_ror:4
+}
+// Sum over the four rows of 16 lanes, in each.
+__device__ __forceinline__ float row_sums(float x) {
+  int u = __builtin_bit_cast(int, x), w = u;
+  asm("" : "+v"(w));
+  const auto r = __builtin_amdgcn_permlane16_swap(u, w, false, false);
+  return tile::sum_halves(__builtin_bit_cast(float, (int)r[0]) + __builtin_bit_cast(float, (int)r[1]));
 }
 
 __device__ __forceinline__ float dot2(unsigned a, unsigned b, float c) {
   return __builtin_fmaf(pipe::lo_f(a), pipe::lo_f(b), __builtin_fmaf(pipe::hi_f(a), pipe::hi_f(b), c));
 }
 
+constexpr int kFew = 64;        // offsets kept in LDS; more are read from memory
+constexpr int kMostHeads = 64;  // to a run
+constexpr int kGradWaves = 8, kGradThreads = 64 * kGradWaves;
+constexpr int kBlockWaves = 6, kSteps = 5, kLoads = 6, kSums = 7;  // waves and their parts
+
 template <int N> struct GradLds {
   __bf16 C[Q * N], B[Q * N];
   struct {
     __bf16 S[N * 64], Z[N * 64], x[Q * 64], h[Q * 64];
   } strip[2];
-  __bf16 M[Q * Q], W[Q * Q];  // [i][j]
-  Steps st[4];
-  float er[Q], er1[32], ec[Q], ec1[32], ed[Q], hx[Q];  // sums of E by rows and columns, its diagonal; h.x
-  float R[N / 32][Q], Qs[N / 32][Q], zs[4];
-  int window[kWindow];
+  __bf16 M[Q * Q], W[Q * Q];       // [i][j]
+  Steps st[2];
+  // sums of E over the columns and rows of each 16 x 16 block, its diagonal; h.x; shares of <Z, S>
+  struct {
+    float er[10][16], ec[10][16], ed[Q], hx[Q], zs[kGradWaves], R[N / 32][Q], Qs[N / 32][Q];
+  } sums[2];
+  struct {
+    float a, bias, D;
+  } heads[kMostHeads];  // of the run
+  int window[kFew];
 };
 
+// A workgroup: 64 rows, a run of strips of one group, one after the other, with the
+// next one's operands on their way to LDS.  For each strip, behind a barrier:
+//   - six waves: M, W and the sums of E, in the ten blocks of 16 x 16 at or under the
+//     diagonal (W and M go to LDS as bf16 operands), and the sixth of them the steps of the
+//     next head; the seventh: the next strip's loads; the eighth: the sums by rows of the
+//     strip before;
+//   - each wave: the states' products for a tile of gC and of gB (N = 64: of one of
+//     them), 32 n x 32 rows, which stay in its accumulators over the strips, and of gx,
+//     32 channels x 16 rows;
+//   - behind a second barrier, the products with M and W, and gx to memory.
+// What the latter need of B over all strips is in registers.
 template <int N>
-__global__ __launch_bounds__(256) void grad_kernel(BwdParams p) {
-  constexpr int NR = N == 128 ? 2 : 1;  // tiles of 32 rows to a wave
+__global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
   __shared__ __attribute__((aligned(1024))) GradLds<N> L;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, col = lane & 31;
-  const int nt = N == 128 ? wave : wave & 1, rt0 = N == 128 ? 0 : wave >> 1;
+  const int g16 = lane >> 4, c16 = lane & 15;
+  const int nt = N == 128 ? wave & 3 : wave & 1, rt = N == 128 ? wave >> 2 : (wave >> 1) & 1;
+  const bool do_c = N == 128 || wave < 4, do_b = N == 128 || wave >= 4;
   const int group = blockIdx.y / p.runs, run = blockIdx.y % p.runs;
-  const int spp = p.P / 64, per_group = p.H / p.G * spp, nstrips = p.H * spp;
+  const int shift = p.P / 128, spp = 1 << shift;  // P is 64 or 128
+  const int per_group = p.H / p.G * spp, nstrips = p.H * spp;
   const int strip0 = group * per_group + run * p.run_strips;
   const int strips_here = min(p.run_strips, per_group - run * p.run_strips);
   const int c0 = blockIdx.x * Q, c1 = min(c0 + Q, p.T);
-  Steps& st = L.st[wave];
-  const Offsets cu = offsets<256>(p.cu, p.R, L.window);
+  Offsets cu = {p.cu, nullptr};
+  if (p.R < kFew) {
+    if ((int)threadIdx.x <= p.R) L.window[threadIdx.x] = p.cu[threadIdx.x];
+    cu.window = L.window;
+  }
+  // the blocks over the diagonal that operands of 32 rows reach stay zero
+  for (int i = threadIdx.x; i < 2 * 16 * 2; i += kGradThreads) {
+    const int r = i / 32 * 32 + i / 2 % 16, at = pipe::row_off<64>(r, i / 32 * 32 + 16 + i % 2 * 8);
+    *reinterpret_cast<u32x4*>(L.M + at) = *reinterpret_cast<u32x4*>(L.W + at) = u32x4{0, 0, 0, 0};
+  }
+  for (int i = threadIdx.x; i < strips_here >> shift; i += kGradThreads) {
+    const int head = (strip0 >> shift) + i;
+    L.heads[i] = {param(p.a, p.p_f32, head), p.bias ? param(p.bias, p.p_f32, head) : 0.f, p.D ? param(p.D, p.p_f32, head) : 0.f};
+  }
+  __syncthreads();
 
   const bool one_run = p.runs == 1;
   const long long share = (long long)p.T * p.G * N;
@@ -302,14 +344,14 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdParams p) {
   float* const shareC = shareB + p.runs * share;
   float* const heads = p.heads + (long long)blockIdx.x * p.H * 3;
 
-  {  // rows of no sequence, and the heads' sums
+  {  // rows of no sequence
     const int lead = p.R ? min(max(cu(0), 0), p.T) : p.T, tail = p.R ? min(max(cu(p.R), 0), p.T) : p.T;
     auto zero = [&](int r0, int r1) {
-      for (int r = r0 + (int)(threadIdx.x / 64); r < r1; r += 4) {
+      for (int r = r0 + wave; r < r1; r += kGradWaves) {
         if (p.zero_rest) {
           for (int i = lane; i < strips_here * 8; i += 64)
             *reinterpret_cast<u32x4*>(static_cast<__bf16*>(p.gx) + r * p.gxs + strip0 * 64 + i * 8) = u32x4{0, 0, 0, 0};
-          for (int i = lane; i < strips_here / spp; i += 64) put_param(p.gdt, p.dt_f32, (long long)r * p.H + strip0 / spp + i, 0.f);
+          for (int i = lane; i < (strips_here >> shift); i += 64) put_param(p.gdt, p.dt_f32, (long long)r * p.H + (strip0 >> shift) + i, 0.f);
         }
         for (int i = lane; i < N; i += 64) {
           const long long at = ((long long)r * p.G + group) * N + i;
@@ -325,16 +367,21 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdParams p) {
     zero(max(tail, c0), c1);
   }
 
-  Stage<N, Q, 4> sc, sb;
-  Stage<64, Q, 4> sx, sh;
-  Stage<64, N, 4> ss;
+  Stage<N, Q, kGradWaves> sc, sb;
+  Stage64 sx, sh, ss;
   sc.init(p.cs, wave);
   sb.init(p.bs, wave);
-  sx.init(p.xs, wave);
-  sh.init(p.gs, wave);
-  ss.init(64, wave);
-  const int rbn = tile::row_base<N>(lane), rb64 = tile::row_base<64>(lane);
-  const int cbn = col_base8<N>(lane), cb64 = col_base8<64>(lane);
+  sx.init(p.xs), sh.init(p.gs), ss.init(64);
+  const int rb64 = tile::row_base<64>(lane), cb64 = col_base8<64>(lane), cbn = col_base8<N>(lane);
+  // operands of 16 rows (columns) for the products of 16 x 16 x 32: rows r0 + l % 16, values k0 + 8 (l / 16) on
+  auto rows16 = [&](const __bf16* t, auto d, int r0, int k0) {
+    return *reinterpret_cast<const u32x4*>(t + pipe::row_off<decltype(d)::value>(r0 + c16, k0 + 8 * g16));
+  };
+  // columns n0 + l % 16, rows k0 + 8 (l / 16) on
+  auto cols16 = [&](const __bf16* t, int k0, int n0) {
+    const int r = k0 + 8 * g16 + (c16 >> 2), e = n0 + 4 * (c16 & 3);
+    return pipe::pair(pipe::ld4_tr(t + pipe::row_off<64>(r, e)), pipe::ld4_tr(t + pipe::row_off<64>(r + 4, e)));
+  };
 
   Walk<true> walk;
   walk.init(cu, p.R, p.T, c0, c1);
@@ -342,214 +389,255 @@ __global__ __launch_bounds__(256) void grad_kernel(BwdParams p) {
   bool later = false;  // than the first piece of these rows
   for (; walk.next(pc); later = true) {
     __syncthreads();  // the piece before is done with its buffers
-    auto stage = [&](int b, int strip) {
-      const long long at = ((long long)piece_id(pc) * nstrips + strip) * N * 64;
-      ss.load(L.strip[b].S, source(p.states[0] + at, 64, 0, N, 64), wave);
-      ss.load(L.strip[b].Z, source(p.states[1] + at, 64, 0, N, 64), wave);
-      sx.load(L.strip[b].x, source(static_cast<const __bf16*>(p.x) + strip * 64, p.xs, pc.row, pc.n, 64), wave);
-      sh.load(L.strip[b].h, source(static_cast<const __bf16*>(p.go) + strip * 64, p.gs, pc.row, pc.n, 64), wave);
+    const long long at = ((long long)piece_id(pc) * nstrips + strip0) * N * 64;
+    // all strips of the run: what is ahead counts against the end
+    const Source from_s = source(p.states[0] + at, 64, 0, N * strips_here, 64), from_z = source(p.states[1] + at, 64, 0, N * strips_here, 64);
+    const Source from_x = source(static_cast<const __bf16*>(p.x) + strip0 * 64, p.xs, pc.row, pc.n, 64 * strips_here);
+    const Source from_h = source(static_cast<const __bf16*>(p.go) + strip0 * 64, p.gs, pc.row, pc.n, 64 * strips_here);
+    auto stage = [&](int s) {  // by one wave: others would wait in line with their loads
+      auto& to = L.strip[s & 1];
+      ss.load<N>(to.S, from_s, s * N * 128);
+      ss.load<N>(to.Z, from_z, s * N * 128);
+      sx.load<Q>(to.x, from_x, s * 128);
+      sh.load<Q>(to.h, from_h, s * 128);
     };
     sc.load(L.C, source(static_cast<const __bf16*>(p.C) + group * N, p.cs, pc.row, pc.n, N), wave);
     sb.load(L.B, source(static_cast<const __bf16*>(p.B) + group * N, p.bs, pc.row, pc.n, N), wave);
-    stage(0, strip0);
+    if (wave == kLoads) stage(0);
 
-    f32x16 gB[NR], gC[NR], cb = zero16();
+    // dt of the rows, a lane each: of the present and the next head (sums), of the next and the one behind that (steps)
+    auto ask = [&](int head) {
+      head = min(head, (strip0 + strips_here - 1) >> shift);
+      return lane < pc.n ? dt_bits(p.dt, p.dt_f32, (long long)(pc.row + lane) * p.dts + head) : 0u;
+    };
+    auto z_of = [&](unsigned bits, int head) { return dt_of(bits, p.dt_f32) + L.heads[head - (strip0 >> shift)].bias; };
+    auto a_of = [&](int head) { return L.heads[head - (strip0 >> shift)].a; };
+    unsigned now = 0, next = 0;
+    float total = 0.f;  // log2 of what the rows keep of a state, of the strip before
+    float sum_a = 0.f, sum_q = 0.f, sum_d = 0.f, sum_k = 0.f, sum_hx = 0.f;  // of its rows, over the strips of a head
+    // Sums by rows of a strip, a lane each, when all of its parts are there.
+    auto by_rows = [&](int s) {
+      const int strip = strip0 + s, head = strip >> shift;
+      const auto& u = L.sums[s & 1];
+      if ((strip & (spp - 1)) == 0) sum_a = sum_q = sum_d = sum_k = sum_hx = 0.f;
+      float r = 0.f, q = 0.f, er = 0.f, ec = 0.f;
 #pragma unroll
-    for (int t = 0; t < NR; ++t) gB[t] = gC[t] = zero16();
-    // tiles of the triangle: (rows i, rows j) of wave 0, 1, 2: (0, 0), (1, 1), (1, 0)
-    const int it = wave == 0 ? 0 : 1, jt = wave == 1 ? 1 : 0;
-    // of wave 3's rows, over the strips of a head
-    float z = 0.f, a = 0.f, total = 0.f, sum_a = 0.f, sum_q = 0.f, sum_d = 0.f, sum_k = 0.f, sum_hx = 0.f;
+      for (int i = 0; i < N / 32; ++i) r += u.R[i][lane], q += u.Qs[i][lane];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i <= g16) er += u.er[g16 * (g16 + 1) / 2 + i][c16];
+        if (i >= g16) ec += u.ec[i * (i + 1) / 2 + g16][c16];
+      }
+      sum_a += (er - ec) + r;
+      sum_q += q;
+      sum_d += ec + u.ed[lane] + q;
+#pragma unroll
+      for (int i = 0; i < kGradWaves; ++i) sum_k += u.zs[i];
+      sum_hx += u.hx[lane];
+      if ((strip & (spp - 1)) == spp - 1) {
+        const float behind = __shfl(pipe::wave_prefix_sum(__shfl(sum_a, 63 - lane)), 63 - lane);
+        const float upto = __shfl(pipe::wave_prefix_sum(sum_q), (lane + 63) & 63);
+        const float gg = behind + (lane ? upto : 0.f) + exp2_(total) * sum_k;
+        const float z = z_of(now, head), a = a_of(head), delta = softplus(z), sig = logistic(z);
+        const bool in = lane < pc.n;
+        const float gz = in ? (delta > 0.f ? sum_d * (sig / delta) : 0.f) + a * gg * sig : 0.f;
+        if (in) put_param(p.gdt, p.dt_f32, (long long)(pc.row + lane) * p.H + head, gz);
+        const float ga = wave_sum(in ? gg * delta : 0.f), gD = wave_sum(in ? sum_hx : 0.f), gb = wave_sum(gz);
+        if (lane == 0) {
+          float* o = heads + head * 3;
+          o[0] = later ? o[0] + ga : ga, o[1] = later ? o[1] + gD : gD, o[2] = later ? o[2] + gb : gb;
+        }
+      }
+    };
+    const int head0 = strip0 >> shift;
+    if (wave == kSums) {
+      now = ask(head0), next = ask(head0 + 1);
+    } else if (wave == kSteps) {
+      const unsigned first = ask(head0);
+      now = ask(head0 + 1), next = ask(head0 + 2);
+      steps(L.st[0], z_of(first, head0), a_of(head0), lane < pc.n);
+    }
+
+    f32x16 gB = zero16(), gC = zero16();
+    f32x4 cb[2];        // C B^T of the wave's blocks
+    u32x4 bt[4];        // columns of B, transposed
 
     for (int s = 0; s < strips_here; ++s) {
-      const int strip = strip0 + s, head = strip / spp, b = s & 1;
+      const int strip = strip0 + s, head = strip >> shift, b = s & 1;
       tile::staged_barrier();
-      if (s + 1 < strips_here) stage(b ^ 1, strip + 1);
-      if (strip % spp == 0) {
-        a = param(p.a, p.p_f32, head);
-        z = lane < pc.n ? dt_at(p.dt, p.dt_f32, (long long)(pc.row + lane) * p.dts + head) + (p.bias ? param(p.bias, p.p_f32, head) : 0.f) : 0.f;
-        total = steps(st, z, a, lane < pc.n);
-        sum_a = sum_q = sum_d = sum_k = sum_hx = 0.f;
-      }
+      now = arrived(now), next = arrived(next);
+      unsigned after = next;
+      if (wave == kSums ? s && (strip & (spp - 1)) == 0 : wave == kSteps && ((strip + 1) & (spp - 1)) == 0)
+        after = ask(wave == kSums ? head + 1 : head + 3);
+      if (wave == kLoads && s + 1 < strips_here) stage(s + 1);
+      const Steps& st = L.st[(head - (strip0 >> shift)) & 1];
       const __bf16 *St = L.strip[b].S, *Zt = L.strip[b].Z, *Xt = L.strip[b].x, *Ht = L.strip[b].h;
-      if (s == 0 && wave < 3) {
+      auto& sums = L.sums[b];
+      if (s == 0) {
 #pragma unroll
-        for (int k = 0; k < N / 16; ++k)
-          cb = tile::mma(tile::row_frag<N>(L.B, rbn, 32 * jt, k), tile::row_frag<N>(L.C, rbn, 32 * it, k), cb);
+        for (int k = 0; k < 4; ++k) bt[k] = col_frag8<N>(L.B, cbn, 16 * k, nt);
       }
-      // M, W and the sums of E: tiles with rows j as elements, rows i as lanes
-      if (wave < 3) {
-        f32x16 w = zero16(), m = cb, e;
+      if (wave < kBlockWaves) {
+        // blocks: rows j as elements 4 g16 + r, rows i as lanes
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          w = tile::mma(tile::row_frag<64>(Xt, rb64, 32 * jt, k), tile::row_frag<64>(Ht, rb64, 32 * it, k), w);
-        const float gi = st.G[32 * it + col], off = exp2_(gi - st.G[31]);
-        float row = 0.f, diag = 0.f, hx = 0.f;
+        for (int n = 0; n < 2; ++n) {
+          const int t = wave + n * kBlockWaves;
+          if (t >= 10) continue;
+          const int ib = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jb = t - ib * (ib + 1) / 2;
+          if (s == 0) {
+            cb[n] = pipe::zero4();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 f4 = *reinterpret_cast<const float4*>((wave == 2 ? st.v : st.u + 32 * jt) + 8 * q + 4 * half);
-          const float f[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int i = 4 * q + j, at = 8 * q + 4 * half + j;
-            const float l = wave == 2 ? off * f[j] : at <= col ? exp2_(gi + f[j]) : 0.f;
-            m[i] *= l;
-            const float x = w[i] * m[i];
-            if (wave < 2) {
-              if (at == col) diag += x, hx += w[i];
-              e[i] = at < col ? x : 0.f;
-            } else {
-              e[i] = x;
-            }
-            row += e[i];
-            w[i] *= l;
+            for (int k = 0; k < N / 32; ++k)
+              cb[n] = pipe::mma32(rows16(L.B, pipe::ic<N>{}, 16 * jb, 32 * k), rows16(L.C, pipe::ic<N>{}, 16 * ib, 32 * k), cb[n]);
           }
-          *reinterpret_cast<u32x2*>(L.M + pipe::row_off<64>(32 * it + col, 32 * jt + 8 * q + 4 * half)) =
-              u32x2{pipe::cvt2(m[4 * q], m[4 * q + 1]), pipe::cvt2(m[4 * q + 2], m[4 * q + 3])};
-          *reinterpret_cast<u32x2*>(L.W + pipe::row_off<64>(32 * it + col, 32 * jt + 8 * q + 4 * half)) =
-              u32x2{pipe::cvt2(w[4 * q], w[4 * q + 1]), pipe::cvt2(w[4 * q + 2], w[4 * q + 3])};
+          f32x4 w = pipe::zero4(), m, e;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            w = pipe::mma32(rows16(Xt, pipe::ic<64>{}, 16 * jb, 32 * k), rows16(Ht, pipe::ic<64>{}, 16 * ib, 32 * k), w);
+          const float gi = st.G[16 * ib + c16];
+          const float4 u4 = *reinterpret_cast<const float4*>(st.u + 16 * jb + 4 * g16);
+          const float u[4] = {u4.x, u4.y, u4.z, u4.w};
+          float row = 0.f;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int j = ib == jb ? 4 * g16 + r : 0;  // against lane c16 where rows i and j are the same ones
+            const float l = ib != jb || j <= c16 ? exp2_(gi + u[r]) : 0.f;
+            m[r] = cb[n][r] * l;
+            const float x = w[r] * m[r];
+            e[r] = ib != jb || j < c16 ? x : 0.f;
+            if (ib == jb && j == c16) sums.ed[16 * ib + c16] = x, sums.hx[16 * ib + c16] = w[r];
+            row += e[r];
+            w[r] *= l;
+          }
+          const int at = pipe::row_off<64>(16 * ib + c16, 16 * jb + 4 * g16);
+          *reinterpret_cast<u32x2*>(L.M + at) = pipe::cvt4(m);
+          *reinterpret_cast<u32x2*>(L.W + at) = pipe::cvt4(w);
+          row = row_sums(row);
+          const float column = column_sums(e);
+          if (g16 == 0) sums.er[t][c16] = row;
+          if (c16 < 4) sums.ec[t][4 * g16 + c16] = column;
         }
-        row = tile::sum_halves(row);
-        const float column = column_sums(e);
-        const int ej = 8 * ((lane & 15) / 4) + 4 * half + (lane & 3);
-        if (wave < 2) {
-          diag = tile::sum_halves(diag), hx = tile::sum_halves(hx);
-          if (half == 0) L.er[32 * it + col] = row, L.ed[32 * it + col] = diag, L.hx[32 * it + col] = hx;
-          if (col < 16) L.ec[32 * jt + ej] = column;
-        } else {
-          if (half == 0) L.er1[col] = row;
-          if (col < 16) L.ec1[ej] = column;
+      } else if (wave == kSums) {
+        if (s) {
+          by_rows(s - 1);
+          if ((strip & (spp - 1)) == 0) now = next, next = after;
         }
+        total = st.total;
+      }
+      if (wave == kSteps && ((strip + 1) & (spp - 1)) == 0 && s + 1 < strips_here) {
+        steps(L.st[(head + 1 - (strip0 >> shift)) & 1], z_of(now, head + 1), a_of(head + 1), lane < pc.n);
+        now = next, next = after;
       }
       {  // <Z, S>
         float dot = 0.f;
         const u32x4* s4 = reinterpret_cast<const u32x4*>(St) + threadIdx.x;
         const u32x4* z4 = reinterpret_cast<const u32x4*>(Zt) + threadIdx.x;
 #pragma unroll
-        for (int i = 0; i < N * 64 / 8 / 256; ++i) {
-          const u32x4 u = s4[i * 256], v = z4[i * 256];
+        for (int i = 0; i < N * 64 / 8 / kGradThreads; ++i) {
+          const u32x4 u = s4[i * kGradThreads], v = z4[i * kGradThreads];
 #pragma unroll
           for (int e = 0; e < 4; ++e) dot = dot2(u[e], v[e], dot);
         }
         dot = wave_sum(dot);
-        if (lane == 0) L.zs[wave] = dot;
+        if (lane == 0) sums.zs[wave] = dot;
       }
-      lds_barrier();
-
-      // gC and gB: tiles of n by rows
+      const int pt = wave & 1, rb = wave >> 1;
+      f32x4 u[2] = {pipe::zero4(), pipe::zero4()};
+      {  // gx: 32 channels by 16 rows, as two tiles of 16
 #pragma unroll
-      for (int t = 0; t < NR; ++t) {
-        const int rt = rt0 + t, row = 32 * rt + col;
-        f32x16 uc = zero16(), ub = zero16();
+        for (int k = 0; k < N / 32; ++k) {
+          const u32x4 rows = rows16(L.B, pipe::ic<N>{}, 16 * rb, 32 * k);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uc = tile::mma(tile::row_frag<64>(St, rb64, 32 * nt, k), tile::row_frag<64>(Ht, rb64, 32 * rt, k), uc);
-          ub = tile::mma(tile::row_frag<64>(Zt, rb64, 32 * nt, k), tile::row_frag<64>(Xt, rb64, 32 * rt, k), ub);
+          for (int i = 0; i < 2; ++i) u[i] = pipe::mma32(cols16(Zt, 32 * k, 32 * pt + 16 * i), rows, u[i]);
         }
-        const float kc = exp2_(st.G[row]), kb = st.w[row];
-        float r = 0.f, q = 0.f;
+        const float kb = st.w[16 * rb + c16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int at = pipe::row_off<N>(row, 32 * nt + 8 * i + 4 * half);
-          const u32x2 cv = pipe::ld4(L.C + at), bv = pipe::ld4(L.B + at);
-          const float cf[4] = {pipe::lo_f(cv[0]), pipe::hi_f(cv[0]), pipe::lo_f(cv[1]), pipe::hi_f(cv[1])};
-          const float bf[4] = {pipe::lo_f(bv[0]), pipe::hi_f(bv[0]), pipe::lo_f(bv[1]), pipe::hi_f(bv[1])};
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float vc = uc[4 * i + j] * kc, vb = ub[4 * i + j] * kb;
-            r = __builtin_fmaf(vc, cf[j], r);
-            q = __builtin_fmaf(vb, bf[j], q);
-            gC[t][4 * i + j] += vc;
-            gB[t][4 * i + j] += vb;
-          }
-        }
-        r = tile::sum_halves(r), q = tile::sum_halves(q);
-        if (half == 0) L.R[nt][row] = r, L.Qs[nt][row] = q;
-        // gC_i += sum over j <= i;  gB_j += sum over i >= j
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k < 2 * rt + 2)
-            gC[t] = tile::mma(col_frag8<N>(L.B, cbn, 16 * k, nt), tile::row_frag<64>(L.W, rb64, 32 * rt, k), gC[t]);
-          if (k >= 2 * rt)
-            gB[t] = tile::mma(col_frag8<N>(L.C, cbn, 16 * k, nt), col_frag8<64>(L.W, cb64, 16 * k, rt), gB[t]);
-        }
+          for (int e = 0; e < 4; ++e) u[i][e] *= kb;
       }
-      {  // gx: a wave's tile of 32 channels by 32 rows
-        const int pt = wave & 1, rt = wave >> 1, row = 32 * rt + col;
+      // gC and gB: elements n, lanes rows
+      const int row = 32 * rt + col;
+      auto inter = [&](f32x16& acc, const __bf16* states, const __bf16* rows, float scale, const __bf16* with, float* out) {
         f32x16 u = zero16();
 #pragma unroll
-        for (int k = 0; k < N / 16; ++k)
-          u = tile::mma(col_frag8<64>(Zt, cb64, 16 * k, pt), tile::row_frag<N>(L.B, rbn, 32 * rt, k), u);
-        const float kb = st.w[row], dskip = p.D ? param(p.D, p.p_f32, head) : 0.f;
+        for (int k = 0; k < 4; ++k)
+          u = tile::mma(tile::row_frag<64>(states, rb64, 32 * nt, k), tile::row_frag<64>(rows, rb64, 32 * rt, k), u);
+        float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) u[e] *= kb;
+        for (int i = 0; i < 4; ++i) {
+          const u32x2 v = pipe::ld4(with + pipe::row_off<N>(row, 32 * nt + 8 * i + 4 * half));
+          const float f[4] = {pipe::lo_f(v[0]), pipe::hi_f(v[0]), pipe::lo_f(v[1]), pipe::hi_f(v[1])};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sum = __builtin_fmaf(u[4 * i + j], f[j], sum);
+            acc[4 * i + j] = __builtin_fmaf(u[4 * i + j], scale, acc[4 * i + j]);
+          }
+        }
+        sum = tile::sum_halves(sum) * scale;
+        if (half == 0) out[row] = sum;
+      };
+      if (do_c) inter(gC, St, Ht, exp2_(st.G[row]), L.C, sums.R[nt]);
+      if (do_b) inter(gB, Zt, Xt, st.w[row], L.B, sums.Qs[nt]);
+      lds_barrier();
+
+      {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (k >= rb / 2) {
+            const u32x4 m = cols16(L.M, 32 * k, 16 * rb);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) u[i] = pipe::mma32(cols16(Ht, 32 * k, 32 * pt + 16 * i), m, u[i]);
+          }
+        const float dskip = L.heads[head - (strip0 >> shift)].D;
+        __bf16* const mine = L.strip[b].S + wave * 512;  // S has been used: on the way to memory
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const u32x2 hv = pipe::ld4(Ht + pipe::row_off<64>(16 * rb + c16, 32 * pt + 16 * i + 4 * g16));
+          u32x2 w;
+          w[0] = pipe::cvt2(__builtin_fmaf(dskip, pipe::lo_f(hv[0]), u[i][0]), __builtin_fmaf(dskip, pipe::hi_f(hv[0]), u[i][1]));
+          w[1] = pipe::cvt2(__builtin_fmaf(dskip, pipe::lo_f(hv[1]), u[i][2]), __builtin_fmaf(dskip, pipe::hi_f(hv[1]), u[i][3]));
+          *reinterpret_cast<u32x2*>(mine + c16 * 32 + 16 * i + 4 * g16) = w;
+        }
+        pipe::issue_fence();
+        const int row = 16 * rb + lane / 4;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(mine + lane * 8);
+        if (row < pc.n)
+          *reinterpret_cast<u32x4*>(static_cast<__bf16*>(p.gx) + (long long)(pc.row + row) * p.gxs + strip * 64 + 32 * pt + lane % 4 * 8) = v;
+      }
+      if (do_c)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (k >= 2 * rt) u = tile::mma(col_frag8<64>(Ht, cb64, 16 * k, pt), col_frag8<64>(L.M, cb64, 16 * k, rt), u);
-        if (row < pc.n) {
-          __bf16* o = static_cast<__bf16*>(p.gx) + (long long)(pc.row + row) * p.gxs + strip * 64 + 32 * pt + 4 * half;
+          if (k < 2 * rt + 2) gC = tile::mma(bt[k], tile::row_frag<64>(L.W, rb64, 32 * rt, k), gC);
+      if (do_b)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const u32x2 hv = pipe::ld4(Ht + pipe::row_off<64>(row, 32 * pt + 8 * q + 4 * half));
-            u32x2 w;
-            w[0] = pipe::cvt2(__builtin_fmaf(dskip, pipe::lo_f(hv[0]), u[4 * q]), __builtin_fmaf(dskip, pipe::hi_f(hv[0]), u[4 * q + 1]));
-            w[1] = pipe::cvt2(__builtin_fmaf(dskip, pipe::lo_f(hv[1]), u[4 * q + 2]), __builtin_fmaf(dskip, pipe::hi_f(hv[1]), u[4 * q + 3]));
-            *reinterpret_cast<u32x2*>(o + 8 * q) = w;
-          }
-        }
-      }
-      lds_barrier();
-      if (wave == 3) {  // sums by rows, a lane each; the next strip's are written behind the next barrier
-        float r = 0.f, q = 0.f;
-#pragma unroll
-        for (int i = 0; i < N / 32; ++i) r += L.R[i][lane], q += L.Qs[i][lane];
-        const float er = L.er[lane] + (lane >= 32 ? L.er1[lane & 31] : 0.f);
-        const float ec = L.ec[lane] + (lane < 32 ? L.ec1[lane & 31] : 0.f);
-        sum_a += (er - ec) + r;
-        sum_q += q;
-        sum_d += ec + L.ed[lane] + q;
-        sum_k += L.zs[0] + L.zs[1] + L.zs[2] + L.zs[3];
-        sum_hx += L.hx[lane];
-        if (strip % spp == spp - 1) {
-          const float behind = __shfl(pipe::wave_prefix_sum(__shfl(sum_a, 63 - lane)), 63 - lane);
-          const float upto = __shfl(pipe::wave_prefix_sum(sum_q), (lane + 63) & 63);
-          const float gg = behind + (lane ? upto : 0.f) + exp2_(total) * sum_k;
-          const float delta = softplus(z), sig = logistic(z);
-          const bool in = lane < pc.n;
-          const float gz = in ? (delta > 0.f ? sum_d * (sig / delta) : 0.f) + a * gg * sig : 0.f;
-          if (in) put_param(p.gdt, p.dt_f32, (long long)(pc.row + lane) * p.H + head, gz);
-          const float ga = wave_sum(in ? gg * delta : 0.f), gD = wave_sum(in ? sum_hx : 0.f), gb = wave_sum(gz);
-          if (lane == 0) {
-            float* o = heads + head * 3;
-            o[0] = later ? o[0] + ga : ga, o[1] = later ? o[1] + gD : gD, o[2] = later ? o[2] + gb : gb;
-          }
-        }
-      }
+        for (int k = 0; k < 4; ++k)
+          if (k >= 2 * rt) gB = tile::mma(col_frag8<N>(L.C, cbn, 16 * k, nt), col_frag8<64>(L.W, cb64, 16 * k, rt), gB);
     }
+    lds_barrier();
+    if (wave == kSums) by_rows(strips_here - 1);
+
     // gB and gC: lanes are rows, elements n = 32 nt + 8 q + 4 half + j
-#pragma unroll
-    for (int t = 0; t < NR; ++t) {
-      const int row = 32 * (rt0 + t) + col;
-      if (row >= pc.n) continue;
+    const int row = 32 * rt + col;
+    if (row < pc.n) {
       const long long r = pc.row + row;
       const int n = group * N + 32 * nt + 4 * half;
+      auto put = [&](const f32x16& v, void* rows, long long stride, float* shares) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (one_run) {
-          *reinterpret_cast<u32x2*>(static_cast<__bf16*>(p.gB) + r * p.gbs + n + 8 * q) =
-              u32x2{pipe::cvt2(gB[t][4 * q], gB[t][4 * q + 1]), pipe::cvt2(gB[t][4 * q + 2], gB[t][4 * q + 3])};
-          *reinterpret_cast<u32x2*>(static_cast<__bf16*>(p.gC) + r * p.gcs + n + 8 * q) =
-              u32x2{pipe::cvt2(gC[t][4 * q], gC[t][4 * q + 1]), pipe::cvt2(gC[t][4 * q + 2], gC[t][4 * q + 3])};
-        } else {
-          const long long at = r * p.G * N + n + 8 * q;
-          *reinterpret_cast<float4*>(shareB + at) = make_float4(gB[t][4 * q], gB[t][4 * q + 1], gB[t][4 * q + 2], gB[t][4 * q + 3]);
-          *reinterpret_cast<float4*>(shareC + at) = make_float4(gC[t][4 * q], gC[t][4 * q + 1], gC[t][4 * q + 2], gC[t][4 * q + 3]);
+        for (int q = 0; q < 4; ++q) {
+          if (one_run)
+            *reinterpret_cast<u32x2*>(static_cast<__bf16*>(rows) + r * stride + n + 8 * q) =
+                u32x2{pipe::cvt2(v[4 * q], v[4 * q + 1]), pipe::cvt2(v[4 * q + 2], v[4 * q + 3])};
+          else
+            *reinterpret_cast<f32x4*>(shares + r * p.G * N + n + 8 * q) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
         }
-      }
+      };
+      if (do_b) put(gB, p.gB, p.gbs, shareB);
+      if (do_c) put(gC, p.gC, p.gcs, shareC);
     }
   }
   if (!later)
-    for (int i = threadIdx.x; i < strips_here / spp * 3; i += 256) heads[strip0 / spp * 3 + i] = 0.f;
+    for (int i = threadIdx.x; i < (strips_here >> shift) * 3; i += kGradThreads) heads[(strip0 >> shift) * 3 + i] = 0.f;
 }
 
 // The first H blocks: a head's sums over the blocks of rows.  Those behind: gB and gC
@@ -617,7 +705,8 @@ Plan plan(int T, int R, int H, int P, int G, int N) {
   // runs of strips: the fewest rounds of workgroups over the CUs, weighed by their length
   const int heads = H / G, base = w.blocks * G;
   long long best = -1;
-  for (int n = 1; n <= heads; ++n) {
+  const int few = (heads + kMostHeads - 1) / kMostHeads;
+  for (int n = few; n <= heads && n < few + 1024; ++n) {
     const int len = (heads + n - 1) / n;
     if ((heads + len - 1) / len != n) continue;
     const long long cost = ((long long)base * n + 255) / 256 * (len * spp + 2);
@@ -661,7 +750,7 @@ hipError_t launch_ssm_scan_bwd(const ScanBwdArgs& a) {
     hipLaunchKernelGGL((states_kernel<N, false, PARTS>), dim3(nstrips, w.nseg, 2), dim3(256), 0, stream, p);
     if (const hipError_t e = hipGetLastError()) return e;
     if (w.blocks) {
-      hipLaunchKernelGGL((grad_kernel<N>), dim3(w.blocks, n.G * w.runs), dim3(256), 0, stream, p);
+      hipLaunchKernelGGL((grad_kernel<N>), dim3(w.blocks, n.G * w.runs), dim3(kGradThreads), 0, stream, p);
       if (const hipError_t e = hipGetLastError()) return e;
     }
     const long long values = w.runs > 1 ? (long long)n.T * n.G * N : 0;
