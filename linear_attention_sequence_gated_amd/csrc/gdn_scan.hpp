@@ -62,45 +62,43 @@ __device__ __forceinline__ Source source(const void* base, long long stride, lon
   return {u32x4{(unsigned)__builtin_amdgcn_readfirstlane((int)at), (unsigned)__builtin_amdgcn_readfirstlane((int)(at >> 32)) & 0xffffu,
                 (unsigned)__builtin_amdgcn_readfirstlane((int)bytes), (unsigned)pipe::kRsrcWord3}};
 }
+// 64 pieces of 16 bytes, `ahead` bytes behind src, to consecutive LDS.
+__device__ __forceinline__ void load_piece(__bf16* lds, const Source& src, unsigned off, int ahead) {
+  const unsigned at = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(unsigned long long)(tile::lds_void*)lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(at), "v"(off), "s"(src.rsrc), "s"(ahead)
+               : "memory");
+}
 template <int D, int N, int NW> struct Stage : tile::Stage<D, N, NW> {
   typedef tile::Stage<D, N, NW> Base;
-  // `ahead`: bytes behind src that the loads begin at.
-  __device__ __forceinline__ void load_one(__bf16* lds, const Source& src, int wave, int i, int ahead = 0) const {
-    const unsigned at = (unsigned)__builtin_amdgcn_readfirstlane(
-        (int)(unsigned)(unsigned long long)(tile::lds_void*)(lds + (wave * Base::LOADS + i) * 512));
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :
-                 : "s"(at), "v"(Base::off[i]), "s"(src.rsrc), "s"(ahead)
-                 : "memory");
+  __device__ __forceinline__ void load_one(__bf16* lds, const Source& src, int wave, int i) const {
+    load_piece(lds + (wave * Base::LOADS + i) * 512, src, Base::off[i], 0);
   }
-  __device__ __forceinline__ void load(__bf16* lds, const Source& src, int wave, int ahead = 0) const {
+  __device__ __forceinline__ void load(__bf16* lds, const Source& src, int wave) const {
 #pragma unroll
-    for (int i = 0; i < Base::LOADS; ++i) load_one(lds, src, wave, i, ahead);
+    for (int i = 0; i < Base::LOADS; ++i) load_one(lds, src, wave, i);
   }
 };
 
-// The same for one wave that loads R rows of 64 values by itself: the swizzle repeats
-// after 16 rows, two loads, so that two offsets serve them all.
-struct Stage64 {
-  unsigned off[2];
+// The same for one wave that loads R rows by itself: the swizzle repeats after 16
+// rows, so that as many offsets as loads of 16 rows serve them all.
+template <int D> struct StageWave {
+  static constexpr int kRows = 512 / D, kOff = 16 / kRows;  // rows to a load; offsets
+  unsigned off[kOff];
   int step;  // bytes between rows 16 apart
   __device__ __forceinline__ void init(long long stride) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 8 * i + lane / 8;
-      off[i] = (unsigned)(r * stride * 2) + (pipe::row_off<64>(r, 8 * (lane % 8)) - r * 64) * 2;
+    for (int i = 0; i < kOff; ++i) {
+      const int r = kRows * i + lane / (D / 8);
+      off[i] = (unsigned)(r * stride * 2) + (pipe::row_off<D>(r, 8 * (lane % (D / 8))) - r * D) * 2;
     }
     step = (int)(stride * 32);
   }
   template <int R> __device__ __forceinline__ void load(__bf16* lds, const Source& src, int ahead) const {
-    const unsigned at = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(unsigned long long)(tile::lds_void*)lds);
 #pragma unroll
-    for (int i = 0; i < R / 8; ++i)
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                   :
-                   : "s"(at + i * 1024), "v"(off[i & 1]), "s"(src.rsrc), "s"(ahead + (i >> 1) * step)
-                   : "memory");
+    for (int i = 0; i < R / kRows; ++i) load_piece(lds + i * 512, src, off[i % kOff], ahead + i / kOff * step);
   }
 };
 

@@ -66,26 +66,32 @@ struct BwdParams {
 };
 
 // ---------------------------------------------------------------- states
+// A stored state: 16-byte pieces of eight channels.  That of row n, channels 8 c on, is
+// the one of this number.
+__device__ __forceinline__ int state_piece(int n, int c) { return (n / 32 * 4 + c / 2) * 64 + (c & 1) * 32 + n % 32; }
+
 // A workgroup: one strip, one segment; blockIdx.z: states downwards, or their
 // gradients upwards.  A wave has 32 n and 64 channels (N = 64: 32 of them) of
 // the transposed state: its lanes the n, its elements the channels, eight in a row to
-// a lane, so that a row of the stored state is written in 16-byte pieces.  What the
-// rows add is weighted on the side of B (C), in PARTS bf16 parts.
+// a lane: a 16-byte piece of the stored state.  Stored are a wave's pieces as they
+// are, 1 KB at a time (see state_piece).  What the rows add is weighted on the side of
+// B (C), in PARTS bf16 parts.  A fifth wave brings the rows of the piece to come and
+// computes its steps, so that the four have nothing but their products to wait for.
+constexpr int kStateThreads = 320;
 template <int N, bool LOCAL, int PARTS>
-__global__ __launch_bounds__(256) void states_kernel(BwdParams p) {
+__global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
   constexpr int NP = N == 128 ? 2 : 1;  // tiles of 32 channels to a wave
   __shared__ __attribute__((aligned(1024))) __bf16 buf[2][Q * N + Q * 64];
-  __shared__ Steps st_all[4];
+  __shared__ Steps st_two[2];
   __shared__ int window[kWindow];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, col = lane & 31;
-  const int nt = N == 128 ? wave : wave & 1, pt0 = N == 128 ? 0 : wave >> 1;
-  Steps& st = st_all[wave];
+  const int nt = N == 128 ? wave & 3 : wave & 1, pt0 = N == 128 ? 0 : (wave >> 1) & 1;
   const int strip = blockIdx.x, spp = p.P / 64, head = strip / spp, hcol = (strip % spp) * 64, group = head / (p.H / p.G);
   const int nstrips = p.H * spp;
   const bool up = blockIdx.z != 0;
   const int seg = LOCAL && up ? blockIdx.y + 1 : blockIdx.y;
   const float a = param(p.a, p.p_f32, head), bias = p.bias ? param(p.bias, p.p_f32, head) : 0.f;
-  const Offsets cu = offsets<256>(p.cu, p.R, window);
+  const Offsets cu = offsets<kStateThreads>(p.cu, p.R, window);
   const int s0 = seg * p.seg, s1 = min(s0 + p.seg, p.T);
   float* const shares = p.seg_ws[up];
   float* const kept = shares + (size_t)(p.nseg - 1) * nstrips * N * 64;
@@ -152,7 +158,7 @@ __global__ __launch_bounds__(256) void states_kernel(BwdParams p) {
       for (int r = k0; r < k1; ++r) {
         const int b = min(max(cu(r), 0), p.T);
         if (min(cu(r + 1), p.T) > b) continue;
-        for (int i = threadIdx.x; i < N * 64; i += 256) {
+        for (int i = threadIdx.x; i < N * 64; i += kStateThreads) {
           const long long at = of_seq(r) + (long long)(i / 64) * p.P + i % 64;
           p.gS0[at] = p.gSf ? p.gSf[at] : 0.f;
         }
@@ -163,39 +169,60 @@ __global__ __launch_bounds__(256) void states_kernel(BwdParams p) {
     load(slot(seg - 1), 64);
   }
 
-  Stage<N, Q, 4> sk;
-  Stage<64, Q, 4> sv;
+  StageWave<N> sk;
+  StageWave<64> sv;
   const __bf16* kg = (up ? static_cast<const __bf16*>(p.C) : static_cast<const __bf16*>(p.B)) + group * N;
   const __bf16* vg = (up ? static_cast<const __bf16*>(p.go) : static_cast<const __bf16*>(p.x)) + strip * 64;
   const long long ks = up ? p.cs : p.bs, vs = up ? p.gs : p.xs;
-  sk.init(ks, wave);
-  sv.init(vs, wave);
-  auto stage = [&](int b, const Piece& pc) {
-    sk.load(buf[b], source(kg, ks, pc.row, pc.n, N), wave);
-    sv.load(buf[b] + Q * N, source(vg, vs, pc.row, pc.n, 64), wave);
+  sk.init(ks), sv.init(vs);
+  const bool helper = wave == 4;
+  auto raw_dt = [&](const Piece& pc) { return lane < pc.n ? dt_bits(p.dt, p.dt_f32, (long long)(pc.row + lane) * p.dts + head) : 0u; };
+  auto take_steps = [&](int b, unsigned bits, const Piece& pc) {
+    Steps& st = st_two[b];
+    steps(st, dt_of(bits, p.dt_f32) + bias, a, lane < pc.n);
+    if (up) {  // what a row adds is weighted by the decays up to it
+      st.w[lane] = exp2_(st.G[lane]);
+      pipe::issue_fence();
+    }
   };
-  auto raw_dt = [&](const Piece& pc) {
-    return lane < pc.n ? dt_at(p.dt, p.dt_f32, (long long)(pc.row + lane) * p.dts + head) + bias : 0.f;
+  auto next = [&](Piece& pc) {
+    const bool some = up ? back.next(pc) : down.next(pc);
+    if (!some) pc.row = pc.n = 0;
+    return some;
   };
-  auto next = [&](Piece& pc) { return up ? back.next(pc) : down.next(pc); };
   const int kb = tile::col_base<N>(lane), vb = col_base_state<64>(lane);
+  auto stage = [&](int b, const Piece& pc) {
+    sk.template load<Q>(buf[b], source(kg, ks, pc.row, pc.n, N), 0);
+    sv.template load<Q>(buf[b] + Q * N, source(vg, vs, pc.row, pc.n, 64), 0);
+  };
 
-  Piece cur, nxt;
-  bool more = next(cur);
-  float z = 0.f;
-  if (more) {
+  Piece cur, nxt, nx2;
+  bool more = next(cur), more2 = more && next(nxt);
+  if (!more2) nxt.row = nxt.n = 0;
+  unsigned bits = 0;  // dt of the next piece: the helper's
+  if (more && helper) {
+    const unsigned first = raw_dt(cur);
+    bits = raw_dt(nxt);
+    take_steps(0, first, cur);
     stage(0, cur);
-    z = raw_dt(cur);
   }
   for (int b = 0; more; b ^= 1) {
     tile::staged_barrier();
-    z = arrived(z);
-    more = next(nxt);
-    float z_next = 0.f;
-    if (more) {
-      z_next = raw_dt(nxt);
-      stage(b ^ 1, nxt);
+    const bool more3 = more2 && next(nx2);
+    if (!more3) nx2.row = nx2.n = 0;
+    if (helper) {
+      bits = arrived(bits);
+      const unsigned after = raw_dt(nx2);
+      if (more2) {
+        stage(b ^ 1, nxt);
+        take_steps(b ^ 1, bits, nxt);
+      }
+      bits = after;
+      cur = nxt, nxt = nx2;
+      more = more2, more2 = more3;
+      continue;
     }
+    const Steps& st = st_two[b];
     if (up ? cur.last : cur.first) {
       const float* src = up ? p.gSf : p.S0;
       if (src) load(src + of_seq(cur.seq), p.P);
@@ -205,18 +232,14 @@ __global__ __launch_bounds__(256) void states_kernel(BwdParams p) {
       }
     }
     if constexpr (!LOCAL) {
-      __bf16* dst = p.states[up] + (((long long)piece_id(cur) * nstrips + strip) * N + n) * 64 + 32 * pt0 + 8 * half;
+      u32x4* dst = reinterpret_cast<u32x4*>(p.states[up] + ((long long)piece_id(cur) * nstrips + strip) * N * 64) + nt * 256 + pt0 * 128 + lane;
 #pragma unroll
       for (int t = 0; t < NP; ++t)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(dst + 32 * t + 16 * i) = operand(S[t], i);
+        for (int i = 0; i < 2; ++i) dst[(2 * t + i) * 64] = operand(S[t], i);
     }
-    const float total = steps(st, z, a, lane < cur.n);
+    const float total = st.total;
     whole += total;
-    if (up) {
-      st.w[lane] = exp2_(st.G[lane]);
-      pipe::issue_fence();
-    }
     const __bf16 *Kt = buf[b], *Vt = buf[b] + Q * N;
     const float keep = exp2_(total);
 #pragma unroll
@@ -237,11 +260,11 @@ __global__ __launch_bounds__(256) void states_kernel(BwdParams p) {
     if constexpr (!LOCAL) {
       if (up && cur.first && p.gS0) store(p.gS0 + of_seq(cur.seq), p.P);
     }
-    cur = nxt;
-    z = z_next;
+    cur = nxt, nxt = nx2;
+    more = more2, more2 = more3;
   }
   if constexpr (LOCAL) {
-    store(slot(blockIdx.y), 64);
+    if (!helper) store(slot(blockIdx.y), 64);
     if (threadIdx.x == 0) kept[(size_t)blockIdx.y * nstrips + strip] = fresh ? kFresh : whole;
   }
 }
@@ -368,10 +391,16 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
   }
 
   Stage<N, Q, kGradWaves> sc, sb;
-  Stage64 sx, sh, ss;
+  StageWave<64> sx, sh;
   sc.init(p.cs, wave);
   sb.init(p.bs, wave);
-  sx.init(p.xs), sh.init(p.gs), ss.init(64);
+  sx.init(p.xs), sh.init(p.gs);
+  unsigned state_off[2];  // of the lane's pieces of rows 0 to 7 and 8 to 15 in the swizzled tile
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 8 * i + lane / 8;
+    state_off[i] = state_piece(r, (pipe::row_off<64>(r, 8 * (lane % 8)) - r * 64) / 8) * 16;
+  }
   const int rb64 = tile::row_base<64>(lane), cb64 = col_base8<64>(lane), cbn = col_base8<N>(lane);
   // operands of 16 rows (columns) for the products of 16 x 16 x 32: rows r0 + l % 16, values k0 + 8 (l / 16) on
   auto rows16 = [&](const __bf16* t, auto d, int r0, int k0) {
@@ -396,8 +425,12 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
     const Source from_h = source(static_cast<const __bf16*>(p.go) + strip0 * 64, p.gs, pc.row, pc.n, 64 * strips_here);
     auto stage = [&](int s) {  // by one wave: others would wait in line with their loads
       auto& to = L.strip[s & 1];
-      ss.load<N>(to.S, from_s, s * N * 128);
-      ss.load<N>(to.Z, from_z, s * N * 128);
+#pragma unroll
+      for (int i = 0; i < N / 8; ++i) {  // 8 rows at a time: 16 rows further is 256 bytes, 32 rows 4 KB
+        const int ahead = s * N * 128 + i / 4 * 4096 + (i / 2 & 1) * 256;
+        load_piece(to.S + i * 512, from_s, state_off[i & 1], ahead);
+        load_piece(to.Z + i * 512, from_z, state_off[i & 1], ahead);
+      }
       sx.load<Q>(to.x, from_x, s * 128);
       sh.load<Q>(to.h, from_h, s * 128);
     };
@@ -696,9 +729,11 @@ Plan plan(int T, int R, int H, int P, int G, int N) {
   Plan w;
   const int nstrips = H * (P / 64), spp = P / 64;
   w.blocks = (T + Q - 1) / Q;
-  // segments: workgroups for every CU three times over, both directions counted, of at least four pieces
-  const int want = nstrips >= 384 ? 1 : 384 / nstrips;
+  // segments: three workgroups for every two CUs, both directions counted, of at least four pieces; where the sequences
+  // would be as long as each other and as a number of pieces, whole ones, whose states need not be joined
+  const int want = nstrips >= 192 ? 1 : 192 / nstrips;
   int per = (w.blocks + want - 1) / want;
+  if (R > 1 && T % R == 0 && T / R % Q == 0 && 2 * (T / R) >= per * Q && T / R <= 2 * per * Q) per = T / R / Q;
   if (per < 4) per = 4;
   w.seg = per * Q;
   w.nseg = T > w.seg ? (T + w.seg - 1) / w.seg : 1;
@@ -741,13 +776,13 @@ hipError_t launch_ssm_scan_bwd(const ScanBwdArgs& a) {
   auto go = [&](auto nn, auto parts) {
     constexpr int N = decltype(nn)::value, PARTS = decltype(parts)::value;
     if (w.nseg > 1) {
-      hipLaunchKernelGGL((states_kernel<N, true, PARTS>), dim3(nstrips, w.nseg - 1, 2), dim3(256), 0, stream, p);
+      hipLaunchKernelGGL((states_kernel<N, true, PARTS>), dim3(nstrips, w.nseg - 1, 2), dim3(kStateThreads), 0, stream, p);
       if (const hipError_t e = hipGetLastError()) return e;
       hipLaunchKernelGGL((join_both_kernel<N>), dim3(N * 64 / 1024, nstrips, 2), dim3(256), 0, stream, p.seg_ws[0], p.seg_ws[1],
                          nstrips, w.nseg - 1);
       if (const hipError_t e = hipGetLastError()) return e;
     }
-    hipLaunchKernelGGL((states_kernel<N, false, PARTS>), dim3(nstrips, w.nseg, 2), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((states_kernel<N, false, PARTS>), dim3(nstrips, w.nseg, 2), dim3(kStateThreads), 0, stream, p);
     if (const hipError_t e = hipGetLastError()) return e;
     if (w.blocks) {
       hipLaunchKernelGGL((grad_kernel<N>), dim3(w.blocks, n.G * w.runs), dim3(kGradThreads), 0, stream, p);
