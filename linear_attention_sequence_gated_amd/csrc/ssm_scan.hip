@@ -16,9 +16,12 @@
 // are alike; where there are several, a first launch finds what each leaves in the
 // state that crosses its end, a second one adds these up along the sequences.
 //
-// Where numbers are rounded: C B^T o L and the state, as it enters the product with
-// C, to bf16 (2^-9 of each term); what goes into the state is kept in three bf16
-// parts, 2^-25 of each term, since the state is a result and is carried on.
+// Where numbers are rounded: C B^T o L between the two halves of a piece, and the state
+// as it enters the product with C, to bf16 (2^-9 of each term); C B^T o L within a half,
+// where the weights are largest, in two parts (2^-17: with one, the relative error of
+// short sequences' results was 2.5e-3 for 2.0e-3, of which the result's own rounding
+// is 1.65e-3); what goes into the state in three parts, 2^-25, since the state is a
+// result and is carried on.
 #include "gdn_scan.hpp"
 
 namespace gdn {
@@ -293,15 +296,20 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
             f[2][4 * u + j] = __builtin_bit_cast(float, __builtin_bit_cast(int, c11[j] * exp2_(g1 + fb[j])) & in);
           }
         }
-        u32x4 w[3];
+        u32x4 w[3], rest[2];
 #pragma unroll
         for (int i = 0; i < 3; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[i][e] = pipe::cvt2(f[i][2 * e], f[i][2 * e + 1]);
+          for (int e = 0; e < 4; ++e) {
+            w[i][e] = pipe::cvt2(f[i][2 * e], f[i][2 * e + 1]);
+            if (i != 1) rest[i / 2][e] = pipe::cvt2(f[i][2 * e] - pipe::lo_f(w[i][e]), f[i][2 * e + 1] - pipe::hi_f(w[i][e]));
+          }
         const u32x4 x0 = tile::col_frag<128>(Xt, xb, 16 * k, xcol), x1 = tile::col_frag<128>(Xt, xb, 32 + 16 * k, xcol);
         y[0] = tile::mma(x0, w[0], y[0]);
         y[1] = tile::mma(x0, w[1], y[1]);
+        y[0] = tile::mma(x0, rest[0], y[0]);
         y[1] = tile::mma(x1, w[2], y[1]);
+        y[1] = tile::mma(x1, rest[1], y[1]);
         __builtin_amdgcn_sched_barrier(0);
       }
       // y: columns are rows of the piece, elements channels 8 q + 4 half + j.  Added to D x, and by 32 rows through a part
