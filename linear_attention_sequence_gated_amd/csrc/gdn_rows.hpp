@@ -50,6 +50,44 @@ template <bool F32> __device__ __forceinline__ void put(void* base, long long at
   *reinterpret_cast<u32x4*>(static_cast<char*>(base) + at * (F32 ? 4 : 2) + (long long)p * 16) = w;
 }
 
+// Pieces of E values, 8 or 16 bytes.
+template <bool F32, int E> struct PieceOf {
+  static_assert(E == (F32 ? 4 : 8) || (!F32 && E == 4), "");
+  typedef std::conditional_t<!F32 && E == 4, u32x2, u32x4> Word;
+  static __device__ __forceinline__ Word zero() {
+    Word w;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Word) / 4); ++i) w[i] = 0;
+    return w;
+  }
+  static __device__ __forceinline__ Word get(const void* base, long long at, int p) {
+    return *reinterpret_cast<const Word*>(static_cast<const char*>(base) + (at + (long long)p * E) * (F32 ? 4 : 2));
+  }
+  static __device__ __forceinline__ void put(void* base, long long at, int p, const Word& w) {
+    *reinterpret_cast<Word*>(static_cast<char*>(base) + (at + (long long)p * E) * (F32 ? 4 : 2)) = w;
+  }
+  static __device__ __forceinline__ void unpack(const Word& w, float (&f)[E]) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = number(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) f[2 * i] = pipe::lo_f(w[i]), f[2 * i + 1] = pipe::hi_f(w[i]);
+    }
+  }
+  static __device__ __forceinline__ Word pack(const float (&f)[E]) {
+    Word w;
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __builtin_bit_cast(unsigned, f[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) w[i] = pipe::cvt2(f[2 * i], f[2 * i + 1]);
+    }
+    return w;
+  }
+};
+
 // N consecutive parameters from index `at`, bf16 or float32; N a multiple of 4
 // and `at` one of N, so that they are whole words of 8 or 16 bytes.
 template <int N> __device__ __forceinline__ void params(const void* base, bool f32, long long at, float (&f)[N]) {

@@ -23,8 +23,8 @@ using namespace rows;
 using pipe::ic;
 
 // The taps and the bias of a thread's channels.
-template <bool F32, int W> struct Taps {
-  static constexpr int PE = kPiece<F32>;
+template <bool F32, int W, int PE = kPiece<F32>> struct Taps {
+  typedef PieceOf<F32, PE> Piece;
   float w[PE * W], b[PE];
   __device__ __forceinline__ void load(const void* weight, const void* bias, bool w_f32, int p) {
     params<PE * W>(weight, w_f32, (long long)p * PE * W, w);
@@ -33,13 +33,13 @@ template <bool F32, int W> struct Taps {
     if (bias) params<PE>(bias, w_f32, (long long)p * PE, b);
   }
   // b + sum_j w_j z_j
-  __device__ __forceinline__ void sum(const u32x4 (&z)[W], float (&p)[PE]) const {
+  __device__ __forceinline__ void sum(const typename Piece::Word (&z)[W], float (&p)[PE]) const {
 #pragma unroll
     for (int e = 0; e < PE; ++e) p[e] = b[e];
 #pragma unroll
     for (int j = 0; j < W; ++j) {
       float f[PE];
-      unpack<F32>(z[j], f);
+      Piece::unpack(z[j], f);
 #pragma unroll
       for (int e = 0; e < PE; ++e) p[e] = __builtin_fmaf(w[e * W + j], f[e], p[e]);
     }
@@ -47,9 +47,10 @@ template <bool F32, int W> struct Taps {
 };
 
 // Row `back` rows before the first of sequence s, from its state; zeros without one.
-template <bool F32, int W> __device__ __forceinline__ u32x4 before(const void* state, int s, int back, int C, int p) {
-  if (!state) return u32x4{0, 0, 0, 0};
-  return piece<F32>(state, ((long long)s * (W - 1) + W - 1 - back) * C, p);
+template <bool F32, int W, int PE = kPiece<F32>>
+__device__ __forceinline__ typename PieceOf<F32, PE>::Word before(const void* state, int s, int back, int C, int p) {
+  if (!state) return PieceOf<F32, PE>::zero();
+  return PieceOf<F32, PE>::get(state, ((long long)s * (W - 1) + W - 1 - back) * C, p);
 }
 
 // -------------------------------------------------------------------- forward
@@ -120,30 +121,34 @@ __global__ __launch_bounds__(256) void conv_kernel(const void* __restrict__ x, c
 
 // ------------------------------------------------------------------ gradients
 // q of row t, from the rows z that its taps see.
+constexpr int kMostRun = 64;
+constexpr int kBwdPiece = 4;  // channels to a thread: with eight, taps, shares and rows took 220 registers
 template <bool F32, int W>
-__device__ __forceinline__ void slope(const Taps<F32, W>& taps, const u32x4 (&z)[W], const u32x4& g, bool silu_on,
-                                      float (&q)[kPiece<F32>]) {
-  unpack<F32>(g, q);
+__device__ __forceinline__ void slope(const Taps<F32, W, kBwdPiece>& taps, const typename PieceOf<F32, kBwdPiece>::Word (&z)[W],
+                                      const typename PieceOf<F32, kBwdPiece>::Word& g, bool silu_on, float (&q)[kBwdPiece]) {
+  PieceOf<F32, kBwdPiece>::unpack(g, q);
   if (!silu_on) return;
-  float p[kPiece<F32>];
+  float p[kBwdPiece];
   taps.sum(z, p);
 #pragma unroll
-  for (int e = 0; e < kPiece<F32>; ++e) q[e] *= silu_slope(p[e]);
+  for (int e = 0; e < kBwdPiece; ++e) q[e] *= silu_slope(p[e]);
 }
 
 // A workgroup: 64 pieces of the channels, four runs of L rows, one after the
 // other's in each wave; shares of gw and gb are added over the waves through LDS
 // and written to ws [runs][W + 1][C].  The workgroups behind the last run take the
 // gradients of the states, one sequence each.
-template <bool F32, int W, int L>
+template <bool F32, int W>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(const void* __restrict__ x, const void* __restrict__ weight,
                                                        const void* __restrict__ bias, const void* __restrict__ grad_out,
                                                        const int* __restrict__ cu, const void* __restrict__ state,
                                                        const void* __restrict__ grad_state_final,
                                                        void* __restrict__ grad_x, void* __restrict__ grad_state,
                                                        float* __restrict__ ws, long long xs, long long gs, int T, int R,
-                                                       int C, bool w_f32, bool silu_on, bool zero_rest, int runs) {
-  constexpr int PE = kPiece<F32>, NR = 4 * L, M = NR + W - 1;
+                                                       int C, bool w_f32, bool silu_on, bool zero_rest, int runs, int L) {
+  constexpr int PE = kBwdPiece, M = 4 * kMostRun + W - 1;
+  typedef PieceOf<F32, PE> Piece;
+  typedef typename Piece::Word Word;
   __shared__ int window[kWindow], seq[M], beg[M], end[M];
   __shared__ float part[4][64 * PE];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -156,7 +161,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const void* __restrict__ 
     if (!here || wave) return;
     const Span sp = span_of(cu, T, s);
     const int n = sp.end - sp.beg;
-    Taps<F32, W> taps;
+    Taps<F32, W, PE> taps;
     taps.load(weight, bias, w_f32, p);
     float acc[W - 1][PE];
 #pragma unroll
@@ -164,19 +169,19 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const void* __restrict__ 
 #pragma unroll
       for (int e = 0; e < PE; ++e) acc[m][e] = 0.f;
       // row m of the state is row m - n of the state afterwards, where the sequence is that short
-      if (grad_state_final && m >= n) unpack<F32>(piece<F32>(grad_state_final, ((long long)s * (W - 1) + m - n) * C, p), acc[m]);
+      if (grad_state_final && m >= n) Piece::unpack(Piece::get(grad_state_final, ((long long)s * (W - 1) + m - n) * C, p), acc[m]);
     }
 #pragma unroll
     for (int t = 0; t < W - 1; ++t) {
       if (t >= n) break;
-      u32x4 z[W];
+      Word z[W];
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         const int back = W - 1 - t - j;
-        z[j] = back > 0 ? before<F32, W>(state, s, back, C, p) : piece<F32>(x, (long long)(sp.beg - back) * xs, p);
+        z[j] = back > 0 ? before<F32, W, PE>(state, s, back, C, p) : Piece::get(x, (long long)(sp.beg - back) * xs, p);
       }
       float q[PE];
-      slope<F32, W>(taps, z, piece<F32>(grad_out, (long long)(sp.beg + t) * gs, p), silu_on, q);
+      slope<F32, W>(taps, z, Piece::get(grad_out, (long long)(sp.beg + t) * gs, p), silu_on, q);
 #pragma unroll
       for (int j = 0; j < W - 1; ++j)
         if (t + j < W - 1)
@@ -184,13 +189,13 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const void* __restrict__ 
           for (int e = 0; e < PE; ++e) acc[t + j][e] = __builtin_fmaf(taps.w[e * W + j], q[e], acc[t + j][e]);
     }
 #pragma unroll
-    for (int m = 0; m < W - 1; ++m) put<F32>(grad_state, ((long long)s * (W - 1) + m) * C, p, pack<F32>(acc[m]));
+    for (int m = 0; m < W - 1; ++m) Piece::put(grad_state, ((long long)s * (W - 1) + m) * C, p, Piece::pack(acc[m]));
     return;
   }
 
-  const int r0 = blockIdx.x * NR;
+  const int r0 = blockIdx.x * 4 * L;
   find_seqs<M, 256>(cu, R, T, r0, window, seq, beg, end);
-  Taps<F32, W> taps;
+  Taps<F32, W, PE> taps;
   taps.load(weight, bias, w_f32, pc);
   const int first = wave * L;  // of r0
   float gw[W][PE], gb[PE];
@@ -202,10 +207,10 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const void* __restrict__ 
   }
   auto row_of = [&](const void* base, long long stride, int i) {
     const int row = r0 + i;
-    return row >= 0 && row < T ? piece<F32>(base, (long long)row * stride, pc) : u32x4{0, 0, 0, 0};
+    return row >= 0 && row < T ? Piece::get(base, (long long)row * stride, pc) : Piece::zero();
   };
   // zs: the rows t - W + 1 .. t;  qs: q of rows t - W + 1 .. t, whose first is s
-  u32x4 zs[W];
+  Word zs[W];
   float qs[W][PE];
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
@@ -215,10 +220,10 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const void* __restrict__ 
   }
   constexpr int U = 4;  // rows whose loads are issued together
   for (int i0 = 0; i0 < L + W - 1; i0 += U) {
-    u32x4 xn[U], gn[U];
+    Word xn[U], gn[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      xn[u] = gn[u] = u32x4{0, 0, 0, 0};
+      xn[u] = gn[u] = Piece::zero();
       if (i0 + u < L + W - 1) {
         xn[u] = row_of(x, xs, first + i0 + u);
         gn[u] = row_of(grad_out, gs, first + i0 + u);
@@ -241,21 +246,21 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const void* __restrict__ 
 #pragma unroll
         for (int e = 0; e < PE; ++e) qs[W - 1][e] = 0.f;
       } else {
-        u32x4 z[W];
+        Word z[W];
 #pragma unroll
         for (int j = 0; j < W; ++j) z[j] = zs[j];
         if (row - b < W - 1) {
           const int s = __builtin_amdgcn_readfirstlane(seq[first + i]);
 #pragma unroll
           for (int j = 0; j < W - 1; ++j)
-            if (row - (W - 1) + j < b) z[j] = before<F32, W>(state, s, b - (row - (W - 1) + j), C, pc);
+            if (row - (W - 1) + j < b) z[j] = before<F32, W, PE>(state, s, b - (row - (W - 1) + j), C, pc);
         }
         slope<F32, W>(taps, z, gn[u], silu_on, qs[W - 1]);
         if (i < L) {
 #pragma unroll
           for (int j = 0; j < W; ++j) {
             float f[PE];
-            unpack<F32>(z[j], f);
+            Piece::unpack(z[j], f);
 #pragma unroll
             for (int e = 0; e < PE; ++e) gw[j][e] = __builtin_fmaf(qs[W - 1][e], f[e], gw[j][e]);
           }
@@ -268,7 +273,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const void* __restrict__ 
       if (is < 0 || s_row >= T) continue;
       const int sb = __builtin_amdgcn_readfirstlane(beg[first + is]);
       if (sb < 0) {
-        if (zero_rest && here) put<F32>(grad_x, (long long)s_row * C, p, u32x4{0, 0, 0, 0});
+        if (zero_rest && here) Piece::put(grad_x, (long long)s_row * C, p, Piece::zero());
         continue;
       }
       const int se = __builtin_amdgcn_readfirstlane(end[first + is]);
@@ -277,14 +282,14 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const void* __restrict__ 
       for (int e = 0; e < PE; ++e) o[e] = 0.f;
       if (grad_state_final && se - s_row <= W - 1) {
         const int s = __builtin_amdgcn_readfirstlane(seq[first + is]);
-        unpack<F32>(piece<F32>(grad_state_final, ((long long)s * (W - 1) + W - 1 - (se - s_row)) * C, pc), o);
+        Piece::unpack(Piece::get(grad_state_final, ((long long)s * (W - 1) + W - 1 - (se - s_row)) * C, pc), o);
       }
 #pragma unroll
       for (int k = 0; k < W; ++k)
         if (s_row + k < se)
 #pragma unroll
           for (int e = 0; e < PE; ++e) o[e] = __builtin_fmaf(taps.w[e * W + W - 1 - k], qs[k][e], o[e]);
-      if (here) put<F32>(grad_x, (long long)s_row * C, p, pack<F32>(o));
+      if (here) Piece::put(grad_x, (long long)s_row * C, p, Piece::pack(o));
     }
   }
 #pragma unroll
@@ -360,15 +365,25 @@ template <class F> hipError_t by_form(bool f32, int W, F f) {
   return f(std::false_type{}, ic<4>{});
 }
 
-int column_groups(int C, bool f32) { return (C / (f32 ? 4 : 8) + 63) / 64; }
+int column_groups(int C, int piece) { return (C / piece + 63) / 64; }
 
-constexpr int kBwdRun = 32;
-int bwd_runs(int T) { return (T + 4 * kBwdRun - 1) / (4 * kBwdRun); }
+// Rows to a wave's run in the gradients: as many as let all workgroups, four to a CU,
+// run at once (8 x 2048 rows of 2304: 73 us; with 32 rows, 1152 workgroups, 80),
+// between 8 and kMostRun; with more rows than that, 40.
+int bwd_run(int T, int C) {
+  const int groups = 1024 / column_groups(C, kBwdPiece);
+  const int L = groups ? (int)(((long long)T + 4 * groups - 1) / (4 * groups)) : kMostRun + 1;
+  return L < 8 ? 8 : L <= kMostRun ? L : 40;
+}
+int bwd_runs(int T, int C) {
+  const int rows = 4 * bwd_run(T, C);
+  return (T + rows - 1) / rows;
+}
 
 }  // namespace
 
 hipError_t launch_short_conv(const ConvArgs& a) {
-  const int cols = column_groups(a.C, a.f32);
+  const int cols = column_groups(a.C, a.f32 ? 4 : 8);
   return by_form(a.f32, a.W, [&](auto f32, auto w) {
     auto go = [&](auto l) {
       constexpr int rows_wg = 4 * decltype(l)::value;
@@ -384,16 +399,16 @@ hipError_t launch_short_conv(const ConvArgs& a) {
   });
 }
 
-size_t short_conv_bwd_workspace_bytes(int T, int C, int W) { return (size_t)bwd_runs(T) * (W + 1) * C * sizeof(float); }
+size_t short_conv_bwd_workspace_bytes(int T, int C, int W) { return (size_t)bwd_runs(T, C) * (W + 1) * C * sizeof(float); }
 
 hipError_t launch_short_conv_bwd(const ConvBwdArgs& a) {
   hipStream_t st = static_cast<hipStream_t>(a.stream);
-  const int cols = column_groups(a.C, a.f32), runs = bwd_runs(a.T), blocks = runs + (a.grad_state ? a.R : 0);
+  const int cols = column_groups(a.C, kBwdPiece), runs = bwd_runs(a.T, a.C), blocks = runs + (a.grad_state ? a.R : 0);
   if (blocks) {
     const hipError_t e = by_form(a.f32, a.W, [&](auto f32, auto w) {
-      hipLaunchKernelGGL((conv_bwd_kernel<decltype(f32)::value, decltype(w)::value, kBwdRun>), dim3(blocks, cols), dim3(256),
+      hipLaunchKernelGGL((conv_bwd_kernel<decltype(f32)::value, decltype(w)::value>), dim3(blocks, cols), dim3(256),
                          0, st, a.x, a.weight, a.bias, a.grad_out, a.cu, a.state, a.grad_state_final, a.grad_x,
-                         a.grad_state, a.ws, a.xs, a.gs, a.T, a.R, a.C, a.w_f32, a.silu, a.zero_rest, runs);
+                         a.grad_state, a.ws, a.xs, a.gs, a.T, a.R, a.C, a.w_f32, a.silu, a.zero_rest, runs, bwd_run(a.T, a.C));
       return hipGetLastError();
     });
     if (e) return e;
@@ -406,7 +421,7 @@ hipError_t launch_short_conv_bwd(const ConvBwdArgs& a) {
 
 hipError_t launch_short_conv_step(const ConvStepArgs& a) {
   return by_form(a.f32, a.W, [&](auto f32, auto w) {
-    hipLaunchKernelGGL((conv_step_kernel<decltype(f32)::value, decltype(w)::value>), dim3((a.R + 3) / 4, column_groups(a.C, a.f32)),
+    hipLaunchKernelGGL((conv_step_kernel<decltype(f32)::value, decltype(w)::value>), dim3((a.R + 3) / 4, column_groups(a.C, a.f32 ? 4 : 8)),
                        dim3(256), 0, static_cast<hipStream_t>(a.stream), a.x, a.weight, a.bias, a.state, a.out, a.xs, a.R,
                        a.C, a.w_f32, a.silu);
     return hipGetLastError();
