@@ -57,15 +57,144 @@ struct ScanParams {
 // are moved by the row, so that neither 16 rows' nor 16 pieces' meet in a bank.
 __device__ __forceinline__ int cb_off(int i, int j) { return i * Q + ((j / 4) ^ (i & 15)) * 4; }
 
-template <int N, int NS, bool OUT>
+// The state S of 32 columns (block xcol of the rows Xt) behind a piece of rows of B and
+// x.  between(k), k = 0 to 3: what else is to be issued behind the products of 16 rows.
+template <int N, class F>
+__device__ __forceinline__ void add_piece(f32x16 (&S)[N / 32], const __bf16* Bt, const __bf16* Xt, int xcol, int cb, int xb,
+                                          const Steps& st, int half, F between) {
+  constexpr int NT = N / 32;
+  const float keep = exp2_(st.total);
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) S[t][e] *= keep;
+  // each 16 rows' operands are read beside the products of the 16 before
+  u32x4 bt[2][NT], xk[2];
+  xk[0] = tile::col_frag<128>(Xt, xb, 0, xcol);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) bt[0][t] = tile::col_frag<N>(Bt, cb, 0, t);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    Split<kParts> xw;
+    xw.make(xk[k & 1], st.w + 16 * k + 4 * half, st.w + 16 * k + 8 + 4 * half);
+    __builtin_amdgcn_sched_barrier(0);
+    if (k < 3) {
+      xk[(k + 1) & 1] = tile::col_frag<128>(Xt, xb, 16 * (k + 1), xcol);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) bt[(k + 1) & 1][t] = tile::col_frag<N>(Bt, cb, 16 * (k + 1), t);
+    }
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) S[t] = tile::mma(bt[k & 1][t], xw.part[q], S[t]);
+    between(k);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// What each segment leaves in the state of the sequence that crosses its end.  As
+// many waves more as strips bring the rows of the piece to come and compute its steps,
+// one strip's each, so that the others have nothing but their products to wait for.
+template <int N, int NS>
+__global__ __launch_bounds__(192 * NS, 1) void ends_kernel(ScanParams p) {
+  constexpr int NT = N / 32, kTile = Q * N, kBuf = kTile + Q * 64 * NS;
+  __shared__ __attribute__((aligned(1024))) __bf16 buf[2][kBuf];
+  __shared__ Steps st_all[2][NS];
+  __shared__ int window[kWindow];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
+  const bool helper = wave >= 2 * NS;
+  const int mine_of = helper ? wave - 2 * NS : wave / 2;  // strip of the set
+  const Strips sp = strips(p.H, p.P, p.G, NS);
+  const int group = blockIdx.x / sp.sets, set = blockIdx.x % sp.sets, seg = blockIdx.y;
+  const int here = min(NS, sp.per_group - set * NS), strip0 = group * sp.per_group + set * NS;
+  const bool mine = mine_of < here;
+  const int strip = strip0 + (mine ? mine_of : 0), spp = p.P / 64, head = strip / spp, hcol = (strip % spp) * 64 + (wave & 1) * 32;
+  const int nstrips = p.H * spp;
+
+  const Offsets cu = offsets<192 * NS>(p.cu, p.R, window);
+  const int s0 = seg * p.seg, s1 = min(s0 + p.seg, p.T);
+  float* const kept = p.ws + (size_t)(p.nseg - 1) * nstrips * N * 64;
+  Walk<false> walk;
+  walk.init(cu, p.R, p.T, s0, s1);
+  const int r = walk.rend - 1;
+  const int b0 = r >= 0 ? min(max(cu(r), 0), p.T) : p.T, e0 = r >= 0 ? min(cu(r + 1), p.T) : 0;
+  if (e0 <= s1 || b0 >= s1) {
+    if ((int)threadIdx.x < here) kept[(size_t)seg * nstrips + strip0 + threadIdx.x] = kNone;
+    return;
+  }
+  walk.r = r, walk.beg = b0, walk.pos = max(b0, s0), walk.end = e0;
+
+  Piece cur, nxt, nx2;
+  bool more = walk.next(cur), more2 = more && walk.next(nxt);
+  if (!more2) nxt.row = nxt.n = 0;
+  if (helper) {
+    Stage<N, Q, NS> sb;
+    Stage<128, Q, NS> sx;  // two strips at a time
+    sb.init(p.bs, mine_of);
+    sx.init(p.xs, mine_of);
+    const __bf16* xg = static_cast<const __bf16*>(p.x) + strip0 * 64;
+    const __bf16* bg = static_cast<const __bf16*>(p.B) + group * N;
+    const float a = param(p.a, p.p_f32, head), bias = p.bias ? param(p.bias, p.p_f32, head) : 0.f;
+    auto stage = [&](int b, const Piece& pc) {
+      sb.load(buf[b], source(bg, p.bs, pc.row, pc.n, N), mine_of);
+#pragma unroll
+      for (int i = 0; i < NS / 2; ++i)
+        if (2 * i < here)
+          sx.load(buf[b] + kTile + i * Q * 128, source(xg + 128 * i, p.xs, pc.row, pc.n, 64 * min(2, here - 2 * i)), mine_of);
+    };
+    auto ask = [&](const Piece& pc) { return lane < pc.n ? dt_bits(p.dt, p.dt_f32, (long long)(pc.row + lane) * p.dts + head) : 0u; };
+    auto take = [&](int b, unsigned bits, const Piece& pc) { steps(st_all[b][mine_of], dt_of(bits, p.dt_f32) + bias, a, lane < pc.n); };
+    unsigned bits = ask(cur), ahead = ask(nxt);
+    if (more) take(0, bits, cur), stage(0, cur);
+    bits = ahead;
+    for (int b = 0; more; b ^= 1) {
+      tile::staged_barrier();
+      bits = arrived(bits);
+      const bool more3 = more2 && walk.next(nx2);
+      if (!more3) nx2.row = nx2.n = 0;
+      ahead = ask(nx2);
+      if (more2) stage(b ^ 1, nxt), take(b ^ 1, bits, nxt);
+      bits = ahead;
+      nxt = nx2;
+      more = more2, more2 = more3;
+    }
+    return;
+  }
+
+  f32x16 S[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) S[t] = zero16();
+  const int cb = col_base_state<N>(lane), xb = tile::col_base<128>(lane);
+  float whole = 0.f;  // log2 of what the segment keeps of a state
+  for (int b = 0; more; b ^= 1) {
+    tile::staged_barrier();
+    const bool more3 = more2 && walk.next(nx2);
+    if (cur.first && p.S0) load_state<NT>(S, p.S0 + (((long long)cur.seq * p.H + head) * N) * p.P + hcol, p.P);
+    const Steps& st = st_all[b][wave / 2];
+    whole += st.total;
+    add_piece<N>(S, buf[b], buf[b] + kTile + wave / 4 * Q * 128, wave % 4, cb, xb, st, half, [](int) {});
+    cur = nxt, nxt = nx2;
+    more = more2, more2 = more3;
+  }
+  if (mine) {
+    f32x4* at = reinterpret_cast<f32x4*>(p.ws + ((size_t)seg * nstrips + strip) * N * 64 + (wave & 1) * N * 32) + lane;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) at[(4 * t + q) * 64] = f32x4{S[t][4 * q], S[t][4 * q + 1], S[t][4 * q + 2], S[t][4 * q + 3]};
+    if (threadIdx.x % 128 == 0) kept[(size_t)seg * nstrips + strip] = b0 >= s0 ? kFresh : whole;
+  }
+}
+
+template <int N, int NS>
 __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanParams p) {
   constexpr int NT = N / 32, kThreads = 128 * NS, kWaves = 2 * NS;
   constexpr int kTile = Q * N, kX = Q * 64 * NS;
-  constexpr int kBuf = (OUT ? 2 : 1) * kTile + kX;
+  constexpr int kBuf = 2 * kTile + kX;
   __shared__ __attribute__((aligned(1024))) __bf16 buf[2][kBuf];
   __shared__ Steps st_all[NS];
-  __shared__ __attribute__((aligned(1024))) float cbs[OUT ? Q * Q : 4];  // C B^T: [i][j], see cb_off
-  __shared__ __attribute__((aligned(16))) __bf16 yts[OUT && N == 64 ? NS * 64 * 32 : 8];
+  __shared__ __attribute__((aligned(1024))) float cbs[Q * Q];  // C B^T: [i][j], see cb_off
+  __shared__ __attribute__((aligned(16))) __bf16 yts[N == 64 ? NS * 64 * 32 : 8];
   __shared__ int window[kWindow];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, col = lane & 31;
 
@@ -92,25 +221,12 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
   for (int t = 0; t < NT; ++t) S[t] = zero16();
   Walk<false> walk;
   walk.init(cu, p.R, p.T, s0, s1);
-  float whole = 0.f;  // log2 of what the segment keeps of a state (not OUT)
-  bool fresh = false;
   const bool goes_on = seg && walk.goes_on();
-  if constexpr (!OUT) {
-    // only the sequence that crosses the segment's end
-    const int r = walk.rend - 1;
-    const int b = r >= 0 ? min(max(cu(r), 0), p.T) : p.T, e = r >= 0 ? min(cu(r + 1), p.T) : 0;
-    if (e <= s1 || b >= s1) {
-      if (threadIdx.x < here) kept[(size_t)seg * nstrips + strip0 + threadIdx.x] = kNone;
-      return;
-    }
-    walk.r = r, walk.beg = b, walk.pos = max(b, s0), walk.end = e;
-    fresh = b >= s0;
-  }
 
   // staging: rows of C, B and x
   Stage<N, Q, kWaves> sc, sb;
   Stage<128, Q, kWaves> sx;  // two strips at a time
-  if constexpr (OUT) sc.init(p.cs, wave);
+  sc.init(p.cs, wave);
   sb.init(p.bs, wave);
   sx.init(p.xs, wave);
   const __bf16* xg = static_cast<const __bf16*>(p.x) + strip0 * 64;
@@ -118,7 +234,7 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
   const __bf16* cg = static_cast<const __bf16*>(p.C) + group * N;
   // One of the kLoads parts of a piece's staging: they are spread over the work on the piece before, since the loads of
   // eight waves in a row wait for each other.
-  constexpr int kLx = decltype(sx)::LOADS, kLb = decltype(sb)::LOADS, kLoads = NS / 2 * kLx + (OUT ? 2 : 1) * kLb;
+  constexpr int kLx = decltype(sx)::LOADS, kLb = decltype(sb)::LOADS, kLoads = NS / 2 * kLx + 2 * kLb;
   auto stage = [&](int b, const Piece& pc, int i) {
     if (i < NS / 2 * kLx) {
       const int pair = i / kLx;
@@ -127,7 +243,7 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
                     source(xg + 128 * pair, p.xs, pc.row, pc.n, 64 * min(2, here - 2 * pair)), wave, i % kLx);
     } else if (i < NS / 2 * kLx + kLb) {
       sb.load_one(buf[b], source(bg, p.bs, pc.row, pc.n, N), wave, i - NS / 2 * kLx);
-    } else if (OUT) {
+    } else {
       sc.load_one(buf[b] + kTile + kX, source(cg, p.cs, pc.row, pc.n, N), wave, i - NS / 2 * kLx - kLb);
     }
   };
@@ -135,7 +251,7 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
     return lane < pc.n ? dt_at(p.dt, p.dt_f32, (long long)(pc.row + lane) * p.dts + head) + bias : 0.f;
   };
   const int rb = tile::row_base<N>(lane), cb = col_base_state<N>(lane), xb = tile::col_base<128>(lane);
-  const float dskip = OUT && p.D ? param(p.D, p.p_f32, head) : 0.f;
+  const float dskip = p.D ? param(p.D, p.p_f32, head) : 0.f;
 
   Piece cur, nxt;
   bool more = walk.next(cur);
@@ -147,7 +263,7 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
     for (int i = 0; i < kLoads; ++i) stage(0, cur, i);
     if (steps_mine) z0 = raw_dt(cur);
   }
-  if constexpr (OUT) {
+  {
     if (goes_on) {  // the state at the border, added up here where that was not done before
       float f = 1.f;
       for (int k = seg - 1;; --k) {
@@ -214,7 +330,7 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
     if (steps_mine) steps(st, z, a, lane < cur.n);
     f32x16 y[2] = {zero16(), zero16()};
     float k0 = 0.f, k1 = 0.f;  // of the lane's two rows
-    if constexpr (OUT) {
+    {
       // C B^T, once for all strips: the ten 16 x 16 blocks at or under the diagonal, rows j by lanes i, by the waves that
       // have no steps to compute
       const int lane = tile::fresh(threadIdx.x & 63);
@@ -236,36 +352,8 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
       }
     }
     lds_barrier();
-    if constexpr (OUT) k0 = st.G[col], k1 = st.G[32 + col];
-    auto state = [&] {  // the state behind the piece
-      const float keep = exp2_(st.total);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) S[t][e] *= keep;
-      // each 16 rows' operands are read beside the products of the 16 before
-      u32x4 bt[2][NT], xk[2];
-      xk[0] = tile::col_frag<128>(Xt, xb, 0, xcol);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) bt[0][t] = tile::col_frag<N>(Bt, cb, 0, t);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        Split<kParts> xw;
-        xw.make(xk[k & 1], st.w + 16 * k + 4 * half, st.w + 16 * k + 8 + 4 * half);
-        __builtin_amdgcn_sched_barrier(0);
-        if (k < 3) {
-          xk[(k + 1) & 1] = tile::col_frag<128>(Xt, xb, 16 * (k + 1), xcol);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) bt[(k + 1) & 1][t] = tile::col_frag<N>(Bt, cb, 16 * (k + 1), t);
-        }
-#pragma unroll
-        for (int q = 0; q < kParts; ++q)
-#pragma unroll
-          for (int t = 0; t < NT; ++t) S[t] = tile::mma(bt[k & 1][t], xw.part[q], S[t]);
-        stage_some(k);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    };
+    k0 = st.G[col], k1 = st.G[32 + col];
+    auto state = [&] { add_piece<N>(S, Bt, Xt, xcol, cb, xb, st, half, stage_some); };
     auto result = [&] {
       // addresses and masks are computed here, not kept over the loop
       const int lane = tile::fresh(threadIdx.x & 63), half = lane >> 5, col = lane & 31;
@@ -339,32 +427,15 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
       }
       __builtin_amdgcn_sched_barrier(0);
     };
-    whole += st.total;
     // The waves of a SIMD take the two in different orders, so that one's products run beside the other's arithmetic.
-    if constexpr (OUT) {
 #pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
-        if (i == wave / (kWaves / 2)) result();
-        else state();
-      }
-    } else {
-      state();
+    for (int i = 0; i < 2; ++i) {
+      if (i == wave / (kWaves / 2)) result();
+      else state();
     }
-    if constexpr (OUT) {
-      if (cur.last && p.S_final && mine) store_state<NT>(S, const_cast<float*>(state_at(p.S_final, cur.seq)), p.P);
-    }
+    if (cur.last && p.S_final && mine) store_state<NT>(S, const_cast<float*>(state_at(p.S_final, cur.seq)), p.P);
     cur = nxt;
     z = z_next;
-  }
-  if constexpr (!OUT) {
-    if (mine) {
-      f32x4* at = slot(seg);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) at[(4 * t + q) * 64] = f32x4{S[t][4 * q], S[t][4 * q + 1], S[t][4 * q + 2], S[t][4 * q + 3]};
-      if (threadIdx.x % 128 == 0) kept[(size_t)seg * nstrips + strip] = fresh ? kFresh : whole;
-    }
   }
 }
 
@@ -413,14 +484,14 @@ hipError_t launch_ssm_scan(const ScanArgs& a) {
   auto go = [&](auto nn, auto per) {
     constexpr int N = decltype(nn)::value, NS = decltype(per)::value;
     if (nseg > 1) {
-      hipLaunchKernelGGL((scan_kernel<N, NS, false>), dim3(c.sets, nseg - 1), dim3(128 * NS), 0, st, p);
+      hipLaunchKernelGGL((ends_kernel<N, NS>), dim3(c.sets, nseg - 1), dim3(192 * NS), 0, st, p);
       if (const hipError_t e = hipGetLastError()) return e;
       if (p.joined) {
         hipLaunchKernelGGL((join_kernel<N>), dim3(N * 64 / 1024, nstrips), dim3(256), 0, st, a.ws, nstrips, nseg - 1);
         if (const hipError_t e = hipGetLastError()) return e;
       }
     }
-    hipLaunchKernelGGL((scan_kernel<N, NS, true>), dim3(c.sets, nseg), dim3(128 * NS), 0, st, p);
+    hipLaunchKernelGGL((scan_kernel<N, NS>), dim3(c.sets, nseg), dim3(128 * NS), 0, st, p);
     return hipGetLastError();
   };
   auto sized = [&](auto nn) { return c.ns == 4 ? go(nn, pipe::ic<4>{}) : go(nn, pipe::ic<2>{}); };
