@@ -19,20 +19,23 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 
 // log(1 + e^z), to a few units of float32's last place also where it is small: the
 // series of log(1 + e) for e below 1/16, otherwise the logarithm of u = 1 + e with what
-// the sum's rounding lost.
+// the sum's rounding lost.  NaN is NaN, here and below.
 __device__ __forceinline__ float softplus(float z) {
   const float e = exp2_(fminf(z, 20.f) * kLog2e), u = 1.f + e;
   const float large = __builtin_fmaf(__builtin_amdgcn_logf(u), 0.6931471805599453f, (e - (u - 1.f)) * __builtin_amdgcn_rcpf(u));
   float small = -1.f / 8;
 #pragma unroll
   for (int n = 7; n; --n) small = __builtin_fmaf(small, e, n % 2 ? 1.f / n : -1.f / n);
-  return z > 20.f ? z : e < 0.0625f ? small * e : large;
+  return !(z <= 20.f) ? z : e < 0.0625f ? small * e : large;
 }
 
 // What a row does to the state, in powers of two: steps of less than 2^-160 are
 // taken for that, since 2^-160 of any float32 number is below the smallest; so the
 // sums over a piece stay below 2^14 and their differences exact to 2^-10.
-__device__ __forceinline__ float log2_keep(float a, float delta) { return fmaxf(a * kLog2e * delta, -160.f); }
+__device__ __forceinline__ float log2_keep(float a, float delta) {
+  const float g = a * kLog2e * delta;
+  return g < -160.f ? -160.f : g;
+}
 
 // Columns of x are taken 64 at a time ("strips"): a head of P = 64 or half of one of
 // 128, whose recurrence runs by itself.  Workgroups take NS neighbouring strips of
@@ -49,10 +52,8 @@ __host__ __device__ inline Strips strips(int H, int P, int G, int NS) {
 // ------------------------------------------------------------------- staging
 // Rows of D values to LDS as tile::Stage puts them, one load (of LOADS) at a time.  As
 // assembly: a load to LDS that the compiler knows of makes it wait for all such loads
-// before whatever it reads from LDS next, of another buffer too, so that nothing would
-// run beside them (7 pieces of 64 rows x 4 x 64 channels, N = 128, a workgroup: 66 us
-// for 37).  The load has no result in a register; its arrival is waited for by
-// tile::staged_barrier().  M0, which nothing else here is kept in, is the address in LDS.
+// before whatever it reads from LDS next, of another buffer too, so that no load would
+// run beside the products.
 struct Source {
   u32x4 rsrc;
 };
@@ -62,13 +63,17 @@ __device__ __forceinline__ Source source(const void* base, long long stride, lon
   return {u32x4{(unsigned)__builtin_amdgcn_readfirstlane((int)at), (unsigned)__builtin_amdgcn_readfirstlane((int)(at >> 32)) & 0xffffu,
                 (unsigned)__builtin_amdgcn_readfirstlane((int)bytes), (unsigned)pipe::kRsrcWord3}};
 }
-// 64 pieces of 16 bytes, `ahead` bytes behind src, to consecutive LDS.
+// 64 pieces of 16 bytes, `ahead` bytes behind src, to consecutive LDS.  The load has no
+// result in a register, and takes its addresses as it is issued; that it has arrived is
+// waited for by tile::staged_barrier() and nothing reads its part of LDS before.  M0 is
+// the address in LDS.  Five waits between a vector instruction that may have written a
+// scalar operand and the load are the assembly's own to keep, and one behind M0.
 __device__ __forceinline__ void load_piece(__bf16* lds, const Source& src, unsigned off, int ahead) {
   const unsigned at = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(unsigned long long)(tile::lds_void*)lds);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(at), "v"(off), "s"(src.rsrc), "s"(ahead)
-               : "memory");
+               : "memory", "m0");
 }
 template <int D, int N, int NW> struct Stage : tile::Stage<D, N, NW> {
   typedef tile::Stage<D, N, NW> Base;
@@ -329,7 +334,7 @@ template <int NT> __device__ __forceinline__ void store_state(const f32x16 (&S)[
 // kNone where no sequence crosses the slot's border, kFresh where the one that does
 // began (ended) in the segment.  Slot s becomes the state at the border; `back` from
 // the last to the first.
-constexpr float kNone = 1.f, kFresh = 2.f;
+constexpr float kNone = 3e38f, kFresh = 2e38f;
 template <int N> __device__ __forceinline__ void join(float* ws, int nstrips, int slots, int strip, int i, bool back) {
   const ptrdiff_t step = (ptrdiff_t)nstrips * N * 64;
   const float* kept = ws + slots * step + strip + (back ? (ptrdiff_t)(slots - 1) * nstrips : 0);

@@ -19,8 +19,7 @@
 // Where numbers are rounded: C B^T o L between the two halves of a piece, and the state
 // as it enters the product with C, to bf16 (2^-9 of each term); C B^T o L within a half,
 // where the weights are largest, in two parts (2^-17: with one, the relative error of
-// short sequences' results was 2.5e-3 for 2.0e-3, of which the result's own rounding
-// is 1.65e-3); what goes into the state in three parts, 2^-25, since the state is a
+// the result was 2.3e-3 for 1.7e-3, of which the result's own rounding is 1.65e-3); what goes into the state in three parts, 2^-25, since the state is a
 // result and is carried on.
 #include "gdn_scan.hpp"
 
