@@ -733,7 +733,7 @@ Plan plan(int T, int R, int H, int P, int G, int N) {
   // would be as long as each other and as a number of pieces, whole ones, whose states need not be joined
   const int want = nstrips >= 192 ? 1 : 192 / nstrips;
   int per = (w.blocks + want - 1) / want;
-  if (R > 1 && T % R == 0 && T / R % Q == 0 && 2 * (T / R) >= per * Q && T / R <= 2 * per * Q) per = T / R / Q;
+  if (want > 1 && R > 1 && T % R == 0 && T / R % Q == 0 && 2 * (T / R) >= per * Q && T / R <= 2 * per * Q) per = T / R / Q;
   if (per < 4) per = 4;
   w.seg = per * Q;
   w.nseg = T > w.seg ? (T + w.seg - 1) / w.seg : 1;
