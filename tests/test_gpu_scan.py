@@ -224,3 +224,190 @@ def test_scan_gradients(name, cu, t, h, p, g, n):
         for lo, hi in zip(cu, cu[1:]):
             inside[lo:hi] = True
         assert not any(down(got[k])[~inside].any() for k in (0, 1, 3, 4))
+
+
+# --------------------------------------------------------------- larger forms
+@pytest.mark.parametrize("name,cu,h,p,g,n", [
+    ("four strips to a workgroup, segments", [0, 700, 701, 1200], 128, 64, 1, 64),
+    ("many segments of one sequence, joined by a launch", [0, 2300], 1, 64, 1, 64),
+    ("a segment's end is a sequence's", [0, 256, 512, 512, 700, 1024], 2, 64, 1, 128),
+    ("more offsets than LDS holds", [min(i, 555) for i in range(601)], 2, 64, 1, 64),
+    ("groups of five strips", [0, 90, 300], 10, 64, 2, 64),
+    ("many groups", [0, 100], 40, 64, 40, 64)])
+def test_scan_forms(name, cu, h, p, g, n):
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    note(f"scan {name}")
+    c = Case(torch, cu, cu[-1], h, p, g, n, slow=True)
+    out, last = gdn.ssm_scan(*c.args(), c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0)
+    check(c, out, last, 2 + cu[-1] // 64)
+
+
+@pytest.mark.parametrize("name,cu,h,p,g,n", [
+    ("many segments", [0, 1100, 1101, 1400], 2, 64, 1, 64), ("sequences as segments", [0, 512, 1024], 1, 64, 1, 64),
+    ("more heads than one run takes", [0, 70], 70, 64, 1, 64), ("more offsets than LDS holds", list(range(0, 560, 4)), 2, 64, 1, 64),
+    ("wide heads of one group", [0, 100, 200], 5, 128, 1, 128)])
+def test_scan_gradients_of_forms(name, cu, h, p, g, n):
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    note(f"scan gradients {name}")
+    t = cu[-1]
+    c = Case(torch, cu, t, h, p, g, n, slow=True)
+    go = torch.from_numpy(np.random.default_rng(1).standard_normal((t, h, p)).astype(np.float32)).to(torch.bfloat16).cuda()
+    gl = torch.from_numpy(np.random.default_rng(2).standard_normal((len(cu) - 1, h, n, p)).astype(np.float32)).cuda()
+    got = gdn.ssm_scan_bwd(*c.args(), go, c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0, grad_S_final=gl)
+    check_gradients(c, got, down(go).astype(np.float64), down(gl).astype(np.float64))
+    again = gdn.ssm_scan_bwd(*c.args(), go, c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0, grad_S_final=gl)
+    assert all(torch.equal(u, v) for u, v in zip(got, again))  # sums in a fixed order
+
+
+# ------------------------------------------------------------------- extremes
+def test_steps_of_all_sizes():
+    """Steps from none to hundreds: decays that forget everything at once, and states that stay for good."""
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    t, h = 200, 4
+    c = Case(torch, [0, 150, t], t, h, 64, 1, 64, dt="f32", param="f32")
+    c.dt = torch.tensor([-200.0, -30.0, 0.0, 300.0], device="cuda")[torch.arange(t * h, device="cuda").view(t, h) * 7 % 4].contiguous()
+    c.bias.zero_()
+    c.x = (c.x / 64).contiguous()
+    out, last = gdn.ssm_scan(*c.args(), c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0)
+    check(c, out, last, 5)
+    go = torch.randn(t, h, 64, device="cuda").to(torch.bfloat16)
+    got = gdn.ssm_scan_bwd(*c.args(), go, c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0)
+    assert all(torch.isfinite(v).all() for v in got)
+    S = c.S0.clone()
+    one = [v if k == "a" else v[:2] for k, v in zip(c.names, c.args())]
+    assert torch.isfinite(gdn.ssm_step(*one, S, D=c.D, dt_bias=c.bias)).all() and torch.isfinite(S).all()
+
+
+def test_a_step_of_zero_has_the_slope_of_softplus():
+    """softplus'(0) = 1/2: dt and bias that cancel."""
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    c = Case(torch, [0, 80], 80, 2, 64, 1, 64, dt="f32", param="f32")
+    c.dt = (-c.bias).expand(80, 2).contiguous()
+    go = torch.from_numpy(np.random.default_rng(4).standard_normal((80, 2, 64)).astype(np.float32)).to(torch.bfloat16).cuda()
+    got = gdn.ssm_scan_bwd(*c.args(), go, c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0)
+    check_gradients(c, got, down(go).astype(np.float64), None)
+
+
+def test_without_the_optional_parts():
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    c = Case(torch, [0, 100], 100, 3, 64, 1, 64, state=False)
+    zero = torch.zeros_like(c.D)
+    out, last = gdn.ssm_scan(*c.args(), c.offsets)
+    want, want_last = gdn.ssm_scan(*c.args(), c.offsets, D=zero, dt_bias=zero, S0=torch.zeros_like(last))
+    assert torch.equal(out, want) and torch.equal(last, want_last)
+    go = torch.randn_like(out)
+    got = gdn.ssm_scan_bwd(*c.args(), go, c.offsets)
+    want = gdn.ssm_scan_bwd(*c.args(), go, c.offsets, D=zero, dt_bias=zero)
+    assert all(torch.equal(u, v) for u, v in zip(got[:5], want[:5])) and got[5:] == (None, None, None)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_what_is_not_finite_stays_in_its_sequence(bad):
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    cu, t = [0, 100, 130, 400], 400
+    c = Case(torch, cu, t, 4, 64, 2, 128)
+    go = torch.randn(t, 4, 64, device="cuda").to(torch.bfloat16)
+    run = lambda: (*gdn.ssm_scan(*c.args(), c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0),  # noqa: E731
+                   gdn.ssm_scan_bwd(*c.args(), go, c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0))
+    out, last, grads = run()
+    for name in ("x", "B", "C", "dt"):
+        v = getattr(c, name)
+        kept = v.clone()
+        v[110] = bad
+        out2, last2, grads2 = run()
+        v[110] = kept[110]
+        rest = torch.tensor([i for i in range(t) if not 100 <= i < 130], device="cuda")
+        assert torch.equal(out2[rest], out[rest]) and torch.equal(last2[[0, 2]], last[[0, 2]]), name
+        assert all(torch.equal(grads2[k][rest], grads[k][rest]) for k in (0, 1, 3, 4)) and torch.equal(grads2[7][[0, 2]], grads[7][[0, 2]]), name
+
+
+@pytest.mark.parametrize("cu", [[-5, 30, 2 ** 31 - 1], [90, 20, 300], [-2 ** 31, 2 ** 31 - 1], [400, 500, 600], [0, 2 ** 31 - 1, 5]])
+def test_offsets_that_lead_outside(cu):
+    """Nothing outside the buffers is read or written."""
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    note(f"scan offsets {cu}")
+    t, h, R = 300, 2, len(cu) - 1
+    c = Case(torch, cu, t, h, 64, 1, 64)
+    big = torch.full((3 * t, h, 64), 5.0, device="cuda", dtype=torch.bfloat16)
+    gdn.ssm_scan(*c.args(), c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0, out=big[t:2 * t])
+    gx = torch.full((3 * t, h, 64), 5.0, device="cuda", dtype=torch.bfloat16)
+    gb = torch.full((3 * t, 2, 64), 5.0, device="cuda", dtype=torch.bfloat16)
+    gdn.ssm_scan_bwd(*c.args(), c.x.contiguous(), c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0, grad_S_final=c.S0, grad_x=gx[t:2 * t],
+                     grad_B=gb[t:2 * t, :1], grad_C=gb[t:2 * t, 1:])
+    torch.cuda.synchronize()
+    for v in (big, gx, gb):
+        assert (v[:t] == 5).all() and (v[2 * t:] == 5).all()
+
+
+def test_given_outputs():
+    """Gradients as parts of one tensor; what stands in rows of no sequence, and behind the parts, stays."""
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    t, h, g, n = 90, 4, 2, 64
+    c = Case(torch, [10, 50, 80], t, h, 64, g, n)
+    go = torch.randn(t, h, 64, device="cuda").to(torch.bfloat16)
+    more = dict(D=c.D, dt_bias=c.bias, S0=c.S0)
+    want = gdn.ssm_scan_bwd(*c.args(), go, c.offsets, **more)
+    rows = torch.full((t, h * 64 + 2 * g * n + 16), 3.0, device="cuda", dtype=torch.bfloat16)
+    gx, gB, gC = rows[:, :h * 64].view(t, h, 64), rows[:, h * 64:h * 64 + g * n].view(t, g, n), rows[:, h * 64 + g * n:-16].view(t, g, n)
+    got = gdn.ssm_scan_bwd(*c.args(), go, c.offsets, **more, grad_x=gx, grad_B=gB, grad_C=gC)
+    assert got[0] is gx and all(torch.equal(u[10:80], v[10:80]) for u, v in zip(got[:5], want[:5]) if u.dim() > 1)
+    assert (rows[:10] == 3).all() and (rows[80:] == 3).all() and (rows[:, -16:] == 3).all()
+    out = torch.full((t, h, 64), 3.0, device="cuda", dtype=torch.bfloat16)
+    last = torch.empty_like(c.S0)
+    a, b = gdn.ssm_scan(*c.args(), c.offsets, **more, out=out, S_final=last)
+    w, wl = gdn.ssm_scan(*c.args(), c.offsets, **more)
+    assert a is out and b is last and torch.equal(out[10:80], w[10:80]) and torch.equal(last, wl)
+    assert (out[:10] == 3).all() and (out[80:] == 3).all()
+
+
+def test_refusals():
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    c = Case(torch, [0, 20], 20, 4, 64, 2, 64)
+    x, dt, a, B, C = c.args()
+    with pytest.raises(TypeError):
+        gdn.ssm_scan(x.float(), dt, a, B, C, c.offsets)
+    with pytest.raises(TypeError):
+        gdn.ssm_scan(x, dt.to(torch.float16), a, B, C, c.offsets)
+    with pytest.raises(TypeError):
+        gdn.ssm_scan(x, dt, a, B, C, c.offsets, D=c.D.float())
+    with pytest.raises(TypeError):
+        gdn.ssm_scan(x, dt, a, B, C, c.offsets, S0=c.S0.to(torch.bfloat16))
+    for call in (lambda: gdn.ssm_scan(x, dt, a, B, C[:, :1], c.offsets), lambda: gdn.ssm_scan(x, dt[:, :2], a, B, C, c.offsets),
+                 lambda: gdn.ssm_scan(x, dt, a[:2], B, C, c.offsets), lambda: gdn.ssm_scan(x.transpose(0, 1), dt, a, B, C, c.offsets),
+                 lambda: gdn.ssm_scan(x, dt, a, B, C, c.offsets[:0]), lambda: gdn.ssm_scan(x, dt, a, B, C, c.offsets, S0=c.S0[:, :2]),
+                 lambda: gdn.ssm_scan(x, dt.t().contiguous().t(), a, B, C, c.offsets),
+                 lambda: gdn.ssm_scan_bwd(x, dt, a, B, C, x[:, :2], c.offsets), lambda: gdn.ssm_step(x, dt, a, B, C, c.S0)):
+        with pytest.raises(ValueError):
+            call()
+    for h, g, n, status in ((3, 2, 64, gdn.gdn.GDN_ERR_SHAPE), (4, 2, 48, gdn.gdn.GDN_ERR_UNSUPPORTED)):
+        z = torch.zeros(20, g, n, device="cuda", dtype=torch.bfloat16)
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.ssm_scan(x[:, :h].contiguous(), dt[:, :h].contiguous(), a[:h].contiguous(), z, z, c.offsets)
+        assert e.value.status == status
+
+
+@pytest.mark.parametrize("name", ["dt", "a", "dt_bias"])
+def test_nan_is_not_hidden(name):
+    """A step or a rate that is NaN gives NaN from its row on, in the scan and in the step."""
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    c = Case(torch, [0, 100], 100, 2, 64, 1, 64, dt="f32", param="f32")
+    if name == "dt":
+        c.dt[40, 1] = float("nan")
+    else:
+        (c.a if name == "a" else c.bias)[1] = float("nan")
+    out, last = gdn.ssm_scan(*c.args(), c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0)
+    assert torch.isnan(out[40:, 1]).all() and torch.isnan(last[:, 1]).all() and torch.isfinite(out[:, 0]).all() and torch.isfinite(last[:, 0]).all()
+    S = c.S0.clone()
+    one = [v if k == "a" else v[40:41] for k, v in zip(c.names, c.args())]
+    y = gdn.ssm_step(*one, S, D=c.D, dt_bias=c.bias)
+    assert torch.isnan(y[:, 1]).all() and torch.isnan(S[:, 1]).all() and torch.isfinite(y[:, 0]).all() and torch.isfinite(S[:, 0]).all()
