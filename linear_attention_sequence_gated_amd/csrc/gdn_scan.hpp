@@ -49,6 +49,14 @@ __host__ __device__ inline Strips strips(int H, int P, int G, int NS) {
   return {per, (per + NS - 1) / NS};
 }
 
+// A workgroup's number among `all`, such that consecutive ones share an XCD and its L2,
+// and with it the rows that they all read: the hardware deals workgroups to the eight
+// XCDs in turn (8 x 2048 rows x 24 heads of 64: 72 us for the scan, so 69).
+__device__ __forceinline__ int neighbours(int id, int all) {
+  const int xcd = id & 7;
+  return xcd * (all >> 3) + min(xcd, all & 7) + (id >> 3);
+}
+
 // ------------------------------------------------------------------- staging
 // Rows of D values to LDS as tile::Stage puts them, one load (of LOADS) at a time.  As
 // assembly: a load to LDS that the compiler knows of makes it wait for all such loads
@@ -106,6 +114,11 @@ template <int D> struct StageWave {
     for (int i = 0; i < R / kRows; ++i) load_piece(lds + i * 512, src, off[i % kOff], ahead + i / kOff * step);
   }
 };
+
+// A barrier behind which all but this wave's last KEEP loads have arrived.
+template <int KEEP> __device__ __forceinline__ void loads_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(KEEP) : "memory");
+}
 
 // x, which has arrived when this is reached.  What a load brought has to be asked for
 // before the next loads to LDS are issued: the compiler, which does not know of those,

@@ -50,6 +50,16 @@ struct ScanParams {
   bool dt_f32, p_f32, zero_rest, joined;
 };
 
+// A workgroup's part of the work: those of a segment, which read the same rows of B and
+// C, are neighbours.
+struct Where {
+  int seg, group, set;
+};
+__device__ __forceinline__ Where where(const ScanParams& p, const Strips& sp, int segs) {
+  const int per = p.G * sp.sets, id = neighbours(blockIdx.x, per * segs);
+  return {id / per, id % per / sp.sets, id % sp.sets};
+}
+
 // The workspace: the states of [segments - 1][strips][N][64], then what each segment
 // keeps (see join).
 // Where four values (j a multiple of 4) of a row i of C B^T lie in LDS: 16-byte pieces
@@ -104,7 +114,8 @@ __global__ __launch_bounds__(192 * NS, 1) void ends_kernel(ScanParams p) {
   const bool helper = wave >= 2 * NS;
   const int mine_of = helper ? wave - 2 * NS : wave / 2;  // strip of the set
   const Strips sp = strips(p.H, p.P, p.G, NS);
-  const int group = blockIdx.x / sp.sets, set = blockIdx.x % sp.sets, seg = blockIdx.y;
+  const Where wg = where(p, sp, p.nseg - 1);
+  const int group = wg.group, set = wg.set, seg = wg.seg;
   const int here = min(NS, sp.per_group - set * NS), strip0 = group * sp.per_group + set * NS;
   const bool mine = mine_of < here;
   const int strip = strip0 + (mine ? mine_of : 0), spp = p.P / 64, head = strip / spp, hcol = (strip % spp) * 64 + (wave & 1) * 32;
@@ -198,7 +209,8 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, col = lane & 31;
 
   const Strips sp = strips(p.H, p.P, p.G, NS);
-  const int group = blockIdx.x / sp.sets, set = blockIdx.x % sp.sets, seg = blockIdx.y;
+  const Where wg = where(p, sp, p.nseg);
+  const int group = wg.group, set = wg.set, seg = wg.seg;
   const int in_group = set * NS, here = min(NS, sp.per_group - in_group);
   const int strip0 = group * sp.per_group + in_group;
   const bool mine = wave / 2 < here;  // otherwise the wave follows the first strip and writes nothing
@@ -483,14 +495,14 @@ hipError_t launch_ssm_scan(const ScanArgs& a) {
   auto go = [&](auto nn, auto per) {
     constexpr int N = decltype(nn)::value, NS = decltype(per)::value;
     if (nseg > 1) {
-      hipLaunchKernelGGL((ends_kernel<N, NS>), dim3(c.sets, nseg - 1), dim3(192 * NS), 0, st, p);
+      hipLaunchKernelGGL((ends_kernel<N, NS>), dim3(c.sets * (nseg - 1)), dim3(192 * NS), 0, st, p);
       if (const hipError_t e = hipGetLastError()) return e;
       if (p.joined) {
         hipLaunchKernelGGL((join_kernel<N>), dim3(N * 64 / 1024, nstrips), dim3(256), 0, st, a.ws, nstrips, nseg - 1);
         if (const hipError_t e = hipGetLastError()) return e;
       }
     }
-    hipLaunchKernelGGL((scan_kernel<N, NS>), dim3(c.sets, nseg), dim3(128 * NS), 0, st, p);
+    hipLaunchKernelGGL((scan_kernel<N, NS>), dim3(c.sets * nseg), dim3(128 * NS), 0, st, p);
     return hipGetLastError();
   };
   auto sized = [&](auto nn) { return c.ns == 4 ? go(nn, pipe::ic<4>{}) : go(nn, pipe::ic<2>{}); };

@@ -70,26 +70,31 @@ struct BwdParams {
 // the one of this number.
 __device__ __forceinline__ int state_piece(int n, int c) { return (n / 32 * 4 + c / 2) * 64 + (c & 1) * 32 + n % 32; }
 
-// A workgroup: one strip, one segment; blockIdx.z: states downwards, or their
-// gradients upwards.  A wave has 32 n and 64 channels (N = 64: 32 of them) of
-// the transposed state: its lanes the n, its elements the channels, eight in a row to
-// a lane: a 16-byte piece of the stored state.  Stored are a wave's pieces as they
-// are, 1 KB at a time (see state_piece).  What the rows add is weighted on the side of
-// B (C), in PARTS bf16 parts.  A fifth wave brings the rows of the piece to come and
-// computes its steps, so that the four have nothing but their products to wait for.
-constexpr int kStateThreads = 320;
+// A workgroup: 64 n of one strip, one segment; states downwards, or their
+// gradients upwards.  Two waves have 32 n and 64 channels each of the transposed
+// state: their lanes the n, their elements the channels, eight in a row to a lane: a
+// 16-byte piece of the stored state.  Stored are a wave's pieces as they are, 1 KB at a
+// time (see state_piece).  What the rows add is weighted on the side of B (C), in PARTS
+// bf16 parts, once.  A third wave brings the rows of the piece after next, and a fourth
+// computes the next one's steps, so that the two have nothing but their products to
+// wait for.  The states go to memory: 8 x 2048 rows x 24 strips, N = 128, write 208 MB
+// and read 110 in 85 us; 13 sequences of up to 1201 rows x 32 strips, N = 64, took 55 us
+// with a piece's rows one piece ahead and four waves of 32 x 32, now 50.
+constexpr int kStateThreads = 256, kHalf = 64;  // n to a workgroup
 template <int N, bool LOCAL, int PARTS>
 __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
-  constexpr int NP = N == 128 ? 2 : 1;  // tiles of 32 channels to a wave
-  __shared__ __attribute__((aligned(1024))) __bf16 buf[2][Q * N + Q * 64];
+  constexpr int NP = 2, kParts = N / kHalf;  // tiles of 32 channels to a wave; workgroups to a strip
+  __shared__ __attribute__((aligned(1024))) __bf16 buf[3][Q * kHalf + Q * 64];
   __shared__ Steps st_two[2];
   __shared__ int window[kWindow];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, col = lane & 31;
-  const int nt = N == 128 ? wave & 3 : wave & 1, pt0 = N == 128 ? 0 : (wave >> 1) & 1;
-  const int strip = blockIdx.x, spp = p.P / 64, head = strip / spp, hcol = (strip % spp) * 64, group = head / (p.H / p.G);
-  const int nstrips = p.H * spp;
-  const bool up = blockIdx.z != 0;
-  const int seg = LOCAL && up ? blockIdx.y + 1 : blockIdx.y;
+  const int spp = p.P / 64, nstrips = p.H * spp, per = nstrips * kParts, slots = p.nseg - LOCAL;
+  // the two halves of a strip, which read the same x, lie nstrips apart: on one XCD where that is a multiple of eight
+  const int id = blockIdx.x, seg0 = id / per % slots;
+  const bool up = id >= per * slots;
+  const int strip = id % nstrips, n0 = id % per / nstrips * kHalf, nt = n0 / 32 + (wave & 1), head = strip / spp;
+  const int hcol = (strip % spp) * 64, group = head / (p.H / p.G);
+  const int seg = LOCAL && up ? seg0 + 1 : seg0;
   const float a = param(p.a, p.p_f32, head), bias = p.bias ? param(p.bias, p.p_f32, head) : 0.f;
   const Offsets cu = offsets<kStateThreads>(p.cu, p.R, window);
   const int s0 = seg * p.seg, s1 = min(s0 + p.seg, p.T);
@@ -106,7 +111,7 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
     for (int t = 0; t < NP; ++t)
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const float4* q = reinterpret_cast<const float4*>(src + n * stride + 32 * (pt0 + t) + 16 * b + 8 * half);
+        const float4* q = reinterpret_cast<const float4*>(src + n * stride + 32 * t + 16 * b + 8 * half);
         const float4 u = q[0], v = q[1];
         S[t][8 * b] = u.x, S[t][8 * b + 1] = u.y, S[t][8 * b + 2] = u.z, S[t][8 * b + 3] = u.w;
         S[t][8 * b + 4] = v.x, S[t][8 * b + 5] = v.y, S[t][8 * b + 6] = v.z, S[t][8 * b + 7] = v.w;
@@ -117,7 +122,7 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
     for (int t = 0; t < NP; ++t)
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        float4* q = reinterpret_cast<float4*>(dst + n * stride + 32 * (pt0 + t) + 16 * b + 8 * half);
+        float4* q = reinterpret_cast<float4*>(dst + n * stride + 32 * t + 16 * b + 8 * half);
         q[0] = make_float4(S[t][8 * b], S[t][8 * b + 1], S[t][8 * b + 2], S[t][8 * b + 3]);
         q[1] = make_float4(S[t][8 * b + 4], S[t][8 * b + 5], S[t][8 * b + 6], S[t][8 * b + 7]);
       }
@@ -149,7 +154,7 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
       fresh = b >= s0;
     }
     if (!crosses) {
-      if (threadIdx.x == 0) kept[(size_t)blockIdx.y * nstrips + strip] = kNone;
+      if (threadIdx.x == 0 && n0 == 0) kept[(size_t)seg0 * nstrips + strip] = kNone;
       return;
     }
   } else if (up) {
@@ -158,8 +163,8 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
       for (int r = k0; r < k1; ++r) {
         const int b = min(max(cu(r), 0), p.T);
         if (min(cu(r + 1), p.T) > b) continue;
-        for (int i = threadIdx.x; i < N * 64; i += kStateThreads) {
-          const long long at = of_seq(r) + (long long)(i / 64) * p.P + i % 64;
+        for (int i = threadIdx.x; i < kHalf * 64; i += kStateThreads) {
+          const long long at = of_seq(r) + (long long)(n0 + i / 64) * p.P + i % 64;
           p.gS0[at] = p.gSf ? p.gSf[at] : 0.f;
         }
       }
@@ -169,13 +174,13 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
     load(slot(seg - 1), 64);
   }
 
-  StageWave<N> sk;
+  StageWave<kHalf> sk;
   StageWave<64> sv;
-  const __bf16* kg = (up ? static_cast<const __bf16*>(p.C) : static_cast<const __bf16*>(p.B)) + group * N;
+  const __bf16* kg = (up ? static_cast<const __bf16*>(p.C) : static_cast<const __bf16*>(p.B)) + group * N + n0;
   const __bf16* vg = (up ? static_cast<const __bf16*>(p.go) : static_cast<const __bf16*>(p.x)) + strip * 64;
   const long long ks = up ? p.cs : p.bs, vs = up ? p.gs : p.xs;
   sk.init(ks), sv.init(vs);
-  const bool helper = wave == 4;
+  const bool loads = wave == 2, steps_mine = wave == 3;
   auto raw_dt = [&](const Piece& pc) { return lane < pc.n ? dt_bits(p.dt, p.dt_f32, (long long)(pc.row + lane) * p.dts + head) : 0u; };
   auto take_steps = [&](int b, unsigned bits, const Piece& pc) {
     Steps& st = st_two[b];
@@ -190,38 +195,47 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
     if (!some) pc.row = pc.n = 0;
     return some;
   };
-  const int kb = tile::col_base<N>(lane), vb = col_base_state<64>(lane);
+  const int kb = tile::col_base<kHalf>(lane), vb = col_base_state<64>(lane);
   auto stage = [&](int b, const Piece& pc) {
-    sk.template load<Q>(buf[b], source(kg, ks, pc.row, pc.n, N), 0);
-    sv.template load<Q>(buf[b] + Q * N, source(vg, vs, pc.row, pc.n, 64), 0);
+    sk.template load<Q>(buf[b], source(kg, ks, pc.row, pc.n, kHalf), 0);
+    sv.template load<Q>(buf[b] + Q * kHalf, source(vg, vs, pc.row, pc.n, 64), 0);
   };
 
   Piece cur, nxt, nx2;
   bool more = next(cur), more2 = more && next(nxt);
   if (!more2) nxt.row = nxt.n = 0;
-  unsigned bits = 0;  // dt of the next piece: the helper's
-  if (more && helper) {
-    const unsigned first = raw_dt(cur);
-    bits = raw_dt(nxt);
-    take_steps(0, first, cur);
-    stage(0, cur);
-  }
-  for (int b = 0; more; b ^= 1) {
-    tile::staged_barrier();
-    const bool more3 = more2 && next(nx2);
-    if (!more3) nx2.row = nx2.n = 0;
-    if (helper) {
-      bits = arrived(bits);
-      const unsigned after = raw_dt(nx2);
-      if (more2) {
-        stage(b ^ 1, nxt);
-        take_steps(b ^ 1, bits, nxt);
-      }
-      bits = after;
-      cur = nxt, nxt = nx2;
-      more = more2, more2 = more3;
-      continue;
+  auto advance = [&](bool more3) { cur = nxt, nxt = nx2, more = more2, more2 = more3; };
+  if (loads) {
+    tile::wait_all_but<0>();  // counted below are staged loads alone
+    if (more) stage(0, cur);
+    if (more2) stage(1, nxt);
+    for (int to = 2; more; to = to == 2 ? 0 : to + 1) {
+      // this piece's rows are here; the next one's, the latest loads, may be on their way
+      if (more2) loads_barrier<(Q * kHalf + Q * 64) / 512>();
+      else loads_barrier<0>();
+      const bool more3 = more2 && next(nx2);
+      if (more3) stage(to, nx2);
+      advance(more3);
     }
+    return;
+  }
+  if (steps_mine) {
+    unsigned bits = raw_dt(nxt);
+    if (more) take_steps(0, raw_dt(cur), cur);
+    for (int b = 0; more; b ^= 1) {
+      lds_barrier();
+      const bool more3 = more2 && next(nx2);
+      if (!more3) nx2.row = nx2.n = 0;
+      const unsigned after = raw_dt(nx2);
+      if (more2) take_steps(b ^ 1, bits, nxt);
+      bits = after;
+      advance(more3);
+    }
+    return;
+  }
+  for (int b = 0, at = 0; more; b ^= 1, at = at == 2 ? 0 : at + 1) {
+    lds_barrier();
+    const bool more3 = more2 && next(nx2);
     const Steps& st = st_two[b];
     if (up ? cur.last : cur.first) {
       const float* src = up ? p.gSf : p.S0;
@@ -232,7 +246,7 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
       }
     }
     if constexpr (!LOCAL) {
-      u32x4* dst = reinterpret_cast<u32x4*>(p.states[up] + ((long long)piece_id(cur) * nstrips + strip) * N * 64) + nt * 256 + pt0 * 128 + lane;
+      u32x4* dst = reinterpret_cast<u32x4*>(p.states[up] + ((long long)piece_id(cur) * nstrips + strip) * N * 64) + nt * 256 + lane;
 #pragma unroll
       for (int t = 0; t < NP; ++t)
 #pragma unroll
@@ -240,7 +254,7 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
     }
     const float total = st.total;
     whole += total;
-    const __bf16 *Kt = buf[b], *Vt = buf[b] + Q * N;
+    const __bf16 *Kt = buf[at], *Vt = buf[at] + Q * kHalf;
     const float keep = exp2_(total);
 #pragma unroll
     for (int t = 0; t < NP; ++t)
@@ -249,10 +263,10 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       Split<PARTS> kw;
-      kw.make(tile::col_frag<N>(Kt, kb, 16 * k, nt), st.w + 16 * k + 4 * half, st.w + 16 * k + 8 + 4 * half);
+      kw.make(tile::col_frag<kHalf>(Kt, kb, 16 * k, wave), st.w + 16 * k + 4 * half, st.w + 16 * k + 8 + 4 * half);
 #pragma unroll
       for (int t = 0; t < NP; ++t) {
-        const u32x4 v = tile::col_frag<64>(Vt, vb, 16 * k, pt0 + t);
+        const u32x4 v = tile::col_frag<64>(Vt, vb, 16 * k, t);
 #pragma unroll
         for (int q = 0; q < PARTS; ++q) S[t] = tile::mma(v, kw.part[q], S[t]);
       }
@@ -260,12 +274,11 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
     if constexpr (!LOCAL) {
       if (up && cur.first && p.gS0) store(p.gS0 + of_seq(cur.seq), p.P);
     }
-    cur = nxt, nxt = nx2;
-    more = more2, more2 = more3;
+    advance(more3);
   }
   if constexpr (LOCAL) {
-    if (!helper) store(slot(blockIdx.y), 64);
-    if (threadIdx.x == 0) kept[(size_t)blockIdx.y * nstrips + strip] = fresh ? kFresh : whole;
+    store(slot(seg0), 64);
+    if (threadIdx.x == 0 && n0 == 0) kept[(size_t)seg0 * nstrips + strip] = fresh ? kFresh : whole;
   }
 }
 
@@ -776,13 +789,13 @@ hipError_t launch_ssm_scan_bwd(const ScanBwdArgs& a) {
   auto go = [&](auto nn, auto parts) {
     constexpr int N = decltype(nn)::value, PARTS = decltype(parts)::value;
     if (w.nseg > 1) {
-      hipLaunchKernelGGL((states_kernel<N, true, PARTS>), dim3(nstrips, w.nseg - 1, 2), dim3(kStateThreads), 0, stream, p);
+      hipLaunchKernelGGL((states_kernel<N, true, PARTS>), dim3(nstrips * (N / kHalf) * (w.nseg - 1) * 2), dim3(kStateThreads), 0, stream, p);
       if (const hipError_t e = hipGetLastError()) return e;
       hipLaunchKernelGGL((join_both_kernel<N>), dim3(N * 64 / 1024, nstrips, 2), dim3(256), 0, stream, p.seg_ws[0], p.seg_ws[1],
                          nstrips, w.nseg - 1);
       if (const hipError_t e = hipGetLastError()) return e;
     }
-    hipLaunchKernelGGL((states_kernel<N, false, PARTS>), dim3(nstrips, w.nseg, 2), dim3(kStateThreads), 0, stream, p);
+    hipLaunchKernelGGL((states_kernel<N, false, PARTS>), dim3(nstrips * (N / kHalf) * w.nseg * 2), dim3(kStateThreads), 0, stream, p);
     if (const hipError_t e = hipGetLastError()) return e;
     if (w.blocks) {
       hipLaunchKernelGGL((grad_kernel<N>), dim3(w.blocks, n.G * w.runs), dim3(kGradThreads), 0, stream, p);
