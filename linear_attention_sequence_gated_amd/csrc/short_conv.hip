@@ -8,11 +8,11 @@
 //
 //   gz_s = sum_j w_j q_{s - j},   gw_j = sum_t q_t z_{t + j},   gb = sum_t q_t.
 //
-// Bound by memory.  A thread takes one 16-byte piece of the channels and walks
-// down a run of rows with the taps' rows in registers, so that each row is read
-// once but for W - 1 rows ahead of a run (and, for the gradients, behind it); a
-// wave's rows are 1 KB of consecutive channels.  Which rows are whose is looked up
-// once per workgroup.  All arithmetic is float32.
+// Bound by memory.  A thread takes four channels and walks down a run of rows with the
+// taps' rows in registers, so that each row is read once but for W - 1 rows ahead of a
+// run (and, for the gradients, behind it); a wave's rows are 256 consecutive channels.
+// Which rows are whose is looked up once per workgroup, while rows are on their way.
+// All arithmetic is float32.
 #include "gdn_block.hpp"
 #include "gdn_rows.hpp"
 
@@ -53,6 +53,11 @@ __device__ __forceinline__ typename PieceOf<F32, PE>::Word before(const void* st
   return PieceOf<F32, PE>::get(state, ((long long)s * (W - 1) + W - 1 - back) * C, p);
 }
 
+// Channels to a thread that walks down rows: with eight, taps and rows (and the
+// gradients' shares) left half as many waves to a SIMD.  8 x 2048 rows of 2304 in bf16:
+// 39 us for 42, 3.9 TB/s.
+constexpr int kRunPiece = 4;
+
 // -------------------------------------------------------------------- forward
 // A workgroup: 64 pieces of the channels, four runs of L rows.  The workgroups
 // behind the last run write the states, one sequence each.
@@ -62,7 +67,9 @@ __global__ __launch_bounds__(256) void conv_kernel(const void* __restrict__ x, c
                                                    const void* __restrict__ state, void* __restrict__ out,
                                                    void* __restrict__ state_final, long long xs, int T, int R, int C,
                                                    bool w_f32, bool silu_on, bool zero_rest, int runs) {
-  constexpr int PE = kPiece<F32>, NR = 4 * L;
+  constexpr int PE = kRunPiece, NR = 4 * L;
+  typedef PieceOf<F32, PE> Piece;
+  typedef typename Piece::Word Word;
   __shared__ int window[kWindow], seq[NR], beg[NR], end[NR];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int p = blockIdx.y * 64 + lane, np = C / PE;
@@ -72,42 +79,42 @@ __global__ __launch_bounds__(256) void conv_kernel(const void* __restrict__ x, c
     const Span sp = span_of(cu, T, s);
     if (p < np && wave < W - 1) {
       const int row = sp.end - (W - 1) + wave;
-      const u32x4 z = row >= sp.beg ? piece<F32>(x, (long long)row * xs, p) : before<F32, W>(state, s, sp.beg - row, C, p);
-      put<F32>(state_final, ((long long)s * (W - 1) + wave) * C, p, z);
+      const Word z = row >= sp.beg ? Piece::get(x, (long long)row * xs, p) : before<F32, W, PE>(state, s, sp.beg - row, C, p);
+      Piece::put(state_final, ((long long)s * (W - 1) + wave) * C, p, z);
     }
     return;
   }
 
-  const int r0 = blockIdx.x * NR;
-  find_seqs<NR, 256>(cu, R, T, r0, window, seq, beg, end);
-  if (p >= np) return;
-  Taps<F32, W> taps;
-  taps.load(weight, bias, w_f32, p);
-  const int first = r0 + wave * L;
-  u32x4 rows_in[L + W - 1];
+  // the rows are on their way while it is found out whose they are
+  const int r0 = blockIdx.x * NR, first = r0 + wave * L;
+  Word rows_in[L + W - 1];
 #pragma unroll
   for (int i = 0; i < L + W - 1; ++i) {
     const int row = first + i - (W - 1);
-    rows_in[i] = u32x4{0, 0, 0, 0};
-    if (row >= 0 && row < T) rows_in[i] = piece<F32>(x, (long long)row * xs, p);
+    rows_in[i] = Piece::zero();
+    if (row >= 0 && row < T && p < np) rows_in[i] = Piece::get(x, (long long)row * xs, p);
   }
+  find_seqs<NR, 256>(cu, R, T, r0, window, seq, beg, end);
+  if (p >= np) return;
+  Taps<F32, W, PE> taps;
+  taps.load(weight, bias, w_f32, p);
 #pragma unroll
   for (int i = 0; i < L; ++i) {
     const int row = first + i;
     if (row >= T) break;
     const int b = __builtin_amdgcn_readfirstlane(beg[wave * L + i]);
     if (b < 0) {
-      if (zero_rest) put<F32>(out, (long long)row * C, p, u32x4{0, 0, 0, 0});
+      if (zero_rest) Piece::put(out, (long long)row * C, p, Piece::zero());
       continue;
     }
-    u32x4 z[W];
+    Word z[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) z[j] = rows_in[i + j];
     if (row - b < W - 1) {
       const int s = __builtin_amdgcn_readfirstlane(seq[wave * L + i]);
 #pragma unroll
       for (int j = 0; j < W - 1; ++j)
-        if (row - (W - 1) + j < b) z[j] = before<F32, W>(state, s, b - (row - (W - 1) + j), C, p);
+        if (row - (W - 1) + j < b) z[j] = before<F32, W, PE>(state, s, b - (row - (W - 1) + j), C, p);
     }
     float y[PE];
     taps.sum(z, y);
@@ -115,23 +122,22 @@ __global__ __launch_bounds__(256) void conv_kernel(const void* __restrict__ x, c
 #pragma unroll
       for (int e = 0; e < PE; ++e) y[e] = silu(y[e]);
     }
-    put<F32>(out, (long long)row * C, p, pack<F32>(y));
+    Piece::put(out, (long long)row * C, p, Piece::pack(y));
   }
 }
 
 // ------------------------------------------------------------------ gradients
 // q of row t, from the rows z that its taps see.
 constexpr int kMostRun = 64;
-constexpr int kBwdPiece = 4;  // channels to a thread: with eight, taps, shares and rows took 220 registers
 template <bool F32, int W>
-__device__ __forceinline__ void slope(const Taps<F32, W, kBwdPiece>& taps, const typename PieceOf<F32, kBwdPiece>::Word (&z)[W],
-                                      const typename PieceOf<F32, kBwdPiece>::Word& g, bool silu_on, float (&q)[kBwdPiece]) {
-  PieceOf<F32, kBwdPiece>::unpack(g, q);
+__device__ __forceinline__ void slope(const Taps<F32, W, kRunPiece>& taps, const typename PieceOf<F32, kRunPiece>::Word (&z)[W],
+                                      const typename PieceOf<F32, kRunPiece>::Word& g, bool silu_on, float (&q)[kRunPiece]) {
+  PieceOf<F32, kRunPiece>::unpack(g, q);
   if (!silu_on) return;
-  float p[kBwdPiece];
+  float p[kRunPiece];
   taps.sum(z, p);
 #pragma unroll
-  for (int e = 0; e < kBwdPiece; ++e) q[e] *= silu_slope(p[e]);
+  for (int e = 0; e < kRunPiece; ++e) q[e] *= silu_slope(p[e]);
 }
 
 // A workgroup: 64 pieces of the channels, four runs of L rows, one after the
@@ -146,7 +152,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const void* __restrict__ 
                                                        void* __restrict__ grad_x, void* __restrict__ grad_state,
                                                        float* __restrict__ ws, long long xs, long long gs, int T, int R,
                                                        int C, bool w_f32, bool silu_on, bool zero_rest, int runs, int L) {
-  constexpr int PE = kBwdPiece, M = 4 * kMostRun + W - 1;
+  constexpr int PE = kRunPiece, M = 4 * kMostRun + W - 1;
   typedef PieceOf<F32, PE> Piece;
   typedef typename Piece::Word Word;
   __shared__ int window[kWindow], seq[M], beg[M], end[M];
@@ -218,7 +224,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const void* __restrict__ 
 #pragma unroll
     for (int e = 0; e < PE; ++e) qs[j + 1][e] = 0.f;
   }
-  constexpr int U = 4;  // rows whose loads are issued together
+  constexpr int U = 6;  // rows whose loads are issued together: 72 us (see bwd_run) for 75 with four, 83 with eight
   for (int i0 = 0; i0 < L + W - 1; i0 += U) {
     Word xn[U], gn[U];
 #pragma unroll
@@ -368,10 +374,10 @@ template <class F> hipError_t by_form(bool f32, int W, F f) {
 int column_groups(int C, int piece) { return (C / piece + 63) / 64; }
 
 // Rows to a wave's run in the gradients: as many as let all workgroups, four to a CU,
-// run at once (8 x 2048 rows of 2304: 73 us; with 32 rows, 1152 workgroups, 80),
+// run at once (8 x 2048 rows of 2304: 72 us, 3.1 TB/s; with 32 rows, 1152 workgroups, 80),
 // between 8 and kMostRun; with more rows than that, 40.
 int bwd_run(int T, int C) {
-  const int groups = 1024 / column_groups(C, kBwdPiece);
+  const int groups = 1024 / column_groups(C, kRunPiece);
   const int L = groups ? (int)(((long long)T + 4 * groups - 1) / (4 * groups)) : kMostRun + 1;
   return L < 8 ? 8 : L <= kMostRun ? L : 40;
 }
@@ -383,7 +389,7 @@ int bwd_runs(int T, int C) {
 }  // namespace
 
 hipError_t launch_short_conv(const ConvArgs& a) {
-  const int cols = column_groups(a.C, a.f32 ? 4 : 8);
+  const int cols = column_groups(a.C, kRunPiece);
   return by_form(a.f32, a.W, [&](auto f32, auto w) {
     auto go = [&](auto l) {
       constexpr int rows_wg = 4 * decltype(l)::value;
@@ -403,7 +409,7 @@ size_t short_conv_bwd_workspace_bytes(int T, int C, int W) { return (size_t)bwd_
 
 hipError_t launch_short_conv_bwd(const ConvBwdArgs& a) {
   hipStream_t st = static_cast<hipStream_t>(a.stream);
-  const int cols = column_groups(a.C, kBwdPiece), runs = bwd_runs(a.T, a.C), blocks = runs + (a.grad_state ? a.R : 0);
+  const int cols = column_groups(a.C, kRunPiece), runs = bwd_runs(a.T, a.C), blocks = runs + (a.grad_state ? a.R : 0);
   if (blocks) {
     const hipError_t e = by_form(a.f32, a.W, [&](auto f32, auto w) {
       hipLaunchKernelGGL((conv_bwd_kernel<decltype(f32)::value, decltype(w)::value>), dim3(blocks, cols), dim3(256),
