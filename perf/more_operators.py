@@ -374,8 +374,8 @@ def _own(st):
     if op == "conv_prompt":
         return list(gdn.short_conv(st["x"], st["weight"], st["cu"], bias=st["bias"], state=st.get("state"), silu=case["silu"]))
     if op == "conv_train":
-        y, _ = gdn.short_conv(st["x"], st["weight"], st["cu"], bias=st["bias"], silu=case["silu"])
-        gx, gw, gb, _ = gdn.short_conv_bwd(st["x"], st["weight"], st["grad_out"], st["cu"], bias=st["bias"], silu=case["silu"])
+        y, _ = gdn.short_conv(st["x"], st["weight"], st["cu"], bias=st["bias"], state=st.get("state"), silu=case["silu"])
+        gx, gw, gb, _ = gdn.short_conv_bwd(st["x"], st["weight"], st["grad_out"], st["cu"], bias=st["bias"], state=st.get("state"), silu=case["silu"])
         return [y, gx, gw, gb]
     if op == "conv_step":
         return [gdn.short_conv_step(st["x"], st["weight"], st["state"], bias=st["bias"], silu=case["silu"]), st["state"]]
