@@ -1,5 +1,6 @@
 """MI355X-native gated delta rule: chunkwise forward, its gradients and single-token decode, the softmax
-attention layers that stand between such layers in a hybrid model, and the norms and short convolutions around both.
+attention layers that stand between such layers in a hybrid model, and what stands around a recurrent layer's state
+update: norms, short convolutions, and a selective state space scan in the delta rule's place.
 
 The compute path is libgdn.so (hand-written HIP kernels for gfx950 behind the C
 ABI of include/gdn.h); this package is its thin ctypes binding.
