@@ -315,7 +315,7 @@ __device__ __forceinline__ float dot2(unsigned a, unsigned b, float c) {
 constexpr int kFew = 64;        // offsets kept in LDS; more are read from memory
 constexpr int kMostHeads = 64;  // to a run
 constexpr int kGradWaves = 8, kGradThreads = 64 * kGradWaves;
-constexpr int kBlockWaves = 6, kSteps = 5, kLoads = 6, kSums = 7;  // waves and their parts
+constexpr int kBlockWaves = 5, kSteps = 5, kLoads = 6, kSums = 7;  // waves and their parts
 
 template <int N> struct GradLds {
   __bf16 C[Q * N], B[Q * N];
@@ -326,7 +326,7 @@ template <int N> struct GradLds {
   Steps st[2];
   // sums of E over the columns and rows of each 16 x 16 block, its diagonal; h.x; shares of <Z, S>
   struct {
-    float er[10][16], ec[10][16], ed[Q], hx[Q], zs[kGradWaves], R[N / 32][Q], Qs[N / 32][Q];
+    float er[10][16], ec[10][16], ed[Q], hx[Q], zs[kGradThreads], R[N / 32][Q], Qs[N / 32][Q];
   } sums[2];
   struct {
     float a, bias, D;
@@ -336,9 +336,9 @@ template <int N> struct GradLds {
 
 // A workgroup: 64 rows, a run of strips of one group, one after the other, with the
 // next one's operands on their way to LDS.  For each strip, behind a barrier:
-//   - six waves: M, W and the sums of E, in the ten blocks of 16 x 16 at or under the
-//     diagonal (W and M go to LDS as bf16 operands), and the sixth of them the steps of the
-//     next head; the seventh: the next strip's loads; the eighth: the sums by rows of the
+//   - five waves: M, W and the sums of E, in the ten blocks of 16 x 16 at or under the
+//     diagonal (W and M go to LDS as bf16 operands); the sixth: the steps of the next head;
+//     the seventh: the next strip's loads; the eighth: the sums by rows of the
 //     strip before;
 //   - each wave: the states' products for a tile of gC and of gB (N = 64: of one of
 //     them), 32 n x 32 rows, which stay in its accumulators over the strips, and of gx,
@@ -478,12 +478,12 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
       sum_q += q;
       sum_d += ec + u.ed[lane] + q;
 #pragma unroll
-      for (int i = 0; i < kGradWaves; ++i) sum_k += u.zs[i];
+      for (int i = 0; i < kGradWaves; ++i) sum_k += u.zs[64 * i + lane];
       sum_hx += u.hx[lane];
       if ((strip & (spp - 1)) == spp - 1) {
         const float behind = __shfl(pipe::wave_prefix_sum(__shfl(sum_a, 63 - lane)), 63 - lane);
         const float upto = __shfl(pipe::wave_prefix_sum(sum_q), (lane + 63) & 63);
-        const float gg = behind + (lane ? upto : 0.f) + exp2_(total) * sum_k;
+        const float gg = behind + (lane ? upto : 0.f) + exp2_(total) * wave_sum(sum_k);
         const float z = z_of(now, head), a = a_of(head), delta = softplus(z), sig = logistic(z);
         const bool in = lane < pc.n;
         const float gz = in ? (delta > 0.f ? sum_d * (sig / delta) : 0.f) + a * gg * sig : 0.f;
@@ -524,44 +524,61 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
         for (int k = 0; k < 4; ++k) bt[k] = col_frag8<N>(L.B, cbn, 16 * k, nt);
       }
       if (wave < kBlockWaves) {
-        // blocks: rows j as elements 4 g16 + r, rows i as lanes
+        // two blocks, one's steps between the other's: rows j as elements 4 g16 + r, rows i as lanes
+        int ib[2], jb[2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           const int t = wave + n * kBlockWaves;
-          if (t >= 10) continue;
-          const int ib = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jb = t - ib * (ib + 1) / 2;
-          if (s == 0) {
+          ib[n] = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jb[n] = t - ib[n] * (ib[n] + 1) / 2;
+        }
+        if (s == 0) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
             cb[n] = pipe::zero4();
 #pragma unroll
             for (int k = 0; k < N / 32; ++k)
-              cb[n] = pipe::mma32(rows16(L.B, pipe::ic<N>{}, 16 * jb, 32 * k), rows16(L.C, pipe::ic<N>{}, 16 * ib, 32 * k), cb[n]);
+              cb[n] = pipe::mma32(rows16(L.B, pipe::ic<N>{}, 16 * jb[n], 32 * k), rows16(L.C, pipe::ic<N>{}, 16 * ib[n], 32 * k), cb[n]);
           }
-          f32x4 w = pipe::zero4(), m, e;
+        }
+        f32x4 w[2], x[2];
+        float row[2], column[2], diagonal[2], hx[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          w[n] = pipe::zero4();
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            w = pipe::mma32(rows16(Xt, pipe::ic<64>{}, 16 * jb, 32 * k), rows16(Ht, pipe::ic<64>{}, 16 * ib, 32 * k), w);
-          const float gi = st.G[16 * ib + c16];
-          const float4 u4 = *reinterpret_cast<const float4*>(st.u + 16 * jb + 4 * g16);
+            w[n] = pipe::mma32(rows16(Xt, pipe::ic<64>{}, 16 * jb[n], 32 * k), rows16(Ht, pipe::ic<64>{}, 16 * ib[n], 32 * k), w[n]);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const bool off = ib[n] != jb[n];
+          const float gi = st.G[16 * ib[n] + c16];
+          const float4 u4 = *reinterpret_cast<const float4*>(st.u + 16 * jb[n] + 4 * g16);
           const float u[4] = {u4.x, u4.y, u4.z, u4.w};
-          float row = 0.f;
+          f32x4 m, e;
+          hx[n] = c16 & 2 ? (c16 & 1 ? w[n][3] : w[n][2]) : (c16 & 1 ? w[n][1] : w[n][0]);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int j = ib == jb ? 4 * g16 + r : 0;  // against lane c16 where rows i and j are the same ones
-            const float l = ib != jb || j <= c16 ? exp2_(gi + u[r]) : 0.f;
+            const int j = 4 * g16 + r;  // against lane c16 where rows i and j are the same ones
+            const float l = off || j <= c16 ? exp2_(gi + u[r]) : 0.f;
             m[r] = cb[n][r] * l;
-            const float x = w[r] * m[r];
-            e[r] = ib != jb || j < c16 ? x : 0.f;
-            if (ib == jb && j == c16) sums.ed[16 * ib + c16] = x, sums.hx[16 * ib + c16] = w[r];
-            row += e[r];
-            w[r] *= l;
+            x[n][r] = w[n][r] * m[r];
+            e[r] = off || j < c16 ? x[n][r] : 0.f;
+            w[n][r] *= l;
           }
-          const int at = pipe::row_off<64>(16 * ib + c16, 16 * jb + 4 * g16);
+          diagonal[n] = c16 & 2 ? (c16 & 1 ? x[n][3] : x[n][2]) : (c16 & 1 ? x[n][1] : x[n][0]);
+          const int at = pipe::row_off<64>(16 * ib[n] + c16, 16 * jb[n] + 4 * g16);
           *reinterpret_cast<u32x2*>(L.M + at) = pipe::cvt4(m);
-          *reinterpret_cast<u32x2*>(L.W + at) = pipe::cvt4(w);
-          row = row_sums(row);
-          const float column = column_sums(e);
-          if (g16 == 0) sums.er[t][c16] = row;
-          if (c16 < 4) sums.ec[t][4 * g16 + c16] = column;
+          *reinterpret_cast<u32x2*>(L.W + at) = pipe::cvt4(w[n]);
+          row[n] = row_sums(((e[0] + e[1]) + e[2]) + e[3]);
+          column[n] = column_sums(e);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int t = wave + n * kBlockWaves;
+          if (g16 == 0) sums.er[t][c16] = row[n];
+          if (c16 < 4) sums.ec[t][4 * g16 + c16] = column[n];
+          if (ib[n] == jb[n] && g16 == c16 / 4) sums.ed[16 * ib[n] + c16] = diagonal[n], sums.hx[16 * ib[n] + c16] = hx[n];
         }
       } else if (wave == kSums) {
         if (s) {
@@ -584,8 +601,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) dot = dot2(u[e], v[e], dot);
         }
-        dot = wave_sum(dot);
-        if (lane == 0) sums.zs[wave] = dot;
+        sums.zs[threadIdx.x] = dot;
       }
       const int pt = wave & 1, rb = wave >> 1;
       f32x4 u[2] = {pipe::zero4(), pipe::zero4()};
