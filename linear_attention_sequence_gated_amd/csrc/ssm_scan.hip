@@ -86,7 +86,6 @@ __device__ __forceinline__ void add_piece(f32x16 (&S)[N / 32], const __bf16* Bt,
   for (int k = 0; k < 4; ++k) {
     Split<kParts> xw;
     xw.make(xk[k & 1], st.w + 16 * k + 4 * half, st.w + 16 * k + 8 + 4 * half);
-    __builtin_amdgcn_sched_barrier(0);
     if (k < 3) {
       xk[(k + 1) & 1] = tile::col_frag<128>(Xt, xb, 16 * (k + 1), xcol);
 #pragma unroll
@@ -97,7 +96,6 @@ __device__ __forceinline__ void add_piece(f32x16 (&S)[N / 32], const __bf16* Bt,
 #pragma unroll
       for (int t = 0; t < NT; ++t) S[t] = tile::mma(bt[k & 1][t], xw.part[q], S[t]);
     between(k);
-    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
