@@ -10,11 +10,11 @@
 //   gs = (w g - n mean(w g n)) / sqrt(mean(s^2) + eps) + h,   gw = sum over rows of g n.
 //
 // Bound by memory: every row is read once into registers, reduced there, and
-// written once.  A row is taken by one wave where its pieces are at most four to
-// a lane (2048 columns of bf16), otherwise by a workgroup.  All arithmetic is
-// float32.  With codes, 9869 rows of 2048 bf16 values with the residual: 26 us,
-// 5.5 TB/s; 16384 rows of 768 forward in 19 us (5.3 TB/s), their gradients in 18.5,
-// and 4 for the sum of the shares; six rows: 3.3 us.
+// written once.  A row is taken by one wave where its pieces are at most two to
+// a lane (1024 columns of bf16), otherwise by a workgroup (by_width).  All arithmetic
+// is float32.  With codes, 9869 rows of 2048 bf16 values with the residual: 24.4 us,
+// 5.8 TB/s; 16384 rows of 768 forward in 19 us (5.3 TB/s), their gradients in 18.5,
+// and 4 for the sum of the shares; six rows: 2.8 us.
 #include "gdn.h"
 #include "gdn_block.hpp"
 #include "gdn_rows.hpp"
@@ -281,13 +281,17 @@ __global__ __launch_bounds__(1024) void shares_kernel(const float* __restrict__ 
   }
 }
 
-// Lanes to a row and pieces to a lane that hold C columns: a wave up to 4 pieces
-// a lane, then the workgroup.
-template <bool F32, class F> hipError_t by_width(int pieces, F f) {
+// Lanes to a row and pieces to a lane that hold C columns: a wave up to two pieces a
+// lane, then the workgroup; with few rows, whose time is one row's, from more than one
+// piece on.  A wave with four pieces a lane against the workgroup, 2048 columns of bf16:
+// 3.5 and 2.5 us for 64 rows, 22.2 and 22.1 for 16384; gradients 40.8 and 37.0.  With
+// two, 768 columns: 2.7 and 2.4 us for 6 rows, 3.3 and 3.4 for 2048, 10.4 and 13.6 for
+// 16384; gradients 19.5 and 29.7.
+template <bool F32, class F> hipError_t by_width(int pieces, bool few, F f) {
   using pipe::ic;
   if (pieces <= 64) return f(ic<64>{}, ic<1>{});
-  if (pieces <= 128) return f(ic<64>{}, ic<2>{});
-  if (pieces <= 256) return f(ic<64>{}, ic<4>{});
+  if (pieces <= 128 && !few) return f(ic<64>{}, ic<2>{});
+  if (pieces <= 256) return f(ic<256>{}, ic<1>{});
   if (pieces <= 512) return f(ic<256>{}, ic<2>{});
   if (pieces <= 1024) return f(ic<256>{}, ic<4>{});
   if constexpr (F32)
@@ -296,7 +300,7 @@ template <bool F32, class F> hipError_t by_width(int pieces, F f) {
 }
 
 int bwd_blocks(int T, int C, bool f32) {
-  const int group = C / (f32 ? 4 : 8) <= 256 ? 4 : 1;  // rows to a workgroup
+  const int group = C / (f32 ? 4 : 8) <= 128 ? 4 : 1;  // rows to a workgroup
   const int most = 1024;
   const int need = (T + group - 1) / group;
   return need < most ? need : most;
@@ -307,7 +311,7 @@ int bwd_blocks(int T, int C, bool f32) {
 hipError_t launch_rms_norm(const NormArgs& a) {
   hipStream_t st = static_cast<hipStream_t>(a.stream);
   auto run = [&](auto f32, auto fmt) {
-    return by_width<decltype(f32)::value>(a.C / kPiece<decltype(f32)::value>, [&](auto lr, auto k) {
+    return by_width<decltype(f32)::value>(a.C / kPiece<decltype(f32)::value>, a.T <= 1024, [&](auto lr, auto k) {
       constexpr int rows_wg = 256 / decltype(lr)::value;
       hipLaunchKernelGGL((norm_kernel<decltype(f32)::value, decltype(lr)::value, decltype(k)::value, decltype(fmt)::value>),
                          dim3((a.T + rows_wg - 1) / rows_wg), dim3(256), 0, st, a.x, a.residual, a.weight, a.out, a.sum,
@@ -328,7 +332,7 @@ hipError_t launch_rms_norm_bwd(const NormBwdArgs& a) {
   const int blocks = bwd_blocks(a.T, a.C, a.f32);
   if (blocks) {
     auto run = [&](auto f32) {
-      return by_width<decltype(f32)::value>(a.C / kPiece<decltype(f32)::value>, [&](auto lr, auto k) {
+      return by_width<decltype(f32)::value>(a.C / kPiece<decltype(f32)::value>, false, [&](auto lr, auto k) {
         hipLaunchKernelGGL((norm_bwd_kernel<decltype(f32)::value, decltype(lr)::value, decltype(k)::value>), dim3(blocks),
                            dim3(256), 0, st, a.sum, a.weight, a.grad_out, a.grad_sum, a.grad_x, a.ws, a.ss, a.gs, a.gss,
                            a.eps, a.T, a.C, a.w_f32);

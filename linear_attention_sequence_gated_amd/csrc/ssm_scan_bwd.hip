@@ -27,6 +27,8 @@
 // workgroup to 64 rows and a run of strips of one group: gB and gC are summed over the
 // strips in its accumulators.  (5) Sums over the runs of strips where there are
 // several, and over rows for a, D and the bias.  All sums are made in a fixed order.
+// 8 x 2048 rows, 24 heads of 64, N = 128: 5 + 5 + 85 + 128 + 5 us; 13 sequences of up to
+// 1201 rows, 16 heads of 128, N = 64: 26 + 5 + 50 + 129 + 5.
 #include "gdn_scan.hpp"
 
 namespace gdn {
@@ -344,7 +346,9 @@ template <int N> struct GradLds {
 //     them), 32 n x 32 rows, which stay in its accumulators over the strips, and of gx,
 //     32 channels x 16 rows;
 //   - behind a second barrier, the products with M and W, and gx to memory.
-// What the latter need of B over all strips is in registers.
+// What the latter need of B over all strips is in registers.  A strip takes 5.1 us: the
+// vector unit is 0.31 busy, LDS 0.27, the matrix unit 0.11; without the loads 4.6, without
+// the states' products 4.3, without M, W and E the same.
 template <int N>
 __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
   __shared__ __attribute__((aligned(1024))) GradLds<N> L;

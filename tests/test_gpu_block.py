@@ -79,6 +79,12 @@ def test_norm_and_its_gradients(t, c, dtype, wdtype):
             near("grad_weight", down(gw), b, wdtype, (CHAIN + TERM + 128) * U * size)
 
 
+@pytest.mark.parametrize("t,c", [(1024, 1024), (1025, 1024), (1500, 520), (1300, 2048)])
+def test_norm_of_many_rows(t, c):
+    """Rows enough for one wave to each, and a few less."""
+    test_norm_and_its_gradients(t, c, "bf16", "bf16")
+
+
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
 @pytest.mark.parametrize("dtype,wdtype", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
 @pytest.mark.parametrize("t,c,block", [(1, 8, 0), (5, 72, 0), (33, 768, 0), (3, 2056, 0), (3, 16384, 0), (1, 128, 128), (9, 384, 128),
