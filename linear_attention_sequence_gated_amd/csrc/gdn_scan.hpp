@@ -73,15 +73,16 @@ __device__ __forceinline__ Source source(const void* base, long long stride, lon
 }
 // 64 pieces of 16 bytes, `ahead` bytes behind src, to consecutive LDS.  The load has no
 // result in a register, and takes its addresses as it is issued; that it has arrived is
-// waited for by tile::staged_barrier() and nothing reads its part of LDS before.  M0 is
-// the address in LDS.  Five waits between a vector instruction that may have written a
+// waited for by a barrier of its wave (tile::staged_barrier, loads_barrier) and nothing
+// reads its part of LDS before.  M0, the address in LDS, is used by nothing else in these
+// kernels.  Five waits between a vector instruction that may have written a
 // scalar operand and the load are the assembly's own to keep, and one behind M0.
 __device__ __forceinline__ void load_piece(__bf16* lds, const Source& src, unsigned off, int ahead) {
   const unsigned at = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(unsigned long long)(tile::lds_void*)lds);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(at), "v"(off), "s"(src.rsrc), "s"(ahead)
-               : "memory", "m0");
+               : "memory");
 }
 template <int D, int N, int NW> struct Stage : tile::Stage<D, N, NW> {
   typedef tile::Stage<D, N, NW> Base;

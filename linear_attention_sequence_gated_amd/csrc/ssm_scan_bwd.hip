@@ -206,7 +206,6 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
   Piece cur, nxt, nx2;
   bool more = next(cur), more2 = more && next(nxt);
   if (!more2) nxt.row = nxt.n = 0;
-  auto advance = [&](bool more3) { cur = nxt, nxt = nx2, more = more2, more2 = more3; };
   if (loads) {
     tile::wait_all_but<0>();  // counted below are staged loads alone
     if (more) stage(0, cur);
@@ -217,7 +216,7 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
       else loads_barrier<0>();
       const bool more3 = more2 && next(nx2);
       if (more3) stage(to, nx2);
-      advance(more3);
+      cur = nxt, nxt = nx2, more = more2, more2 = more3;
     }
     return;
   }
@@ -231,7 +230,7 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
       const unsigned after = raw_dt(nx2);
       if (more2) take_steps(b ^ 1, bits, nxt);
       bits = after;
-      advance(more3);
+      cur = nxt, nxt = nx2, more = more2, more2 = more3;
     }
     return;
   }
@@ -276,7 +275,7 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
     if constexpr (!LOCAL) {
       if (up && cur.first && p.gS0) store(p.gS0 + of_seq(cur.seq), p.P);
     }
-    advance(more3);
+    cur = nxt, nxt = nx2, more = more2, more2 = more3;
   }
   if constexpr (LOCAL) {
     store(slot(seg0), 64);
