@@ -501,7 +501,8 @@ int gdn_attn_prompt_bwd(const void *q, const void *k, const void *v, const void 
  *     set to zero; nothing that they hold reaches a result.
  *   - Sums over rows (gradients of parameters) are made in a fixed order.
  *   - What a call writes overlaps nothing that it reads, but for the states that
- *     a step updates in place.
+ *     a step updates in place.  Of the convolution and the scan, results that are
+ *     the very rows or states that are read are refused (GDN_ERR_UNSUPPORTED).
  *   - Errors as for gdn_chunk_fwd.
  * ------------------------------------------------------------------------ */
 

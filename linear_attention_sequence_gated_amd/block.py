@@ -172,8 +172,8 @@ def short_conv(x, weight, cu_seqlens, bias=None, state=None, silu: bool = True, 
     from 2 to 4 (the last tap meets the row itself) and bias [C] of x's dtype or float32, cu_seqlens [R + 1] int32 the
     offsets of the sequences, state [R, W - 1, C] the rows before each (zeros unless given).
 
-    Returns (out [T, C], state_final [R, W - 1, C]).  Rows in no sequence are not written; an out that is allocated here
-    holds zeros there.
+    Returns (out [T, C], state_final [R, W - 1, C]), which may not be x and state.  Rows in no sequence are not written; an
+    out that is allocated here holds zeros there.
     """
     dev, t, c, w, code, wcode, xs, bp = _conv_inputs(x, weight, bias, "short_conv")
     r = _sequences(cu_seqlens, dev)
@@ -289,8 +289,8 @@ def ssm_scan(x, dt, a, B, C, cu_seqlens, D=None, dt_bias=None, S0=None, out=None
     of wider rows; dt [T, H] bf16 or float32; a (negative), D, dt_bias [H] bf16 or float32, one dtype; cu_seqlens [R + 1]
     int32 the offsets of the sequences; S0 [R, H, N, P] float32 the states before (zeros unless given).
 
-    Returns (out [T, H, P] bf16, S_final [R, H, N, P] float32).  Rows in no sequence are not written; an out that is
-    allocated here holds zeros there.  The workspace is allocated here with torch.
+    Returns (out [T, H, P] bf16, S_final [R, H, N, P] float32), which may not be x and S0.  Rows in no sequence are not
+    written; an out that is allocated here holds zeros there.  The workspace is allocated here with torch.
     """
     dev, ptrs, strides, (t, h, p, g, n), types = _scan_inputs(x, dt, a, B, C, D, dt_bias, "ssm_scan")
     r = _sequences(cu_seqlens, dev)

@@ -17,6 +17,10 @@ template <int N> bool all_aligned(const void* const (&ptrs)[N]) {
   return true;
 }
 
+// Whether a buffer that one workgroup reads is one that another writes: states before
+// and behind a call, or rows and results of a convolution.
+bool same(const void* read, const void* written) { return read && read == written; }
+
 int status(hipError_t e) { return e == hipSuccess ? GDN_OK : GDN_ERR_HIP; }
 
 bool known_dtype(int d) { return d == GDN_F32 || d == GDN_BF16 || d == GDN_C64; }
@@ -129,6 +133,7 @@ int gdn_short_conv(const void* x, const void* weight, const void* bias, const in
   if (!weight || !cu_seqlens || (T && (!x || !out))) return GDN_ERR_NULL;
   const void* ptrs[] = {x, weight, bias, cu_seqlens, state, out, state_final};
   if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
+  if (same(T ? x : nullptr, out) || same(state, state_final)) return GDN_ERR_UNSUPPORTED;
   return status(gdn::launch_short_conv({x, weight, bias, cu_seqlens, state, out, state_final, x_stride, T, R, C, W,
                                         dtype == GDN_F32, weight_dtype == GDN_F32, silu != 0, zero_rest != 0, stream}));
 }
@@ -151,6 +156,9 @@ int gdn_short_conv_bwd(const void* x, const void* weight, const void* bias, cons
   if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
   const size_t need = gdn::short_conv_bwd_workspace_bytes(T, C, W);
   if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+  if (same(T ? x : nullptr, grad_x) || same(T ? grad_out : nullptr, grad_x) || same(state, grad_state) ||
+      same(grad_state_final, grad_state))
+    return GDN_ERR_UNSUPPORTED;
   return status(gdn::launch_short_conv_bwd({x, weight, bias, grad_out, cu_seqlens, state, grad_state_final, grad_x, grad_weight,
                                             grad_bias, grad_state, static_cast<float*>(workspace), x_stride, grad_out_stride,
                                             T, R, C, W, dtype == GDN_F32, weight_dtype == GDN_F32, silu != 0, zero_rest != 0,
@@ -190,6 +198,7 @@ int gdn_ssm_scan(const void* x, const void* dt, const void* a, const void* B, co
   if (!all_aligned(ptrs) || !params_aligned({dt}, dt_dtype) || !params_aligned({a, D, dt_bias}, param_dtype)) return GDN_ERR_ALIGN;
   const size_t need = gdn::ssm_scan_workspace_bytes(T, H, P, G, N);
   if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+  if (same(T ? x : nullptr, out) || same(S0, S_final)) return GDN_ERR_UNSUPPORTED;
   return status(gdn::launch_ssm_scan({x, dt, a, B, C, D, dt_bias, cu_seqlens, S0, out, S_final, static_cast<float*>(workspace),
                                       x_stride, dt_stride, B_stride, C_stride,
                                       {T, R, H, P, G, N, dt_dtype == GDN_F32, param_dtype == GDN_F32}, zero_rest != 0, stream}));
@@ -221,6 +230,9 @@ int gdn_ssm_scan_bwd(const void* x, const void* dt, const void* a, const void* B
     return GDN_ERR_ALIGN;
   const size_t need = gdn::ssm_scan_bwd_workspace_bytes(T, R, H, P, G, N);
   if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+  if (same(T ? x : nullptr, grad_x) || same(T ? grad_out : nullptr, grad_x) || same(T ? B : nullptr, grad_B) ||
+      same(T ? C : nullptr, grad_C) || same(S0, grad_S0) || same(grad_S_final, grad_S0))
+    return GDN_ERR_UNSUPPORTED;
   return status(gdn::launch_ssm_scan_bwd({x, dt, a, B, C, D, dt_bias, grad_out, cu_seqlens, S0, grad_S_final, grad_x, grad_dt,
                                           grad_a, grad_B, grad_C, grad_D, grad_dt_bias, grad_S0, workspace, x_stride, dt_stride,
                                           B_stride, C_stride, grad_out_stride, grad_x_stride, grad_B_stride, grad_C_stride,

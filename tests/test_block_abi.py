@@ -271,3 +271,19 @@ def test_scan_helpers_refuse_host_tensors():
         gdn.ssm_scan_bwd(x, dt, a, B, B, x, cu)
     with pytest.raises(ValueError, match="HIP device"):
         gdn.ssm_step(x, dt, a, B, B, torch.zeros(4, 2, 64, 64))
+
+
+OTHER = A + 0x10000
+
+
+@pytest.mark.parametrize("call,apart,pairs", [
+    (conv, ("out", "state_final"), [("x", "out"), ("state", "state_final")]),
+    (conv_bwd, ("grad_x", "grad_state"), [("x", "grad_x"), ("grad_out", "grad_x"), ("state", "grad_state"), ("grad_state_final", "grad_state")]),
+    (scan, ("out", "S_final"), [("x", "out"), ("S0", "S_final")]),
+    (scan_bwd, ("grad_x", "grad_B", "grad_C", "grad_S0"), [("x", "grad_x"), ("grad_out", "grad_x"), ("B", "grad_B"), ("C", "grad_C"),
+                                                           ("S0", "grad_S0"), ("grad_S_final", "grad_S0")])])
+def test_results_in_place_of_what_is_read_are_refused(call, apart, pairs):
+    for read, written in pairs:
+        kw = {k: OTHER + 0x1000 * i for i, k in enumerate(apart)}
+        kw[read] = kw[written]
+        assert call(**kw) == raw.GDN_ERR_UNSUPPORTED, (read, written)
