@@ -307,8 +307,7 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
       if (tail < s1) zero(max(tail, s0), s1);
     }
     if (p.S_final && mine) {
-      const int k0 = seg ? cu.below(p.R, s0) : 0, k1 = seg == p.nseg - 1 ? p.R : cu.below(p.R, s1);
-      for (int r = k0; r < k1; ++r) {
+      for (int r = seg; r < p.R; r += p.nseg) {  // dealt to all segments: a padded batch has many of them in one place
         const int b = min(max(cu(r), 0), p.T);
         if (min(cu(r + 1), p.T) > b) continue;
         float* dst = p.S_final + (((long long)r * p.H + head) * N) * p.P + hcol;

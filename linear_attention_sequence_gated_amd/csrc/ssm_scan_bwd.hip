@@ -161,8 +161,7 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
     }
   } else if (up) {
     if (p.gS0) {  // sequences without rows
-      const int k0 = seg ? cu.below(p.R, s0) : 0, k1 = seg == p.nseg - 1 ? p.R : cu.below(p.R, s1);
-      for (int r = k0; r < k1; ++r) {
+      for (int r = seg; r < p.R; r += p.nseg) {  // dealt to all segments: a padded batch has many of them in one place
         const int b = min(max(cu(r), 0), p.T);
         if (min(cu(r + 1), p.T) > b) continue;
         for (int i = threadIdx.x; i < kHalf * 64; i += kStateThreads) {
