@@ -310,9 +310,14 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
       for (int r = seg; r < p.R; r += p.nseg) {  // dealt to all segments: a padded batch has many of them in one place
         const int b = min(max(cu(r), 0), p.T);
         if (min(cu(r + 1), p.T) > b) continue;
-        float* dst = p.S_final + (((long long)r * p.H + head) * N) * p.P + hcol;
-        const float* src = p.S0 ? state_at(p.S0, r) : nullptr;
-        for (int n = half; n < N; n += 2) dst[(long long)n * p.P + col] = src ? src[(long long)n * p.P + col] : 0.f;
+        const long long at = (((long long)r * p.H + head) * N + lane / 8) * p.P + hcol + lane % 8 * 4;
+        for (int n = 0; n < N; n += 32) {
+          f32x4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = p.S0 ? *reinterpret_cast<const f32x4*>(p.S0 + at + (n + 8 * i) * p.P) : pipe::zero4();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(p.S_final + at + (n + 8 * i) * p.P) = v[i];
+        }
       }
     }
   }

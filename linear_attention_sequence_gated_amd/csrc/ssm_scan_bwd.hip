@@ -164,9 +164,9 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
       for (int r = seg; r < p.R; r += p.nseg) {  // dealt to all segments: a padded batch has many of them in one place
         const int b = min(max(cu(r), 0), p.T);
         if (min(cu(r + 1), p.T) > b) continue;
-        for (int i = threadIdx.x; i < kHalf * 64; i += kStateThreads) {
-          const long long at = of_seq(r) + (long long)(n0 + i / 64) * p.P + i % 64;
-          p.gS0[at] = p.gSf ? p.gSf[at] : 0.f;
+        for (int i = threadIdx.x; i < kHalf * 16; i += kStateThreads) {
+          const long long at = of_seq(r) + (long long)(n0 + i / 16) * p.P + i % 16 * 4;
+          *reinterpret_cast<f32x4*>(p.gS0 + at) = p.gSf ? *reinterpret_cast<const f32x4*>(p.gSf + at) : pipe::zero4();
         }
       }
     }

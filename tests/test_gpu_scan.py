@@ -411,3 +411,23 @@ def test_nan_is_not_hidden(name):
     one = [v if k == "a" else v[40:41] for k, v in zip(c.names, c.args())]
     y = gdn.ssm_step(*one, S, D=c.D, dt_bias=c.bias)
     assert torch.isnan(y[:, 1]).all() and torch.isnan(S[:, 1]).all() and torch.isfinite(y[:, 0]).all() and torch.isfinite(S[:, 0]).all()
+
+
+@pytest.mark.parametrize("p,n", [(64, 64), (64, 128), (128, 128)])
+def test_a_padded_batch(p, n):
+    """Many sequences without rows, among the others and behind them: their states pass through, gradients back."""
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    cu = [0, 300] + [300] * 40 + [700, 701] + [701] * 90
+    c = Case(torch, cu, 720, 4, p, 2, n, slow=True)
+    lengths = np.diff(cu)
+    empty = torch.from_numpy(np.flatnonzero(lengths == 0)).cuda()
+    out, last = gdn.ssm_scan(*c.args(), c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0)
+    assert torch.equal(last[empty], c.S0[empty])
+    check(c, out, last, 2 + 720 // 64)
+    assert (gdn.ssm_scan(*c.args(), c.offsets)[1][empty] == 0).all()
+    go = torch.from_numpy(np.random.default_rng(6).standard_normal((720, 4, p)).astype(np.float32)).to(torch.bfloat16).cuda()
+    gl = torch.from_numpy(np.random.default_rng(7).standard_normal(tuple(c.S0.shape)).astype(np.float32)).cuda()
+    got = gdn.ssm_scan_bwd(*c.args(), go, c.offsets, D=c.D, dt_bias=c.bias, S0=c.S0, grad_S_final=gl)
+    assert torch.equal(got[7][empty], gl[empty])
+    check_gradients(c, got, down(go).astype(np.float64), down(gl).astype(np.float64))
