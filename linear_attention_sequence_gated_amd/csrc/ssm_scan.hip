@@ -51,22 +51,21 @@ struct ScanParams {
   float* S_final;
   float* ws;
   long long xs, dts, bs, cs;
-  int T, R, H, P, G, seg, nseg;
+  int T, R, H, P, G, seg, nseg, idle;  // idle: segments without rows behind the others (see Idle)
   bool dt_f32, p_f32, zero_rest, joined;
 };
 
 // A workgroup's part of the work: those of a segment, which read the same rows of B and
-// C, are neighbours.
+// C, are neighbours.  Segments without rows are behind all others.
 struct Where {
   int seg, group, set;
 };
 __device__ __forceinline__ Where where(const ScanParams& p, const Strips& sp, int segs) {
-  const int per = p.G * sp.sets, id = neighbours(blockIdx.x, per * segs);
+  const int per = p.G * sp.sets, all = per * segs;
+  const int id = (int)blockIdx.x < all ? neighbours(blockIdx.x, all) : blockIdx.x;
   return {id / per, id % per / sp.sets, id % sp.sets};
 }
 
-// The workspace: the states of [segments - 1][strips][N][64], then what each segment
-// keeps (see join).
 // Where four values (j a multiple of 4) of a row i of C B^T lie in LDS: 16-byte pieces
 // are moved by the row, so that neither 16 rows' nor 16 pieces' meet in a bank.
 __device__ __forceinline__ int cb_off(int i, int j) { return i * Q + ((j / 4) ^ (i & 15)) * 4; }
@@ -223,7 +222,7 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
   const float a = param(p.a, p.p_f32, head), bias = p.bias ? param(p.bias, p.p_f32, head) : 0.f;
 
   const Offsets cu = offsets<kThreads>(p.cu, p.R, window);
-  const int s0 = seg * p.seg, s1 = min(s0 + p.seg, p.T);
+  const int s0 = min(seg * p.seg, p.T), s1 = min(s0 + p.seg, p.T);
   float* const local = p.ws;
   float* const kept = p.ws + (size_t)(p.nseg - 1) * nstrips * N * 64;
   auto state_at = [&](const float* base, int seq) { return base + (((long long)seq * p.H + head) * N) * p.P + hcol; };
@@ -307,16 +306,22 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
       if (tail < s1) zero(max(tail, s0), s1);
     }
     if (p.S_final && mine) {
-      for (int r = seg; r < p.R; r += p.nseg) {  // dealt to all segments: a padded batch has many of them in one place
+      const Idle of = idle_of(seg, p.nseg, p.idle);
+      for (int r = of.first; r < p.R; r += of.step) {
         const int b = min(max(cu(r), 0), p.T);
         if (min(cu(r + 1), p.T) > b) continue;
+        // by 64 rows, whose loads are issued together; addresses are computed here
+        const int lane = tile::fresh(threadIdx.x & 63), step = tile::fresh(8 * p.P);
         const long long at = (((long long)r * p.H + head) * N + lane / 8) * p.P + hcol + lane % 8 * 4;
-        for (int n = 0; n < N; n += 32) {
-          f32x4 v[4];
+        const float* from = p.S0 + at;
+        float* to = p.S_final + at;
+#pragma unroll 1
+        for (int n = 0; n < N; n += 64) {
+          f32x4 v[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = p.S0 ? *reinterpret_cast<const f32x4*>(p.S0 + at + (n + 8 * i) * p.P) : pipe::zero4();
+          for (int i = 0; i < 8; ++i, from += step) v[i] = p.S0 ? *reinterpret_cast<const f32x4*>(from) : pipe::zero4();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(p.S_final + at + (n + 8 * i) * p.P) = v[i];
+          for (int i = 0; i < 8; ++i, to += step) *reinterpret_cast<f32x4*>(to) = v[i];
         }
       }
     }
@@ -489,6 +494,8 @@ bool joins(int T, int R, int seg) { return (long long)T > 8LL * seg * (R > 1 ? R
 
 }  // namespace
 
+// The workspace: the states of [segments - 1][strips][N][64], then what each segment
+// keeps (see join).
 size_t ssm_scan_workspace_bytes(int T, int H, int P, int G, int N) {
   const size_t slots = cut(T, H, P, G).nseg - 1, nstrips = (size_t)H * (P / 64);
   return slots * nstrips * (N * 64 + 1) * sizeof(float);
@@ -499,8 +506,9 @@ hipError_t launch_ssm_scan(const ScanArgs& a) {
   const ScanShape& n = a.n;
   const Cut c = cut(n.T, n.H, n.P, n.G);
   const int nseg = c.nseg, nstrips = n.H * (n.P / 64);
+  const int idle = a.S_final ? idle_segments(n.R, 256 / c.sets - nseg) : 0;  // one workgroup to a CU
   const ScanParams p = {a.x, a.dt, a.a, a.B, a.C, a.D, a.bias, a.cu, a.S0, a.out, a.S_final, a.ws, a.xs, a.dts, a.bs, a.cs,
-                        n.T, n.R, n.H, n.P, n.G, c.seg, nseg, n.dt_f32, n.p_f32, a.zero_rest, joins(n.T, n.R, c.seg)};
+                        n.T, n.R, n.H, n.P, n.G, c.seg, nseg, idle, n.dt_f32, n.p_f32, a.zero_rest, joins(n.T, n.R, c.seg)};
   auto go = [&](auto nn, auto per) {
     constexpr int N = decltype(nn)::value, NS = decltype(per)::value;
     if (nseg > 1) {
@@ -511,7 +519,7 @@ hipError_t launch_ssm_scan(const ScanArgs& a) {
         if (const hipError_t e = hipGetLastError()) return e;
       }
     }
-    hipLaunchKernelGGL((scan_kernel<N, NS>), dim3(c.sets * nseg), dim3(128 * NS), 0, st, p);
+    hipLaunchKernelGGL((scan_kernel<N, NS>), dim3(c.sets * (nseg + idle)), dim3(128 * NS), 0, st, p);
     return hipGetLastError();
   };
   auto sized = [&](auto nn) { return c.ns == 4 ? go(nn, pipe::ic<4>{}) : go(nn, pipe::ic<2>{}); };

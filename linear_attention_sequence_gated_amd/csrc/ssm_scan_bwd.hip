@@ -63,7 +63,7 @@ struct BwdParams {
   float* shares;       // [gB, gC][runs][T][G][N], where runs > 1
   float* heads;        // [64-row blocks][H][3]: of a, D, bias
   long long xs, dts, bs, cs, gs, gxs, gbs, gcs;
-  int T, R, H, P, G, seg, nseg, runs, run_strips;
+  int T, R, H, P, G, seg, nseg, idle, runs, run_strips;
   bool dt_f32, p_f32, zero_rest;
 };
 
@@ -92,14 +92,14 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, col = lane & 31;
   const int spp = p.P / 64, nstrips = p.H * spp, per = nstrips * kParts, slots = p.nseg - LOCAL;
   // the two halves of a strip, which read the same x, lie nstrips apart: on one XCD where that is a multiple of eight
-  const int id = blockIdx.x, seg0 = id / per % slots;
-  const bool up = id >= per * slots;
+  const bool up = (int)blockIdx.x >= per * slots;  // and behind those, segments without rows
+  const int id = blockIdx.x - up * per * slots, seg0 = id / per;
   const int strip = id % nstrips, n0 = id % per / nstrips * kHalf, nt = n0 / 32 + (wave & 1), head = strip / spp;
   const int hcol = (strip % spp) * 64, group = head / (p.H / p.G);
   const int seg = LOCAL && up ? seg0 + 1 : seg0;
   const float a = param(p.a, p.p_f32, head), bias = p.bias ? param(p.bias, p.p_f32, head) : 0.f;
   const Offsets cu = offsets<kStateThreads>(p.cu, p.R, window);
-  const int s0 = seg * p.seg, s1 = min(s0 + p.seg, p.T);
+  const int s0 = min(seg * p.seg, p.T), s1 = min(s0 + p.seg, p.T);
   float* const shares = p.seg_ws[up];
   float* const kept = shares + (size_t)(p.nseg - 1) * nstrips * N * 64;
 
@@ -161,15 +161,20 @@ __global__ __launch_bounds__(kStateThreads, 3) void states_kernel(BwdParams p) {
     }
   } else if (up) {
     if (p.gS0) {  // sequences without rows
-      for (int r = seg; r < p.R; r += p.nseg) {  // dealt to all segments: a padded batch has many of them in one place
+      const Idle of = idle_of(seg, p.nseg, p.idle);
+      for (int r = of.first; r < p.R; r += of.step) {
         const int b = min(max(cu(r), 0), p.T);
         if (min(cu(r + 1), p.T) > b) continue;
-        for (int i = threadIdx.x; i < kHalf * 16; i += kStateThreads) {
-          const long long at = of_seq(r) + (long long)(n0 + i / 16) * p.P + i % 16 * 4;
-          *reinterpret_cast<f32x4*>(p.gS0 + at) = p.gSf ? *reinterpret_cast<const f32x4*>(p.gSf + at) : pipe::zero4();
-        }
+        constexpr int K = kHalf * 16 / kStateThreads;
+        const long long at = of_seq(r) + (long long)(n0 + (int)threadIdx.x / 16) * p.P + threadIdx.x % 16 * 4;
+        f32x4 v[K];
+#pragma unroll
+        for (int i = 0; i < K; ++i) v[i] = p.gSf ? *reinterpret_cast<const f32x4*>(p.gSf + at + i * (kStateThreads / 16) * p.P) : pipe::zero4();
+#pragma unroll
+        for (int i = 0; i < K; ++i) *reinterpret_cast<f32x4*>(p.gS0 + at + i * (kStateThreads / 16) * p.P) = v[i];
       }
     }
+    if (seg >= p.nseg) return;
     if (back.r >= back.rlow && back.pos > max(back.beg, s0) && back.end > s1) load(slot(seg), 64);
   } else if (seg && down.goes_on()) {
     load(slot(seg - 1), 64);
@@ -796,24 +801,25 @@ hipError_t launch_ssm_scan_bwd(const ScanBwdArgs& a) {
   const ScanShape& n = a.n;
   const Plan w = plan(n.T, n.R, n.H, n.P, n.G, n.N);
   char* ws = static_cast<char*>(a.ws);
-  const int nstrips = n.H * (n.P / 64);
+  const int nstrips = n.H * (n.P / 64), per = nstrips * (n.N / kHalf);
+  const int idle = a.grad_S0 ? idle_segments(n.R, 768 / per - 2 * w.nseg) : 0;  // three workgroups to a CU
   BwdParams p = {a.x, a.dt, a.a, a.B, a.C, a.D, a.bias, a.grad_out, a.cu, a.S0, a.grad_S_final, a.grad_x, a.grad_dt, a.grad_a,
                  a.grad_B, a.grad_C, a.grad_D, a.grad_bias, a.grad_S0,
                  {reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + w.share)},
                  {reinterpret_cast<__bf16*>(ws + 2 * w.share), reinterpret_cast<__bf16*>(ws + 2 * w.share + w.states)},
                  reinterpret_cast<float*>(ws + 2 * w.share + 2 * w.states + w.heads),
                  reinterpret_cast<float*>(ws + 2 * w.share + 2 * w.states), a.xs, a.dts, a.bs, a.cs, a.gs, a.gxs, a.gbs, a.gcs,
-                 n.T, n.R, n.H, n.P, n.G, w.seg, w.nseg, w.runs, w.run_strips, n.dt_f32, n.p_f32, a.zero_rest};
+                 n.T, n.R, n.H, n.P, n.G, w.seg, w.nseg, idle, w.runs, w.run_strips, n.dt_f32, n.p_f32, a.zero_rest};
   auto go = [&](auto nn, auto parts) {
     constexpr int N = decltype(nn)::value, PARTS = decltype(parts)::value;
     if (w.nseg > 1) {
-      hipLaunchKernelGGL((states_kernel<N, true, PARTS>), dim3(nstrips * (N / kHalf) * (w.nseg - 1) * 2), dim3(kStateThreads), 0, stream, p);
+      hipLaunchKernelGGL((states_kernel<N, true, PARTS>), dim3(per * (w.nseg - 1) * 2), dim3(kStateThreads), 0, stream, p);
       if (const hipError_t e = hipGetLastError()) return e;
       hipLaunchKernelGGL((join_both_kernel<N>), dim3(N * 64 / 1024, nstrips, 2), dim3(256), 0, stream, p.seg_ws[0], p.seg_ws[1],
                          nstrips, w.nseg - 1);
       if (const hipError_t e = hipGetLastError()) return e;
     }
-    hipLaunchKernelGGL((states_kernel<N, false, PARTS>), dim3(nstrips * (N / kHalf) * w.nseg * 2), dim3(kStateThreads), 0, stream, p);
+    hipLaunchKernelGGL((states_kernel<N, false, PARTS>), dim3(per * (w.nseg * 2 + idle)), dim3(kStateThreads), 0, stream, p);
     if (const hipError_t e = hipGetLastError()) return e;
     if (w.blocks) {
       hipLaunchKernelGGL((grad_kernel<N>), dim3(w.blocks, n.G * w.runs), dim3(kGradThreads), 0, stream, p);
