@@ -501,8 +501,10 @@ int gdn_attn_prompt_bwd(const void *q, const void *k, const void *v, const void 
  *     set to zero; nothing that they hold reaches a result.
  *   - Sums over rows (gradients of parameters) are made in a fixed order.
  *   - What a call writes overlaps nothing that it reads, but for the states that
- *     a step updates in place.  Of the convolution and the scan, results that are
- *     the very rows or states that are read are refused (GDN_ERR_UNSUPPORTED).
+ *     a step updates in place, and the norm's rows: out and sum may be x or residual,
+ *     grad_x may be sum, grad_out or grad_sum, where those rows are C apart.
+ *     Otherwise results that are the very rows or states that are read are refused
+ *     (GDN_ERR_UNSUPPORTED).
  *   - Errors as for gdn_chunk_fwd.
  * ------------------------------------------------------------------------ */
 

@@ -78,7 +78,8 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out=None, sum_out=None
     """Root-mean-square norm of the rows s = x + residual: s weight / sqrt(mean(s^2) + eps).
 
     x, residual [T, C] bfloat16 or float32, C a multiple of 8; weight [C] of that dtype or float32.  Returns (out [T, C],
-    s [T, C], rounded to x's dtype before it is normalised; x itself without a residual).
+    s [T, C], rounded to x's dtype before it is normalised; x itself without a residual).  out and sum_out may be x or
+    residual, where their rows lie side by side: sum_out=residual carries the residual on in place.
     """
     dev, t, c, code, wcode, xs, rs = _norm_inputs(x, weight, residual, "rms_norm")
     if out is None:
@@ -97,7 +98,7 @@ def rms_norm_quant(x, weight, residual=None, eps: float = 1e-6, dtype=torch.floa
     """rms_norm with an output in 8 bits, for a product in 8 bits: codes [T, C] of dtype (int8 or float8_e4m3fn), and a
     float32 scale for each block of 128 columns [T, C / 128] or, with block = 0, for each row [T, 1].
 
-    Returns (codes, scale, s): a value is its code times its scale.
+    Returns (codes, scale, s): a value is its code times its scale.  sum_out: as for rms_norm.
     """
     dev, t, c, code, wcode, xs, rs = _norm_inputs(x, weight, residual, "rms_norm_quant")
     fmt = _FORMATS.get(dtype)

@@ -21,6 +21,13 @@ template <int N> bool all_aligned(const void* const (&ptrs)[N]) {
 // and behind a call, or rows and results of a convolution.
 bool same(const void* read, const void* written) { return read && read == written; }
 
+// Whether a norm's result, whose rows are C apart, begins where rows do that lie
+// elsewhere: the threads that write a row have read the same values of the rows then
+// only if these are C apart too.
+bool elsewhere(const void* rows, long long stride, const void* result, int T, int C) {
+  return T > 1 && stride != C && same(rows, result);
+}
+
 int status(hipError_t e) { return e == hipSuccess ? GDN_OK : GDN_ERR_HIP; }
 
 bool known_dtype(int d) { return d == GDN_F32 || d == GDN_BF16 || d == GDN_C64; }
@@ -58,6 +65,11 @@ int norm(const void* x, const void* residual, const void* weight, void* out, voi
   if (!x || !weight || !out || (residual && !sum) || (fmt >= 0 && !scale)) return GDN_ERR_NULL;
   const void* ptrs[] = {x, residual, weight, out, sum, scale};
   if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
+  const void* results[] = {out, residual ? sum : nullptr};
+  for (const void* r : results)
+    if (elsewhere(x, xs, r, T, C) || elsewhere(residual, rs, r, T, C)) return GDN_ERR_UNSUPPORTED;
+  if (same(out, results[1])) return GDN_ERR_UNSUPPORTED;
+  if (fmt >= 0 && (same(x, out) || same(residual, out) || same(x, scale) || same(residual, scale))) return GDN_ERR_UNSUPPORTED;
   return status(gdn::launch_rms_norm({x, residual, weight, out, sum, scale, xs, rs, eps, T, C, dtype == GDN_F32,
                                       weight_dtype == GDN_F32, fmt, block, stream}));
 }
@@ -118,6 +130,9 @@ int gdn_rms_norm_bwd(const void* sum, const void* weight, const void* grad_out, 
   if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
   const size_t need = gdn::rms_norm_bwd_workspace_bytes(T, C, dtype == GDN_F32);
   if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+  if (elsewhere(sum, sum_stride, grad_x, T, C) || elsewhere(grad_out, grad_out_stride, grad_x, T, C) ||
+      elsewhere(grad_sum, grad_sum_stride, grad_x, T, C))
+    return GDN_ERR_UNSUPPORTED;
   return status(gdn::launch_rms_norm_bwd({sum, weight, grad_out, grad_sum, grad_x, grad_weight, static_cast<float*>(workspace),
                                           sum_stride, grad_out_stride, grad_sum_stride, eps, T, C, dtype == GDN_F32,
                                           weight_dtype == GDN_F32, stream}));

@@ -66,10 +66,11 @@ template <int FMT, int N> __device__ __forceinline__ void put_codes(void* out, l
   else *p = w[0];
 }
 
+// out and sum may be the rows of x or residual: a lane reads its pieces of a row, and
+// all pieces of both, before it writes the same ones.
 template <bool F32, int LR, int K, int FMT>
-__global__ __launch_bounds__(256) void norm_kernel(const void* __restrict__ x, const void* __restrict__ residual,
-                                                   const void* __restrict__ weight, void* __restrict__ out,
-                                                   void* __restrict__ sum, float* __restrict__ scale, long long xs,
+__global__ __launch_bounds__(256) void norm_kernel(const void* x, const void* residual, const void* __restrict__ weight,
+                                                   void* out, void* sum, float* __restrict__ scale, long long xs,
                                                    long long rs, float eps, int T, int C, bool w_f32, int block) {
   constexpr int PE = kPiece<F32>;
   __shared__ float red[4];
@@ -171,11 +172,11 @@ __global__ __launch_bounds__(256) void norm_kernel(const void* __restrict__ x, c
 // ---------------------------------------------------------------- gradients
 // Rows are dealt to the waves (workgroups) in turn; each keeps its share of gw in
 // registers over its rows.  The shares are added in a fixed order by a second
-// launch, so that a call's results are the same every time.
+// launch, so that a call's results are the same every time.  grad_x may be the rows of
+// any of the three that are read.
 template <bool F32, int LR, int K>
-__global__ __launch_bounds__(256) void norm_bwd_kernel(const void* __restrict__ sum, const void* __restrict__ weight,
-                                                       const void* __restrict__ grad_out,
-                                                       const void* __restrict__ grad_sum, void* __restrict__ grad_x,
+__global__ __launch_bounds__(256) void norm_bwd_kernel(const void* sum, const void* __restrict__ weight,
+                                                       const void* grad_out, const void* grad_sum, void* grad_x,
                                                        float* __restrict__ ws, long long ss, long long gs,
                                                        long long gss, float eps, int T, int C, bool w_f32) {
   constexpr int PE = kPiece<F32>, G = 256 / LR;
