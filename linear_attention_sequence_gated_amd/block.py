@@ -224,7 +224,8 @@ def short_conv_bwd(x, weight, grad_out, cu_seqlens, bias=None, state=None, silu:
 
 @_on_stream
 def short_conv_step(x, weight, state, bias=None, silu: bool = True, out=None):
-    """One new row x [R, C] for each of R sequences: returns out [R, C] and moves state [R, W - 1, C] on in place."""
+    """One new row x [R, C] for each of R sequences: returns out [R, C], which may not be x, and moves state [R, W - 1, C] on
+    in place."""
     dev, r, c, w, code, wcode, xs, bp = _conv_inputs(x, weight, bias, "short_conv_step")
     _dense(state, "state", (r, w - 1, c), x.dtype, dev)
     if out is None:
@@ -352,7 +353,7 @@ def ssm_scan_bwd(x, dt, a, B, C, grad_out, cu_seqlens, D=None, dt_bias=None, S0=
 @_on_stream
 def ssm_step(x, dt, a, B, C, S, D=None, dt_bias=None, out=None):
     """One token for each of R sequences of ssm_scan: x [R, H, P], dt [R, H], B, C [R, G, N], in place on S [R, H, N, P]
-    float32.  Returns out [R, H, P] bf16."""
+    float32.  Returns out [R, H, P] bf16, which may not be x."""
     dev, ptrs, strides, (r, h, p, g, n), types = _scan_inputs(x, dt, a, B, C, D, dt_bias, "ssm_step")
     _dense(S, "S", (r, h, n, p), torch.float32, dev)
     if out is None:

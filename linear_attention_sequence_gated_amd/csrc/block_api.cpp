@@ -21,6 +21,16 @@ template <int N> bool all_aligned(const void* const (&ptrs)[N]) {
 // and behind a call, or rows and results of a convolution.
 bool same(const void* read, const void* written) { return read && read == written; }
 
+// Whether any result is any of what is read; if_any: rows (states), which a call without
+// tokens (sequences) does not read.
+bool in_place(std::initializer_list<const void*> read, std::initializer_list<const void*> written) {
+  for (const void* r : read)
+    for (const void* w : written)
+      if (same(r, w)) return true;
+  return false;
+}
+const void* if_any(int n, const void* p) { return n ? p : nullptr; }
+
 // Whether a norm's result, whose rows are C apart, begins where rows do that lie
 // elsewhere: the threads that write a row have read the same values of the rows then
 // only if these are C apart too.
@@ -148,7 +158,7 @@ int gdn_short_conv(const void* x, const void* weight, const void* bias, const in
   if (!weight || !cu_seqlens || (T && (!x || !out))) return GDN_ERR_NULL;
   const void* ptrs[] = {x, weight, bias, cu_seqlens, state, out, state_final};
   if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
-  if (same(T ? x : nullptr, out) || same(state, state_final)) return GDN_ERR_UNSUPPORTED;
+  if (in_place({if_any(T, x), if_any(R, state)}, {out, state_final})) return GDN_ERR_UNSUPPORTED;
   return status(gdn::launch_short_conv({x, weight, bias, cu_seqlens, state, out, state_final, x_stride, T, R, C, W,
                                         dtype == GDN_F32, weight_dtype == GDN_F32, silu != 0, zero_rest != 0, stream}));
 }
@@ -171,8 +181,7 @@ int gdn_short_conv_bwd(const void* x, const void* weight, const void* bias, cons
   if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
   const size_t need = gdn::short_conv_bwd_workspace_bytes(T, C, W);
   if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
-  if (same(T ? x : nullptr, grad_x) || same(T ? grad_out : nullptr, grad_x) || same(state, grad_state) ||
-      same(grad_state_final, grad_state))
+  if (in_place({if_any(T, x), if_any(T, grad_out), if_any(R, state), if_any(R, grad_state_final)}, {grad_x, grad_state}))
     return GDN_ERR_UNSUPPORTED;
   return status(gdn::launch_short_conv_bwd({x, weight, bias, grad_out, cu_seqlens, state, grad_state_final, grad_x, grad_weight,
                                             grad_bias, grad_state, static_cast<float*>(workspace), x_stride, grad_out_stride,
@@ -189,6 +198,7 @@ int gdn_short_conv_step(const void* x, const void* weight, const void* bias, voi
   if (!x || !weight || !state || !out) return GDN_ERR_NULL;
   const void* ptrs[] = {x, weight, bias, state, out};
   if (!all_aligned(ptrs)) return GDN_ERR_ALIGN;
+  if (in_place({x, state}, {out}) || same(x, state)) return GDN_ERR_UNSUPPORTED;
   return status(gdn::launch_short_conv_step({x, weight, bias, state, out, x_stride, R, C, W, dtype == GDN_F32,
                                              weight_dtype == GDN_F32, silu != 0, stream}));
 }
@@ -213,7 +223,7 @@ int gdn_ssm_scan(const void* x, const void* dt, const void* a, const void* B, co
   if (!all_aligned(ptrs) || !params_aligned({dt}, dt_dtype) || !params_aligned({a, D, dt_bias}, param_dtype)) return GDN_ERR_ALIGN;
   const size_t need = gdn::ssm_scan_workspace_bytes(T, H, P, G, N);
   if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
-  if (same(T ? x : nullptr, out) || same(S0, S_final)) return GDN_ERR_UNSUPPORTED;
+  if (in_place({if_any(T, x), if_any(T, dt), if_any(T, B), if_any(T, C), if_any(R, S0)}, {out, S_final})) return GDN_ERR_UNSUPPORTED;
   return status(gdn::launch_ssm_scan({x, dt, a, B, C, D, dt_bias, cu_seqlens, S0, out, S_final, static_cast<float*>(workspace),
                                       x_stride, dt_stride, B_stride, C_stride,
                                       {T, R, H, P, G, N, dt_dtype == GDN_F32, param_dtype == GDN_F32}, zero_rest != 0, stream}));
@@ -245,8 +255,8 @@ int gdn_ssm_scan_bwd(const void* x, const void* dt, const void* a, const void* B
     return GDN_ERR_ALIGN;
   const size_t need = gdn::ssm_scan_bwd_workspace_bytes(T, R, H, P, G, N);
   if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
-  if (same(T ? x : nullptr, grad_x) || same(T ? grad_out : nullptr, grad_x) || same(T ? B : nullptr, grad_B) ||
-      same(T ? C : nullptr, grad_C) || same(S0, grad_S0) || same(grad_S_final, grad_S0))
+  if (in_place({if_any(T, x), if_any(T, dt), if_any(T, B), if_any(T, C), if_any(T, grad_out), if_any(R, S0), if_any(R, grad_S_final)},
+               {grad_x, grad_dt, grad_B, grad_C, grad_S0}))
     return GDN_ERR_UNSUPPORTED;
   return status(gdn::launch_ssm_scan_bwd({x, dt, a, B, C, D, dt_bias, grad_out, cu_seqlens, S0, grad_S_final, grad_x, grad_dt,
                                           grad_a, grad_B, grad_C, grad_D, grad_dt_bias, grad_S0, workspace, x_stride, dt_stride,
@@ -268,6 +278,7 @@ int gdn_ssm_step(const void* x, const void* dt, const void* a, const void* B, co
   if (!x || !dt || !a || !B || !C || !S || !out) return GDN_ERR_NULL;
   const void* ptrs[] = {x, B, C, S, out};
   if (!all_aligned(ptrs) || !params_aligned({dt}, dt_dtype) || !params_aligned({a, D, dt_bias}, param_dtype)) return GDN_ERR_ALIGN;
+  if (in_place({x, dt, B, C, S}, {out}) || in_place({x, dt, B, C}, {S})) return GDN_ERR_UNSUPPORTED;
   return status(gdn::launch_ssm_step({x, dt, a, B, C, D, dt_bias, S, out, x_stride, dt_stride, B_stride, C_stride,
                                       {R, R, H, P, G, N, dt_dtype == GDN_F32, param_dtype == GDN_F32}, stream}));
 }

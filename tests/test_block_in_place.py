@@ -4,7 +4,7 @@ import pytest
 
 import linear_attention_sequence_gated_amd as gdn
 from linear_attention_sequence_gated_amd import gdn as raw
-from test_block_abi import A, norm, norm_bwd, quant
+from test_block_abi import A, conv, conv_bwd, conv_step, norm, norm_bwd, quant, scan, scan_bwd, step
 
 FAR = [A + 0x100000 * i for i in range(1, 24)]
 
@@ -73,3 +73,32 @@ def test_norm_in_place_gives_the_same(t, c, dtype, wdtype):
         torch.cuda.synchronize()
         assert torch.equal(rows[at], gx) and torch.equal(got_w, gw)
         assert all(torch.equal(u, v) for i, (u, v) in enumerate(zip(rows, (s, g, h))) if i != at)
+
+
+CONV_STEP = ("x", "weight", "bias", "state", "out")
+STEP = ("x", "dt", "a", "B", "C", "D", "dt_bias", "S", "out")
+SCAN = ("x", "dt", "a", "B", "C", "D", "dt_bias", "cu_seqlens", "S0", "out", "S_final", "workspace")
+SCAN_BWD = ("x", "dt", "a", "B", "C", "D", "dt_bias", "grad_out", "cu_seqlens", "S0", "grad_S_final", "grad_x", "grad_dt", "grad_a", "grad_B",
+            "grad_C", "grad_D", "grad_dt_bias", "grad_S0", "workspace")
+CONV = ("x", "weight", "bias", "cu_seqlens", "state", "out", "state_final")
+CONV_BWD = ("x", "weight", "bias", "grad_out", "cu_seqlens", "state", "grad_state_final", "grad_x", "grad_weight", "grad_bias", "grad_state",
+            "workspace")
+
+
+@pytest.mark.parametrize("call,names,reads,writes", [
+    (conv, CONV, ("x", "state"), ("out", "state_final")), (conv_bwd, CONV_BWD, ("x", "grad_out", "state", "grad_state_final"), ("grad_x", "grad_state")),
+    (conv_step, CONV_STEP, ("x", "state"), ("out",)), (conv_step, CONV_STEP, ("x",), ("state",)),
+    (scan, SCAN, ("x", "dt", "B", "C", "S0"), ("out", "S_final")),
+    (scan_bwd, SCAN_BWD, ("x", "dt", "B", "C", "grad_out", "S0", "grad_S_final"), ("grad_x", "grad_dt", "grad_B", "grad_C", "grad_S0")),
+    (step, STEP, ("x", "dt", "B", "C", "S"), ("out",)), (step, STEP, ("x", "dt", "B", "C"), ("S",))])
+def test_results_in_place_of_any_rows_or_states_are_refused(call, names, reads, writes):
+    for read in reads:
+        for written in writes:
+            assert apart(call, names, **{written: read}) == raw.GDN_ERR_UNSUPPORTED, (read, written)
+
+
+def test_nothing_read_is_nothing_in_place():
+    """Without rows (sequences), the addresses of rows (states) say nothing."""
+    at = dict(zip(SCAN, FAR))
+    assert scan(**{**at, "T": 0, "R": 0, "x": A, "out": A}) == raw.GDN_OK
+    assert conv(**{**dict(zip(CONV, FAR)), "T": 0, "R": 0, "x": A, "out": A}) == raw.GDN_OK
