@@ -529,7 +529,7 @@ int gdn_rms_norm(const void *x, const void *residual, const void *weight, void *
 
 /*
  * The same with an output in 8 bits (format: the codes of a cache), for a
- * product in 8 bits: a value is its code times its scale.
+ * product in 8 bits of the caller's: a value is its code times its scale.
  *
  *   codes [T, C] written;  scale written: [T, C / 128] where block is 128 (C a
  *   multiple of it), [T] where block is 0 (a scale to a row)
@@ -631,8 +631,10 @@ int gdn_short_conv_step(const void *x, const void *weight, const void *bias, voi
  *
  * P and N are 64 or 128 each.  States and every sum are float32; weights of rows and
  * the state are rounded to bf16 where they enter a product whose result is out, and
- * taken in three bf16 parts (2^-25) where it is a state.  A decay of less than 2^-160
- * a token is taken for that.  Inputs are finite and a <= 0: others give results that
+ * taken in three bf16 parts (2^-25) where it is a state.  Decays are float32 numbers:
+ * where a token, or a piece of up to 64, keeps less than 2^-126 of the state, it keeps
+ * nothing, and a weight within a piece is off by up to 9 E 2^-24 of itself, E the sum of
+ * the piece's log2 decays, each counted up to 160.  Inputs are finite and a <= 0: others give results that
  * are undefined, typically non-finite, in their own sequence and nowhere else.
  * Workspace: gdn_ssm_scan_workspace_bytes (0 for short T), scratch on entry and
  * exit, no clearing needed.  T is below 2^26, T * H below 2^31, R below 2^20, R * H
@@ -658,9 +660,9 @@ int gdn_ssm_scan(const void *x, const void *dt, const void *a, const void *B, co
  *
  * Sums are float32, in a fixed order, and rounded once.  Weights, states and gradients
  * of states are rounded to bf16 where they enter a product (grad_S0: as states of the
- * forward are); grad_dt, grad_a and grad_dt_bias, sums of many terms that may cancel,
- * are as exact as that leaves their terms (2^-8 of each).  Rows in no sequence: as for
- * the forward.  Workspace: gdn_ssm_scan_bwd_workspace_bytes, scratch on entry and exit,
+ * forward are).  grad_dt, grad_a and grad_dt_bias, sums of many terms that may cancel,
+ * are as exact as that leaves their terms (2^-8 of each), also where they are float32.
+ * Rows in no sequence: as for the forward.  Workspace: gdn_ssm_scan_bwd_workspace_bytes, scratch on entry and exit,
  * no clearing needed; it holds two bf16 states for each head and 64 tokens, and for
  * each head and sequence.
  */

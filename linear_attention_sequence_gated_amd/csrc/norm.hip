@@ -287,7 +287,9 @@ __global__ __launch_bounds__(1024) void shares_kernel(const float* __restrict__ 
 // piece on.  A wave with four pieces a lane against the workgroup, 2048 columns of bf16:
 // 3.5 and 2.5 us for 64 rows, 22.2 and 22.1 for 16384; gradients 40.8 and 37.0.  With
 // two, 768 columns: 2.7 and 2.4 us for 6 rows, 3.3 and 3.4 for 2048, 10.4 and 13.6 for
-// 16384; gradients 19.5 and 29.7.
+// 16384; gradients 19.5 and 29.7.  Eight float32 pieces a lane leave one wave to a SIMD:
+// 4096 rows of 8192 with the residual take 239 us, 2048 of 16384, as many bytes with
+// sixteen, 110 (bf16: 40 and 44).
 template <bool F32, class F> hipError_t by_width(int pieces, bool few, F f) {
   using pipe::ic;
   if (pieces <= 64) return f(ic<64>{}, ic<1>{});
@@ -300,6 +302,10 @@ template <bool F32, class F> hipError_t by_width(int pieces, bool few, F f) {
   return f(ic<256>{}, ic<8>{});
 }
 
+// Workgroups of the gradients, each of which writes a share of C numbers.  With 512, 1024
+// and 2048 at most: 16384 rows of 768 in bf16 21.4, 22.2 and 25.8 us, in float32 37.7, 34.5
+// and 37.8; one row at a time, 4096 of 4096 in bf16 26.6, 28.6 and 34.9, 1464 of 8192 24.6,
+// 30.7 and 39.0 (256: 26.0), 4096 of 8192 in float32 107, 112 and 125.
 int bwd_blocks(int T, int C, bool f32) {
   const int group = C / (f32 ? 4 : 8) <= 128 ? 4 : 1;  // rows to a workgroup
   const int most = 1024;

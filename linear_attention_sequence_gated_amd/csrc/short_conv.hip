@@ -12,7 +12,8 @@
 // taps' rows in registers, so that each row is read once but for W - 1 rows ahead of a
 // run (and, for the gradients, behind it); a wave's rows are 256 consecutive channels.
 // Which rows are whose is looked up once per workgroup, while rows are on their way.
-// All arithmetic is float32.
+// All arithmetic is float32.  In the gradients' loop, of 1660 vector instructions for 24
+// values a lane, 450 move rows along, 190 ask whose a row is, 48 are transcendental.
 #include "gdn_block.hpp"
 #include "gdn_rows.hpp"
 
@@ -375,7 +376,9 @@ int column_groups(int C, int piece) { return (C / piece + 63) / 64; }
 
 // Rows to a wave's run in the gradients: as many as let all workgroups, four to a CU,
 // run at once (8 x 2048 rows of 2304: 72 us, 3.1 TB/s; with 32 rows, 1152 workgroups, 80),
-// between 8 and kMostRun; with more rows than that, 40.
+// between 8 and kMostRun; with more rows than that, 40 (bf16, with 24, 32, 40 and 64 rows:
+// 32768 rows of 2304 147, 142, 147 and 157 us, 131072 500, 487, 476 and 475, 16384 of 8192
+// 255, 234, 239 and 230).
 int bwd_run(int T, int C) {
   const int groups = 1024 / column_groups(C, kRunPiece);
   const int L = groups ? (int)(((long long)T + 4 * groups - 1) / (4 * groups)) : kMostRun + 1;

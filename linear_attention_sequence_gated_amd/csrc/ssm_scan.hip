@@ -19,13 +19,15 @@
 // Where numbers are rounded: C B^T o L between the two halves of a piece, and the state
 // as it enters the product with C, to bf16 (2^-9 of each term); C B^T o L within a half,
 // where the weights are largest, in two parts (2^-17: with one, the relative error of
-// the result was 2.3e-3 for 1.7e-3, of which the result's own rounding is 1.65e-3); what goes into the state in three parts, 2^-25, since the state is a
-// result and is carried on.
+// the result was 2.3e-3 for 1.7e-3, of which the result's own rounding is 1.65e-3; where
+// most of a result comes from the state that a piece begins with, it is 2.4e-3 off); what
+// goes into the state in three parts, 2^-25, since the state is a result and is carried on.
 //
 // 8 x 2048 rows, 24 heads of 64, N = 128: 28 us for the segments' ends, 67 for the rest,
 // 0.14 PFLOP/s of the formulas' own work; 1 x 16384, 32 heads of 128: 60 + 12 + 137.  What
-// bounds it is the chain of a piece (8.5 us for four strips), not a unit: the matrix unit
-// is 0.18 to 0.27 busy, the vector unit 0.37 to 0.51.
+// bounds it is the chain of a piece (8.5 us for four strips), beside which nothing runs on a
+// CU, since LDS holds one workgroup: the matrix unit is 0.18 to 0.27 busy, the vector unit
+// 0.36 to 0.51.  Scalars that do not fit are kept in lanes (47 to 59 of them).
 #include "gdn_scan.hpp"
 
 namespace gdn {

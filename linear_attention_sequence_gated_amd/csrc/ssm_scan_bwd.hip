@@ -23,7 +23,10 @@
 // Launches.  (1) Where there are several segments of rows, each one's share in the
 // state and in Z at its border, and (2) their sum along the sequences.  (3) The states
 // before each piece of 64 rows and Z behind it, walked down and up the segments, to
-// memory in bf16: as such they enter every product below.  (4) All gradients, a
+// memory in bf16: as such they enter every product below, and M and W as bf16 too (x's,
+// B's and C's gradients are 2.3e-3 off, of which their own rounding is 1.66e-3; those of a
+// and dt_bias, for which <Z, S> is taken of two such factors, 1e-4 to 1e-3 in float32, up to
+// 4e-3 where their rows' terms cancel).  (4) All gradients, a
 // workgroup to 64 rows and a run of strips of one group: gB and gC are summed over the
 // strips in its accumulators.  (5) Sums over the runs of strips where there are
 // several, and over rows for a, D and the bias.  All sums are made in a fixed order.
@@ -79,8 +82,8 @@ __device__ __forceinline__ int state_piece(int n, int c) { return (n / 32 * 4 + 
 // time (see state_piece).  What the rows add is weighted on the side of B (C), in PARTS
 // bf16 parts, once.  A third wave brings the rows of the piece after next, and a fourth
 // computes the next one's steps, so that the two have nothing but their products to
-// wait for.  The states go to memory: 8 x 2048 rows x 24 strips, N = 128, write 208 MB
-// and read 110 in 85 us; 13 sequences of up to 1201 rows x 32 strips, N = 64, took 55 us
+// wait for.  The states go to memory: 8 x 2048 rows x 24 strips, N = 128, write 201 MB
+// and read 194 in 85 us; 13 sequences of up to 1201 rows x 32 strips, N = 64, took 55 us
 // with a piece's rows one piece ahead and four waves of 32 x 32, now 50.
 constexpr int kStateThreads = 256, kHalf = 64;  // n to a workgroup
 template <int N, bool LOCAL, int PARTS>
@@ -351,7 +354,10 @@ template <int N> struct GradLds {
 //   - behind a second barrier, the products with M and W, and gx to memory.
 // What the latter need of B over all strips is in registers.  A strip takes 5.1 us: the
 // vector unit is 0.31 busy, LDS 0.27, the matrix unit 0.11; without the loads 4.6, without
-// the states' products 4.3, without M, W and E the same.
+// the states' products 4.3, without M, W and E the same: the waves wait 0.6 of the time,
+// mostly at the two barriers, with one workgroup to a CU.  Pointers, strides and resources are
+// live in every wave over the whole walk: 343 scalars (N = 64: 298) are kept in lanes, and the
+// loop over the pieces has about 600 reads of these beside 40 (32) matrix instructions.
 template <int N>
 __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
   __shared__ __attribute__((aligned(1024))) GradLds<N> L;

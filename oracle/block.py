@@ -1,6 +1,6 @@
 """fp64 references of what stands around a recurrent layer's state update, from the definitions in include/gdn.h: the
 root-mean-square norm with the residual's addition and an 8-bit output, the short causal convolution over packed
-sequences.  numpy only; everything is computed in float64 from the stored inputs."""
+sequences, and the selective state space scan.  numpy only; everything is computed in float64 from the stored inputs."""
 from __future__ import annotations
 
 import numpy as np
