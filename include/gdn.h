@@ -630,8 +630,8 @@ int gdn_short_conv_step(const void *x, const void *weight, const void *bias, voi
  *   S_final    [R, H, N, P] float32, written; may be NULL
  *
  * P and N are 64 or 128 each.  States and every sum are float32; weights of rows and
- * the state are rounded to bf16 where they enter a product whose result is out, and
- * taken in three bf16 parts (2^-25) where it is a state.  Decays are float32 numbers:
+ * the state are taken in two bf16 parts (2^-17) where they enter a product whose result
+ * is out, and in three (2^-25) where it is a state.  Decays are float32 numbers:
  * where a token, or a piece of up to 64, keeps less than 2^-126 of the state, it keeps
  * nothing, and a weight within a piece is off by up to 9 E 2^-24 of itself, E the sum of
  * the piece's log2 decays, each counted up to 160.  Inputs are finite and a <= 0: others give results that

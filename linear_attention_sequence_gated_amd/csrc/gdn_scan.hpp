@@ -342,6 +342,22 @@ template <int PARTS> struct Split {
   }
 };
 
+// Elements 8 b .. 8 b + 7 of an accumulator tile as two bf16 operands that add up to them,
+// to 2^-17.
+struct Two {
+  u32x4 part[2];
+};
+__device__ __forceinline__ Two two_parts(const f32x16& x, int b) {
+  Two t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float f = x[8 * b + 2 * i], g = x[8 * b + 2 * i + 1];
+    t.part[0][i] = pipe::cvt2(f, g);
+    t.part[1][i] = pipe::cvt2(f - pipe::lo_f(t.part[0][i]), g - pipe::hi_f(t.part[0][i]));
+  }
+  return t;
+}
+
 // States in memory, [N][P] float32: the part of a wave's 32 columns.  Addresses are
 // computed here, not kept in registers over a loop.
 template <int NT> __device__ __forceinline__ void load_state(f32x16 (&S)[NT], const float* src, int P) {

@@ -16,12 +16,12 @@
 // are alike; where there are several, a first launch finds what each leaves in the
 // state that crosses its end, a second one adds these up along the sequences.
 //
-// Where numbers are rounded: C B^T o L between the two halves of a piece, and the state
-// as it enters the product with C, to bf16 (2^-9 of each term); C B^T o L within a half,
-// where the weights are largest, in two parts (2^-17: with one, the relative error of
-// the result was 2.3e-3 for 1.7e-3, of which the result's own rounding is 1.65e-3; where
-// most of a result comes from the state that a piece begins with, it is 2.4e-3 off); what
-// goes into the state in three parts, 2^-25, since the state is a result and is carried on.
+// Where numbers are rounded: C B^T o L, and the state as it enters the product with C, are
+// taken in two bf16 parts (2^-17 of each term), so that the result is off by its own
+// rounding alone (1.66e-3 in norm; with one part of the state and of the weights between the
+// halves of a piece it was 1.8e-3, 2.4e-3 where most of it comes from the state, in 94.7
+// and 205 us for 99.5 and 216 of the two cases below).  What goes into the state is taken
+// in three parts, 2^-25, since the state is a result and is carried on.
 //
 // 8 x 2048 rows, 24 heads of 64, N = 128: 28 us for the segments' ends, 67 for the rest,
 // 0.14 PFLOP/s of the formulas' own work; 1 x 16384, 32 heads of 128: 60 + 12 + 137.  What
@@ -34,7 +34,6 @@ namespace gdn {
 namespace {
 
 using namespace scan;
-using tile::operand;
 using tile::zero16;
 
 constexpr int kParts = 3;
@@ -371,9 +370,13 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
       }
 #pragma unroll
       for (int ks = 0; ks < N / 16; ++ks) {
-        const u32x4 s = operand(S[ks / 2], ks % 2);
-        y[0] = tile::mma(s, tile::row_frag<N>(Ct, rb, 0, ks), y[0]);
-        y[1] = tile::mma(s, tile::row_frag<N>(Ct, rb, 32, ks), y[1]);
+        const Two s = two_parts(S[ks / 2], ks % 2);
+        const u32x4 c0 = tile::row_frag<N>(Ct, rb, 0, ks), c1 = tile::row_frag<N>(Ct, rb, 32, ks);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          y[0] = tile::mma(s.part[q], c0, y[0]);
+          y[1] = tile::mma(s.part[q], c1, y[1]);
+        }
       }
     }
     lds_barrier();
@@ -409,20 +412,21 @@ __global__ __launch_bounds__(128 * NS, NS == 4 ? 2 : 1) void scan_kernel(ScanPar
             f[2][4 * u + j] = __builtin_bit_cast(float, __builtin_bit_cast(int, c11[j] * exp2_(g1 + fb[j])) & in);
           }
         }
-        u32x4 w[3], rest[2];
+        u32x4 w[3], rest[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             w[i][e] = pipe::cvt2(f[i][2 * e], f[i][2 * e + 1]);
-            if (i != 1) rest[i / 2][e] = pipe::cvt2(f[i][2 * e] - pipe::lo_f(w[i][e]), f[i][2 * e + 1] - pipe::hi_f(w[i][e]));
+            rest[i][e] = pipe::cvt2(f[i][2 * e] - pipe::lo_f(w[i][e]), f[i][2 * e + 1] - pipe::hi_f(w[i][e]));
           }
         const u32x4 x0 = tile::col_frag<128>(Xt, xb, 16 * k, xcol), x1 = tile::col_frag<128>(Xt, xb, 32 + 16 * k, xcol);
         y[0] = tile::mma(x0, w[0], y[0]);
         y[1] = tile::mma(x0, w[1], y[1]);
         y[0] = tile::mma(x0, rest[0], y[0]);
+        y[1] = tile::mma(x0, rest[1], y[1]);
         y[1] = tile::mma(x1, w[2], y[1]);
-        y[1] = tile::mma(x1, rest[1], y[1]);
+        y[1] = tile::mma(x1, rest[2], y[1]);
         __builtin_amdgcn_sched_barrier(0);
       }
       // y: columns are rows of the piece, elements channels 8 q + 4 half + j.  Added to D x, and by 32 rows through a part
