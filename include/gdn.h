@@ -658,9 +658,9 @@ int gdn_ssm_scan(const void *x, const void *dt, const void *a, const void *B, co
  *   grad_a, grad_D, grad_dt_bias [H] of param_dtype; the latter two may be NULL
  *   grad_S_final, grad_S0 [R, H, N, P] float32; may be NULL
  *
- * Sums are float32, in a fixed order, and rounded once.  Weights, states and gradients
- * of states are rounded to bf16 where they enter a product (grad_S0: as states of the
- * forward are).  grad_dt, grad_a and grad_dt_bias, sums of many terms that may cancel,
+ * Sums are float32, in a fixed order, and rounded once.  Weights are taken in two bf16
+ * parts; states and gradients of states, before and behind every 64 tokens, are rounded to
+ * bf16 where they enter a product (grad_S0: as states of the forward are).  grad_dt, grad_a and grad_dt_bias, sums of many terms that may cancel,
  * are as exact as that leaves their terms (2^-8 of each), also where they are float32.
  * Rows in no sequence: as for the forward.  Workspace: gdn_ssm_scan_bwd_workspace_bytes, scratch on entry and exit,
  * no clearing needed; it holds two bf16 states for each head and 64 tokens, and for

@@ -23,11 +23,11 @@
 // and 205 us for 99.5 and 216 of the two cases below).  What goes into the state is taken
 // in three parts, 2^-25, since the state is a result and is carried on.
 //
-// 8 x 2048 rows, 24 heads of 64, N = 128: 28 us for the segments' ends, 67 for the rest,
-// 0.14 PFLOP/s of the formulas' own work; 1 x 16384, 32 heads of 128: 60 + 12 + 137.  What
-// bounds it is the chain of a piece (8.5 us for four strips), beside which nothing runs on a
-// CU, since LDS holds one workgroup: the matrix unit is 0.18 to 0.27 busy, the vector unit
-// 0.36 to 0.51.  Scalars that do not fit are kept in lanes (47 to 59 of them).
+// 8 x 2048 rows, 24 heads of 64, N = 128: 28 us for the segments' ends, 72 for the rest,
+// 0.13 PFLOP/s of the formulas' own work; 1 x 16384, 32 heads of 128: 60 + 12 + 150.  What
+// bounds it is the chain of a piece (9 us for four strips), beside which nothing runs on a
+// CU, since LDS holds one workgroup: the matrix unit is 0.22 to 0.30 busy, the vector unit
+// 0.41 to 0.56.  Scalars that do not fit are kept in lanes (47 to 59 of them).
 #include "gdn_scan.hpp"
 
 namespace gdn {

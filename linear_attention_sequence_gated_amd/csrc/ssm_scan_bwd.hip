@@ -23,10 +23,13 @@
 // Launches.  (1) Where there are several segments of rows, each one's share in the
 // state and in Z at its border, and (2) their sum along the sequences.  (3) The states
 // before each piece of 64 rows and Z behind it, walked down and up the segments, to
-// memory in bf16: as such they enter every product below, and M and W as bf16 too (x's,
-// B's and C's gradients are 2.3e-3 off, of which their own rounding is 1.66e-3; those of a
-// and dt_bias, for which <Z, S> is taken of two such factors, 1e-4 to 1e-3 in float32, up to
-// 4e-3 where their rows' terms cancel).  (4) All gradients, a
+// memory in bf16: as such they enter every product below.  (M, and W summed over a run's
+// heads in float32, are taken in two bf16 parts: x's, B's and C's gradients are 1.7e-3 off,
+// of which their own rounding is 1.66e-3; with one part, and W rounded for each head, 2.3e-3,
+// and 6.7e-3 where heads cancel.  Those of a and dt_bias, for which <Z, S> is taken of two
+// states as stored, are 1e-4 to 1e-3 off in float32, up to 4e-3 where their rows' terms
+// cancel; states in two parts would be 400 MB more to move at the 8 x 2048 rows below, and
+// no LDS is left for them at N = 128.)  (4) All gradients, a
 // workgroup to 64 rows and a run of strips of one group: gB and gC are summed over the
 // strips in its accumulators.  (5) Sums over the runs of strips where there are
 // several, and over rows for a, D and the bias.  All sums are made in a fixed order.
@@ -330,7 +333,7 @@ template <int N> struct GradLds {
   struct {
     __bf16 S[N * 64], Z[N * 64], x[Q * 64], h[Q * 64];
   } strip[2];
-  __bf16 M[Q * Q], W[Q * Q];       // [i][j]
+  __bf16 M[2][Q * Q];              // [i][j], in two parts; at the end W, summed over the strips
   Steps st[2];
   // sums of E over the columns and rows of each 16 x 16 block, its diagonal; h.x; shares of <Z, S>
   struct {
@@ -345,19 +348,20 @@ template <int N> struct GradLds {
 // A workgroup: 64 rows, a run of strips of one group, one after the other, with the
 // next one's operands on their way to LDS.  For each strip, behind a barrier:
 //   - five waves: M, W and the sums of E, in the ten blocks of 16 x 16 at or under the
-//     diagonal (W and M go to LDS as bf16 operands); the sixth: the steps of the next head;
+//     diagonal (M goes to LDS as operands in two bf16 parts, W is summed over the strips in
+//     their registers); the sixth: the steps of the next head;
 //     the seventh: the next strip's loads; the eighth: the sums by rows of the
 //     strip before;
 //   - each wave: the states' products for a tile of gC and of gB (N = 64: of one of
 //     them), 32 n x 32 rows, which stay in its accumulators over the strips, and of gx,
 //     32 channels x 16 rows;
-//   - behind a second barrier, the products with M and W, and gx to memory.
-// What the latter need of B over all strips is in registers.  A strip takes 5.1 us: the
-// vector unit is 0.31 busy, LDS 0.27, the matrix unit 0.11; without the loads 4.6, without
-// the states' products 4.3, without M, W and E the same: the waves wait 0.6 of the time,
-// mostly at the two barriers, with one workgroup to a CU.  Pointers, strides and resources are
-// live in every wave over the whole walk: 343 scalars (N = 64: 298) are kept in lanes, and the
-// loop over the pieces has about 600 reads of these beside 40 (32) matrix instructions.
+//   - behind a second barrier, the products with M, and gx to memory.
+// Behind the last strip W, in two parts, takes M's place for its products with C and B.
+// A strip takes some 5 us: the vector unit is 0.32 busy, LDS 0.25, the matrix unit 0.09.
+// (With W's products in every strip it was 5.1, without the loads 4.6, without the states'
+// products 4.3, without M, W and E the same.)  The waves wait 0.62 of the time, mostly at the two barriers, with one workgroup to a CU.  Pointers, strides and
+// resources are live in every wave over the whole walk: 351 scalars (N = 64: 283) are kept in
+// lanes, and the loop over the pieces has some 600 reads of these.
 template <int N>
 __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
   __shared__ __attribute__((aligned(1024))) GradLds<N> L;
@@ -379,7 +383,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
   // the blocks over the diagonal that operands of 32 rows reach stay zero
   for (int i = threadIdx.x; i < 2 * 16 * 2; i += kGradThreads) {
     const int r = i / 32 * 32 + i / 2 % 16, at = pipe::row_off<64>(r, i / 32 * 32 + 16 + i % 2 * 8);
-    *reinterpret_cast<u32x4*>(L.M + at) = *reinterpret_cast<u32x4*>(L.W + at) = u32x4{0, 0, 0, 0};
+    *reinterpret_cast<u32x4*>(L.M[0] + at) = *reinterpret_cast<u32x4*>(L.M[1] + at) = u32x4{0, 0, 0, 0};
   }
   for (int i = threadIdx.x; i < strips_here >> shift; i += kGradThreads) {
     const int head = (strip0 >> shift) + i;
@@ -518,8 +522,19 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
     }
 
     f32x16 gB = zero16(), gC = zero16();
-    f32x4 cb[2];        // C B^T of the wave's blocks
-    u32x4 bt[4];        // columns of B, transposed
+    f32x4 cb[2], wsum[2];  // C B^T of the wave's blocks, and W over the strips
+    // the wave's n-th block of 16 x 16, ib >= jb
+    auto block_of = [&](int n, int& ib, int& jb) {
+      const int t = wave + n * kBlockWaves;
+      ib = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jb = t - ib * (ib + 1) / 2;
+    };
+    auto put_parts = [&](int ib, int jb, const f32x4& v) {
+      const int at = pipe::row_off<64>(16 * ib + c16, 16 * jb + 4 * g16);
+      const u32x2 hi = pipe::cvt4(v);
+      *reinterpret_cast<u32x2*>(L.M[0] + at) = hi;
+      *reinterpret_cast<u32x2*>(L.M[1] + at) = pipe::cvt4(f32x4{v[0] - pipe::lo_f(hi[0]), v[1] - pipe::hi_f(hi[0]), v[2] - pipe::lo_f(hi[1]),
+                                                                v[3] - pipe::hi_f(hi[1])});
+    };
 
     for (int s = 0; s < strips_here; ++s) {
       const int strip = strip0 + s, head = strip >> shift, b = s & 1;
@@ -532,22 +547,15 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
       const Steps& st = L.st[(head - (strip0 >> shift)) & 1];
       const __bf16 *St = L.strip[b].S, *Zt = L.strip[b].Z, *Xt = L.strip[b].x, *Ht = L.strip[b].h;
       auto& sums = L.sums[b];
-      if (s == 0) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) bt[k] = col_frag8<N>(L.B, cbn, 16 * k, nt);
-      }
       if (wave < kBlockWaves) {
         // two blocks, one's steps between the other's: rows j as elements 4 g16 + r, rows i as lanes
         int ib[2], jb[2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int t = wave + n * kBlockWaves;
-          ib[n] = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jb[n] = t - ib[n] * (ib[n] + 1) / 2;
-        }
+        for (int n = 0; n < 2; ++n) block_of(n, ib[n], jb[n]);
         if (s == 0) {
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            cb[n] = pipe::zero4();
+            cb[n] = wsum[n] = pipe::zero4();
 #pragma unroll
             for (int k = 0; k < N / 32; ++k)
               cb[n] = pipe::mma32(rows16(L.B, pipe::ic<N>{}, 16 * jb[n], 32 * k), rows16(L.C, pipe::ic<N>{}, 16 * ib[n], 32 * k), cb[n]);
@@ -577,12 +585,10 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
             m[r] = cb[n][r] * l;
             x[n][r] = w[n][r] * m[r];
             e[r] = off || j < c16 ? x[n][r] : 0.f;
-            w[n][r] *= l;
+            wsum[n][r] = __builtin_fmaf(w[n][r], l, wsum[n][r]);
           }
           diagonal[n] = c16 & 2 ? (c16 & 1 ? x[n][3] : x[n][2]) : (c16 & 1 ? x[n][1] : x[n][0]);
-          const int at = pipe::row_off<64>(16 * ib[n] + c16, 16 * jb[n] + 4 * g16);
-          *reinterpret_cast<u32x2*>(L.M + at) = pipe::cvt4(m);
-          *reinterpret_cast<u32x2*>(L.W + at) = pipe::cvt4(w[n]);
+          put_parts(ib[n], jb[n], m);
           row[n] = row_sums(((e[0] + e[1]) + e[2]) + e[3]);
           column[n] = column_sums(e);
         }
@@ -660,9 +666,13 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           if (k >= rb / 2) {
-            const u32x4 m = cols16(L.M, 32 * k, 16 * rb);
+            const u32x4 m0 = cols16(L.M[0], 32 * k, 16 * rb), m1 = cols16(L.M[1], 32 * k, 16 * rb);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) u[i] = pipe::mma32(cols16(Ht, 32 * k, 32 * pt + 16 * i), m, u[i]);
+            for (int i = 0; i < 2; ++i) {
+              const u32x4 h = cols16(Ht, 32 * k, 32 * pt + 16 * i);
+              u[i] = pipe::mma32(h, m0, u[i]);
+              u[i] = pipe::mma32(h, m1, u[i]);
+            }
           }
         const float dskip = L.heads[head - (strip0 >> shift)].D;
         __bf16* const mine = L.strip[b].S + wave * 512;  // S has been used: on the way to memory
@@ -680,17 +690,35 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(BwdParams p) {
         if (row < pc.n)
           *reinterpret_cast<u32x4*>(static_cast<__bf16*>(p.gx) + (long long)(pc.row + row) * p.gxs + strip * 64 + 32 * pt + lane % 4 * 8) = v;
       }
-      if (do_c)
+    }
+    lds_barrier();  // the last M has been used
+    if (wave < kBlockWaves) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (k < 2 * rt + 2) gC = tile::mma(bt[k], tile::row_frag<64>(L.W, rb64, 32 * rt, k), gC);
-      if (do_b)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (k >= 2 * rt) gB = tile::mma(col_frag8<N>(L.C, cbn, 16 * k, nt), col_frag8<64>(L.W, cb64, 16 * k, rt), gB);
+      for (int n = 0; n < 2; ++n) {
+        int ib, jb;
+        block_of(n, ib, jb);
+        put_parts(ib, jb, wsum[n]);
+      }
+    } else if (wave == kSums) {
+      by_rows(strips_here - 1);
     }
     lds_barrier();
-    if (wave == kSums) by_rows(strips_here - 1);
+    if (do_c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < 2 * rt + 2) {
+          const u32x4 b = col_frag8<N>(L.B, cbn, 16 * k, nt);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) gC = tile::mma(b, tile::row_frag<64>(L.M[q], rb64, 32 * rt, k), gC);
+        }
+    if (do_b)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k >= 2 * rt) {
+          const u32x4 c = col_frag8<N>(L.C, cbn, 16 * k, nt);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) gB = tile::mma(c, col_frag8<64>(L.M[q], cb64, 16 * k, rt), gB);
+        }
 
     // gB and gC: lanes are rows, elements n = 32 nt + 8 q + 4 half + j
     const int row = 32 * rt + col;

@@ -9,7 +9,7 @@ import pytest
 
 from gpu_util import down, note, torch_dev
 from oracle import block as ref
-from test_gpu_scan import Case
+from test_gpu_scan import Case, gradients
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,19 @@ def test_output_is_rounded_once(kind, h, p, g, n):
     want, _ = ref.ssm_scan(x, dt, a, B, C, D, bias, cu, S0)
     size, _ = ref.ssm_scan(np.abs(x), dt, a, np.abs(B), np.abs(C), np.abs(D), bias, cu, None if S0 is None else np.abs(S0))
     once("out", out, want, size, n + 128 + 16 * c.exponents())
+
+
+@pytest.mark.parametrize("h,p,g,n", [(8, 64, 1, 64), (6, 64, 2, 128), (4, 128, 1, 64), (5, 128, 1, 128), (24, 64, 1, 128), (195, 64, 65, 64), (220, 128, 44, 64)])
+@pytest.mark.parametrize("cu", [[0, 1, 2, 3], [0, 20, 64, 70], [0, 64, 100]])
+def test_gradients_of_a_piece_are_rounded_once(cu, h, p, g, n):
+    """x, B and C, those summed over the heads of a group, which may cancel."""
+    torch = torch_dev()
+    import linear_attention_sequence_gated_amd as gdn
+    note(f"scan gradients' bits {cu} h{h} p{p} g{g} n{n}")
+    t = cu[-1]
+    c = Case(torch, cu, t, h, p, g, n, seed=5, dt="f32", param="f32", state=False, slow=True)
+    go = torch.from_numpy(np.random.default_rng(h).standard_normal((t, h, p)).astype(np.float32)).to(torch.bfloat16).cuda()
+    got = gdn.ssm_scan_bwd(*c.args(), go, c.offsets, D=c.D, dt_bias=c.bias)
+    want, size = gradients(c, down(go).astype(np.float64), None)
+    for k, name in ((0, "x"), (3, "B"), (4, "C")):
+        once(name, got[k], want[k], size[k], 384 + 16 * c.exponents())
