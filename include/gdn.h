@@ -634,8 +634,9 @@ int gdn_short_conv_step(const void *x, const void *weight, const void *bias, voi
  * is out, and in three (2^-25) where it is a state.  Decays are float32 numbers:
  * where a token, or a piece of up to 64, keeps less than 2^-126 of the state, it keeps
  * nothing, and a weight within a piece is off by up to 9 E 2^-24 of itself, E the sum of
- * the piece's log2 decays, each counted up to 160.  Inputs are finite and a <= 0: others give results that
- * are undefined, typically non-finite, in their own sequence and nowhere else.
+ * the piece's log2 decays, each counted up to 160.  Inputs are finite and a <= 0: others
+ * give results that are undefined, typically non-finite, in their own sequence and
+ * nowhere else.
  * Workspace: gdn_ssm_scan_workspace_bytes (0 for short T), scratch on entry and
  * exit, no clearing needed.  T is below 2^26, T * H below 2^31, R below 2^20, R * H
  * below 2^22, the strides of x, B and C below 2^24.
@@ -660,11 +661,12 @@ int gdn_ssm_scan(const void *x, const void *dt, const void *a, const void *B, co
  *
  * Sums are float32, in a fixed order, and rounded once.  Weights are taken in two bf16
  * parts; states and gradients of states, before and behind every 64 tokens, are rounded to
- * bf16 where they enter a product (grad_S0: as states of the forward are).  grad_dt, grad_a and grad_dt_bias, sums of many terms that may cancel,
- * are as exact as that leaves their terms (2^-8 of each), also where they are float32.
- * Rows in no sequence: as for the forward.  Workspace: gdn_ssm_scan_bwd_workspace_bytes, scratch on entry and exit,
- * no clearing needed; it holds two bf16 states for each head and 64 tokens, and for
- * each head and sequence.
+ * bf16 where they enter a product (grad_S0: as states of the forward are).  grad_dt,
+ * grad_a and grad_dt_bias, sums of many terms that may cancel, are as exact as that
+ * leaves their terms (2^-8 of each), also where they are float32.  Rows in no sequence:
+ * as for the forward.  Workspace: gdn_ssm_scan_bwd_workspace_bytes, scratch on entry and
+ * exit, no clearing needed; it holds two bf16 states for each head and 64 tokens, and
+ * for each head and sequence.
  */
 size_t gdn_ssm_scan_bwd_workspace_bytes(int T, int R, int H, int P, int G, int N);
 int gdn_ssm_scan_bwd(const void *x, const void *dt, const void *a, const void *B, const void *C, const void *D,
